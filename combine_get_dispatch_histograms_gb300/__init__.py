@@ -27,7 +27,10 @@ import torch
 from . import _lib
 from ._lib import EpConfig, EpDispatchHandle, EpError, check
 
-__all__ = ["Context", "LLBuffer", "EpError", "load_library", "ll_size_hint", "ll_message_bytes"]
+from .experts import check_status, expert_gemm, expert_swiglu, new_status
+
+__all__ = ["Context", "LLBuffer", "EpError", "load_library", "ll_size_hint", "ll_message_bytes",
+           "expert_gemm", "expert_swiglu", "new_status", "check_status"]
 
 
 def load_library():

@@ -33,6 +33,18 @@ class EpDispatchHandle(ctypes.Structure):
         "stage_base", "stage_pos")]
 
 
+class EpFp8Rows(ctypes.Structure):
+    _fields_ = [("codes", P), ("code_stride", I64), ("scales", P), ("scale_stride", I64), ("rows", I64)]
+
+
+class EpRowGroups(ctypes.Structure):
+    _fields_ = [("counts", P), ("offsets", P), ("bases", P), ("per_base", I32), ("stride", I64)]
+
+
+class EpFp8Weight(ctypes.Structure):
+    _fields_ = [("codes", P), ("scales", P), ("groups", I32), ("n", I32), ("k", I32)]
+
+
 # name -> (restype, argtypes); every name here is declared in include/ep.h
 SIGNATURES = {
     "ep_last_error": (ctypes.c_char_p, []),
@@ -62,6 +74,10 @@ SIGNATURES = {
     "ep_combine": (INT, [P, ctypes.POINTER(EpDispatchHandle), P, I64, P, P, P, P]),
     "ep_dispatch_hier": (INT, [P, P, P, P, ctypes.POINTER(EpDispatchHandle), P, P, P, I64, P, P, P, P, P, I64, P]),
     "ep_combine_hier": (INT, [P, ctypes.POINTER(EpDispatchHandle), P, I64, P, P, P, P]),
+    "ep_expert_gemm": (INT, [ctypes.POINTER(EpFp8Rows), ctypes.POINTER(EpRowGroups), ctypes.POINTER(EpFp8Weight), P, I64,
+                             P, P]),
+    "ep_expert_swiglu": (INT, [ctypes.POINTER(EpFp8Rows), ctypes.POINTER(EpRowGroups), ctypes.POINTER(EpFp8Weight), P,
+                               I64, P, I64, P, P]),
     "ep_ll_message_bytes": (I64, [INT]),
     "ep_ll_size_hint": (I64, [INT, INT, INT, INT]),
     "ep_ll_buffer_create": (INT, [ctypes.POINTER(EpConfig), INT, ctypes.POINTER(P)]),

@@ -46,16 +46,8 @@ __device__ __forceinline__ float div_by_scale(float x, float scale, float y) {
 constexpr float kRcpScaleMin = 0x1p-100f;
 constexpr float kRcpScaleMax = 3.0e38f;
 
-// Quantises the 16 channels a lane holds; the 8 lanes of an aligned lane group
-// hold one 128-channel block and share its scale.  Every lane of the warp must
-// call it (shuffles); lanes without data pass zeros.
-__device__ __forceinline__ int4 quantize16(const float* v, float* scale_out) {
-    float amax = 0.0f;
-#pragma unroll
-    for (int u = 0; u < 16; ++u) amax = fmaxf(amax, fabsf(v[u]));
-#pragma unroll
-    for (int o = 1; o < 8; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    const float scale = __fdiv_rn(amax, 448.0f);
+// The codes of 16 channels whose block has this scale.
+__device__ __forceinline__ int4 quantize16_by(const float* v, float scale) {
     uint32_t w4[4];
     if (scale == 0.0f) {
 #pragma unroll
@@ -81,8 +73,21 @@ __device__ __forceinline__ int4 quantize16(const float* v, float* scale_out) {
             w4[u] = (lo & 0xffffu) | (hi << 16);
         }
     }
-    *scale_out = scale;
     return make_int4((int)w4[0], (int)w4[1], (int)w4[2], (int)w4[3]);
+}
+
+// Quantises the 16 channels a lane holds; the 8 lanes of an aligned lane group
+// hold one 128-channel block and share its scale.  Every lane of the warp must
+// call it (shuffles); lanes without data pass zeros.
+__device__ __forceinline__ int4 quantize16(const float* v, float* scale_out) {
+    float amax = 0.0f;
+#pragma unroll
+    for (int u = 0; u < 16; ++u) amax = fmaxf(amax, fabsf(v[u]));
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    const float scale = __fdiv_rn(amax, 448.0f);
+    *scale_out = scale;
+    return quantize16_by(v, scale);
 }
 
 }  // namespace ep

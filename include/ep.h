@@ -370,6 +370,70 @@ ep_status ep_combine_hier(ep_ctx* ctx, const ep_dispatch_handle* handle, const v
                           const float* topk_weights, void* out, void* stream);
 
 /* ------------------------------------------------------------------------ */
+/* The experts' products on FP8 rows (what dispatch delivers, what combine      */
+/* reads); the pages leave the experts to the caller, so they name none of it   */
+/* ------------------------------------------------------------------------ */
+
+/* FP8 rows: row r has its e4m3 codes at codes + r * code_stride (bytes; a
+ * multiple of 16) and one fp32 scale per 128 channels at scales +
+ * r * scale_stride (floats).  The rows of ep_quantize_fp8 and the FP8
+ * dispatches: code_stride = ep_fp8_row_bytes(H), scales = codes + H,
+ * scale_stride = code_stride / 4; the packed low-latency rows: H and H / 128. */
+typedef struct ep_fp8_rows {
+    const uint8_t* codes;
+    int64_t code_stride;
+    const float* scales;
+    int64_t scale_stride;
+    int64_t rows; /* rows that the arrays hold: nothing past them is read or written */
+} ep_fp8_rows;
+
+/* Which rows belong to group g (one group per expert).  First row:
+ * (offsets ? offsets[g] : g * stride) + (bases ? bases[g / per_base] : 0);
+ * rows: counts ? counts[g] : stride.  Device arrays, read by the kernel.
+ *   permuted layout: offsets = handle->expert_offsets, bases =
+ *     handle->perm_rank_base, per_base = L, counts = handle->num_recv_per_expert;
+ *   packed low-latency layout: stride = R * cap, counts = packed_recv_count;
+ *   one dense group: stride = the number of rows, all pointers NULL.
+ * A group may be empty; rows of no group are neither read nor written. */
+typedef struct ep_row_groups {
+    const int32_t* counts;
+    const int32_t* offsets;
+    const int32_t* bases;
+    int32_t per_base;
+    int64_t stride;
+} ep_row_groups;
+
+/* FP8 weights: codes [groups][n][k] e4m3 (contiguous, 16-byte aligned), scales
+ * [groups][ceil(n / 128)][k / 128] fp32, one per block of 128 x 128.
+ * groups 1..4096, k a multiple of 128. */
+typedef struct ep_fp8_weight {
+    const uint8_t* codes;
+    const float* scales;
+    int32_t groups, n, k;
+} ep_fp8_weight;
+
+/* y[r][c] = bf16( sum over k of x[r][k] * w[g][c][k] ) for every row r of every
+ * group g, codes times scales; per block of 128 channels the sum runs on the
+ * tensor cores, the blocks are added in fp32, and the result is rounded once.
+ * out: bf16 rows, out_stride elements apart.  x->rows is also the capacity of
+ * out.  status_out (device, nullable): error bits are ORed into it (2 = a
+ * group's rows lie outside x->rows, they were cut off; 4 = a bounded wait ran
+ * out); the caller zeroes it.  No host synchronisation, no workspace. */
+ep_status ep_expert_gemm(const ep_fp8_rows* x, const ep_row_groups* groups, const ep_fp8_weight* w, void* out,
+                         int64_t out_stride, uint32_t* status_out, void* stream);
+
+/* The first product with the activation and the requantisation: with
+ * w13 [groups][2I][k] (gate rows, then up rows; I = w13->n / 2 a multiple of
+ * 128), h = silu(gate) * up in fp32, then per 128 channels scale = amax / 448
+ * and code = e4m3 RNE-satfinite of h / scale (the rule of ep_quantize_fp8).
+ * out: codes, out_stride bytes apart (a multiple of 16), and out_scales,
+ * out_scale_stride floats apart: FP8 rows of I channels, which ep_expert_gemm
+ * reads with the same groups. */
+ep_status ep_expert_swiglu(const ep_fp8_rows* x, const ep_row_groups* groups, const ep_fp8_weight* w13, uint8_t* out,
+                           int64_t out_stride, float* out_scales, int64_t out_scale_stride, uint32_t* status_out,
+                           void* stream);
+
+/* ------------------------------------------------------------------------ */
 /* Low-latency mode ([P1] 低延迟模式; [P2] low-latency ping-pong; [P3] 2.2, 4.2) */
 /* ------------------------------------------------------------------------ */
 

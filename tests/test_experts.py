@@ -1,0 +1,254 @@
+"""The expert products (FP8 rows x FP8 weights) against 64-bit references."""
+import pytest
+import torch
+
+import combine_get_dispatch_histograms_gb300 as ep
+from expert_util import (assert_bf16_close, assert_fp8_close, gen, product64, quantize_rows, quantize_weight, randn,
+                               rows64, swiglu64, weight64)
+
+gpu = pytest.mark.gpu
+
+
+def groups_of(counts, gap=0):
+    """(counts, offsets, rows) on the GPU; `gap` unused rows before every group."""
+    off, r = [], 0
+    for c in counts:
+        r += gap
+        off.append(r)
+        r += c
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    return i32(counts), i32(off), off, max(1, r)
+
+
+def case(counts, K, N, seed=0, gap=0):
+    g = gen(seed)
+    cnt, off, hoff, rows = groups_of(counts, gap)
+    x, xs = quantize_rows(randn((rows, K), g))
+    w, ws = quantize_weight(randn((len(counts), N, K), g) * K ** -0.5)
+    return cnt, off, hoff, x, xs, w, ws
+
+
+RAGGED = [0, 1, 7, 128, 129, 31, 0, 255, 300, 0]
+
+
+@gpu
+@pytest.mark.parametrize("K,N", [(128, 128), (128, 1), (256, 130), (640, 256), (1408, 600), (2048, 1099), (512, 8), (384, 257)])
+@pytest.mark.parametrize("counts", [[1], [5, 0, 64], RAGGED])
+def test_gemm_ragged(K, N, counts):
+    cnt, off, hoff, x, xs, w, ws = case(counts, K, N, seed=K + N, gap=3)
+    st = ep.new_status()
+    out = torch.full((x.shape[0], N), 7.0, dtype=torch.bfloat16, device="cuda")
+    ep.expert_gemm(x, xs, w, ws, counts=cnt, offsets=off, out=out, status=st)
+    ep.check_status(st)
+    own = torch.zeros(x.shape[0], dtype=torch.bool, device="cuda")
+    for e, (o, c) in enumerate(zip(hoff, counts)):
+        own[o:o + c] = True
+        if c:
+            y, err = product64(rows64(x[o:o + c], xs[o:o + c]), weight64(w[e], ws[e]))
+            assert_bf16_close(out[o:o + c], y, err, f"group {e}")
+    assert (out[~own] == 7.0).all(), "rows of no group were written"
+
+
+@gpu
+@pytest.mark.parametrize("K,I", [(128, 128), (640, 384), (1024, 256), (4096, 128)])
+@pytest.mark.parametrize("counts", [[1], [5, 0, 64], RAGGED])
+def test_swiglu_ragged(K, I, counts):
+    cnt, off, hoff, x, xs, w, ws = case(counts, K, 2 * I, seed=K + I, gap=2)
+    st = ep.new_status()
+    codes = torch.full((x.shape[0], I), 9, dtype=torch.uint8, device="cuda")
+    scales = torch.full((x.shape[0], I // 128), 5.0, device="cuda")
+    ep.expert_swiglu(x, xs, w, ws, counts=cnt, offsets=off, out=(codes, scales), status=st)
+    ep.check_status(st)
+    own = torch.zeros(x.shape[0], dtype=torch.bool, device="cuda")
+    for e, (o, c) in enumerate(zip(hoff, counts)):
+        own[o:o + c] = True
+        if c:
+            h, err = swiglu64(rows64(x[o:o + c], xs[o:o + c]), weight64(w[e], ws[e]))
+            assert_fp8_close(codes[o:o + c], scales[o:o + c], h, err, f"group {e}")
+    assert (codes[~own] == 9).all() and (scales[~own] == 5.0).all(), "rows of no group were written"
+
+
+@gpu
+@pytest.mark.parametrize("rows", [1, 2, 33, 127, 128, 129, 256, 500])
+@pytest.mark.parametrize("K,N", [(2048, 512), (128, 77), (7168, 256)])
+def test_gemm_dense(rows, K, N):
+    g = gen(rows + K)
+    x, xs = quantize_rows(randn((rows, K), g))
+    w, ws = quantize_weight(randn((1, N, K), g) * K ** -0.5)
+    out = ep.expert_gemm(x, xs, w[0], ws[0])
+    y, err = product64(rows64(x, xs), weight64(w[0], ws[0]))
+    assert_bf16_close(out, y, err)
+
+
+@gpu
+@pytest.mark.parametrize("fn", ["gemm", "swiglu"])
+def test_packed_regions(fn):
+    g = gen(3)
+    E, cap, K, N = 6, 200, 384, 256
+    counts = [0, 1, 200, 130, 17, 64]
+    cnt = torch.tensor(counts, dtype=torch.int32, device="cuda")
+    x, xs = quantize_rows(randn((E, cap, K), g))
+    w, ws = quantize_weight(randn((E, N, K), g) * K ** -0.5)
+    if fn == "gemm":
+        out = ep.expert_gemm(x, xs, w, ws, counts=cnt)
+    else:
+        codes, scales = ep.expert_swiglu(x, xs, w, ws, counts=cnt)
+    for e, c in enumerate(counts):
+        if not c:
+            continue
+        r, wt = rows64(x[e, :c], xs[e, :c]), weight64(w[e], ws[e])
+        if fn == "gemm":
+            assert_bf16_close(out[e, :c], *product64(r, wt), f"expert {e}")
+        else:
+            assert_fp8_close(codes[e, :c], scales[e, :c], *swiglu64(r, wt), f"expert {e}")
+
+
+@gpu
+@pytest.mark.parametrize("K,N", [(128, 128), (512, 200), (1024, 8)])
+def test_gemm_exact_integers(K, N):
+    """Small integers times powers of two: the sum is exact in fp32, so the result is the exact value rounded once."""
+    g = gen(K * 3 + N)
+    rows = 150
+    v = torch.randint(-2, 3, (rows, K), generator=g, device="cuda").float()
+    w = torch.randint(-2, 3, (N, K), generator=g, device="cuda").float()
+    x = v.to(torch.float8_e4m3fn)
+    xs = torch.exp2(torch.randint(-3, 4, (rows, K // 128), generator=g, device="cuda").float())
+    wc = w.to(torch.float8_e4m3fn)
+    ws = torch.exp2(torch.randint(-3, 4, (-(-N // 128), K // 128), generator=g, device="cuda").float())
+    out = ep.expert_gemm(x, xs, wc, ws)
+    ref = rows64(x, xs) @ weight64(wc, ws).t()
+    assert (ref == ref.float().double()).all()
+    assert torch.equal(out.view(torch.int16), ref.float().to(torch.bfloat16).view(torch.int16))
+
+
+@gpu
+def test_gemm_strides_and_unaligned_output():
+    """Rows of the FP8 dispatch (scales behind the codes), an output inside a wider array, and one at an odd element."""
+    g = gen(17)
+    rows, K, N = 140, 256, 264
+    q, s = quantize_rows(randn((rows, K), g))
+    buf = torch.zeros(rows, K + 16, dtype=torch.uint8, device="cuda")
+    buf[:, :K] = q
+    buf[:, K:K + 8] = s.view(torch.uint8)
+    x, xs = buf[:, :K], buf[:, K:K + 8].view(torch.float32)
+    w, ws = quantize_weight(randn((1, N, K), g) * K ** -0.5)
+    y, err = product64(rows64(q, s), weight64(w[0], ws[0]))
+    for pad, first in ((24, 8), (7, 3)):
+        wide = torch.full((rows, N + pad), 3.0, dtype=torch.bfloat16, device="cuda")
+        ep.expert_gemm(x, xs, w[0], ws[0], out=wide[:, first:first + N])
+        assert_bf16_close(wide[:, first:first + N], y, err)
+        assert (wide[:, :first] == 3.0).all() and (wide[:, first + N:] == 3.0).all()
+
+
+@gpu
+def test_swiglu_writes_fp8_rows_that_gemm_reads():
+    """The two products chained through FP8 rows with their scales behind the codes, on a stream of their own."""
+    g = gen(23)
+    counts = [70, 0, 3, 140]
+    cnt, off, hoff, x, xs, w13, w13s = case(counts, 256, 512, seed=23)
+    w2, w2s = quantize_weight(randn((4, 300, 256), g) * 256 ** -0.5)
+    rows = x.shape[0]
+    buf = torch.zeros(rows, 256 + 16, dtype=torch.uint8, device="cuda")
+    h, hs = buf[:, :256], buf[:, 256:264].view(torch.float32)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    ep.expert_swiglu(x, xs, w13, w13s, counts=cnt, offsets=off, out=(h, hs), stream=side)
+    y = ep.expert_gemm(h, hs, w2, w2s, counts=cnt, offsets=off, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    for e, (o, c) in enumerate(zip(hoff, counts)):
+        if c:
+            assert_fp8_close(h[o:o + c], hs[o:o + c], *swiglu64(rows64(x[o:o + c], xs[o:o + c]), weight64(w13[e], w13s[e])))
+            assert_bf16_close(y[o:o + c], *product64(rows64(h[o:o + c], hs[o:o + c]), weight64(w2[e], w2s[e])))
+
+
+@gpu
+def test_non_finite_and_zero_rows_stay_in_their_row():
+    g = gen(29)
+    rows, K, N = 160, 256, 512
+    x, xs = quantize_rows(randn((rows, K), g))
+    x[3, 7] = 0x7F                       # a NaN code
+    xs[5, 1] = float("inf")
+    x[9] = 0
+    w, ws = quantize_weight(randn((1, N, K), g) * K ** -0.5)
+    out = ep.expert_gemm(x, xs, w[0], ws[0])
+    ok = torch.ones(rows, dtype=torch.bool, device="cuda")
+    ok[3] = ok[5] = False
+    y, err = product64(rows64(x[ok], xs[ok]), weight64(w[0], ws[0]))
+    assert_bf16_close(out[ok], y, err)
+    assert torch.isnan(out[3]).all() and not torch.isfinite(out[5]).any()
+    codes, scales = ep.expert_swiglu(x, xs, w[0], ws[0])
+    h, err = swiglu64(rows64(x[ok], xs[ok]), weight64(w[0], ws[0]))
+    assert_fp8_close(codes[ok], scales[ok], h, err)
+    assert (codes[9] & 0x7F == 0).all() and (scales[9] == 0).all()
+
+
+@gpu
+def test_repeats_bitwise():
+    cnt, off, _, x, xs, w, ws = case(RAGGED, 1024, 512, seed=5)
+    a = ep.expert_gemm(x, xs, w, ws, counts=cnt, offsets=off, out=torch.zeros(x.shape[0], 512, dtype=torch.bfloat16, device="cuda"))
+    for _ in range(3):
+        b = ep.expert_gemm(x, xs, w, ws, counts=cnt, offsets=off, out=torch.zeros_like(a))
+        assert torch.equal(a.view(torch.int16), b.view(torch.int16))
+
+
+@gpu
+def test_rows_outside_the_arrays_are_cut_and_flagged():
+    cnt, off, hoff, x, xs, w, ws = case([40, 50], 128, 256, seed=8)
+    st = ep.new_status()
+    off = off.clone()
+    off[1] = 60                          # rows 60 .. 109 of 90
+    out = torch.zeros(90, 256, dtype=torch.bfloat16, device="cuda")
+    ep.expert_gemm(x, xs, w, ws, counts=cnt, offsets=off, out=out, status=st)
+    with pytest.raises(ep.EpError) as e:
+        ep.check_status(st)
+    assert e.value.status == "EP_ERR_CAPACITY"
+    ep.check_status(st)                  # cleared
+    for g_, (o, n) in enumerate(((0, 40), (60, 30))):
+        assert_bf16_close(out[o:o + n], *product64(rows64(x[o:o + n], xs[o:o + n]), weight64(w[g_], ws[g_])))
+
+
+@gpu
+def test_refusals():
+    cnt, off, _, x, xs, w, ws = case([4, 4], 256, 256, seed=9)
+    ok = dict(counts=cnt, offsets=off)
+    bad = [
+        lambda: ep.expert_gemm(x.cpu(), xs, w, ws, **ok),
+        lambda: ep.expert_gemm(x.float(), xs, w, ws, **ok),
+        lambda: ep.expert_gemm(x, xs[:, :1], w, ws, **ok),
+        lambda: ep.expert_gemm(x[:, :200], xs, w, ws, **ok),
+        lambda: ep.expert_gemm(x, xs, w[:, :, :128].contiguous(), ws, **ok),
+        lambda: ep.expert_gemm(x, xs, w, ws[:, :, :1].contiguous(), **ok),
+        lambda: ep.expert_gemm(x, xs, w, ws),
+        lambda: ep.expert_gemm(x, xs, w, ws, counts=cnt.long(), offsets=off),
+        lambda: ep.expert_gemm(x, xs, w, ws, out=torch.empty(8, 255, dtype=torch.bfloat16, device="cuda"), **ok),
+        lambda: ep.expert_gemm(x, xs, w, ws, out=torch.empty(8, 256, device="cuda"), **ok),
+        lambda: ep.expert_swiglu(x, xs, w[:, :130].contiguous(), ws, **ok),
+    ]
+    for i, f in enumerate(bad):
+        with pytest.raises((ValueError, ep.EpError)):
+            f()
+            pytest.fail(f"refusal {i} was accepted")
+    # codes off a 16-byte boundary are refused by the library
+    flat = torch.zeros(8 * 256 + 16, dtype=torch.uint8, device="cuda")
+    with pytest.raises(ep.EpError):
+        ep.expert_gemm(flat[1:1 + 8 * 256].view(8, 256), xs, w, ws, **ok)
+
+
+def test_c_refusals_without_a_gpu():
+    from combine_get_dispatch_histograms_gb300 import _lib
+    import ctypes
+    lib = _lib.load()
+    x = _lib.EpFp8Rows(256, 128, 256, 1, 4)
+    g = _lib.EpRowGroups(None, None, None, 0, 4)
+    w = lambda **k: _lib.EpFp8Weight(*[dict(dict(codes=256, scales=256, groups=1, n=8, k=128), **k)[n] for n in  # noqa: E731
+                                       ("codes", "scales", "groups", "n", "k")])
+    call = lambda x_, w_: lib.ep_expert_gemm(ctypes.byref(x_), ctypes.byref(g), ctypes.byref(w_), 256, 8, None, None)  # noqa: E731
+    assert lib.ep_expert_gemm(None, None, None, None, 0, None, None) == -1
+    for bad in (dict(groups=0), dict(groups=5000), dict(n=0), dict(k=100), dict(codes=None), dict(scales=None), dict(codes=257)):
+        assert call(x, w(**bad)) == -1, bad
+    assert call(_lib.EpFp8Rows(256, 100, 256, 1, 4), w()) == -1        # row stride
+    assert call(_lib.EpFp8Rows(256, 128, 256, 0, 4), w()) == -1        # scale stride
+    assert call(_lib.EpFp8Rows(256, 128, 256, 1, -1), w()) == -1       # rows
+    assert call(_lib.EpFp8Rows(None, 0, None, 0, 0), w()) == 0         # nothing to do
+    w13 = w(n=128)
+    assert lib.ep_expert_swiglu(ctypes.byref(x), ctypes.byref(g), ctypes.byref(w13), 256, 128, 256, 1, None, None) == -1
