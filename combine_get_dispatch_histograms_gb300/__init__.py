@@ -27,10 +27,10 @@ import torch
 from . import _lib
 from ._lib import EpConfig, EpDispatchHandle, EpError, check
 
-from .experts import check_status, expert_gemm, expert_swiglu, new_status
+from .experts import check_status, expert_gemm, expert_swiglu, moe_tokens, moe_tokens_workspace, new_status
 
 __all__ = ["Context", "LLBuffer", "EpError", "load_library", "ll_size_hint", "ll_message_bytes",
-           "expert_gemm", "expert_swiglu", "new_status", "check_status"]
+           "expert_gemm", "expert_swiglu", "moe_tokens", "moe_tokens_workspace", "new_status", "check_status"]
 
 
 def load_library():

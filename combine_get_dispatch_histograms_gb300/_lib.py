@@ -45,6 +45,11 @@ class EpFp8Weight(ctypes.Structure):
     _fields_ = [("codes", P), ("scales", P), ("groups", I32), ("n", I32), ("k", I32)]
 
 
+class EpMoeWeights(ctypes.Structure):
+    _fields_ = [("w13", P), ("w13_scales", P), ("w2", P), ("w2_scales", P), ("experts", I32), ("hidden", I32),
+                ("inter", I32)]
+
+
 # name -> (restype, argtypes); every name here is declared in include/ep.h
 SIGNATURES = {
     "ep_last_error": (ctypes.c_char_p, []),
@@ -78,6 +83,8 @@ SIGNATURES = {
                              P, P]),
     "ep_expert_swiglu": (INT, [ctypes.POINTER(EpFp8Rows), ctypes.POINTER(EpRowGroups), ctypes.POINTER(EpFp8Weight), P,
                                I64, P, I64, P, P]),
+    "ep_moe_tokens_workspace": (I64, [I32, I32, I32, I32]),
+    "ep_moe_tokens": (INT, [P, I64, I32, P, P, I32, ctypes.POINTER(EpMoeWeights), P, I64, P, I64, P, P]),
     "ep_ll_message_bytes": (I64, [INT]),
     "ep_ll_size_hint": (I64, [INT, INT, INT, INT]),
     "ep_ll_buffer_create": (INT, [ctypes.POINTER(EpConfig), INT, ctypes.POINTER(P)]),

@@ -13,6 +13,8 @@ rows come as one of
   packed low-latency layout), or all of them without counts,
 * [rows][K] with a 2-D weight: one dense product.
 
+    out = moe_tokens(x, topk_idx, topk_weights, w13, w2, w13_scales, w2_scales)   # a whole layer, up to 64 tokens
+
 Context.expert_swiglu / expert_gemm and LLBuffer.expert_swiglu / expert_gemm
 take the groups from the dispatch handle and the packed dict.
 """
@@ -24,7 +26,7 @@ from typing import Optional
 import torch
 
 from . import _lib
-from ._lib import EpError, EpFp8Rows, EpFp8Weight, EpRowGroups, check
+from ._lib import EpError, EpFp8Rows, EpFp8Weight, EpMoeWeights, EpRowGroups, check
 
 _CODES = (torch.uint8, torch.float8_e4m3fn)
 # bits of a status word, as the C entry points OR them in, by the status a check raises first
@@ -170,3 +172,55 @@ def expert_swiglu(x, x_scales, w13, w13_scales, counts=None, offsets=None, out=N
     c.run("ep_expert_swiglu", stream, codes.data_ptr(), _row_stride("expert_swiglu: out codes", codes, c.lead, inter),
           scales.data_ptr(), _row_stride("expert_swiglu: out scales", scales, c.lead, inter // 128), _status_ptr(status, c.device))
     return codes, scales
+
+
+def moe_tokens(x, topk_idx, topk_weights, w13, w2, w13_scales=None, w2_scales=None, out=None, workspace=None, status=None,
+               stream=None):
+    """The whole layer for up to 64 tokens, without dispatch and combine:
+    out[t] = sum_k topk_weights[t][k] * W2[e] (silu(Wg[e] x[t]) * (Wu[e] x[t])), e = topk_idx[t][k], -1 skipped.
+
+    x [T][H] bf16; w13 = [gate; up] [E][2I][H] and w2 [E][H][I], bf16, or e4m3 codes with their block scales.
+    `workspace` (uint8, moe_tokens_workspace bytes) is allocated when it is not given."""
+    _need(x.is_cuda, "moe_tokens: all tensors must be on a CUDA device")
+    dev = x.device
+    _on(dev, topk_idx=topk_idx, topk_weights=topk_weights, w13=w13, w2=w2, w13_scales=w13_scales, w2_scales=w2_scales, out=out,
+        workspace=workspace)
+    _need(x.dtype == torch.bfloat16 and x.dim() == 2 and x.stride(1) == 1, "moe_tokens: x bf16 [T][H], channels contiguous")
+    T, H = x.shape
+    _need(topk_idx.dim() == 2 and topk_idx.shape[0] == T and topk_idx.dtype == torch.int64 and topk_idx.is_contiguous(),
+          "moe_tokens: topk_idx int64 [T][K], contiguous")
+    _need(topk_weights.shape == topk_idx.shape and topk_weights.dtype == torch.float32 and topk_weights.is_contiguous(),
+          "moe_tokens: topk_weights fp32 of topk_idx's shape, contiguous")
+    K = topk_idx.shape[1]
+    _need(w13.dim() == 3 and w2.dim() == 3 and w13.is_contiguous() and w2.is_contiguous(), "moe_tokens: weights [E][rows][cols], contiguous")
+    E, I = w13.shape[0], w2.shape[2]
+    _need(tuple(w13.shape) == (E, 2 * I, H) and tuple(w2.shape) == (E, H, I),
+          f"moe_tokens: w13 {tuple(w13.shape)}, w2 {tuple(w2.shape)} for {H} channels")
+    fp8 = w13_scales is not None or w2_scales is not None
+    if fp8:
+        _need(w13_scales is not None and w2_scales is not None, "moe_tokens: scales for both weights, or for none")
+        _need(w13.dtype in _CODES and w2.dtype in _CODES, "moe_tokens: weights with scales are e4m3 codes")
+        for name, t, r, c in (("w13_scales", w13_scales, 2 * I, H), ("w2_scales", w2_scales, H, I)):
+            _need(t.dtype == torch.float32 and t.is_contiguous() and tuple(t.shape) == (E, r // 128, c // 128),
+                  f"moe_tokens: {name} fp32 {(E, r // 128, c // 128)}, contiguous")
+    else:
+        _need(w13.dtype == w2.dtype == torch.bfloat16, "moe_tokens: weights without scales are bf16")
+    lib = _lib.load()
+    with torch.cuda.device(dev), torch.cuda.stream(stream):
+        if out is None:
+            out = torch.empty(T, H, dtype=torch.bfloat16, device=dev)
+        if workspace is None:
+            workspace = torch.empty(int(lib.ep_moe_tokens_workspace(T, K, H, I)), dtype=torch.uint8, device=dev)
+        _need(out.dtype == torch.bfloat16, "moe_tokens: out is bf16")
+        p = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+        w = EpMoeWeights(w13.data_ptr(), p(w13_scales), w2.data_ptr(), p(w2_scales), E, H, I)
+        check("ep_moe_tokens", lib.ep_moe_tokens(
+            x.data_ptr(), x.stride(0) if T > 1 else H, T, topk_idx.data_ptr(), topk_weights.data_ptr(), K, ctypes.byref(w),
+            out.data_ptr(), _row_stride("moe_tokens: out", out, (T,), H), workspace.data_ptr(), workspace.numel(),
+            _status_ptr(status, dev), _stream_of(stream, dev)))
+    return out
+
+
+def moe_tokens_workspace(num_tokens: int, num_topk: int, hidden: int, inter: int) -> int:
+    """Bytes of workspace moe_tokens needs (0 for sizes it refuses)."""
+    return int(_lib.load().ep_moe_tokens_workspace(num_tokens, num_topk, hidden, inter))

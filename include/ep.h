@@ -433,6 +433,39 @@ ep_status ep_expert_swiglu(const ep_fp8_rows* x, const ep_row_groups* groups, co
                            int64_t out_stride, float* out_scales, int64_t out_scale_stride, uint32_t* status_out,
                            void* stream);
 
+/* The weights of a mixture-of-experts layer: w13 [experts][2 * inter][hidden]
+ * (gate rows, then up rows) and w2 [experts][hidden][inter], contiguous and
+ * 16-byte aligned; e4m3 codes with fp32 scales [..][rows / 128][cols / 128]
+ * (hidden and inter multiples of 128), or bf16 with both scale pointers NULL
+ * (multiples of 32). */
+typedef struct ep_moe_weights {
+    const void* w13;
+    const float* w13_scales;
+    const void* w2;
+    const float* w2_scales;
+    int32_t experts, hidden, inter;
+} ep_moe_weights;
+
+/* Bytes of workspace ep_moe_tokens needs on the current device (0 for sizes it
+ * refuses). */
+int64_t ep_moe_tokens_workspace(int32_t num_tokens, int32_t num_topk, int32_t hidden, int32_t inter);
+
+/* A whole layer for 0..64 tokens, in two kernels:
+ *   out[t] = bf16( sum over k of w[t][k] * W2[e] ( silu(Wg[e] x[t]) * (Wu[e] x[t]) ) ),  e = topk_idx[t][k],
+ * x and out bf16 rows, strides in elements (x 16-byte aligned, x_stride a
+ * multiple of 8).  Every sum is fp32 and h keeps 16 bits of mantissa between
+ * the kernels.  -1 entries are skipped, a token with no valid entry gets +0;
+ * an entry outside [-1, experts) is skipped and ORs 1 into status_out (device,
+ * nullable, zeroed by the caller).  The experts a token names twice count with
+ * the sum of both weights.  The order of the sums depends on the routing and
+ * the device alone, so equal calls give equal bits.  The workspace (16-byte
+ * aligned) belongs to the call until it has finished on `stream`; it needs no
+ * initialisation.  Asynchronous, no allocation. */
+ep_status ep_moe_tokens(const void* x, int64_t x_stride, int32_t num_tokens, const int64_t* topk_idx,
+                        const float* topk_weights, int32_t num_topk, const ep_moe_weights* w, void* out,
+                        int64_t out_stride, void* workspace, int64_t workspace_bytes, uint32_t* status_out,
+                        void* stream);
+
 /* ------------------------------------------------------------------------ */
 /* Low-latency mode ([P1] 低延迟模式; [P2] low-latency ping-pong; [P3] 2.2, 4.2) */
 /* ------------------------------------------------------------------------ */
