@@ -16,6 +16,10 @@ binding without the built library (or without a GPU) raises.
     ll = LLBuffer(num_ranks=16, num_experts=256, num_topk=8, num_tokens=128, hidden=7168, cap=128)
     pk = ll.dispatch(x, topk_idx)                            # FP8, no host sync
     out = ll.combine(y_ll, topk_idx, topk_weights, pk)
+
+The experts between them: expert_swiglu and expert_gemm (methods of both, on
+FP8 rows and e4m3 weights), and moe_tokens, a whole layer for up to 64 tokens;
+layer.MoELayer runs them together.
 """
 from __future__ import annotations
 
@@ -27,10 +31,10 @@ import torch
 from . import _lib
 from ._lib import EpConfig, EpDispatchHandle, EpError, check
 
-from .experts import check_status, expert_gemm, expert_swiglu, moe_tokens, moe_tokens_workspace, new_status
+from .experts import check_status, expert_gemm, expert_swiglu, fp8_row_views, moe_tokens, moe_tokens_workspace, new_status
 
 __all__ = ["Context", "LLBuffer", "EpError", "load_library", "ll_size_hint", "ll_message_bytes",
-           "expert_gemm", "expert_swiglu", "moe_tokens", "moe_tokens_workspace", "new_status", "check_status"]
+           "expert_gemm", "expert_swiglu", "fp8_row_views", "moe_tokens", "moe_tokens_workspace", "new_status", "check_status"]
 
 
 def load_library():
@@ -380,6 +384,29 @@ class Context:
     def combine_hier(self, handle, expert_out, topk_idx, topk_weights, stream=None, out=None):
         return self.combine(handle, expert_out, topk_idx, topk_weights, stream=stream, out=out, hier=True)
 
+    # ---- the experts' products on permuted FP8 rows --------------------------------
+    def _groups(self, handle: Handle) -> dict:
+        return dict(counts=handle["num_recv_per_expert"], offsets=handle["expert_offsets"], bases=handle["perm_rank_base"],
+                    status=self.lib.ep_ctx_status_word(self._ctx))
+
+    def expert_swiglu(self, handle: Handle, permuted_xq, w13, w13_scales, stream=None, out=None):
+        """silu(x wg^T) * (x wu^T) of the permuted FP8 rows [P][row bytes], w13 = [gate; up] [E][2I][H] e4m3 codes with
+        block scales, as FP8 rows of I channels in the same layout (expert_gemm reads them)."""
+        inter = w13.shape[1] // 2
+        if out is None:
+            with torch.cuda.stream(stream):
+                out = torch.empty(permuted_xq.shape[0], int(self.lib.ep_fp8_row_bytes(inter)), dtype=torch.uint8,
+                                  device=self.device)
+        x, xs = fp8_row_views(permuted_xq, w13.shape[2])
+        expert_swiglu(x, xs, w13, w13_scales, out=fp8_row_views(out, inter), stream=stream, **self._groups(handle))
+        return out
+
+    def expert_gemm(self, handle: Handle, permuted_xq, w, w_scales, stream=None, out=None):
+        """y = x w^T of the permuted FP8 rows [P][row bytes], w [E][N][K] e4m3 codes with block scales: bf16 [P][N],
+        with N = H what combine reads."""
+        x, xs = fp8_row_views(permuted_xq, w.shape[2])
+        return expert_gemm(x, xs, w, w_scales, out=out, stream=stream, **self._groups(handle))
+
     # ---- hierarchical dispatch -------------------------------------------------
     def dispatch_hier(self, x, topk_idx, topk_weights, handle: Handle, stream=None, out=None, staging=None) -> dict:
         _require_cuda(x, topk_idx, topk_weights)
@@ -478,6 +505,22 @@ class LLBuffer:
             _ptr(o["packed_src_info"]), _ptr(o["packed_recv_count"]), _ptr(o["layout_range"]), _ptr(o["slot"]),
             _stream(stream)))
         return o
+
+    def expert_swiglu(self, packed: dict, w13, w13_scales, stream=None, out=None):
+        """silu(x wg^T) * (x wu^T) of the received tokens: (codes [E][R*cap][I], scales [E][R*cap][I/128])."""
+        rows = self.R * self.cap
+        return expert_swiglu(packed["packed_x"].view(self.E, rows, self.H),
+                             packed["packed_scales"].view(self.E, rows, self.H // 128), w13, w13_scales,
+                             counts=packed["packed_recv_count"].view(-1), out=out,
+                             status=self.lib.ep_ll_status_word(self._buf), stream=stream)
+
+    def expert_gemm(self, h, packed: dict, w, w_scales, stream=None, out=None):
+        """y = h w^T of expert_swiglu's (codes, scales): bf16 [R][L][R*cap][N], with N = H what combine reads."""
+        rows = self.R * self.cap
+        y = expert_gemm(h[0], h[1], w, w_scales, counts=packed["packed_recv_count"].view(-1),
+                        out=None if out is None else out.view(self.E, rows, -1),
+                        status=self.lib.ep_ll_status_word(self._buf), stream=stream)
+        return y.view(self.R, self.L, rows, -1)
 
     def combine(self, y_ll, topk_idx, topk_weights, packed: dict, t0: int = 0, n: Optional[int] = None,
                 stream=None, out=None):

@@ -58,6 +58,7 @@ SIGNATURES = {
     "ep_ctx_create": (INT, [ctypes.POINTER(EpConfig), ctypes.POINTER(P)]),
     "ep_ctx_destroy": (None, [P]),
     "ep_ctx_check": (INT, [P, P]),
+    "ep_ctx_status_word": (P, [P]),
     "ep_ctx_set_wait_timeout_us": (INT, [P, I64]),
     "ep_ctx_set_expert_alignment": (INT, [P, INT]),
     "ep_ctx_expert_alignment": (I32, [P]),
@@ -96,6 +97,7 @@ SIGNATURES = {
     "ep_ll_dispatch": (INT, [P, P, P, INT, INT, P, P, P, P, P, P, P]),
     "ep_ll_combine": (INT, [P, P, P, P, P, P, INT, INT, P, P]),
     "ep_ll_check": (INT, [P, P]),
+    "ep_ll_status_word": (P, [P]),
     "ep_ll_count_slots": (P, [P, INT]),
     "ep_ll_current_buffer": (INT, [P]),
 }

@@ -698,6 +698,8 @@ extern "C" ep_status ep_ctx_check(ep_ctx* c, void* stream) {
     return status_from_flags(flags);
 }
 
+extern "C" uint32_t* ep_ctx_status_word(ep_ctx* c) { return c ? c->status : nullptr; }
+
 extern "C" ep_status ep_ctx_set_wait_timeout_us(ep_ctx* c, int64_t us) {
     if (!c || us <= 0) return set_error(EP_ERR_INVALID_ARG, "bad context or timeout");
     c->wait_timeout_ns = us * 1000;

@@ -482,6 +482,8 @@ extern "C" ep_status ep_ll_check(ep_ll_buffer* b, void* stream) {
     return status_from_flags(flags);
 }
 
+extern "C" uint32_t* ep_ll_status_word(ep_ll_buffer* b) { return b ? b->status : nullptr; }
+
 extern "C" int32_t* ep_ll_count_slots(ep_ll_buffer* b, int which) {
     if (!b || which < 0 || which > 1) return nullptr;
     return b->counts[which];

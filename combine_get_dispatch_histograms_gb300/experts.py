@@ -126,9 +126,14 @@ class _Call:
                                        _stream_of(stream, self.device)))
 
 
+def fp8_row_views(rows: torch.Tensor, channels: int):
+    """(codes, scales) of FP8 rows [rows][row bytes]: `channels` e4m3 codes, then channels / 128 fp32 scales."""
+    return rows[:, :channels], rows[:, channels:channels + channels // 32].view(torch.float32)
+
+
 def _status_ptr(status, device):
-    if status is None:
-        return None
+    if status is None or isinstance(status, int):  # an address: the status word of a context or a buffer
+        return status
     _need(status.dtype in (torch.int32, torch.uint32) and status.numel() >= 1, "status: an int32 device word")
     _on(device, status=status)
     return status.data_ptr()

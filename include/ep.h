@@ -88,6 +88,9 @@ void ep_ctx_destroy(ep_ctx* ctx);
 /* Synchronises `stream`, reads and clears the device status word.  Returns
  * EP_OK, EP_ERR_INVALID_INPUT, EP_ERR_CAPACITY or EP_ERR_TIMEOUT. */
 ep_status ep_ctx_check(ep_ctx* ctx, void* stream);
+/* The context's device status word, for the status_out of the calls that take
+ * one: ep_ctx_check then reports their errors too (NULL if ctx is NULL). */
+uint32_t* ep_ctx_status_word(ep_ctx* ctx);
 
 /* Limit, in microseconds, of every bounded device wait of this context
  * (copy-pipeline barriers).  Default 2 000 000. */
@@ -539,6 +542,8 @@ ep_status ep_ll_combine(ep_ll_buffer* buf, const void* y_ll, const int64_t* topk
 
 /* Synchronises `stream`, reads and clears the buffer's status word. */
 ep_status ep_ll_check(ep_ll_buffer* buf, void* stream);
+/* The buffer's device status word, as ep_ctx_status_word. */
+uint32_t* ep_ll_status_word(ep_ll_buffer* buf);
 
 /* Device pointer to the count slots [E][R] int32 of ping-pong buffer
  * `which` (0 or 1), and the index of the buffer the last send used. */
