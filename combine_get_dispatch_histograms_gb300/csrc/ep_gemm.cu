@@ -15,16 +15,24 @@
 
 namespace ep {
 
-constexpr int kBM = 128;               // rows of a tile
-constexpr int kBN = 256;               // weight rows of a tile
+constexpr int kBM = 128;               // rows of a tile in each block of a pair
+constexpr int kTileM = 2 * kBM;        // rows of a tile
+constexpr int kBN = 256;               // weight rows of a tile, half of them in each block
 constexpr int kBK = 128;               // one scale block of K
-constexpr int kStageA = kBM * kBK;     // bytes
-constexpr int kStageB = kBN * kBK;
-constexpr int kStages = 4;
+constexpr int kStageA = kBM * kBK;     // bytes in each block
+constexpr int kStageB = kBN / 2 * kBK;
+constexpr int kStages = 5;
 constexpr int kBoxRows = 32;           // rows of one copy of x: a short group copies only the boxes it has rows in
-constexpr int kGemmThreads = 384;      // copy, mma, tensor-memory and spare warp; two warpgroups that sum
+constexpr int kSumGroups = 4;           // warpgroups that sum, each a quarter of the tile's columns
+constexpr int kSumWarps = 4 * kSumGroups;
+constexpr int kGemmThreads = 128 + 128 * kSumGroups;  // copy, mma, tensor-memory and spare warp first
+constexpr int kOutStride = 80;          // bytes of a staged row of 32 bf16: rows fall into other banks
+constexpr int kOutStage = 32 * kOutStride;  // of one warp
+constexpr int kTileRing = 4;            // tiles announced ahead
+constexpr int kScaleChunk = 8;          // blocks of K whose scales are staged together
+constexpr int kScaleRing = 2;
 constexpr int kMaxGroups = 4096;
-constexpr int kChunkM = 16;            // row tiles that share a pass over the weight's tiles
+constexpr int kChunkM = 8;             // row tiles that share a pass over the weight's tiles
 constexpr int64_t kGemmWaitNs = 2000000000ll;
 
 struct GemmArgs {
@@ -40,22 +48,27 @@ struct GemmArgs {
     int64_t out_stride; // elements
     float* out_scales;
     int64_t out_sstride;
-    bool out_vec;
+    bool out_vec;       // 16-byte stores
+    bool x_vec;         // 16-byte loads of row scales
     uint32_t* status;
 };
 
-struct GemmShared {
-    uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2], amax_full[2], drain;
-    uint32_t tmem;
-    int abort;
-    int scan[kGemmThreads / 32];
-    float amax[2][2][kBM];
+struct GemmTile {
+    int g, n;   // group, column tile
+    int row0;   // first row
+    int rows;   // 1..kTileM; 0: no tile is left
 };
 
-struct GemmTile {
-    int g, n;       // group, column tile
-    int64_t row0;   // first row
-    int rows;       // 1..kBM
+struct GemmShared {
+    // done: the products of a stage's block have finished; frees the stage and hands over its accumulator
+    uint64_t full[kStages], done[kStages], acc_empty[2], amax_full[2];
+    uint64_t tile_full[kTileRing], tile_empty[kTileRing], scale_full[kScaleRing], scale_empty[kScaleRing], drain;
+    uint32_t tmem;
+    int abort;
+    GemmTile tile[kTileRing];
+    float amax[2][kSumGroups][kBM];
+    // sx * sw of a chunk of blocks: [block][first or second weight block of the tile][row]
+    float scale[kScaleRing][kScaleChunk][2][kBM];
 };
 
 __device__ __forceinline__ int64_t group_first(const GemmArgs& a, int g) {
@@ -79,53 +92,113 @@ __device__ __forceinline__ int group_rows(const GemmArgs& a, int g, bool* cut) {
     return (int)n;
 }
 
-// Tile t of the launch: groups in order; inside a group, chunks of kChunkM row
-// tiles, column tiles inside a chunk, row tiles innermost, so that what runs at
-// the same time shares a chunk of rows and few weight tiles.
-__device__ __forceinline__ GemmTile find_tile(const GemmArgs& a, const int* start, int t) {
-    int lo = 0, hi = a.G;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (start[mid] <= t) lo = mid;
-        else hi = mid;
+// Position in a ring of barriers, by the number of steps taken: the slot's
+// barrier and the parity of its next phase.  kSize is a power of two.
+template <int kSize>
+struct RingPos {
+    uint32_t n = 0;
+    __device__ __forceinline__ int slot() const { return n & (kSize - 1); }
+    __device__ __forceinline__ uint32_t phase() const { return n / kSize & 1; }
+    __device__ __forceinline__ uint32_t bar(uint32_t first) const { return first + slot() * 8; }
+};
+// The same for any size.
+struct StagePos {
+    int slot = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void step() {
+        if (++slot == kStages) {
+            slot = 0;
+            phase ^= 1;
+        }
     }
+};
+
+// One warp walks the groups for tile t, t + pairs, ...: 32 groups at a time,
+// each lane one group's tiles.  Groups in order; inside a group, chunks of
+// kChunkM row tiles, column tiles inside a chunk, row tiles innermost, so that
+// what runs at the same time shares a chunk of rows and few weight tiles.
+struct TileWalk {
+    int g0 = -32, start = 0, sum = 0;  // batch of groups, its first tile, its tiles
+    int inc, tiles, rows, first;       // this lane's group: tiles up to and with it, tiles, rows, first row
     bool cut = false;
-    const int rows = group_rows(a, lo, &cut);
-    const int mt = (rows + kBM - 1) / kBM;
-    int r = t - start[lo];
-    const int chunk = r / (kChunkM * a.n_tiles);
-    r -= chunk * kChunkM * a.n_tiles;
-    const int m0 = chunk * kChunkM, mc = min(kChunkM, mt - m0);
-    GemmTile tile;
-    tile.g = lo;
-    tile.n = r / mc;
-    const int m = m0 + r % mc;
-    tile.row0 = group_first(a, lo) + (int64_t)m * kBM;
-    tile.rows = min(kBM, rows - m * kBM);
-    return tile;
+
+    // false: no tile t
+    __device__ __forceinline__ bool find(const GemmArgs& a, int t, int lane, GemmTile* out) {
+        while (t >= start + sum) {
+            start += sum;
+            g0 += 32;
+            if (g0 >= a.G) {
+                sum = 0;
+                g0 = a.G;
+                return false;
+            }
+            const int g = g0 + lane;
+            rows = g < a.G ? group_rows(a, g, &cut) : 0;
+            first = rows ? (int)group_first(a, g) : 0;
+            tiles = (rows + kTileM - 1) / kTileM * a.n_tiles;
+            inc = tiles;
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, inc, o);
+                if (lane >= o) inc += v;
+            }
+            sum = __shfl_sync(0xffffffffu, inc, 31);
+        }
+        const int src = __ffs(__ballot_sync(0xffffffffu, t < start + inc)) - 1;
+        const int n = __shfl_sync(0xffffffffu, rows, src);
+        int r = t - start - __shfl_sync(0xffffffffu, inc - tiles, src);
+        const int mt = (n + kTileM - 1) / kTileM, chunk = r / (kChunkM * a.n_tiles);
+        r -= chunk * kChunkM * a.n_tiles;
+        const int m0 = chunk * kChunkM, mc = min(kChunkM, mt - m0), m = m0 + r % mc;
+        out->g = g0 + src;
+        out->n = r / mc;
+        out->row0 = __shfl_sync(0xffffffffu, first, src) + m * kTileM;
+        out->rows = min(kTileM, n - m * kTileM);
+        return true;
+    }
+};
+
+// silu(g) * u with the approximate power and reciprocal, each off by a few
+// 2^-23 of itself, as the product's own sum is.  For g below about -88 the power is
+// infinite and the result -0.
+__device__ __forceinline__ float silu_mul(float g, float u) {
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+    return g * r * u;
 }
 
 // kSwiglu: the tile's 256 weight rows are 128 gate rows and the 128 up rows of
 // the same channels; otherwise 256 consecutive rows.
 template <bool kSwiglu>
-__global__ void __launch_bounds__(kGemmThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
 gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w, const GemmArgs a) {
     extern __shared__ __align__(1024) uint8_t dyn[];
     __shared__ GemmShared sh;
     uint8_t* tiles = dyn + ((1024u - (smem_u32(dyn) & 1023u)) & 1023u);
-    int* start = reinterpret_cast<int*>(tiles + kStages * (kStageA + kStageB));  // [G + 1]
+    uint8_t* out_stage = tiles + kStages * (kStageA + kStageB);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rank = (int)cluster_rank(), pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
     volatile int* abort = &sh.abort;
+    const uint32_t full = smem_u32(sh.full), done = smem_u32(sh.done), acc_empty = smem_u32(sh.acc_empty);
+    const uint32_t tile_full = smem_u32(sh.tile_full), tile_empty = smem_u32(sh.tile_empty);
+    const uint32_t scale_full = smem_u32(sh.scale_full), scale_empty = smem_u32(sh.scale_empty);
 
     if (tid == 0) {
         for (int s = 0; s < kStages; ++s) {
             mbar_init(&sh.full[s], 1);
-            mbar_init(&sh.empty[s], 1);
+            mbar_init(&sh.done[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
-            mbar_init(&sh.acc_full[b], 1);
-            mbar_init(&sh.acc_empty[b], 8);
-            mbar_init(&sh.amax_full[b], 8);
+            mbar_init(&sh.acc_empty[b], 2 * kSumWarps);
+            mbar_init(&sh.amax_full[b], kSumWarps);
+        }
+        for (int b = 0; b < kTileRing; ++b) {
+            mbar_init(&sh.tile_full[b], 1);
+            mbar_init(&sh.tile_empty[b], kSumWarps + 1 + (rank == 0));
+        }
+        for (int b = 0; b < kScaleRing; ++b) {
+            mbar_init(&sh.scale_full[b], 1);
+            mbar_init(&sh.scale_empty[b], kSumWarps);
         }
         mbar_init(&sh.drain, 1);
         sh.abort = 0;
@@ -134,207 +207,286 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
         tma_prefetch_desc(&map_w);
     }
     if (warp == 2) tmem_alloc(&sh.tmem, 512);
-
-    // first tile of every group: each thread sums a run of groups, one scan over the threads
-    {
-        const int per = (a.G + kGemmThreads - 1) / kGemmThreads, g0 = tid * per;
-        int sum = 0;
-        bool cut = false;
-        for (int g = g0; g < min(a.G, g0 + per); ++g) {
-            const int n = (group_rows(a, g, &cut) + kBM - 1) / kBM * a.n_tiles;
-            start[g] = sum;
-            sum += n;
-        }
-        if (cut && a.status && blockIdx.x == 0) flag(a.status, FLAG_CAPACITY);
-        int inc = sum;
-        for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, inc, o);
-            if (lane >= o) inc += v;
-        }
-        if (lane == 31) sh.scan[warp] = inc;
-        tc_fence_before();
-        __syncthreads();
-        tc_fence_after();
-        int before = inc - sum;
-        for (int w = 0; w < warp; ++w) before += sh.scan[w];
-        for (int g = g0; g < min(a.G, g0 + per); ++g) start[g] += before;
-        if (tid == kGemmThreads - 1) start[a.G] = before + sum;
-        __syncthreads();
-    }
-    const int total = start[a.G];
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();  // both blocks' barriers are ready
+    tc_fence_after();
     const uint32_t tmem = sh.tmem;
 
     if (warp < 4) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
-        if (warp == 0 && lane == 0) {
-            // ---- copies: kStages blocks of K ahead of the products --------------
-            int stage = 0;
-            uint32_t phase = 0, issued = 0;
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 32;");
+        if (warp == 3) {
+            // ---- tiles and scales: announces each tile, then stages its blocks' scales, so that the
+            // other warps never wait for global memory themselves
+            TileWalk walk;
+            RingPos<kTileRing> tr;
+            RingPos<kScaleRing> sr;
+            for (int t = pair;; t += pairs) {
+                GemmTile tile = {0, 0, 0, 0};
+                const bool some = walk.find(a, t, lane, &tile);
+                mbar_wait_warp(tr.bar(tile_empty), tr.phase() ^ 1, kGemmWaitNs, abort);
+                if (__any_sync(0xffffffffu, *abort)) break;
+                if (lane == 0) {
+                    sh.tile[tr.slot()] = tile;
+                    mbar_arrive(tr.bar(tile_full));
+                }
+                ++tr.n;
+                if (!some) break;
+                const int mine = min(tile.rows - rank * kBM, kBM);
+                // lanes 0-7 and 8-15: the weight blocks' scales of a chunk
+                const int b0 = kSwiglu ? tile.n : tile.n * 2;
+                const int b1 = kSwiglu ? a.N / 256 + tile.n : min(b0 + 1, (a.N - 1) / 128);
+                const float* ws = a.w_scales + tile.g * a.w_sgroup + (int64_t)(lane < 8 ? b0 : b1) * a.KB + (lane & 7);
+                const float* xs = a.x_scales + (int64_t)(tile.row0 + rank * kBM) * a.x_sstride;
+#pragma unroll 1
+                for (int kb = 0; kb < a.KB; kb += kScaleChunk) {
+                    mbar_wait_warp(sr.bar(scale_empty), sr.phase() ^ 1, kGemmWaitNs, abort);
+                    const float w = lane < 16 && kb + (lane & 7) < a.KB ? __ldg(ws + kb) : 0.0f;
+                    float* dst = &sh.scale[sr.slot()][0][0][0];
+#pragma unroll 1
+                    for (int i = 0; i < kScaleChunk && kb + i < a.KB; i += 4) {
+                        const float w00 = __shfl_sync(0xffffffffu, w, i), w01 = __shfl_sync(0xffffffffu, w, 8 + i);
+                        const float w10 = __shfl_sync(0xffffffffu, w, i + 1), w11 = __shfl_sync(0xffffffffu, w, 9 + i);
+                        const float w20 = __shfl_sync(0xffffffffu, w, i + 2), w21 = __shfl_sync(0xffffffffu, w, 10 + i);
+                        const float w30 = __shfl_sync(0xffffffffu, w, i + 3), w31 = __shfl_sync(0xffffffffu, w, 11 + i);
+#pragma unroll 1
+                        for (int r = lane; r < mine; r += 32) {
+                            const float* p = xs + r * a.x_sstride + kb + i;
+                            float4 v;
+                            if (a.x_vec && kb + i + 4 <= a.KB) {
+                                v = __ldg(reinterpret_cast<const float4*>(p));
+                            } else {
+                                v.x = __ldg(p);
+                                v.y = kb + i + 1 < a.KB ? __ldg(p + 1) : 0.0f;
+                                v.z = kb + i + 2 < a.KB ? __ldg(p + 2) : 0.0f;
+                                v.w = kb + i + 3 < a.KB ? __ldg(p + 3) : 0.0f;
+                            }
+                            float* d = dst + i * 2 * kBM + r;
+                            d[0] = v.x * w00;
+                            d[kBM] = v.x * w01;
+                            d[2 * kBM] = v.y * w10;
+                            d[3 * kBM] = v.y * w11;
+                            d[4 * kBM] = v.z * w20;
+                            d[5 * kBM] = v.z * w21;
+                            d[6 * kBM] = v.w * w30;
+                            d[7 * kBM] = v.w * w31;
+                        }
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(sr.bar(scale_full));
+                    ++sr.n;
+                }
+            }
+            if (walk.cut && a.status && blockIdx.x == 0) flag(a.status, FLAG_CAPACITY);
+        } else if (warp == 0 && lane == 0) {
+            // ---- copies: kStages blocks of K ahead of the products.  Each block fills its
+            // own half of a stage; block 0's barrier counts the bytes of both.
+            RingPos<kTileRing> tr;
+            StagePos st;
+            uint32_t issued = 0;
             bool ok = true;
-            for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
-                const GemmTile tile = find_tile(a, start, t);
-                const int boxes = (tile.rows + kBoxRows - 1) / kBoxRows;
-                const uint32_t bytes = boxes * kBoxRows * kBK + kStageB;
-                const int w0 = kSwiglu ? tile.n * 128 : tile.n * kBN;
-                const int w1 = kSwiglu ? a.N / 2 + tile.n * 128 : w0 + 128;
+            while (ok) {
+                if (!mbar_wait_or_abort(tr.bar(tile_full), tr.phase(), kGemmWaitNs, abort)) break;
+                const GemmTile tile = sh.tile[tr.slot()];
+                mbar_arrive(tr.bar(tile_empty));
+                ++tr.n;
+                if (tile.rows == 0) break;
+                const int boxes0 = (min(tile.rows, kBM) + kBoxRows - 1) / kBoxRows;
+                const int boxes1 = (max(tile.rows - kBM, 0) + kBoxRows - 1) / kBoxRows;
+                const uint32_t bytes = (boxes0 + boxes1) * kBoxRows * kBK + 2 * kStageB;
+                const int boxes = rank ? boxes1 : boxes0;
+                const int row = tile.row0 + rank * kBM;
+                const int wrow = kSwiglu ? rank * (a.N / 2) + tile.n * 128 : tile.n * kBN + rank * 128;
                 for (int kb = 0; kb < a.KB; ++kb) {
-                    if (!mbar_wait_or_abort(&sh.empty[stage], phase ^ 1, kGemmWaitNs, abort)) {
+                    if (!mbar_wait_or_abort(done + st.slot * 8, st.phase ^ 1, kGemmWaitNs, abort)) {
                         ok = false;
                         break;
                     }
-                    uint8_t* sa = tiles + stage * (kStageA + kStageB);
-                    uint8_t* sb = sa + kStageA;
-                    mbar_arrive_expect_tx(&sh.full[stage], bytes);
-                    tma_load_3d(sb, &map_w, kb * kBK, w0, tile.g, &sh.full[stage]);
-                    tma_load_3d(sb + kStageB / 2, &map_w, kb * kBK, w1, tile.g, &sh.full[stage]);
+                    uint8_t* sa = tiles + st.slot * (kStageA + kStageB);
+                    const uint32_t bar = smem_of(full + st.slot * 8, 0);
+                    if (rank == 0) mbar_arrive_expect_tx(&sh.full[st.slot], bytes);
+                    tma_load_3d(sa + kStageA, &map_w, kb * kBK, wrow, tile.g, bar);
                     for (int b = 0; b < boxes; ++b)
-                        tma_load_2d(sa + b * kBoxRows * kBK, &map_x, kb * kBK, (int)tile.row0 + b * kBoxRows, &sh.full[stage]);
+                        tma_load_2d(sa + b * kBoxRows * kBK, &map_x, kb * kBK, row + b * kBoxRows, bar);
                     ++issued;
-                    if (++stage == kStages) {
-                        stage = 0;
-                        phase ^= 1;
-                    }
+                    st.step();
                 }
             }
-            // no copy may be in flight when the block ends, also after a wait that ran out
-            for (uint32_t i = issued > kStages ? issued - kStages : 0; i < issued; ++i)
-                mbar_wait_bounded(&sh.full[i % kStages], (i / kStages) & 1, kGemmWaitNs);
-        } else if (warp == 1 && lane == 0) {
-            // ---- products: one block of K per accumulator, two accumulators ------
-            const uint32_t idesc = idesc_e4m3(kBM, kBN);
-            int stage = 0, buf = 0;
-            uint32_t phase = 0, bphase = 0;
-            bool ok = true;
-            for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+            // no copy may be in flight when the blocks end, also after a wait that ran out
+            if (rank == 0)
+                for (uint32_t i = issued > kStages ? issued - kStages : 0; i < issued; ++i)
+                    mbar_wait_bounded(&sh.full[i % kStages], (i / kStages) & 1, kGemmWaitNs);
+        } else if (warp == 1 && rank == 0) {
+            // ---- products: one block of K per accumulator, two accumulators.  The whole warp runs the
+            // loop, so that descriptors stay in uniform registers; one lane issues
+            const uint32_t idesc = idesc_e4m3(kTileM, kBN);
+            const uint64_t da0 = smem_desc_sw128(tiles), db0 = smem_desc_sw128(tiles + kStageA);
+            RingPos<kTileRing> tr;
+            StagePos st;
+            RingPos<2> acc;
+            while (true) {
+                mbar_wait_warp(tr.bar(tile_full), tr.phase(), kGemmWaitNs, abort);
+                const int rows = sh.tile[tr.slot()].rows;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(tr.bar(tile_empty));
+                ++tr.n;
+                if (rows == 0 || __any_sync(0xffffffffu, *abort)) break;
+#pragma unroll 1
                 for (int kb = 0; kb < a.KB; ++kb) {
-                    if (!mbar_wait_or_abort(&sh.full[stage], phase, kGemmWaitNs, abort) ||
-                        !mbar_wait_or_abort(&sh.acc_empty[buf], bphase ^ 1, kGemmWaitNs, abort)) {
-                        ok = false;
-                        break;
-                    }
+                    mbar_wait_warp(full + st.slot * 8, st.phase, kGemmWaitNs, abort);
+                    mbar_wait_warp(acc.bar(acc_empty), acc.phase() ^ 1, kGemmWaitNs, abort);
                     tc_fence_after();
-                    const uint8_t* sa = tiles + stage * (kStageA + kStageB);
-                    const uint64_t da = smem_desc_sw128(sa), db = smem_desc_sw128(sa + kStageA);
+                    const uint64_t da = da0 + st.slot * ((kStageA + kStageB) >> 4), db = db0 + st.slot * ((kStageA + kStageB) >> 4);
+                    if (elect_one()) {
 #pragma unroll
-                    for (int k = 0; k < kBK / 32; ++k)
-                        mma_e4m3(tmem + buf * kBN, da + k * 2, db + k * 2, idesc, k > 0);
-                    mma_commit(&sh.empty[stage]);
-                    mma_commit(&sh.acc_full[buf]);
-                    if (++stage == kStages) {
-                        stage = 0;
-                        phase ^= 1;
+                        for (int k = 0; k < kBK / 32; ++k)
+                            mma_e4m3(tmem + acc.slot() * kBN, da + k * 2, db + k * 2, idesc, k > 0);
+                        mma_commit(done + st.slot * 8);
                     }
-                    if ((buf ^= 1) == 0) bphase ^= 1;
+                    __syncwarp();
+                    st.step();
+                    ++acc.n;
                 }
             }
-            mma_commit(&sh.drain);  // every product has finished before tensor memory is freed
+            if (elect_one()) mma_commit(smem_u32(&sh.drain));  // every product has finished before tensor memory is freed
+            __syncwarp();
             mbar_wait_bounded(&sh.drain, 0, kGemmWaitNs);
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
-        // ---- sums: warpgroup `half` adds its 128 columns of every block ----------
-        const int half = (warp - 4) >> 2, r = ((warp & 3) << 5) + lane;
-        // swiglu: 64 gate columns and the 64 up columns of the same channels
-        const uint32_t c0 = kSwiglu ? half * 64 : half * 128, c1 = kSwiglu ? 128 + half * 64 : half * 128 + 64;
+        // 512 x 112 + 128 x 32 registers are the launch's 640 x 96
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 112;");
+        // ---- sums: each warpgroup adds its columns of every block of K -----------
+        const int quarter = (warp - 4) >> 2, r = ((warp & 3) << 5) + lane;
+        // swiglu: 32 gate columns and the 32 up columns of the same channels
+        const uint32_t c0 = kSwiglu ? quarter * 32 : quarter * 64, c1 = kSwiglu ? 128 + quarter * 32 : quarter * 64 + 32;
         const uint32_t lane_base = tmem + ((uint32_t)(warp & 3) << 21);
-        int buf = 0, mbuf = 0;
-        uint32_t bphase = 0, mphase = 0;
-        bool ok = true;
-        for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
-            const GemmTile tile = find_tile(a, start, t);
-            const bool valid = r < tile.rows;
-            const int64_t row = tile.row0 + (valid ? r : 0);
-            const float* xs = a.x_scales + row * a.x_sstride;
-            const int nb = (kSwiglu ? a.N / 2 : a.N) / 128;
-            const int b0 = kSwiglu ? tile.n : min(tile.n * 2 + half, (a.N - 1) / 128);
-            const float* ws0 = a.w_scales + tile.g * a.w_sgroup + (int64_t)b0 * a.KB;
-            const float* ws1 = kSwiglu ? ws0 + (int64_t)nb * a.KB : ws0;
-            float acc[128];
+        const uint32_t free_bar = smem_of(acc_empty, 0);
+        const uint32_t sc0 = smem_u32(&sh.scale[0][0][kSwiglu ? 0 : quarter >> 1][r]);
+        RingPos<kTileRing> tr;
+        RingPos<kScaleRing> sr;
+        RingPos<2> ac;
+        StagePos st;
+        while (true) {
+            mbar_wait_warp(tr.bar(tile_full), tr.phase(), kGemmWaitNs, abort);
+            // the slot is held until the tile is written, so that its fields need no registers
+            const GemmTile* tile = &sh.tile[tr.slot()];
+            if (tile->rows == 0 || __any_sync(0xffffffffu, *abort)) break;
+            const bool rows_here = rank * kBM + (warp & 3) * 32 < tile->rows;
+            float acc[64];
 #pragma unroll
-            for (int i = 0; i < 128; ++i) acc[i] = 0.0f;
-            float sx = __ldg(xs), s0 = __ldg(ws0), s1 = __ldg(ws1);
+            for (int i = 0; i < 64; ++i) acc[i] = 0.0f;
+            uint32_t sc = 0;
+#pragma unroll 1
             for (int kb = 0; kb < a.KB; ++kb) {
-                const float f0 = sx * s0, f1 = kSwiglu ? sx * s1 : f0;
-                if (kb + 1 < a.KB) {  // the next block's scales, used after the next wait
-                    sx = __ldg(xs + kb + 1);
-                    s0 = __ldg(ws0 + kb + 1);
-                    if (kSwiglu) s1 = __ldg(ws1 + kb + 1);
+                if ((kb & (kScaleChunk - 1)) == 0) {
+                    mbar_wait_warp(sr.bar(scale_full), sr.phase(), kGemmWaitNs, abort);
+                    sc = sc0 + sr.slot() * (kScaleChunk * 2 * kBM * 4);
                 }
-                ok = mbar_wait_or_abort(&sh.acc_full[buf], bphase, kGemmWaitNs, abort);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
-                tc_fence_after();
-                const uint32_t ad = lane_base + buf * kBN;
-                float v[2][32];
-                tmem_ld32(ad + c0, v[0]);
-                tmem_wait_ld(v[0]);
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    if (q < 3) tmem_ld32(ad + (q + 1 < 2 ? c0 + 32 : c1 + (q - 1) * 32), v[(q + 1) & 1]);
-                    const float f = q < 2 ? f0 : f1;
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) acc[q * 32 + i] = fmaf(v[q & 1][i], f, acc[q * 32 + i]);
-                    if (q < 3) tmem_wait_ld(v[(q + 1) & 1]);
-                    if (q == 2) {  // all four loads are in registers: the accumulator is free
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&sh.acc_empty[buf]);
-                    }
+                const float f0 = ld_shared_f32(sc), f1 = kSwiglu ? ld_shared_f32(sc + kBM * 4) : f0;
+                sc += 2 * kBM * 4;
+                mbar_wait_warp(done + st.slot * 8, st.phase, kGemmWaitNs, abort);
+                st.step();
+                if (rows_here) {
+                    tc_fence_after();
+                    const uint32_t ad = lane_base + ac.slot() * kBN;
+                    float v[32];
+                    tmem_ld32(ad + c0, v);
+                    tmem_wait_ld(v);
+                    fma32(acc, v, f0);
+                    tmem_ld32(ad + c1, v);
+                    tmem_wait_ld(v);
+                    tc_fence_before();
+                    __syncwarp();  // all loads are in registers: the accumulator is free
+                    if (lane == 0) mbar_arrive_cluster(ac.bar(free_bar));
+                    fma32(acc + 32, v, f1);
+                } else if (lane == 0) {
+                    mbar_arrive_cluster(ac.bar(free_bar));
                 }
-                if ((buf ^= 1) == 0) bphase ^= 1;
+                ++ac.n;
+                if ((kb & (kScaleChunk - 1)) == kScaleChunk - 1 || kb + 1 == a.KB) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(sr.bar(scale_empty));
+                    ++sr.n;
+                }
             }
-            if (!ok) break;
+            const int mine = tile->rows - rank * kBM;  // rows of this block, also none or more than kBM
+            const int row0 = tile->row0 + rank * kBM, tn = tile->n;
             if constexpr (kSwiglu) {
                 float m = 0.0f;
 #pragma unroll
-                for (int i = 0; i < 64; ++i) {
-                    const float gate = acc[i];
-                    acc[i] = gate / (1.0f + expf(-gate)) * acc[64 + i];
+                for (int i = 0; i < 32; ++i) {
+                    acc[i] = silu_mul(acc[i], acc[32 + i]);
                     m = fmaxf(m, fabsf(acc[i]));
                 }
-                // the block's maximum over both warpgroups' channels; two buffers: a
+                // the block's maximum over all warpgroups' channels; two buffers: a
                 // warp writes one again only after every warp has passed the other
-                sh.amax[mbuf][half][r] = m;
+                const int mx = tr.n & 1;
+                sh.amax[mx][quarter][r] = m;
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.amax_full[mbuf]);
-                ok = mbar_wait_or_abort(&sh.amax_full[mbuf], mphase, kGemmWaitNs, abort);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
-                m = fmaxf(m, sh.amax[mbuf][half ^ 1][r]);
-                if ((mbuf ^= 1) == 0) mphase ^= 1;
+                if (lane == 0) mbar_arrive(smem_u32(&sh.amax_full[mx]));
+                mbar_wait_warp(smem_u32(&sh.amax_full[mx]), tr.n >> 1 & 1, kGemmWaitNs, abort);
+#pragma unroll
+                for (int i = 0; i < kSumGroups; ++i) m = fmaxf(m, sh.amax[mx][i][r]);
                 const float scale = __fdiv_rn(m, 448.0f);
-                if (valid) {
-                    uint8_t* o = reinterpret_cast<uint8_t*>(a.out) + row * a.out_stride + tile.n * 128 + half * 64;
+                if (r < mine) {
+                    const int64_t row = row0 + r;
+                    uint8_t* o = reinterpret_cast<uint8_t*>(a.out) + row * a.out_stride + tn * 128 + quarter * 32;
 #pragma unroll
-                    for (int q = 0; q < 4; ++q)
+                    for (int q = 0; q < 2; ++q)
                         *reinterpret_cast<int4*>(o + q * 16) = quantize16_by(&acc[q * 16], scale);
-                    if (half == 0) a.out_scales[row * a.out_sstride + tile.n] = scale;
+                    if (quarter == 0) a.out_scales[row * a.out_sstride + tn] = scale;
                 }
-            } else if (valid) {
-                const int n0 = tile.n * kBN + half * 128;
-                __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(a.out) + row * a.out_stride + n0;
+            } else if (rows_here) {
+                // 32 columns at a time through shared memory, so that a warp's store covers whole
+                // 64-byte pieces of rows
+                uint8_t* stage = out_stage + (warp - 4) * kOutStage;
+                const int n0 = tn * kBN + quarter * 64, rows = min(32, mine - (warp & 3) * 32);
+                __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(a.out) +
+                                   (int64_t)(row0 + (warp & 3) * 32) * a.out_stride + n0;
 #pragma unroll
-                for (int q = 0; q < 16; ++q) {
-                    if (a.out_vec && n0 + q * 8 + 8 <= a.N) {
+                for (int z = 0; z < 2; ++z) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
                         __nv_bfloat162 p[4];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) p[i] = __floats2bfloat162_rn(acc[q * 8 + 2 * i], acc[q * 8 + 2 * i + 1]);
-                        *reinterpret_cast<int4*>(o + q * 8) = *reinterpret_cast<const int4*>(p);
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            if (n0 + q * 8 + i < a.N) o[q * 8 + i] = __float2bfloat16_rn(acc[q * 8 + i]);
+                        for (int i = 0; i < 4; ++i)
+                            p[i] = __floats2bfloat162_rn(acc[z * 32 + q * 8 + 2 * i], acc[z * 32 + q * 8 + 2 * i + 1]);
+                        *reinterpret_cast<int4*>(stage + lane * kOutStride + q * 16) = *reinterpret_cast<const int4*>(p);
                     }
+                    __syncwarp();
+                    if (a.out_vec) {
+                        const int c = (lane & 3) * 8;
+                        for (int i = lane >> 2; i < rows; i += 8) {
+                            const int4 v = *reinterpret_cast<const int4*>(stage + i * kOutStride + c * 2);
+                            __nv_bfloat16* d = o + i * a.out_stride + z * 32 + c;
+                            if (n0 + z * 32 + c + 8 <= a.N) {
+                                *reinterpret_cast<int4*>(d) = v;
+                            } else {
+                                const __nv_bfloat16* e = reinterpret_cast<const __nv_bfloat16*>(&v);
+                                for (int j = 0; j < 8; ++j)
+                                    if (n0 + z * 32 + c + j < a.N) d[j] = e[j];
+                            }
+                        }
+                    } else if (n0 + z * 32 + lane < a.N) {
+                        for (int i = 0; i < rows; ++i)
+                            o[i * a.out_stride + z * 32 + lane] = *reinterpret_cast<const __nv_bfloat16*>(stage + i * kOutStride + lane * 2);
+                    }
+                    __syncwarp();
                 }
             }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(tr.bar(tile_empty));
+            ++tr.n;
         }
     }
     __syncwarp();
     tc_fence_before();
-    __syncthreads();
+    cluster_sync();
     tc_fence_after();
     if (warp == 2) tmem_free(tmem, 512);
     if (tid == 0 && *abort && a.status) flag(a.status, FLAG_TIMEOUT);
+    __syncwarp();
+    cluster_sync();  // neither block ends while the other still frees
 }
 
 // ---- host -------------------------------------------------------------------------
@@ -374,7 +526,7 @@ static ep_status check_products(const char* fn, const ep_fp8_rows* x, const ep_r
         return set_error(EP_ERR_INVALID_ARG, "%s: weight rows %d, channels %d (a multiple of 128)", fn, w->n, w->k);
     if (!w->codes || !w->scales || !aligned16(w->codes))
         return set_error(EP_ERR_INVALID_ARG, "%s: weight codes (16-byte aligned) and scales are required", fn);
-    if (x->rows < 0 || x->rows > 0x7fffffff - kBM)
+    if (x->rows < 0 || x->rows > 0x7fffffff - kTileM)
         return set_error(EP_ERR_INVALID_ARG, "%s: %lld rows", fn, (long long)x->rows);
     if (x->rows > 0) {
         if (!x->codes || !x->scales || !aligned16(x->codes))
@@ -393,6 +545,7 @@ static ep_status launch_gemm(const char* fn, const ep_fp8_rows* x, const ep_row_
                              GemmArgs a, void* stream) {
     a.x_scales = x->scales;
     a.x_sstride = x->scale_stride;
+    a.x_vec = aligned16(x->scales) && x->scale_stride % 4 == 0;
     a.w_scales = w->scales;
     a.G = w->groups;
     a.N = w->n;
@@ -407,7 +560,7 @@ static ep_status launch_gemm(const char* fn, const ep_fp8_rows* x, const ep_row_
     a.group_stride = g->stride;
     a.rows = x->rows;
     // the tiles are counted in 32 bits: every group's last tile may be partial
-    const int64_t most = ((x->rows + kBM - 1) / kBM + w->groups) * (int64_t)a.n_tiles;
+    const int64_t most = ((x->rows + kTileM - 1) / kTileM + w->groups) * (int64_t)a.n_tiles;
     if (most > 0x7fffffff) return set_error(EP_ERR_INVALID_ARG, "%s: %lld tiles", fn, (long long)most);
 
     CUtensorMap map_x, map_w;
@@ -428,9 +581,10 @@ static ep_status launch_gemm(const char* fn, const ep_fp8_rows* x, const ep_row_
     int dev = 0, sms = 0;
     EP_CUDA(cudaGetDevice(&dev));
     EP_CUDA(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
-    const size_t smem = 1024 + kStages * (kStageA + kStageB) + sizeof(int) * (a.G + 1);
+    const size_t smem = 1024 + kStages * (kStageA + kStageB) + kSumWarps * kOutStage;
     EP_CUDA(cudaFuncSetAttribute(gemm_kernel<kSwiglu>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
-    gemm_kernel<kSwiglu><<<(int)(most < sms ? most : sms), kGemmThreads, smem, as_stream(stream)>>>(map_x, map_w, a);
+    const int pairs = (int)(most < sms / 2 ? most : sms / 2);
+    gemm_kernel<kSwiglu><<<2 * pairs, kGemmThreads, smem, as_stream(stream)>>>(map_x, map_w, a);
     EP_CHECK_LAUNCH(fn);
     return EP_OK;
 }

@@ -7,16 +7,29 @@
 
 namespace ep {
 
-// ---- bounded mbarrier wait ------------------------------------------------------
-// Spins on the barrier's own suspended wait; the clock is read only once in
-// 256 failed tries, so that a wait in the hot loop costs no timer access.
-// Returns false after `limit_ns`, or as soon as another role gave up (*abort).
-__device__ __forceinline__ bool mbar_wait_or_abort(uint64_t* bar, uint32_t parity, int64_t limit_ns,
-                                                   volatile int* abort) {
-    if (mbar_try_wait(bar, parity)) return true;
+// ---- bounded mbarrier waits, on shared addresses -----------------------------------
+__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// The clock is read only once in 256 failed tries (each suspends the thread for
+// a while), so that a wait in a hot loop costs no timer access.  Returns false
+// after `limit_ns`, or as soon as another role gave up (*abort).
+__device__ __forceinline__ bool mbar_wait_or_abort(uint32_t bar, uint32_t parity, int64_t limit_ns, volatile int* abort) {
+    if (mbar_try(bar, parity)) return true;
     uint64_t t0 = 0;
     for (uint32_t i = 1;; ++i) {
-        if (mbar_try_wait(bar, parity)) return true;
+        if (mbar_try(bar, parity)) return true;
         if ((i & 255u) == 0) {
             if (*abort) return false;
             const uint64_t t = globaltimer_ns();
@@ -28,54 +41,107 @@ __device__ __forceinline__ bool mbar_wait_or_abort(uint64_t* bar, uint32_t parit
         }
     }
 }
-__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+// The same for a whole warp, which stays together; after a give-up it returns
+// as after success, and the caller looks at *abort where it can leave.
+__device__ __forceinline__ void mbar_wait_warp(uint32_t bar, uint32_t parity, int64_t limit_ns, volatile int* abort) {
+    if (__all_sync(0xffffffffu, mbar_try(bar, parity))) return;
+    uint64_t t0 = 0;
+    for (uint32_t i = 1;; ++i) {
+        if (__all_sync(0xffffffffu, mbar_try(bar, parity))) return;
+        if ((i & 255u) == 0) {
+            const uint64_t t = globaltimer_ns();
+            if (t0 == 0) t0 = t;
+            const bool over = (int64_t)(t - t0) > limit_ns;
+            if (over) *abort = 1;
+            if (__any_sync(0xffffffffu, over || *abort)) return;
+        }
+    }
+}
+
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
+// ---- the two blocks of a cluster ---------------------------------------------------
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Cluster address of the same shared variable in block `rank`.
+__device__ __forceinline__ uint32_t smem_of(uint32_t addr, uint32_t rank) {
+    uint32_t a;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
+    return a;
+}
+__device__ __forceinline__ float ld_shared_f32(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+// Arrives on a barrier of either block.  It orders tensor-memory reads, which
+// tcgen05 fences cover; a release at cluster scope would also wait for the
+// thread's stores to global memory (about 1000 cycles per call, measured).
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 // ---- tiled bulk copies (the innermost coordinate is a multiple of 16 bytes) ------
+// Into this block's shared memory; `bar` (a cluster address) counts the bytes,
+// also where it lies in the other block of the pair.
 __device__ __forceinline__ void tma_prefetch_desc(const CUtensorMap* m) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
 }
-__device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* m, int x, int y, uint64_t* bar) {
+__device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* m, int x, int y, uint32_t bar) {
     asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(
-            smem_u32(dst)),
-        "l"(m), "r"(smem_u32(bar)), "r"(x), "r"(y)
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], "
+        "[%2];" ::"r"(smem_u32(dst)),
+        "l"(m), "r"(bar), "r"(x), "r"(y)
         : "memory");
 }
-__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* m, int x, int y, int z, uint64_t* bar) {
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* m, int x, int y, int z, uint32_t bar) {
     asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], "
-        "[%2];" ::"r"(smem_u32(dst)),
-        "l"(m), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, "
+        "%5}], [%2];" ::"r"(smem_u32(dst)),
+        "l"(m), "r"(bar), "r"(x), "r"(y), "r"(z)
         : "memory");
 }
 
-// ---- tensor memory and tcgen05.mma -----------------------------------------------
-__device__ __forceinline__ void tmem_alloc(uint32_t* slot, uint32_t cols) {  // whole warp
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)), "r"(cols)
+// ---- tensor memory and tcgen05.mma, by pairs of blocks ----------------------------
+__device__ __forceinline__ void tmem_alloc(uint32_t* slot, uint32_t cols) {  // a whole warp of both blocks
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)), "r"(cols)
                  : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
 }
-__device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t cols) {  // the same warp
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
+__device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t cols) {  // the same warps
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
 }
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
-// D[128 x N] (+)= A[128 x 32] B[N x 32]^T, e4m3 operands in shared memory.
+// D[256 x N] (+)= A[256 x 32] B[N x 32]^T, e4m3 operands in shared memory: each
+// block of the pair holds half of A's rows, half of B's rows and the
+// accumulator rows of its half of A.  Issued by one thread of block 0.
 __device__ __forceinline__ void mma_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
         "setp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
         "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
         : "memory");
 }
-// Arrives on `bar` when every tcgen05.mma this thread issued has finished.
-__device__ __forceinline__ void mma_commit(uint64_t* bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
-                 : "memory");
+// Arrives on `bar` of both blocks when every tcgen05.mma this thread issued has finished.
+__device__ __forceinline__ void mma_commit(uint32_t bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "h"((uint16_t)3)
+        : "memory");
 }
 // 32 consecutive columns of this warp's 32 lanes: thread i gets lane i's row.
 __device__ __forceinline__ void tmem_ld32(uint32_t addr, float (&v)[32]) {
@@ -111,6 +177,18 @@ __device__ __forceinline__ uint64_t smem_desc_sw128(const void* p) {
 // Instruction descriptor: fp32 accumulator, e4m3 x e4m3, both K-major.
 __host__ __device__ constexpr uint32_t idesc_e4m3(int m, int n) {
     return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+}
+
+// d[0..31] += v[0..31] * f, two at a time: half the instructions, and fewer
+// register-bank conflicts (1.2 cycles a value and warp against 1.5, measured).
+__device__ __forceinline__ void fma32(float* d, float (&v)[32], float f) {
+#pragma unroll
+    for (int i = 0; i < 32; i += 2)
+        asm("{\n\t.reg .b64 a, b, c;\n\t"
+            "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %4};\n\tmov.b64 c, {%0, %1};\n\t"
+            "fma.rn.f32x2 c, a, b, c;\n\tmov.b64 {%0, %1}, c;\n\t}"
+            : "+f"(d[i]), "+f"(d[i + 1])
+            : "f"(v[i]), "f"(v[i + 1]), "f"(f));
 }
 
 }  // namespace ep
