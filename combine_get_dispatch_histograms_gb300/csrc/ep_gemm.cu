@@ -21,7 +21,7 @@ constexpr int kBN = 256;               // weight rows of a tile, half of them in
 constexpr int kBK = 128;               // one scale block of K
 constexpr int kStageA = kBM * kBK;     // bytes in each block
 constexpr int kStageB = kBN / 2 * kBK;
-constexpr int kStages = 5;
+constexpr int kStages = 4;             // blocks of K in flight; the loops over K are unrolled by it
 constexpr int kBoxRows = 32;           // rows of one copy of x: a short group copies only the boxes it has rows in
 constexpr int kSumGroups = 4;           // warpgroups that sum, each a quarter of the tile's columns
 constexpr int kSumWarps = 4 * kSumGroups;
@@ -101,18 +101,8 @@ struct RingPos {
     __device__ __forceinline__ uint32_t phase() const { return n / kSize & 1; }
     __device__ __forceinline__ uint32_t bar(uint32_t first) const { return first + slot() * 8; }
 };
-// The same for any size.
-struct StagePos {
-    int slot = 0;
-    uint32_t phase = 0;
-    __device__ __forceinline__ void step() {
-        if (++slot == kStages) {
-            slot = 0;
-            phase ^= 1;
-        }
-    }
-};
-
+// Every tile starts at stage 0 and accumulator 0, so that in the unrolled loops
+// both are constants; bit u of a mask is the parity of slot u's next phase.
 // One warp walks the groups for tile t, t + pairs, ...: 32 groups at a time,
 // each lane one group's tiles.  Groups in order; inside a group, chunks of
 // kChunkM row tiles, column tiles inside a chunk, row tiles innermost, so that
@@ -282,8 +272,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
             // ---- copies: kStages blocks of K ahead of the products.  Each block fills its
             // own half of a stage; block 0's barrier counts the bytes of both.
             RingPos<kTileRing> tr;
-            StagePos st;
-            uint32_t issued = 0;
+            uint32_t free_phase = (1u << kStages) - 1;  // a fresh barrier counts as passed
             bool ok = true;
             while (ok) {
                 if (!mbar_wait_or_abort(tr.bar(tile_full), tr.phase(), kGemmWaitNs, abort)) break;
@@ -297,33 +286,33 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
                 const int boxes = rank ? boxes1 : boxes0;
                 const int row = tile.row0 + rank * kBM;
                 const int wrow = kSwiglu ? rank * (a.N / 2) + tile.n * 128 : tile.n * kBN + rank * 128;
+                const uint32_t full0 = smem_of(full, 0);
                 for (int kb = 0; kb < a.KB; ++kb) {
-                    if (!mbar_wait_or_abort(done + st.slot * 8, st.phase ^ 1, kGemmWaitNs, abort)) {
+                    const int u = kb & (kStages - 1);
+                    if (!mbar_wait_or_abort(done + u * 8, free_phase >> u & 1, kGemmWaitNs, abort)) {
                         ok = false;
                         break;
                     }
-                    uint8_t* sa = tiles + st.slot * (kStageA + kStageB);
-                    const uint32_t bar = smem_of(full + st.slot * 8, 0);
-                    if (rank == 0) mbar_arrive_expect_tx(&sh.full[st.slot], bytes);
-                    tma_load_3d(sa + kStageA, &map_w, kb * kBK, wrow, tile.g, bar);
+                    free_phase ^= 1u << u;
+                    uint8_t* sa = tiles + u * (kStageA + kStageB);
+                    if (rank == 0) mbar_arrive_expect_tx(&sh.full[u], bytes);
+                    tma_load_3d(sa + kStageA, &map_w, kb * kBK, wrow, tile.g, full0 + u * 8);
                     for (int b = 0; b < boxes; ++b)
-                        tma_load_2d(sa + b * kBoxRows * kBK, &map_x, kb * kBK, row + b * kBoxRows, bar);
-                    ++issued;
-                    st.step();
+                        tma_load_2d(sa + b * kBoxRows * kBK, &map_x, kb * kBK, row + b * kBoxRows, full0 + u * 8);
                 }
             }
-            // no copy may be in flight when the blocks end, also after a wait that ran out
+            // no copy may be in flight when the blocks end, also after a wait that ran out: the last
+            // phase that this stage's copies complete is the one before its next
             if (rank == 0)
-                for (uint32_t i = issued > kStages ? issued - kStages : 0; i < issued; ++i)
-                    mbar_wait_bounded(&sh.full[i % kStages], (i / kStages) & 1, kGemmWaitNs);
+                for (int u = 0; u < kStages; ++u)
+                    mbar_wait_bounded(&sh.full[u], free_phase >> u & 1, kGemmWaitNs);
         } else if (warp == 1 && rank == 0) {
             // ---- products: one block of K per accumulator, two accumulators.  The whole warp runs the
             // loop, so that descriptors stay in uniform registers; one lane issues
             const uint32_t idesc = idesc_e4m3(kTileM, kBN);
             const uint64_t da0 = smem_desc_sw128(tiles), db0 = smem_desc_sw128(tiles + kStageA);
             RingPos<kTileRing> tr;
-            StagePos st;
-            RingPos<2> acc;
+            uint32_t full_phase = 0, empty_phase = 3;
             while (true) {
                 mbar_wait_warp(tr.bar(tile_full), tr.phase(), kGemmWaitNs, abort);
                 const int rows = sh.tile[tr.slot()].rows;
@@ -333,19 +322,20 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
                 if (rows == 0 || __any_sync(0xffffffffu, *abort)) break;
 #pragma unroll 1
                 for (int kb = 0; kb < a.KB; ++kb) {
-                    mbar_wait_warp(full + st.slot * 8, st.phase, kGemmWaitNs, abort);
-                    mbar_wait_warp(acc.bar(acc_empty), acc.phase() ^ 1, kGemmWaitNs, abort);
+                    const int u = kb & (kStages - 1), c = kb & 1;
+                    mbar_wait_warp(full + u * 8, full_phase >> u & 1, kGemmWaitNs, abort);
+                    mbar_wait_warp(acc_empty + c * 8, empty_phase >> c & 1, kGemmWaitNs, abort);
+                    full_phase ^= 1u << u;
+                    empty_phase ^= 1u << c;
                     tc_fence_after();
-                    const uint64_t da = da0 + st.slot * ((kStageA + kStageB) >> 4), db = db0 + st.slot * ((kStageA + kStageB) >> 4);
+                    const uint32_t at = u * ((kStageA + kStageB) >> 4);
                     if (elect_one()) {
 #pragma unroll
                         for (int k = 0; k < kBK / 32; ++k)
-                            mma_e4m3(tmem + acc.slot() * kBN, da + k * 2, db + k * 2, idesc, k > 0);
-                        mma_commit(done + st.slot * 8);
+                            mma_e4m3(tmem + c * kBN, da0 + at + k * 2, db0 + at + k * 2, idesc, k > 0);
+                        mma_commit(done + u * 8);
                     }
                     __syncwarp();
-                    st.step();
-                    ++acc.n;
                 }
             }
             if (elect_one()) mma_commit(smem_u32(&sh.drain));  // every product has finished before tensor memory is freed
@@ -364,8 +354,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
         const uint32_t sc0 = smem_u32(&sh.scale[0][0][kSwiglu ? 0 : quarter >> 1][r]);
         RingPos<kTileRing> tr;
         RingPos<kScaleRing> sr;
-        RingPos<2> ac;
-        StagePos st;
+        uint32_t done_phase = 0;
         while (true) {
             mbar_wait_warp(tr.bar(tile_full), tr.phase(), kGemmWaitNs, abort);
             // the slot is held until the tile is written, so that its fields need no registers
@@ -377,33 +366,37 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
             for (int i = 0; i < 64; ++i) acc[i] = 0.0f;
             uint32_t sc = 0;
 #pragma unroll 1
-            for (int kb = 0; kb < a.KB; ++kb) {
+            for (int kb = 0; kb < a.KB; kb += kStages) {
                 if ((kb & (kScaleChunk - 1)) == 0) {
                     mbar_wait_warp(sr.bar(scale_full), sr.phase(), kGemmWaitNs, abort);
                     sc = sc0 + sr.slot() * (kScaleChunk * 2 * kBM * 4);
                 }
-                const float f0 = ld_shared_f32(sc), f1 = kSwiglu ? ld_shared_f32(sc + kBM * 4) : f0;
-                sc += 2 * kBM * 4;
-                mbar_wait_warp(done + st.slot * 8, st.phase, kGemmWaitNs, abort);
-                st.step();
-                if (rows_here) {
-                    tc_fence_after();
-                    const uint32_t ad = lane_base + ac.slot() * kBN;
-                    float v[32];
-                    tmem_ld32(ad + c0, v);
-                    tmem_wait_ld(v);
-                    fma32(acc, v, f0);
-                    tmem_ld32(ad + c1, v);
-                    tmem_wait_ld(v);
-                    tc_fence_before();
-                    __syncwarp();  // all loads are in registers: the accumulator is free
-                    if (lane == 0) mbar_arrive_cluster(ac.bar(free_bar));
-                    fma32(acc + 32, v, f1);
-                } else if (lane == 0) {
-                    mbar_arrive_cluster(ac.bar(free_bar));
+#pragma unroll
+                for (int u = 0; u < kStages; ++u) {
+                    if (kb + u >= a.KB) break;
+                    const float f0 = ld_shared_f32(sc + u * (2 * kBM * 4));
+                    const float f1 = kSwiglu ? ld_shared_f32(sc + u * (2 * kBM * 4) + kBM * 4) : f0;
+                    mbar_wait_warp(done + u * 8, done_phase >> u & 1, kGemmWaitNs, abort);
+                    done_phase ^= 1u << u;
+                    if (rows_here) {
+                        tc_fence_after();
+                        const uint32_t ad = lane_base + (u & 1) * kBN;
+                        float v[32];
+                        tmem_ld(ad + c0, v);
+                        tmem_wait_ld(v);
+                        fma32(acc, v, f0);
+                        tmem_ld(ad + c1, v);
+                        tmem_wait_ld(v);
+                        tc_fence_before();
+                        __syncwarp();  // all loads are in registers: the accumulator is free
+                        if (lane == 0) mbar_arrive_cluster(free_bar + (u & 1) * 8);
+                        fma32(acc + 32, v, f1);
+                    } else if (lane == 0) {
+                        mbar_arrive_cluster(free_bar + (u & 1) * 8);
+                    }
                 }
-                ++ac.n;
-                if ((kb & (kScaleChunk - 1)) == kScaleChunk - 1 || kb + 1 == a.KB) {
+                sc += kStages * 2 * kBM * 4;
+                if ((kb & (kScaleChunk - 1)) == kScaleChunk - kStages || kb + kStages >= a.KB) {
                     __syncwarp();
                     if (lane == 0) mbar_arrive(sr.bar(scale_empty));
                     ++sr.n;
