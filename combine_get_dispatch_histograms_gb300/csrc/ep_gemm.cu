@@ -15,24 +15,36 @@
 
 namespace ep {
 
-constexpr int kBM = 128;               // rows of a tile in each block of a pair
-constexpr int kTileM = 2 * kBM;        // rows of a tile
-constexpr int kBN = 256;               // weight rows of a tile, half of them in each block
+constexpr int kBM = 128;               // rows of a tile in each block
+constexpr int kBN = 256;               // weight rows of a tile
 constexpr int kBK = 128;               // one scale block of K
-constexpr int kStageA = kBM * kBK;     // bytes in each block
-constexpr int kStageB = kBN / 2 * kBK;
 constexpr int kStages = 4;             // blocks of K in flight; the loops over K are unrolled by it
 constexpr int kBoxRows = 32;           // rows of one copy of x: a short group copies only the boxes it has rows in
-constexpr int kSumGroups = 4;           // warpgroups that sum, each a quarter of the tile's columns
+constexpr int kSumGroups = 4;          // warpgroups that sum, each a quarter of the tile's columns
 constexpr int kSumWarps = 4 * kSumGroups;
-constexpr int kGemmThreads = 128 + 128 * kSumGroups;  // copy, mma, tensor-memory and spare warp first
-constexpr int kOutStride = 80;          // bytes of a staged row of 32 bf16: rows fall into other banks
+constexpr int kGemmThreads = 128 + 128 * kSumGroups;  // copy, mma, tensor-memory and tile warp first
+constexpr int kOutStride = 80;         // bytes of a staged row of 32 bf16: rows fall into other banks
 constexpr int kOutStage = 32 * kOutStride;  // of one warp
+
+// The two shapes of the kernel.  kCtas = 2: a pair of blocks makes a tile of 256
+// rows; each copies half of the weight's rows, so that a block moves 32 KB per
+// block of K instead of 48.  kCtas = 1: tiles of 128 rows, for groups too short
+// to fill both halves, where the weight's bytes bound the time.
+template <int kCtas>
+struct GemmShape {
+    static constexpr int kTileM = kCtas * kBM;
+    static constexpr int kStageA = kBM * kBK;          // bytes in each block
+    static constexpr int kStageB = kBN / kCtas * kBK;
+    static constexpr int kStage = kStageA + kStageB;
+    static constexpr bool kStageOut = kCtas == 2;      // with 48 KB stages there is no room
+    static constexpr size_t kSmem = 1024 + kStages * kStage + (kStageOut ? kSumWarps * kOutStage : 0);
+};
 constexpr int kTileRing = 4;            // tiles announced ahead
 constexpr int kScaleChunk = 8;          // blocks of K whose scales are staged together
 constexpr int kScaleRing = 2;
 constexpr int kMaxGroups = 4096;
-constexpr int kChunkM = 8;             // row tiles that share a pass over the weight's tiles
+constexpr int kChunkRows = 2048;       // rows that share a pass over the weight's tiles
+constexpr int kPairRows = 192;         // rows of a group from which pairs of blocks are faster
 constexpr int64_t kGemmWaitNs = 2000000000ll;
 
 struct GemmArgs {
@@ -56,7 +68,7 @@ struct GemmArgs {
 struct GemmTile {
     int g, n;   // group, column tile
     int row0;   // first row
-    int rows;   // 1..kTileM; 0: no tile is left
+    int rows;   // 1 .. rows of a tile; 0: no tile is left
 };
 
 struct GemmShared {
@@ -103,11 +115,13 @@ struct RingPos {
 };
 // Every tile starts at stage 0 and accumulator 0, so that in the unrolled loops
 // both are constants; bit u of a mask is the parity of slot u's next phase.
-// One warp walks the groups for tile t, t + pairs, ...: 32 groups at a time,
+// One warp walks the groups for tile t, t + units, ...: 32 groups at a time,
 // each lane one group's tiles.  Groups in order; inside a group, chunks of
-// kChunkM row tiles, column tiles inside a chunk, row tiles innermost, so that
+// kChunkRows rows, column tiles inside a chunk, row tiles innermost, so that
 // what runs at the same time shares a chunk of rows and few weight tiles.
+template <int kTileM>
 struct TileWalk {
+    static constexpr int kChunkM = kChunkRows / kTileM;
     int g0 = -32, start = 0, sum = 0;  // batch of groups, its first tile, its tiles
     int inc, tiles, rows, first;       // this lane's group: tiles up to and with it, tiles, rows, first row
     bool cut = false;
@@ -159,15 +173,17 @@ __device__ __forceinline__ float silu_mul(float g, float u) {
 
 // kSwiglu: the tile's 256 weight rows are 128 gate rows and the 128 up rows of
 // the same channels; otherwise 256 consecutive rows.
-template <bool kSwiglu>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
+template <bool kSwiglu, int kCtas>
+__global__ void __launch_bounds__(kGemmThreads, 1)
 gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w, const GemmArgs a) {
+    using Shape = GemmShape<kCtas>;
+    constexpr int kTileM = Shape::kTileM, kStage = Shape::kStage, kStageA = Shape::kStageA;
     extern __shared__ __align__(1024) uint8_t dyn[];
     __shared__ GemmShared sh;
     uint8_t* tiles = dyn + ((1024u - (smem_u32(dyn) & 1023u)) & 1023u);
-    uint8_t* out_stage = tiles + kStages * (kStageA + kStageB);
+    uint8_t* out_stage = tiles + kStages * kStage;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int rank = (int)cluster_rank(), pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+    const int rank = kCtas == 2 ? (int)cluster_rank() : 0, unit = blockIdx.x / kCtas, units = gridDim.x / kCtas;
     volatile int* abort = &sh.abort;
     const uint32_t full = smem_u32(sh.full), done = smem_u32(sh.done), acc_empty = smem_u32(sh.acc_empty);
     const uint32_t tile_full = smem_u32(sh.tile_full), tile_empty = smem_u32(sh.tile_empty);
@@ -179,7 +195,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
             mbar_init(&sh.done[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
-            mbar_init(&sh.acc_empty[b], 2 * kSumWarps);
+            mbar_init(&sh.acc_empty[b], kCtas * kSumWarps);
             mbar_init(&sh.amax_full[b], kSumWarps);
         }
         for (int b = 0; b < kTileRing; ++b) {
@@ -196,10 +212,10 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
         tma_prefetch_desc(&map_x);
         tma_prefetch_desc(&map_w);
     }
-    if (warp == 2) tmem_alloc(&sh.tmem, 512);
+    if (warp == 2) tmem_alloc<kCtas>(&sh.tmem, 512);
     tc_fence_before();
     __syncthreads();
-    cluster_sync();  // both blocks' barriers are ready
+    if (kCtas == 2) cluster_sync();  // both blocks' barriers are ready
     tc_fence_after();
     const uint32_t tmem = sh.tmem;
 
@@ -208,10 +224,10 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
         if (warp == 3) {
             // ---- tiles and scales: announces each tile, then stages its blocks' scales, so that the
             // other warps never wait for global memory themselves
-            TileWalk walk;
+            TileWalk<kTileM> walk;
             RingPos<kTileRing> tr;
             RingPos<kScaleRing> sr;
-            for (int t = pair;; t += pairs) {
+            for (int t = unit;; t += units) {
                 GemmTile tile = {0, 0, 0, 0};
                 const bool some = walk.find(a, t, lane, &tile);
                 mbar_wait_warp(tr.bar(tile_empty), tr.phase() ^ 1, kGemmWaitNs, abort);
@@ -282,11 +298,11 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
                 if (tile.rows == 0) break;
                 const int boxes0 = (min(tile.rows, kBM) + kBoxRows - 1) / kBoxRows;
                 const int boxes1 = (max(tile.rows - kBM, 0) + kBoxRows - 1) / kBoxRows;
-                const uint32_t bytes = (boxes0 + boxes1) * kBoxRows * kBK + 2 * kStageB;
+                const uint32_t bytes = (boxes0 + boxes1) * kBoxRows * kBK + kBN * kBK;
                 const int boxes = rank ? boxes1 : boxes0;
                 const int row = tile.row0 + rank * kBM;
-                const int wrow = kSwiglu ? rank * (a.N / 2) + tile.n * 128 : tile.n * kBN + rank * 128;
-                const uint32_t full0 = smem_of(full, 0);
+                const int w0 = kSwiglu ? tile.n * 128 : tile.n * kBN, w1 = kSwiglu ? a.N / 2 + w0 : w0 + 128;
+                const uint32_t full0 = kCtas == 2 ? smem_of(full, 0) : full;
                 for (int kb = 0; kb < a.KB; ++kb) {
                     const int u = kb & (kStages - 1);
                     if (!mbar_wait_or_abort(done + u * 8, free_phase >> u & 1, kGemmWaitNs, abort)) {
@@ -294,11 +310,12 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
                         break;
                     }
                     free_phase ^= 1u << u;
-                    uint8_t* sa = tiles + u * (kStageA + kStageB);
+                    uint8_t* sa = tiles + u * kStage;
                     if (rank == 0) mbar_arrive_expect_tx(&sh.full[u], bytes);
-                    tma_load_3d(sa + kStageA, &map_w, kb * kBK, wrow, tile.g, full0 + u * 8);
+                    tma_load_3d<kCtas>(sa + kStageA, &map_w, kb * kBK, rank ? w1 : w0, tile.g, full0 + u * 8);
+                    if (kCtas == 1) tma_load_3d<kCtas>(sa + kStageA + 128 * kBK, &map_w, kb * kBK, w1, tile.g, full0 + u * 8);
                     for (int b = 0; b < boxes; ++b)
-                        tma_load_2d(sa + b * kBoxRows * kBK, &map_x, kb * kBK, row + b * kBoxRows, full0 + u * 8);
+                        tma_load_2d<kCtas>(sa + b * kBoxRows * kBK, &map_x, kb * kBK, row + b * kBoxRows, full0 + u * 8);
                 }
             }
             // no copy may be in flight when the blocks end, also after a wait that ran out: the last
@@ -328,17 +345,17 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
                     full_phase ^= 1u << u;
                     empty_phase ^= 1u << c;
                     tc_fence_after();
-                    const uint32_t at = u * ((kStageA + kStageB) >> 4);
+                    const uint32_t at = u * (kStage >> 4);
                     if (elect_one()) {
 #pragma unroll
                         for (int k = 0; k < kBK / 32; ++k)
-                            mma_e4m3(tmem + c * kBN, da0 + at + k * 2, db0 + at + k * 2, idesc, k > 0);
-                        mma_commit(done + u * 8);
+                            mma_e4m3<kCtas>(tmem + c * kBN, da0 + at + k * 2, db0 + at + k * 2, idesc, k > 0);
+                        mma_commit<kCtas>(done + u * 8);
                     }
                     __syncwarp();
                 }
             }
-            if (elect_one()) mma_commit(smem_u32(&sh.drain));  // every product has finished before tensor memory is freed
+            if (elect_one()) mma_commit<kCtas>(smem_u32(&sh.drain));  // every product has finished before tensor memory is freed
             __syncwarp();
             mbar_wait_bounded(&sh.drain, 0, kGemmWaitNs);
         }
@@ -350,7 +367,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
         // swiglu: 32 gate columns and the 32 up columns of the same channels
         const uint32_t c0 = kSwiglu ? quarter * 32 : quarter * 64, c1 = kSwiglu ? 128 + quarter * 32 : quarter * 64 + 32;
         const uint32_t lane_base = tmem + ((uint32_t)(warp & 3) << 21);
-        const uint32_t free_bar = smem_of(acc_empty, 0);
+        const uint32_t free_bar = kCtas == 2 ? smem_of(acc_empty, 0) : acc_empty;
         const uint32_t sc0 = smem_u32(&sh.scale[0][0][kSwiglu ? 0 : quarter >> 1][r]);
         RingPos<kTileRing> tr;
         RingPos<kScaleRing> sr;
@@ -389,10 +406,10 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
                         tmem_wait_ld(v);
                         tc_fence_before();
                         __syncwarp();  // all loads are in registers: the accumulator is free
-                        if (lane == 0) mbar_arrive_cluster(free_bar + (u & 1) * 8);
+                        if (lane == 0) mbar_hand_back(free_bar + (u & 1) * 8);
                         fma32(acc + 32, v, f1);
                     } else if (lane == 0) {
-                        mbar_arrive_cluster(free_bar + (u & 1) * 8);
+                        mbar_hand_back(free_bar + (u & 1) * 8);
                     }
                 }
                 sc += kStages * 2 * kBM * 4;
@@ -430,41 +447,63 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
                     if (quarter == 0) a.out_scales[row * a.out_sstride + tn] = scale;
                 }
             } else if (rows_here) {
-                // 32 columns at a time through shared memory, so that a warp's store covers whole
-                // 64-byte pieces of rows
-                uint8_t* stage = out_stage + (warp - 4) * kOutStage;
-                const int n0 = tn * kBN + quarter * 64, rows = min(32, mine - (warp & 3) * 32);
-                __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(a.out) +
-                                   (int64_t)(row0 + (warp & 3) * 32) * a.out_stride + n0;
+                const int n0 = tn * kBN + quarter * 64;
+                if constexpr (!Shape::kStageOut) {
+                    // few rows: each lane stores its own
+                    if (r < mine) {
+                        __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(a.out) + (int64_t)(row0 + r) * a.out_stride + n0;
 #pragma unroll
-                for (int z = 0; z < 2; ++z) {
+                        for (int q = 0; q < 8; ++q) {
+                            if (a.out_vec && n0 + q * 8 + 8 <= a.N) {
+                                __nv_bfloat162 p[4];
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        __nv_bfloat162 p[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            p[i] = __floats2bfloat162_rn(acc[z * 32 + q * 8 + 2 * i], acc[z * 32 + q * 8 + 2 * i + 1]);
-                        *reinterpret_cast<int4*>(stage + lane * kOutStride + q * 16) = *reinterpret_cast<const int4*>(p);
-                    }
-                    __syncwarp();
-                    if (a.out_vec) {
-                        const int c = (lane & 3) * 8;
-                        for (int i = lane >> 2; i < rows; i += 8) {
-                            const int4 v = *reinterpret_cast<const int4*>(stage + i * kOutStride + c * 2);
-                            __nv_bfloat16* d = o + i * a.out_stride + z * 32 + c;
-                            if (n0 + z * 32 + c + 8 <= a.N) {
-                                *reinterpret_cast<int4*>(d) = v;
+                                for (int i = 0; i < 4; ++i)
+                                    p[i] = __floats2bfloat162_rn(acc[q * 8 + 2 * i], acc[q * 8 + 2 * i + 1]);
+                                *reinterpret_cast<int4*>(o + q * 8) = *reinterpret_cast<const int4*>(p);
                             } else {
-                                const __nv_bfloat16* e = reinterpret_cast<const __nv_bfloat16*>(&v);
-                                for (int j = 0; j < 8; ++j)
-                                    if (n0 + z * 32 + c + j < a.N) d[j] = e[j];
+#pragma unroll
+                                for (int i = 0; i < 8; ++i)
+                                    if (n0 + q * 8 + i < a.N) o[q * 8 + i] = __float2bfloat16_rn(acc[q * 8 + i]);
                             }
                         }
-                    } else if (n0 + z * 32 + lane < a.N) {
-                        for (int i = 0; i < rows; ++i)
-                            o[i * a.out_stride + z * 32 + lane] = *reinterpret_cast<const __nv_bfloat16*>(stage + i * kOutStride + lane * 2);
                     }
-                    __syncwarp();
+                } else {
+                    // 32 columns at a time through shared memory, so that a warp's store covers whole
+                    // 64-byte pieces of rows
+                    uint8_t* stage = out_stage + (warp - 4) * kOutStage;
+                    const int rows = min(32, mine - (warp & 3) * 32);
+                    __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(a.out) +
+                                       (int64_t)(row0 + (warp & 3) * 32) * a.out_stride + n0;
+    #pragma unroll
+                    for (int z = 0; z < 2; ++z) {
+    #pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            __nv_bfloat162 p[4];
+    #pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                p[i] = __floats2bfloat162_rn(acc[z * 32 + q * 8 + 2 * i], acc[z * 32 + q * 8 + 2 * i + 1]);
+                            *reinterpret_cast<int4*>(stage + lane * kOutStride + q * 16) = *reinterpret_cast<const int4*>(p);
+                        }
+                        __syncwarp();
+                        if (a.out_vec) {
+                            const int c = (lane & 3) * 8;
+                            for (int i = lane >> 2; i < rows; i += 8) {
+                                const int4 v = *reinterpret_cast<const int4*>(stage + i * kOutStride + c * 2);
+                                __nv_bfloat16* d = o + i * a.out_stride + z * 32 + c;
+                                if (n0 + z * 32 + c + 8 <= a.N) {
+                                    *reinterpret_cast<int4*>(d) = v;
+                                } else {
+                                    const __nv_bfloat16* e = reinterpret_cast<const __nv_bfloat16*>(&v);
+                                    for (int j = 0; j < 8; ++j)
+                                        if (n0 + z * 32 + c + j < a.N) d[j] = e[j];
+                                }
+                            }
+                        } else if (n0 + z * 32 + lane < a.N) {
+                            for (int i = 0; i < rows; ++i)
+                                o[i * a.out_stride + z * 32 + lane] = *reinterpret_cast<const __nv_bfloat16*>(stage + i * kOutStride + lane * 2);
+                        }
+                        __syncwarp();
+                    }
                 }
             }
             __syncwarp();
@@ -474,12 +513,13 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
     }
     __syncwarp();
     tc_fence_before();
-    cluster_sync();
+    __syncthreads();
+    if (kCtas == 2) cluster_sync();
     tc_fence_after();
-    if (warp == 2) tmem_free(tmem, 512);
+    if (warp == 2) tmem_free<kCtas>(tmem, 512);
     if (tid == 0 && *abort && a.status) flag(a.status, FLAG_TIMEOUT);
     __syncwarp();
-    cluster_sync();  // neither block ends while the other still frees
+    if (kCtas == 2) cluster_sync();  // neither block ends while the other still frees
 }
 
 // ---- host -------------------------------------------------------------------------
@@ -519,7 +559,7 @@ static ep_status check_products(const char* fn, const ep_fp8_rows* x, const ep_r
         return set_error(EP_ERR_INVALID_ARG, "%s: weight rows %d, channels %d (a multiple of 128)", fn, w->n, w->k);
     if (!w->codes || !w->scales || !aligned16(w->codes))
         return set_error(EP_ERR_INVALID_ARG, "%s: weight codes (16-byte aligned) and scales are required", fn);
-    if (x->rows < 0 || x->rows > 0x7fffffff - kTileM)
+    if (x->rows < 0 || x->rows > 0x7fffffff - 2 * kBM)
         return set_error(EP_ERR_INVALID_ARG, "%s: %lld rows", fn, (long long)x->rows);
     if (x->rows > 0) {
         if (!x->codes || !x->scales || !aligned16(x->codes))
@@ -530,6 +570,32 @@ static ep_status check_products(const char* fn, const ep_fp8_rows* x, const ep_r
     }
     if (g->bases && g->per_base < 1) return set_error(EP_ERR_INVALID_ARG, "%s: groups per base %d", fn, g->per_base);
     if (g->stride < 0) return set_error(EP_ERR_INVALID_ARG, "%s: group stride %lld", fn, (long long)g->stride);
+    return EP_OK;
+}
+
+template <bool kSwiglu, int kCtas>
+static ep_status launch_shape(const char* fn, const CUtensorMap& map_x, const CUtensorMap& map_w, const GemmArgs& a, void* stream) {
+    using Shape = GemmShape<kCtas>;
+    // the tiles are counted in 32 bits: every group's last tile may be partial
+    const int64_t most = ((a.rows + Shape::kTileM - 1) / Shape::kTileM + a.G) * (int64_t)a.n_tiles;
+    if (most > 0x7fffffff) return set_error(EP_ERR_INVALID_ARG, "%s: %lld tiles", fn, (long long)most);
+    int dev = 0, sms = 0;
+    EP_CUDA(cudaGetDevice(&dev));
+    EP_CUDA(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
+    EP_CUDA(cudaFuncSetAttribute(gemm_kernel<kSwiglu, kCtas>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Shape::kSmem));
+    const int units = (int)(most < sms / kCtas ? most : sms / kCtas);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(units * kCtas));
+    cfg.blockDim = dim3(kGemmThreads);
+    cfg.dynamicSmemBytes = Shape::kSmem;
+    cfg.stream = as_stream(stream);
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = kCtas;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    EP_CUDA(cudaLaunchKernelEx(&cfg, gemm_kernel<kSwiglu, kCtas>, map_x, map_w, a));
     return EP_OK;
 }
 
@@ -552,10 +618,6 @@ static ep_status launch_gemm(const char* fn, const ep_fp8_rows* x, const ep_row_
     a.per_base = g->per_base;
     a.group_stride = g->stride;
     a.rows = x->rows;
-    // the tiles are counted in 32 bits: every group's last tile may be partial
-    const int64_t most = ((x->rows + kTileM - 1) / kTileM + w->groups) * (int64_t)a.n_tiles;
-    if (most > 0x7fffffff) return set_error(EP_ERR_INVALID_ARG, "%s: %lld tiles", fn, (long long)most);
-
     CUtensorMap map_x, map_w;
     {
         const cuuint64_t dims[2] = {(cuuint64_t)w->k, (cuuint64_t)x->rows};
@@ -571,15 +633,11 @@ static ep_status launch_gemm(const char* fn, const ep_fp8_rows* x, const ep_row_
         const ep_status st = encode(&map_w, w->codes, 3, dims, strides, box, fn);
         if (st != EP_OK) return st;
     }
-    int dev = 0, sms = 0;
-    EP_CUDA(cudaGetDevice(&dev));
-    EP_CUDA(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
-    const size_t smem = 1024 + kStages * (kStageA + kStageB) + kSumWarps * kOutStage;
-    EP_CUDA(cudaFuncSetAttribute(gemm_kernel<kSwiglu>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
-    const int pairs = (int)(most < sms / 2 ? most : sms / 2);
-    gemm_kernel<kSwiglu><<<2 * pairs, kGemmThreads, smem, as_stream(stream)>>>(map_x, map_w, a);
-    EP_CHECK_LAUNCH(fn);
-    return EP_OK;
+    // Rows of a group: what the arrays hold, shared out.  The regions of the packed layout are sized for
+    // the worst case, a low-latency step fills a few percent of them.
+    const int64_t per_group = x->rows / w->groups / (w->groups > 1 && !g->offsets ? 16 : 1);
+    if (per_group >= kPairRows) return launch_shape<kSwiglu, 2>(fn, map_x, map_w, a, stream);
+    return launch_shape<kSwiglu, 1>(fn, map_x, map_w, a, stream);
 }
 
 }  // namespace ep

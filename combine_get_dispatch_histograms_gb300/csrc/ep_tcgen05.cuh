@@ -89,60 +89,101 @@ __device__ __forceinline__ float ld_shared_f32(uint32_t addr) {
 // over is tensor memory, read through tcgen05.wait::ld, and the fences of
 // tcgen05 order that.  A release here costs the warp 200 (block scope) to 1000
 // cycles (cluster scope) a call, measured.
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
+__device__ __forceinline__ void mbar_hand_back(uint32_t bar) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 // ---- tiled bulk copies (the innermost coordinate is a multiple of 16 bytes) ------
 // Into this block's shared memory; `bar` (a cluster address) counts the bytes,
-// also where it lies in the other block of the pair.
+// with kCtas = 2 also where it lies in the other block of the pair.
 __device__ __forceinline__ void tma_prefetch_desc(const CUtensorMap* m) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
 }
+template <int kCtas>
 __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* m, int x, int y, uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], "
-        "[%2];" ::"r"(smem_u32(dst)),
-        "l"(m), "r"(bar), "r"(x), "r"(y)
-        : "memory");
+    if constexpr (kCtas == 2)
+        asm volatile(
+            "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], "
+            "[%2];" ::"r"(smem_u32(dst)),
+            "l"(m), "r"(bar), "r"(x), "r"(y)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(
+                smem_u32(dst)),
+            "l"(m), "r"(bar), "r"(x), "r"(y)
+            : "memory");
 }
+template <int kCtas>
 __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* m, int x, int y, int z, uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, "
-        "%5}], [%2];" ::"r"(smem_u32(dst)),
-        "l"(m), "r"(bar), "r"(x), "r"(y), "r"(z)
-        : "memory");
+    if constexpr (kCtas == 2)
+        asm volatile(
+            "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, "
+            "%5}], [%2];" ::"r"(smem_u32(dst)),
+            "l"(m), "r"(bar), "r"(x), "r"(y), "r"(z)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], "
+            "[%2];" ::"r"(smem_u32(dst)),
+            "l"(m), "r"(bar), "r"(x), "r"(y), "r"(z)
+            : "memory");
 }
 
-// ---- tensor memory and tcgen05.mma, by pairs of blocks ----------------------------
-__device__ __forceinline__ void tmem_alloc(uint32_t* slot, uint32_t cols) {  // a whole warp of both blocks
-    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)), "r"(cols)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+// ---- tensor memory and tcgen05.mma, by one block or by pairs of blocks ---------------
+// Every tcgen05 instruction of a kernel names the same number of blocks.
+template <int kCtas>
+__device__ __forceinline__ void tmem_alloc(uint32_t* slot, uint32_t cols) {  // a whole warp (of both blocks)
+    if constexpr (kCtas == 2) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)), "r"(cols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    } else {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)), "r"(cols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
 }
+template <int kCtas>
 __device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t cols) {  // the same warps
-    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
+    if constexpr (kCtas == 2)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
+    else
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
 }
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
-// D[256 x N] (+)= A[256 x 32] B[N x 32]^T, e4m3 operands in shared memory: each
-// block of the pair holds half of A's rows, half of B's rows and the
-// accumulator rows of its half of A.  Issued by one thread of block 0.
+// D[kCtas * 128 x N] (+)= A[kCtas * 128 x 32] B[N x 32]^T, e4m3 operands in
+// shared memory.  With two blocks each holds half of A's rows, half of B's rows
+// and the accumulator rows of its half of A; one thread of block 0 issues.
+template <int kCtas>
 __device__ __forceinline__ void mma_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
-        : "memory");
+    if constexpr (kCtas == 2)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.u32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.u32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+            : "memory");
 }
-// Arrives on `bar` of both blocks when every tcgen05.mma this thread issued has finished.
+// Arrives on `bar` (of both blocks) when every tcgen05.mma this thread issued has finished.
+template <int kCtas>
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
-    asm volatile(
-        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-        "h"((uint16_t)3)
-        : "memory");
+    if constexpr (kCtas == 2)
+        asm volatile(
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+            "h"((uint16_t)3)
+            : "memory");
+    else
+        asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
 // Consecutive columns of this warp's 32 lanes: thread i gets lane i's row.
 __device__ __forceinline__ void tmem_ld(uint32_t addr, float (&v)[32]) {

@@ -29,11 +29,12 @@ def case(counts, K, N, seed=0, gap=0):
 
 
 RAGGED = [0, 1, 7, 128, 129, 31, 0, 255, 300, 0]
+LONG = [300, 0, 513, 256, 1, 255, 640]   # long groups: pairs of blocks, with full, half-full and one-row tiles
 
 
 @gpu
 @pytest.mark.parametrize("K,N", [(128, 128), (128, 1), (256, 130), (640, 256), (1408, 600), (2048, 1099), (512, 8), (384, 257)])
-@pytest.mark.parametrize("counts", [[1], [5, 0, 64], RAGGED])
+@pytest.mark.parametrize("counts", [[1], [5, 0, 64], RAGGED, LONG])
 def test_gemm_ragged(K, N, counts):
     cnt, off, hoff, x, xs, w, ws = case(counts, K, N, seed=K + N, gap=3)
     st = ep.new_status()
@@ -51,7 +52,7 @@ def test_gemm_ragged(K, N, counts):
 
 @gpu
 @pytest.mark.parametrize("K,I", [(128, 128), (640, 384), (1024, 256), (4096, 128)])
-@pytest.mark.parametrize("counts", [[1], [5, 0, 64], RAGGED])
+@pytest.mark.parametrize("counts", [[1], [5, 0, 64], RAGGED, LONG])
 def test_swiglu_ragged(K, I, counts):
     cnt, off, hoff, x, xs, w, ws = case(counts, K, 2 * I, seed=K + I, gap=2)
     st = ep.new_status()
