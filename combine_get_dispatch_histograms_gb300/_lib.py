@@ -113,6 +113,8 @@ def library_path() -> str:
 def load(build_if_missing: bool = True):
     """Load libep_gb300.so (building it with nvcc if it is missing or stale)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib

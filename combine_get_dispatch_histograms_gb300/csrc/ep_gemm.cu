@@ -8,7 +8,7 @@
 // block's accumulator leaves tensor memory and is added, times sx * sw, to an
 // fp32 sum in registers.  One thread owns one row and 128 columns of the tile,
 // so that factor is one scalar per thread and block.
-#include <cstdlib>
+#include <atomic>
 
 #include "ep_fp8.cuh"
 #include "ep_tcgen05.cuh"
@@ -581,8 +581,13 @@ static ep_status launch_shape(const char* fn, const CUtensorMap& map_x, const CU
     if (most > 0x7fffffff) return set_error(EP_ERR_INVALID_ARG, "%s: %lld tiles", fn, (long long)most);
     int dev = 0, sms = 0;
     EP_CUDA(cudaGetDevice(&dev));
-    EP_CUDA(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
-    EP_CUDA(cudaFuncSetAttribute(gemm_kernel<kSwiglu, kCtas>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Shape::kSmem));
+    static std::atomic<int> known[kMaxDevicesTracked];  // SMs of a device whose launch attribute is set
+    if (dev < kMaxDevicesTracked) sms = known[dev].load(std::memory_order_relaxed);
+    if (sms == 0) {
+        EP_CUDA(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
+        EP_CUDA(cudaFuncSetAttribute(gemm_kernel<kSwiglu, kCtas>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Shape::kSmem));
+        if (dev < kMaxDevicesTracked) known[dev].store(sms, std::memory_order_relaxed);
+    }
     const int units = (int)(most < sms / kCtas ? most : sms / kCtas);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(units * kCtas));

@@ -19,6 +19,7 @@
 //
 // Work items are (expert, 16 channels of gate and up) and (32 output channels,
 // expert); each block takes a contiguous run of them, equal to within one.
+#include <atomic>
 #include <type_traits>
 
 #include "ep_fp8.cuh"
@@ -432,8 +433,15 @@ static TokWorkspace tok_workspace(int T, int K, int H, int I, int blocks) {
 template <bool kFp8>
 static ep_status launch_tokens(TokArgs a, const ep_moe_weights* w, int sms, const TokWorkspace& ws, uint8_t* mem, cudaStream_t st) {
     const size_t smem = tok_smem(a.T, a.K, a.list);
-    EP_CUDA(cudaFuncSetAttribute(tok_kernel<false, kFp8>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
-    EP_CUDA(cudaFuncSetAttribute(tok_kernel<true, kFp8>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+    int dev = 0;
+    EP_CUDA(cudaGetDevice(&dev));
+    static std::atomic<bool> known[kMaxDevicesTracked];  // devices whose launch attributes are set
+    if (dev >= kMaxDevicesTracked || !known[dev].load(std::memory_order_relaxed)) {
+        const int most = (int)tok_smem(kTokMax, kMaxTopk, kTokMax * kMaxTopk);
+        EP_CUDA(cudaFuncSetAttribute(tok_kernel<false, kFp8>, cudaFuncAttributeMaxDynamicSharedMemorySize, most));
+        EP_CUDA(cudaFuncSetAttribute(tok_kernel<true, kFp8>, cudaFuncAttributeMaxDynamicSharedMemorySize, most));
+        if (dev < kMaxDevicesTracked) known[dev].store(true, std::memory_order_relaxed);
+    }
     a.h_hi = reinterpret_cast<__nv_bfloat16*>(mem);
     a.h_lo = reinterpret_cast<__nv_bfloat16*>(mem + ws.h_lo);
     a.part = reinterpret_cast<float*>(mem + ws.part);
