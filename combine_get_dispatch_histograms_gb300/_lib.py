@@ -84,7 +84,7 @@ SIGNATURES = {
                              P, P]),
     "ep_expert_swiglu": (INT, [ctypes.POINTER(EpFp8Rows), ctypes.POINTER(EpRowGroups), ctypes.POINTER(EpFp8Weight), P,
                                I64, P, I64, P, P]),
-    "ep_moe_tokens_workspace": (I64, [I32, I32, I32, I32]),
+    "ep_moe_tokens_workspace": (I64, [I32, I32, ctypes.POINTER(EpMoeWeights)]),
     "ep_moe_tokens": (INT, [P, I64, I32, P, P, I32, ctypes.POINTER(EpMoeWeights), P, I64, P, I64, P, P]),
     "ep_ll_message_bytes": (I64, [INT]),
     "ep_ll_size_hint": (I64, [INT, INT, INT, INT]),

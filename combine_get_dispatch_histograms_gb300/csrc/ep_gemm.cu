@@ -161,16 +161,6 @@ struct TileWalk {
     }
 };
 
-// silu(g) * u with the approximate power and reciprocal, each off by a few
-// 2^-23 of itself, as the product's own sum is.  For g below about -88 the power is
-// infinite and the result -0.
-__device__ __forceinline__ float silu_mul(float g, float u) {
-    float e, r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
-    return g * r * u;
-}
-
 // kSwiglu: the tile's 256 weight rows are 128 gate rows and the 128 up rows of
 // the same channels; otherwise 256 consecutive rows.
 template <bool kSwiglu, int kCtas>
@@ -523,34 +513,6 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
 }
 
 // ---- host -------------------------------------------------------------------------
-using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-static EncodeTiled encode_tiled() {
-    static const EncodeTiled fn = [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-            q != cudaDriverEntryPointSuccess)
-            p = nullptr;
-        return reinterpret_cast<EncodeTiled>(p);
-    }();
-    return fn;
-}
-
-static ep_status encode(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
-                        const cuuint32_t* box, const char* what) {
-    const EncodeTiled fn = encode_tiled();
-    if (!fn) return set_error(EP_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
-    const cuuint32_t ones[3] = {1, 1, 1};
-    const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, rank, const_cast<void*>(base), dims, strides, box, ones,
-                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    if (r != CUDA_SUCCESS) return set_error(EP_ERR_INVALID_ARG, "%s: the tensor map was refused (%d)", what, (int)r);
-    return EP_OK;
-}
-
 static ep_status check_products(const char* fn, const ep_fp8_rows* x, const ep_row_groups* g, const ep_fp8_weight* w) {
     if (!x || !g || !w) return set_error(EP_ERR_INVALID_ARG, "%s: null descriptor", fn);
     if (w->groups < 1 || w->groups > kMaxGroups)
@@ -628,14 +590,14 @@ static ep_status launch_gemm(const char* fn, const ep_fp8_rows* x, const ep_row_
         const cuuint64_t dims[2] = {(cuuint64_t)w->k, (cuuint64_t)x->rows};
         const cuuint64_t strides[1] = {(cuuint64_t)x->code_stride};
         const cuuint32_t box[2] = {kBK, kBoxRows};
-        const ep_status st = encode(&map_x, x->codes, 2, dims, strides, box, fn);
+        const ep_status st = encode_rows(&map_x, x->codes, 2, dims, strides, box, fn);
         if (st != EP_OK) return st;
     }
     {
         const cuuint64_t dims[3] = {(cuuint64_t)w->k, (cuuint64_t)w->n, (cuuint64_t)w->groups};
         const cuuint64_t strides[2] = {(cuuint64_t)w->k, (cuuint64_t)w->k * (cuuint64_t)w->n};
         const cuuint32_t box[3] = {kBK, 128, 1};
-        const ep_status st = encode(&map_w, w->codes, 3, dims, strides, box, fn);
+        const ep_status st = encode_rows(&map_w, w->codes, 3, dims, strides, box, fn);
         if (st != EP_OK) return st;
     }
     // Rows of a group: what the arrays hold, shared out.  The regions of the packed layout are sized for

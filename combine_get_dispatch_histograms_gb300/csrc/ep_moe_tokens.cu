@@ -3,38 +3,55 @@
 //
 // Mathematics.  For token t with choices e = topk_idx[t][k], weights v[t][k]:
 //   h[t,e] = silu(Wg[e] x[t]) * (Wu[e] x[t]),   out[t] = sum_k v[t][k] * W2[e] h[t,e].
-// Kernel 1 computes h for every (token, expert) pair, kernel 2 the weighted sum.
+// Kernel 1 leaves the sums Wg x and Wu x of every (token, expert) pair in fp32,
+// kernel 2 forms h from them and the weighted sum.
 //
 // Bound.  Each weight byte of the experts that any token chose is read once;
-// with one to a few tokens per expert the operations are far below the tensor
-// cores' rate, so the kernels are bound by that stream.  One block per SM,
-// every thread feeds itself through a private ring of asynchronous 16-byte
-// copies (no barrier between copy and use), and 16 warps split the channels of
-// the reduction.  The product is the register-operand m16n8k16 form with the
-// weights as its 16 rows and up to 8 tokens as its columns: a warp's weights go
-// from shared memory through registers (e4m3 to bf16, exact) straight into it,
-// where a tensor-memory product would need them back in shared memory.  The
-// order of k inside a product is free, so each thread's 16 consecutive bytes
-// of a weight row are its fragments and no data moves between threads.
+// with one to a few tokens per expert that stream bounds the time.  So the
+// weights are the 128 rows of the tensor-core product and go from memory to
+// shared memory by tiled copies and nowhere else; the few tokens are its
+// columns, written beside them by warps that convert them block by block:
+//   fp8 weights: a token's 128 channels times a power of two are split into
+//     e4m3 pieces, v = p1 + p2 / 16 (+ p3 / 256), each a column of its own; two
+//     pieces hold a bf16 value exactly (8 bits of significand; an element below
+//     2^-13 of its block's largest is off by at most 2^-21 of that), three hold
+//     h to 2^-13 of itself;
+//   bf16 weights: x itself, and h as the sum of two bf16.
+// A block of 128 channels is one accumulator; it leaves tensor memory, times its
+// weight scale and the tokens' powers of two, for an fp32 sum in registers.
 //
-// Work items are (expert, 16 channels of gate and up) and (32 output channels,
-// expert); each block takes a contiguous run of them, equal to within one.
+// Work items are (expert, 64 gate + 64 up channels, part of K) in kernel 1 and
+// (128 output channels, expert, block of K) in kernel 2; each thread block takes
+// a contiguous run of them, equal to within one.
 #include <atomic>
-#include <type_traits>
 
 #include "ep_fp8.cuh"
+#include "ep_tcgen05.cuh"
 
 namespace ep {
 
-constexpr int kTokMax = 64;                 // tokens of a call: an expert's tokens are one 64-bit mask
-constexpr int kTokThreads = 512;
-constexpr int kTokWarps = kTokThreads / 32;
-constexpr int kTokRing = 4;                 // copies in flight per thread: kTokRing - 1 stages
-constexpr int kTokStage = 64;               // bytes of a weight row per stage
-constexpr int kTokRows = 32;                // weight rows of an item
-constexpr int kTokSlots = 16;               // tokens of a pass over an item's weights
-constexpr int kPartStride = kTokSlots + 1;  // floats: consecutive rows fall into other banks
-constexpr int kPartFloats = kTokWarps * kTokRows * kPartStride;
+constexpr int kTokMax = 64;        // tokens of a call: an expert's tokens are one 64-bit mask
+constexpr int kTokThreads = 512;   // copy, mma, tensor-memory and spare warp; 8 that convert; 4 that sum
+constexpr int kTokFillMost = 8;    // warps that convert tokens, at most
+constexpr int kTokSlots = 16;      // tokens of a list entry: an expert with more has several, next to each other
+constexpr int kTokRows = 128;      // weight rows of an item
+constexpr int kTokBytes = 128;     // of a weight row per stage
+constexpr int kTokScaleRing = 16;  // stages whose powers of two are kept: more than are ever between writer and reader
+constexpr int64_t kTokWaitNs = 2000000000ll;
+
+template <bool kDown, bool kFp8>
+struct TokShape {
+    static constexpr int kPieces = kFp8 ? (kDown ? 3 : 2) : (kDown ? 2 : 1);  // columns of a token
+    static constexpr int kCols = kTokSlots * kPieces;
+    static constexpr int kStageA = kTokRows * kTokBytes, kStage = kStageA + kCols * kTokBytes;
+    static constexpr int kStages = kDown ? (kFp8 ? 7 : 8) : 10;
+    static constexpr int kChannels = kFp8 ? 128 : 64;  // of a stage
+    // Each converting warp takes every kFill-th stage.  When it waits for the stage before its next one
+    // to be done, it knows its own last one to be filled, so that stage kFill + kStages back is done; a
+    // wait by parity is unambiguous if that is not later than 2 kStages back.
+    static constexpr int kFill = kStages < kTokFillMost ? kStages : kTokFillMost;
+    static_assert(kFill <= kStages, "a wait by parity could pass a whole round early");
+};
 
 struct TokArgs {
     const __nv_bfloat16* x;
@@ -42,66 +59,48 @@ struct TokArgs {
     const int64_t* topk_idx;
     const float* topk_weights;
     int T, K, E, H, I;
-    const uint8_t* w;       // w13 in kernel 1, w2 in kernel 2
-    const float* ws;        // their scales (e4m3 only)
-    int stages;             // of a weight row
-    int warps;              // that share a row's stages
-    int list;               // entries of the expert list: min(E, T * K)
-    __nv_bfloat16 *h_hi, *h_lo;  // [pairs][I]: h as the sum of two bf16, 16 bits of mantissa
-    float* part;            // [blocks][2][T][kTokRows] sums of a chunk that several blocks share
-    uint32_t* done;         // [H / kTokRows] blocks that have written theirs
+    const float* ws;        // scales of w13 in kernel 1, of w2 in kernel 2 (e4m3 only)
+    int blocks_k;           // stages of a weight row
+    int split;              // parts of K in kernel 1
+    int list;               // entries of the expert list, at most
+    float* sums;            // [split][T * K][2 I]: Wg x, then Wu x, of each pair
+    float* part;            // [blocks][2][T][kTokRows]: sums of a tile that several blocks share
+    uint32_t* done;         // [output tiles]: blocks that have written theirs
     __nv_bfloat16* out;
     int64_t out_stride;
     uint32_t* status;
 };
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-    asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                         uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-// Four e4m3 codes to two bf16 pairs; exact, as bf16 holds every e4m3 value.
-__device__ __forceinline__ void e4m3x4_to_bf16(uint32_t c, uint32_t& lo, uint32_t& hi) {
-    const __half2_raw a = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(c & 0xffffu), __NV_E4M3);
-    const __half2_raw b = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(c >> 16), __NV_E4M3);
-    const float2 fa = __half22float2(__half2(a)), fb = __half22float2(__half2(b));
-    const __nv_bfloat162 ba = __floats2bfloat162_rn(fa.x, fa.y), bb = __floats2bfloat162_rn(fb.x, fb.y);
-    lo = *reinterpret_cast<const uint32_t*>(&ba);
-    hi = *reinterpret_cast<const uint32_t*>(&bb);
-}
-
-struct TokShared {
-    uint8_t* ring;      // [kTokRing][4][kTokThreads] 16-byte pieces
-    float* part;        // [2][kPartFloats]
-    float* acc;         // [T][kTokRows] (kernel 2)
-    float* weight;      // [pairs] (kernel 2)
-    uint16_t* expert;   // [list]
-    uint16_t* base;     // [list + 1]: pairs of entry i are base[i] .. base[i + 1] - 1
-    uint8_t* token;     // [pairs]
+struct TokBarriers {
+    uint64_t copied[10], filled[10], done[10], acc_empty[2], drain;
+    uint32_t tmem;
+    int abort, last;
+    float scale[kTokScaleRing][kTokSlots];
 };
 
-__host__ __device__ inline size_t tok_smem(int T, int K, int list) {
-    const size_t pairs = (size_t)T * K;
-    return (size_t)kTokRing * 4 * 16 * kTokThreads + 2 * sizeof(float) * kPartFloats + sizeof(float) * T * kTokRows +
-           sizeof(float) * pairs + sizeof(uint16_t) * (2 * list + 2) + pairs + 16;
+struct TokLists {
+    float* acc;        // [T][kTokRows] (kernel 2)
+    float* weight;     // [pairs] (kernel 2)
+    uint16_t* expert;  // [list]
+    uint16_t* base;    // [list + 1]: pairs of entry i are base[i] .. base[i + 1] - 1
+    uint8_t* token;    // [pairs]
+};
+
+template <bool kDown, bool kFp8>
+constexpr size_t tok_smem(int T, int K, int list) {
+    using Shape = TokShape<kDown, kFp8>;
+    return 1024 + (size_t)Shape::kStages * Shape::kStage + (kDown ? sizeof(float) * T * (kTokRows + K) : 0) +
+           sizeof(uint16_t) * (2 * list + 2) + (size_t)T * K + 16;
 }
 
-// The experts that some token chose, ascending, and their tokens, ascending.
-// Every block builds the list for itself.  Returns the number of experts.
+// The experts that some token chose, ascending, and their tokens, ascending, at
+// most kTokSlots to an entry.  Every block builds the list for itself.  Returns
+// the number of entries.
 template <bool kDown>
-__device__ __forceinline__ int build_list(const TokArgs& a, const TokShared& s) {
-    __shared__ int scan[kTokWarps];
-    unsigned long long* mask = reinterpret_cast<unsigned long long*>(s.part);       // [E], 32 KB at most
+__device__ __forceinline__ int build_list(const TokArgs& a, const TokLists& s, uint8_t* scratch) {
+    constexpr int kWarps = kTokThreads / 32;
+    __shared__ int scan[kWarps];
+    unsigned long long* mask = reinterpret_cast<unsigned long long*>(scratch);      // [E], 32 KB at most
     uint16_t* pair_expert = reinterpret_cast<uint16_t*>(mask + kMaxExperts);        // [pairs]
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     for (int e = tid; e < a.E; e += kTokThreads) mask[e] = 0;
@@ -113,8 +112,11 @@ __device__ __forceinline__ int build_list(const TokArgs& a, const TokShared& s) 
     }
     __syncthreads();
     const int per = (a.E + kTokThreads - 1) / kTokThreads, e0 = min(a.E, tid * per), e1 = min(a.E, e0 + per);
-    int sum = 0;  // experts in the high half, pairs in the low: both at most 2048
-    for (int e = e0; e < e1; ++e) sum += mask[e] ? (1 << 16) + __popcll(mask[e]) : 0;
+    int sum = 0;  // entries in the high half, pairs in the low: at most 2176 and 2048
+    for (int e = e0; e < e1; ++e) {
+        const int m = __popcll(mask[e]);
+        sum += ((m + kTokSlots - 1) / kTokSlots << 16) + m;
+    }
     int inc = sum;
     for (int o = 1; o < 32; o <<= 1) {
         const int v = __shfl_up_sync(0xffffffffu, inc, o);
@@ -123,19 +125,19 @@ __device__ __forceinline__ int build_list(const TokArgs& a, const TokShared& s) 
     if (lane == 31) scan[warp] = inc;
     __syncthreads();
     int at = inc - sum, total = 0;
-    for (int w = 0; w < kTokWarps; ++w) {
+    for (int w = 0; w < kWarps; ++w) {
         if (w < warp) at += scan[w];
         total += scan[w];
     }
     for (int e = e0; e < e1; ++e) {
         unsigned long long m = mask[e];
-        if (!m) continue;
-        const int i = at >> 16;
-        int p = at & 0xffff;
-        s.expert[i] = (uint16_t)e;
-        s.base[i] = (uint16_t)p;
-        at += (1 << 16) + __popcll(m);
-        for (; m; m &= m - 1, ++p) {
+        for (int z = 0; m; m &= m - 1, ++z, ++at) {
+            const int p = at & 0xffff;
+            if (z % kTokSlots == 0) {
+                s.expert[at >> 16] = (uint16_t)e;
+                s.base[at >> 16] = (uint16_t)p;
+                at += 1 << 16;
+            }
             s.token[p] = (uint8_t)(__ffsll(m) - 1);
             pair_expert[p] = (uint16_t)e;
         }
@@ -156,323 +158,466 @@ __device__ __forceinline__ int build_list(const TokArgs& a, const TokShared& s) 
     return total >> 16;
 }
 
+// The runs of one block: an entry's tile and a range of its blocks of K.
+// Kernel 1 takes every `step`-th item, so that the tiles of one entry, and what
+// they cost, are spread over the blocks.  Kernel 2 takes a contiguous range of
+// the blocks of K, tile after tile, so that most of a tile's entries meet in
+// one block's sum.
+template <bool kDown>
+struct TokRuns {
+    int at, end, step, A, tiles, blocks_k, split;
+    int ai, tile, k0, k1, part;
+    __device__ __forceinline__ bool next() {
+        if (at >= end) return false;
+        if constexpr (kDown) {
+            const int item = at / blocks_k;
+            k0 = at - item * blocks_k;
+            k1 = min(blocks_k, k0 + end - at);
+            tile = item / A;
+            ai = item - tile * A;
+            part = 0;
+            at += k1 - k0;
+        } else {
+            const int item = at / split;
+            part = at - item * split;
+            ai = item / tiles;
+            tile = item - ai * tiles;
+            k0 = part * blocks_k / split;
+            k1 = (part + 1) * blocks_k / split;
+            at += step;
+        }
+        return true;
+    }
+};
+
+__device__ __forceinline__ uint32_t pack_e4m3(float a, float b, float c, float d) {
+    return (e4m3x2(a, b) & 0xffffu) | (e4m3x2(c, d) << 16);
+}
+// v[0..3] minus the values of their codes, times 16: what the next piece holds.
+__device__ __forceinline__ void next_piece(float* v, uint32_t codes) {
+    const float2 lo = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(codes & 0xffffu), __NV_E4M3)));
+    const float2 hi = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(codes >> 16), __NV_E4M3)));
+    v[0] = (v[0] - lo.x) * 16.0f;
+    v[1] = (v[1] - lo.y) * 16.0f;
+    v[2] = (v[2] - hi.x) * 16.0f;
+    v[3] = (v[3] - hi.y) * 16.0f;
+}
+
+// h of kN channels of a pair from the parts of its sums.
+template <int kN>
+__device__ __forceinline__ void load_h(const TokArgs& a, int pair, int ch, float* v) {
+    float g[kN] = {}, u[kN] = {};
+    const int64_t part = (int64_t)a.T * a.K * 2 * a.I;
+    const float* p = a.sums + (int64_t)pair * 2 * a.I + ch;
+    for (int s = 0; s < a.split; ++s, p += part) {
+        if constexpr (kN == 4) {
+            const float4 x = *reinterpret_cast<const float4*>(p), y = *reinterpret_cast<const float4*>(p + a.I);
+            g[0] += x.x, g[1] += x.y, g[2] += x.z, g[3] += x.w;
+            u[0] += y.x, u[1] += y.y, u[2] += y.z, u[3] += y.w;
+        } else {
+            const float2 x = *reinterpret_cast<const float2*>(p), y = *reinterpret_cast<const float2*>(p + a.I);
+            g[0] += x.x, g[1] += x.y;
+            u[0] += y.x, u[1] += y.y;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kN; ++i) v[i] = g[i] / (1.0f + __expf(-g[i])) * u[i];
+}
+
 // kDown: kernel 2.  kFp8: e4m3 weights with block scales, otherwise bf16.
 template <bool kDown, bool kFp8>
-__global__ void __launch_bounds__(kTokThreads, 1) tok_kernel(const TokArgs a) {
-    extern __shared__ __align__(16) uint8_t dyn[];
-    __shared__ int last;
-    TokShared s;
-    s.ring = dyn;
-    s.part = reinterpret_cast<float*>(dyn + kTokRing * 4 * 16 * kTokThreads);
-    s.acc = s.part + 2 * kPartFloats;
-    s.weight = s.acc + a.T * kTokRows;
-    s.expert = reinterpret_cast<uint16_t*>(s.weight + a.T * a.K);
+__global__ void __launch_bounds__(kTokThreads, 1) tok_kernel(const __grid_constant__ CUtensorMap map_w, const TokArgs a) {
+    using Shape = TokShape<kDown, kFp8>;
+    constexpr int kStages = Shape::kStages, kPieces = Shape::kPieces;
+    extern __shared__ __align__(1024) uint8_t dyn[];
+    __shared__ TokBarriers sh;
+    uint8_t* ring = dyn + ((1024u - (smem_u32(dyn) & 1023u)) & 1023u);
+    TokLists s;
+    s.acc = reinterpret_cast<float*>(ring + kStages * Shape::kStage);
+    s.weight = s.acc + (kDown ? a.T * kTokRows : 0);
+    s.expert = reinterpret_cast<uint16_t*>(s.weight + (kDown ? a.T * a.K : 0));
     s.base = s.expert + a.list;
     s.token = reinterpret_cast<uint8_t*>(s.base + a.list + 1);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q = lane & 3;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    volatile int* abort = &sh.abort;
+    const uint32_t copied = smem_u32(sh.copied), filled = smem_u32(sh.filled), done = smem_u32(sh.done);
+    const uint32_t acc_empty = smem_u32(sh.acc_empty);
 
     if constexpr (!kDown) {
         asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
         if (blockIdx.x == 0)
-            for (int i = tid; i < a.H / kTokRows; i += kTokThreads) a.done[i] = 0;
+            for (int i = tid; i < (a.H + kTokRows - 1) / kTokRows; i += kTokThreads) a.done[i] = 0;
     }
-    const int A = build_list<kDown>(a, s);
+    if (tid == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(&sh.copied[i], 1);
+            mbar_init(&sh.filled[i], 1);
+            mbar_init(&sh.done[i], 1);
+        }
+        mbar_init(&sh.acc_empty[0], 4);
+        mbar_init(&sh.acc_empty[1], 4);
+        mbar_init(&sh.drain, 1);
+        sh.abort = 0;
+        fence_mbar_init();
+        tma_prefetch_desc(&map_w);
+    }
+    if (warp == 2) tmem_alloc<1>(&sh.tmem, 128);
+    const int A = build_list<kDown>(a, s, ring);
+    fence_proxy_async_smem();  // the list's scratch becomes the ring
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sh.tmem;
 
-    const int chunks = kDown ? a.H / kTokRows : a.I / (kTokRows / 2);
-    const int64_t total = (int64_t)A * chunks;
-    const int64_t blocks = total < gridDim.x ? (total > 0 ? total : 1) : gridDim.x;  // each has an item; the rest are idle
-    const bool idle = blockIdx.x >= blocks;
-    const int64_t i0 = idle ? total : total * blockIdx.x / blocks, i1 = idle ? total : total * (blockIdx.x + 1) / blocks;
-    const int64_t row_bytes = (int64_t)a.stages * kTokStage;
-    const int64_t rows = kDown ? a.H : 2 * (int64_t)a.I;  // of one expert
-    const int KB = (a.stages + 1) / 2;                    // scale blocks of a row (e4m3)
-    const int outer = kDown ? A : chunks;                 // length of the inner index of an item
-    const int my_stages = warp < a.warps ? (a.stages - warp + a.warps - 1) / a.warps : 0;
+    const int tiles = kDown ? (a.H + kTokRows - 1) / kTokRows : (a.I + kTokRows / 2 - 1) / (kTokRows / 2);
+    const int total = A * tiles * (kDown ? a.blocks_k : a.split);
+    const int blocks = max(1, min(total, (int)gridDim.x));  // each has work; the rest are idle
+    auto first_of = [&](int b) { return (int)((int64_t)total * b / blocks); };
+    TokRuns<kDown> run;
+    const bool idle = (int)blockIdx.x >= blocks;
+    run.at = idle ? total : kDown ? first_of(blockIdx.x) : blockIdx.x;
+    run.end = idle || !kDown ? total : first_of(blockIdx.x + 1);
+    run.step = blocks;
+    run.A = A;
+    run.tiles = tiles;
+    run.blocks_k = a.blocks_k;
+    run.split = a.split;
+    const int begin = run.at;
 
-    // ---- copies: stage after stage of pass after pass of item after item ----------
-    int64_t c_item = i0;
-    int c_hi = outer ? (int)(i0 / outer) : 0, c_lo = outer ? (int)(i0 % outer) : 0, c_pass = 0, c_j = 0, c_slot = 0;
-    const uint8_t* c_row = nullptr;
-    auto locate = [&] {  // the thread's first weight row of the item, at its 16 bytes of a stage
-        const int e = s.expert[kDown ? c_lo : c_hi], chunk = kDown ? c_hi : c_lo;
-        c_row = a.w + ((int64_t)e * rows + chunk * (kDown ? 32 : 16) + g) * row_bytes + q * 16;
-    };
-    if (c_item < i1) locate();
-    const int64_t up = kDown ? 8 * row_bytes : a.I * row_bytes;   // rows 8..15 of a product
-    const int64_t next = kDown ? 16 * row_bytes : 8 * row_bytes;  // the second product's rows
-    const uint32_t ring = smem_u32(s.ring) + tid * 16;
-    auto copy = [&] {
-        if (c_item < i1 && my_stages > 0) {
-            const uint8_t* p = c_row + (int64_t)(warp + c_j * a.warps) * kTokStage;
-            const uint32_t d = ring + c_slot * (4 * 16 * kTokThreads);
-            cp_async16(d, p);
-            cp_async16(d + 16 * kTokThreads, p + up);
-            cp_async16(d + 32 * kTokThreads, p + next);
-            cp_async16(d + 48 * kTokThreads, p + next + up);
-            c_slot = c_slot + 1 == kTokRing ? 0 : c_slot + 1;
-            if (++c_j == my_stages) {
-                c_j = 0;
-                const int i = kDown ? c_lo : c_hi;
-                if (++c_pass * kTokSlots >= s.base[i + 1] - s.base[i]) {
-                    c_pass = 0;
-                    ++c_item;
-                    if (++c_lo == outer) {
-                        c_lo = 0;
-                        ++c_hi;
+    if (warp == 0) {
+        if (lane == 0) {
+            // ---- weights: two boxes of 64 rows a stage ----------------------------
+            uint32_t n = 0;
+            bool ok = true;
+            while (ok && run.next()) {
+                const int e = s.expert[run.ai];
+                const int r0 = kDown ? run.tile * kTokRows : run.tile * (kTokRows / 2), r1 = kDown ? r0 + 64 : a.I + r0;
+                for (int k = run.k0; k < run.k1; ++k, ++n) {
+                    const uint32_t u = n % kStages;
+                    if (!mbar_wait_or_abort(done + u * 8, n / kStages & 1 ^ 1, kTokWaitNs, abort)) {
+                        ok = false;
+                        break;
                     }
-                    if (c_item < i1) locate();
+                    uint8_t* st = ring + u * Shape::kStage;
+                    mbar_arrive_expect_tx(&sh.copied[u], Shape::kStageA);
+                    tma_load_3d<1>(st, &map_w, k * kTokBytes, r0, e, copied + u * 8);
+                    tma_load_3d<1>(st + 64 * kTokBytes, &map_w, k * kTokBytes, r1, e, copied + u * 8);
                 }
             }
+            // no copy may be in flight when the block ends, also after a wait that ran out
+            for (uint32_t i = n > kStages ? n - kStages : 0; i < n; ++i)
+                mbar_wait_bounded(&sh.copied[i % kStages], i / kStages & 1, kTokWaitNs);
         }
-        cp_async_commit();
-    };
-    for (int i = 0; i < kTokRing - 1; ++i) copy();
-
-    if constexpr (kDown) asm volatile("griddepcontrol.wait;" ::: "memory");  // h and the counters of kernel 1
-
-    if (kDown && A == 0)
-        for (int64_t i = blockIdx.x * (int64_t)kTokThreads + tid; i < (int64_t)a.T * a.H; i += (int64_t)gridDim.x * kTokThreads)
-            a.out[i / a.H * a.out_stride + i % a.H] = __float2bfloat16_rn(0.0f);
-
-    int slot = 0, buf = 0;
-    int hi = outer ? (int)(i0 / outer) : 0, lo = outer ? (int)(i0 % outer) : 0;
-    for (int64_t item = i0; item < i1; ++item) {
-        const int ai = kDown ? lo : hi, chunk = kDown ? hi : lo;
-        const int e = s.expert[ai], p0 = s.base[ai], m = s.base[ai + 1] - p0;
-        const float* sc = nullptr;
-        int64_t sc_up = 0;
-        if constexpr (kFp8) {
-            sc = a.ws + ((int64_t)e * (rows / 128) + (kDown ? chunk * 32 : chunk * 16) / 128) * KB;
-            sc_up = kDown ? 0 : (int64_t)(a.I / 128) * KB;
-        }
-        for (int first = 0; first < m; first += kTokSlots) {
-            const int cnt = min(kTokSlots, m - first);
-            float tot[2][2][4];
+    } else if (warp == 1) {
+        // ---- products: one block of K per accumulator, two accumulators ------------
+        const uint32_t idesc = kFp8 ? idesc_e4m3(kTokRows, Shape::kCols) : idesc_bf16(kTokRows, Shape::kCols);
+        const uint64_t d0 = smem_desc_sw128(ring);
+        uint32_t n = 0;
+        while (run.next()) {
+#pragma unroll 1
+            for (int k = run.k0; k < run.k1; ++k, ++n) {
+                const uint32_t u = n % kStages, ph = n / kStages & 1;
+                mbar_wait_warp(copied + u * 8, ph, kTokWaitNs, abort);
+                mbar_wait_warp(filled + u * 8, ph, kTokWaitNs, abort);
+                mbar_wait_warp(acc_empty + (n & 1) * 8, n >> 1 & 1 ^ 1, kTokWaitNs, abort);
+                tc_fence_after();
+                const uint64_t da = d0 + u * (Shape::kStage >> 4), db = da + (Shape::kStageA >> 4);
+                if (elect_one()) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) (&tot[0][0][0])[i] = 0.0f;
-
-            auto pass = [&](auto nt_tag) {
-                constexpr int NT = decltype(nt_tag)::value;
-                constexpr int kElems = kFp8 ? 16 : 8;          // of a thread's 16 bytes
-                constexpr int kB = kDown ? 2 : 1;              // h comes as two bf16
-                const __nv_bfloat16* xb[NT][kB];
-                bool have[NT];
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    have[n] = g + 8 * n < cnt;
-                    const int pair = p0 + first + (have[n] ? g + 8 * n : 0);
-                    if constexpr (kDown) {
-                        xb[n][0] = a.h_hi + (int64_t)pair * a.I + q * kElems;
-                        xb[n][1] = a.h_lo + (int64_t)pair * a.I + q * kElems;
-                    } else {
-                        xb[n][0] = a.x + s.token[pair] * a.x_stride + q * kElems;
+                    for (int q = 0; q < 4; ++q) {
+                        if constexpr (kFp8) mma_e4m3<1>(tmem + (n & 1) * 64, da + q * 2, db + q * 2, idesc, q > 0);
+                        else mma_bf16_ss(tmem + (n & 1) * 64, da + q * 2, db + q * 2, idesc, q > 0);
                     }
+                    mma_commit<1>(done + u * 8);
                 }
-                for (int j = 0; j < my_stages; ++j) {
-                    const int u = warp + j * a.warps;
-                    uint32_t b[NT][kB][kElems / 2];
+                __syncwarp();
+            }
+        }
+        if (elect_one()) mma_commit<1>(smem_u32(&sh.drain));  // every product has finished before tensor memory is freed
+        __syncwarp();
+        mbar_wait_bounded(&sh.drain, 0, kTokWaitNs);
+    } else if (warp >= 4 && warp < 4 + kTokFillMost) {
+        // ---- tokens: warp w converts stages w, w + kFill, ... of the block ----------------
+        constexpr uint32_t kFill = Shape::kFill;
+        if (warp - 4 >= (int)kFill) run.at = run.end;
+        if constexpr (kDown) asm volatile("griddepcontrol.wait;" ::: "memory");  // the sums of kernel 1
+        uint32_t n0 = 0;
+        while (run.next()) {
+            const int p0 = s.base[run.ai], cnt = s.base[run.ai + 1] - p0, len = run.k1 - run.k0;
+            for (int i = (warp - 4 + kFill - n0 % kFill) % kFill; i < len; i += kFill) {
+                const uint32_t n = n0 + i, u = n % kStages;
+                constexpr int kLane = Shape::kChannels / 32;  // channels of a lane
+                const int ch = (run.k0 + i) * Shape::kChannels + lane * kLane;
+                const bool in = ch < (kDown ? a.I : a.H);
+                uint8_t* st = ring + u * Shape::kStage + Shape::kStageA;
+                bool waited = false;
+                for (int j0 = 0; j0 < cnt; j0 += 4) {
+                    float v[4][kLane];
 #pragma unroll
-                    for (int n = 0; n < NT; ++n)
+                    for (int q = 0; q < 4; ++q) {
 #pragma unroll
-                        for (int z = 0; z < kB; ++z)
+                        for (int z = 0; z < kLane; ++z) v[q][z] = 0.0f;
+                        if (in && j0 + q < cnt) {
+                            const int pair = p0 + j0 + q;
+                            if constexpr (kDown) {
+                                load_h<kLane>(a, pair, ch, v[q]);
+                            } else {
+                                const __nv_bfloat16* p = a.x + s.token[pair] * a.x_stride + ch;
+                                const uint32_t* w = reinterpret_cast<const uint32_t*>(p);
 #pragma unroll
-                            for (int i = 0; i < kElems / 8; ++i) {
-                                int4 v = make_int4(0, 0, 0, 0);
-                                if (have[n]) v = *reinterpret_cast<const int4*>(xb[n][z] + u * (4 * kElems) + i * 8);
-                                b[n][z][4 * i] = v.x;
-                                b[n][z][4 * i + 1] = v.y;
-                                b[n][z][4 * i + 2] = v.z;
-                                b[n][z][4 * i + 3] = v.w;
+                                for (int z = 0; z < kLane; z += 2) {
+                                    const uint32_t b = w[z / 2];
+                                    v[q][z] = __uint_as_float(b << 16);
+                                    v[q][z + 1] = __uint_as_float(b & 0xffff0000u);
+                                }
                             }
-                    float s0 = 1.0f, s1 = 1.0f;
-                    if constexpr (kFp8) {
-                        s0 = __ldg(sc + (u >> 1));
-                        s1 = kDown ? s0 : __ldg(sc + sc_up + (u >> 1));
+                        }
                     }
-                    cp_async_wait<kTokRing - 2>();
-                    const uint8_t* src = s.ring + slot * (4 * 16 * kTokThreads) + tid * 16;
-                    slot = slot + 1 == kTokRing ? 0 : slot + 1;
+                    if (!waited) {  // the loads are on their way
+                        mbar_wait_warp(done + u * 8, n / kStages & 1 ^ 1, kTokWaitNs, abort);
+                        waited = true;
+                    }
 #pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        const int4 r0 = *reinterpret_cast<const int4*>(src + (2 * t) * 16 * kTokThreads);
-                        const int4 r1 = *reinterpret_cast<const int4*>(src + (2 * t + 1) * 16 * kTokThreads);
-                        const uint32_t w0[4] = {(uint32_t)r0.x, (uint32_t)r0.y, (uint32_t)r0.z, (uint32_t)r0.w};
-                        const uint32_t w1[4] = {(uint32_t)r1.x, (uint32_t)r1.y, (uint32_t)r1.z, (uint32_t)r1.w};
+                    for (int q = 0; q < 4; ++q) {
+                        if (j0 + q >= cnt) break;
+                        const int col = (j0 + q) * kPieces;
+                        // piece z of the token is row col + z of the tile, 4 bytes a lane, 16-byte units
+                        // exchanged by the 128-byte swizzle
+                        auto put = [&](int z, uint32_t w) {
+                            const int r = col + z;
+                            *reinterpret_cast<uint32_t*>(st + r * kTokBytes + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4) = w;
+                        };
                         if constexpr (kFp8) {
-                            float blk[NT][4] = {};
+                            uint32_t top = 0;  // the largest magnitude's bits, above infinity's where one is NaN
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                uint32_t a0, a1, a2, a3;
-                                e4m3x4_to_bf16(w0[k], a0, a2);
-                                e4m3x4_to_bf16(w1[k], a1, a3);
+                            for (int z = 0; z < 4; ++z) top = max(top, __float_as_uint(v[q][z]) & 0x7fffffffu);
+                            top = __reduce_max_sync(0xffffffffu, top);
+                            const int e = max((int)(top >> 23) - 127, -100);  // |v| < 2^(e + 1)
+                            const bool odd = top >= 0x7f800000u;
+                            const float up = odd ? 1.0f : __uint_as_float((uint32_t)(7 - e + 127) << 23);
+                            const float down = odd ? 1.0f : __uint_as_float((uint32_t)(e - 7 + 127) << 23);
 #pragma unroll
-                                for (int n = 0; n < NT; ++n)
+                            for (int z = 0; z < 4; ++z) v[q][z] *= up;
+                            if (odd) {  // an infinity or a NaN makes the token's whole block NaN
 #pragma unroll
-                                    for (int z = 0; z < kB; ++z)
-                                        mma_bf16(blk[n], a0, a1, a2, a3, b[n][z][2 * k], b[n][z][2 * k + 1]);
+                                for (int z = 0; z < kPieces; ++z) put(z, 0x7f7f7f7fu);
+                            } else {
+#pragma unroll
+                                for (int z = 0; z < kPieces; ++z) {
+                                    const uint32_t c = pack_e4m3(v[q][0], v[q][1], v[q][2], v[q][3]);
+                                    put(z, c);
+                                    if (z + 1 < kPieces) next_piece(v[q], c);
+                                }
                             }
-#pragma unroll
-                            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                                for (int i = 0; i < 4; ++i) tot[t][n][i] = fmaf(blk[n][i], i < 2 ? s0 : s1, tot[t][n][i]);
+                            if (lane == 0) sh.scale[n % kTokScaleRing][j0 + q] = down;
                         } else {
 #pragma unroll
-                            for (int k = 0; k < 2; ++k)
-#pragma unroll
-                                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                                    for (int z = 0; z < kB; ++z)
-                                        mma_bf16(tot[t][n], w0[2 * k], w1[2 * k], w0[2 * k + 1], w1[2 * k + 1],
-                                                 b[n][z][2 * k], b[n][z][2 * k + 1]);
+                            for (int z = 0; z < kPieces; ++z) {
+                                const __nv_bfloat162 b = __floats2bfloat162_rn(v[q][0], v[q][1]);
+                                put(z, *reinterpret_cast<const uint32_t*>(&b));
+                                const float2 f = __bfloat1622float2(b);
+                                v[q][0] = isfinite(f.x) ? v[q][0] - f.x : 0.0f;
+                                v[q][1] = isfinite(f.y) ? v[q][1] - f.y : 0.0f;
+                            }
                         }
                     }
-                    copy();
                 }
-            };
-            if (cnt > 8) pass(std::integral_constant<int, 2>{});
-            else pass(std::integral_constant<int, 1>{});
-
-            // the warps' sums of this item meet in shared memory, added in warp order
-            float* part = s.part + buf * kPartFloats;
-            buf ^= 1;
-            if (warp < a.warps) {
-#pragma unroll
-                for (int t = 0; t < 2; ++t)
-#pragma unroll
-                    for (int n = 0; n < 2; ++n)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            part[(warp * kTokRows + t * 16 + (i >> 1) * 8 + g) * kPartStride + n * 8 + 2 * q + (i & 1)] =
-                                tot[t][n][i];
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(filled + u * 8);
             }
-            __syncthreads();
-            if constexpr (!kDown) {
-                const int ch = tid & 15, at = tid >> 4;
-                if (at < cnt) {
-                    const float* p = part + ((ch >> 3) * 16 + (ch & 7)) * kPartStride + at;
-                    float gate = 0.0f, upv = 0.0f;
-                    for (int w = 0; w < a.warps; ++w) {
-                        gate += p[w * kTokRows * kPartStride];
-                        upv += p[(w * kTokRows + 8) * kPartStride];
-                    }
-                    const float h = gate / (1.0f + expf(-gate)) * upv;
-                    const __nv_bfloat16 top = __float2bfloat16_rn(h);
-                    const float rest = isfinite(__bfloat162float(top)) ? h - __bfloat162float(top) : 0.0f;
-                    const int64_t o = (int64_t)(p0 + first + at) * a.I + chunk * 16 + ch;
-                    a.h_hi[o] = top;
-                    a.h_lo[o] = __float2bfloat16_rn(rest);
-                }
-            } else {
-                const int r = tid & 31, at = tid >> 5;
-                if (at < cnt) {
-                    const float* p = part + r * kPartStride + at;
-                    float y = 0.0f;
-                    for (int w = 0; w < a.warps; ++w) y += p[w * kTokRows * kPartStride];
-                    const int pair = p0 + first + at;
-                    float* acc = s.acc + s.token[pair] * kTokRows + r;
-                    *acc = fmaf(s.weight[pair], y, *acc);
-                }
-            }
+            n0 += len;
         }
-        if (++lo == outer || (kDown && item + 1 == i1)) {
+    } else if (warp >= 12) {
+        // ---- sums: thread r owns weight row r of the tile ---------------------------------
+        const int r = (warp - 12) * 32 + lane;
+        const uint32_t lane_base = tmem + ((uint32_t)(warp - 12) << 21);
+        if constexpr (kDown) asm volatile("griddepcontrol.wait;" ::: "memory");  // the counters of kernel 1
+        if (kDown && A == 0)
+            for (int64_t i = blockIdx.x * 128ll + r; i < (int64_t)a.T * a.H; i += gridDim.x * 128ll)
+                a.out[i / a.H * a.out_stride + i % a.H] = __float2bfloat16_rn(0.0f);
+        uint32_t n = 0;
+        while (run.next()) {
+            const int p0 = s.base[run.ai], cnt = s.base[run.ai + 1] - p0;
+            // the row's channel: kernel 1 has 64 gate rows, then the 64 up rows of the same channels
+            const int ch = kDown ? run.tile * kTokRows + r : run.tile * (kTokRows / 2) + (r & 63);
+            const int row = kDown ? ch : (r < 64 ? ch : a.I + ch);
+            const float* ws = nullptr;
+            if constexpr (kFp8)
+                ws = a.ws + ((int64_t)s.expert[run.ai] * ((kDown ? a.H : 2 * a.I) / 128) + row / 128) * a.blocks_k;
+            float acc[kTokSlots];
+#pragma unroll
+            for (int j = 0; j < kTokSlots; ++j) acc[j] = 0.0f;
+            float sw = kFp8 ? __ldg(ws + run.k0) : 1.0f;
+#pragma unroll 1
+            for (int k = run.k0; k < run.k1; ++k, ++n) {
+                const float f = sw;
+                if (kFp8 && k + 1 < run.k1) sw = __ldg(ws + k + 1);
+                mbar_wait_warp(done + n % kStages * 8, n / kStages & 1, kTokWaitNs, abort);
+                tc_fence_after();
+                const float* sc = sh.scale[n % kTokScaleRing];
+                // 16 columns at a time: the pieces of 16 / kPieces tokens, in order
+                float t[kPieces == 3 ? 48 : 16 * kPieces];
+                const uint32_t ad = lane_base + (n & 1) * 64;
+#pragma unroll
+                for (int q = 0; q < kPieces; ++q)
+                    if (cnt * kPieces > q * 16) tmem_ld(ad + q * 16, *reinterpret_cast<float(*)[16]>(t + q * 16));
+#pragma unroll
+                for (int q = 0; q < kPieces; ++q) tmem_wait_ld(*reinterpret_cast<float(*)[16]>(t + q * 16));
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_hand_back(acc_empty + (n & 1) * 8);
+#pragma unroll
+                for (int j = 0; j < kTokSlots; ++j) {
+                    if ((j & 3) == 0 && j >= cnt) break;
+                    float y = t[j * kPieces];
+                    if constexpr (kFp8) {
+                        y = fmaf(t[j * kPieces + 1], 0.0625f, y);
+                        if constexpr (kPieces == 3) y = fmaf(t[j * kPieces + 2], 0.00390625f, y);
+                        acc[j] = fmaf(y, f * sc[j], acc[j]);
+                    } else {
+                        if constexpr (kPieces == 2) y += t[j * kPieces + 1];
+                        acc[j] += y;
+                    }
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < kTokSlots; ++j) {
+                if (j >= cnt) break;
+                const int pair = p0 + j;
+                if constexpr (kDown) {
+                    float* o = s.acc + s.token[pair] * kTokRows + r;
+                    *o = fmaf(s.weight[pair], acc[j], *o);
+                } else if (ch < a.I) {
+                    a.sums[((int64_t)run.part * a.T * a.K + pair) * 2 * a.I + row] = acc[j];
+                }
+            }
             if constexpr (kDown) {
-                // the end of this block's part of a chunk: write the chunk, or leave the part
-                // where the block that finishes the chunk last adds the parts in block order
-                __syncthreads();
-                const int64_t lo0 = (int64_t)chunk * A, hi1 = lo0 + A;
-                const bool whole = i0 <= lo0 && i1 >= hi1;
-                float* mine = a.part + ((int64_t)blockIdx.x * 2 + (chunk != i0 / A)) * a.T * kTokRows;
-                if (tid == 0) last = 1;
-                if (!whole) {
-                    for (int i = tid; i < a.T * kTokRows; i += kTokThreads) mine[i] = s.acc[i];
+                const int per = A * a.blocks_k;  // units of a tile
+                if (run.at < run.end && run.at / per == run.tile) continue;
+                // the end of this block's part of a tile: write the tile, or leave the part where the
+                // block that finishes the tile last adds the parts in block order
+                const int lo = run.tile * per, hi = lo + per;
+                bool write = true;
+                if (begin > lo || run.end < hi) {
+                    float* mine = a.part + ((int64_t)blockIdx.x * 2 + (run.tile != begin / per)) * a.T * kTokRows + r;
+                    for (int t = 0; t < a.T; ++t) mine[t * kTokRows] = s.acc[t * kTokRows + r];
                     __threadfence();
-                    __syncthreads();
-                    const int64_t b0 = ((lo0 + 1) * blocks - 1) / total, b1 = (hi1 * blocks - 1) / total;
-                    if (tid == 0) {
-                        last = atomicAdd(&a.done[chunk], 1u) == (uint32_t)(b1 - b0);
+                    asm volatile("bar.sync 1, 128;" ::: "memory");
+                    const int b0 = (int)(((int64_t)(lo + 1) * blocks - 1) / total), b1 = (int)(((int64_t)hi * blocks - 1) / total);
+                    if (r == 0) {
+                        sh.last = atomicAdd(&a.done[run.tile], 1u) == (uint32_t)(b1 - b0);
                         __threadfence();
                     }
-                    __syncthreads();
-                    if (last)
-                        for (int i = tid; i < a.T * kTokRows; i += kTokThreads) {
-                            float v = 0.0f;
-                            for (int64_t b = b0; b <= b1; ++b)
-                                v += __ldcg(a.part + (b * 2 + (chunk != (total * b / blocks) / A)) * a.T * kTokRows + i);
-                            s.acc[i] = v;
+                    asm volatile("bar.sync 1, 128;" ::: "memory");
+                    write = sh.last;
+                    if (write)
+                        for (int t0 = 0; t0 < a.T; t0 += 8) {  // eight loads on their way at a time
+                            float v[8] = {};
+                            for (int b = b0; b <= b1; ++b) {
+                                const float* p = a.part + ((int64_t)b * 2 + (run.tile != first_of(b) / per)) * a.T * kTokRows + r;
+#pragma unroll
+                                for (int q = 0; q < 8; ++q)
+                                    if (t0 + q < a.T) v[q] += __ldcg(p + (t0 + q) * kTokRows);
+                            }
+#pragma unroll
+                            for (int q = 0; q < 8; ++q)
+                                if (t0 + q < a.T) s.acc[(t0 + q) * kTokRows + r] = v[q];
                         }
                 }
-                __syncthreads();
-                for (int i = tid; i < a.T * kTokRows; i += kTokThreads) {
-                    if (last) a.out[i / kTokRows * a.out_stride + chunk * kTokRows + i % kTokRows] = __float2bfloat16_rn(s.acc[i]);
-                    s.acc[i] = 0.0f;
+                for (int t = 0; t < a.T; ++t) {
+                    if (write && ch < a.H) a.out[t * a.out_stride + ch] = __float2bfloat16_rn(s.acc[t * kTokRows + r]);
+                    s.acc[t * kTokRows + r] = 0.0f;
                 }
-                __syncthreads();
-            }
-            if (lo == outer) {
-                lo = 0;
-                ++hi;
+                asm volatile("bar.sync 1, 128;" ::: "memory");  // sh.last may be written again
             }
         }
     }
-    cp_async_wait<0>();
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 2) tmem_free<1>(tmem, 128);
+    if (tid == 0 && *abort && a.status) flag(a.status, FLAG_TIMEOUT);
 }
 
+// Entries of the expert list, at most: one for each expert that is chosen, and one more for every kTokSlots pairs.
+static int tok_list(int T, int K, int E) { return (E < T * K ? E : T * K) + T * K / kTokSlots; }
+
 struct TokWorkspace {
-    int64_t h_lo, part, done, bytes;
+    int split;
+    int64_t part, done, bytes;
 };
-static TokWorkspace tok_workspace(int T, int K, int H, int I, int blocks) {
+// The parts of K in kernel 1: enough items that the blocks' shares differ little,
+// each with a few stages left.
+static TokWorkspace tok_workspace(int T, int K, int E, int H, int I, bool fp8, int sms) {
     auto up = [](int64_t v) { return (v + 255) / 256 * 256; };
+    const int blocks_k = (H * (fp8 ? 1 : 2) + kTokBytes - 1) / kTokBytes;
+    const int64_t items = (int64_t)(E < T * K ? E : T * K) * ((I + kTokRows / 2 - 1) / (kTokRows / 2));
+    int64_t split = (6 * sms + items - 1) / items;
+    if (split > 8) split = 8;
+    if (split > blocks_k / 4) split = blocks_k / 4;
     TokWorkspace w;
-    w.h_lo = up((int64_t)T * K * I * 2);
-    w.part = 2 * w.h_lo;
-    w.done = w.part + up((int64_t)blocks * 2 * T * kTokRows * 4);
-    w.bytes = w.done + up((int64_t)(H / kTokRows) * 4);
+    w.split = split < 1 ? 1 : (int)split;
+    w.part = up((int64_t)w.split * T * K * 2 * I * 4);
+    w.done = w.part + up((int64_t)sms * 2 * T * kTokRows * 4);
+    w.bytes = w.done + up((int64_t)((H + kTokRows - 1) / kTokRows) * 4);
     return w;
+}
+
+static ep_status tok_map(CUtensorMap* m, const void* w, int64_t row_bytes, int64_t rows, int experts, const char* fn) {
+    const cuuint64_t dims[3] = {(cuuint64_t)row_bytes, (cuuint64_t)rows, (cuuint64_t)experts};
+    const cuuint64_t strides[2] = {(cuuint64_t)row_bytes, (cuuint64_t)(row_bytes * rows)};
+    const cuuint32_t box[3] = {kTokBytes, 64, 1};
+    return encode_rows(m, w, 3, dims, strides, box, fn);
 }
 
 template <bool kFp8>
 static ep_status launch_tokens(TokArgs a, const ep_moe_weights* w, int sms, const TokWorkspace& ws, uint8_t* mem, cudaStream_t st) {
-    const size_t smem = tok_smem(a.T, a.K, a.list);
+    const char* fn = "ep_moe_tokens";
     int dev = 0;
     EP_CUDA(cudaGetDevice(&dev));
     static std::atomic<bool> known[kMaxDevicesTracked];  // devices whose launch attributes are set
     if (dev >= kMaxDevicesTracked || !known[dev].load(std::memory_order_relaxed)) {
-        const int most = (int)tok_smem(kTokMax, kMaxTopk, kTokMax * kMaxTopk);
-        EP_CUDA(cudaFuncSetAttribute(tok_kernel<false, kFp8>, cudaFuncAttributeMaxDynamicSharedMemorySize, most));
-        EP_CUDA(cudaFuncSetAttribute(tok_kernel<true, kFp8>, cudaFuncAttributeMaxDynamicSharedMemorySize, most));
+        constexpr int kMost = kTokMax * kMaxTopk + kTokMax * kMaxTopk / kTokSlots;
+        EP_CUDA(cudaFuncSetAttribute(tok_kernel<false, kFp8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     (int)tok_smem<false, kFp8>(kTokMax, kMaxTopk, kMost)));
+        EP_CUDA(cudaFuncSetAttribute(tok_kernel<true, kFp8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     (int)tok_smem<true, kFp8>(kTokMax, kMaxTopk, kMost)));
         if (dev < kMaxDevicesTracked) known[dev].store(true, std::memory_order_relaxed);
     }
-    a.h_hi = reinterpret_cast<__nv_bfloat16*>(mem);
-    a.h_lo = reinterpret_cast<__nv_bfloat16*>(mem + ws.h_lo);
+    constexpr int kByte = kFp8 ? 1 : 2;
+    CUtensorMap m13, m2;
+    ep_status rc = tok_map(&m13, w->w13, (int64_t)a.H * kByte, 2 * (int64_t)a.I, a.E, fn);
+    if (rc == EP_OK) rc = tok_map(&m2, w->w2, (int64_t)a.I * kByte, a.H, a.E, fn);
+    if (rc != EP_OK) return rc;
+    const int tiles1 = (a.I + kTokRows / 2 - 1) / (kTokRows / 2), tiles2 = (a.H + kTokRows - 1) / kTokRows;
+    const int k1 = (a.H * kByte + kTokBytes - 1) / kTokBytes, k2 = (a.I * kByte + kTokBytes - 1) / kTokBytes;
+    if ((int64_t)a.list * tiles1 * 8 > 0x7fffffff || (int64_t)a.list * tiles2 * k2 > 0x7fffffff)
+        return set_error(EP_ERR_INVALID_ARG, "%s: %d x %d channels of %d experts are too many", fn, a.H, a.I, a.list);
+    a.split = ws.split;
+    a.sums = reinterpret_cast<float*>(mem);
     a.part = reinterpret_cast<float*>(mem + ws.part);
     a.done = reinterpret_cast<uint32_t*>(mem + ws.done);
-    // the fewest rounds of kTokWarps warps over a row's stages, then the fewest warps with that many
-    auto split = [&](int channels) {
-        a.stages = channels * (kFp8 ? 1 : 2) / kTokStage;
-        const int rounds = (a.stages + kTokWarps - 1) / kTokWarps;
-        a.warps = (a.stages + rounds - 1) / rounds;
-    };
-    split(a.H);
-    a.w = static_cast<const uint8_t*>(w->w13);
+    a.blocks_k = k1;
     a.ws = w->w13_scales;
-    const int64_t items1 = (int64_t)a.list * (a.I / 16), items2 = (int64_t)a.list * (a.H / kTokRows);
-    tok_kernel<false, kFp8><<<(int)(items1 < sms ? items1 : sms), kTokThreads, smem, st>>>(a);
-    EP_CHECK_LAUNCH("ep_moe_tokens");
-    split(a.I);
-    a.w = static_cast<const uint8_t*>(w->w2);
+    const int64_t items1 = (int64_t)a.list * tiles1 * a.split, items2 = (int64_t)a.list * tiles2 * k2;
+    tok_kernel<false, kFp8><<<(int)(items1 < sms ? items1 : sms), kTokThreads, tok_smem<false, kFp8>(a.T, a.K, a.list), st>>>(m13, a);
+    EP_CHECK_LAUNCH(fn);
+    a.blocks_k = k2;
     a.ws = w->w2_scales;
-    // kernel 2 starts while kernel 1 drains: its list and first weights do not depend on h
+    // kernel 2 starts while kernel 1 drains: its list and first weights do not depend on the sums
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(items2 < sms ? items2 : sms));
     cfg.blockDim = dim3(kTokThreads);
-    cfg.dynamicSmemBytes = smem;
+    cfg.dynamicSmemBytes = tok_smem<true, kFp8>(a.T, a.K, a.list);
     cfg.stream = st;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    EP_CUDA(cudaLaunchKernelEx(&cfg, tok_kernel<true, kFp8>, a));
+    EP_CUDA(cudaLaunchKernelEx(&cfg, tok_kernel<true, kFp8>, m2, a));
     return EP_OK;
 }
 
@@ -487,9 +632,11 @@ static int sm_count() {
 
 using namespace ep;
 
-extern "C" int64_t ep_moe_tokens_workspace(int32_t num_tokens, int32_t num_topk, int32_t hidden, int32_t inter) {
-    if (num_tokens < 1 || num_tokens > kTokMax || num_topk < 1 || num_topk > kMaxTopk || hidden < 32 || inter < 32) return 0;
-    return tok_workspace(num_tokens, num_topk, hidden, inter, sm_count()).bytes;
+extern "C" int64_t ep_moe_tokens_workspace(int32_t num_tokens, int32_t num_topk, const ep_moe_weights* w) {
+    if (!w || num_tokens < 1 || num_tokens > kTokMax || num_topk < 1 || num_topk > kMaxTopk || w->hidden < 32 || w->inter < 32 ||
+        w->experts < 1)
+        return 0;
+    return tok_workspace(num_tokens, num_topk, w->experts, w->hidden, w->inter, w->w13_scales != nullptr, sm_count()).bytes;
 }
 
 extern "C" ep_status ep_moe_tokens(const void* x, int64_t x_stride, int32_t num_tokens, const int64_t* topk_idx,
@@ -514,7 +661,7 @@ extern "C" ep_status ep_moe_tokens(const void* x, int64_t x_stride, int32_t num_
                          (long long)out_stride, H);
     const int sms = sm_count();
     if (sms < 1) return set_error(EP_ERR_CUDA, "%s: no CUDA device", fn);
-    const TokWorkspace ws = tok_workspace(num_tokens, num_topk, H, I, sms);
+    const TokWorkspace ws = tok_workspace(num_tokens, num_topk, w->experts, H, I, fp8, sms);
     if (!workspace || !aligned16(workspace) || workspace_bytes < ws.bytes)
         return set_error(EP_ERR_CAPACITY, "%s: workspace of %lld bytes, %lld needed", fn, (long long)workspace_bytes, (long long)ws.bytes);
     TokArgs a{};
@@ -527,7 +674,7 @@ extern "C" ep_status ep_moe_tokens(const void* x, int64_t x_stride, int32_t num_
     a.E = w->experts;
     a.H = H;
     a.I = I;
-    a.list = a.E < a.T * a.K ? a.E : a.T * a.K;
+    a.list = tok_list(a.T, a.K, a.E);
     a.out = static_cast<__nv_bfloat16*>(out);
     a.out_stride = out_stride;
     a.status = status_out;

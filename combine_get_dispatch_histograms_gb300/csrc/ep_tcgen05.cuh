@@ -174,6 +174,15 @@ __device__ __forceinline__ void mma_e4m3(uint32_t d, uint64_t a, uint64_t b, uin
             "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
             : "memory");
 }
+// The same for one block and bf16 operands: D[128 x N] (+)= A[128 x 16] B[N x 16]^T.
+__device__ __forceinline__ void mma_bf16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+        : "memory");
+}
 // Arrives on `bar` (of both blocks) when every tcgen05.mma this thread issued has finished.
 template <int kCtas>
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
@@ -198,6 +207,15 @@ __device__ __forceinline__ void tmem_ld(uint32_t addr, float (&v)[32]) {
           "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
         : "r"(addr));
 }
+__device__ __forceinline__ void tmem_ld(uint32_t addr, float (&v)[16]) {
+    uint32_t* r = reinterpret_cast<uint32_t*>(v);
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(addr));
+}
 // Waits for this warp's tensor-memory loads.  `v` passes through the statement
 // so that no use of the loaded values moves above the wait.
 __device__ __forceinline__ void tmem_wait_ld(float (&v)[32]) {
@@ -211,6 +229,15 @@ __device__ __forceinline__ void tmem_wait_ld(float (&v)[32]) {
         : "memory");
 }
 
+__device__ __forceinline__ void tmem_wait_ld(float (&v)[16]) {
+    asm volatile(
+        "tcgen05.wait::ld.sync.aligned;"
+        : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]), "+f"(v[8]),
+          "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15])
+        :
+        : "memory");
+}
+
 // Shared-memory descriptor of a K-major tile with 128-byte rows in the 128-byte
 // swizzle (8-row atoms of 1024 bytes).
 __device__ __forceinline__ uint64_t smem_desc_sw128(const void* p) {
@@ -219,6 +246,18 @@ __device__ __forceinline__ uint64_t smem_desc_sw128(const void* p) {
 // Instruction descriptor: fp32 accumulator, e4m3 x e4m3, both K-major.
 __host__ __device__ constexpr uint32_t idesc_e4m3(int m, int n) {
     return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+}
+// The same with bf16 x bf16.
+__host__ __device__ constexpr uint32_t idesc_bf16(int m, int n) { return idesc_e4m3(m, n) | (1u << 7) | (1u << 10); }
+
+// silu(g) * u with the approximate power and reciprocal, each off by a few
+// 2^-23 of itself, as the product's own sum is.  For g below about -88 the power is
+// infinite and the result -0.
+__device__ __forceinline__ float silu_mul(float g, float u) {
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+    return g * r * u;
 }
 
 // d[0..31] += v[0..31] * f, two at a time: half the instructions, and fewer
@@ -231,6 +270,36 @@ __device__ __forceinline__ void fma32(float* d, float (&v)[32], float f) {
             "fma.rn.f32x2 c, a, b, c;\n\tmov.b64 {%0, %1}, c;\n\t}"
             : "+f"(d[i]), "+f"(d[i + 1])
             : "f"(v[i]), "f"(v[i + 1]), "f"(f));
+}
+
+// ---- host: tensor maps ------------------------------------------------------------
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+inline EncodeTiled encode_tiled() {
+    static const EncodeTiled fn = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<EncodeTiled>(p);
+    }();
+    return fn;
+}
+
+// A map of bytes [..][rows][row bytes] in boxes of 128 bytes x rows, 128-byte swizzle.
+inline ep_status encode_rows(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
+                             const cuuint32_t* box, const char* what) {
+    const EncodeTiled fn = encode_tiled();
+    if (!fn) return set_error(EP_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
+    const cuuint32_t ones[3] = {1, 1, 1};
+    const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, rank, const_cast<void*>(base), dims, strides, box, ones,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return set_error(EP_ERR_INVALID_ARG, "%s: the tensor map was refused (%d)", what, (int)r);
+    return EP_OK;
 }
 
 }  // namespace ep

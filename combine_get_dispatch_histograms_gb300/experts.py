@@ -228,7 +228,7 @@ def moe_tokens(x, topk_idx, topk_weights, w13, w2, w13_scales=None, w2_scales=No
             if out is None:
                 out = torch.empty(T, H, dtype=_BF16, device=x.device)
             if workspace is None:
-                workspace = torch.empty(_workspace_bytes(index, T, K, H, I), dtype=_U8, device=x.device)
+                workspace = torch.empty(_workspace_bytes(index, T, K, E, H, I, p13 is not None), dtype=_U8, device=x.device)
     step = _output(f"{name}: out", out, (T, H), _BF16, index)
     w = EpMoeWeights(w13.data_ptr(), p13, w2.data_ptr(), p2, E, H, I)
     _call("ep_moe_tokens", index, x.data_ptr(), _step(name, x), T, topk_idx.data_ptr(), topk_weights.data_ptr(), K,
@@ -237,12 +237,13 @@ def moe_tokens(x, topk_idx, topk_weights, w13, w2, w13_scales=None, w2_scales=No
     return out
 
 
-def moe_tokens_workspace(num_tokens: int, num_topk: int, hidden: int, inter: int) -> int:
+def moe_tokens_workspace(num_tokens: int, num_topk: int, experts: int, hidden: int, inter: int, fp8: bool = True) -> int:
     """Bytes of workspace moe_tokens needs on the current device (0 for sizes it refuses)."""
-    return int(_lib.load().ep_moe_tokens_workspace(num_tokens, num_topk, hidden, inter))
+    w = EpMoeWeights(None, 1 if fp8 else None, None, 1 if fp8 else None, experts, hidden, inter)
+    return int(_lib.load().ep_moe_tokens_workspace(num_tokens, num_topk, ctypes.byref(w)))
 
 
 @functools.lru_cache(maxsize=256)
-def _workspace_bytes(index: int, num_tokens: int, num_topk: int, hidden: int, inter: int) -> int:
+def _workspace_bytes(index: int, *sizes) -> int:
     with torch.cuda.device(index):
-        return moe_tokens_workspace(num_tokens, num_topk, hidden, inter)
+        return moe_tokens_workspace(*sizes)

@@ -449,15 +449,16 @@ typedef struct ep_moe_weights {
     int32_t experts, hidden, inter;
 } ep_moe_weights;
 
-/* Bytes of workspace ep_moe_tokens needs on the current device (0 for sizes it
- * refuses). */
-int64_t ep_moe_tokens_workspace(int32_t num_tokens, int32_t num_topk, int32_t hidden, int32_t inter);
+/* Bytes of workspace ep_moe_tokens needs on the current device for these sizes
+ * (0 for sizes it refuses); of the weights only the sizes and whether there are
+ * scales are read. */
+int64_t ep_moe_tokens_workspace(int32_t num_tokens, int32_t num_topk, const ep_moe_weights* w);
 
 /* A whole layer for 0..64 tokens, in two kernels:
  *   out[t] = bf16( sum over k of w[t][k] * W2[e] ( silu(Wg[e] x[t]) * (Wu[e] x[t]) ) ),  e = topk_idx[t][k],
  * x and out bf16 rows, strides in elements (x 16-byte aligned, x_stride a
- * multiple of 8).  Every sum is fp32 and h keeps 16 bits of mantissa between
- * the kernels.  -1 entries are skipped, a token with no valid entry gets +0;
+ * multiple of 8).  Every sum is fp32; h enters the second product with an error
+ * below 2^-13 of itself.  -1 entries are skipped, a token with no valid entry gets +0;
  * an entry outside [-1, experts) is skipped and ORs 1 into status_out (device,
  * nullable, zeroed by the caller).  The experts a token names twice count with
  * the sum of both weights.  The order of the sums depends on the routing and
