@@ -37,6 +37,7 @@ constexpr int kTokSlots = 16;      // tokens of a list entry: an expert with mor
 constexpr int kTokRows = 128;      // weight rows of an item
 constexpr int kTokBytes = 128;     // of a weight row per stage
 constexpr int kTokScaleRing = 16;  // stages whose powers of two are kept: more than are ever between writer and reader
+constexpr int kTokSplitMost = 4;   // parts of K in kernel 1, at most
 constexpr int64_t kTokWaitNs = 2000000000ll;
 
 template <bool kDown, bool kFp8>
@@ -203,29 +204,20 @@ __device__ __forceinline__ void next_piece(float* v, uint32_t codes) {
     v[3] = (v[3] - hi.y) * 16.0f;
 }
 
-// h of kN channels of a pair from the parts of its sums.
+// kN consecutive 32-bit words.
 template <int kN>
-__device__ __forceinline__ void load_h(const TokArgs& a, int pair, int ch, float* v) {
-    float g[kN] = {}, u[kN] = {};
-    const int64_t part = (int64_t)a.T * a.K * 2 * a.I;
-    const float* p = a.sums + (int64_t)pair * 2 * a.I + ch;
-    for (int s = 0; s < a.split; ++s, p += part) {
-        if constexpr (kN == 4) {
-            const float4 x = *reinterpret_cast<const float4*>(p), y = *reinterpret_cast<const float4*>(p + a.I);
-            g[0] += x.x, g[1] += x.y, g[2] += x.z, g[3] += x.w;
-            u[0] += y.x, u[1] += y.y, u[2] += y.z, u[3] += y.w;
-        } else {
-            const float2 x = *reinterpret_cast<const float2*>(p), y = *reinterpret_cast<const float2*>(p + a.I);
-            g[0] += x.x, g[1] += x.y;
-            u[0] += y.x, u[1] += y.y;
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < kN; ++i) v[i] = g[i] / (1.0f + __expf(-g[i])) * u[i];
+__device__ __forceinline__ void load_words(const float* p, float* v) {
+    if constexpr (kN == 4) *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(p);
+    else if constexpr (kN == 2) *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(p);
+    else *v = *p;
 }
 
 // kDown: kernel 2.  kFp8: e4m3 weights with block scales, otherwise bf16.
-template <bool kDown, bool kFp8>
+// kParts: the sums come in several parts (few items, so few tokens); without
+// them the next tokens' sums are loaded while these are converted, for which
+// both forms in one kernel leave too few registers (64 tokens: 938 us instead of
+// 904).
+template <bool kDown, bool kFp8, bool kParts>
 __global__ void __launch_bounds__(kTokThreads, 1) tok_kernel(const __grid_constant__ CUtensorMap map_w, const TokArgs a) {
     using Shape = TokShape<kDown, kFp8>;
     constexpr int kStages = Shape::kStages, kPieces = Shape::kPieces;
@@ -350,36 +342,60 @@ __global__ void __launch_bounds__(kTokThreads, 1) tok_kernel(const __grid_consta
                 const int ch = (run.k0 + i) * Shape::kChannels + lane * kLane;
                 const bool in = ch < (kDown ? a.I : a.H);
                 uint8_t* st = ring + u * Shape::kStage + Shape::kStageA;
-                bool waited = false;
-                for (int j0 = 0; j0 < cnt; j0 += 4) {
-                    float v[4][kLane];
+                // what a lane reads of a token: its channels of x, or of both sums
+                constexpr int kRaw = kDown ? 2 * kLane : kLane / 2;
+                const int64_t part = (int64_t)a.T * a.K * 2 * a.I;
+                auto sums_of = [&](int j) { return a.sums + (int64_t)(p0 + j) * 2 * a.I + ch; };
+                auto load = [&](int j0, float(&raw)[4][kRaw]) {
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
 #pragma unroll
-                        for (int z = 0; z < kLane; ++z) v[q][z] = 0.0f;
+                        for (int z = 0; z < kRaw; ++z) raw[q][z] = 0.0f;
                         if (in && j0 + q < cnt) {
-                            const int pair = p0 + j0 + q;
                             if constexpr (kDown) {
-                                load_h<kLane>(a, pair, ch, v[q]);
-                            } else {
-                                const __nv_bfloat16* p = a.x + s.token[pair] * a.x_stride + ch;
-                                const uint32_t* w = reinterpret_cast<const uint32_t*>(p);
+                                const float* p = sums_of(j0 + q);
+                                load_words<kLane>(p, raw[q]);
+                                load_words<kLane>(p + a.I, raw[q] + kLane);
+                                if constexpr (kParts) {  // the other parts, all on their way at once
+                                    float more[kTokSplitMost - 1][kRaw];
 #pragma unroll
-                                for (int z = 0; z < kLane; z += 2) {
-                                    const uint32_t b = w[z / 2];
-                                    v[q][z] = __uint_as_float(b << 16);
-                                    v[q][z + 1] = __uint_as_float(b & 0xffff0000u);
+                                    for (int z = 0; z < kTokSplitMost - 1; ++z)
+                                        if (z + 1 < a.split) {
+                                            load_words<kLane>(p + (z + 1) * part, more[z]);
+                                            load_words<kLane>(p + (z + 1) * part + a.I, more[z] + kLane);
+                                        }
+#pragma unroll
+                                    for (int z = 0; z < kTokSplitMost - 1; ++z)
+                                        if (z + 1 < a.split)
+#pragma unroll
+                                            for (int i = 0; i < kRaw; ++i) raw[q][i] += more[z][i];
                                 }
+                            } else {
+                                load_words<kLane / 2>(
+                                    reinterpret_cast<const float*>(a.x + s.token[p0 + j0 + q] * a.x_stride + ch), raw[q]);
                             }
                         }
                     }
-                    if (!waited) {  // the loads are on their way
-                        mbar_wait_warp(done + u * 8, n / kStages & 1 ^ 1, kTokWaitNs, abort);
-                        waited = true;
-                    }
+                };
+                auto convert = [&](int j0, float(&raw)[4][kRaw]) {
+                    float v[4][kLane];
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
-                        if (j0 + q >= cnt) break;
+                        float(&w)[kRaw] = raw[q];
+                        if constexpr (kDown) {
+#pragma unroll
+                            for (int z = 0; z < kLane; ++z) v[q][z] = silu_mul(w[z], w[kLane + z]);
+                        } else {
+#pragma unroll
+                            for (int z = 0; z < kLane; z += 2) {
+                                const uint32_t two = __float_as_uint(w[z / 2]);
+                                v[q][z] = __uint_as_float(two << 16);
+                                v[q][z + 1] = __uint_as_float(two & 0xffff0000u);
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {  // four independent chains; a token too many is zeros
                         const int col = (j0 + q) * kPieces;
                         // piece z of the token is row col + z of the tile, 4 bytes a lane, 16-byte units
                         // exchanged by the 128-byte swizzle
@@ -398,16 +414,11 @@ __global__ void __launch_bounds__(kTokThreads, 1) tok_kernel(const __grid_consta
                             const float down = odd ? 1.0f : __uint_as_float((uint32_t)(e - 7 + 127) << 23);
 #pragma unroll
                             for (int z = 0; z < 4; ++z) v[q][z] *= up;
-                            if (odd) {  // an infinity or a NaN makes the token's whole block NaN
 #pragma unroll
-                                for (int z = 0; z < kPieces; ++z) put(z, 0x7f7f7f7fu);
-                            } else {
-#pragma unroll
-                                for (int z = 0; z < kPieces; ++z) {
-                                    const uint32_t c = pack_e4m3(v[q][0], v[q][1], v[q][2], v[q][3]);
-                                    put(z, c);
-                                    if (z + 1 < kPieces) next_piece(v[q], c);
-                                }
+                            for (int z = 0; z < kPieces; ++z) {
+                                const uint32_t c = pack_e4m3(v[q][0], v[q][1], v[q][2], v[q][3]);
+                                put(z, odd ? 0x7f7f7f7fu : c);  // an infinity or a NaN makes the token's whole block NaN
+                                if (z + 1 < kPieces) next_piece(v[q], c);
                             }
                             if (lane == 0) sh.scale[n % kTokScaleRing][j0 + q] = down;
                         } else {
@@ -420,6 +431,23 @@ __global__ void __launch_bounds__(kTokThreads, 1) tok_kernel(const __grid_consta
                                 v[q][1] = isfinite(f.y) ? v[q][1] - f.y : 0.0f;
                             }
                         }
+                    }
+                };
+                float raw[kParts ? 1 : 2][4][kRaw];
+                load(0, raw[0]);
+                mbar_wait_warp(done + u * 8, n / kStages & 1 ^ 1, kTokWaitNs, abort);
+                if constexpr (kParts) {
+#pragma unroll 1
+                    for (int j0 = 0; j0 < cnt; j0 += 4) {
+                        if (j0 > 0) load(j0, raw[0]);
+                        convert(j0, raw[0]);
+                    }
+                } else {
+#pragma unroll
+                    for (int b = 0; b < kTokSlots / 4; ++b) {
+                        if (b * 4 >= cnt) break;
+                        if (b * 4 + 4 < cnt) load(b * 4 + 4, raw[(b + 1) & 1]);  // on their way while these are converted
+                        convert(b * 4, raw[b & 1]);
                     }
                 }
                 fence_proxy_async_smem();
@@ -555,7 +583,7 @@ static TokWorkspace tok_workspace(int T, int K, int E, int H, int I, bool fp8, i
     const int blocks_k = (H * (fp8 ? 1 : 2) + kTokBytes - 1) / kTokBytes;
     const int64_t items = (int64_t)(E < T * K ? E : T * K) * ((I + kTokRows / 2 - 1) / (kTokRows / 2));
     int64_t split = (6 * sms + items - 1) / items;
-    if (split > 8) split = 8;
+    if (split > kTokSplitMost) split = kTokSplitMost;
     if (split > blocks_k / 4) split = blocks_k / 4;
     TokWorkspace w;
     w.split = split < 1 ? 1 : (int)split;
@@ -580,10 +608,11 @@ static ep_status launch_tokens(TokArgs a, const ep_moe_weights* w, int sms, cons
     static std::atomic<bool> known[kMaxDevicesTracked];  // devices whose launch attributes are set
     if (dev >= kMaxDevicesTracked || !known[dev].load(std::memory_order_relaxed)) {
         constexpr int kMost = kTokMax * kMaxTopk + kTokMax * kMaxTopk / kTokSlots;
-        EP_CUDA(cudaFuncSetAttribute(tok_kernel<false, kFp8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        EP_CUDA(cudaFuncSetAttribute(tok_kernel<false, kFp8, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      (int)tok_smem<false, kFp8>(kTokMax, kMaxTopk, kMost)));
-        EP_CUDA(cudaFuncSetAttribute(tok_kernel<true, kFp8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     (int)tok_smem<true, kFp8>(kTokMax, kMaxTopk, kMost)));
+        const int most = (int)tok_smem<true, kFp8>(kTokMax, kMaxTopk, kMost);
+        EP_CUDA(cudaFuncSetAttribute(tok_kernel<true, kFp8, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, most));
+        EP_CUDA(cudaFuncSetAttribute(tok_kernel<true, kFp8, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, most));
         if (dev < kMaxDevicesTracked) known[dev].store(true, std::memory_order_relaxed);
     }
     constexpr int kByte = kFp8 ? 1 : 2;
@@ -593,7 +622,7 @@ static ep_status launch_tokens(TokArgs a, const ep_moe_weights* w, int sms, cons
     if (rc != EP_OK) return rc;
     const int tiles1 = (a.I + kTokRows / 2 - 1) / (kTokRows / 2), tiles2 = (a.H + kTokRows - 1) / kTokRows;
     const int k1 = (a.H * kByte + kTokBytes - 1) / kTokBytes, k2 = (a.I * kByte + kTokBytes - 1) / kTokBytes;
-    if ((int64_t)a.list * tiles1 * 8 > 0x7fffffff || (int64_t)a.list * tiles2 * k2 > 0x7fffffff)
+    if ((int64_t)a.list * tiles1 * kTokSplitMost > 0x7fffffff || (int64_t)a.list * tiles2 * k2 > 0x7fffffff)
         return set_error(EP_ERR_INVALID_ARG, "%s: %d x %d channels of %d experts are too many", fn, a.H, a.I, a.list);
     a.split = ws.split;
     a.sums = reinterpret_cast<float*>(mem);
@@ -602,7 +631,7 @@ static ep_status launch_tokens(TokArgs a, const ep_moe_weights* w, int sms, cons
     a.blocks_k = k1;
     a.ws = w->w13_scales;
     const int64_t items1 = (int64_t)a.list * tiles1 * a.split, items2 = (int64_t)a.list * tiles2 * k2;
-    tok_kernel<false, kFp8><<<(int)(items1 < sms ? items1 : sms), kTokThreads, tok_smem<false, kFp8>(a.T, a.K, a.list), st>>>(m13, a);
+    tok_kernel<false, kFp8, false><<<(int)(items1 < sms ? items1 : sms), kTokThreads, tok_smem<false, kFp8>(a.T, a.K, a.list), st>>>(m13, a);
     EP_CHECK_LAUNCH(fn);
     a.blocks_k = k2;
     a.ws = w->w2_scales;
@@ -617,7 +646,7 @@ static ep_status launch_tokens(TokArgs a, const ep_moe_weights* w, int sms, cons
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    EP_CUDA(cudaLaunchKernelEx(&cfg, tok_kernel<true, kFp8>, m2, a));
+    EP_CUDA(cudaLaunchKernelEx(&cfg, a.split > 1 ? tok_kernel<true, kFp8, true> : tok_kernel<true, kFp8, false>, m2, a));
     return EP_OK;
 }
 
