@@ -24,7 +24,6 @@ constexpr int kSumGroups = 4;          // warpgroups that sum, each a quarter of
 constexpr int kSumWarps = 4 * kSumGroups;
 constexpr int kGemmThreads = 128 + 128 * kSumGroups;  // copy, mma, tensor-memory and tile warp first
 constexpr int kOutStride = 80;         // bytes of a staged row of 32 bf16: rows fall into other banks
-constexpr int kOutStage = 32 * kOutStride;  // of one warp
 
 // The two shapes of the kernel.  kCtas = 2: a pair of blocks makes a tile of 256
 // rows; each copies half of the weight's rows, so that a block moves 32 KB per
@@ -36,8 +35,9 @@ struct GemmShape {
     static constexpr int kStageA = kBM * kBK;          // bytes in each block
     static constexpr int kStageB = kBN / kCtas * kBK;
     static constexpr int kStage = kStageA + kStageB;
-    static constexpr bool kStageOut = kCtas == 2;      // with 48 KB stages there is no room
-    static constexpr size_t kSmem = 1024 + kStages * kStage + (kStageOut ? kSumWarps * kOutStage : 0);
+    // of a warp's output on its way: 32 rows of 32 columns, padded, or (48 KB stages leave no room) of 8
+    static constexpr int kOut = kCtas == 2 ? 32 * kOutStride : 32 * 16;
+    static constexpr size_t kSmem = 1024 + kStages * kStage + kSumWarps * kOut;
 };
 constexpr int kTileRing = 4;            // tiles announced ahead
 constexpr int kScaleChunk = 8;          // blocks of K whose scales are staged together
@@ -45,6 +45,9 @@ constexpr int kScaleRing = 2;
 constexpr int kMaxGroups = 4096;
 constexpr int kChunkRows = 2048;       // rows that share a pass over the weight's tiles
 constexpr int kPairRows = 192;         // rows of a group from which pairs of blocks are faster
+constexpr int kSplitMost = 4;          // blocks of a cluster that share a tile's K (one row, K 7168, N 4096:
+                                       // 27.6 us alone, 18.8 by 2, 14.1 by 4, 21.0 by 8)
+constexpr int kSplitStride = kBN + 4;  // floats of a row of sums: rows fall into other banks
 constexpr int64_t kGemmWaitNs = 2000000000ll;
 
 struct GemmArgs {
@@ -163,7 +166,10 @@ struct TileWalk {
 
 // kSwiglu: the tile's 256 weight rows are 128 gate rows and the 128 up rows of
 // the same channels; otherwise 256 consecutive rows.
-template <bool kSwiglu, int kCtas>
+// kSplit (with kCtas = 1): the blocks of a cluster make one tile, each from its
+// share of the blocks of K.  For launches with fewer tiles than SMs, where one
+// block alone would walk all of K; every cluster has at most one tile.
+template <bool kSwiglu, int kCtas, bool kSplit>
 __global__ void __launch_bounds__(kGemmThreads, 1)
 gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w, const GemmArgs a) {
     using Shape = GemmShape<kCtas>;
@@ -173,7 +179,10 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
     uint8_t* tiles = dyn + ((1024u - (smem_u32(dyn) & 1023u)) & 1023u);
     uint8_t* out_stage = tiles + kStages * kStage;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int rank = kCtas == 2 ? (int)cluster_rank() : 0, unit = blockIdx.x / kCtas, units = gridDim.x / kCtas;
+    const int rank = kCtas == 2 ? (int)cluster_rank() : 0;
+    const int part = kSplit ? (int)cluster_rank() : 0, parts = kSplit ? cluster_size() : 1;
+    const int unit = blockIdx.x / (kCtas * parts), units = gridDim.x / (kCtas * parts);
+    const int k0 = kSplit ? part * a.KB / parts : 0, k1 = kSplit ? (part + 1) * a.KB / parts : a.KB;
     volatile int* abort = &sh.abort;
     const uint32_t full = smem_u32(sh.full), done = smem_u32(sh.done), acc_empty = smem_u32(sh.acc_empty);
     const uint32_t tile_full = smem_u32(sh.tile_full), tile_empty = smem_u32(sh.tile_empty);
@@ -235,12 +244,12 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
                 const float* ws = a.w_scales + tile.g * a.w_sgroup + (int64_t)(lane < 8 ? b0 : b1) * a.KB + (lane & 7);
                 const float* xs = a.x_scales + (int64_t)(tile.row0 + rank * kBM) * a.x_sstride;
 #pragma unroll 1
-                for (int kb = 0; kb < a.KB; kb += kScaleChunk) {
+                for (int kb = k0; kb < k1; kb += kScaleChunk) {
                     mbar_wait_warp(sr.bar(scale_empty), sr.phase() ^ 1, kGemmWaitNs, abort);
-                    const float w = lane < 16 && kb + (lane & 7) < a.KB ? __ldg(ws + kb) : 0.0f;
+                    const float w = lane < 16 && kb + (lane & 7) < k1 ? __ldg(ws + kb) : 0.0f;
                     float* dst = &sh.scale[sr.slot()][0][0][0];
 #pragma unroll 1
-                    for (int i = 0; i < kScaleChunk && kb + i < a.KB; i += 4) {
+                    for (int i = 0; i < kScaleChunk && kb + i < k1; i += 4) {
                         const float w00 = __shfl_sync(0xffffffffu, w, i), w01 = __shfl_sync(0xffffffffu, w, 8 + i);
                         const float w10 = __shfl_sync(0xffffffffu, w, i + 1), w11 = __shfl_sync(0xffffffffu, w, 9 + i);
                         const float w20 = __shfl_sync(0xffffffffu, w, i + 2), w21 = __shfl_sync(0xffffffffu, w, 10 + i);
@@ -249,13 +258,13 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
                         for (int r = lane; r < mine; r += 32) {
                             const float* p = xs + r * a.x_sstride + kb + i;
                             float4 v;
-                            if (a.x_vec && kb + i + 4 <= a.KB) {
+                            if (a.x_vec && (!kSplit || (k0 & 3) == 0) && kb + i + 4 <= k1) {
                                 v = __ldg(reinterpret_cast<const float4*>(p));
                             } else {
                                 v.x = __ldg(p);
-                                v.y = kb + i + 1 < a.KB ? __ldg(p + 1) : 0.0f;
-                                v.z = kb + i + 2 < a.KB ? __ldg(p + 2) : 0.0f;
-                                v.w = kb + i + 3 < a.KB ? __ldg(p + 3) : 0.0f;
+                                v.y = kb + i + 1 < k1 ? __ldg(p + 1) : 0.0f;
+                                v.z = kb + i + 2 < k1 ? __ldg(p + 2) : 0.0f;
+                                v.w = kb + i + 3 < k1 ? __ldg(p + 3) : 0.0f;
                             }
                             float* d = dst + i * 2 * kBM + r;
                             d[0] = v.x * w00;
@@ -293,8 +302,8 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
                 const int row = tile.row0 + rank * kBM;
                 const int w0 = kSwiglu ? tile.n * 128 : tile.n * kBN, w1 = kSwiglu ? a.N / 2 + w0 : w0 + 128;
                 const uint32_t full0 = kCtas == 2 ? smem_of(full, 0) : full;
-                for (int kb = 0; kb < a.KB; ++kb) {
-                    const int u = kb & (kStages - 1);
+                for (int kb = k0; kb < k1; ++kb) {
+                    const int u = (kb - k0) & (kStages - 1);
                     if (!mbar_wait_or_abort(done + u * 8, free_phase >> u & 1, kGemmWaitNs, abort)) {
                         ok = false;
                         break;
@@ -328,7 +337,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
                 ++tr.n;
                 if (rows == 0 || __any_sync(0xffffffffu, *abort)) break;
 #pragma unroll 1
-                for (int kb = 0; kb < a.KB; ++kb) {
+                for (int kb = 0; kb < k1 - k0; ++kb) {
                     const int u = kb & (kStages - 1), c = kb & 1;
                     mbar_wait_warp(full + u * 8, full_phase >> u & 1, kGemmWaitNs, abort);
                     mbar_wait_warp(acc_empty + c * 8, empty_phase >> c & 1, kGemmWaitNs, abort);
@@ -348,6 +357,11 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
             if (elect_one()) mma_commit<kCtas>(smem_u32(&sh.drain));  // every product has finished before tensor memory is freed
             __syncwarp();
             mbar_wait_bounded(&sh.drain, 0, kGemmWaitNs);
+        }
+        if constexpr (kSplit) {
+            __syncwarp();
+            cluster_sync();
+            cluster_sync();
         }
     } else {
         // 512 x 112 + 128 x 32 registers are the launch's 640 x 96
@@ -373,14 +387,14 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
             for (int i = 0; i < 64; ++i) acc[i] = 0.0f;
             uint32_t sc = 0;
 #pragma unroll 1
-            for (int kb = 0; kb < a.KB; kb += kStages) {
+            for (int kb = 0; kb < k1 - k0; kb += kStages) {
                 if ((kb & (kScaleChunk - 1)) == 0) {
                     mbar_wait_warp(sr.bar(scale_full), sr.phase(), kGemmWaitNs, abort);
                     sc = sc0 + sr.slot() * (kScaleChunk * 2 * kBM * 4);
                 }
 #pragma unroll
                 for (int u = 0; u < kStages; ++u) {
-                    if (kb + u >= a.KB) break;
+                    if (kb + u >= k1 - k0) break;
                     const float f0 = ld_shared_f32(sc + u * (2 * kBM * 4));
                     const float f1 = kSwiglu ? ld_shared_f32(sc + u * (2 * kBM * 4) + kBM * 4) : f0;
                     mbar_wait_warp(done + u * 8, done_phase >> u & 1, kGemmWaitNs, abort);
@@ -403,7 +417,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
                     }
                 }
                 sc += kStages * 2 * kBM * 4;
-                if ((kb & (kScaleChunk - 1)) == kScaleChunk - kStages || kb + kStages >= a.KB) {
+                if ((kb & (kScaleChunk - 1)) == kScaleChunk - kStages || kb + kStages >= k1 - k0) {
                     __syncwarp();
                     if (lane == 0) mbar_arrive(sr.bar(scale_empty));
                     ++sr.n;
@@ -411,7 +425,17 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
             }
             const int mine = tile->rows - rank * kBM;  // rows of this block, also none or more than kBM
             const int row0 = tile->row0 + rank * kBM, tn = tile->n;
-            if constexpr (kSwiglu) {
+            if constexpr (kSplit) {
+                // the ring is idle now: the block's sums wait there for the cluster's
+                if (r < mine) {
+                    float* d = reinterpret_cast<float*>(tiles) + r * kSplitStride;
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4) {
+                        *reinterpret_cast<float4*>(d + c0 + i) = make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
+                        *reinterpret_cast<float4*>(d + c1 + i) = make_float4(acc[32 + i], acc[33 + i], acc[34 + i], acc[35 + i]);
+                    }
+                }
+            } else if constexpr (kSwiglu) {
                 float m = 0.0f;
 #pragma unroll
                 for (int i = 0; i < 32; ++i) {
@@ -438,38 +462,40 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
                 }
             } else if (rows_here) {
                 const int n0 = tn * kBN + quarter * 64;
-                if constexpr (!Shape::kStageOut) {
-                    // few rows: each lane stores its own
-                    if (r < mine) {
-                        __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(a.out) + (int64_t)(row0 + r) * a.out_stride + n0;
+                uint8_t* stage = out_stage + (warp - 4) * Shape::kOut;
+                const int rows = min(32, mine - (warp & 3) * 32);
+                __nv_bfloat16* o =
+                    reinterpret_cast<__nv_bfloat16*>(a.out) + (int64_t)(row0 + (warp & 3) * 32) * a.out_stride + n0;
+                if constexpr (kCtas == 1) {
+                    // 8 columns at a time: each lane its row's 16 bytes, or, where rows are not so aligned,
+                    // through shared memory, so that 8 lanes store neighbours
 #pragma unroll
-                        for (int q = 0; q < 8; ++q) {
-                            if (a.out_vec && n0 + q * 8 + 8 <= a.N) {
-                                __nv_bfloat162 p[4];
+                    for (int q = 0; q < 8; ++q) {
+                        __nv_bfloat162 p[4];
 #pragma unroll
-                                for (int i = 0; i < 4; ++i)
-                                    p[i] = __floats2bfloat162_rn(acc[q * 8 + 2 * i], acc[q * 8 + 2 * i + 1]);
-                                *reinterpret_cast<int4*>(o + q * 8) = *reinterpret_cast<const int4*>(p);
-                            } else {
-#pragma unroll
-                                for (int i = 0; i < 8; ++i)
-                                    if (n0 + q * 8 + i < a.N) o[q * 8 + i] = __float2bfloat16_rn(acc[q * 8 + i]);
-                            }
+                        for (int i = 0; i < 4; ++i) p[i] = __floats2bfloat162_rn(acc[q * 8 + 2 * i], acc[q * 8 + 2 * i + 1]);
+                        const int n = n0 + q * 8;
+                        if (a.out_vec && n + 8 <= a.N) {
+                            if (lane < rows) *reinterpret_cast<int4*>(o + lane * a.out_stride + q * 8) = *reinterpret_cast<const int4*>(p);
+                        } else if (n < a.N) {
+                            *reinterpret_cast<int4*>(stage + lane * 16) = *reinterpret_cast<const int4*>(p);
+                            __syncwarp();
+                            const int c = lane & 7;
+                            if (n + c < a.N)
+                                for (int i = lane >> 3; i < rows; i += 4)
+                                    o[i * a.out_stride + q * 8 + c] = *reinterpret_cast<const __nv_bfloat16*>(stage + i * 16 + c * 2);
+                            __syncwarp();
                         }
                     }
                 } else {
                     // 32 columns at a time through shared memory, so that a warp's store covers whole
                     // 64-byte pieces of rows
-                    uint8_t* stage = out_stage + (warp - 4) * kOutStage;
-                    const int rows = min(32, mine - (warp & 3) * 32);
-                    __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(a.out) +
-                                       (int64_t)(row0 + (warp & 3) * 32) * a.out_stride + n0;
-    #pragma unroll
+#pragma unroll
                     for (int z = 0; z < 2; ++z) {
-    #pragma unroll
+#pragma unroll
                         for (int q = 0; q < 4; ++q) {
                             __nv_bfloat162 p[4];
-    #pragma unroll
+#pragma unroll
                             for (int i = 0; i < 4; ++i)
                                 p[i] = __floats2bfloat162_rn(acc[z * 32 + q * 8 + 2 * i], acc[z * 32 + q * 8 + 2 * i + 1]);
                             *reinterpret_cast<int4*>(stage + lane * kOutStride + q * 16) = *reinterpret_cast<const int4*>(p);
@@ -499,6 +525,78 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
             __syncwarp();
             if (lane == 0) mbar_arrive(tr.bar(tile_empty));
             ++tr.n;
+        }
+        if constexpr (kSplit) {
+            __syncwarp();
+            cluster_sync();
+            // rows part, part + parts, ... of the tile, a warp each: the blocks' sums in block order.  Only
+            // these warps have the registers for it; the others pass both barriers below
+            const GemmTile tile = sh.tile[0];
+            for (int r = part + parts * (warp - 4); r < tile.rows; r += parts * kSumWarps) {
+                const uint32_t at = smem_u32(tiles) + r * kSplitStride * 4;
+                float v[8] = {};
+                if (kSwiglu || a.out_vec) {
+                    // gate and up of 4 channels, or 8 neighbours
+                    const int ca = kSwiglu ? lane * 4 : lane * 8, cb = kSwiglu ? 128 + lane * 4 : lane * 8 + 4;
+                    float4 x[kSplitMost], y[kSplitMost];
+#pragma unroll
+                    for (int b = 0; b < kSplitMost; ++b)
+                        if (b < parts) {
+                            x[b] = ld_cluster_f32x4(smem_of(at + ca * 4, b));
+                            y[b] = ld_cluster_f32x4(smem_of(at + cb * 4, b));
+                        }
+#pragma unroll
+                    for (int b = 0; b < kSplitMost; ++b)
+                        if (b < parts) {
+                            v[0] += x[b].x, v[1] += x[b].y, v[2] += x[b].z, v[3] += x[b].w;
+                            v[4] += y[b].x, v[5] += y[b].y, v[6] += y[b].z, v[7] += y[b].w;
+                        }
+                } else {  // column lane + 32 i: unaligned rows are stored 2 bytes a lane, neighbours by neighbours
+                    float x[kSplitMost][8];
+#pragma unroll
+                    for (int b = 0; b < kSplitMost; ++b)
+                        if (b < parts)
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) x[b][i] = ld_cluster_f32(smem_of(at + (lane + 32 * i) * 4, b));
+#pragma unroll
+                    for (int b = 0; b < kSplitMost; ++b)
+                        if (b < parts)
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) v[i] += x[b][i];
+                }
+                const int64_t row = tile.row0 + r;
+                if constexpr (kSwiglu) {
+                    float h[16] = {}, m = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        h[i] = silu_mul(v[i], v[4 + i]);
+                        m = fmaxf(m, fabsf(h[i]));
+                    }
+#pragma unroll
+                    for (int o = 1; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                    const float scale = __fdiv_rn(m, 448.0f);
+                    uint8_t* o = reinterpret_cast<uint8_t*>(a.out) + row * a.out_stride + tile.n * 128 + lane * 4;
+                    *reinterpret_cast<int*>(o) = quantize16_by(h, scale).x;
+                    if (lane == 0) a.out_scales[row * a.out_sstride + tile.n] = scale;
+                } else {
+                    __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(a.out) + row * a.out_stride;
+                    const int n0 = tile.n * kBN + lane * 8;
+                    if (a.out_vec && n0 + 8 <= a.N) {
+                        __nv_bfloat162 p[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) p[i] = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+                        *reinterpret_cast<int4*>(o + n0) = *reinterpret_cast<const int4*>(p);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const int n = a.out_vec ? n0 + i : tile.n * kBN + lane + 32 * i;
+                            if (n < a.N) o[n] = __float2bfloat16_rn(v[i]);
+                        }
+                    }
+                }
+            }
+            __syncwarp();
+            cluster_sync();  // no block ends while another reads its sums
         }
     }
     __syncwarp();
@@ -535,34 +633,39 @@ static ep_status check_products(const char* fn, const ep_fp8_rows* x, const ep_r
     return EP_OK;
 }
 
-template <bool kSwiglu, int kCtas>
-static ep_status launch_shape(const char* fn, const CUtensorMap& map_x, const CUtensorMap& map_w, const GemmArgs& a, void* stream) {
+// Tiles of a launch, at most: a group's last tile may be partial, and a group
+// with a tile has a row.
+static int64_t most_tiles(const GemmArgs& a, int tile_rows) {
+    const int64_t most = (a.rows + (int64_t)a.G * (tile_rows - 1)) / tile_rows;
+    return (most < a.rows ? most : a.rows) * a.n_tiles;
+}
+
+template <bool kSwiglu, int kCtas, bool kSplit>
+static ep_status launch_shape(const char* fn, const CUtensorMap& map_x, const CUtensorMap& map_w, const GemmArgs& a, int sms,
+                              int cluster, void* stream) {
     using Shape = GemmShape<kCtas>;
-    // the tiles are counted in 32 bits: every group's last tile may be partial
-    const int64_t most = ((a.rows + Shape::kTileM - 1) / Shape::kTileM + a.G) * (int64_t)a.n_tiles;
+    const int64_t most = most_tiles(a, Shape::kTileM);
     if (most > 0x7fffffff) return set_error(EP_ERR_INVALID_ARG, "%s: %lld tiles", fn, (long long)most);
-    int dev = 0, sms = 0;
+    int dev = 0;
     EP_CUDA(cudaGetDevice(&dev));
-    static std::atomic<int> known[kMaxDevicesTracked];  // SMs of a device whose launch attribute is set
-    if (dev < kMaxDevicesTracked) sms = known[dev].load(std::memory_order_relaxed);
-    if (sms == 0) {
-        EP_CUDA(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
-        EP_CUDA(cudaFuncSetAttribute(gemm_kernel<kSwiglu, kCtas>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Shape::kSmem));
-        if (dev < kMaxDevicesTracked) known[dev].store(sms, std::memory_order_relaxed);
+    static std::atomic<bool> known[kMaxDevicesTracked];  // devices whose launch attribute is set
+    if (dev >= kMaxDevicesTracked || !known[dev].load(std::memory_order_relaxed)) {
+        EP_CUDA(cudaFuncSetAttribute(gemm_kernel<kSwiglu, kCtas, kSplit>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Shape::kSmem));
+        if (dev < kMaxDevicesTracked) known[dev].store(true, std::memory_order_relaxed);
     }
-    const int units = (int)(most < sms / kCtas ? most : sms / kCtas);
+    const int units = (int)(most < sms / cluster ? most : sms / cluster);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(units * kCtas));
+    cfg.gridDim = dim3((unsigned)(units * cluster));
     cfg.blockDim = dim3(kGemmThreads);
     cfg.dynamicSmemBytes = Shape::kSmem;
     cfg.stream = as_stream(stream);
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = kCtas;
+    attr.val.clusterDim.x = cluster;
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    EP_CUDA(cudaLaunchKernelEx(&cfg, gemm_kernel<kSwiglu, kCtas>, map_x, map_w, a));
+    EP_CUDA(cudaLaunchKernelEx(&cfg, gemm_kernel<kSwiglu, kCtas, kSplit>, map_x, map_w, a));
     return EP_OK;
 }
 
@@ -600,11 +703,18 @@ static ep_status launch_gemm(const char* fn, const ep_fp8_rows* x, const ep_row_
         const ep_status st = encode_rows(&map_w, w->codes, 3, dims, strides, box, fn);
         if (st != EP_OK) return st;
     }
+    int dev = 0, sms = 0;
+    EP_CUDA(cudaGetDevice(&dev));
+    EP_CUDA(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
+    // Few tiles: as many blocks to a tile's K as leave each two blocks of K and every cluster one tile.
+    int split = 1;
+    while (split < kSplitMost && most_tiles(a, kBM) * split * 2 <= sms && a.KB >= split * 4) split *= 2;
+    if (split > 1) return launch_shape<kSwiglu, 1, true>(fn, map_x, map_w, a, sms, split, stream);
     // Rows of a group: what the arrays hold, shared out.  The regions of the packed layout are sized for
     // the worst case, a low-latency step fills a few percent of them.
     const int64_t per_group = x->rows / w->groups / (w->groups > 1 && !g->offsets ? 16 : 1);
-    if (per_group >= kPairRows) return launch_shape<kSwiglu, 2>(fn, map_x, map_w, a, stream);
-    return launch_shape<kSwiglu, 1>(fn, map_x, map_w, a, stream);
+    if (per_group >= kPairRows) return launch_shape<kSwiglu, 2, false>(fn, map_x, map_w, a, sms, 2, stream);
+    return launch_shape<kSwiglu, 1, false>(fn, map_x, map_w, a, sms, 1, stream);
 }
 
 }  // namespace ep

@@ -82,6 +82,32 @@ def test_gemm_dense(rows, K, N):
 
 
 @gpu
+@pytest.mark.parametrize("rows", [1, 3, 130])
+@pytest.mark.parametrize("K,I", [(7168, 128), (1408, 256), (512, 640)])
+def test_swiglu_dense(rows, K, I):
+    """Few tiles: the blocks of a cluster share K."""
+    g = gen(rows + K + I)
+    x, xs = quantize_rows(randn((rows, K), g))
+    w, ws = quantize_weight(randn((1, 2 * I, K), g) * K ** -0.5)
+    codes, scales = ep.expert_swiglu(x, xs, w[0], ws[0])
+    assert_fp8_close(codes, scales, *swiglu64(rows64(x, xs), weight64(w[0], ws[0])))
+
+
+@gpu
+@pytest.mark.parametrize("counts", [[0, 0, 3], [0, 0, 0], [130, 1, 0]])
+def test_few_tiles_with_empty_groups(counts):
+    cnt, off, hoff, x, xs, w, ws = case(counts, 1024, 136, seed=sum(counts), gap=1)
+    out = torch.full((x.shape[0], 136), 7.0, dtype=torch.bfloat16, device="cuda")
+    ep.expert_gemm(x, xs, w, ws, counts=cnt, offsets=off, out=out)
+    own = torch.zeros(x.shape[0], dtype=torch.bool, device="cuda")
+    for e, (o, c) in enumerate(zip(hoff, counts)):
+        own[o:o + c] = True
+        if c:
+            assert_bf16_close(out[o:o + c], *product64(rows64(x[o:o + c], xs[o:o + c]), weight64(w[e], ws[e])), f"group {e}")
+    assert (out[~own] == 7.0).all()
+
+
+@gpu
 @pytest.mark.parametrize("fn", ["gemm", "swiglu"])
 def test_packed_regions(fn):
     g = gen(3)
