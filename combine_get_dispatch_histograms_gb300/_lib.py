@@ -38,7 +38,8 @@ class EpFp8Rows(ctypes.Structure):
 
 
 class EpRowGroups(ctypes.Structure):
-    _fields_ = [("counts", P), ("offsets", P), ("bases", P), ("per_base", I32), ("stride", I64)]
+    _fields_ = [("counts", P), ("offsets", P), ("bases", P), ("per_base", I32), ("stride", I64),
+                ("expected", I64)]
 
 
 class EpFp8Weight(ctypes.Structure):

@@ -629,7 +629,8 @@ static ep_status check_products(const char* fn, const ep_fp8_rows* x, const ep_r
                              (long long)x->scale_stride, w->k);
     }
     if (g->bases && g->per_base < 1) return set_error(EP_ERR_INVALID_ARG, "%s: groups per base %d", fn, g->per_base);
-    if (g->stride < 0) return set_error(EP_ERR_INVALID_ARG, "%s: group stride %lld", fn, (long long)g->stride);
+    if (g->stride < 0 || g->expected < 0)
+        return set_error(EP_ERR_INVALID_ARG, "%s: group stride %lld, expected rows %lld", fn, (long long)g->stride, (long long)g->expected);
     return EP_OK;
 }
 
@@ -710,9 +711,10 @@ static ep_status launch_gemm(const char* fn, const ep_fp8_rows* x, const ep_row_
     int split = 1;
     while (split < kSplitMost && most_tiles(a, kBM) * split * 2 <= sms && a.KB >= split * 4) split *= 2;
     if (split > 1) return launch_shape<kSwiglu, 1, true>(fn, map_x, map_w, a, sms, split, stream);
-    // Rows of a group: what the arrays hold, shared out.  The regions of the packed layout are sized for
-    // the worst case, a low-latency step fills a few percent of them.
-    const int64_t per_group = x->rows / w->groups / (w->groups > 1 && !g->offsets ? 16 : 1);
+    // Rows of a group: as the caller expects, or what the arrays hold, shared out.  The regions of the
+    // packed layout are sized for the worst case, a low-latency step fills a few percent of them.
+    const int64_t per_group =
+        g->expected > 0 ? g->expected : x->rows / w->groups / (w->groups > 1 && !g->offsets ? 16 : 1);
     if (per_group >= kPairRows) return launch_shape<kSwiglu, 2, false>(fn, map_x, map_w, a, sms, 2, stream);
     return launch_shape<kSwiglu, 1, false>(fn, map_x, map_w, a, sms, 1, stream);
 }

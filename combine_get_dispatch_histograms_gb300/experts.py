@@ -86,7 +86,7 @@ def _step(name: str, t: torch.Tensor) -> int:
     return st[0] if shape[0] > 1 else max(st[0], n)
 
 
-def _products(name, x, x_scales, w, w_scales, counts, offsets, bases):
+def _products(name, x, x_scales, w, w_scales, counts, offsets, bases, expected):
     """The C descriptors of one product and (device index, row shape, weight rows), all checked."""
     index = x.get_device()
     if index < 0:
@@ -126,7 +126,7 @@ def _products(name, x, x_scales, w, w_scales, counts, offsets, bases):
     return (index, xs[:-1], n,
             EpFp8Rows(x.data_ptr(), _step(name, x), x_scales.data_ptr(), _step(name, x_scales), rows),
             EpRowGroups(None if counts is None else counts.data_ptr(), None if offsets is None else offsets.data_ptr(),
-                        None if bases is None else bases.data_ptr(), per_base, stride),
+                        None if bases is None else bases.data_ptr(), per_base, stride, expected),
             EpFp8Weight(w.data_ptr(), w_scales.data_ptr(), groups, n, k))
 
 
@@ -154,9 +154,12 @@ def _output(name, t, shape, dtype, index):
     return _step(name, t)
 
 
-def expert_gemm(x, x_scales, w, w_scales, counts=None, offsets=None, out=None, status=None, stream=None, *, bases=None):
-    """y = x w^T per expert: bf16 [rows][N] (or [E][cap][N]).  Rows of no expert are not written."""
-    index, lead, n, cx, cg, cw = _products("expert_gemm", x, x_scales, w, w_scales, counts, offsets, bases)
+def expert_gemm(x, x_scales, w, w_scales, counts=None, offsets=None, out=None, status=None, stream=None, *, bases=None, expected_rows=0):
+    """y = x w^T per expert: bf16 [rows][N] (or [E][cap][N]).  Rows of no expert are not written.
+
+    bases: int32 [R + 1], added to the offsets of R equal runs of experts (a dispatch handle's perm_rank_base).
+    expected_rows: about how many rows an expert has, where the caller knows; it only chooses the kernel's shape."""
+    index, lead, n, cx, cg, cw = _products("expert_gemm", x, x_scales, w, w_scales, counts, offsets, bases, expected_rows)
     if out is None:
         with torch.cuda.stream(stream):
             out = torch.empty(*lead, n, dtype=_BF16, device=x.device)
@@ -166,10 +169,10 @@ def expert_gemm(x, x_scales, w, w_scales, counts=None, offsets=None, out=None, s
     return out
 
 
-def expert_swiglu(x, x_scales, w13, w13_scales, counts=None, offsets=None, out=None, status=None, stream=None, *, bases=None):
+def expert_swiglu(x, x_scales, w13, w13_scales, counts=None, offsets=None, out=None, status=None, stream=None, *, bases=None, expected_rows=0):
     """silu(x wg^T) * (x wu^T) per expert, w13 = [gate; up] [E][2I][K], requantised:
     (codes [rows][I] uint8, scales [rows][I / 128]) (or [E][cap][..])."""
-    index, lead, n, cx, cg, cw = _products("expert_swiglu", x, x_scales, w13, w13_scales, counts, offsets, bases)
+    index, lead, n, cx, cg, cw = _products("expert_swiglu", x, x_scales, w13, w13_scales, counts, offsets, bases, expected_rows)
     if n % 256:
         _refuse(f"expert_swiglu: {n} weight rows are no gate and up of a multiple of 128 each")
     inter = n // 2

@@ -210,6 +210,21 @@ def test_non_finite_and_zero_rows_stay_in_their_row():
 
 
 @gpu
+@pytest.mark.parametrize("expected", [1, 4096])
+def test_expected_rows_only_choose_the_shape(expected):
+    """Both shapes of the kernel on the same groups, whatever the caller expects."""
+    for counts in (RAGGED, LONG):
+        cnt, off, hoff, x, xs, w, ws = case(counts, 384, 512, seed=sum(counts))
+        y = ep.expert_gemm(x, xs, w, ws, counts=cnt, offsets=off, expected_rows=expected)
+        codes, scales = ep.expert_swiglu(x, xs, w, ws, counts=cnt, offsets=off, expected_rows=expected)
+        for e, (o, c) in enumerate(zip(hoff, counts)):
+            if c:
+                r, wt = rows64(x[o:o + c], xs[o:o + c]), weight64(w[e], ws[e])
+                assert_bf16_close(y[o:o + c], *product64(r, wt), f"group {e}")
+                assert_fp8_close(codes[o:o + c], scales[o:o + c], *swiglu64(r, wt), f"group {e}")
+
+
+@gpu
 def test_repeats_bitwise():
     cnt, off, _, x, xs, w, ws = case(RAGGED, 1024, 512, seed=5)
     a = ep.expert_gemm(x, xs, w, ws, counts=cnt, offsets=off, out=torch.zeros(x.shape[0], 512, dtype=torch.bfloat16, device="cuda"))
@@ -266,7 +281,7 @@ def test_c_refusals_without_a_gpu():
     import ctypes
     lib = _lib.load()
     x = _lib.EpFp8Rows(256, 128, 256, 1, 4)
-    g = _lib.EpRowGroups(None, None, None, 0, 4)
+    g = _lib.EpRowGroups(None, None, None, 0, 4, 0)
     w = lambda **k: _lib.EpFp8Weight(*[dict(dict(codes=256, scales=256, groups=1, n=8, k=128), **k)[n] for n in  # noqa: E731
                                        ("codes", "scales", "groups", "n", "k")])
     call = lambda x_, w_: lib.ep_expert_gemm(ctypes.byref(x_), ctypes.byref(g), ctypes.byref(w_), 256, 8, None, None)  # noqa: E731
