@@ -23,7 +23,6 @@ constexpr int kBoxRows = 32;           // rows of one copy of x: a short group c
 constexpr int kSumGroups = 4;          // warpgroups that sum, each a quarter of the tile's columns
 constexpr int kSumWarps = 4 * kSumGroups;
 constexpr int kGemmThreads = 128 + 128 * kSumGroups;  // copy, mma, tensor-memory and tile warp first
-constexpr int kOutStride = 80;         // bytes of a staged row of 32 bf16: rows fall into other banks
 
 // The two shapes of the kernel.  kCtas = 2: a pair of blocks makes a tile of 256
 // rows; each copies half of the weight's rows, so that a block moves 32 KB per
@@ -35,8 +34,8 @@ struct GemmShape {
     static constexpr int kStageA = kBM * kBK;          // bytes in each block
     static constexpr int kStageB = kBN / kCtas * kBK;
     static constexpr int kStage = kStageA + kStageB;
-    // of a warp's output on its way: 32 rows of 32 columns, padded, or (48 KB stages leave no room) of 8
-    static constexpr int kOut = kCtas == 2 ? 32 * kOutStride : 32 * 16;
+    // of a warp's output on its way: 32 rows of 64 columns, or (48 KB stages leave no room) of 8
+    static constexpr int kOut = kCtas == 2 ? 32 * 128 : 32 * 16;
     static constexpr size_t kSmem = 1024 + kStages * kStage + kSumWarps * kOut;
 };
 constexpr int kTileRing = 4;            // tiles announced ahead
@@ -44,7 +43,9 @@ constexpr int kScaleChunk = 8;          // blocks of K whose scales are staged t
 constexpr int kScaleRing = 2;
 constexpr int kMaxGroups = 4096;
 constexpr int kChunkRows = 2048;       // rows that share a pass over the weight's tiles
-constexpr int kPairRows = 192;         // rows of a group from which pairs of blocks are faster
+constexpr int kPairRows = 144;         // rows of a group from which pairs of blocks are faster (40 groups, K 2048,
+                                       // N 7168, us by one block / by pairs: 64 rows 111 / 135, 128 147 / 158,
+                                       // 160 240 / 160, 256 211 / 164, 320 260 / 291, 512 393 / 290)
 constexpr int kSplitMost = 4;          // blocks of a cluster that share a tile's K (one row, K 7168, N 4096:
                                        // 27.6 us alone, 18.8 by 2, 14.1 by 4, 21.0 by 8)
 constexpr int kSplitStride = kBN + 4;  // floats of a row of sums: rows fall into other banks
@@ -171,7 +172,8 @@ struct TileWalk {
 // block alone would walk all of K; every cluster has at most one tile.
 template <bool kSwiglu, int kCtas, bool kSplit>
 __global__ void __launch_bounds__(kGemmThreads, 1)
-gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w, const GemmArgs a) {
+gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
+            const __grid_constant__ CUtensorMap map_out, const GemmArgs a) {
     using Shape = GemmShape<kCtas>;
     constexpr int kTileM = Shape::kTileM, kStage = Shape::kStage, kStageA = Shape::kStageA;
     extern __shared__ __align__(1024) uint8_t dyn[];
@@ -210,6 +212,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
         fence_mbar_init();
         tma_prefetch_desc(&map_x);
         tma_prefetch_desc(&map_w);
+        if (!kSwiglu && kCtas == 2 && a.out_vec) tma_prefetch_desc(&map_out);
     }
     if (warp == 2) tmem_alloc<kCtas>(&sh.tmem, 512);
     tc_fence_before();
@@ -488,37 +491,46 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
                         }
                     }
                 } else {
-                    // 32 columns at a time through shared memory, so that a warp's store covers whole
-                    // 64-byte pieces of rows
+                    // The warp's 32 rows x 64 columns through shared memory in the 128-byte swizzle.  A full
+                    // set of rows goes out as one copy, which the next tile's products hide; the rows of
+                    // a group's last tile, and unaligned rows, are stored by the lanes.
+                    bulk_wait_read<0>();  // lane 0's copy of the last tile has read the buffer
+                    __syncwarp();
 #pragma unroll
-                    for (int z = 0; z < 2; ++z) {
+                    for (int q = 0; q < 8; ++q) {
+                        __nv_bfloat162 p[4];
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            __nv_bfloat162 p[4];
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                p[i] = __floats2bfloat162_rn(acc[z * 32 + q * 8 + 2 * i], acc[z * 32 + q * 8 + 2 * i + 1]);
-                            *reinterpret_cast<int4*>(stage + lane * kOutStride + q * 16) = *reinterpret_cast<const int4*>(p);
-                        }
+                        for (int i = 0; i < 4; ++i) p[i] = __floats2bfloat162_rn(acc[q * 8 + 2 * i], acc[q * 8 + 2 * i + 1]);
+                        *reinterpret_cast<int4*>(stage + lane * 128 + ((q ^ (lane & 7)) << 4)) = *reinterpret_cast<const int4*>(p);
+                    }
+                    if (a.out_vec && rows == 32) {
+                        fence_proxy_async_smem();
                         __syncwarp();
+                        if (lane == 0) {
+                            if (n0 < a.N) tma_store_2d(&map_out, stage, n0 * 2, row0 + (warp & 3) * 32);
+                            bulk_commit();
+                        }
+                    } else {
+                        __syncwarp();
+                        auto at = [&](int i, int c) { return stage + i * 128 + (((c >> 3) ^ (i & 7)) << 4) + (c & 7) * 2; };
                         if (a.out_vec) {
-                            const int c = (lane & 3) * 8;
-                            for (int i = lane >> 2; i < rows; i += 8) {
-                                const int4 v = *reinterpret_cast<const int4*>(stage + i * kOutStride + c * 2);
-                                __nv_bfloat16* d = o + i * a.out_stride + z * 32 + c;
-                                if (n0 + z * 32 + c + 8 <= a.N) {
+                            const int c = (lane & 7) * 8;
+                            for (int i = lane >> 3; i < rows; i += 4) {
+                                const int4 v = *reinterpret_cast<const int4*>(at(i, c));
+                                __nv_bfloat16* d = o + i * a.out_stride + c;
+                                if (n0 + c + 8 <= a.N) {
                                     *reinterpret_cast<int4*>(d) = v;
                                 } else {
                                     const __nv_bfloat16* e = reinterpret_cast<const __nv_bfloat16*>(&v);
                                     for (int j = 0; j < 8; ++j)
-                                        if (n0 + z * 32 + c + j < a.N) d[j] = e[j];
+                                        if (n0 + c + j < a.N) d[j] = e[j];
                                 }
                             }
-                        } else if (n0 + z * 32 + lane < a.N) {
-                            for (int i = 0; i < rows; ++i)
-                                o[i * a.out_stride + z * 32 + lane] = *reinterpret_cast<const __nv_bfloat16*>(stage + i * kOutStride + lane * 2);
+                        } else {
+                            for (int c = lane; c < 64 && n0 + c < a.N; c += 32)
+                                for (int i = 0; i < rows; ++i)
+                                    o[i * a.out_stride + c] = *reinterpret_cast<const __nv_bfloat16*>(at(i, c));
                         }
-                        __syncwarp();
                     }
                 }
             }
@@ -526,6 +538,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
             if (lane == 0) mbar_arrive(tr.bar(tile_empty));
             ++tr.n;
         }
+        bulk_wait_all();
         if constexpr (kSplit) {
             __syncwarp();
             cluster_sync();
@@ -642,7 +655,8 @@ static int64_t most_tiles(const GemmArgs& a, int tile_rows) {
 }
 
 template <bool kSwiglu, int kCtas, bool kSplit>
-static ep_status launch_shape(const char* fn, const CUtensorMap& map_x, const CUtensorMap& map_w, const GemmArgs& a, int sms,
+static ep_status launch_shape(const char* fn, const CUtensorMap& map_x, const CUtensorMap& map_w,
+                              const CUtensorMap& map_out, const GemmArgs& a, int sms,
                               int cluster, void* stream) {
     using Shape = GemmShape<kCtas>;
     const int64_t most = most_tiles(a, Shape::kTileM);
@@ -666,7 +680,7 @@ static ep_status launch_shape(const char* fn, const CUtensorMap& map_x, const CU
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    EP_CUDA(cudaLaunchKernelEx(&cfg, gemm_kernel<kSwiglu, kCtas, kSplit>, map_x, map_w, a));
+    EP_CUDA(cudaLaunchKernelEx(&cfg, gemm_kernel<kSwiglu, kCtas, kSplit>, map_x, map_w, map_out, a));
     return EP_OK;
 }
 
@@ -689,7 +703,7 @@ static ep_status launch_gemm(const char* fn, const ep_fp8_rows* x, const ep_row_
     a.per_base = g->per_base;
     a.group_stride = g->stride;
     a.rows = x->rows;
-    CUtensorMap map_x, map_w;
+    CUtensorMap map_x, map_w, map_out;
     {
         const cuuint64_t dims[2] = {(cuuint64_t)w->k, (cuuint64_t)x->rows};
         const cuuint64_t strides[1] = {(cuuint64_t)x->code_stride};
@@ -704,19 +718,28 @@ static ep_status launch_gemm(const char* fn, const ep_fp8_rows* x, const ep_row_
         const ep_status st = encode_rows(&map_w, w->codes, 3, dims, strides, box, fn);
         if (st != EP_OK) return st;
     }
+    if (!kSwiglu && a.out_vec) {
+        const cuuint64_t dims[2] = {(cuuint64_t)w->n * 2, (cuuint64_t)x->rows};
+        const cuuint64_t strides[1] = {(cuuint64_t)a.out_stride * 2};
+        const cuuint32_t box[2] = {128, 32};
+        const ep_status st = encode_rows(&map_out, a.out, 2, dims, strides, box, fn);
+        if (st != EP_OK) return st;
+    } else {
+        map_out = map_x;  // not used
+    }
     int dev = 0, sms = 0;
     EP_CUDA(cudaGetDevice(&dev));
     EP_CUDA(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
     // Few tiles: as many blocks to a tile's K as leave each two blocks of K and every cluster one tile.
     int split = 1;
     while (split < kSplitMost && most_tiles(a, kBM) * split * 2 <= sms && a.KB >= split * 4) split *= 2;
-    if (split > 1) return launch_shape<kSwiglu, 1, true>(fn, map_x, map_w, a, sms, split, stream);
+    if (split > 1) return launch_shape<kSwiglu, 1, true>(fn, map_x, map_w, map_out, a, sms, split, stream);
     // Rows of a group: as the caller expects, or what the arrays hold, shared out.  The regions of the
     // packed layout are sized for the worst case, a low-latency step fills a few percent of them.
     const int64_t per_group =
         g->expected > 0 ? g->expected : x->rows / w->groups / (w->groups > 1 && !g->offsets ? 16 : 1);
-    if (per_group >= kPairRows) return launch_shape<kSwiglu, 2, false>(fn, map_x, map_w, a, sms, 2, stream);
-    return launch_shape<kSwiglu, 1, false>(fn, map_x, map_w, a, sms, 1, stream);
+    if (per_group >= kPairRows) return launch_shape<kSwiglu, 2, false>(fn, map_x, map_w, map_out, a, sms, 2, stream);
+    return launch_shape<kSwiglu, 1, false>(fn, map_x, map_w, map_out, a, sms, 1, stream);
 }
 
 }  // namespace ep

@@ -148,6 +148,14 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* m, int
             : "memory");
 }
 
+// From this block's shared memory, 128-byte rows in the 128-byte swizzle; part of
+// the thread's bulk group.
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* m, const void* src, int x, int y) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(m), "r"(smem_u32(src)),
+                 "r"(x), "r"(y)
+                 : "memory");
+}
+
 // ---- tensor memory and tcgen05.mma, by one block or by pairs of blocks ---------------
 // Every tcgen05 instruction of a kernel names the same number of blocks.
 template <int kCtas>
