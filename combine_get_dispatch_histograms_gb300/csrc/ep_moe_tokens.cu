@@ -75,7 +75,7 @@ struct TokArgs {
 struct TokBarriers {
     uint64_t copied[10], filled[10], done[10], acc_empty[2], drain;
     uint32_t tmem;
-    int abort, last;
+    int abort, last, entries;
     float scale[kTokScaleRing][kTokSlots];
 };
 
@@ -157,6 +157,53 @@ __device__ __forceinline__ int build_list(const TokArgs& a, const TokLists& s, u
     }
     __syncthreads();
     return total >> 16;
+}
+
+// The same for at most 32 pairs of at most kTokSlots tokens, by one warp: a pair
+// per lane, so that a block waits for one load and no barrier (2.1 us for the
+// general form, most of it barriers).  Entries in the order in which the pairs
+// first name their experts.
+template <bool kDown>
+__device__ __forceinline__ void build_short_list(const TokArgs& a, const TokLists& s, int* entries) {
+    const int lane = threadIdx.x & 31, pairs = a.T * a.K, t = lane / a.K;
+    const int64_t e64 = lane < pairs ? a.topk_idx[lane] : -1;
+    const float w = kDown && lane < pairs ? a.topk_weights[lane] : 0.0f;
+    const bool ok = e64 >= 0 && e64 < a.E;
+    if (!kDown && !ok && e64 != -1 && a.status && blockIdx.x == 0) flag(a.status, FLAG_INVALID_TOPK);
+    const int e = ok ? (int)e64 : -1 - lane;  // its own group, left out below
+    const uint32_t same = __match_any_sync(0xffffffffu, e), lower = lanemask_lt();
+    const uint32_t token = __match_any_sync(0xffffffffu, t);
+    // a token that names an expert again adds its weight to the first pair
+    const bool first = ok && !(same & token & lower);
+    const uint32_t firsts = __ballot_sync(0xffffffffu, first);
+    const bool leads = ok && !(same & lower);
+    const uint32_t leaders = __ballot_sync(0xffffffffu, leads);
+    // pairs of the entries of earlier leaders: every lane's entry is its group's leader's
+    int base = 0;
+    for (uint32_t m = leaders; m; m &= m - 1) {
+        const int b = __ffs(m) - 1;
+        const int n = __popc(__shfl_sync(0xffffffffu, same, b) & firsts);
+        if (b < __ffs(same) - 1) base += n;
+    }
+    const int at = base + __popc(same & firsts & lower);
+    if (leads) {
+        const int i = __popc(leaders & lower);
+        s.expert[i] = (uint16_t)e;
+        s.base[i] = (uint16_t)base;
+    }
+    if (first) s.token[at] = (uint8_t)t;
+    if constexpr (kDown) {
+        float v = 0.0f;
+        for (int b = 0; b < 32; ++b) {
+            const float x = __shfl_sync(0xffffffffu, w, b);
+            if (same & token & (1u << b)) v += x;
+        }
+        if (first) s.weight[at] = v;
+    }
+    if (lane == 0) {
+        *entries = __popc(leaders);
+        s.base[*entries] = (uint16_t)__popc(firsts);
+    }
 }
 
 // The runs of one block: an entry's tile and a range of its blocks of K.
@@ -254,12 +301,21 @@ __global__ void __launch_bounds__(kTokThreads, 1) tok_kernel(const __grid_consta
         tma_prefetch_desc(&map_w);
     }
     if (warp == 2) tmem_alloc<1>(&sh.tmem, 128);
-    const int A = build_list<kDown>(a, s, ring);
-    fence_proxy_async_smem();  // the list's scratch becomes the ring
+    int A = 0;
+    const bool brief = a.T <= kTokSlots && a.T * a.K <= 32;
+    if (brief) {
+        if (warp == 3) build_short_list<kDown>(a, s, &sh.entries);
+        if (kDown)
+            for (int i = tid; i < a.T * kTokRows; i += kTokThreads) s.acc[i] = 0.0f;
+    } else {
+        A = build_list<kDown>(a, s, ring);
+        fence_proxy_async_smem();  // the list's scratch becomes the ring
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sh.tmem;
+    if (brief) A = sh.entries;
 
     const int tiles = kDown ? (a.H + kTokRows - 1) / kTokRows : (a.I + kTokRows / 2 - 1) / (kTokRows / 2);
     const int total = A * tiles * (kDown ? a.blocks_k : a.split);

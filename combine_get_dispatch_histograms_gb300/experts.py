@@ -148,6 +148,14 @@ def _call(name: str, index: int, *args):
             check(name, fn(*args))
 
 
+def _empty(like, stream, shape, dtype=None):
+    """A tensor on `like`'s device (of its type by default), allocated for `stream`."""
+    if stream is None:
+        return like.new_empty(shape) if dtype is None else like.new_empty(shape, dtype=dtype)
+    with torch.cuda.stream(stream):
+        return like.new_empty(shape, dtype=dtype)
+
+
 def _output(name, t, shape, dtype, index):
     if t.shape != shape or t.dtype != dtype or t.get_device() != index:
         _refuse(f"{name}: {dtype} {tuple(shape)} on the same device: got {t.dtype} {tuple(t.shape)}")
@@ -161,8 +169,7 @@ def expert_gemm(x, x_scales, w, w_scales, counts=None, offsets=None, out=None, s
     expected_rows: about how many rows an expert has, where the caller knows; it only chooses the kernel's shape."""
     index, lead, n, cx, cg, cw = _products("expert_gemm", x, x_scales, w, w_scales, counts, offsets, bases, expected_rows)
     if out is None:
-        with torch.cuda.stream(stream):
-            out = torch.empty(*lead, n, dtype=_BF16, device=x.device)
+        out = _empty(x, stream, (*lead, n), _BF16)
     step = _output("expert_gemm: out", out, (*lead, n), _BF16, index)
     _call("ep_expert_gemm", index, ctypes.byref(cx), ctypes.byref(cg), ctypes.byref(cw), out.data_ptr(), step,
           _status_ptr(status, index), _stream_of(stream, index))
@@ -177,9 +184,7 @@ def expert_swiglu(x, x_scales, w13, w13_scales, counts=None, offsets=None, out=N
         _refuse(f"expert_swiglu: {n} weight rows are no gate and up of a multiple of 128 each")
     inter = n // 2
     if out is None:
-        with torch.cuda.stream(stream):
-            out = (torch.empty(*lead, inter, dtype=_U8, device=x.device),
-                   torch.empty(*lead, inter // 128, dtype=_F32, device=x.device))
+        out = _empty(x, stream, (*lead, inter), _U8), _empty(x, stream, (*lead, inter // 128), _F32)
     codes, scales = out
     step = _output("expert_swiglu: out codes", codes, (*lead, inter), _E4M3 if codes.dtype == _E4M3 else _U8, index)
     sstep = _output("expert_swiglu: out scales", scales, (*lead, inter // 128), _F32, index)
@@ -226,12 +231,10 @@ def moe_tokens(x, topk_idx, topk_weights, w13, w2, w13_scales=None, w2_scales=No
     if (topk_idx.get_device() != index or topk_weights.get_device() != index or w13.get_device() != index
             or w2.get_device() != index or (workspace is not None and workspace.get_device() != index)):
         _refuse(f"{name}: all tensors must be on the same CUDA device")
-    if out is None or workspace is None:
-        with torch.cuda.stream(stream):
-            if out is None:
-                out = torch.empty(T, H, dtype=_BF16, device=x.device)
-            if workspace is None:
-                workspace = torch.empty(_workspace_bytes(index, T, K, E, H, I, p13 is not None), dtype=_U8, device=x.device)
+    if out is None:
+        out = _empty(x, stream, (T, H))
+    if workspace is None:
+        workspace = _empty(x, stream, (_workspace_bytes(index, T, K, E, H, I, p13 is not None) // 2,))
     step = _output(f"{name}: out", out, (T, H), _BF16, index)
     w = EpMoeWeights(w13.data_ptr(), p13, w2.data_ptr(), p2, E, H, I)
     _call("ep_moe_tokens", index, x.data_ptr(), _step(name, x), T, topk_idx.data_ptr(), topk_weights.data_ptr(), K,

@@ -74,6 +74,17 @@ def test_layer(kind, T, E, K, H, I):
 
 
 @gpu
+@pytest.mark.parametrize("T,K,E", [(16, 2, 3), (4, 8, 4), (3, 10, 2), (1, 32, 64), (16, 2, 1), (17, 1, 2), (11, 3, 3), (2, 16, 5)])
+def test_short_and_long_lists_with_repeats(T, K, E):
+    """Up to 32 pairs one warp builds the expert list, beyond that the block does: repeats, masks, full entries."""
+    g = gen(T * K + E)
+    w = weights(E, 128, 128, "fp8", g)
+    idx = torch.randint(-1, E, (T, K), generator=g, device="cuda")
+    idx[0, 0] = E - 1
+    check(randn((T, 128), g).to(torch.bfloat16), idx, torch.rand(T, K, generator=g, device="cuda"), w)
+
+
+@gpu
 @pytest.mark.parametrize("H,I", [(32, 32), (96, 160), (1056, 32), (64, 1120)])
 def test_bf16_sizes_off_128(H, I):
     g = gen(H + I)
