@@ -232,7 +232,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
             for (int t = unit;; t += units) {
                 GemmTile tile = {0, 0, 0, 0};
                 const bool some = walk.find(a, t, lane, &tile);
-                mbar_wait_warp(tr.bar(tile_empty), tr.phase() ^ 1, kGemmWaitNs, abort);
+                mbar_wait_warp<true>(tr.bar(tile_empty), tr.phase() ^ 1, kGemmWaitNs, abort);
                 if (__any_sync(0xffffffffu, *abort)) break;
                 if (lane == 0) {
                     sh.tile[tr.slot()] = tile;
@@ -248,7 +248,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
                 const float* xs = a.x_scales + (int64_t)(tile.row0 + rank * kBM) * a.x_sstride;
 #pragma unroll 1
                 for (int kb = k0; kb < k1; kb += kScaleChunk) {
-                    mbar_wait_warp(sr.bar(scale_empty), sr.phase() ^ 1, kGemmWaitNs, abort);
+                    mbar_wait_warp<true>(sr.bar(scale_empty), sr.phase() ^ 1, kGemmWaitNs, abort);
                     const float w = lane < 16 && kb + (lane & 7) < k1 ? __ldg(ws + kb) : 0.0f;
                     float* dst = &sh.scale[sr.slot()][0][0][0];
 #pragma unroll 1
@@ -293,7 +293,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
             uint32_t free_phase = (1u << kStages) - 1;  // a fresh barrier counts as passed
             bool ok = true;
             while (ok) {
-                if (!mbar_wait_or_abort(tr.bar(tile_full), tr.phase(), kGemmWaitNs, abort)) break;
+                if (!mbar_wait_or_abort<true>(tr.bar(tile_full), tr.phase(), kGemmWaitNs, abort)) break;
                 const GemmTile tile = sh.tile[tr.slot()];
                 mbar_arrive(tr.bar(tile_empty));
                 ++tr.n;
@@ -307,7 +307,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
                 const uint32_t full0 = kCtas == 2 ? smem_of(full, 0) : full;
                 for (int kb = k0; kb < k1; ++kb) {
                     const int u = (kb - k0) & (kStages - 1);
-                    if (!mbar_wait_or_abort(done + u * 8, free_phase >> u & 1, kGemmWaitNs, abort)) {
+                    if (!mbar_wait_or_abort<true>(done + u * 8, free_phase >> u & 1, kGemmWaitNs, abort)) {
                         ok = false;
                         break;
                     }
@@ -333,7 +333,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
             RingPos<kTileRing> tr;
             uint32_t full_phase = 0, empty_phase = 3;
             while (true) {
-                mbar_wait_warp(tr.bar(tile_full), tr.phase(), kGemmWaitNs, abort);
+                mbar_wait_warp<true>(tr.bar(tile_full), tr.phase(), kGemmWaitNs, abort);
                 const int rows = sh.tile[tr.slot()].rows;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(tr.bar(tile_empty));
@@ -342,8 +342,8 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
 #pragma unroll 1
                 for (int kb = 0; kb < k1 - k0; ++kb) {
                     const int u = kb & (kStages - 1), c = kb & 1;
-                    mbar_wait_warp(full + u * 8, full_phase >> u & 1, kGemmWaitNs, abort);
-                    mbar_wait_warp(acc_empty + c * 8, empty_phase >> c & 1, kGemmWaitNs, abort);
+                    mbar_wait_warp<true>(full + u * 8, full_phase >> u & 1, kGemmWaitNs, abort);
+                    mbar_wait_warp<true>(acc_empty + c * 8, empty_phase >> c & 1, kGemmWaitNs, abort);
                     full_phase ^= 1u << u;
                     empty_phase ^= 1u << c;
                     tc_fence_after();
@@ -380,7 +380,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
         RingPos<kScaleRing> sr;
         uint32_t done_phase = 0;
         while (true) {
-            mbar_wait_warp(tr.bar(tile_full), tr.phase(), kGemmWaitNs, abort);
+            mbar_wait_warp<true>(tr.bar(tile_full), tr.phase(), kGemmWaitNs, abort);
             // the slot is held until the tile is written, so that its fields need no registers
             const GemmTile* tile = &sh.tile[tr.slot()];
             if (tile->rows == 0 || __any_sync(0xffffffffu, *abort)) break;
@@ -392,7 +392,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
 #pragma unroll 1
             for (int kb = 0; kb < k1 - k0; kb += kStages) {
                 if ((kb & (kScaleChunk - 1)) == 0) {
-                    mbar_wait_warp(sr.bar(scale_full), sr.phase(), kGemmWaitNs, abort);
+                    mbar_wait_warp<true>(sr.bar(scale_full), sr.phase(), kGemmWaitNs, abort);
                     sc = sc0 + sr.slot() * (kScaleChunk * 2 * kBM * 4);
                 }
 #pragma unroll
@@ -400,7 +400,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
                     if (kb + u >= k1 - k0) break;
                     const float f0 = ld_shared_f32(sc + u * (2 * kBM * 4));
                     const float f1 = kSwiglu ? ld_shared_f32(sc + u * (2 * kBM * 4) + kBM * 4) : f0;
-                    mbar_wait_warp(done + u * 8, done_phase >> u & 1, kGemmWaitNs, abort);
+                    mbar_wait_warp<true>(done + u * 8, done_phase >> u & 1, kGemmWaitNs, abort);
                     done_phase ^= 1u << u;
                     if (rows_here) {
                         tc_fence_after();
@@ -408,13 +408,13 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
                         float v[32];
                         tmem_ld(ad + c0, v);
                         tmem_wait_ld(v);
-                        fma32(acc, v, f0);
+                        fma_by(acc, v, f0);
                         tmem_ld(ad + c1, v);
                         tmem_wait_ld(v);
                         tc_fence_before();
                         __syncwarp();  // all loads are in registers: the accumulator is free
                         if (lane == 0) mbar_hand_back(free_bar + (u & 1) * 8);
-                        fma32(acc + 32, v, f1);
+                        fma_by(acc + 32, v, f1);
                     } else if (lane == 0) {
                         mbar_hand_back(free_bar + (u & 1) * 8);
                     }
@@ -451,7 +451,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
                 sh.amax[mx][quarter][r] = m;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&sh.amax_full[mx]));
-                mbar_wait_warp(smem_u32(&sh.amax_full[mx]), tr.n >> 1 & 1, kGemmWaitNs, abort);
+                mbar_wait_warp<true>(smem_u32(&sh.amax_full[mx]), tr.n >> 1 & 1, kGemmWaitNs, abort);
 #pragma unroll
                 for (int i = 0; i < kSumGroups; ++i) m = fmaxf(m, sh.amax[mx][i][r]);
                 const float scale = __fdiv_rn(m, 448.0f);

@@ -8,15 +8,28 @@
 namespace ep {
 
 // ---- bounded mbarrier waits, on shared addresses -----------------------------------
+// kLong: a thread that has to wait is suspended for up to 20 us instead of the
+// system's own limit, so that waiting warps do not take issue slots from those
+// that share their scheduler.
+template <bool kLong>
 __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
     uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
+    if constexpr (kLong)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity), "r"(20000u)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity)
+            : "memory");
     return ok != 0;
 }
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
@@ -25,11 +38,12 @@ __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
 // The clock is read only once in 256 failed tries (each suspends the thread for
 // a while), so that a wait in a hot loop costs no timer access.  Returns false
 // after `limit_ns`, or as soon as another role gave up (*abort).
+template <bool kLong = false>
 __device__ __forceinline__ bool mbar_wait_or_abort(uint32_t bar, uint32_t parity, int64_t limit_ns, volatile int* abort) {
-    if (mbar_try(bar, parity)) return true;
+    if (mbar_try<kLong>(bar, parity)) return true;
     uint64_t t0 = 0;
     for (uint32_t i = 1;; ++i) {
-        if (mbar_try(bar, parity)) return true;
+        if (mbar_try<kLong>(bar, parity)) return true;
         if ((i & 255u) == 0) {
             if (*abort) return false;
             const uint64_t t = globaltimer_ns();
@@ -43,11 +57,12 @@ __device__ __forceinline__ bool mbar_wait_or_abort(uint32_t bar, uint32_t parity
 }
 // The same for a whole warp, which stays together; after a give-up it returns
 // as after success, and the caller looks at *abort where it can leave.
+template <bool kLong = false>
 __device__ __forceinline__ void mbar_wait_warp(uint32_t bar, uint32_t parity, int64_t limit_ns, volatile int* abort) {
-    if (__all_sync(0xffffffffu, mbar_try(bar, parity))) return;
+    if (__all_sync(0xffffffffu, mbar_try<kLong>(bar, parity))) return;
     uint64_t t0 = 0;
     for (uint32_t i = 1;; ++i) {
-        if (__all_sync(0xffffffffu, mbar_try(bar, parity))) return;
+        if (__all_sync(0xffffffffu, mbar_try<kLong>(bar, parity))) return;
         if ((i & 255u) == 0) {
             const uint64_t t = globaltimer_ns();
             if (t0 == 0) t0 = t;
@@ -286,16 +301,16 @@ __device__ __forceinline__ float silu_mul(float g, float u) {
     return g * r * u;
 }
 
-// d[0..31] += v[0..31] * f, two at a time: half the instructions, and fewer
-// register-bank conflicts (1.2 cycles a value and warp against 1.5, measured).
-__device__ __forceinline__ void fma32(float* d, float (&v)[32], float f) {
+// d[i] += v[i] * f, two at a time: half the instructions, and fewer register-bank
+// conflicts (1.2 cycles a value and warp against 1.5, measured).
+template <int kN>
+__device__ __forceinline__ void fma_by(float* d, float (&v)[kN], float f) {
 #pragma unroll
-    for (int i = 0; i < 32; i += 2)
-        asm("{\n\t.reg .b64 a, b, c;\n\t"
-            "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %4};\n\tmov.b64 c, {%0, %1};\n\t"
-            "fma.rn.f32x2 c, a, b, c;\n\tmov.b64 {%0, %1}, c;\n\t}"
-            : "+f"(d[i]), "+f"(d[i + 1])
-            : "f"(v[i]), "f"(v[i + 1]), "f"(f));
+    for (int i = 0; i < kN; i += 2) {
+        const float2 s = __ffma2_rn(make_float2(v[i], v[i + 1]), make_float2(f, f), make_float2(d[i], d[i + 1]));
+        d[i] = s.x;
+        d[i + 1] = s.y;
+    }
 }
 
 // ---- host: tensor maps ------------------------------------------------------------
