@@ -73,8 +73,10 @@ def _refuse(text: str):
 
 def _step(name: str, t: torch.Tensor) -> int:
     """Elements between the rows of t [rows][n] or [E][rows][n], whose rows have to be evenly spaced."""
+    n = t.shape[-1]
+    if t.is_contiguous():
+        return n
     shape, st = t.shape, t.stride()
-    n = shape[-1]
     if n > 1 and st[-1] != 1:
         _refuse(f"{name}: channels must be contiguous (strides {st})")
     if len(shape) == 2:
@@ -148,12 +150,12 @@ def _call(name: str, index: int, *args):
             check(name, fn(*args))
 
 
-def _empty(like, stream, shape, dtype=None):
-    """A tensor on `like`'s device (of its type by default), allocated for `stream`."""
+def _empty(like, stream, shape, dtype):
+    """A tensor on `like`'s device, allocated for `stream`."""
     if stream is None:
-        return like.new_empty(shape) if dtype is None else like.new_empty(shape, dtype=dtype)
+        return torch.empty(shape, dtype=dtype, device=like.device)
     with torch.cuda.stream(stream):
-        return like.new_empty(shape, dtype=dtype)
+        return torch.empty(shape, dtype=dtype, device=like.device)
 
 
 def _output(name, t, shape, dtype, index):
@@ -232,9 +234,9 @@ def moe_tokens(x, topk_idx, topk_weights, w13, w2, w13_scales=None, w2_scales=No
             or w2.get_device() != index or (workspace is not None and workspace.get_device() != index)):
         _refuse(f"{name}: all tensors must be on the same CUDA device")
     if out is None:
-        out = _empty(x, stream, (T, H))
+        out = _empty(x, stream, (T, H), _BF16)
     if workspace is None:
-        workspace = _empty(x, stream, (_workspace_bytes(index, T, K, E, H, I, p13 is not None) // 2,))
+        workspace = _empty(x, stream, (_workspace_bytes(index, T, K, E, H, I, p13 is not None),), _U8)
     step = _output(f"{name}: out", out, (T, H), _BF16, index)
     w = EpMoeWeights(w13.data_ptr(), p13, w2.data_ptr(), p2, E, H, I)
     _call("ep_moe_tokens", index, x.data_ptr(), _step(name, x), T, topk_idx.data_ptr(), topk_weights.data_ptr(), K,
