@@ -319,7 +319,11 @@ __global__ void __launch_bounds__(kTokThreads, 1) tok_kernel(const __grid_consta
 
     const int tiles = kDown ? (a.H + kTokRows - 1) / kTokRows : (a.I + kTokRows / 2 - 1) / (kTokRows / 2);
     const int total = A * tiles * (kDown ? a.blocks_k : a.split);
-    const int blocks = max(1, min(total, (int)gridDim.x));  // each has work; the rest are idle
+    // Blocks with work; the rest are idle.  In kernel 2 the blocks of a tile each stream per / n stages (0.4 us
+    // each) and the last one adds n parts of T tokens (0.1 us for 4 tokens each, about): n as makes both equal.
+    int most = gridDim.x;
+    if constexpr (kDown) most = min(most, tiles * max(1, (int)sqrtf(4.0f * A * a.blocks_k / ((a.T + 3) / 4))));
+    const int blocks = max(1, min(total, most));
     auto first_of = [&](int b) { return (int)((int64_t)total * b / blocks); };
     TokRuns<kDown> run;
     const bool idle = (int)blockIdx.x >= blocks;
@@ -596,17 +600,26 @@ __global__ void __launch_bounds__(kTokThreads, 1) tok_kernel(const __grid_consta
                     asm volatile("bar.sync 1, 128;" ::: "memory");
                     write = sh.last;
                     if (write)
-                        for (int t0 = 0; t0 < a.T; t0 += 8) {  // eight loads on their way at a time
-                            float v[8] = {};
-                            for (int b = b0; b <= b1; ++b) {
-                                const float* p = a.part + ((int64_t)b * 2 + (run.tile != first_of(b) / per)) * a.T * kTokRows + r;
+                        for (int t0 = 0; t0 < a.T; t0 += 4) {
+                            float v[4] = {};
+                            for (int q0 = b0; q0 <= b1; q0 += 4) {  // sixteen loads on their way at a time
+                                float x[4][4];
 #pragma unroll
-                                for (int q = 0; q < 8; ++q)
-                                    if (t0 + q < a.T) v[q] += __ldcg(p + (t0 + q) * kTokRows);
+                                for (int q = 0; q < 4; ++q) {
+                                    const int b = min(q0 + q, b1);
+                                    const float* p = a.part + ((int64_t)b * 2 + (run.tile != first_of(b) / per)) * a.T * kTokRows + r;
+#pragma unroll
+                                    for (int z = 0; z < 4; ++z) x[q][z] = __ldcg(p + min(t0 + z, a.T - 1) * kTokRows);
+                                }
+#pragma unroll
+                                for (int q = 0; q < 4; ++q)
+                                    if (q0 + q <= b1)
+#pragma unroll
+                                        for (int z = 0; z < 4; ++z) v[z] += x[q][z];
                             }
 #pragma unroll
-                            for (int q = 0; q < 8; ++q)
-                                if (t0 + q < a.T) s.acc[(t0 + q) * kTokRows + r] = v[q];
+                            for (int z = 0; z < 4; ++z)
+                                if (t0 + z < a.T) s.acc[(t0 + z) * kTokRows + r] = v[z];
                         }
                 }
                 for (int t = 0; t < a.T; ++t) {

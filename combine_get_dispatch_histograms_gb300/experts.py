@@ -122,9 +122,10 @@ def _products(name, x, x_scales, w, w_scales, counts, offsets, bases, expected):
         stride = rows
     per_base = 0
     if bases is not None:
-        if bases.dtype != _I32 or not bases.is_contiguous() or bases.get_device() != index:
-            _refuse(f"{name}: bases int32, contiguous, on the same device")
-        per_base = groups // max(1, bases.numel() - 1)
+        runs = bases.numel() - 1
+        if bases.dtype != _I32 or runs < 1 or groups % runs or not bases.is_contiguous() or bases.get_device() != index:
+            _refuse(f"{name}: bases int32 [R + 1] for {groups} groups in R equal runs, contiguous, on the same device")
+        per_base = groups // runs
     return (index, xs[:-1], n,
             EpFp8Rows(x.data_ptr(), _step(name, x), x_scales.data_ptr(), _step(name, x_scales), rows),
             EpRowGroups(None if counts is None else counts.data_ptr(), None if offsets is None else offsets.data_ptr(),

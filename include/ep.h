@@ -397,7 +397,8 @@ typedef struct ep_fp8_rows {
  *     handle->perm_rank_base, per_base = L, counts = handle->num_recv_per_expert;
  *   packed low-latency layout: stride = R * cap, counts = packed_recv_count;
  *   one dense group: stride = the number of rows, all pointers NULL.
- * A group may be empty; rows of no group are neither read nor written. */
+ * A group may be empty; rows of no group are neither read nor written.  bases
+ * holds ceil(groups / per_base) entries at least. */
 typedef struct ep_row_groups {
     const int32_t* counts;
     const int32_t* offsets;
