@@ -110,6 +110,10 @@ __device__ __forceinline__ int group_rows(const GemmArgs& a, int g, bool* cut) {
     int64_t n = a.counts ? (int64_t)a.counts[g] : a.group_stride;
     const int64_t f = group_first(a, g);
     if (n <= 0) return 0;
+    if (!a.offsets && n > a.group_stride) {  // more than its region holds
+        *cut = true;
+        n = a.group_stride;
+    }
     if (f < 0 || f >= a.rows) {
         *cut = true;
         return 0;

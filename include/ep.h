@@ -423,7 +423,8 @@ typedef struct ep_fp8_weight {
  * tensor cores, the blocks are added in fp32, and the result is rounded once.
  * out: bf16 rows, out_stride elements apart.  x->rows is also the capacity of
  * out.  status_out (device, nullable): error bits are ORed into it (2 = a
- * group's rows lie outside x->rows, they were cut off; 4 = a bounded wait ran
+ * group's rows lie outside x->rows, or outside its region of `stride` rows where
+ * there are no offsets, they were cut off; 4 = a bounded wait ran
  * out); the caller zeroes it.  No host synchronisation, no workspace. */
 ep_status ep_expert_gemm(const ep_fp8_rows* x, const ep_row_groups* groups, const ep_fp8_weight* w, void* out,
                          int64_t out_stride, uint32_t* status_out, void* stream);

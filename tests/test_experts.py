@@ -276,6 +276,50 @@ def test_refusals():
         ep.expert_gemm(flat[1:1 + 8 * 256].view(8, 256), xs, w, ws, **ok)
 
 
+@gpu
+def test_regions_hold_no_more_than_their_rows():
+    cnt, off, hoff, x, xs, w, ws = case([40, 40], 128, 256, seed=81)
+    st = ep.new_status()
+    counts = torch.tensor([70, 40], dtype=torch.int32, device="cuda")    # regions of 40 rows
+    out = ep.expert_gemm(x.view(2, 40, 128), xs.view(2, 40, 1), w, ws, counts=counts, status=st)
+    with pytest.raises(ep.EpError) as e:
+        ep.check_status(st)
+    assert e.value.status == "EP_ERR_CAPACITY"
+    for g_ in range(2):
+        r = slice(40 * g_, 40 * g_ + 40)
+        assert_bf16_close(out[g_], *product64(rows64(x[r], xs[r]), weight64(w[g_], ws[g_])))
+
+
+@gpu
+def test_no_rows_and_no_groups_rows():
+    cnt, off, _, x, xs, w, ws = case([3, 4], 128, 128, seed=82)
+    assert ep.expert_gemm(x[:0], xs[:0], w, ws, counts=cnt * 0, offsets=off).shape == (0, 128)
+    out = torch.full((7, 128), 2.0, dtype=torch.bfloat16, device="cuda")
+    ep.expert_gemm(x, xs, w, ws, counts=cnt * 0, offsets=off, out=out)
+    assert (out == 2.0).all()
+    codes, scales = ep.expert_swiglu(x[:0], xs[:0], w.view(1, 256, 128), ws.view(1, 2, 1), counts=cnt[:1] * 0, offsets=off[:1])
+    assert codes.shape == (0, 128) and scales.shape == (0, 1)
+
+
+@gpu
+def test_offsets_past_32_bits():
+    """Rows 60 million elements apart: the last row of x and of the output lies past 2^31 elements and 2^32 bytes."""
+    g = gen(83)
+    rows, K, N, step = 40, 128, 136, 60_000_000
+    q, s = quantize_rows(randn((rows, K), g))
+    xb = torch.empty(rows * step, dtype=torch.uint8, device="cuda")
+    x = torch.as_strided(xb, (rows, K), (step, 1))
+    x.copy_(q)
+    ob = torch.empty(rows * step, dtype=torch.bfloat16, device="cuda")
+    out = torch.as_strided(ob, (rows, N), (step, 1))
+    w, ws = quantize_weight(randn((1, N, K), g) * K ** -0.5)
+    y, err = product64(rows64(q, s), weight64(w[0], ws[0]))
+    for expected in (1, 4096):
+        out.zero_()
+        ep.expert_gemm(x, s, w[0], ws[0], out=out, expected_rows=expected)
+        assert_bf16_close(out, y, err)
+
+
 def test_c_refusals_without_a_gpu():
     from combine_get_dispatch_histograms_gb300 import _lib
     import ctypes
