@@ -81,10 +81,9 @@ SIGNATURES = {
     "ep_combine": (INT, [P, ctypes.POINTER(EpDispatchHandle), P, I64, P, P, P, P]),
     "ep_dispatch_hier": (INT, [P, P, P, P, ctypes.POINTER(EpDispatchHandle), P, P, P, I64, P, P, P, P, P, I64, P]),
     "ep_combine_hier": (INT, [P, ctypes.POINTER(EpDispatchHandle), P, I64, P, P, P, P]),
-    "ep_expert_gemm": (INT, [ctypes.POINTER(EpFp8Rows), ctypes.POINTER(EpRowGroups), ctypes.POINTER(EpFp8Weight), P, I64,
-                             P, P]),
-    "ep_expert_swiglu": (INT, [ctypes.POINTER(EpFp8Rows), ctypes.POINTER(EpRowGroups), ctypes.POINTER(EpFp8Weight), P,
-                               I64, P, I64, P, P]),
+    # the three descriptors by address: a structure's, or bytes packed like it
+    "ep_expert_gemm": (INT, [P, P, P, P, I64, P, P]),
+    "ep_expert_swiglu": (INT, [P, P, P, P, I64, P, I64, P, P]),
     "ep_moe_tokens_workspace": (I64, [I32, I32, ctypes.POINTER(EpMoeWeights)]),
     "ep_moe_tokens": (INT, [P, I64, I32, P, P, I32, ctypes.POINTER(EpMoeWeights), P, I64, P, I64, P, P]),
     "ep_ll_message_bytes": (I64, [INT]),

@@ -22,13 +22,15 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import struct
 
 import torch
 
 from . import _lib
-from ._lib import EpError, EpFp8Rows, EpFp8Weight, EpMoeWeights, EpRowGroups, check
+from ._lib import EpError, EpMoeWeights, check
 
 _U8, _E4M3, _F32, _I32, _BF16 = torch.uint8, torch.float8_e4m3fn, torch.float32, torch.int32, torch.bfloat16
+_CODES = (_U8, _E4M3)
 # bits of a status word, as the C entry points OR them in, by the status a check raises first
 _STATUS_BITS = ((1, -2, "topk_idx holds a value outside [-1, E)"), (4, -4, "a bounded device wait ran out"),
                 (2, -3, "a group's rows lie outside the row arrays"))
@@ -88,49 +90,57 @@ def _step(name: str, t: torch.Tensor) -> int:
     return st[0] if shape[0] > 1 else max(st[0], n)
 
 
+# ep_fp8_rows, ep_row_groups and ep_fp8_weight as the C side lays them out
+_ROWS, _GROUPS, _WEIGHT = struct.Struct("@PqPqq").pack, struct.Struct("@PPPiqq").pack, struct.Struct("@PPiii0P").pack
+
+
 def _products(name, x, x_scales, w, w_scales, counts, offsets, bases, expected):
-    """The C descriptors of one product and (device index, row shape, weight rows), all checked."""
+    """(device index, row shape, weight rows, the three C descriptors) of one product, all checked."""
     index = x.get_device()
+    xs, ws = x.shape, w.shape
+    lead, dims = len(xs), len(ws)
     if index < 0:
         _refuse(f"{name}: all tensors must be on a CUDA device")
-    xs, ws = x.shape, w.shape
-    k, n = xs[-1], ws[-2] if len(ws) >= 2 else 0
-    if len(xs) not in (2, 3) or x.dtype not in (_U8, _E4M3) or k == 0 or k % 128:
+    if lead not in (2, 3) or x.dtype not in _CODES or xs[-1] == 0 or xs[-1] % 128:
         _refuse(f"{name}: codes [rows][K] or [E][rows][K], uint8 or e4m3, K a multiple of 128: got {x.dtype} {tuple(xs)}")
-    if x_scales.dtype != _F32 or x_scales.shape != (*xs[:-1], k // 128):
-        _refuse(f"{name}: fp32 scales {(*xs[:-1], k // 128)}: got {x_scales.dtype} {tuple(x_scales.shape)}")
-    if len(ws) not in (2, 3) or w.dtype not in (_U8, _E4M3) or ws[-1] != k or not w.is_contiguous():
+    k = xs[-1]
+    kb = k // 128
+    ss = x_scales.shape
+    if x_scales.dtype != _F32 or len(ss) != lead or ss[-1] != kb or ss[0] != xs[0] or ss[-2] != xs[-2]:
+        _refuse(f"{name}: fp32 scales {(*xs[:-1], kb)}: got {x_scales.dtype} {tuple(ss)}")
+    if dims not in (2, 3) or w.dtype not in _CODES or ws[-1] != k or not w.is_contiguous():
         _refuse(f"{name}: weight codes [E][N][{k}] or [N][{k}], uint8 or e4m3, contiguous: got {w.dtype} {tuple(ws)}")
-    groups = ws[0] if len(ws) == 3 else 1
-    if w_scales.dtype != _F32 or w_scales.shape != (*ws[:-2], (n + 127) // 128, k // 128) or not w_scales.is_contiguous():
-        _refuse(f"{name}: weight scales fp32 {(*ws[:-2], (n + 127) // 128, k // 128)}, contiguous: got {w_scales.dtype} "
-                f"{tuple(w_scales.shape)}")
+    n, groups = ws[-2], ws[0] if dims == 3 else 1
+    ss = w_scales.shape
+    if (w_scales.dtype != _F32 or len(ss) != dims or ss[-1] != kb or ss[-2] != (n + 127) // 128 or (dims == 3 and ss[0] != groups)
+            or not w_scales.is_contiguous()):
+        _refuse(f"{name}: weight scales fp32 {(*ws[:-2], (n + 127) // 128, kb)}, contiguous: got {w_scales.dtype} {tuple(ss)}")
     if x_scales.get_device() != index or w.get_device() != index or w_scales.get_device() != index:
         _refuse(f"{name}: all tensors must be on the same CUDA device")
-    for t in (counts, offsets):
-        if t is not None and (t.dtype != _I32 or t.numel() != groups or not t.is_contiguous() or t.get_device() != index):
-            _refuse(f"{name}: counts and offsets int32 [{groups}], contiguous, on the same device")
-    rows = xs[0]
-    if len(xs) == 3:
+    counts_at = offsets_at = bases_at = per_base = 0
+    if counts is not None:
+        if counts.dtype != _I32 or counts.numel() != groups or not counts.is_contiguous() or counts.get_device() != index:
+            _refuse(f"{name}: counts int32 [{groups}], contiguous, on the same device")
+        counts_at = counts.data_ptr()
+    if offsets is not None:
+        if offsets.dtype != _I32 or offsets.numel() != groups or not offsets.is_contiguous() or offsets.get_device() != index:
+            _refuse(f"{name}: offsets int32 [{groups}], contiguous, on the same device")
+        offsets_at = offsets.data_ptr()
+    rows = stride = xs[0]
+    if lead == 3:
         if rows != groups or offsets is not None:
             _refuse(f"{name}: {rows} regions for {groups} weights, which take no offsets")
         stride = xs[1]
         rows *= stride
-    else:
-        if groups != 1 and (counts is None or offsets is None):
-            _refuse(f"{name}: {groups} groups need counts and offsets")
-        stride = rows
-    per_base = 0
+    elif groups != 1 and (counts is None or offsets is None):
+        _refuse(f"{name}: {groups} groups need counts and offsets")
     if bases is not None:
         runs = bases.numel() - 1
         if bases.dtype != _I32 or runs < 1 or groups % runs or not bases.is_contiguous() or bases.get_device() != index:
             _refuse(f"{name}: bases int32 [R + 1] for {groups} groups in R equal runs, contiguous, on the same device")
-        per_base = groups // runs
-    return (index, xs[:-1], n,
-            EpFp8Rows(x.data_ptr(), _step(name, x), x_scales.data_ptr(), _step(name, x_scales), rows),
-            EpRowGroups(None if counts is None else counts.data_ptr(), None if offsets is None else offsets.data_ptr(),
-                        None if bases is None else bases.data_ptr(), per_base, stride, expected),
-            EpFp8Weight(w.data_ptr(), w_scales.data_ptr(), groups, n, k))
+        bases_at, per_base = bases.data_ptr(), groups // runs
+    return (index, xs, n, _ROWS(x.data_ptr(), _step(name, x), x_scales.data_ptr(), _step(name, x_scales), rows),
+            _GROUPS(counts_at, offsets_at, bases_at, per_base, stride, expected), _WEIGHT(w.data_ptr(), w_scales.data_ptr(), groups, n, k))
 
 
 def _status_ptr(status, index: int):
@@ -141,14 +151,20 @@ def _status_ptr(status, index: int):
     return status.data_ptr()
 
 
+@functools.lru_cache(maxsize=None)
+def _entry(name: str):
+    return getattr(_lib.load(), name)
+
+
 def _call(name: str, index: int, *args):
     """The C entry point with the tensors' device current."""
-    fn = getattr(_lib.load(), name)
     if _current_device() == index:
-        check(name, fn(*args))
+        code = _entry(name)(*args)
     else:
         with torch.cuda.device(index):
-            check(name, fn(*args))
+            code = _entry(name)(*args)
+    if code:
+        check(name, code)
 
 
 def _empty(like, stream, shape, dtype):
@@ -159,9 +175,12 @@ def _empty(like, stream, shape, dtype):
         return torch.empty(shape, dtype=dtype, device=like.device)
 
 
-def _output(name, t, shape, dtype, index):
-    if t.shape != shape or t.dtype != dtype or t.get_device() != index:
-        _refuse(f"{name}: {dtype} {tuple(shape)} on the same device: got {t.dtype} {tuple(t.shape)}")
+def _output(name, t, like, n, dtypes, index):
+    """Elements between the rows of an output with `like`'s rows and n channels."""
+    shape = t.shape
+    if (len(shape) != len(like) or shape[-1] != n or shape[0] != like[0] or shape[-2] != like[-2] or t.dtype not in dtypes
+            or t.get_device() != index):
+        _refuse(f"{name}: {dtypes[0]} {(*like[:-1], n)} on the same device: got {t.dtype} {tuple(shape)}")
     return _step(name, t)
 
 
@@ -170,11 +189,10 @@ def expert_gemm(x, x_scales, w, w_scales, counts=None, offsets=None, out=None, s
 
     bases: int32 [R + 1], added to the offsets of R equal runs of experts (a dispatch handle's perm_rank_base).
     expected_rows: about how many rows an expert has, where the caller knows; it only chooses the kernel's shape."""
-    index, lead, n, cx, cg, cw = _products("expert_gemm", x, x_scales, w, w_scales, counts, offsets, bases, expected_rows)
+    index, shape, n, cx, cg, cw = _products("expert_gemm", x, x_scales, w, w_scales, counts, offsets, bases, expected_rows)
     if out is None:
-        out = _empty(x, stream, (*lead, n), _BF16)
-    step = _output("expert_gemm: out", out, (*lead, n), _BF16, index)
-    _call("ep_expert_gemm", index, ctypes.byref(cx), ctypes.byref(cg), ctypes.byref(cw), out.data_ptr(), step,
+        out = _empty(x, stream, (*shape[:-1], n), _BF16)
+    _call("ep_expert_gemm", index, cx, cg, cw, out.data_ptr(), _output("expert_gemm: out", out, shape, n, (_BF16,), index),
           _status_ptr(status, index), _stream_of(stream, index))
     return out
 
@@ -182,17 +200,17 @@ def expert_gemm(x, x_scales, w, w_scales, counts=None, offsets=None, out=None, s
 def expert_swiglu(x, x_scales, w13, w13_scales, counts=None, offsets=None, out=None, status=None, stream=None, *, bases=None, expected_rows=0):
     """silu(x wg^T) * (x wu^T) per expert, w13 = [gate; up] [E][2I][K], requantised:
     (codes [rows][I] uint8, scales [rows][I / 128]) (or [E][cap][..])."""
-    index, lead, n, cx, cg, cw = _products("expert_swiglu", x, x_scales, w13, w13_scales, counts, offsets, bases, expected_rows)
+    index, shape, n, cx, cg, cw = _products("expert_swiglu", x, x_scales, w13, w13_scales, counts, offsets, bases, expected_rows)
     if n % 256:
         _refuse(f"expert_swiglu: {n} weight rows are no gate and up of a multiple of 128 each")
     inter = n // 2
     if out is None:
-        out = _empty(x, stream, (*lead, inter), _U8), _empty(x, stream, (*lead, inter // 128), _F32)
+        out = _empty(x, stream, (*shape[:-1], inter), _U8), _empty(x, stream, (*shape[:-1], inter // 128), _F32)
     codes, scales = out
-    step = _output("expert_swiglu: out codes", codes, (*lead, inter), _E4M3 if codes.dtype == _E4M3 else _U8, index)
-    sstep = _output("expert_swiglu: out scales", scales, (*lead, inter // 128), _F32, index)
-    _call("ep_expert_swiglu", index, ctypes.byref(cx), ctypes.byref(cg), ctypes.byref(cw), codes.data_ptr(), step,
-          scales.data_ptr(), sstep, _status_ptr(status, index), _stream_of(stream, index))
+    _call("ep_expert_swiglu", index, cx, cg, cw, codes.data_ptr(),
+          _output("expert_swiglu: out codes", codes, shape, inter, _CODES, index), scales.data_ptr(),
+          _output("expert_swiglu: out scales", scales, shape, inter // 128, (_F32,), index), _status_ptr(status, index),
+          _stream_of(stream, index))
     return codes, scales
 
 
@@ -225,7 +243,7 @@ def moe_tokens(x, topk_idx, topk_weights, w13, w2, w13_scales=None, w2_scales=No
             _refuse(f"{name}: weights without scales are bf16: got {w13.dtype}, {w2.dtype}")
         p13 = p2 = None
     else:
-        if w13_scales is None or w2_scales is None or w13.dtype not in (_U8, _E4M3) or w2.dtype not in (_U8, _E4M3):
+        if w13_scales is None or w2_scales is None or w13.dtype not in _CODES or w2.dtype not in _CODES:
             _refuse(f"{name}: e4m3 codes with scales for both weights, or bf16 without")
         for t, r, c in ((w13_scales, 2 * I, H), (w2_scales, H, I)):
             if t.dtype != _F32 or t.shape != (E, r // 128, c // 128) or not t.is_contiguous() or t.get_device() != index:
@@ -238,7 +256,7 @@ def moe_tokens(x, topk_idx, topk_weights, w13, w2, w13_scales=None, w2_scales=No
         out = _empty(x, stream, (T, H), _BF16)
     if workspace is None:
         workspace = _empty(x, stream, (_workspace_bytes(index, T, K, E, H, I, p13 is not None),), _U8)
-    step = _output(f"{name}: out", out, (T, H), _BF16, index)
+    step = _output("moe_tokens: out", out, x.shape, H, (_BF16,), index)
     w = EpMoeWeights(w13.data_ptr(), p13, w2.data_ptr(), p2, E, H, I)
     _call("ep_moe_tokens", index, x.data_ptr(), _step(name, x), T, topk_idx.data_ptr(), topk_weights.data_ptr(), K,
           ctypes.byref(w), out.data_ptr(), step, workspace.data_ptr(), workspace.numel() * workspace.element_size(),

@@ -276,6 +276,19 @@ def test_refusals():
         ep.expert_gemm(flat[1:1 + 8 * 256].view(8, 256), xs, w, ws, **ok)
 
 
+def test_packed_descriptors_are_laid_out_like_the_structures():
+    """The binding packs the C descriptors as bytes: field for field what the ctypes structures hold."""
+    import ctypes
+    from combine_get_dispatch_histograms_gb300 import _lib, experts
+    for pack, struct_, values in ((experts._ROWS, _lib.EpFp8Rows, (3, 5, 7, 11, 1 << 40)),
+                                  (experts._GROUPS, _lib.EpRowGroups, (3, 5, 0, 13, 1 << 35, 9)),
+                                  (experts._WEIGHT, _lib.EpFp8Weight, (1 << 41, 5, 7, 11, 13))):
+        raw = pack(*values)
+        assert len(raw) == ctypes.sizeof(struct_)
+        back = struct_.from_buffer_copy(raw)
+        assert tuple(getattr(back, f) or 0 for f, _ in struct_._fields_) == values
+
+
 @gpu
 def test_regions_hold_no_more_than_their_rows():
     cnt, off, hoff, x, xs, w, ws = case([40, 40], 128, 256, seed=81)
