@@ -1,5 +1,6 @@
 // ep_moe_tokens.cu -- a whole mixture-of-experts layer for up to 64 tokens, in
-// two kernels, without the dispatch / permute / combine round trip.
+// two kernels (and two small ones above 16 tokens), without the dispatch /
+// permute / combine round trip.
 //
 // Mathematics.  For token t with choices e = topk_idx[t][k], weights v[t][k]:
 //   h[t,e] = silu(Wg[e] x[t]) * (Wu[e] x[t]),   out[t] = sum_k v[t][k] * W2[e] h[t,e].
@@ -17,6 +18,8 @@
 //     2^-13 of its block's largest is off by at most 2^-21 of that), three hold
 //     h to 2^-13 of itself;
 //   bf16 weights: x itself, and h as the sum of two bf16.
+// Up to 16 tokens each block converts what it needs; for more, whose experts'
+// blocks would repeat much of it, the pieces are made once beforehand.
 // A block of 128 channels is one accumulator; it leaves tensor memory, times its
 // weight scale and the tokens' powers of two, for an fp32 sum in registers.
 //
@@ -26,8 +29,8 @@
 //
 // Measured: one token of 8 experts (H 7168, I 2048, fp8) 74 us, 42 of them kernel
 // 1 at 6.5 TB/s while it streams; 17 tokens, 75 experts, bf16 (H 4096, I 1408)
-// 423 us, 6.2 TB/s; 64 tokens, 99 experts 954 us, of which 236 are conversion that
-// the stream does not hide.
+// 423 us, 6.2 TB/s; 64 tokens, 99 experts 740 us (954 when every block converted
+// its tokens itself).
 #include <atomic>
 
 #include "ep_fp8.cuh"
@@ -71,7 +74,9 @@ struct TokArgs {
     int list;               // entries of the expert list, at most
     float* sums;            // [split][T * K][2 I]: Wg x, then Wu x, of each pair
     float* part;            // [blocks][2][T][kTokRows]: sums of a tile that several blocks share
-    uint32_t* done;         // [output tiles]: blocks that have written theirs
+    uint32_t* done;         // [output tiles]: blocks that have written theirs; then the number of pairs
+    uint8_t* formed;        // [T or pairs][blocks_k][pieces][kTokBytes]: pieces made beforehand, of x or of h
+    float* powers;          // [T or pairs][blocks_k]: their powers of two (e4m3 only)
     __nv_bfloat16* out;
     int64_t out_stride;
     uint32_t* status;
@@ -264,12 +269,96 @@ __device__ __forceinline__ void load_words(const float* p, float* v) {
     else *v = *p;
 }
 
+// A lane's channels of a token's block as kPieces pieces, each handed to put(piece, 4 bytes).  Returns the
+// power of two that the block's sums are multiplied by (e4m3 only).
+template <bool kFp8, int kPieces, int kLane, class Put>
+__device__ __forceinline__ float write_pieces(float (&v)[kLane], Put put) {
+    if constexpr (kFp8) {
+        uint32_t top = 0;  // the largest magnitude's bits, above infinity's where one is NaN
+#pragma unroll
+        for (int z = 0; z < 4; ++z) top = max(top, __float_as_uint(v[z]) & 0x7fffffffu);
+        top = __reduce_max_sync(0xffffffffu, top);
+        const int e = max((int)(top >> 23) - 127, -100);  // |v| < 2^(e + 1)
+        const bool odd = top >= 0x7f800000u;
+        const float up = odd ? 1.0f : __uint_as_float((uint32_t)(7 - e + 127) << 23);
+#pragma unroll
+        for (int z = 0; z < 4; ++z) v[z] *= up;
+#pragma unroll
+        for (int z = 0; z < kPieces; ++z) {
+            const uint32_t c = pack_e4m3(v[0], v[1], v[2], v[3]);
+            put(z, odd ? 0x7f7f7f7fu : c);  // an infinity or a NaN makes the token's whole block NaN
+            if (z + 1 < kPieces) next_piece(v, c);
+        }
+        return odd ? 1.0f : __uint_as_float((uint32_t)(e - 7 + 127) << 23);
+    } else {
+#pragma unroll
+        for (int z = 0; z < kPieces; ++z) {
+            const __nv_bfloat162 b = __floats2bfloat162_rn(v[0], v[1]);
+            put(z, *reinterpret_cast<const uint32_t*>(&b));
+            const float2 f = __bfloat1622float2(b);
+            v[0] = isfinite(f.x) ? v[0] - f.x : 0.0f;
+            v[1] = isfinite(f.y) ? v[1] - f.y : 0.0f;
+        }
+        return 1.0f;
+    }
+}
+
+// A lane's channels of x, or of h from both sums.
+template <bool kDown, int kLane>
+__device__ __forceinline__ void values_of(const float* w, float (&v)[kLane]) {
+    if constexpr (kDown) {
+#pragma unroll
+        for (int z = 0; z < kLane; ++z) v[z] = silu_mul(w[z], w[kLane + z]);
+    } else {
+#pragma unroll
+        for (int z = 0; z < kLane; z += 2) {
+            const uint32_t two = __float_as_uint(w[z / 2]);
+            v[z] = __uint_as_float(two << 16);
+            v[z + 1] = __uint_as_float(two & 0xffff0000u);
+        }
+    }
+}
+
+// The pieces of x (before kernel 1) or of h (between both), once for all blocks:
+// a warp per token or pair and block of channels.
+template <bool kDown, bool kFp8>
+__global__ void __launch_bounds__(256) form_kernel(const TokArgs a) {
+    using Shape = TokShape<kDown, kFp8>;
+    constexpr int kPieces = Shape::kPieces, kLane = Shape::kChannels / 32, kRaw = kDown ? 2 * kLane : kLane / 2;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if constexpr (kDown) asm volatile("griddepcontrol.wait;" ::: "memory");  // the sums of kernel 1
+    const int lane = threadIdx.x & 31;
+    const int rows = kDown ? (int)a.done[(a.H + kTokRows - 1) / kTokRows] : a.T;
+    for (int i = (blockIdx.x * 256 + threadIdx.x) >> 5; i < rows * a.blocks_k; i += gridDim.x * 8) {
+        const int row = i / a.blocks_k, ch = (i - row * a.blocks_k) * Shape::kChannels + lane * kLane;
+        float raw[kRaw] = {}, v[kLane];
+        if (ch < (kDown ? a.I : a.H)) {
+            if constexpr (kDown) {
+                for (int z = 0; z < a.split; ++z) {
+                    const float* p = a.sums + ((int64_t)z * a.T * a.K + row) * 2 * a.I + ch;
+                    float more[kRaw];
+                    load_words<kLane>(p, more);
+                    load_words<kLane>(p + a.I, more + kLane);
+#pragma unroll
+                    for (int q = 0; q < kRaw; ++q) raw[q] += more[q];
+                }
+            } else {
+                load_words<kRaw>(reinterpret_cast<const float*>(a.x + row * a.x_stride + ch), raw);
+            }
+        }
+        values_of<kDown>(raw, v);
+        uint8_t* to = a.formed + (int64_t)i * kPieces * kTokBytes + lane * 4;
+        const float power = write_pieces<kFp8, kPieces>(v, [&](int z, uint32_t w) { *reinterpret_cast<uint32_t*>(to + z * kTokBytes) = w; });
+        if (kFp8 && lane == 0) a.powers[i] = power;
+    }
+}
+
 // kDown: kernel 2.  kFp8: e4m3 weights with block scales, otherwise bf16.
 // kParts: the sums come in several parts (few items, so few tokens); without
 // them the next tokens' sums are loaded while these are converted, for which
 // both forms in one kernel leave too few registers (64 tokens: 938 us instead of
-// 904).
-template <bool kDown, bool kFp8, bool kParts>
+// 904).  kFormed: the tokens' pieces were made beforehand and are copied.
+template <bool kDown, bool kFp8, bool kParts, bool kFormed>
 __global__ void __launch_bounds__(kTokThreads, 1) tok_kernel(const __grid_constant__ CUtensorMap map_w, const TokArgs a) {
     using Shape = TokShape<kDown, kFp8>;
     constexpr int kStages = Shape::kStages, kPieces = Shape::kPieces;
@@ -321,6 +410,7 @@ __global__ void __launch_bounds__(kTokThreads, 1) tok_kernel(const __grid_consta
     tc_fence_after();
     const uint32_t tmem = sh.tmem;
     if (brief) A = sh.entries;
+    if (!kDown && blockIdx.x == 0 && tid == 0) a.done[(a.H + kTokRows - 1) / kTokRows] = s.base[A];
 
     const int tiles = kDown ? (a.H + kTokRows - 1) / kTokRows : (a.I + kTokRows / 2 - 1) / (kTokRows / 2);
     const int total = A * tiles * (kDown ? a.blocks_k : a.split);
@@ -397,12 +487,38 @@ __global__ void __launch_bounds__(kTokThreads, 1) tok_kernel(const __grid_consta
         // ---- tokens: warp w converts stages w, w + kFill, ... of the block ----------------
         constexpr uint32_t kFill = Shape::kFill;
         if (warp - 4 >= (int)kFill) run.at = run.end;
-        if constexpr (kDown) asm volatile("griddepcontrol.wait;" ::: "memory");  // the sums of kernel 1
+        if constexpr (kDown || kFormed) asm volatile("griddepcontrol.wait;" ::: "memory");  // the sums of kernel 1, or the pieces
         uint32_t n0 = 0;
         while (run.next()) {
             const int p0 = s.base[run.ai], cnt = s.base[run.ai + 1] - p0, len = run.k1 - run.k0;
             for (int i = (warp - 4 + kFill - n0 % kFill) % kFill; i < len; i += kFill) {
                 const uint32_t n = n0 + i, u = n % kStages;
+                if constexpr (kFormed) {
+                    // four rows (a piece of a token each) at a time, 16 bytes a lane
+                    const int unit = lane & 7, k = run.k0 + i;
+                    auto source = [&](int j) { return (int64_t)(kDown ? p0 + j : s.token[p0 + j]) * a.blocks_k + k; };
+                    int4 w[Shape::kCols / 4];
+                    float power = 0.0f;
+#pragma unroll
+                    for (int q = 0; q < Shape::kCols / 4; ++q) {
+                        const int r = q * 4 + (lane >> 3), j = r / kPieces;
+                        if (j < cnt)
+                            w[q] = __ldcg(reinterpret_cast<const int4*>(a.formed + (source(j) * kPieces + r - j * kPieces) * kTokBytes) + unit);
+                    }
+                    if (kFp8 && lane < cnt) power = __ldcg(a.powers + source(lane));
+                    mbar_wait_warp(done + u * 8, n / kStages & 1 ^ 1, kTokWaitNs, abort);
+                    uint8_t* st = ring + u * Shape::kStage + Shape::kStageA;
+#pragma unroll
+                    for (int q = 0; q < Shape::kCols / 4; ++q) {
+                        const int r = q * 4 + (lane >> 3);
+                        if (r / kPieces < cnt) *reinterpret_cast<int4*>(st + r * kTokBytes + ((unit ^ (r & 7)) << 4)) = w[q];
+                    }
+                    if (kFp8 && lane < cnt) sh.scale[n % kTokScaleRing][lane] = power;
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(filled + u * 8);
+                    continue;
+                }
                 constexpr int kLane = Shape::kChannels / 32;  // channels of a lane
                 const int ch = (run.k0 + i) * Shape::kChannels + lane * kLane;
                 const bool in = ch < (kDown ? a.I : a.H);
@@ -445,57 +561,17 @@ __global__ void __launch_bounds__(kTokThreads, 1) tok_kernel(const __grid_consta
                 auto convert = [&](int j0, float(&raw)[4][kRaw]) {
                     float v[4][kLane];
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        float(&w)[kRaw] = raw[q];
-                        if constexpr (kDown) {
-#pragma unroll
-                            for (int z = 0; z < kLane; ++z) v[q][z] = silu_mul(w[z], w[kLane + z]);
-                        } else {
-#pragma unroll
-                            for (int z = 0; z < kLane; z += 2) {
-                                const uint32_t two = __float_as_uint(w[z / 2]);
-                                v[q][z] = __uint_as_float(two << 16);
-                                v[q][z + 1] = __uint_as_float(two & 0xffff0000u);
-                            }
-                        }
-                    }
+                    for (int q = 0; q < 4; ++q) values_of<kDown>(raw[q], v[q]);
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {  // four independent chains; a token too many is zeros
-                        const int col = (j0 + q) * kPieces;
                         // piece z of the token is row col + z of the tile, 4 bytes a lane, 16-byte units
                         // exchanged by the 128-byte swizzle
-                        auto put = [&](int z, uint32_t w) {
+                        const int col = (j0 + q) * kPieces;
+                        const float power = write_pieces<kFp8, kPieces>(v[q], [&](int z, uint32_t w) {
                             const int r = col + z;
                             *reinterpret_cast<uint32_t*>(st + r * kTokBytes + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4) = w;
-                        };
-                        if constexpr (kFp8) {
-                            uint32_t top = 0;  // the largest magnitude's bits, above infinity's where one is NaN
-#pragma unroll
-                            for (int z = 0; z < 4; ++z) top = max(top, __float_as_uint(v[q][z]) & 0x7fffffffu);
-                            top = __reduce_max_sync(0xffffffffu, top);
-                            const int e = max((int)(top >> 23) - 127, -100);  // |v| < 2^(e + 1)
-                            const bool odd = top >= 0x7f800000u;
-                            const float up = odd ? 1.0f : __uint_as_float((uint32_t)(7 - e + 127) << 23);
-                            const float down = odd ? 1.0f : __uint_as_float((uint32_t)(e - 7 + 127) << 23);
-#pragma unroll
-                            for (int z = 0; z < 4; ++z) v[q][z] *= up;
-#pragma unroll
-                            for (int z = 0; z < kPieces; ++z) {
-                                const uint32_t c = pack_e4m3(v[q][0], v[q][1], v[q][2], v[q][3]);
-                                put(z, odd ? 0x7f7f7f7fu : c);  // an infinity or a NaN makes the token's whole block NaN
-                                if (z + 1 < kPieces) next_piece(v[q], c);
-                            }
-                            if (lane == 0) sh.scale[n % kTokScaleRing][j0 + q] = down;
-                        } else {
-#pragma unroll
-                            for (int z = 0; z < kPieces; ++z) {
-                                const __nv_bfloat162 b = __floats2bfloat162_rn(v[q][0], v[q][1]);
-                                put(z, *reinterpret_cast<const uint32_t*>(&b));
-                                const float2 f = __bfloat1622float2(b);
-                                v[q][0] = isfinite(f.x) ? v[q][0] - f.x : 0.0f;
-                                v[q][1] = isfinite(f.y) ? v[q][1] - f.y : 0.0f;
-                            }
-                        }
+                        });
+                        if (kFp8 && lane == 0) sh.scale[n % kTokScaleRing][j0 + q] = power;
                     }
                 };
                 float raw[kParts ? 1 : 2][4][kRaw];
@@ -643,12 +719,19 @@ __global__ void __launch_bounds__(kTokThreads, 1) tok_kernel(const __grid_consta
     if (tid == 0 && *abort && a.status) flag(a.status, FLAG_TIMEOUT);
 }
 
+// Whether the pieces are made beforehand: two launches and their hand-over, about 4 us, against a conversion
+// by every block that meets the token (us, by each block / beforehand).  fp8, 128 experts, top-8, H 7168,
+// I 2048: 8 tokens 377 / 376, 16 553 / 547, 32 734 / 722, 64 951 / 858, skewed 774 / 563; 16 experts, top-2,
+// H 4096, I 1408: 8 tokens 54 / 56, 16 71 / 74, 24 84 / 81, 64 131 / 110.  bf16 halves only h: 16 experts, 32
+// tokens 128 / 126, 64 171 / 148; 75 experts, top-6, 64 tokens 427 / 435.
+static bool tok_formed(int T, int K, int E, bool fp8) { return T > kTokSlots && (fp8 || T * K >= 6 * E); }
+
 // Entries of the expert list, at most: one for each expert that is chosen, and one more for every kTokSlots pairs.
 static int tok_list(int T, int K, int E) { return (E < T * K ? E : T * K) + T * K / kTokSlots; }
 
 struct TokWorkspace {
     int split;
-    int64_t part, done, bytes;
+    int64_t part, done, formed_x, formed_h, powers, bytes;
 };
 // The parts of K in kernel 1: enough items that the blocks' shares differ little,
 // each with a few stages left.
@@ -663,7 +746,14 @@ static TokWorkspace tok_workspace(int T, int K, int E, int H, int I, bool fp8, i
     w.split = split < 1 ? 1 : (int)split;
     w.part = up((int64_t)w.split * T * K * 2 * I * 4);
     w.done = w.part + up((int64_t)sms * 2 * T * kTokRows * 4);
-    w.bytes = w.done + up((int64_t)((H + kTokRows - 1) / kTokRows) * 4);
+    w.formed_x = w.formed_h = w.powers = w.bytes = w.done + up((int64_t)((H + kTokRows - 1) / kTokRows + 1) * 4);
+    if (tok_formed(T, K, E, fp8)) {
+        const int64_t blocks_x = fp8 ? (int64_t)T * blocks_k : 0;
+        const int64_t blocks_h = (int64_t)T * K * ((I * (fp8 ? 1 : 2) + kTokBytes - 1) / kTokBytes);
+        w.formed_h = w.formed_x + blocks_x * TokShape<false, true>::kPieces * kTokBytes;
+        w.powers = w.formed_h + blocks_h * (fp8 ? TokShape<true, true>::kPieces : TokShape<true, false>::kPieces) * kTokBytes;
+        w.bytes = w.powers + up((blocks_x > blocks_h ? blocks_x : blocks_h) * 4);
+    }
     return w;
 }
 
@@ -682,11 +772,15 @@ static ep_status launch_tokens(TokArgs a, const ep_moe_weights* w, int sms, cons
     static std::atomic<bool> known[kMaxDevicesTracked];  // devices whose launch attributes are set
     if (dev >= kMaxDevicesTracked || !known[dev].load(std::memory_order_relaxed)) {
         constexpr int kMost = kTokMax * kMaxTopk + kTokMax * kMaxTopk / kTokSlots;
-        EP_CUDA(cudaFuncSetAttribute(tok_kernel<false, kFp8, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     (int)tok_smem<false, kFp8>(kTokMax, kMaxTopk, kMost)));
-        const int most = (int)tok_smem<true, kFp8>(kTokMax, kMaxTopk, kMost);
-        EP_CUDA(cudaFuncSetAttribute(tok_kernel<true, kFp8, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, most));
-        EP_CUDA(cudaFuncSetAttribute(tok_kernel<true, kFp8, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, most));
+        auto allow = [](auto* kernel, size_t bytes) {
+            return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+        };
+        const size_t most1 = tok_smem<false, kFp8>(kTokMax, kMaxTopk, kMost), most2 = tok_smem<true, kFp8>(kTokMax, kMaxTopk, kMost);
+        EP_CUDA(allow(tok_kernel<false, kFp8, false, false>, most1));
+        if constexpr (kFp8) EP_CUDA(allow(tok_kernel<false, true, false, true>, most1));
+        EP_CUDA(allow(tok_kernel<true, kFp8, false, false>, most2));
+        EP_CUDA(allow(tok_kernel<true, kFp8, true, false>, most2));
+        EP_CUDA(allow(tok_kernel<true, kFp8, false, true>, most2));
         if (dev < kMaxDevicesTracked) known[dev].store(true, std::memory_order_relaxed);
     }
     constexpr int kByte = kFp8 ? 1 : 2;
@@ -705,22 +799,46 @@ static ep_status launch_tokens(TokArgs a, const ep_moe_weights* w, int sms, cons
     a.blocks_k = k1;
     a.ws = w->w13_scales;
     const int64_t items1 = (int64_t)a.list * tiles1 * a.split, items2 = (int64_t)a.list * tiles2 * k2;
-    tok_kernel<false, kFp8, false><<<(int)(items1 < sms ? items1 : sms), kTokThreads, tok_smem<false, kFp8>(a.T, a.K, a.list), st>>>(m13, a);
-    EP_CHECK_LAUNCH(fn);
+    // Each kernel but the first starts while the one before drains: its list and first weights depend on none.
+    cudaLaunchAttribute early;
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    auto config = [&](int64_t blocks, int threads, size_t smem, bool follows) {
+        cudaLaunchConfig_t c = {};
+        c.gridDim = dim3((unsigned)blocks);
+        c.blockDim = dim3(threads);
+        c.dynamicSmemBytes = smem;
+        c.stream = st;
+        c.attrs = &early;
+        c.numAttrs = follows ? 1 : 0;
+        return c;
+    };
+    auto at_most = [](int64_t n, int64_t most) { return n < most ? n : most; };
+    const bool formed = tok_formed(a.T, a.K, a.E, kFp8);
+    const auto c1 = config(at_most(items1, sms), kTokThreads, tok_smem<false, kFp8>(a.T, a.K, a.list), kFp8 && formed);
+    if (kFp8 && formed) {
+        a.formed = mem + ws.formed_x;
+        a.powers = reinterpret_cast<float*>(mem + ws.powers);
+        const auto c0 = config(at_most(((int64_t)a.T * k1 + 7) / 8, 4 * sms), 256, 0, false);
+        if constexpr (kFp8) {
+            EP_CUDA(cudaLaunchKernelEx(&c0, form_kernel<false, true>, a));
+            EP_CUDA(cudaLaunchKernelEx(&c1, tok_kernel<false, true, false, true>, m13, a));
+        }
+    } else {
+        EP_CUDA(cudaLaunchKernelEx(&c1, tok_kernel<false, kFp8, false, false>, m13, a));
+    }
     a.blocks_k = k2;
     a.ws = w->w2_scales;
-    // kernel 2 starts while kernel 1 drains: its list and first weights do not depend on the sums
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(items2 < sms ? items2 : sms));
-    cfg.blockDim = dim3(kTokThreads);
-    cfg.dynamicSmemBytes = tok_smem<true, kFp8>(a.T, a.K, a.list);
-    cfg.stream = st;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    EP_CUDA(cudaLaunchKernelEx(&cfg, a.split > 1 ? tok_kernel<true, kFp8, true> : tok_kernel<true, kFp8, false>, m2, a));
+    const auto c2 = config(at_most(items2, sms), kTokThreads, tok_smem<true, kFp8>(a.T, a.K, a.list), true);
+    if (formed) {
+        a.formed = mem + ws.formed_h;
+        a.powers = reinterpret_cast<float*>(mem + ws.powers);
+        const auto cf = config(at_most(((int64_t)a.T * a.K * k2 + 7) / 8, 4 * sms), 256, 0, true);
+        EP_CUDA(cudaLaunchKernelEx(&cf, form_kernel<true, kFp8>, a));
+        EP_CUDA(cudaLaunchKernelEx(&c2, tok_kernel<true, kFp8, false, true>, m2, a));
+    } else {
+        EP_CUDA(cudaLaunchKernelEx(&c2, a.split > 1 ? tok_kernel<true, kFp8, true, false> : tok_kernel<true, kFp8, false, false>, m2, a));
+    }
     return EP_OK;
 }
 

@@ -186,6 +186,46 @@ def test_graph_and_side_stream():
 
 
 @gpu
+@pytest.mark.parametrize("kind,T,E,K,H,I", [("fp8", 18, 40, 2, 384, 128), ("fp8", 64, 3, 3, 128, 640), ("fp8", 64, 5, 1, 1152, 128),
+                                            ("bf16", 40, 3, 3, 96, 160), ("bf16", 64, 4, 4, 1056, 32), ("bf16", 17, 1, 1, 32, 1120),
+                                            ("bf16", 36, 6, 1, 64, 96), ("bf16", 35, 6, 1, 64, 96)])
+def test_tokens_converted_beforehand(kind, T, E, K, H, I):
+    """Above 16 tokens: pieces made once for all blocks; a token without an expert, one with a NaN, an infinity."""
+    g = gen(T + E + H)
+    w = weights(E, H, I, kind, g)
+    x = randn((T, H), g).to(torch.bfloat16)
+    idx, v = routing(T, E, K, g, mask=0.15)
+    idx[0] = -1
+    clean = check(x, idx, v, w)
+    x[0] = float("nan")                  # nobody reads it
+    x[2, 7], x[T - 1, H - 1] = float("inf"), float("nan")
+    out = ep.moe_tokens(x, idx, v, w[0], w[2], w[1], w[3])
+    ok = [t for t in range(T) if t not in (2, T - 1) or (idx[t] < 0).all()]
+    assert torch.equal(out[ok].view(torch.int16), clean[ok].view(torch.int16))
+    for t in (2, T - 1):
+        assert t in ok or not torch.isfinite(out[t]).any()
+    idx[:] = -1
+    assert (ep.moe_tokens(x, idx, v, w[0], w[2], w[1], w[3]).view(torch.int16) == 0).all()
+
+
+@gpu
+@pytest.mark.parametrize("kind", ["fp8", "bf16"])
+def test_calls_of_all_lengths_share_a_workspace(kind):
+    """Back to back on one stream, without a wait: each kernel starts while the one before drains."""
+    g = gen(91)
+    w = weights(4, 256, 256, kind, g)
+    ws = torch.empty(max(ep.moe_tokens_workspace(t, 2, 4, 256, 256, kind == "fp8") for t in (1, 16, 17, 64)), dtype=torch.uint8, device="cuda")
+    calls = []
+    for t in (64, 1, 17, 16, 64, 64, 2, 33):
+        x = randn((t, 256), g).to(torch.bfloat16)
+        calls.append((x, *routing(t, 4, 2, g, mask=0.1)))
+    outs = [ep.moe_tokens(x, idx, v, w[0], w[2], w[1], w[3], workspace=ws) for x, idx, v in calls]
+    for (x, idx, v), out in zip(calls, outs):
+        ref, err = reference(x, idx, v, w)
+        assert ((out.double() - ref).abs() <= 2.0 ** -8 * ref.abs() + err + 1e-38).all()
+
+
+@gpu
 def test_refusals():
     g = gen(15)
     w13, s13, w2, s2 = weights(4, 256, 128, "fp8", g)
