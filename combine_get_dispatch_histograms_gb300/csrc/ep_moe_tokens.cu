@@ -415,9 +415,9 @@ __global__ void __launch_bounds__(kTokThreads, 1) tok_kernel(const __grid_consta
     const int tiles = kDown ? (a.H + kTokRows - 1) / kTokRows : (a.I + kTokRows / 2 - 1) / (kTokRows / 2);
     const int total = A * tiles * (kDown ? a.blocks_k : a.split);
     // Blocks with work; the rest are idle.  In kernel 2 the blocks of a tile each stream per / n stages (0.4 us
-    // each) and the last one adds n parts of T tokens (0.1 us for 4 tokens each, about): n as makes both equal.
+    // each) and the last one adds n parts of T tokens (0.05 us for 4 tokens each, about): n as makes both equal.
     int most = gridDim.x;
-    if constexpr (kDown) most = min(most, tiles * max(1, (int)sqrtf(4.0f * A * a.blocks_k / ((a.T + 3) / 4))));
+    if constexpr (kDown) most = min(most, tiles * max(1, (int)sqrtf(8.0f * A * a.blocks_k / ((a.T + 3) / 4))));
     const int blocks = max(1, min(total, most));
     auto first_of = [&](int b) { return (int)((int64_t)total * b / blocks); };
     TokRuns<kDown> run;
@@ -680,28 +680,39 @@ __global__ void __launch_bounds__(kTokThreads, 1) tok_kernel(const __grid_consta
                     }
                     asm volatile("bar.sync 1, 128;" ::: "memory");
                     write = sh.last;
-                    if (write)
-                        for (int t0 = 0; t0 < a.T; t0 += 4) {
-                            float v[4] = {};
-                            for (int q0 = b0; q0 <= b1; q0 += 4) {  // sixteen loads on their way at a time
-                                float x[4][4];
+                    if (write) {
+                        // A warp per token, four rows a lane: four parts of two tokens on their way at a time.  The
+                        // later blocks began in this tile; the first one may have left another's part before.
+                        constexpr int kAt = 4;
+                        const int second = first_of(b0) < lo;
+                        auto from = [&](int b, int t) {
+                            return __ldcg(reinterpret_cast<const float4*>(a.part + ((int64_t)(b * 2 + (b == b0 ? second : 0)) * a.T + t) * kTokRows) + lane);
+                        };
+                        for (int t = warp - 12; t < a.T; t += 8) {
+                            const bool two = t + 4 < a.T;
+                            float4 v[2] = {};
+                            for (int q0 = b0; q0 <= b1; q0 += kAt) {
+                                float4 x[kAt][2];
 #pragma unroll
-                                for (int q = 0; q < 4; ++q) {
-                                    const int b = min(q0 + q, b1);
-                                    const float* p = a.part + ((int64_t)b * 2 + (run.tile != first_of(b) / per)) * a.T * kTokRows + r;
+                                for (int q = 0; q < kAt; ++q)
+                                    if (q0 + q <= b1) {
+                                        x[q][0] = from(q0 + q, t);
+                                        if (two) x[q][1] = from(q0 + q, t + 4);
+                                    }
 #pragma unroll
-                                    for (int z = 0; z < 4; ++z) x[q][z] = __ldcg(p + min(t0 + z, a.T - 1) * kTokRows);
-                                }
-#pragma unroll
-                                for (int q = 0; q < 4; ++q)
+                                for (int q = 0; q < kAt; ++q)
                                     if (q0 + q <= b1)
 #pragma unroll
-                                        for (int z = 0; z < 4; ++z) v[z] += x[q][z];
+                                        for (int z = 0; z < 2; ++z) {
+                                            v[z].x += x[q][z].x, v[z].y += x[q][z].y;
+                                            v[z].z += x[q][z].z, v[z].w += x[q][z].w;
+                                        }
                             }
-#pragma unroll
-                            for (int z = 0; z < 4; ++z)
-                                if (t0 + z < a.T) s.acc[(t0 + z) * kTokRows + r] = v[z];
+                            *reinterpret_cast<float4*>(s.acc + t * kTokRows + lane * 4) = v[0];
+                            if (two) *reinterpret_cast<float4*>(s.acc + (t + 4) * kTokRows + lane * 4) = v[1];
                         }
+                        asm volatile("bar.sync 1, 128;" ::: "memory");
+                    }
                 }
                 for (int t = 0; t < a.T; ++t) {
                     if (write && ch < a.H) a.out[t * a.out_stride + ch] = __float2bfloat16_rn(s.acc[t * kTokRows + r]);
@@ -723,7 +734,8 @@ __global__ void __launch_bounds__(kTokThreads, 1) tok_kernel(const __grid_consta
 // by every block that meets the token (us, by each block / beforehand).  fp8, 128 experts, top-8, H 7168,
 // I 2048: 8 tokens 377 / 376, 16 553 / 547, 32 734 / 722, 64 951 / 858, skewed 774 / 563; 16 experts, top-2,
 // H 4096, I 1408: 8 tokens 54 / 56, 16 71 / 74, 24 84 / 81, 64 131 / 110.  bf16 halves only h: 16 experts, 32
-// tokens 128 / 126, 64 171 / 148; 75 experts, top-6, 64 tokens 427 / 435.
+// tokens 128 / 126, 64 171 / 148; 75 experts, top-6, 64 tokens 427 / 435.  (All with the tiles' parts still
+// added 16 loads at a time by 128 threads, up to 40 us more than now, on both sides.)
 static bool tok_formed(int T, int K, int E, bool fp8) { return T > kTokSlots && (fp8 || T * K >= 6 * E); }
 
 // Entries of the expert list, at most: one for each expert that is chosen, and one more for every kTokSlots pairs.
