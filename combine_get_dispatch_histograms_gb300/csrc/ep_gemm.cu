@@ -239,6 +239,9 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
     __syncthreads();
     if (kCtas == 2) cluster_sync();  // both blocks' barriers are ready
     tc_fence_after();
+    // All above may run beside the end of the kernel before; the kernel after may do the same.
+    grid_wait();
+    grid_launch_next();
     const uint32_t tmem = sh.tmem;
 
     if (warp < 4) {
@@ -695,12 +698,14 @@ static ep_status launch_shape(const char* fn, const CUtensorMap& map_x, const CU
     cfg.blockDim = dim3(kGemmThreads);
     cfg.dynamicSmemBytes = Shape::kSmem;
     cfg.stream = as_stream(stream);
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = cluster;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = cluster;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
     EP_CUDA(cudaLaunchKernelEx(&cfg, gemm_kernel<kSwiglu, kCtas, kSplit>, map_x, map_w, map_out, a));
     return EP_OK;
 }

@@ -325,8 +325,8 @@ template <bool kDown, bool kFp8>
 __global__ void __launch_bounds__(256) form_kernel(const TokArgs a) {
     using Shape = TokShape<kDown, kFp8>;
     constexpr int kPieces = Shape::kPieces, kLane = Shape::kChannels / 32, kRaw = kDown ? 2 * kLane : kLane / 2;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if constexpr (kDown) asm volatile("griddepcontrol.wait;" ::: "memory");  // the sums of kernel 1
+    grid_wait();  // kernel 1, or what ran before the call
+    grid_launch_next();
     const int lane = threadIdx.x & 31;
     const int rows = kDown ? (int)a.done[(a.H + kTokRows - 1) / kTokRows] : a.T;
     for (int i = (blockIdx.x * 256 + threadIdx.x) >> 5; i < rows * a.blocks_k; i += gridDim.x * 8) {
@@ -376,11 +376,6 @@ __global__ void __launch_bounds__(kTokThreads, 1) tok_kernel(const __grid_consta
     const uint32_t copied = smem_u32(sh.copied), filled = smem_u32(sh.filled), done = smem_u32(sh.done);
     const uint32_t acc_empty = smem_u32(sh.acc_empty);
 
-    if constexpr (!kDown) {
-        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-        if (blockIdx.x == 0)
-            for (int i = tid; i < (a.H + kTokRows - 1) / kTokRows; i += kTokThreads) a.done[i] = 0;
-    }
     if (tid == 0) {
         for (int i = 0; i < kStages; ++i) {
             mbar_init(&sh.copied[i], 1);
@@ -395,6 +390,12 @@ __global__ void __launch_bounds__(kTokThreads, 1) tok_kernel(const __grid_consta
         tma_prefetch_desc(&map_w);
     }
     if (warp == 2) tmem_alloc<1>(&sh.tmem, 128);
+    // What is above may run beside the end of the kernel before.  The first kernel of a call waits for what
+    // ran before the call; the later ones start after that, and wait below, where they read their own.
+    if constexpr (!kDown && !kFormed) grid_wait();
+    grid_launch_next();
+    if (!kDown && blockIdx.x == 0)
+        for (int i = tid; i < (a.H + kTokRows - 1) / kTokRows; i += kTokThreads) a.done[i] = 0;
     int A = 0;
     const bool brief = a.T <= kTokSlots && a.T * a.K <= 32;
     if (brief) {
@@ -487,7 +488,7 @@ __global__ void __launch_bounds__(kTokThreads, 1) tok_kernel(const __grid_consta
         // ---- tokens: warp w converts stages w, w + kFill, ... of the block ----------------
         constexpr uint32_t kFill = Shape::kFill;
         if (warp - 4 >= (int)kFill) run.at = run.end;
-        if constexpr (kDown || kFormed) asm volatile("griddepcontrol.wait;" ::: "memory");  // the sums of kernel 1, or the pieces
+        if constexpr (kDown || kFormed) grid_wait();  // the sums of kernel 1, or the pieces
         uint32_t n0 = 0;
         while (run.next()) {
             const int p0 = s.base[run.ai], cnt = s.base[run.ai + 1] - p0, len = run.k1 - run.k0;
@@ -601,7 +602,7 @@ __global__ void __launch_bounds__(kTokThreads, 1) tok_kernel(const __grid_consta
         // ---- sums: thread r owns weight row r of the tile ---------------------------------
         const int r = (warp - 12) * 32 + lane;
         const uint32_t lane_base = tmem + ((uint32_t)(warp - 12) << 21);
-        if constexpr (kDown) asm volatile("griddepcontrol.wait;" ::: "memory");  // the counters of kernel 1
+        if constexpr (kDown) grid_wait();  // the counters of kernel 1
         if (kDown && A == 0)
             for (int64_t i = blockIdx.x * 128ll + r; i < (int64_t)a.T * a.H; i += gridDim.x * 128ll)
                 a.out[i / a.H * a.out_stride + i % a.H] = __float2bfloat16_rn(0.0f);
@@ -811,27 +812,27 @@ static ep_status launch_tokens(TokArgs a, const ep_moe_weights* w, int sms, cons
     a.blocks_k = k1;
     a.ws = w->w13_scales;
     const int64_t items1 = (int64_t)a.list * tiles1 * a.split, items2 = (int64_t)a.list * tiles2 * k2;
-    // Each kernel but the first starts while the one before drains: its list and first weights depend on none.
+    // Each kernel starts while the one before drains: its list and first weights depend on none of the call's.
     cudaLaunchAttribute early;
     early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     early.val.programmaticStreamSerializationAllowed = 1;
-    auto config = [&](int64_t blocks, int threads, size_t smem, bool follows) {
+    auto config = [&](int64_t blocks, int threads, size_t smem) {
         cudaLaunchConfig_t c = {};
         c.gridDim = dim3((unsigned)blocks);
         c.blockDim = dim3(threads);
         c.dynamicSmemBytes = smem;
         c.stream = st;
         c.attrs = &early;
-        c.numAttrs = follows ? 1 : 0;
+        c.numAttrs = 1;
         return c;
     };
     auto at_most = [](int64_t n, int64_t most) { return n < most ? n : most; };
     const bool formed = tok_formed(a.T, a.K, a.E, kFp8);
-    const auto c1 = config(at_most(items1, sms), kTokThreads, tok_smem<false, kFp8>(a.T, a.K, a.list), kFp8 && formed);
+    const auto c1 = config(at_most(items1, sms), kTokThreads, tok_smem<false, kFp8>(a.T, a.K, a.list));
     if (kFp8 && formed) {
         a.formed = mem + ws.formed_x;
         a.powers = reinterpret_cast<float*>(mem + ws.powers);
-        const auto c0 = config(at_most(((int64_t)a.T * k1 + 7) / 8, 4 * sms), 256, 0, false);
+        const auto c0 = config(at_most(((int64_t)a.T * k1 + 7) / 8, 4 * sms), 256, 0);
         if constexpr (kFp8) {
             EP_CUDA(cudaLaunchKernelEx(&c0, form_kernel<false, true>, a));
             EP_CUDA(cudaLaunchKernelEx(&c1, tok_kernel<false, true, false, true>, m13, a));
@@ -841,11 +842,11 @@ static ep_status launch_tokens(TokArgs a, const ep_moe_weights* w, int sms, cons
     }
     a.blocks_k = k2;
     a.ws = w->w2_scales;
-    const auto c2 = config(at_most(items2, sms), kTokThreads, tok_smem<true, kFp8>(a.T, a.K, a.list), true);
+    const auto c2 = config(at_most(items2, sms), kTokThreads, tok_smem<true, kFp8>(a.T, a.K, a.list));
     if (formed) {
         a.formed = mem + ws.formed_h;
         a.powers = reinterpret_cast<float*>(mem + ws.powers);
-        const auto cf = config(at_most(((int64_t)a.T * a.K * k2 + 7) / 8, 4 * sms), 256, 0, true);
+        const auto cf = config(at_most(((int64_t)a.T * a.K * k2 + 7) / 8, 4 * sms), 256, 0);
         EP_CUDA(cudaLaunchKernelEx(&cf, form_kernel<true, kFp8>, a));
         EP_CUDA(cudaLaunchKernelEx(&c2, tok_kernel<true, kFp8, false, true>, m2, a));
     } else {

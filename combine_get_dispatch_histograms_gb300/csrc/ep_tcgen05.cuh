@@ -73,6 +73,13 @@ __device__ __forceinline__ void mbar_wait_warp(uint32_t bar, uint32_t parity, in
     }
 }
 
+// Programmatic launches.  grid_wait: until the kernel before has ended and its writes are visible.  It ends
+// after its own wait, so that everything before it has ended too.  grid_launch_next: once every block has said
+// so, the next kernel may start, if it was launched for that; whoever calls it after grid_wait promises the
+// next kernel that all before this one is complete.
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_launch_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // True in one lane of a converged warp.
 __device__ __forceinline__ bool elect_one() {
     uint32_t p;
