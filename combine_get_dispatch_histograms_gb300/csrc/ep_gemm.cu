@@ -22,6 +22,7 @@
 // 2I 2816).  With short groups the weights' bytes: 64 rows a group run at
 // 6.6 TB/s (second product 0.61 ms, first 1.14 ms of 256 groups).
 #include <atomic>
+#include <initializer_list>
 
 #include "ep_fp8.cuh"
 #include "ep_tcgen05.cuh"
@@ -59,8 +60,6 @@ constexpr int kChunkRows = 2048;       // rows that share a pass over the weight
 constexpr int kPairRows = 144;         // rows of a group from which pairs of blocks are faster (40 groups, K 2048,
                                        // N 7168, us by one block / by pairs: 64 rows 111 / 135, 128 147 / 158,
                                        // 160 240 / 160, 256 211 / 164, 320 260 / 291, 512 393 / 290)
-constexpr int kSplitMost = 4;          // blocks of a cluster that share a tile's K (one row, K 7168, N 4096:
-                                       // 27.6 us alone, 18.8 by 2, 14.1 by 4, 21.0 by 8)
 constexpr int kSplitStride = kBN + 4;  // floats of a row of sums: rows fall into other banks
 constexpr int64_t kGemmWaitNs = 2000000000ll;
 
@@ -272,7 +271,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
 #pragma unroll 1
                 for (int kb = k0; kb < k1; kb += kScaleChunk) {
                     mbar_wait_warp<true>(sr.bar(scale_empty), sr.phase() ^ 1, kGemmWaitNs, abort);
-                    const float w = lane < 16 && kb + (lane & 7) < k1 ? __ldg(ws + kb) : 0.0f;
+                    const float w = lane < 16 && kb + (lane & 7) < k1 ? ws[kb] : 0.0f;
                     float* dst = &sh.scale[sr.slot()][0][0][0];
 #pragma unroll 1
                     for (int i = 0; i < kScaleChunk && kb + i < k1; i += 4) {
@@ -285,12 +284,12 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
                             const float* p = xs + r * a.x_sstride + kb + i;
                             float4 v;
                             if (a.x_vec && (!kSplit || (k0 & 3) == 0) && kb + i + 4 <= k1) {
-                                v = __ldg(reinterpret_cast<const float4*>(p));
+                                v = *reinterpret_cast<const float4*>(p);
                             } else {
-                                v.x = __ldg(p);
-                                v.y = kb + i + 1 < k1 ? __ldg(p + 1) : 0.0f;
-                                v.z = kb + i + 2 < k1 ? __ldg(p + 2) : 0.0f;
-                                v.w = kb + i + 3 < k1 ? __ldg(p + 3) : 0.0f;
+                                v.x = *p;
+                                v.y = kb + i + 1 < k1 ? p[1] : 0.0f;
+                                v.z = kb + i + 2 < k1 ? p[2] : 0.0f;
+                                v.w = kb + i + 3 < k1 ? p[3] : 0.0f;
                             }
                             float* d = dst + i * 2 * kBM + r;
                             d[0] = v.x * w00;
@@ -572,34 +571,38 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
             for (int r = part + parts * (warp - 4); r < tile.rows && !*abort; r += parts * kSumWarps) {
                 const uint32_t at = smem_u32(tiles) + r * kSplitStride * 4;
                 float v[8] = {};
-                if (kSwiglu || a.out_vec) {
-                    // gate and up of 4 channels, or 8 neighbours
-                    const int ca = kSwiglu ? lane * 4 : lane * 8, cb = kSwiglu ? 128 + lane * 4 : lane * 8 + 4;
-                    float4 x[kSplitMost], y[kSplitMost];
+                // four blocks' at a time
+#pragma unroll 1
+                for (int b0 = 0; b0 < parts; b0 += 4) {
+                    if (kSwiglu || a.out_vec) {
+                        // gate and up of 4 channels, or 8 neighbours
+                        const int ca = kSwiglu ? lane * 4 : lane * 8, cb = kSwiglu ? 128 + lane * 4 : lane * 8 + 4;
+                        float4 x[4], y[4];
 #pragma unroll
-                    for (int b = 0; b < kSplitMost; ++b)
-                        if (b < parts) {
-                            x[b] = ld_cluster_f32x4(smem_of(at + ca * 4, b));
-                            y[b] = ld_cluster_f32x4(smem_of(at + cb * 4, b));
-                        }
+                        for (int b = 0; b < 4; ++b)
+                            if (b0 + b < parts) {
+                                x[b] = ld_cluster_f32x4(smem_of(at + ca * 4, b0 + b));
+                                y[b] = ld_cluster_f32x4(smem_of(at + cb * 4, b0 + b));
+                            }
 #pragma unroll
-                    for (int b = 0; b < kSplitMost; ++b)
-                        if (b < parts) {
-                            v[0] += x[b].x, v[1] += x[b].y, v[2] += x[b].z, v[3] += x[b].w;
-                            v[4] += y[b].x, v[5] += y[b].y, v[6] += y[b].z, v[7] += y[b].w;
-                        }
-                } else {  // column lane + 32 i: unaligned rows are stored 2 bytes a lane, neighbours by neighbours
-                    float x[kSplitMost][8];
+                        for (int b = 0; b < 4; ++b)
+                            if (b0 + b < parts) {
+                                v[0] += x[b].x, v[1] += x[b].y, v[2] += x[b].z, v[3] += x[b].w;
+                                v[4] += y[b].x, v[5] += y[b].y, v[6] += y[b].z, v[7] += y[b].w;
+                            }
+                    } else {  // column lane + 32 i: unaligned rows are stored 2 bytes a lane, neighbours by neighbours
+                        float x[4][8];
 #pragma unroll
-                    for (int b = 0; b < kSplitMost; ++b)
-                        if (b < parts)
+                        for (int b = 0; b < 4; ++b)
+                            if (b0 + b < parts)
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) x[b][i] = ld_cluster_f32(smem_of(at + (lane + 32 * i) * 4, b));
+                                for (int i = 0; i < 8; ++i) x[b][i] = ld_cluster_f32(smem_of(at + (lane + 32 * i) * 4, b0 + b));
 #pragma unroll
-                    for (int b = 0; b < kSplitMost; ++b)
-                        if (b < parts)
+                        for (int b = 0; b < 4; ++b)
+                            if (b0 + b < parts)
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) v[i] += x[b][i];
+                                for (int i = 0; i < 8; ++i) v[i] += x[b][i];
+                    }
                 }
                 const int64_t row = tile.row0 + r;
                 if constexpr (kSwiglu) {
@@ -710,6 +713,18 @@ static ep_status launch_shape(const char* fn, const CUtensorMap& map_x, const CU
     return EP_OK;
 }
 
+// Blocks that share a tile's K where the tiles are few: by 4 or 2 if that needs no more than the SMs and leaves
+// each two blocks of K.  Clusters of other sizes leave some SMs of a group of SMs without one, and a second wave
+// doubles the time, so that they may take only a part of the SMs; beyond 4 a block keeps more blocks of K.
+// One row, us by 4 or 2 / by this: K 7168, N 256 10.2 / 7.8 (8), 2048 10.4 / 8.8 (8), 4096 10.7 / 10.4 (6; by 8
+// 16.8), 5120 11.8 / 11.1 (5), 10240 18.6 / 14.5 (3); K 16384, N 256 16.7 / 11.1 (8), 4096 17.4 / 14.9 (6).
+static int split_of(int64_t tiles, int kb, int sms) {
+    struct Rule { int split, blocks, percent; };  // blocks of K for each, share of the SMs
+    for (const Rule r : {Rule{8, 4, 66}, {6, 8, 66}, {5, 8, 66}, {4, 2, 100}, {3, 2, 80}, {2, 2, 100}})
+        if (kb >= r.split * r.blocks && tiles * r.split * 100 <= (int64_t)sms * r.percent) return r.split;
+    return 1;
+}
+
 template <bool kSwiglu>
 static ep_status launch_gemm(const char* fn, const ep_fp8_rows* x, const ep_row_groups* g, const ep_fp8_weight* w,
                              GemmArgs a, void* stream) {
@@ -756,9 +771,7 @@ static ep_status launch_gemm(const char* fn, const ep_fp8_rows* x, const ep_row_
     int dev = 0, sms = 0;
     EP_CUDA(cudaGetDevice(&dev));
     EP_CUDA(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
-    // Few tiles: as many blocks to a tile's K as leave each two blocks of K and every cluster one tile.
-    int split = 1;
-    while (split < kSplitMost && most_tiles(a, kBM) * split * 2 <= sms && a.KB >= split * 4) split *= 2;
+    const int split = split_of(most_tiles(a, kBM), a.KB, sms);
     if (split > 1) return launch_shape<kSwiglu, 1, true>(fn, map_x, map_w, map_out, a, sms, split, stream);
     // Rows of a group: as the caller expects, or what the arrays hold, shared out.  The regions of the
     // packed layout are sized for the worst case, a low-latency step fills a few percent of them.

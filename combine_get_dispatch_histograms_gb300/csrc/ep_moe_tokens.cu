@@ -618,11 +618,11 @@ __global__ void __launch_bounds__(kTokThreads, 1) tok_kernel(const __grid_consta
             float acc[kTokSlots];
 #pragma unroll
             for (int j = 0; j < kTokSlots; ++j) acc[j] = 0.0f;
-            float sw = kFp8 ? __ldg(ws + run.k0) : 1.0f;
+            float sw = kFp8 ? ws[run.k0] : 1.0f;
 #pragma unroll 1
             for (int k = run.k0; k < run.k1; ++k, ++n) {
                 const float f = sw;
-                if (kFp8 && k + 1 < run.k1) sw = __ldg(ws + k + 1);
+                if (kFp8 && k + 1 < run.k1) sw = ws[k + 1];
                 mbar_wait_warp(done + n % kStages * 8, n / kStages & 1, kTokWaitNs, abort);
                 tc_fence_after();
                 const float* sc = sh.scale[n % kTokScaleRing];

@@ -94,6 +94,19 @@ def test_swiglu_dense(rows, K, I):
 
 
 @gpu
+@pytest.mark.parametrize("K,N", [(4096, 136), (2560, 3000), (16384, 200), (5376, 7000), (6144, 4096), (6272, 9999), (768, 9728)])
+def test_one_row_by_clusters_of_all_sizes(K, N):
+    g = gen(K + N)
+    q, s = quantize_rows(randn((3, K), g))
+    w, ws = quantize_weight(randn((1, N, K), g) * K ** -0.5)
+    for rows in (1, 3):
+        assert_bf16_close(ep.expert_gemm(q[:rows], s[:rows], w[0], ws[0]), *product64(rows64(q[:rows], s[:rows]), weight64(w[0], ws[0])))
+    if N % 256 == 0:
+        codes, scales = ep.expert_swiglu(q, s, w[0], ws[0])
+        assert_fp8_close(codes, scales, *swiglu64(rows64(q, s), weight64(w[0], ws[0])))
+
+
+@gpu
 @pytest.mark.parametrize("counts", [[0, 0, 3], [0, 0, 0], [130, 1, 0]])
 def test_few_tiles_with_empty_groups(counts):
     cnt, off, hoff, x, xs, w, ws = case(counts, 1024, 136, seed=sum(counts), gap=1)
