@@ -14,10 +14,15 @@
 // products, one announces tiles and stages scales, 16 add; each has what it
 // needs in shared memory and none waits for global memory in the loop over K.
 //
-// Bound.  With long groups the sums: a block of K costs the tensor cores 517
-// cycles (128 x 256 x 128 of each SM) and the 16 warps about 750, of which the
-// 32,768 multiply-adds alone are 292; their loads, waits and the hand-back of
-// the accumulator make up the rest.  Measured: 2.25 PFLOP/s (262144 rows,
+// Bound.  With long groups the round trip of the two accumulators.  A block of K
+// costs the tensor cores 517 cycles (128 x 256 x 128 of each SM), but takes 860:
+// a warp adds for about 600 of them (365 while no products run; 292 are the
+// 32,768 multiply-adds), hands its accumulator back half way through, and waits
+// 220 for the next one, which could not start before.  A third accumulator has
+// no room, nor have the registers for loading all of one before adding it; halves
+// handed back on their own (two issuing warps) read the rows' tile twice from
+// shared memory and are slower (1163 -> 1305 us, K 8192).  Sustained, power: 1360
+// of 1400 W, and the clock falls to 1.7 - 1.76 GHz.  Measured: 2.25 PFLOP/s (262144 rows,
 // K 2048, N 7168, 256 groups: 3.42 ms), 2.43 PFLOP/s (first product, K 4096,
 // 2I 2816).  With short groups the weights' bytes: 64 rows a group run at
 // 6.6 TB/s (second product 0.61 ms, first 1.14 ms of 256 groups).
