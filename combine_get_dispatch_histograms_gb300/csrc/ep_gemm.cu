@@ -236,7 +236,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
         fence_mbar_init();
         tma_prefetch_desc(&map_x);
         tma_prefetch_desc(&map_w);
-        if (!kSwiglu && kCtas == 2 && a.out_vec) tma_prefetch_desc(&map_out);
+        if (kCtas == 2 && (kSwiglu || a.out_vec)) tma_prefetch_desc(&map_out);
     }
     if (warp == 2) tmem_alloc<kCtas>(&sh.tmem, 512);
     tc_fence_before();
@@ -483,13 +483,27 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
 #pragma unroll
                 for (int i = 0; i < kSumGroups; ++i) m = fmaxf(m, sh.amax[mx][i][r]);
                 const float scale = __fdiv_rn(m, 448.0f);
-                if (r < mine) {
-                    const int64_t row = row0 + r;
+                const int64_t row = row0 + r;
+                if (quarter == 0 && r < mine) a.out_scales[row * a.out_sstride + tn] = scale;
+                if (kCtas == 2 && mine - (warp & 3) * 32 >= 32) {
+                    // a full set of rows goes out as one copy (32 lanes' rows cost the stores a cycle each)
+                    uint8_t* stage = out_stage + (warp - 4) * Shape::kOut;
+                    bulk_wait_read<0>();  // lane 0's copy of the last tile has read the buffer
+                    __syncwarp();
+#pragma unroll
+                    for (int q = 0; q < 2; ++q)
+                        *reinterpret_cast<int4*>(stage + lane * 32 + q * 16) = quantize16_by(&acc[q * 16], scale);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        tma_store_2d(&map_out, stage, tn * 128 + quarter * 32, row0 + (warp & 3) * 32);
+                        bulk_commit();
+                    }
+                } else if (r < mine) {
                     uint8_t* o = reinterpret_cast<uint8_t*>(a.out) + row * a.out_stride + tn * 128 + quarter * 32;
 #pragma unroll
                     for (int q = 0; q < 2; ++q)
                         *reinterpret_cast<int4*>(o + q * 16) = quantize16_by(&acc[q * 16], scale);
-                    if (quarter == 0) a.out_scales[row * a.out_sstride + tn] = scale;
                 }
             } else if (rows_here) {
                 const int n0 = tn * kBN + quarter * 64;
@@ -764,15 +778,7 @@ static ep_status launch_gemm(const char* fn, const ep_fp8_rows* x, const ep_row_
         const ep_status st = encode_rows(&map_w, w->codes, 3, dims, strides, box, fn);
         if (st != EP_OK) return st;
     }
-    if (!kSwiglu && a.out_vec) {
-        const cuuint64_t dims[2] = {(cuuint64_t)w->n * 2, (cuuint64_t)x->rows};
-        const cuuint64_t strides[1] = {(cuuint64_t)a.out_stride * 2};
-        const cuuint32_t box[2] = {128, 32};
-        const ep_status st = encode_rows(&map_out, a.out, 2, dims, strides, box, fn);
-        if (st != EP_OK) return st;
-    } else {
-        map_out = map_x;  // not used
-    }
+    map_out = map_x;  // used by pairs of blocks only
     int dev = 0, sms = 0;
     EP_CUDA(cudaGetDevice(&dev));
     EP_CUDA(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
@@ -782,7 +788,18 @@ static ep_status launch_gemm(const char* fn, const ep_fp8_rows* x, const ep_row_
     // packed layout are sized for the worst case, a low-latency step fills a few percent of them.
     const int64_t per_group =
         g->expected > 0 ? g->expected : x->rows / w->groups / (w->groups > 1 && !g->offsets ? 16 : 1);
-    if (per_group >= kPairRows) return launch_shape<kSwiglu, 2, false>(fn, map_x, map_w, map_out, a, sms, 2, stream);
+    if (per_group >= kPairRows) {
+        if (kSwiglu || a.out_vec) {
+            constexpr int kBytes = kSwiglu ? 1 : 2;
+            const cuuint64_t dims[2] = {(cuuint64_t)(kSwiglu ? w->n / 2 : w->n) * kBytes, (cuuint64_t)x->rows};
+            const cuuint64_t strides[1] = {(cuuint64_t)a.out_stride * kBytes};
+            const cuuint32_t box[2] = {kSwiglu ? 32 : 128, 32};
+            const ep_status st = encode_rows(&map_out, a.out, 2, dims, strides, box, fn,
+                                             kSwiglu ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B);
+            if (st != EP_OK) return st;
+        }
+        return launch_shape<kSwiglu, 2, false>(fn, map_x, map_w, map_out, a, sms, 2, stream);
+    }
     return launch_shape<kSwiglu, 1, false>(fn, map_x, map_w, map_out, a, sms, 1, stream);
 }
 

@@ -339,12 +339,13 @@ inline EncodeTiled encode_tiled() {
 
 // A map of bytes [..][rows][row bytes] in boxes of 128 bytes x rows, 128-byte swizzle.
 inline ep_status encode_rows(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
-                             const cuuint32_t* box, const char* what) {
+                             const cuuint32_t* box, const char* what,
+                             CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
     const EncodeTiled fn = encode_tiled();
     if (!fn) return set_error(EP_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
     const cuuint32_t ones[3] = {1, 1, 1};
     const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, rank, const_cast<void*>(base), dims, strides, box, ones,
-                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return set_error(EP_ERR_INVALID_ARG, "%s: the tensor map was refused (%d)", what, (int)r);
     return EP_OK;
