@@ -84,8 +84,8 @@ SIGNATURES = {
     # the three descriptors by address: a structure's, or bytes packed like it
     "ep_expert_gemm": (INT, [P, P, P, P, I64, P, P]),
     "ep_expert_swiglu": (INT, [P, P, P, P, I64, P, I64, P, P]),
-    "ep_moe_tokens_workspace": (I64, [I32, I32, ctypes.POINTER(EpMoeWeights)]),
-    "ep_moe_tokens": (INT, [P, I64, I32, P, P, I32, ctypes.POINTER(EpMoeWeights), P, I64, P, I64, P, P]),
+    "ep_moe_tokens_workspace": (I64, [I32, I32, P]),
+    "ep_moe_tokens": (INT, [P, I64, I32, P, P, I32, P, P, I64, P, I64, P, P]),
     "ep_ll_message_bytes": (I64, [INT]),
     "ep_ll_size_hint": (I64, [INT, INT, INT, INT]),
     "ep_ll_buffer_create": (INT, [ctypes.POINTER(EpConfig), INT, ctypes.POINTER(P)]),

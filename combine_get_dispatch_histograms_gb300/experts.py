@@ -20,14 +20,13 @@ take the groups from the dispatch handle and the packed dict.
 """
 from __future__ import annotations
 
-import ctypes
 import functools
 import struct
 
 import torch
 
 from . import _lib
-from ._lib import EpError, EpMoeWeights, check
+from ._lib import EpError, check
 
 _U8, _E4M3, _F32, _I32, _BF16 = torch.uint8, torch.float8_e4m3fn, torch.float32, torch.int32, torch.bfloat16
 _CODES = (_U8, _E4M3)
@@ -90,8 +89,9 @@ def _step(name: str, t: torch.Tensor) -> int:
     return st[0] if shape[0] > 1 else max(st[0], n)
 
 
-# ep_fp8_rows, ep_row_groups and ep_fp8_weight as the C side lays them out
+# ep_fp8_rows, ep_row_groups, ep_fp8_weight and ep_moe_weights as the C side lays them out
 _ROWS, _GROUPS, _WEIGHT = struct.Struct("@PqPqq").pack, struct.Struct("@PPPiqq").pack, struct.Struct("@PPiii0P").pack
+_MOE = struct.Struct("@PPPPiii0P").pack
 
 
 def _products(name, x, x_scales, w, w_scales, counts, offsets, bases, expected):
@@ -221,53 +221,51 @@ def moe_tokens(x, topk_idx, topk_weights, w13, w2, w13_scales=None, w2_scales=No
 
     x [T][H] bf16; w13 = [gate; up] [E][2I][H] and w2 [E][H][I], bf16, or e4m3 codes with their block scales.
     `workspace` (uint8, moe_tokens_workspace bytes) is allocated when it is not given."""
-    name = "moe_tokens"
     index = x.get_device()
+    xs, ts, ws, vs = x.shape, topk_idx.shape, w13.shape, w2.shape
     if index < 0:
-        _refuse(f"{name}: all tensors must be on a CUDA device")
-    if x.dtype != _BF16 or x.dim() != 2:
-        _refuse(f"{name}: x bf16 [T][H]: got {x.dtype} {tuple(x.shape)}")
-    T, H = x.shape
-    if topk_idx.dtype != torch.int64 or topk_idx.dim() != 2 or topk_idx.shape[0] != T or not topk_idx.is_contiguous():
-        _refuse(f"{name}: topk_idx int64 [{T}][K], contiguous: got {topk_idx.dtype} {tuple(topk_idx.shape)}")
-    if topk_weights.dtype != _F32 or topk_weights.shape != topk_idx.shape or not topk_weights.is_contiguous():
-        _refuse(f"{name}: topk_weights fp32 {tuple(topk_idx.shape)}, contiguous: got {topk_weights.dtype} {tuple(topk_weights.shape)}")
-    K = topk_idx.shape[1]
-    if w13.dim() != 3 or w2.dim() != 3 or not w13.is_contiguous() or not w2.is_contiguous():
-        _refuse(f"{name}: weights [E][rows][cols], contiguous")
-    E, I = w13.shape[0], w2.shape[2]
-    if w13.shape != (E, 2 * I, H) or w2.shape != (E, H, I):
-        _refuse(f"{name}: w13 {tuple(w13.shape)}, w2 {tuple(w2.shape)} for {H} channels")
+        _refuse("moe_tokens: all tensors must be on a CUDA device")
+    if x.dtype != _BF16 or len(xs) != 2:
+        _refuse(f"moe_tokens: x bf16 [T][H]: got {x.dtype} {tuple(xs)}")
+    T, H = xs
+    if topk_idx.dtype != torch.int64 or len(ts) != 2 or ts[0] != T or not topk_idx.is_contiguous():
+        _refuse(f"moe_tokens: topk_idx int64 [{T}][K], contiguous: got {topk_idx.dtype} {tuple(ts)}")
+    if topk_weights.dtype != _F32 or topk_weights.shape != ts or not topk_weights.is_contiguous():
+        _refuse(f"moe_tokens: topk_weights fp32 {tuple(ts)}, contiguous: got {topk_weights.dtype} {tuple(topk_weights.shape)}")
+    K = ts[1]
+    if len(ws) != 3 or len(vs) != 3 or not w13.is_contiguous() or not w2.is_contiguous():
+        _refuse("moe_tokens: weights [E][rows][cols], contiguous")
+    E, I = ws[0], vs[2]
+    if ws[1] != 2 * I or ws[2] != H or vs[0] != E or vs[1] != H:
+        _refuse(f"moe_tokens: w13 {tuple(ws)}, w2 {tuple(vs)} for {H} channels")
+    p13 = p2 = 0
     if w13_scales is None and w2_scales is None:
         if w13.dtype != _BF16 or w2.dtype != _BF16:
-            _refuse(f"{name}: weights without scales are bf16: got {w13.dtype}, {w2.dtype}")
-        p13 = p2 = None
+            _refuse(f"moe_tokens: weights without scales are bf16: got {w13.dtype}, {w2.dtype}")
     else:
         if w13_scales is None or w2_scales is None or w13.dtype not in _CODES or w2.dtype not in _CODES:
-            _refuse(f"{name}: e4m3 codes with scales for both weights, or bf16 without")
+            _refuse("moe_tokens: e4m3 codes with scales for both weights, or bf16 without")
         for t, r, c in ((w13_scales, 2 * I, H), (w2_scales, H, I)):
             if t.dtype != _F32 or t.shape != (E, r // 128, c // 128) or not t.is_contiguous() or t.get_device() != index:
-                _refuse(f"{name}: weight scales fp32 {(E, r // 128, c // 128)}, contiguous, on the same device")
+                _refuse(f"moe_tokens: weight scales fp32 {(E, r // 128, c // 128)}, contiguous, on the same device")
         p13, p2 = w13_scales.data_ptr(), w2_scales.data_ptr()
     if (topk_idx.get_device() != index or topk_weights.get_device() != index or w13.get_device() != index
             or w2.get_device() != index or (workspace is not None and workspace.get_device() != index)):
-        _refuse(f"{name}: all tensors must be on the same CUDA device")
+        _refuse("moe_tokens: all tensors must be on the same CUDA device")
     if out is None:
         out = _empty(x, stream, (T, H), _BF16)
     if workspace is None:
-        workspace = _empty(x, stream, (_workspace_bytes(index, T, K, E, H, I, p13 is not None),), _U8)
-    step = _output("moe_tokens: out", out, x.shape, H, (_BF16,), index)
-    w = EpMoeWeights(w13.data_ptr(), p13, w2.data_ptr(), p2, E, H, I)
-    _call("ep_moe_tokens", index, x.data_ptr(), _step(name, x), T, topk_idx.data_ptr(), topk_weights.data_ptr(), K,
-          ctypes.byref(w), out.data_ptr(), step, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+        workspace = _empty(x, stream, (_workspace_bytes(index, T, K, E, H, I, p13 != 0),), _U8)
+    _call("ep_moe_tokens", index, x.data_ptr(), _step("moe_tokens", x), T, topk_idx.data_ptr(), topk_weights.data_ptr(), K,
+          _MOE(w13.data_ptr(), p13, w2.data_ptr(), p2, E, H, I), out.data_ptr(),
+          _output("moe_tokens: out", out, xs, H, (_BF16,), index), workspace.data_ptr(), workspace.nbytes,
           _status_ptr(status, index), _stream_of(stream, index))
     return out
 
 
 def moe_tokens_workspace(num_tokens: int, num_topk: int, experts: int, hidden: int, inter: int, fp8: bool = True) -> int:
     """Bytes of workspace moe_tokens needs on the current device (0 for sizes it refuses)."""
-    w = EpMoeWeights(None, 1 if fp8 else None, None, 1 if fp8 else None, experts, hidden, inter)
-    return int(_lib.load().ep_moe_tokens_workspace(num_tokens, num_topk, ctypes.byref(w)))
+    return int(_lib.load().ep_moe_tokens_workspace(num_tokens, num_topk, _MOE(0, int(fp8), 0, int(fp8), experts, hidden, inter)))
 
 
 @functools.lru_cache(maxsize=256)

@@ -295,7 +295,8 @@ def test_packed_descriptors_are_laid_out_like_the_structures():
     from combine_get_dispatch_histograms_gb300 import _lib, experts
     for pack, struct_, values in ((experts._ROWS, _lib.EpFp8Rows, (3, 5, 7, 11, 1 << 40)),
                                   (experts._GROUPS, _lib.EpRowGroups, (3, 5, 0, 13, 1 << 35, 9)),
-                                  (experts._WEIGHT, _lib.EpFp8Weight, (1 << 41, 5, 7, 11, 13))):
+                                  (experts._WEIGHT, _lib.EpFp8Weight, (1 << 41, 5, 7, 11, 13)),
+                                  (experts._MOE, _lib.EpMoeWeights, (1 << 41, 5, 0, 1 << 42, 11, 13, 17))):
         raw = pack(*values)
         assert len(raw) == ctypes.sizeof(struct_)
         back = struct_.from_buffer_copy(raw)
