@@ -85,7 +85,7 @@ struct TokArgs {
 struct TokBarriers {
     uint64_t copied[10], filled[10], done[10], acc_empty[2], drain;
     uint32_t tmem;
-    int abort, last, entries;
+    int abort, last[2], entries;
     float scale[kTokScaleRing][kTokSlots];
 };
 
@@ -665,69 +665,87 @@ __global__ void __launch_bounds__(kTokThreads, 1) tok_kernel(const __grid_consta
             if constexpr (kDown) {
                 const int per = A * a.blocks_k;  // units of a tile
                 if (run.at < run.end && run.at / per == run.tile) continue;
-                // the end of this block's part of a tile: write the tile, or leave the part where the
-                // block that finishes the tile last adds the parts in block order
-                const int lo = run.tile * per, hi = lo + per;
-                bool write = true;
-                if (begin > lo || run.end < hi) {
-                    float* mine = a.part + ((int64_t)blockIdx.x * 2 + (run.tile != begin / per)) * a.T * kTokRows + r;
-                    for (int t = 0; t < a.T; ++t) mine[t * kTokRows] = s.acc[t * kTokRows + r];
-                    __threadfence();
-                    asm volatile("bar.sync 1, 128;" ::: "memory");
-                    const int b0 = (int)(((int64_t)(lo + 1) * blocks - 1) / total), b1 = (int)(((int64_t)hi * blocks - 1) / total);
-                    if (r == 0) {
-                        sh.last = atomicAdd(&a.done[run.tile], 1u) == (uint32_t)(b1 - b0);
-                        __threadfence();
-                    }
-                    asm volatile("bar.sync 1, 128;" ::: "memory");
-                    write = sh.last;
-                    if (write) {
-                        // A warp per token, four rows a lane: four parts of two tokens on their way at a time.  The
-                        // later blocks began in this tile; the first one may have left another's part before.
-                        constexpr int kAt = 4;
-                        const int second = first_of(b0) < lo;
-                        auto from = [&](int b, int t) {
-                            return __ldcg(reinterpret_cast<const float4*>(a.part + ((int64_t)(b * 2 + (b == b0 ? second : 0)) * a.T + t) * kTokRows) + lane);
-                        };
-                        for (int t = warp - 12; t < a.T; t += 8) {
-                            const bool two = t + 4 < a.T;
-                            float4 v[2] = {};
-                            for (int q0 = b0; q0 <= b1; q0 += kAt) {
-                                float4 x[kAt][2];
-#pragma unroll
-                                for (int q = 0; q < kAt; ++q)
-                                    if (q0 + q <= b1) {
-                                        x[q][0] = from(q0 + q, t);
-                                        if (two) x[q][1] = from(q0 + q, t + 4);
-                                    }
-#pragma unroll
-                                for (int q = 0; q < kAt; ++q)
-                                    if (q0 + q <= b1)
-#pragma unroll
-                                        for (int z = 0; z < 2; ++z) {
-                                            v[z].x += x[q][z].x, v[z].y += x[q][z].y;
-                                            v[z].z += x[q][z].z, v[z].w += x[q][z].w;
-                                        }
-                            }
-                            *reinterpret_cast<float4*>(s.acc + t * kTokRows + lane * 4) = v[0];
-                            if (two) *reinterpret_cast<float4*>(s.acc + (t + 4) * kTokRows + lane * 4) = v[1];
-                        }
-                        asm volatile("bar.sync 1, 128;" ::: "memory");
-                    }
-                }
+                // The end of this block's part of a tile: its outputs, or, where other blocks share it, its part.
+                // Only the block's first and last tile can be shared; both are joined at the block's end, so
+                // that the sums between do not wait.
+                const int lo = run.tile * per;
+                const bool shared = begin > lo || run.end < lo + per;
+                float* mine = a.part + ((int64_t)blockIdx.x * 2 + (run.tile != begin / per)) * a.T * kTokRows + r;
                 for (int t = 0; t < a.T; ++t) {
-                    if (write && ch < a.H) a.out[t * a.out_stride + ch] = __float2bfloat16_rn(s.acc[t * kTokRows + r]);
+                    const float v = s.acc[t * kTokRows + r];
+                    if (shared) mine[t * kTokRows] = v;
+                    else if (ch < a.H) a.out[t * a.out_stride + ch] = __float2bfloat16_rn(v);
                     s.acc[t * kTokRows + r] = 0.0f;
                 }
-                asm volatile("bar.sync 1, 128;" ::: "memory");  // sh.last may be written again
             }
         }
+        if constexpr (kDown) __threadfence();
     }
     __syncwarp();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     if (warp == 2) tmem_free<1>(tmem, 128);
+    if constexpr (kDown) {
+        // the block that leaves a tile's last part adds the parts in block order
+        if (!idle && A > 0) {
+            const int per = A * a.blocks_k, first = begin / per, last = (run.end - 1) / per;
+            auto block_of = [&](int unit) { return (int)(((int64_t)(unit + 1) * blocks - 1) / total); };
+            if (lane == 0 && warp < 2) {  // a warp for each of the two tiles
+                const int tile = warp == 0 ? first : last, lo = tile * per;
+                bool is_last = false;
+                if ((warp == 0 || last > first) && (begin > lo || run.end < lo + per)) {
+                    is_last = atomicAdd(&a.done[tile], 1u) == (uint32_t)(block_of(lo + per - 1) - block_of(lo));
+                    __threadfence();
+                }
+                sh.last[warp] = is_last;
+            }
+            __syncthreads();
+            for (int z = 0; z < 2; ++z) {
+                if (!sh.last[z]) continue;
+                // A warp per token, four rows a lane: four parts of two tokens on their way at a time.  The
+                // later blocks began in this tile; the first one may have left another's part before.
+                constexpr int kAt = 4, kWarps = kTokThreads / 32;
+                const int tile = z ? last : first, lo = tile * per;
+                const int b0 = block_of(lo), b1 = block_of(lo + per - 1), second = first_of(b0) < lo;
+                auto from = [&](int b, int t) {
+                    return __ldcg(reinterpret_cast<const float4*>(a.part + ((int64_t)(b * 2 + (b == b0 ? second : 0)) * a.T + t) * kTokRows) + lane);
+                };
+                for (int t = warp; t < a.T; t += 2 * kWarps) {
+                    const bool two = t + kWarps < a.T;
+                    float4 v[2] = {};
+                    for (int q0 = b0; q0 <= b1; q0 += kAt) {
+                        float4 x[kAt][2];
+#pragma unroll
+                        for (int q = 0; q < kAt; ++q)
+                            if (q0 + q <= b1) {
+                                x[q][0] = from(q0 + q, t);
+                                if (two) x[q][1] = from(q0 + q, t + kWarps);
+                            }
+#pragma unroll
+                        for (int q = 0; q < kAt; ++q)
+                            if (q0 + q <= b1)
+#pragma unroll
+                                for (int i = 0; i < 2; ++i) {
+                                    v[i].x += x[q][i].x, v[i].y += x[q][i].y;
+                                    v[i].z += x[q][i].z, v[i].w += x[q][i].w;
+                                }
+                    }
+                    const int ch = tile * kTokRows + lane * 4;  // H is a multiple of 32
+                    if (ch < a.H)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            if (i == 0 || two) {
+                                __nv_bfloat16* o = a.out + (t + i * kWarps) * a.out_stride + ch;
+                                o[0] = __float2bfloat16_rn(v[i].x);
+                                o[1] = __float2bfloat16_rn(v[i].y);
+                                o[2] = __float2bfloat16_rn(v[i].z);
+                                o[3] = __float2bfloat16_rn(v[i].w);
+                            }
+                }
+            }
+        }
+    }
     if (tid == 0 && *abort && a.status) flag(a.status, FLAG_TIMEOUT);
 }
 
