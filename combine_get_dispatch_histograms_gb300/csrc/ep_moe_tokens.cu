@@ -27,10 +27,11 @@
 // (128 output channels, expert, block of K) in kernel 2; each thread block takes
 // its share, equal to within one.
 //
-// Measured: one token of 8 experts (H 7168, I 2048, fp8) 74 us, 42 of them kernel
-// 1 at 6.5 TB/s while it streams; 17 tokens, 75 experts, bf16 (H 4096, I 1408)
-// 423 us, 6.2 TB/s; 64 tokens, 99 experts 740 us (954 when every block converted
-// its tokens itself).
+// Measured: one token of 8 experts (H 7168, I 2048, fp8) 69 us: kernel 1 streams
+// for 37 of them at 6.3 TB/s, the hand-over between the kernels leaves the memory
+// idle for 2.5, the ends of the blocks' shares and their joining take 5.  17
+// tokens, 75 experts, bf16 (H 4096, I 1408) 422 us, 6.2 TB/s; 64 tokens, 99 experts
+// 720 us (954 when every block converted its tokens itself).
 #include <atomic>
 
 #include "ep_fp8.cuh"
