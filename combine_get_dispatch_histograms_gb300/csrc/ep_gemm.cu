@@ -82,6 +82,7 @@ struct GemmArgs {
     float* out_scales;
     int64_t out_sstride;
     bool out_vec;       // 16-byte stores
+    bool out_wide;      // 32-byte stores
     bool x_vec;         // 16-byte loads of row scales
     uint32_t* status;
 };
@@ -512,24 +513,33 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
                 __nv_bfloat16* o =
                     reinterpret_cast<__nv_bfloat16*>(a.out) + (int64_t)(row0 + (warp & 3) * 32) * a.out_stride + n0;
                 if constexpr (kCtas == 1) {
-                    // 8 columns at a time: each lane its row's 16 bytes, or, where rows are not so aligned,
-                    // through shared memory, so that 8 lanes store neighbours
+                    // 16 columns at a time: each lane its row's 32 bytes, a whole sector (128 rows a group: 222 us, by 16
+                    // bytes 236), or twice 16 bytes, or, where rows are not so aligned, 8 columns through shared
+                    // memory, so that 8 lanes store neighbours
 #pragma unroll
-                    for (int q = 0; q < 8; ++q) {
-                        __nv_bfloat162 p[4];
+                    for (int q = 0; q < 4; ++q) {
+                        __nv_bfloat162 p[8];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) p[i] = __floats2bfloat162_rn(acc[q * 8 + 2 * i], acc[q * 8 + 2 * i + 1]);
-                        const int n = n0 + q * 8;
-                        if (a.out_vec && n + 8 <= a.N) {
-                            if (lane < rows) *reinterpret_cast<int4*>(o + lane * a.out_stride + q * 8) = *reinterpret_cast<const int4*>(p);
-                        } else if (n < a.N) {
-                            *reinterpret_cast<int4*>(stage + lane * 16) = *reinterpret_cast<const int4*>(p);
-                            __syncwarp();
-                            const int c = lane & 7;
-                            if (n + c < a.N)
-                                for (int i = lane >> 3; i < rows; i += 4)
-                                    o[i * a.out_stride + q * 8 + c] = *reinterpret_cast<const __nv_bfloat16*>(stage + i * 16 + c * 2);
-                            __syncwarp();
+                        for (int i = 0; i < 8; ++i) p[i] = __floats2bfloat162_rn(acc[q * 16 + 2 * i], acc[q * 16 + 2 * i + 1]);
+                        if (a.out_wide && n0 + 64 <= a.N) {
+                            if (lane < rows) st_global_32(o + lane * a.out_stride + q * 16, reinterpret_cast<const uint32_t*>(p));
+                            continue;
+                        }
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const int at = q * 16 + h * 8, n = n0 + at;
+                            const int4 v = *reinterpret_cast<const int4*>(p + h * 4);
+                            if (a.out_vec && n + 8 <= a.N) {
+                                if (lane < rows) *reinterpret_cast<int4*>(o + lane * a.out_stride + at) = v;
+                            } else if (n < a.N) {
+                                *reinterpret_cast<int4*>(stage + lane * 16) = v;
+                                __syncwarp();
+                                const int c = lane & 7;
+                                if (n + c < a.N)
+                                    for (int i = lane >> 3; i < rows; i += 4)
+                                        o[i * a.out_stride + at + c] = *reinterpret_cast<const __nv_bfloat16*>(stage + i * 16 + c * 2);
+                                __syncwarp();
+                            }
                         }
                     }
                 } else {
@@ -819,6 +829,7 @@ extern "C" ep_status ep_expert_gemm(const ep_fp8_rows* x, const ep_row_groups* g
     a.out = out;
     a.out_stride = out_stride;
     a.out_vec = aligned16(out) && out_stride % 8 == 0;
+    a.out_wide = (reinterpret_cast<uintptr_t>(out) & 31) == 0 && out_stride % 16 == 0;
     a.status = status_out;
     return launch_gemm<false>(fn, x, groups, w, a, stream);
 }

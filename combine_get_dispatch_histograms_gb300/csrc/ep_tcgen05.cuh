@@ -73,6 +73,13 @@ __device__ __forceinline__ void mbar_wait_warp(uint32_t bar, uint32_t parity, in
     }
 }
 
+// 32 bytes to a 32-byte aligned address.
+__device__ __forceinline__ void st_global_32(void* p, const uint32_t* v) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),
+                 "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+
 // Programmatic launches.  grid_wait: until the kernel before has ended and its writes are visible.  It ends
 // after its own wait, so that everything before it has ended too.  grid_launch_next: once every block has said
 // so, the next kernel may start, if it was launched for that; whoever calls it after grid_wait promises the

@@ -107,6 +107,22 @@ def test_one_row_by_clusters_of_all_sizes(K, N):
 
 
 @gpu
+@pytest.mark.parametrize("shift,stride", [(0, 576), (16, 576), (8, 576), (0, 568), (8, 568), (4, 568), (0, 571), (3, 571)])
+def test_short_groups_at_every_alignment_of_the_output(shift, stride):
+    """Stores of 32, 16 and 2 bytes; the elements between the rows keep their values."""
+    counts = [60, 33, 0, 1] * 16        # more tiles than share their K
+    cnt, off, hoff, x, xs, w, ws = case(counts, 256, 552, seed=shift + stride)
+    buf = torch.full((x.shape[0] * stride + 64,), 9.0, dtype=torch.bfloat16, device="cuda")
+    out = torch.as_strided(buf, (x.shape[0], 552), (stride, 1), shift)
+    ep.expert_gemm(x, xs, w, ws, counts=cnt, offsets=off, out=out, expected_rows=1)
+    for e, (o, c) in enumerate(zip(hoff, counts)):
+        if c:
+            assert_bf16_close(out[o:o + c], *product64(rows64(x[o:o + c], xs[o:o + c]), weight64(w[e], ws[e])), f"group {e}")
+    buf[shift:shift + x.shape[0] * stride].view(-1, stride)[:, :552] = 9.0
+    assert (buf == 9.0).all()
+
+
+@gpu
 @pytest.mark.parametrize("counts", [[0, 0, 3], [0, 0, 0], [130, 1, 0]])
 def test_few_tiles_with_empty_groups(counts):
     cnt, off, hoff, x, xs, w, ws = case(counts, 1024, 136, seed=sum(counts), gap=1)
