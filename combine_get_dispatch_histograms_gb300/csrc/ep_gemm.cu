@@ -62,9 +62,6 @@ constexpr int kScaleChunk = 8;          // blocks of K whose scales are staged t
 constexpr int kScaleRing = 2;
 constexpr int kMaxGroups = 4096;
 constexpr int kChunkRows = 2048;       // rows that share a pass over the weight's tiles
-constexpr int kPairRows = 144;         // rows of a group from which pairs of blocks are faster (40 groups, K 2048,
-                                       // N 7168, us by one block / by pairs: 64 rows 111 / 135, 128 147 / 158,
-                                       // 160 240 / 160, 256 211 / 164, 320 260 / 291, 512 393 / 290)
 constexpr int kSplitStride = kBN + 4;  // floats of a row of sums: rows fall into other banks
 constexpr int64_t kGemmWaitNs = 2000000000ll;
 
@@ -754,6 +751,12 @@ static int split_of(int64_t tiles, int kb, int sms) {
     return 1;
 }
 
+// Whether pairs of blocks make the tiles: where they need fewer tiles, by more than the 1.6 times (first product
+// 1.75) that one of theirs costs.  40 groups, us by one block / by pairs, K 2048, N 7168: 64 rows a group 107 /
+// 129, 128 133 / 148, 160 211 / 149, 256 180 / 156, 320 222 / 260, 384 250 / 256, 512 324 / 264, 1024 610 / 494;
+// first product, K 7168, 2I 4096: 64 205 / 256, 160 380 / 293, 320 393 / 519, 512 538 / 495.
+static bool by_pairs(int64_t rows) { return rows > kBM && (rows <= 2 * kBM || rows > 3 * kBM); }
+
 template <bool kSwiglu>
 static ep_status launch_gemm(const char* fn, const ep_fp8_rows* x, const ep_row_groups* g, const ep_fp8_weight* w,
                              GemmArgs a, void* stream) {
@@ -798,7 +801,7 @@ static ep_status launch_gemm(const char* fn, const ep_fp8_rows* x, const ep_row_
     // packed layout are sized for the worst case, a low-latency step fills a few percent of them.
     const int64_t per_group =
         g->expected > 0 ? g->expected : x->rows / w->groups / (w->groups > 1 && !g->offsets ? 16 : 1);
-    if (per_group >= kPairRows) {
+    if (by_pairs(per_group)) {
         if (kSwiglu || a.out_vec) {
             constexpr int kBytes = kSwiglu ? 1 : 2;
             const cuuint64_t dims[2] = {(cuuint64_t)(kSwiglu ? w->n / 2 : w->n) * kBytes, (cuuint64_t)x->rows};

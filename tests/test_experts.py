@@ -107,6 +107,27 @@ def test_one_row_by_clusters_of_all_sizes(K, N):
 
 
 @gpu
+@pytest.mark.parametrize("expected", [64, 200, 300, 500])
+@pytest.mark.parametrize("K,N", [(128, 256), (640, 512), (1408, 768), (2048, 1280)])
+def test_both_shapes_on_long_and_ragged_groups(K, N, expected):
+    """One block a tile or two, whatever the groups hold."""
+    for counts in (LONG, RAGGED):
+        cnt, off, hoff, x, xs, w, ws = case(counts, K, N, seed=K + N + expected, gap=2)
+        out = torch.full((x.shape[0], N), 7.0, dtype=torch.bfloat16, device="cuda")
+        ep.expert_gemm(x, xs, w, ws, counts=cnt, offsets=off, out=out, expected_rows=expected)
+        hc, hs = (torch.full((x.shape[0], n), 7, dtype=t, device="cuda") for n, t in ((N // 2, torch.uint8), (N // 256, torch.float32)))
+        ep.expert_swiglu(x, xs, w, ws, counts=cnt, offsets=off, out=(hc, hs), expected_rows=expected)
+        own = torch.zeros(x.shape[0], dtype=torch.bool, device="cuda")
+        for e, (o, c) in enumerate(zip(hoff, counts)):
+            own[o:o + c] = True
+            if c:
+                X, W = rows64(x[o:o + c], xs[o:o + c]), weight64(w[e], ws[e])
+                assert_bf16_close(out[o:o + c], *product64(X, W), f"group {e}")
+                assert_fp8_close(hc[o:o + c], hs[o:o + c], *swiglu64(X, W))
+        assert (out[~own] == 7.0).all() and (hc[~own] == 7).all() and (hs[~own] == 7).all()
+
+
+@gpu
 @pytest.mark.parametrize("shift,stride", [(0, 576), (16, 576), (8, 576), (0, 568), (8, 568), (4, 568), (0, 571), (3, 571)])
 def test_short_groups_at_every_alignment_of_the_output(shift, stride):
     """Stores of 32, 16 and 2 bytes; the elements between the rows keep their values."""
