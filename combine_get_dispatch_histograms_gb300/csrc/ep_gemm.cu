@@ -80,6 +80,7 @@ struct GemmArgs {
     int64_t out_sstride;
     bool out_vec;       // 16-byte stores
     bool out_wide;      // 32-byte stores
+    bool out_clip;      // rows end at a multiple of 16 bytes, so that a tiled copy that crosses their end is cut there
     bool x_vec;         // 16-byte loads of row scales
     uint32_t* status;
 };
@@ -542,7 +543,8 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
                 } else {
                     // The warp's 32 rows x 64 columns through shared memory in the 128-byte swizzle.  A full
                     // set of rows goes out as one copy, which the next tile's products hide; the rows of
-                    // a group's last tile, and unaligned rows, are stored by the lanes.
+                    // a group's last tile, and unaligned rows, are stored by the lanes.  So are the last columns
+                    // where N is no multiple of 8: a copy writes whole 16 bytes, also past the row's end.
                     bulk_wait_read<0>();  // lane 0's copy of the last tile has read the buffer
                     __syncwarp();
 #pragma unroll
@@ -552,7 +554,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
                         for (int i = 0; i < 4; ++i) p[i] = __floats2bfloat162_rn(acc[q * 8 + 2 * i], acc[q * 8 + 2 * i + 1]);
                         *reinterpret_cast<int4*>(stage + lane * 128 + ((q ^ (lane & 7)) << 4)) = *reinterpret_cast<const int4*>(p);
                     }
-                    if (a.out_vec && rows == 32) {
+                    if (a.out_vec && rows == 32 && (a.out_clip || n0 + 64 <= a.N)) {
                         fence_proxy_async_smem();
                         __syncwarp();
                         if (lane == 0) {
@@ -833,6 +835,7 @@ extern "C" ep_status ep_expert_gemm(const ep_fp8_rows* x, const ep_row_groups* g
     a.out_stride = out_stride;
     a.out_vec = aligned16(out) && out_stride % 8 == 0;
     a.out_wide = (reinterpret_cast<uintptr_t>(out) & 31) == 0 && out_stride % 16 == 0;
+    a.out_clip = w->n % 8 == 0;
     a.status = status_out;
     return launch_gemm<false>(fn, x, groups, w, a, stream);
 }
