@@ -470,7 +470,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
 #pragma unroll
                 for (int i = 0; i < 32; ++i) {
                     acc[i] = silu_mul(acc[i], acc[32 + i]);
-                    m = fmaxf(m, fabsf(acc[i]));
+                    m = max_or_nan(m, fabsf(acc[i]));
                 }
                 // the block's maximum over all warpgroups' channels; two buffers: a
                 // warp writes one again only after every warp has passed the other
@@ -480,7 +480,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
                 if (lane == 0) mbar_arrive(smem_u32(&sh.amax_full[mx]));
                 mbar_wait_warp<true>(smem_u32(&sh.amax_full[mx]), tr.n >> 1 & 1, kGemmWaitNs, abort);
 #pragma unroll
-                for (int i = 0; i < kSumGroups; ++i) m = fmaxf(m, sh.amax[mx][i][r]);
+                for (int i = 0; i < kSumGroups; ++i) m = max_or_nan(m, sh.amax[mx][i][r]);
                 const float scale = __fdiv_rn(m, 448.0f);
                 const int64_t row = row0 + r;
                 if (quarter == 0 && r < mine) a.out_scales[row * a.out_sstride + tn] = scale;
@@ -638,10 +638,10 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         h[i] = silu_mul(v[i], v[4 + i]);
-                        m = fmaxf(m, fabsf(h[i]));
+                        m = max_or_nan(m, fabsf(h[i]));
                     }
 #pragma unroll
-                    for (int o = 1; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                    for (int o = 1; o < 32; o <<= 1) m = max_or_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
                     const float scale = __fdiv_rn(m, 448.0f);
                     uint8_t* o = reinterpret_cast<uint8_t*>(a.out) + row * a.out_stride + tile.n * 128 + lane * 4;
                     *reinterpret_cast<int*>(o) = quantize16_by(h, scale).x;

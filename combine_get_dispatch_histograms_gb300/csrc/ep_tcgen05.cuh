@@ -315,6 +315,13 @@ __device__ __forceinline__ float silu_mul(float g, float u) {
     return g * r * u;
 }
 
+// The larger of both, or NaN if either is one: a block's maximum, and with it its scale and codes, keeps a NaN.
+__device__ __forceinline__ float max_or_nan(float a, float b) {
+    float m;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+    return m;
+}
+
 // d[i] += v[i] * f, two at a time: half the instructions, and fewer register-bank
 // conflicts (1.2 cycles a value and warp against 1.5, measured).
 template <int kN>

@@ -432,7 +432,8 @@ ep_status ep_expert_gemm(const ep_fp8_rows* x, const ep_row_groups* groups, cons
 /* The first product with the activation and the requantisation: with
  * w13 [groups][2I][k] (gate rows, then up rows; I = w13->n / 2 a multiple of
  * 128), h = silu(gate) * up in fp32, then per 128 channels scale = amax / 448
- * and code = e4m3 RNE-satfinite of h / scale (the rule of ep_quantize_fp8).
+ * and code = e4m3 RNE-satfinite of h / scale (the rule of ep_quantize_fp8; a
+ * NaN among the 128 makes the scale and all their codes NaN).
  * out: codes, out_stride bytes apart (a multiple of 16), and out_scales,
  * out_scale_stride floats apart: FP8 rows of I channels, which ep_expert_gemm
  * reads with the same groups. */

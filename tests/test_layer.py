@@ -91,3 +91,20 @@ def test_forward_in_a_graph_on_new_routing():
     ctx.check()
     _, ref = layer_and_reference(E, H, I, x, idx, v, 7)
     assert far(out, ref) < 0.12
+
+
+@gpu
+@pytest.mark.parametrize("R,E,K,T,H,I", [(4, 8, 2, 40, 256, 128), (2, 6, 2, 20, 256, 128)])
+def test_a_tokens_nan_stays_a_nan(R, E, K, T, H, I):
+    """Over dispatch, over the low-latency buffer and (40 tokens) as a few-token layer: no finite output for it."""
+    x, v = inputs.random_x(R, T, H, 1).cuda(), inputs.random_weights(R, T, K, 2).cuda()
+    idx = inputs.random_topk(R, E, K, T, 3).cuda()
+    layer, _ = layer_and_reference(E, H, I, x, idx, v, 8)
+    x[1, 3, 17] = x[0, 5, H - 1] = float("nan")
+    ctx, buf = Context(R, E, K, T, H), LLBuffer(R, E, K, T, H, T)
+    for out in (layer.forward(ctx, x, idx, v), layer.forward_ll(buf, x, idx, v)):
+        bad = torch.zeros(R, T, dtype=torch.bool, device="cuda")
+        bad[1, 3] = bad[0, 5] = True
+        assert torch.isnan(out[bad]).all() and torch.isfinite(out[~bad]).all()
+    ctx.check()
+    buf.check()
