@@ -1,7 +1,7 @@
 // ep_fp8.cuh -- the e4m3 codec shared by the low-latency send and the FP8
 // normal-mode rows: per 128 channels, scale = amax / 448 (IEEE fp32 division),
 // code = cvt.rn.satfinite.e4m3 of x / scale (the IEEE fp32 quotient); a zero
-// scale keeps only the sign of x.
+// scale keeps only the sign of x, and that it is NaN.
 #pragma once
 #include <cuda_fp8.h>
 
@@ -54,7 +54,10 @@ __device__ __forceinline__ int4 quantize16_by(const float* v, float scale) {
         for (int u = 0; u < 4; ++u) {
             uint32_t c = 0;
 #pragma unroll
-            for (int b = 0; b < 4; ++b) c |= ((__float_as_uint(v[4 * u + b]) >> 31) ? 0x80u : 0u) << (8 * b);
+            for (int b = 0; b < 4; ++b) {
+                const uint32_t x = __float_as_uint(v[4 * u + b]);
+                c |= ((x >> 31 ? 0x80u : 0u) | ((x & 0x7fffffffu) > 0x7f800000u ? 0x7fu : 0u)) << (8 * b);
+            }
             w4[u] = c;
         }
     } else if (scale >= kRcpScaleMin && scale <= kRcpScaleMax) {

@@ -511,7 +511,7 @@ ep_status ep_ll_set_wait_trace(ep_ll_buffer* buf, int64_t* wait_ns);
 /* Sends the microbatch of tokens [t0, t0+n) of every source rank (n <= cap):
  * flips to the other ping-pong buffer, quantises each token once to e4m3 with
  * per-128-channel fp32 scales (scale = amax / 448, code = RNE-satfinite(x /
- * scale), a zero scale keeps only the sign), and writes one message per valid
+ * scale), a zero scale keeps only the sign and a NaN), and writes one message per valid
  * (t, k) to slot `slot` of region (e*R + s) (address = base + (expert*R +
  * src_rank)*cap + slot, [P1] 低延迟模式).  The slot of (s, t, k) is the number
  * of earlier (t', k') of the same source and microbatch with the same expert;

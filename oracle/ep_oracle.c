@@ -111,7 +111,8 @@ void orc_e4m3_encode_array(const float* v, uint8_t* out, int64_t n) {
 }
 
 /* Per 128-channel block: amax = max |x|, scale = amax / 448 (fp32 division),
- * code = e4m3(x / scale) (fp32 division).  A zero scale keeps only the sign. */
+ * code = e4m3(x / scale) (fp32 division).  A zero scale keeps only the sign, and
+ * that x is NaN (the maximum passes over NaN). */
 void orc_quantize_row(const uint16_t* x, int H, uint8_t* codes, float* scales) {
     for (int b = 0; b < H / 128; ++b) {
         float amax = 0.0f;
@@ -124,7 +125,7 @@ void orc_quantize_row(const uint16_t* x, int H, uint8_t* codes, float* scales) {
         for (int i = 0; i < 128; ++i) {
             float xv = orc_bf16_to_f32(x[b * 128 + i]);
             if (scale == 0.0f) {
-                codes[b * 128 + i] = signbit(xv) ? 0x80u : 0x00u;
+                codes[b * 128 + i] = (uint8_t)((signbit(xv) ? 0x80u : 0x00u) | (isnan(xv) ? 0x7Fu : 0x00u));
             } else {
                 volatile float q = xv / scale;
                 codes[b * 128 + i] = orc_e4m3_encode(q);

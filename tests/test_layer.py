@@ -108,3 +108,17 @@ def test_a_tokens_nan_stays_a_nan(R, E, K, T, H, I):
         assert torch.isnan(out[bad]).all() and torch.isfinite(out[~bad]).all()
     ctx.check()
     buf.check()
+
+
+@gpu
+def test_a_token_of_nothing_but_nan_stays_a_nan():
+    R, E, K, T, H, I = 4, 8, 2, 40, 256, 128
+    x, v = inputs.random_x(R, T, H, 1).cuda(), inputs.random_weights(R, T, K, 2).cuda()
+    idx = inputs.random_topk(R, E, K, T, 3).cuda()
+    layer, _ = layer_and_reference(E, H, I, x, idx, v, 9)
+    x[2, 1] = float("nan")
+    ctx, buf = Context(R, E, K, T, H), LLBuffer(R, E, K, T, H, T)
+    for out in (layer.forward(ctx, x, idx, v), layer.forward_ll(buf, x, idx, v)):
+        assert torch.isnan(out[2, 1]).all() and int(torch.isnan(out).any(-1).sum()) == 1
+    ctx.check()
+    buf.check()
