@@ -220,7 +220,7 @@ def moe_tokens(x, topk_idx, topk_weights, w13, w2, w13_scales=None, w2_scales=No
     out[t] = sum_k topk_weights[t][k] * W2[e] (silu(Wg[e] x[t]) * (Wu[e] x[t])), e = topk_idx[t][k], -1 skipped.
 
     x [T][H] bf16; w13 = [gate; up] [E][2I][H] and w2 [E][H][I], bf16, or e4m3 codes with their block scales.
-    `workspace` (uint8, moe_tokens_workspace bytes) is allocated when it is not given."""
+    `workspace` (contiguous, moe_tokens_workspace bytes) is allocated when it is not given."""
     index = x.get_device()
     xs, ts, ws, vs = x.shape, topk_idx.shape, w13.shape, w2.shape
     if index < 0:
@@ -256,6 +256,8 @@ def moe_tokens(x, topk_idx, topk_weights, w13, w2, w13_scales=None, w2_scales=No
         out = _empty(x, stream, (T, H), _BF16)
     if workspace is None:
         workspace = _empty(x, stream, (_workspace_bytes(index, T, K, E, H, I, p13 != 0),), _U8)
+    elif not workspace.is_contiguous():
+        _refuse(f"moe_tokens: workspace must be contiguous (strides {workspace.stride()})")
     _call("ep_moe_tokens", index, x.data_ptr(), _step("moe_tokens", x), T, topk_idx.data_ptr(), topk_weights.data_ptr(), K,
           _MOE(w13.data_ptr(), p13, w2.data_ptr(), p2, E, H, I), out.data_ptr(),
           _output("moe_tokens: out", out, xs, H, (_BF16,), index), workspace.data_ptr(), workspace.nbytes,

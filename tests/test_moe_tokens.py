@@ -265,3 +265,19 @@ def test_c_refusals_without_a_gpu():
     size = lambda T, **k: lib.ep_moe_tokens_workspace(  # noqa: E731
         T, 1, ctypes.byref(_lib.EpMoeWeights(*[dict(good, **k)[n] for n in names])))
     assert size(65) == 0 and size(1, hidden=0) == 0 and lib.ep_moe_tokens_workspace(1, 1, None) == 0
+
+
+@gpu
+def test_a_workspace_with_gaps_is_refused():
+    """It would be written as if it had none."""
+    g = gen(16)
+    w13, s13, w2, s2 = weights(4, 256, 128, "fp8", g)
+    x = randn((3, 256), g).to(torch.bfloat16)
+    idx, v = routing(3, 4, 2, g)
+    need = ep.moe_tokens_workspace(3, 2, 4, 256, 128)
+    buf = torch.full((2 * need,), 0xAB, dtype=torch.uint8, device="cuda")
+    for ws in (buf[::2], buf.view(-1, 32)[:, :16]):
+        assert ws.nbytes >= need
+        with pytest.raises(ValueError, match="contiguous"):
+            ep.moe_tokens(x, idx, v, w13, w2, s13, s2, workspace=ws)
+    assert (buf == 0xAB).all()
