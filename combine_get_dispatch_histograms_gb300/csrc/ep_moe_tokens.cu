@@ -47,6 +47,7 @@ constexpr int kTokRows = 128;      // weight rows of an item
 constexpr int kTokBytes = 128;     // of a weight row per stage
 constexpr int kTokScaleRing = 16;  // stages whose powers of two are kept: more than are ever between writer and reader
 constexpr int kTokSplitMost = 4;   // parts of K in kernel 1, at most
+constexpr int kTokChannelsMost = 1 << 28;  // hidden and inter: bytes and rows of a weight stay within 32 bits
 constexpr int64_t kTokWaitNs = 2000000000ll;
 
 template <bool kDown, bool kFp8>
@@ -822,8 +823,6 @@ static ep_status launch_tokens(TokArgs a, const ep_moe_weights* w, int sms, cons
     if (rc != EP_OK) return rc;
     const int tiles1 = (a.I + kTokRows / 2 - 1) / (kTokRows / 2), tiles2 = (a.H + kTokRows - 1) / kTokRows;
     const int k1 = (a.H * kByte + kTokBytes - 1) / kTokBytes, k2 = (a.I * kByte + kTokBytes - 1) / kTokBytes;
-    if ((int64_t)a.list * tiles1 * kTokSplitMost > 0x7fffffff || (int64_t)a.list * tiles2 * k2 > 0x7fffffff)
-        return set_error(EP_ERR_INVALID_ARG, "%s: %d x %d channels of %d experts are too many", fn, a.H, a.I, a.list);
     a.split = ws.split;
     a.sums = reinterpret_cast<float*>(mem);
     a.part = reinterpret_cast<float*>(mem + ws.part);
@@ -885,11 +884,31 @@ static int sm_count() {
 
 using namespace ep;
 
+// The sizes that the operator takes; what it refuses needs no workspace.
+static ep_status check_sizes(const char* fn, int num_tokens, int num_topk, const ep_moe_weights* w) {
+    if (!w) return set_error(EP_ERR_INVALID_ARG, "%s: null weights", fn);
+    const int unit = w->w13_scales ? 128 : 32;
+    if (num_tokens < 0 || num_tokens > kTokMax) return set_error(EP_ERR_INVALID_ARG, "%s: %d tokens outside 0..%d", fn, num_tokens, kTokMax);
+    if (num_topk < 1 || num_topk > kMaxTopk) return set_error(EP_ERR_INVALID_ARG, "%s: top-k %d outside 1..%d", fn, num_topk, kMaxTopk);
+    if (w->experts < 1 || w->experts > kMaxExperts) return set_error(EP_ERR_INVALID_ARG, "%s: %d experts", fn, w->experts);
+    if (w->hidden < unit || w->hidden % unit || w->inter < unit || w->inter % unit)
+        return set_error(EP_ERR_INVALID_ARG, "%s: hidden %d and inter %d must be multiples of %d", fn, w->hidden, w->inter, unit);
+    if ((w->w2_scales != nullptr) != (w->w13_scales != nullptr))
+        return set_error(EP_ERR_INVALID_ARG, "%s: scales for both weights, or for none", fn);
+    // the kernels count channels and work items in 32 bits
+    const int list = tok_list(num_tokens, num_topk, w->experts);
+    const int64_t bytes1 = (int64_t)w->hidden * (w->w13_scales ? 1 : 2), bytes2 = (int64_t)w->inter * (w->w13_scales ? 1 : 2);
+    const int64_t tiles1 = ((int64_t)w->inter + kTokRows / 2 - 1) / (kTokRows / 2), tiles2 = ((int64_t)w->hidden + kTokRows - 1) / kTokRows;
+    if (w->hidden > kTokChannelsMost || w->inter > kTokChannelsMost || list * tiles1 * kTokSplitMost > 0x7fffffff ||
+        list * tiles2 * ((bytes2 + kTokBytes - 1) / kTokBytes) > 0x7fffffff || num_tokens * ((bytes1 + kTokBytes - 1) / kTokBytes) > 0x7fffffff)
+        return set_error(EP_ERR_INVALID_ARG, "%s: %d x %d channels of %d experts are too many", fn, w->hidden, w->inter, list);
+    return EP_OK;
+}
+
 extern "C" int64_t ep_moe_tokens_workspace(int32_t num_tokens, int32_t num_topk, const ep_moe_weights* w) {
-    if (!w || num_tokens < 1 || num_tokens > kTokMax || num_topk < 1 || num_topk > kMaxTopk || w->hidden < 32 || w->inter < 32 ||
-        w->experts < 1)
-        return 0;
-    return tok_workspace(num_tokens, num_topk, w->experts, w->hidden, w->inter, w->w13_scales != nullptr, sm_count()).bytes;
+    const int sms = sm_count();
+    if (check_sizes("ep_moe_tokens_workspace", num_tokens, num_topk, w) != EP_OK || num_tokens == 0 || sms < 1) return 0;
+    return tok_workspace(num_tokens, num_topk, w->experts, w->hidden, w->inter, w->w13_scales != nullptr, sms).bytes;
 }
 
 extern "C" ep_status ep_moe_tokens(const void* x, int64_t x_stride, int32_t num_tokens, const int64_t* topk_idx,
@@ -897,15 +916,10 @@ extern "C" ep_status ep_moe_tokens(const void* x, int64_t x_stride, int32_t num_
                                    int64_t out_stride, void* workspace, int64_t workspace_bytes, uint32_t* status_out,
                                    void* stream) {
     const char* fn = "ep_moe_tokens";
-    if (!w) return set_error(EP_ERR_INVALID_ARG, "%s: null weights", fn);
+    const ep_status sizes = check_sizes(fn, num_tokens, num_topk, w);
+    if (sizes != EP_OK) return sizes;
     const bool fp8 = w->w13_scales != nullptr;
-    const int H = w->hidden, I = w->inter, unit = fp8 ? 128 : 32;
-    if (num_tokens < 0 || num_tokens > kTokMax) return set_error(EP_ERR_INVALID_ARG, "%s: %d tokens outside 0..%d", fn, num_tokens, kTokMax);
-    if (num_topk < 1 || num_topk > kMaxTopk) return set_error(EP_ERR_INVALID_ARG, "%s: top-k %d outside 1..%d", fn, num_topk, kMaxTopk);
-    if (w->experts < 1 || w->experts > kMaxExperts) return set_error(EP_ERR_INVALID_ARG, "%s: %d experts", fn, w->experts);
-    if (H < unit || H % unit || I < unit || I % unit)
-        return set_error(EP_ERR_INVALID_ARG, "%s: hidden %d and inter %d must be multiples of %d", fn, H, I, unit);
-    if ((w->w2_scales != nullptr) != fp8) return set_error(EP_ERR_INVALID_ARG, "%s: scales for both weights, or for none", fn);
+    const int H = w->hidden, I = w->inter;
     if (num_tokens == 0) return EP_OK;
     if (!x || !topk_idx || !topk_weights || !out || !w->w13 || !w->w2 || !aligned16(x) || !aligned16(w->w13) || !aligned16(w->w2))
         return set_error(EP_ERR_INVALID_ARG, "%s: null or unaligned (16 bytes: x, weights) pointer", fn);

@@ -281,3 +281,27 @@ def test_a_workspace_with_gaps_is_refused():
         with pytest.raises(ValueError, match="contiguous"):
             ep.moe_tokens(x, idx, v, w13, w2, s13, s2, workspace=ws)
     assert (buf == 0xAB).all()
+
+
+@pytest.mark.parametrize("bad", [dict(T=65), dict(T=0), dict(T=-1), dict(K=0), dict(K=33), dict(experts=0), dict(experts=4097),
+                                 dict(hidden=96), dict(hidden=160), dict(inter=64), dict(inter=-128), dict(w2_scales=None),
+                                 dict(hidden=1 << 29), dict(inter=1 << 30), dict(w13_scales=None, w2_scales=None, hidden=48),
+                                 dict(w13_scales=None, w2_scales=None, inter=16)])
+def test_refused_sizes_need_no_workspace(bad):
+    """What ep_moe_tokens refuses has a workspace of 0 bytes."""
+    from combine_get_dispatch_histograms_gb300 import _lib
+    lib = _lib.load()
+    c = dict(dict(T=1, K=1, w13=256, w13_scales=256, w2=256, w2_scales=256, experts=4, hidden=128, inter=128), **bad)
+    w = _lib.EpMoeWeights(*[c[n] for n in ("w13", "w13_scales", "w2", "w2_scales", "experts", "hidden", "inter")])
+    call = lib.ep_moe_tokens(256, 1 << 32, c["T"], 256, 256, c["K"], ctypes.byref(w), 256, 1 << 32, 256, 0, None, None)
+    assert call == (0 if c["T"] == 0 else -1)
+    assert lib.ep_moe_tokens_workspace(c["T"], c["K"], ctypes.byref(w)) == 0
+
+
+@gpu
+def test_every_refused_size_needs_no_workspace_on_a_gpu():
+    """The same where the device is known, next to sizes that are taken."""
+    size = lambda T=1, K=1, E=4, H=128, I=128, fp8=True: ep.moe_tokens_workspace(T, K, E, H, I, fp8)  # noqa: E731
+    assert size() > 0 and size(fp8=False, H=32, I=160) > 0 and size(T=64, K=32, E=4096) > 0
+    for bad in (dict(T=65), dict(T=0), dict(K=33), dict(E=4097), dict(H=160), dict(I=64), dict(H=48, fp8=False), dict(H=1 << 29)):
+        assert size(**bad) == 0, bad
