@@ -670,7 +670,12 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
     __syncwarp();
     tc_fence_before();
     __syncthreads();
-    if (kCtas == 2) cluster_sync();
+    if constexpr (kCtas == 2) {
+        // the last commit arrives in both blocks: the second one, too, lives until it has
+        if (rank == 1 && warp == 1) mbar_wait_bounded(&sh.drain, 0, kGemmWaitNs);
+        __syncwarp();
+        cluster_sync();
+    }
     tc_fence_after();
     if (warp == 2) tmem_free<kCtas>(tmem, 512);
     if (tid == 0 && *abort && a.status) flag(a.status, FLAG_TIMEOUT);

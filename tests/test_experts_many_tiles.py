@@ -111,3 +111,22 @@ def test_rest_of_the_ring_in_both_forms(form, KB, N):
             X, W = rows64(x[o:o + c], xs[o:o + c]), weight64(w[e], ws[e])
             assert_bf16_close(out[o:o + c], *product64(X, W), f"group {e}")
             assert_fp8_close(codes[o:o + c], scales[o:o + c], *swiglu64(X, W), f"group {e}")
+
+
+@gpu
+def test_short_launches_of_both_forms_in_turn():
+    """Blocks end and start on the same SM by the hundred: nothing that one launch signals arrives in the next."""
+    counts = [130, 200, 256] * 28
+    cnt, off, hoff, x, xs, w, ws = case(counts, 128, 256, seed=77)
+    outs, forms = {}, ("pairs", "one", "pairs", "pairs", "one")
+    for form in ("one", "pairs"):
+        assert form_of(x.shape[0], len(counts), 256, 128, FORMS[form]) == form
+        outs[form] = ep.expert_gemm(x, xs, w, ws, counts=cnt, offsets=off, expected_rows=FORMS[form])
+        for e, (o, c) in enumerate(zip(hoff, counts)):
+            assert_bf16_close(outs[form][o:o + c], *product64(rows64(x[o:o + c], xs[o:o + c]), weight64(w[e], ws[e])), f"group {e}")
+    own = owned(counts, hoff, x.shape[0])
+    st = ep.new_status()
+    got = [ep.expert_gemm(x, xs, w, ws, counts=cnt, offsets=off, expected_rows=FORMS[f], status=st) for f in forms * 60]
+    ep.check_status(st)
+    for f, y in zip(forms * 60, got):
+        assert torch.equal(y[own].view(torch.int16), outs[f][own].view(torch.int16))
