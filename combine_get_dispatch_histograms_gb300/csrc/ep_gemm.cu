@@ -61,6 +61,7 @@ constexpr int kTileRing = 4;            // tiles announced ahead
 constexpr int kScaleChunk = 8;          // blocks of K whose scales are staged together
 constexpr int kScaleRing = 2;
 constexpr int kMaxGroups = 4096;
+constexpr int kMaxTiles = 0x7fffffff - 65536;  // a block's next tile, one grid further on, stays within 31 bits
 constexpr int kChunkRows = 2048;       // rows that share a pass over the weight's tiles
 constexpr int kSplitStride = kBN + 4;  // floats of a row of sums: rows fall into other banks
 constexpr int64_t kGemmWaitNs = 2000000000ll;
@@ -71,6 +72,7 @@ struct GemmArgs {
     const float* w_scales;
     int64_t w_sgroup;   // floats of one group's scales
     int G, N, K, KB, n_tiles;
+    int most;           // tiles of groups that share no row, at most
     const int32_t *counts, *offsets, *bases;
     int per_base;
     int64_t group_stride, rows;
@@ -148,12 +150,16 @@ struct RingPos {
 template <int kTileM>
 struct TileWalk {
     static constexpr int kChunkM = kChunkRows / kTileM;
-    int g0 = -32, start = 0, sum = 0;  // batch of groups, its first tile, its tiles
-    int inc, tiles, rows, first;       // this lane's group: tiles up to and with it, tiles, rows, first row
+    int g0 = -32;
+    uint32_t start = 0, sum = 0;       // first tile of a batch of groups, its tiles
+    uint32_t inc;                      // tiles up to and with this lane's group
+    int rows, first;                   // its rows, first row
     bool cut = false;
 
-    // false: no tile t
-    __device__ __forceinline__ bool find(const GemmArgs& a, int t, int lane, GemmTile* out) {
+    // false: no tile t.  Groups that overlap may have any number of tiles: those past a.most are cut off, and
+    // sums that would pass 31 bits stay there, above every t.
+    __device__ __forceinline__ bool find(const GemmArgs& a, int unit_tile, int lane, GemmTile* out) {
+        const uint32_t t = min(unit_tile, a.most);
         while (t >= start + sum) {
             start += sum;
             g0 += 32;
@@ -165,17 +171,21 @@ struct TileWalk {
             const int g = g0 + lane;
             rows = g < a.G ? group_rows(a, g, &cut) : 0;
             first = rows ? (int)group_first(a, g) : 0;
-            tiles = (rows + kTileM - 1) / kTileM * a.n_tiles;
-            inc = tiles;
+            inc = (uint32_t)((rows + kTileM - 1) / kTileM * a.n_tiles);
             for (int o = 1; o < 32; o <<= 1) {
-                const int v = __shfl_up_sync(0xffffffffu, inc, o);
-                if (lane >= o) inc += v;
+                const uint32_t v = __shfl_up_sync(0xffffffffu, inc, o);
+                if (lane >= o) inc = min(inc + v, 0x7fffffffu);
             }
             sum = __shfl_sync(0xffffffffu, inc, 31);
         }
+        if (t == (uint32_t)a.most) {
+            cut = true;
+            return false;
+        }
         const int src = __ffs(__ballot_sync(0xffffffffu, t < start + inc)) - 1;
         const int n = __shfl_sync(0xffffffffu, rows, src);
-        int r = t - start - __shfl_sync(0xffffffffu, inc - tiles, src);
+        const uint32_t before = __shfl_sync(0xffffffffu, inc, src > 0 ? src - 1 : 0);
+        int r = (int)(t - start - (src > 0 ? before : 0));
         const int mt = (n + kTileM - 1) / kTileM, chunk = r / (kChunkM * a.n_tiles);
         r -= chunk * kChunkM * a.n_tiles;
         const int m0 = chunk * kChunkM, mc = min(kChunkM, mt - m0), m = m0 + r % mc;
@@ -688,7 +698,7 @@ static ep_status check_products(const char* fn, const ep_fp8_rows* x, const ep_r
     if (!x || !g || !w) return set_error(EP_ERR_INVALID_ARG, "%s: null descriptor", fn);
     if (w->groups < 1 || w->groups > kMaxGroups)
         return set_error(EP_ERR_INVALID_ARG, "%s: groups %d outside 1..%d", fn, w->groups, kMaxGroups);
-    if (w->n < 1 || w->k < 128 || w->k % 128)
+    if (w->n < 1 || w->n > 0x7fffffff - kBN || w->k < 128 || w->k % 128)
         return set_error(EP_ERR_INVALID_ARG, "%s: weight rows %d, channels %d (a multiple of 128)", fn, w->n, w->k);
     if (!w->codes || !w->scales || !aligned16(w->codes))
         return set_error(EP_ERR_INVALID_ARG, "%s: weight codes (16-byte aligned) and scales are required", fn);
@@ -716,11 +726,12 @@ static int64_t most_tiles(const GemmArgs& a, int tile_rows) {
 
 template <bool kSwiglu, int kCtas, bool kSplit>
 static ep_status launch_shape(const char* fn, const CUtensorMap& map_x, const CUtensorMap& map_w,
-                              const CUtensorMap& map_out, const GemmArgs& a, int sms,
+                              const CUtensorMap& map_out, GemmArgs a, int sms,
                               int cluster, void* stream) {
     using Shape = GemmShape<kCtas>;
     const int64_t most = most_tiles(a, Shape::kTileM);
-    if (most > 0x7fffffff) return set_error(EP_ERR_INVALID_ARG, "%s: %lld tiles", fn, (long long)most);
+    if (most > kMaxTiles) return set_error(EP_ERR_INVALID_ARG, "%s: %lld tiles", fn, (long long)most);
+    a.most = (int)most;
     int dev = 0;
     EP_CUDA(cudaGetDevice(&dev));
     static std::atomic<bool> known[kMaxDevicesTracked];  // devices whose launch attribute is set

@@ -397,7 +397,8 @@ typedef struct ep_fp8_rows {
  *     handle->perm_rank_base, per_base = L, counts = handle->num_recv_per_expert;
  *   packed low-latency layout: stride = R * cap, counts = packed_recv_count;
  *   one dense group: stride = the number of rows, all pointers NULL.
- * A group may be empty; rows of no group are neither read nor written.  bases
+ * A group may be empty; rows of no group are not written and count for nothing.
+ * Groups that share rows write the same output: what it holds then is open.  bases
  * holds ceil(groups / per_base) entries at least. */
 typedef struct ep_row_groups {
     const int32_t* counts;
@@ -424,7 +425,8 @@ typedef struct ep_fp8_weight {
  * out: bf16 rows, out_stride elements apart.  x->rows is also the capacity of
  * out.  status_out (device, nullable): error bits are ORed into it (2 = a
  * group's rows lie outside x->rows, or outside its region of `stride` rows where
- * there are no offsets, they were cut off; 4 = a bounded wait ran
+ * there are no offsets, or groups overlap so far that they have more tiles than
+ * x->rows could: they were cut off; 4 = a bounded wait ran
  * out); the caller zeroes it.  No host synchronisation, no workspace. */
 ep_status ep_expert_gemm(const ep_fp8_rows* x, const ep_row_groups* groups, const ep_fp8_weight* w, void* out,
                          int64_t out_stride, uint32_t* status_out, void* stream);

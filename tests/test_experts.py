@@ -402,3 +402,74 @@ def test_c_refusals_without_a_gpu():
     assert call(_lib.EpFp8Rows(None, 0, None, 0, 0), w()) == 0         # nothing to do
     w13 = w(n=128)
     assert lib.ep_expert_swiglu(ctypes.byref(x), ctypes.byref(g), ctypes.byref(w13), 256, 128, 256, 1, None, None) == -1
+
+
+@gpu
+@pytest.mark.parametrize("form,G,rows,K,N,expected", [("cluster", 3, 140, 1024, 512, 0), ("one", 90, 300, 128, 1024, 64),
+                                                      ("pairs", 90, 1000, 128, 1024, 500)])
+def test_groups_that_overlap_are_cut_and_flagged(form, G, rows, K, N, expected):
+    """Every group claims all rows: more tiles than the rows could have.  Blocks write them beside one another, so that an
+    element holds some group's product, or is left alone."""
+    from expert_shapes import form_of
+    assert form_of(rows, G, N, K, expected) == form
+    g = gen(G)
+    x, xs = quantize_rows(randn((rows, K), g))
+    w, ws = quantize_weight(randn((G, N, K), g) * K ** -0.5)
+    cnt, off = torch.full((G,), rows, dtype=torch.int32, device="cuda"), torch.zeros(G, dtype=torch.int32, device="cuda")
+    st = ep.new_status()
+    out = torch.full((rows, N), 7.0, dtype=torch.bfloat16, device="cuda")
+    ep.expert_gemm(x, xs, w, ws, counts=cnt, offsets=off, out=out, status=st, expected_rows=expected)
+    with pytest.raises(ep.EpError) as e:
+        ep.check_status(st)
+    assert e.value.status == "EP_ERR_CAPACITY"
+    ep.expert_swiglu(x, xs, w, ws, counts=cnt, offsets=off, status=st, expected_rows=expected)
+    with pytest.raises(ep.EpError):
+        ep.check_status(st)
+    fits = out == 7.0
+    for i in range(G):
+        y, err = product64(rows64(x, xs), weight64(w[i], ws[i]))
+        fits |= (out.double() - y).abs() <= 2.0 ** -8 * y.abs() + err
+    assert fits.all()
+    # one group after the other is no overlap
+    cnt = torch.tensor([rows] + [0] * (G - 1), dtype=torch.int32, device="cuda")
+    ep.expert_gemm(x, xs, w, ws, counts=cnt, offsets=off, out=out, status=st, expected_rows=expected)
+    ep.check_status(st)
+    assert_bf16_close(out, *product64(rows64(x, xs), weight64(w[0], ws[0])))
+
+
+def test_tile_walk_stays_within_31_bits():
+    """The walk's arithmetic, restated: groups that claim every row, with more than 2^31 tiles in all."""
+    def walk(tiles, most, unit, units, u32=1 << 32):
+        """(group, tile of the group) that `unit` takes, as the kernel's warp does with 32-bit sums."""
+        start = total = 0
+        g0, inc, got, t = -32, [], [], unit
+        while True:
+            at = min(t, most)
+            while at >= (start + total) % u32:
+                start = (start + total) % u32
+                g0 += 32
+                if g0 >= len(tiles):
+                    return got, False
+                inc, run = [], 0
+                for v in (tiles[g0:g0 + 32] + [0] * 32)[:32]:
+                    run = min(run + v, 0x7FFFFFFF)
+                    inc.append(run)
+                total = inc[-1]
+            if at == most:
+                return got, True
+            src = next(i for i in range(32) if at < start + inc[i])
+            got.append((g0 + src, at - start - (inc[src - 1] if src else 0)))
+            t += units
+            assert t < 1 << 31
+    most = 0x7FFFFFFF - 65536
+    huge = [most // 2 + 7] * 4096
+    units = 60000                        # a grid has fewer blocks than this
+    for unit in (0, 1, units - 1):
+        got, cut = walk(huge, most, unit, units)
+        assert cut and len(got) == len(range(unit, most, units))
+        for i, (g, r) in enumerate(got):
+            assert 0 <= r < huge[g] and g * huge[0] + r == unit + i * units
+    fine = [3, 0, 5, 0] * 100
+    seen = sorted(p for unit in range(7) for p in walk(fine, sum(fine), unit, 7)[0])
+    assert seen == [(g, r) for g, n in enumerate(fine) for r in range(n)]
+    assert not any(walk(fine, sum(fine), unit, 7)[1] for unit in range(7))
