@@ -12,12 +12,20 @@
 // weights are the 128 rows of the tensor-core product and go from memory to
 // shared memory by tiled copies and nowhere else; the few tokens are its
 // columns, written beside them by warps that convert them block by block:
-//   fp8 weights: a token's 128 channels times a power of two are split into
-//     e4m3 pieces, v = p1 + p2 / 16 (+ p3 / 256), each a column of its own; two
-//     pieces hold a bf16 value exactly (8 bits of significand; an element below
-//     2^-13 of its block's largest is off by at most 2^-21 of that), three hold
-//     h to 2^-13 of itself;
-//   bf16 weights: x itself, and h as the sum of two bf16.
+//   fp8 weights: a token's 128 channels times a power of two, |v| < 256, are split
+//     into e4m3 pieces, each the rest that the ones before leave, times 2^5 more
+//     (a rest is at most 2^-5 of the range below 256, so that it fits again), and
+//     each a column of its own.  A piece takes 5 bits and ends at 2^-9 of its power.
+//     h, 24 bits: five pieces hold an element of 2^-13 of the block's largest or
+//     more exactly, a smaller one to 2^-37 of the largest.  x, 8 bits: two pieces hold
+//     an element of 2^-14 of the largest or more; what they leave of a smaller one is
+//     at most 2^-15, and two more pieces, from 2^23 on, hold that.  An element of 2^-37
+//     or more is exact, a smaller one off by at most 2^-45 (of the block's largest);
+//   bf16 weights: x itself, and h as the sum of three bf16, which are its 24 bits.
+// So the sums add x and h as a 32-bit form does.  Two pieces of x and three of h
+// (two bf16) were off by up to 2^-21 of the largest and 2^-13 of h, which outputs
+// that cancel show, and took 71 us where these take 76 (one token), 694 / 754 (64
+// tokens), 417 / 418 (bf16).
 // Up to 16 tokens each block converts what it needs; for more, whose experts'
 // blocks would repeat much of it, the pieces are made once beforehand.
 // A block of 128 channels is one accumulator; it leaves tensor memory, times its
@@ -52,10 +60,13 @@ constexpr int64_t kTokWaitNs = 2000000000ll;
 
 template <bool kDown, bool kFp8>
 struct TokShape {
-    static constexpr int kPieces = kFp8 ? (kDown ? 3 : 2) : (kDown ? 2 : 1);  // columns of a token
+    static constexpr int kPieces = kFp8 ? (kDown ? 5 : 4) : (kDown ? 3 : 1);  // columns of a token
     static constexpr int kCols = kTokSlots * kPieces;
+    static constexpr int kAccCols = kCols <= 64 ? 64 : 128;  // tensor-memory columns of an accumulator
+    // what piece z + 1 is multiplied by beyond piece z
+    static constexpr float step(int z) { return !kFp8 ? 1.0f : !kDown && z == 1 ? 0x1p18f : 32.0f; }
     static constexpr int kStageA = kTokRows * kTokBytes, kStage = kStageA + kCols * kTokBytes;
-    static constexpr int kStages = kDown ? (kFp8 ? 7 : 8) : 10;
+    static constexpr int kStages = kDown ? (kFp8 ? 6 : 7) : (kFp8 ? 8 : 10);
     static constexpr int kChannels = kFp8 ? 128 : 64;  // of a stage
     // Each converting warp takes every kFill-th stage.  When it waits for the stage before its next one
     // to be done, it knows its own last one to be filled, so that stage kFill + kStages back is done; a
@@ -253,14 +264,14 @@ struct TokRuns {
 __device__ __forceinline__ uint32_t pack_e4m3(float a, float b, float c, float d) {
     return (e4m3x2(a, b) & 0xffffu) | (e4m3x2(c, d) << 16);
 }
-// v[0..3] minus the values of their codes, times 16: what the next piece holds.
-__device__ __forceinline__ void next_piece(float* v, uint32_t codes) {
+// v[0..3] minus the values of their codes, times `step`: what the next piece holds.
+__device__ __forceinline__ void next_piece(float* v, uint32_t codes, float step) {
     const float2 lo = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(codes & 0xffffu), __NV_E4M3)));
     const float2 hi = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(codes >> 16), __NV_E4M3)));
-    v[0] = (v[0] - lo.x) * 16.0f;
-    v[1] = (v[1] - lo.y) * 16.0f;
-    v[2] = (v[2] - hi.x) * 16.0f;
-    v[3] = (v[3] - hi.y) * 16.0f;
+    v[0] = (v[0] - lo.x) * step;
+    v[1] = (v[1] - lo.y) * step;
+    v[2] = (v[2] - hi.x) * step;
+    v[3] = (v[3] - hi.y) * step;
 }
 
 // kN consecutive 32-bit words.
@@ -271,10 +282,12 @@ __device__ __forceinline__ void load_words(const float* p, float* v) {
     else *v = *p;
 }
 
-// A lane's channels of a token's block as kPieces pieces, each handed to put(piece, 4 bytes).  Returns the
+// A lane's channels of a token's block as pieces, each handed to put(piece, 4 bytes).  Returns the
 // power of two that the block's sums are multiplied by (e4m3 only).
-template <bool kFp8, int kPieces, int kLane, class Put>
+template <bool kDown, bool kFp8, int kLane, class Put>
 __device__ __forceinline__ float write_pieces(float (&v)[kLane], Put put) {
+    using Shape = TokShape<kDown, kFp8>;
+    constexpr int kPieces = Shape::kPieces;
     if constexpr (kFp8) {
         uint32_t top = 0;  // the largest magnitude's bits, above infinity's where one is NaN
 #pragma unroll
@@ -289,7 +302,7 @@ __device__ __forceinline__ float write_pieces(float (&v)[kLane], Put put) {
         for (int z = 0; z < kPieces; ++z) {
             const uint32_t c = pack_e4m3(v[0], v[1], v[2], v[3]);
             put(z, odd ? 0x7f7f7f7fu : c);  // an infinity or a NaN makes the token's whole block NaN
-            if (z + 1 < kPieces) next_piece(v, c);
+            if (z + 1 < kPieces) next_piece(v, c, Shape::step(z));
         }
         return odd ? 1.0f : __uint_as_float((uint32_t)(e - 7 + 127) << 23);
     } else {
@@ -350,7 +363,7 @@ __global__ void __launch_bounds__(256) form_kernel(const TokArgs a) {
         }
         values_of<kDown>(raw, v);
         uint8_t* to = a.formed + (int64_t)i * kPieces * kTokBytes + lane * 4;
-        const float power = write_pieces<kFp8, kPieces>(v, [&](int z, uint32_t w) { *reinterpret_cast<uint32_t*>(to + z * kTokBytes) = w; });
+        const float power = write_pieces<kDown, kFp8>(v, [&](int z, uint32_t w) { *reinterpret_cast<uint32_t*>(to + z * kTokBytes) = w; });
         if (kFp8 && lane == 0) a.powers[i] = power;
     }
 }
@@ -391,7 +404,7 @@ __global__ void __launch_bounds__(kTokThreads, 1) tok_kernel(const __grid_consta
         fence_mbar_init();
         tma_prefetch_desc(&map_w);
     }
-    if (warp == 2) tmem_alloc<1>(&sh.tmem, 128);
+    if (warp == 2) tmem_alloc<1>(&sh.tmem, 2 * Shape::kAccCols);
     // What is above may run beside the end of the kernel before.  The first kernel of a call waits for what
     // ran before the call; the later ones start after that, and wait below, where they read their own.
     if constexpr (!kDown && !kFormed) grid_wait();
@@ -475,8 +488,8 @@ __global__ void __launch_bounds__(kTokThreads, 1) tok_kernel(const __grid_consta
                 if (elect_one()) {
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
-                        if constexpr (kFp8) mma_e4m3<1>(tmem + (n & 1) * 64, da + q * 2, db + q * 2, idesc, q > 0);
-                        else mma_bf16_ss(tmem + (n & 1) * 64, da + q * 2, db + q * 2, idesc, q > 0);
+                        if constexpr (kFp8) mma_e4m3<1>(tmem + (n & 1) * Shape::kAccCols, da + q * 2, db + q * 2, idesc, q > 0);
+                        else mma_bf16_ss(tmem + (n & 1) * Shape::kAccCols, da + q * 2, db + q * 2, idesc, q > 0);
                     }
                     mma_commit<1>(done + u * 8);
                 }
@@ -500,21 +513,32 @@ __global__ void __launch_bounds__(kTokThreads, 1) tok_kernel(const __grid_consta
                     // four rows (a piece of a token each) at a time, 16 bytes a lane
                     const int unit = lane & 7, k = run.k0 + i;
                     auto source = [&](int j) { return (int64_t)(kDown ? p0 + j : s.token[p0 + j]) * a.blocks_k + k; };
-                    int4 w[Shape::kCols / 4];
+                    constexpr int kAt = Shape::kCols <= 48 ? Shape::kCols / 4 : Shape::kCols / 8;  // on their way at once
+                    int4 w[kAt];
                     float power = 0.0f;
+                    uint8_t* st = ring + u * Shape::kStage + Shape::kStageA;
+                    auto load = [&](int r0) {
 #pragma unroll
-                    for (int q = 0; q < Shape::kCols / 4; ++q) {
-                        const int r = q * 4 + (lane >> 3), j = r / kPieces;
-                        if (j < cnt)
-                            w[q] = __ldcg(reinterpret_cast<const int4*>(a.formed + (source(j) * kPieces + r - j * kPieces) * kTokBytes) + unit);
-                    }
+                        for (int q = 0; q < kAt; ++q) {
+                            const int r = r0 + q * 4 + (lane >> 3), j = r / kPieces;
+                            if (j < cnt)
+                                w[q] = __ldcg(reinterpret_cast<const int4*>(a.formed + (source(j) * kPieces + r - j * kPieces) * kTokBytes) + unit);
+                        }
+                    };
+                    auto store = [&](int r0) {
+#pragma unroll
+                        for (int q = 0; q < kAt; ++q) {
+                            const int r = r0 + q * 4 + (lane >> 3);
+                            if (r / kPieces < cnt) *reinterpret_cast<int4*>(st + r * kTokBytes + ((unit ^ (r & 7)) << 4)) = w[q];
+                        }
+                    };
+                    load(0);
                     if (kFp8 && lane < cnt) power = __ldcg(a.powers + source(lane));
                     mbar_wait_warp(done + u * 8, n / kStages & 1 ^ 1, kTokWaitNs, abort);
-                    uint8_t* st = ring + u * Shape::kStage + Shape::kStageA;
-#pragma unroll
-                    for (int q = 0; q < Shape::kCols / 4; ++q) {
-                        const int r = q * 4 + (lane >> 3);
-                        if (r / kPieces < cnt) *reinterpret_cast<int4*>(st + r * kTokBytes + ((unit ^ (r & 7)) << 4)) = w[q];
+                    store(0);
+                    if (kAt * 4 < Shape::kCols && cnt * kPieces > kAt * 4) {
+                        load(kAt * 4);
+                        store(kAt * 4);
                     }
                     if (kFp8 && lane < cnt) sh.scale[n % kTokScaleRing][lane] = power;
                     fence_proxy_async_smem();
@@ -570,7 +594,7 @@ __global__ void __launch_bounds__(kTokThreads, 1) tok_kernel(const __grid_consta
                         // piece z of the token is row col + z of the tile, 4 bytes a lane, 16-byte units
                         // exchanged by the 128-byte swizzle
                         const int col = (j0 + q) * kPieces;
-                        const float power = write_pieces<kFp8, kPieces>(v[q], [&](int z, uint32_t w) {
+                        const float power = write_pieces<kDown, kFp8>(v[q], [&](int z, uint32_t w) {
                             const int r = col + z;
                             *reinterpret_cast<uint32_t*>(st + r * kTokBytes + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4) = w;
                         });
@@ -628,28 +652,31 @@ __global__ void __launch_bounds__(kTokThreads, 1) tok_kernel(const __grid_consta
                 mbar_wait_warp(done + n % kStages * 8, n / kStages & 1, kTokWaitNs, abort);
                 tc_fence_after();
                 const float* sc = sh.scale[n % kTokScaleRing];
-                // 16 columns at a time: the pieces of 16 / kPieces tokens, in order
-                float t[kPieces == 3 ? 48 : 16 * kPieces];
-                const uint32_t ad = lane_base + (n & 1) * 64;
+                // the pieces of kAt tokens, in order, 16 columns at a time
+                constexpr int kAt = kPieces > 3 ? kTokSlots / 2 : kTokSlots, kLoads = (kAt * kPieces + 15) / 16;
+                const uint32_t ad = lane_base + (n & 1) * Shape::kAccCols;
 #pragma unroll
-                for (int q = 0; q < kPieces; ++q)
-                    if (cnt * kPieces > q * 16) tmem_ld(ad + q * 16, *reinterpret_cast<float(*)[16]>(t + q * 16));
+                for (int j0 = 0; j0 < kTokSlots; j0 += kAt) {
+                    if (j0 >= cnt) break;
+                    float t[16 * kLoads];
 #pragma unroll
-                for (int q = 0; q < kPieces; ++q) tmem_wait_ld(*reinterpret_cast<float(*)[16]>(t + q * 16));
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_hand_back(acc_empty + (n & 1) * 8);
+                    for (int q = 0; q < kLoads; ++q)
+                        if ((cnt - j0) * kPieces > q * 16) tmem_ld(ad + j0 * kPieces + q * 16, *reinterpret_cast<float(*)[16]>(t + q * 16));
 #pragma unroll
-                for (int j = 0; j < kTokSlots; ++j) {
-                    if ((j & 3) == 0 && j >= cnt) break;
-                    float y = t[j * kPieces];
-                    if constexpr (kFp8) {
-                        y = fmaf(t[j * kPieces + 1], 0.0625f, y);
-                        if constexpr (kPieces == 3) y = fmaf(t[j * kPieces + 2], 0.00390625f, y);
-                        acc[j] = fmaf(y, f * sc[j], acc[j]);
-                    } else {
-                        if constexpr (kPieces == 2) y += t[j * kPieces + 1];
-                        acc[j] += y;
+                    for (int q = 0; q < kLoads; ++q) tmem_wait_ld(*reinterpret_cast<float(*)[16]>(t + q * 16));
+                    if (j0 + kAt >= cnt) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_hand_back(acc_empty + (n & 1) * 8);
+                    }
+#pragma unroll
+                    for (int j = 0; j < kAt; ++j) {
+                        if ((j & 3) == 0 && j0 + j >= cnt) break;
+                        float y = t[j * kPieces + kPieces - 1];
+#pragma unroll
+                        for (int z = kPieces - 2; z >= 0; --z) y = fmaf(y, 1.0f / Shape::step(z), t[j * kPieces + z]);
+                        if constexpr (kFp8) acc[j0 + j] = fmaf(y, f * sc[j0 + j], acc[j0 + j]);
+                        else acc[j0 + j] += y;
                     }
                 }
             }
@@ -687,7 +714,7 @@ __global__ void __launch_bounds__(kTokThreads, 1) tok_kernel(const __grid_consta
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 2) tmem_free<1>(tmem, 128);
+    if (warp == 2) tmem_free<1>(tmem, 2 * Shape::kAccCols);
     if constexpr (kDown) {
         // the block that leaves a tile's last part adds the parts in block order
         if (!idle && A > 0) {
@@ -808,6 +835,8 @@ static ep_status launch_tokens(TokArgs a, const ep_moe_weights* w, int sms, cons
         auto allow = [](auto* kernel, size_t bytes) {
             return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
         };
+        static_assert(tok_smem<false, kFp8>(kTokMax, kMaxTopk, kMost) + sizeof(TokBarriers) + 128 <= 227 * 1024 &&
+                      tok_smem<true, kFp8>(kTokMax, kMaxTopk, kMost) + sizeof(TokBarriers) + 128 <= 227 * 1024, "shared memory");
         const size_t most1 = tok_smem<false, kFp8>(kTokMax, kMaxTopk, kMost), most2 = tok_smem<true, kFp8>(kTokMax, kMaxTopk, kMost);
         EP_CUDA(allow(tok_kernel<false, kFp8, false, false>, most1));
         if constexpr (kFp8) EP_CUDA(allow(tok_kernel<false, true, false, true>, most1));

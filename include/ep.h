@@ -464,8 +464,11 @@ int64_t ep_moe_tokens_workspace(int32_t num_tokens, int32_t num_topk, const ep_m
 /* A whole layer for 0..64 tokens, in two kernels (above 16 tokens up to two small ones more):
  *   out[t] = bf16( sum over k of w[t][k] * W2[e] ( silu(Wg[e] x[t]) * (Wu[e] x[t]) ) ),  e = topk_idx[t][k],
  * x and out bf16 rows, strides in elements (x 16-byte aligned, x_stride a
- * multiple of 8).  Every sum is fp32; h enters the second product with an error
- * below 2^-13 of itself.  -1 entries are skipped, a token with no valid entry gets +0;
+ * multiple of 8).  Every sum is fp32, and x and h enter the products with the
+ * bits of a 32-bit form: with e4m3 weights an element of x is exact down to 2^-37
+ * of its 128 channels' largest and off by at most 2^-45 of that below, one of h
+ * exact down to 2^-13 and off by at most 2^-37 below; with
+ * bf16 weights both are exact.  -1 entries are skipped, a token with no valid entry gets +0;
  * an entry outside [-1, experts) is skipped and ORs 1 into status_out (device,
  * nullable, zeroed by the caller).  The experts a token names twice count with
  * the sum of both weights.  The order of the sums depends on the routing and
