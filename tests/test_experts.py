@@ -473,3 +473,29 @@ def test_tile_walk_stays_within_31_bits():
     seen = sorted(p for unit in range(7) for p in walk(fine, sum(fine), unit, 7)[0])
     assert seen == [(g, r) for g, n in enumerate(fine) for r in range(n)]
     assert not any(walk(fine, sum(fine), unit, 7)[1] for unit in range(7))
+
+
+@gpu
+def test_activation_over_its_range():
+    """One code times a scale of any fp32 value: gate and up are exact, all 128 channels of a block are equal, and the
+    block's scale is |h| / 448 in fp32.  silu(g) * u is off by at most 8 * 2^-23 of itself, for negative g by |g| * 2^-23
+    more; the division rounds to 2^-24.  Below -87 it may be 0."""
+    s = torch.cat([torch.logspace(-4, 1.93, 4000, device="cuda"), torch.tensor([85.0, 86.9, 87.5, 89.0, 120.0, 1e4], device="cuda")])
+    rows = s.numel()
+    x = torch.zeros(rows, 128, device="cuda")
+    x[:, 0] = 1
+    w = torch.zeros(512, 128, device="cuda")
+    w[:128, 0], w[128:256, 0], w[256:, 0] = -1, 1, 1         # gate -s in block 0, s in block 1; up s
+    one = torch.ones(4, 1, device="cuda")
+    for shape in ("cluster or one", "pairs"):
+        G = 1 if shape != "pairs" else 40
+        n = rows // G * G
+        kw = {} if G == 1 else dict(counts=torch.full((G,), n // G, dtype=torch.int32, device="cuda"),
+                                    offsets=torch.arange(0, n, n // G, dtype=torch.int32, device="cuda"), expected_rows=500)
+        W, WS = w.to(torch.float8_e4m3fn).expand(G, -1, -1).contiguous(), one.expand(G, -1, -1).contiguous()
+        _, scales = ep.expert_swiglu(x[:n].to(torch.float8_e4m3fn), s[:n, None].contiguous(), W, WS, **kw)
+        g = torch.stack([-s[:n], s[:n]], 1).double()
+        h = (g / (1 + torch.exp(-g)) * s[:n, None].double()).abs()
+        d = (scales.double() * 448 - h).abs()
+        lim = (8 + g.clamp(max=0).abs() + 1) * 2.0 ** -23 * h + torch.where(g < -87, 88 * 2.0 ** -126 * s[:n, None].double(), 0.0) + 1e-43
+        assert (d <= lim).all(), f"{shape}: worst {float((d / lim).max()):.3g} of the bound"
