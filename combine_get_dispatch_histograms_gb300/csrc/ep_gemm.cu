@@ -815,10 +815,10 @@ static ep_status launch_gemm(const char* fn, const ep_fp8_rows* x, const ep_row_
     EP_CUDA(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
     const int split = split_of(most_tiles(a, kBM), a.KB, sms);
     if (split > 1) return launch_shape<kSwiglu, 1, true>(fn, map_x, map_w, map_out, a, sms, split, stream);
-    // Rows of a group: as the caller expects, or what the arrays hold, shared out.  The regions of the
-    // packed layout are sized for the worst case, a low-latency step fills a few percent of them.
+    // Rows of a group: as the caller expects, or what the arrays hold, shared out.  Regions with counts, as the
+    // packed layout has, are sized for the worst case: a low-latency step fills a few percent of them.
     const int64_t per_group =
-        g->expected > 0 ? g->expected : x->rows / w->groups / (w->groups > 1 && !g->offsets ? 16 : 1);
+        g->expected > 0 ? g->expected : x->rows / w->groups / (w->groups > 1 && !g->offsets && g->counts ? 16 : 1);
     if (by_pairs(per_group)) {
         if (kSwiglu || a.out_vec) {
             constexpr int kBytes = kSwiglu ? 1 : 2;

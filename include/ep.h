@@ -407,7 +407,7 @@ typedef struct ep_row_groups {
     int32_t per_base;
     int64_t stride;
     int64_t expected; /* rows to expect in a group, for the choice of the kernel's shape alone; 0: the
-                         rows shared out, a packed region filled to a sixteenth */
+                         rows shared out, a region with a count filled to a sixteenth */
 } ep_row_groups;
 
 /* FP8 weights: codes [groups][n][k] e4m3 (contiguous, 16-byte aligned), scales
