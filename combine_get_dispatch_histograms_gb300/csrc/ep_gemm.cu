@@ -769,11 +769,16 @@ static int split_of(int64_t tiles, int kb, int sms) {
     return 1;
 }
 
-// Whether pairs of blocks make the tiles: where they need fewer tiles, by more than the 1.6 times (first product
-// 1.75) that one of theirs costs.  40 groups, us by one block / by pairs, K 2048, N 7168: 64 rows a group 107 /
-// 129, 128 133 / 148, 160 211 / 149, 256 180 / 156, 320 222 / 260, 384 250 / 256, 512 324 / 264, 1024 610 / 494;
-// first product, K 7168, 2I 4096: 64 205 / 256, 160 380 / 293, 320 393 / 519, 512 538 / 495.
-static bool by_pairs(int64_t rows) { return rows > kBM && (rows <= 2 * kBM || rows > 3 * kBM); }
+// Whether pairs of blocks make the tiles: where they need fewer tiles, 1.75 times or better (one of theirs costs 1.6
+// to 1.75).  40 groups, us by one block / by pairs, K 2048, N 7168: 64 rows a group 103 / 128, 128 120 / 141, 256
+// 169 / 148, 320 215 / 262, 384 235 / 258, 448 308 / 260, 512 304 / 266, 576 358 / 375, 640 384 / 389, 704 454 / 391,
+// 896 521 / 502, 1024 587 / 497; first product, K 7168, 2I 4096: 64 200 / 248, 256 300 / 286, 320 381 / 482, 448
+// 548 / 475, 576 646 / 674, 640 643 / 666, 704 774 / 663, 896 880 / 880, 1024 1058 / 902.
+static bool by_pairs(int64_t rows) {
+    if (rows > 0x7fffffff) return true;
+    const int64_t one = (rows + kBM - 1) / kBM, two = (rows + 2 * kBM - 1) / (2 * kBM);
+    return one * 4 >= two * 7;
+}
 
 template <bool kSwiglu>
 static ep_status launch_gemm(const char* fn, const ep_fp8_rows* x, const ep_row_groups* g, const ep_fp8_weight* w,

@@ -24,9 +24,9 @@ def both(x, xs, w, ws, out, hidden, **kw):
 
 @gpu
 @pytest.mark.parametrize("m,form", [(64, "one"), (128, "one"), (129, "pairs"), (256, "pairs"), (257, "one"), (384, "one"), (385, "pairs"),
-                                    (512, "pairs"), (641, "pairs"), (896, "pairs"), (1025, "pairs")])
+                                    (512, "pairs"), (513, "one"), (640, "one"), (641, "pairs"), (896, "pairs"), (1025, "pairs")])
 def test_by_the_rows_of_a_group(m, form):
-    """What the arrays hold, shared out, or what the caller expects."""
+    """What the arrays hold, shared out, or what the caller expects: pairs where they need 1.75 times fewer tiles or better."""
     G, K, N = 40, 256, 1024
     a = arrays(G, (G * m,), K, N)
     cnt = torch.full((G,), m, dtype=torch.int32, device="cuda")
