@@ -506,23 +506,25 @@ class LLBuffer:
             _stream(stream)))
         return o
 
-    def _expected(self) -> int:
-        return max(1, self.R * self.T * self.K // self.E)
+    def _expected(self, n: Optional[int]) -> int:
+        return max(1, self.R * (self.T if n is None else n) * self.K // self.E)
 
-    def expert_swiglu(self, packed: dict, w13, w13_scales, stream=None, out=None):
-        """silu(x wg^T) * (x wu^T) of the received tokens: (codes [E][R*cap][I], scales [E][R*cap][I/128])."""
+    def expert_swiglu(self, packed: dict, w13, w13_scales, stream=None, out=None, n: Optional[int] = None):
+        """silu(x wg^T) * (x wu^T) of the received tokens: (codes [E][R*cap][I], scales [E][R*cap][I/128]).
+
+        n: tokens per rank that were dispatched, where they are a microbatch; it only chooses the kernel's shape."""
         rows = self.R * self.cap
         return expert_swiglu(packed["packed_x"].view(self.E, rows, self.H),
                              packed["packed_scales"].view(self.E, rows, self.H // 128), w13, w13_scales,
                              counts=packed["packed_recv_count"].view(-1), out=out,
-                             status=self.lib.ep_ll_status_word(self._buf), stream=stream, expected_rows=self._expected())
+                             status=self.lib.ep_ll_status_word(self._buf), stream=stream, expected_rows=self._expected(n))
 
-    def expert_gemm(self, h, packed: dict, w, w_scales, stream=None, out=None):
-        """y = h w^T of expert_swiglu's (codes, scales): bf16 [R][L][R*cap][N], with N = H what combine reads."""
+    def expert_gemm(self, h, packed: dict, w, w_scales, stream=None, out=None, n: Optional[int] = None):
+        """y = h w^T of expert_swiglu's (codes, scales): bf16 [R][L][R*cap][N], with N = H what combine reads.  n as there."""
         rows = self.R * self.cap
         y = expert_gemm(h[0], h[1], w, w_scales, counts=packed["packed_recv_count"].view(-1),
                         out=None if out is None else out.view(self.E, rows, -1),
-                        status=self.lib.ep_ll_status_word(self._buf), stream=stream, expected_rows=self._expected())
+                        status=self.lib.ep_ll_status_word(self._buf), stream=stream, expected_rows=self._expected(n))
         return y.view(self.R, self.L, rows, -1)
 
     def combine(self, y_ll, topk_idx, topk_weights, packed: dict, t0: int = 0, n: Optional[int] = None,

@@ -54,3 +54,17 @@ def test_regions(cap, full, counted):
 def test_few_tiles_share_their_k(rows, N, K):
     x, xs, w, ws, out, hidden = arrays(1, (rows,), K, N)
     assert both(x, xs, w[0], ws[0], out, hidden) == "cluster" == form_of(rows, 1, N, K)
+
+
+@gpu
+def test_a_microbatch_expects_its_own_tokens():
+    R, E, K, T, H, I = 4, 8, 2, 256, 256, 512
+    buf = LLBuffer(R, E, K, T, H, T)
+    x, idx = inputs.random_x(R, T, H, 1).cuda(), inputs.random_topk(R, E, K, T, 3).cuda()
+    _, w, ws, y, hidden = arrays(E, (E, R * T), H, 2 * I)[1:]
+    _, w2, w2s, y, _ = arrays(E, (E, R * T), I, 1024)[1:]
+    packed = buf.dispatch(x, idx, 0, 64)
+    for n, form in ((None, "pairs"), (64, "one"), (128, "one"), (200, "pairs")):      # 256, 64, 128, 200 rows an expert
+        assert form_launched(lambda s: buf.expert_swiglu(packed, w, ws, out=hidden, stream=s, n=n)) == form
+        assert form_launched(lambda s: buf.expert_gemm(hidden, packed, w2, w2s, out=y, stream=s, n=n)) == form
+    buf.check()
