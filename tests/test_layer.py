@@ -122,3 +122,42 @@ def test_a_token_of_nothing_but_nan_stays_a_nan():
         assert torch.isnan(out[2, 1]).all() and int(torch.isnan(out).any(-1).sum()) == 1
     ctx.check()
     buf.check()
+
+
+def quantised_reference(layer, E, H, x, idx, v):
+    """The layer of the FP8 forms: x and h through the codec, y rounded to bf16, all else in 64 bits."""
+    from expert_util import rows64
+
+    def codec(r):  # divided by a tensor: torch multiplies by the reciprocal of a number, which moves x's many ties
+        b = r.reshape(r.shape[0], -1, 128)
+        sc = b.abs().amax(-1) / torch.full_like(b[..., 0], 448.0)
+        c = (b / sc[..., None]).clamp(-448, 448).to(torch.float8_e4m3fn)
+        return rows64(c.view(torch.uint8).reshape(r.shape), sc)
+    X = codec(x.view(-1, H).float())
+    J, V = idx.view(-1, idx.shape[-1]), v.view(-1, idx.shape[-1]).double()
+    I = layer.w2.shape[2]
+    ref = torch.zeros_like(X)
+    for e in range(E):
+        t, k = torch.nonzero(J == e, as_tuple=True)
+        y = X[t] @ weight64(layer.w13[e], layer.w13_scales[e]).t()
+        h = codec((silu64(y[:, :I]) * y[:, I:]).float())
+        ref.index_add_(0, t, V[t, k][:, None] * (h @ weight64(layer.w2[e], layer.w2_scales[e]).t()).to(torch.bfloat16).double())
+    return ref.view(x.shape)
+
+
+@gpu
+@pytest.mark.parametrize("R,E,K,T,H,I", [(4, 8, 2, 40, 128, 128), (2, 16, 4, 100, 512, 384)])
+def test_fp8_forms_against_the_quantised_layer(R, E, K, T, H, I):
+    """Both sides round x and h by the codec: what is left is bf16 (2^-9 / sqrt(3) = 1.1e-3 in the mean square, for y and
+    for the output) and codes that round the other way (2^-4 each, one in 10^4 at most: 6e-4).  A scale off by 1 % is
+    seen."""
+    x, v = inputs.random_x(R, T, H, 1).cuda(), inputs.random_weights(R, T, K, 2).cuda()
+    idx = inputs.random_topk(R, E, K, T, 3, mask_p=0.1).cuda()
+    layer, _ = layer_and_reference(E, H, I, x, idx, v, 10)
+    ref = quantised_reference(layer, E, H, x, idx, v)
+    ctx, buf = Context(R, E, K, T, H), LLBuffer(R, E, K, T, H, T)
+    over, low = layer.forward(ctx, x, idx, v), layer.forward_ll(buf, x, idx, v)
+    ctx.check()
+    buf.check()
+    assert far(over, ref) < 4e-3 and far(low, ref) < 4e-3, (far(over, ref), far(low, ref))
+    assert far(1.01 * over.float(), ref) > 4e-3                   # the bound's own strength
