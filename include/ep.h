@@ -92,8 +92,10 @@ ep_status ep_ctx_check(ep_ctx* ctx, void* stream);
  * one: ep_ctx_check then reports their errors too (NULL if ctx is NULL). */
 uint32_t* ep_ctx_status_word(ep_ctx* ctx);
 
-/* Limit, in microseconds, of every bounded device wait of this context
- * (copy-pipeline barriers).  Default 2 000 000. */
+/* Limit, in microseconds, of every bounded device wait of this context's own
+ * calls (copy-pipeline barriers).  Default 2 000 000.  The expert products and
+ * ep_moe_tokens take no context: their waits end after 2 s, also where they
+ * report into its status word. */
 ep_status ep_ctx_set_wait_timeout_us(ep_ctx* ctx, int64_t us);
 
 /* Expert alignment of the permuted layout (default 1 = none; 1..65536, and
