@@ -694,7 +694,8 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
 }
 
 // ---- host -------------------------------------------------------------------------
-static ep_status check_products(const char* fn, const ep_fp8_rows* x, const ep_row_groups* g, const ep_fp8_weight* w) {
+static ep_status check_products(const char* fn, const ep_fp8_rows* x, const ep_row_groups* g, const ep_fp8_weight* w,
+                                const uint32_t* status_out) {
     if (!x || !g || !w) return set_error(EP_ERR_INVALID_ARG, "%s: null descriptor", fn);
     if (w->groups < 1 || w->groups > kMaxGroups)
         return set_error(EP_ERR_INVALID_ARG, "%s: groups %d outside 1..%d", fn, w->groups, kMaxGroups);
@@ -711,6 +712,9 @@ static ep_status check_products(const char* fn, const ep_fp8_rows* x, const ep_r
             return set_error(EP_ERR_INVALID_ARG, "%s: row strides %lld, %lld for %d channels", fn, (long long)x->code_stride,
                              (long long)x->scale_stride, w->k);
     }
+    if (!aligned_to(w->scales, 4) || !aligned_to(x->scales, 4) || !aligned_to(g->counts, 4) || !aligned_to(g->offsets, 4) ||
+        !aligned_to(g->bases, 4) || !aligned_to(status_out, 4))
+        return set_error(EP_ERR_INVALID_ARG, "%s: a pointer is not aligned to its elements", fn);
     if (g->bases && g->per_base < 1) return set_error(EP_ERR_INVALID_ARG, "%s: groups per base %d", fn, g->per_base);
     if (g->stride < 0 || g->expected < 0)
         return set_error(EP_ERR_INVALID_ARG, "%s: group stride %lld, expected rows %lld", fn, (long long)g->stride, (long long)g->expected);
@@ -846,7 +850,7 @@ using namespace ep;
 extern "C" ep_status ep_expert_gemm(const ep_fp8_rows* x, const ep_row_groups* groups, const ep_fp8_weight* w, void* out,
                                     int64_t out_stride, uint32_t* status_out, void* stream) {
     const char* fn = "ep_expert_gemm";
-    const ep_status st = check_products(fn, x, groups, w);
+    const ep_status st = check_products(fn, x, groups, w, status_out);
     if (st != EP_OK) return st;
     if (x->rows == 0) return EP_OK;
     if (!out || out_stride < w->n) return set_error(EP_ERR_INVALID_ARG, "%s: output stride %lld for %d channels", fn, (long long)out_stride, w->n);
@@ -865,12 +869,12 @@ extern "C" ep_status ep_expert_swiglu(const ep_fp8_rows* x, const ep_row_groups*
                                       int64_t out_stride, float* out_scales, int64_t out_scale_stride,
                                       uint32_t* status_out, void* stream) {
     const char* fn = "ep_expert_swiglu";
-    const ep_status st = check_products(fn, x, groups, w13);
+    const ep_status st = check_products(fn, x, groups, w13, status_out);
     if (st != EP_OK) return st;
     if (w13->n % 256) return set_error(EP_ERR_INVALID_ARG, "%s: %d weight rows (gate and up, each a multiple of 128)", fn, w13->n);
     if (x->rows == 0) return EP_OK;
     const int inter = w13->n / 2;
-    if (!out || !out_scales || !aligned16(out) || out_stride < inter || out_stride % 16 || out_scale_stride < inter / 128)
+    if (!out || !out_scales || !aligned16(out) || !aligned_to(out_scales, 4) || out_stride < inter || out_stride % 16 || out_scale_stride < inter / 128)
         return set_error(EP_ERR_INVALID_ARG, "%s: output rows (16-byte aligned, strides %lld, %lld) for %d channels", fn,
                          (long long)out_stride, (long long)out_scale_stride, inter);
     GemmArgs a{};

@@ -42,6 +42,7 @@ ep_status cuda_error(cudaError_t e, const char* what);
     } while (0)
 ep_status status_from_flags(uint32_t flags);
 bool aligned16(const void* p);
+inline bool aligned_to(const void* p, unsigned bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
 
 // ---- geometry of the token tiles (layout / notify) -------------------------
 // Channel c owns tokens [c*ct, min(T, (c+1)*ct)), ct = ceil(T / C); each channel

@@ -952,6 +952,9 @@ extern "C" ep_status ep_moe_tokens(const void* x, int64_t x_stride, int32_t num_
     if (num_tokens == 0) return EP_OK;
     if (!x || !topk_idx || !topk_weights || !out || !w->w13 || !w->w2 || !aligned16(x) || !aligned16(w->w13) || !aligned16(w->w2))
         return set_error(EP_ERR_INVALID_ARG, "%s: null or unaligned (16 bytes: x, weights) pointer", fn);
+    if (!aligned_to(topk_idx, 8) || !aligned_to(topk_weights, 4) || !aligned_to(out, 2) || !aligned_to(w->w13_scales, 4) ||
+        !aligned_to(w->w2_scales, 4) || !aligned_to(status_out, 4))
+        return set_error(EP_ERR_INVALID_ARG, "%s: a pointer is not aligned to its elements", fn);
     if (x_stride < H || x_stride % 8 || out_stride < H)
         return set_error(EP_ERR_INVALID_ARG, "%s: row strides %lld (a multiple of 8), %lld for %d channels", fn, (long long)x_stride,
                          (long long)out_stride, H);

@@ -499,3 +499,24 @@ def test_activation_over_its_range():
         d = (scales.double() * 448 - h).abs()
         lim = (8 + g.clamp(max=0).abs() + 1) * 2.0 ** -23 * h + torch.where(g < -87, 88 * 2.0 ** -126 * s[:n, None].double(), 0.0) + 1e-43
         assert (d <= lim).all(), f"{shape}: worst {float((d / lim).max()):.3g} of the bound"
+
+
+def test_c_refuses_pointers_off_their_elements():
+    """A count, an offset or a scale off its 4 bytes would be a misaligned address on the GPU."""
+    import ctypes
+    from combine_get_dispatch_histograms_gb300 import _lib
+    lib = _lib.load()
+
+    def call(fn="gemm", xs=256, ws=256, counts=256, offsets=256, bases=None, out=256, out_scales=256, status=256):
+        x = _lib.EpFp8Rows(256, 128, xs, 1, 4)
+        g = _lib.EpRowGroups(counts, offsets, bases, 1, 4, 0)
+        w = _lib.EpFp8Weight(256, ws, 1, 256, 128)
+        p = [ctypes.byref(a) for a in (x, g, w)]
+        if fn == "gemm":
+            return lib.ep_expert_gemm(*p, out, 256, status, None)
+        return lib.ep_expert_swiglu(*p, out, 128, out_scales, 1, status, None)
+    for fn in ("gemm", "swiglu"):
+        for bad in (dict(xs=258), dict(ws=257), dict(counts=258), dict(offsets=257), dict(bases=258), dict(status=259), dict(out=257)):
+            assert call(fn, **bad) == -1, (fn, bad)
+            assert b"align" in lib.ep_last_error() or b"output" in lib.ep_last_error()
+    assert call("swiglu", out_scales=258) == -1

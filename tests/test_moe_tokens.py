@@ -305,3 +305,16 @@ def test_every_refused_size_needs_no_workspace_on_a_gpu():
     assert size() > 0 and size(fp8=False, H=32, I=160) > 0 and size(T=64, K=32, E=4096) > 0
     for bad in (dict(T=65), dict(T=0), dict(K=33), dict(E=4097), dict(H=160), dict(I=64), dict(H=48, fp8=False), dict(H=1 << 29)):
         assert size(**bad) == 0, bad
+
+
+@pytest.mark.parametrize("bad", ["topk_idx", "topk_weights", "out", "w13_scales", "w2_scales", "status"])
+def test_c_refuses_pointers_off_their_elements(bad):
+    from combine_get_dispatch_histograms_gb300 import _lib
+    lib = _lib.load()
+    at = {n: 256 + (1 if n == bad else 0) for n in ("topk_idx", "topk_weights", "out", "w13_scales", "w2_scales", "status")}
+    if bad == "topk_idx":
+        at[bad] = 260                    # a multiple of 4, not of 8
+    w = _lib.EpMoeWeights(256, at["w13_scales"], 256, at["w2_scales"], 4, 128, 128)
+    assert lib.ep_moe_tokens(256, 128, 1, at["topk_idx"], at["topk_weights"], 1, ctypes.byref(w), at["out"], 128, 256, 1 << 30,
+                             at["status"], None) == -1
+    assert b"aligned to its elements" in lib.ep_last_error()
