@@ -394,7 +394,9 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
                     __syncwarp();
                 }
             }
-            if (elect_one()) mma_commit<kCtas>(smem_u32(&sh.drain));  // every product has finished before tensor memory is freed
+            // every product has finished before either block frees its tensor memory or ends: the second block waits
+            // for this one below, and nothing arrives on its own barrier, which would have to outlive the arrival
+            if (elect_one()) mma_commit_here<kCtas>(smem_u32(&sh.drain));
             __syncwarp();
             mbar_wait_bounded(&sh.drain, 0, kGemmWaitNs);
         }
@@ -680,12 +682,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
     __syncwarp();
     tc_fence_before();
     __syncthreads();
-    if constexpr (kCtas == 2) {
-        // the last commit arrives in both blocks: the second one, too, lives until it has
-        if (rank == 1 && warp == 1) mbar_wait_bounded(&sh.drain, 0, kGemmWaitNs);
-        __syncwarp();
-        cluster_sync();
-    }
+    if (kCtas == 2) cluster_sync();
     tc_fence_after();
     if (warp == 2) tmem_free<kCtas>(tmem, 512);
     if (tid == 0 && *abort && a.status) flag(a.status, FLAG_TIMEOUT);

@@ -249,6 +249,14 @@ __device__ __forceinline__ void mma_commit(uint32_t bar) {
     else
         asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
+// The same on the barrier of the issuing block alone.
+template <int kCtas>
+__device__ __forceinline__ void mma_commit_here(uint32_t bar) {
+    if constexpr (kCtas == 2)
+        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+    else
+        asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
 // Consecutive columns of this warp's 32 lanes: thread i gets lane i's row.
 __device__ __forceinline__ void tmem_ld(uint32_t addr, float (&v)[32]) {
     uint32_t* r = reinterpret_cast<uint32_t*>(v);
