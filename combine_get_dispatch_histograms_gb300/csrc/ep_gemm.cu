@@ -61,7 +61,7 @@ constexpr int kTileRing = 4;            // tiles announced ahead
 constexpr int kScaleChunk = 8;          // blocks of K whose scales are staged together
 constexpr int kScaleRing = 2;
 constexpr int kMaxGroups = 4096;
-constexpr int kMaxTiles = 0x7fffffff - 65536;  // a block's next tile, one grid further on, stays within 31 bits
+constexpr int kMaxTiles = 1 << 25;      // 32 groups' tiles, and a block's next tile, stay within 31 bits; no memory holds more
 constexpr int kChunkRows = 2048;       // rows that share a pass over the weight's tiles
 constexpr int kSplitStride = kBN + 4;  // floats of a row of sums: rows fall into other banks
 constexpr int64_t kGemmWaitNs = 2000000000ll;
@@ -150,16 +150,12 @@ struct RingPos {
 template <int kTileM>
 struct TileWalk {
     static constexpr int kChunkM = kChunkRows / kTileM;
-    int g0 = -32;
-    uint32_t start = 0, sum = 0;       // first tile of a batch of groups, its tiles
-    uint32_t inc;                      // tiles up to and with this lane's group
-    int rows, first;                   // its rows, first row
+    int g0 = -32, start = 0, sum = 0;  // batch of groups, its first tile, its tiles
+    int inc, tiles, rows, first;       // this lane's group: tiles up to and with it, tiles, rows, first row
     bool cut = false;
 
-    // false: no tile t.  Groups that overlap may have any number of tiles: those past a.most are cut off, and
-    // sums that would pass 31 bits stay there, above every t.
-    __device__ __forceinline__ bool find(const GemmArgs& a, int unit_tile, int lane, GemmTile* out) {
-        const uint32_t t = min(unit_tile, a.most);
+    // false: no tile t.  A group has at most kMaxTiles tiles, and t is no larger, so that no sum passes 31 bits.
+    __device__ __forceinline__ bool find(const GemmArgs& a, int t, int lane, GemmTile* out) {
         while (t >= start + sum) {
             start += sum;
             g0 += 32;
@@ -171,21 +167,17 @@ struct TileWalk {
             const int g = g0 + lane;
             rows = g < a.G ? group_rows(a, g, &cut) : 0;
             first = rows ? (int)group_first(a, g) : 0;
-            inc = (uint32_t)((rows + kTileM - 1) / kTileM * a.n_tiles);
+            tiles = (rows + kTileM - 1) / kTileM * a.n_tiles;
+            inc = tiles;
             for (int o = 1; o < 32; o <<= 1) {
-                const uint32_t v = __shfl_up_sync(0xffffffffu, inc, o);
-                if (lane >= o) inc = min(inc + v, 0x7fffffffu);
+                const int v = __shfl_up_sync(0xffffffffu, inc, o);
+                if (lane >= o) inc += v;
             }
             sum = __shfl_sync(0xffffffffu, inc, 31);
         }
-        if (t == (uint32_t)a.most) {
-            cut = true;
-            return false;
-        }
         const int src = __ffs(__ballot_sync(0xffffffffu, t < start + inc)) - 1;
         const int n = __shfl_sync(0xffffffffu, rows, src);
-        const uint32_t before = __shfl_sync(0xffffffffu, inc, src > 0 ? src - 1 : 0);
-        int r = (int)(t - start - (src > 0 ? before : 0));
+        int r = t - start - __shfl_sync(0xffffffffu, inc - tiles, src);
         const int mt = (n + kTileM - 1) / kTileM, chunk = r / (kChunkM * a.n_tiles);
         r -= chunk * kChunkM * a.n_tiles;
         const int m0 = chunk * kChunkM, mc = min(kChunkM, mt - m0), m = m0 + r % mc;
@@ -267,7 +259,9 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
             RingPos<kScaleRing> sr;
             for (int t = unit;; t += units) {
                 GemmTile tile = {0, 0, 0, 0};
-                const bool some = walk.find(a, t, lane, &tile);
+                // groups that overlap may have any number of tiles: those past a.most are cut off
+                const bool some = walk.find(a, min(t, a.most), lane, &tile);
+                if (t >= a.most) tile.rows = 0;
                 mbar_wait_warp<true>(tr.bar(tile_empty), tr.phase() ^ 1, kGemmWaitNs, abort);
                 if (__any_sync(0xffffffffu, *abort)) break;
                 if (lane == 0) {
@@ -275,7 +269,10 @@ gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
                     mbar_arrive(tr.bar(tile_full));
                 }
                 ++tr.n;
-                if (!some) break;
+                if (!some || t >= a.most) {
+                    walk.cut |= some;
+                    break;
+                }
                 const int mine = min(tile.rows - rank * kBM, kBM);
                 // lanes 0-7 and 8-15: the weight blocks' scales of a chunk
                 const int b0 = kSwiglu ? tile.n : tile.n * 2;

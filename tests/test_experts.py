@@ -438,37 +438,41 @@ def test_groups_that_overlap_are_cut_and_flagged(form, G, rows, K, N, expected):
 
 
 def test_tile_walk_stays_within_31_bits():
-    """The walk's arithmetic, restated: groups that claim every row, with more than 2^31 tiles in all."""
-    def walk(tiles, most, unit, units, u32=1 << 32):
-        """(group, tile of the group) that `unit` takes, as the kernel's warp does with 32-bit sums."""
+    """The walk's arithmetic, restated: groups that claim every row, with far more than 2^31 tiles in all, at the most
+    tiles that the host lets through; and groups that share none."""
+    most_tiles = 1 << 25
+
+    def walk(tiles, most, unit, units):
+        """(group, tile of the group) that `unit` takes, and whether tiles were cut off; no sum may pass 31 bits."""
         start = total = 0
         g0, inc, got, t = -32, [], [], unit
         while True:
             at = min(t, most)
-            while at >= (start + total) % u32:
-                start = (start + total) % u32
+            while at >= start + total:
+                start += total
                 g0 += 32
                 if g0 >= len(tiles):
                     return got, False
                 inc, run = [], 0
                 for v in (tiles[g0:g0 + 32] + [0] * 32)[:32]:
-                    run = min(run + v, 0x7FFFFFFF)
+                    run += v
                     inc.append(run)
                 total = inc[-1]
-            if at == most:
+                assert start + total < 1 << 31
+            if t >= most:
                 return got, True
             src = next(i for i in range(32) if at < start + inc[i])
             got.append((g0 + src, at - start - (inc[src - 1] if src else 0)))
             t += units
             assert t < 1 << 31
-    most = 0x7FFFFFFF - 65536
-    huge = [most // 2 + 7] * 4096
+    huge = [most_tiles] * 4096
     units = 60000                        # a grid has fewer blocks than this
     for unit in (0, 1, units - 1):
-        got, cut = walk(huge, most, unit, units)
-        assert cut and len(got) == len(range(unit, most, units))
-        for i, (g, r) in enumerate(got):
-            assert 0 <= r < huge[g] and g * huge[0] + r == unit + i * units
+        got, cut = walk(huge, most_tiles, unit, units)
+        assert cut and got == [(0, t) for t in range(unit, most_tiles, units)]
+    parts = [most_tiles // 100 + 3] * 200
+    got, cut = walk(parts, most_tiles, 5, units)
+    assert cut and [g * parts[0] + r for g, r in got] == list(range(5, most_tiles, units))
     fine = [3, 0, 5, 0] * 100
     seen = sorted(p for unit in range(7) for p in walk(fine, sum(fine), unit, 7)[0])
     assert seen == [(g, r) for g, n in enumerate(fine) for r in range(n)]
