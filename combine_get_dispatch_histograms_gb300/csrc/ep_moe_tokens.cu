@@ -1,6 +1,6 @@
 // ep_moe_tokens.cu -- a whole mixture-of-experts layer for up to 64 tokens, in
-// two kernels (and two small ones above 16 tokens), without the dispatch /
-// permute / combine round trip.
+// two kernels (and two small ones above 16 tokens or for large layers), without
+// the dispatch / permute / combine round trip.
 //
 // Mathematics.  For token t with choices e = topk_idx[t][k], weights v[t][k]:
 //   h[t,e] = silu(Wg[e] x[t]) * (Wu[e] x[t]),   out[t] = sum_k v[t][k] * W2[e] h[t,e].
@@ -26,8 +26,8 @@
 // (two bf16) were off by up to 2^-21 of the largest and 2^-13 of h, which outputs
 // that cancel show, and took 71 us where these take 76 (one token), 694 / 754 (64
 // tokens), 417 / 418 (bf16).
-// Up to 16 tokens each block converts what it needs; for more, whose experts'
-// blocks would repeat much of it, the pieces are made once beforehand.
+// For few tokens of a small layer each block converts what it needs; otherwise,
+// where blocks would repeat much of it, the pieces are made once beforehand.
 // A block of 128 channels is one accumulator; it leaves tensor memory, times its
 // weight scale and the tokens' powers of two, for an fp32 sum in registers.
 //
@@ -778,13 +778,18 @@ __global__ void __launch_bounds__(kTokThreads, 1) tok_kernel(const __grid_consta
     if (tid == 0 && *abort && a.status) flag(a.status, FLAG_TIMEOUT);
 }
 
-// Whether the pieces are made beforehand: two launches and their hand-over, about 4 us, against a conversion
-// by every block that meets the token (us, by each block / beforehand).  fp8, 128 experts, top-8, H 7168,
-// I 2048: 8 tokens 377 / 376, 16 553 / 547, 32 734 / 722, 64 951 / 858, skewed 774 / 563; 16 experts, top-2,
-// H 4096, I 1408: 8 tokens 54 / 56, 16 71 / 74, 24 84 / 81, 64 131 / 110.  bf16 halves only h: 16 experts, 32
-// tokens 128 / 126, 64 171 / 148; 75 experts, top-6, 64 tokens 427 / 435.  (All with the tiles' parts still
-// added 16 loads at a time by 128 threads, up to 40 us more than now, on both sides.)
-static bool tok_formed(int T, int K, int E, bool fp8) { return T > kTokSlots && (fp8 || T * K >= 6 * E); }
+// Whether the pieces are made beforehand: two launches and their hand-over, 4 to 5 us of the host's time or of a
+// short call's, against a conversion by every block that meets the token (us, by each block / beforehand).  fp8, 128
+// experts, top-8, H 7168, I 2048: one token 74.8 / 71.4, 8 373 / 366, 16 569 / 558, 32 780 / 759, 64 986 / 861, skewed
+// 942 / 605; 32 experts, top-4, H 2048, I 768: 2 24.7 / 26.8, 8 39.4 / 38.3, 16 52.4 / 48.2; 16 experts, top-2, H 4096,
+// I 1408: 1 23.9 / 26.7, 2 30.1 / 31.0, 4 38.5 / 37.9, 16 64.7 / 60.8, 64 129 / 83; H 2048, I 768: 8 27.4 / 28.2, 16
+// 32.9 / 33.0, 17 35.5 / 34.9; 8 experts, H 1024, I 512: 16 22.5 / 26.0, 17 25.0 / 25.7, 32 35.4 / 27.5.  So above 16
+// tokens, and where the chosen experts' weights have 100 MB, so that the call hides the launches.  bf16 halves only h:
+// 16 experts, 17 tokens 95.5 / 98.1, 32 114 / 108, 64 142 / 117; 75 experts, top-6, 64 tokens 404 / 410.
+static bool tok_formed(int T, int K, int E, int H, int I, bool fp8) {
+    if (!fp8) return T > kTokSlots && T * K >= 6 * E;
+    return T > kTokSlots || (int64_t)(E < T * K ? E : T * K) * H * I >= 100000000 / 3;
+}
 
 // Entries of the expert list, at most: one for each expert that is chosen, and one more for every kTokSlots pairs.
 static int tok_list(int T, int K, int E) { return (E < T * K ? E : T * K) + T * K / kTokSlots; }
@@ -807,7 +812,7 @@ static TokWorkspace tok_workspace(int T, int K, int E, int H, int I, bool fp8, i
     w.part = up((int64_t)w.split * T * K * 2 * I * 4);
     w.done = w.part + up((int64_t)sms * 2 * T * kTokRows * 4);
     w.formed_x = w.formed_h = w.powers = w.bytes = w.done + up((int64_t)((H + kTokRows - 1) / kTokRows + 1) * 4);
-    if (tok_formed(T, K, E, fp8)) {
+    if (tok_formed(T, K, E, H, I, fp8)) {
         const int64_t blocks_x = fp8 ? (int64_t)T * blocks_k : 0;
         const int64_t blocks_h = (int64_t)T * K * ((I * (fp8 ? 1 : 2) + kTokBytes - 1) / kTokBytes);
         w.formed_h = w.formed_x + blocks_x * TokShape<false, true>::kPieces * kTokBytes;
@@ -874,7 +879,7 @@ static ep_status launch_tokens(TokArgs a, const ep_moe_weights* w, int sms, cons
         return c;
     };
     auto at_most = [](int64_t n, int64_t most) { return n < most ? n : most; };
-    const bool formed = tok_formed(a.T, a.K, a.E, kFp8);
+    const bool formed = tok_formed(a.T, a.K, a.E, a.H, a.I, kFp8);
     const auto c1 = config(at_most(items1, sms), kTokThreads, tok_smem<false, kFp8>(a.T, a.K, a.list));
     if (kFp8 && formed) {
         a.formed = mem + ws.formed_x;

@@ -463,7 +463,7 @@ typedef struct ep_moe_weights {
  * scales are read. */
 int64_t ep_moe_tokens_workspace(int32_t num_tokens, int32_t num_topk, const ep_moe_weights* w);
 
-/* A whole layer for 0..64 tokens, in two kernels (above 16 tokens up to two small ones more):
+/* A whole layer for 0..64 tokens, in two kernels (above 16 tokens and for large layers up to two small ones more):
  *   out[t] = bf16( sum over k of w[t][k] * W2[e] ( silu(Wg[e] x[t]) * (Wu[e] x[t]) ) ),  e = topk_idx[t][k],
  * x and out bf16 rows, strides in elements (x 16-byte aligned, x_stride a
  * multiple of 8).  Every sum is fp32, and x and h enter the products with the

@@ -318,3 +318,32 @@ def test_c_refuses_pointers_off_their_elements(bad):
     assert lib.ep_moe_tokens(256, 128, 1, at["topk_idx"], at["topk_weights"], 1, ctypes.byref(w), at["out"], 128, 256, 1 << 30,
                              at["status"], None) == -1
     assert b"aligned to its elements" in lib.ep_last_error()
+
+
+@gpu
+@pytest.mark.parametrize("T,K", [(1, 8), (4, 8), (5, 7), (16, 3), (15, 8)])
+def test_few_tokens_of_a_large_layer(T, K):
+    """100 MB of weights: the pieces are made beforehand for fewer than 17 tokens too, with short and long lists."""
+    from expert_shapes import launches
+    E, H, I = 12, 2048, 2176
+    g = gen(T * 10 + K)
+    w = weights(E, H, I, "fp8", g)
+    x = randn((T, H), g).to(torch.bfloat16)
+    idx, v = routing(T, E, K, g, mask=0.1 if T > 1 else 0.0)
+    out, ws = torch.empty(T, H, dtype=torch.bfloat16, device="cuda"), torch.empty(
+        ep.moe_tokens_workspace(T, K, E, H, I), dtype=torch.uint8, device="cuda")
+    names = [n for n, _ in launches(lambda s: ep.moe_tokens(x, idx, v, w[0], w[2], w[1], w[3], out=out, workspace=ws, stream=s))]
+    assert ["form_kernel" in n for n in names] == [True, False, True, False], names
+    clean = check(x, idx, v, w)
+    if T > 1:
+        x[0, 3] = float("nan")
+        out = ep.moe_tokens(x, idx, v, w[0], w[2], w[1], w[3])
+        assert torch.isnan(out[0]).all() or (idx[0] < 0).all()
+        assert torch.equal(out[1:].view(torch.int16), clean[1:].view(torch.int16))
+        idx[1] = -1                      # other routing, another order of the sums
+        out = ep.moe_tokens(x, idx, v, w[0], w[2], w[1], w[3])
+        assert (out[1].view(torch.int16) == 0).all()
+        x[0] = 1.0
+        check(x, idx, v, w)
+    idx[:] = -1
+    assert (ep.moe_tokens(x, idx, v, w[0], w[2], w[1], w[3]).view(torch.int16) == 0).all()
