@@ -14,18 +14,24 @@
 // products, one announces tiles and stages scales, 16 add; each has what it
 // needs in shared memory and none waits for global memory in the loop over K.
 //
-// Bound.  With long groups the round trip of the two accumulators.  A block of K
-// costs the tensor cores 517 cycles (128 x 256 x 128 of each SM), but takes 860:
-// a warp adds for about 600 of them (365 while no products run; 292 are the
-// 32,768 multiply-adds), hands its accumulator back half way through, and waits
-// 220 for the next one, which could not start before.  A third accumulator has
-// no room, nor have the registers for loading all of one before adding it; halves
-// handed back on their own (two issuing warps) read the rows' tile twice from
-// shared memory and are slower (1163 -> 1305 us, K 8192).  Sustained, power: 1360
-// of 1400 W, and the clock falls to 1.7 - 1.76 GHz.  Measured: 2.25 PFLOP/s (262144 rows,
-// K 2048, N 7168, 256 groups: 3.42 ms), 2.43 PFLOP/s (first product, K 4096,
-// 2I 2816).  With short groups the weights' bytes: 64 rows a group run at
-// 6.6 TB/s (second product 0.61 ms, first 1.14 ms of 256 groups).
+// Bound.  With long groups not the tensor cores: a block of K takes them 517
+// cycles (128 x 256 x 128 of each SM) and the kernel 860 to 1000, by the clock that
+// power leaves.  What holds it there is not settled.  The adding takes its share:
+// a warp adds for about 600 cycles (365 while no products run; 292 are the 32,768
+// multiply-adds), hands its accumulator back half way through, and waits 220 for
+// the next one; a third accumulator has no room, nor have the registers for loading
+// all of one before adding it.  But a variant that read no accumulator and handed
+// each back at once kept 88 % of the time (K 8192: 964 us of 1099, 882 cycles a
+// block of 1005 at the same clock), so that the copies (32 KB per SM and block,
+// 11.7 TB/s out of the second-level cache at that rate) or the issue of both must
+// come close to it.  Halves of the tile handed back on their own (two issuing warps)
+// read the rows' tile twice from shared memory and are slower (1163 -> 1305 us).
+// The warps with 32 registers spill some 130 to 140 bytes.  Sustained, power: 1360
+// of 1400 W, and the clock falls to 1.7 - 1.76 GHz.  Measured: second product, 262144
+// rows, K 2048, N 7168, 256 groups, 3.42 ms from a cool start (2.25 PFLOP/s) and
+// 3.74 sustained (2.06); first product, 498304 rows, K 4096, 2I 2816, 4.41 ms (2.6)
+// and 4.84 (2.4).  With short groups the weights' bytes: 64 rows a group run at
+// 6.6 TB/s (second product 0.60 ms, first 1.13 ms of 256 groups).
 #include <atomic>
 #include <initializer_list>
 

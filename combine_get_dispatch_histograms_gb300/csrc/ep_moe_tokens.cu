@@ -24,8 +24,7 @@
 //   bf16 weights: x itself, and h as the sum of three bf16, which are its 24 bits.
 // So the sums add x and h as a 32-bit form does.  Two pieces of x and three of h
 // (two bf16) were off by up to 2^-21 of the largest and 2^-13 of h, which outputs
-// that cancel show, and took 71 us where these take 76 (one token), 694 / 754 (64
-// tokens), 417 / 418 (bf16).
+// that cancel show; 64 tokens took 694 us with them and take 754, bf16 417 / 418.
 // For few tokens of a small layer each block converts what it needs; otherwise,
 // where blocks would repeat much of it, the pieces are made once beforehand.
 // A block of 128 channels is one accumulator; it leaves tensor memory, times its
@@ -35,11 +34,9 @@
 // (128 output channels, expert, block of K) in kernel 2; each thread block takes
 // its share, equal to within one.
 //
-// Measured: one token of 8 experts (H 7168, I 2048, fp8) 69 us: kernel 1 streams
-// for 37 of them at 6.3 TB/s, the hand-over between the kernels leaves the memory
-// idle for 2.5, the ends of the blocks' shares and their joining take 5.  17
-// tokens, 75 experts, bf16 (H 4096, I 1408) 422 us, 6.2 TB/s; 64 tokens, 99 experts
-// 720 us (954 when every block converted its tokens itself).
+// Measured: one token of 8 experts (H 7168, I 2048, fp8) 71 us, of which the
+// weights' bytes take 53; 17 tokens, 75 experts, bf16 (H 4096, I 1408) 425 us, 6.1
+// TB/s; 64 tokens, 99 experts 750 to 790 us, by its routing.
 #include <atomic>
 
 #include "ep_fp8.cuh"

@@ -5,7 +5,7 @@
     out = layer.forward_ll(buf, x, topk_idx, topk_weights)      # over a low-latency LLBuffer
 
 forward chooses by the number of tokens in all: up to FEW_TOKENS run as
-moe_tokens (two kernels, activations in bf16); more are quantised and dispatched
+moe_tokens (two to four kernels, x in bf16); more are quantised and dispatched
 into the per-expert blocks, run through the two expert products and combined.
 Neither form waits on the host, so each can be captured in a CUDA graph.
 """
