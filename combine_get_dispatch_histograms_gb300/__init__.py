@@ -17,6 +17,9 @@ binding without the built library (or without a GPU) raises.
     pk = ll.dispatch(x, topk_idx)                            # FP8, no host sync
     out = ll.combine(y_ll, topk_idx, topk_weights, pk)
 
+What comes before: rms_norm (x and its FP8 rows), route (topk_idx and
+topk_weights from router logits), balance_loss and the gradients of all three.
+
 The experts between them: expert_swiglu and expert_gemm (methods of both, on
 FP8 rows and e4m3 weights), and moe_tokens, a whole layer for up to 64 tokens;
 layer.MoELayer runs them together.
@@ -32,8 +35,12 @@ from . import _lib
 from ._lib import EpConfig, EpDispatchHandle, EpError, check
 
 from .experts import check_status, expert_gemm, expert_swiglu, fp8_row_views, moe_tokens, moe_tokens_workspace, new_status
+from .norm import rms_norm, rms_norm_backward, rms_norm_backward_workspace
+from .router import balance_loss, balance_loss_workspace, route, router_backward
 
 __all__ = ["Context", "LLBuffer", "EpError", "load_library", "ll_size_hint", "ll_message_bytes",
+           "rms_norm", "rms_norm_backward", "rms_norm_backward_workspace",
+           "route", "balance_loss", "balance_loss_workspace", "router_backward",
            "expert_gemm", "expert_swiglu", "fp8_row_views", "moe_tokens", "moe_tokens_workspace", "new_status", "check_status"]
 
 
@@ -155,6 +162,16 @@ class Context:
         (from the next notify on); padding rows are left unwritten."""
         check("ep_ctx_set_expert_alignment", self.lib.ep_ctx_set_expert_alignment(self._ctx, int(alignment)))
         self.expert_alignment = int(alignment)
+
+    # ---- routing ---------------------------------------------------------------
+    def route(self, logits: torch.Tensor, stream=None, out=None, topk_nodes: Optional[int] = None, **how):
+        """(topk_idx, topk_weights) [R][T][K] of router logits [R][T][E], as router.route.  topk_nodes: each token's experts on
+        that many of the N nodes at most, so that the node-wise dispatch sends so many copies."""
+        if logits.shape != (self.R, self.T, self.E):
+            raise ValueError(f"Context.route: logits {(self.R, self.T, self.E)}: got {tuple(logits.shape)}")
+        if topk_nodes is not None:
+            how.update(groups=self.N, topk_groups=topk_nodes)
+        return route(logits, self.K, stream=stream, out=out, **how)
 
     # ---- layout ----------------------------------------------------------------
     def get_dispatch_layout(self, topk_idx: torch.Tensor, nodes: Optional[bool] = None, stream=None, out=None):

@@ -14,6 +14,7 @@ from . import build as _build
 P = ctypes.c_void_p
 I32 = ctypes.c_int32
 I64 = ctypes.c_int64
+F32 = ctypes.c_float
 INT = ctypes.c_int
 
 EP_OK = 0
@@ -51,6 +52,11 @@ class EpMoeWeights(ctypes.Structure):
                 ("inter", I32)]
 
 
+class EpRouter(ctypes.Structure):
+    _fields_ = [("tokens", I64), ("experts", I32), ("topk", I32), ("logits_type", I32), ("scoring", I32), ("normalize", I32),
+                ("groups", I32), ("topk_groups", I32), ("scale", F32)]
+
+
 # name -> (restype, argtypes); every name here is declared in include/ep.h
 SIGNATURES = {
     "ep_last_error": (ctypes.c_char_p, []),
@@ -86,6 +92,14 @@ SIGNATURES = {
     "ep_expert_swiglu": (INT, [P, P, P, P, I64, P, I64, P, P]),
     "ep_moe_tokens_workspace": (I64, [I32, I32, P]),
     "ep_moe_tokens": (INT, [P, I64, I32, P, P, I32, P, P, I64, P, I64, P, P]),
+    "ep_rms_norm": (INT, [P, I64, P, I64, I32, P, I32, F32, I64, I32, P, I64, P, I64, P, I64, P]),
+    "ep_rms_norm_backward_workspace": (I64, [I64, I32]),
+    "ep_rms_norm_backward": (INT, [P, I64, P, I64, I32, P, I32, F32, P, I64, I64, I32, P, I64, P, P, I64, P]),
+    # the router's descriptor by address, as above
+    "ep_route": (INT, [P, P, I64, P, P, P, P, P]),
+    "ep_balance_loss_workspace": (I64, [P, I32]),
+    "ep_balance_loss": (INT, [P, P, I64, P, I32, F32, P, P, P, P, I64, P, P]),
+    "ep_router_backward": (INT, [P, P, I64, P, P, P, I32, P, P, I64, P, P]),
     "ep_ll_message_bytes": (I64, [INT]),
     "ep_ll_size_hint": (I64, [INT, INT, INT, INT]),
     "ep_ll_buffer_create": (INT, [ctypes.POINTER(EpConfig), INT, ctypes.POINTER(P)]),

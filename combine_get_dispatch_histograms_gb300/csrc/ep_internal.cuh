@@ -35,6 +35,11 @@ ep_status cuda_error(cudaError_t e, const char* what);
         cudaError_t e__ = (call);                                       \
         if (e__ != cudaSuccess) return ::ep::cuda_error(e__, #call);    \
     } while (0)
+#define EP_TRY(call)                                                    \
+    do {                                                                \
+        const ep_status st__ = (call);                                  \
+        if (st__ != EP_OK) return st__;                                 \
+    } while (0)
 #define EP_CHECK_LAUNCH(what)                                           \
     do {                                                                \
         cudaError_t e__ = cudaGetLastError();                           \
@@ -229,5 +234,21 @@ ep_status dispatch_permuted_rows(ep_ctx* c, const void* x, int64_t row_bytes, co
 
 // ---- launch helpers -------------------------------------------------------------
 inline cudaStream_t as_stream(void* s) { return reinterpret_cast<cudaStream_t>(s); }
+
+// A kernel that may start while the one before drains: it calls grid_wait before its first access to memory.
+template <typename... Params, typename... Args>
+ep_status launch_next(void (*kernel)(Params...), int64_t blocks, int threads, void* stream, const Args&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)blocks);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.stream = as_stream(stream);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    EP_CUDA(cudaLaunchKernelEx(&cfg, kernel, args...));
+    return EP_OK;
+}
 
 }  // namespace ep

@@ -1,0 +1,646 @@
+// ep_router.cu -- the router around dispatch: logits to topk_idx and topk_weights, the balance loss
+// with its per-expert counts, and the gradient of the logits.
+//
+// A warp per token.  Lane i holds experts i V .. i V + V - 1 of the row in registers, so that the lowest
+// expert of equal ones is the first of the lowest lane.
+//
+// Choice.  key = fp32(logit + bias), compared as integers in the same order (NaN the largest, -inf and
+// closed groups 0 = never chosen); top-k by repeated maxima: a warp-wide maximum of the lanes' best, whose
+// first owner gives up its first expert of that key.  Lane k keeps choice k.
+//
+// Balance.  With c_se the choices of expert e in sequence s, m_s = sum_e c_se, n_s the tokens that chose:
+//   F_se = coef E c_se / (S m_s n_s),   loss = sum_s sum_e F_se sum_t q_ste,   q: softmax, or sigmoid / its sum
+// F is held constant in the gradient, and sum_e q_e = 1, so that F less its mean over e gives the same
+// gradient; F - mean = coef (E c_se - m_s) / (S m_s n_s) is formed from integers, and keeps its bits where
+// the load is nearly balanced.
+//   softmax:  dl_e = q_e (F_e - sum_j F_j q_j);   sigmoid (p, p' = p (1 - p)):  dl_e = p'_e (F_e - sum_j F_j q_j) / sum p
+#include <climits>
+
+#include "ep_tcgen05.cuh"
+
+namespace ep {
+
+constexpr int kRouterThreads = 256, kRouterWarps = kRouterThreads / 32;
+constexpr int kRouterMaxExperts = 1024, kRouterMaxGroups = 32;
+constexpr uint32_t kKeyNegInf = 0x007fffffu;  // the ordered key of -inf
+constexpr uint32_t kAll = 0xffffffffu;
+
+struct RouterArgs {
+    const void* logits;
+    int64_t stride, tokens;
+    int E, K, groups, topk_groups;
+    bool normalize, vec;
+    float scale;
+    const float* bias;
+    const uint8_t* mask;
+    int64_t* idx;
+    float* weights;
+};
+
+// Ordered as the floats are; both zeros alike, every NaN the largest.
+__device__ __forceinline__ uint32_t ordered(float v) {
+    if (v != v) return kAll;
+    const uint32_t u = __float_as_uint(v + 0.0f);
+    return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float unordered(uint32_t k) {
+    return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : kAll));  // kAll comes back as a NaN
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
+    return v;
+}
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, o));
+    return v;
+}
+
+// This lane's V logits of a row; -inf past the last expert.
+template <typename T, int V>
+__device__ __forceinline__ void load_logits(const T* row, int E, int lane, bool vec, float (&v)[V]) {
+    constexpr int kPer = 16 / sizeof(T);
+    if constexpr (V % kPer == 0) {
+        if (vec) {
+#pragma unroll
+            for (int c = 0; c < V; c += kPer) {
+                const int e = lane * V + c;
+                if (e < E) {
+                    const int4 r = ld_nc_na_v4(row + e);
+                    const uint32_t u[4] = {(uint32_t)r.x, (uint32_t)r.y, (uint32_t)r.z, (uint32_t)r.w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if constexpr (sizeof(T) == 4) {
+                            v[c + i] = __uint_as_float(u[i]);
+                        } else {
+                            v[c + 2 * i] = __uint_as_float(u[i] << 16);
+                            v[c + 2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < kPer; ++i) v[c + i] = -INFINITY;
+                }
+            }
+            return;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = lane * V + i < E ? (float)row[lane * V + i] : -INFINITY;
+}
+
+// sigmoid(l) and its slope, from e^-|l|: neither cancels.
+__device__ __forceinline__ float sigmoid_of(float l, float* slope) {
+    const float e = expf(-fabsf(l)), r = 1.0f / (1.0f + e);
+    *slope = e * r * r;
+    return l < 0.0f ? e * r : r;  // a NaN stays one: r
+}
+
+// The scores of a row: softmax, with *top the largest logit and *by 1 / sum of e^(l - top); or sigmoid and its
+// slope, with *by 1 / its sum (0 for a sum of 0).
+template <int V, bool kSigmoid>
+__device__ __forceinline__ void scores(const float (&l)[V], int E, int lane, float (&p)[V], float (&slope)[V], float* top, float* by) {
+    if constexpr (kSigmoid) {
+        float s = 0.0f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            p[i] = sigmoid_of(l[i], &slope[i]);
+            if (lane * V + i >= E) p[i] = slope[i] = 0.0f;
+            s += p[i];
+        }
+        s = warp_sum(s);
+        *by = s != 0.0f ? 1.0f / s : 0.0f;
+    } else {
+        float m = l[0], s = 0.0f;
+#pragma unroll
+        for (int i = 1; i < V; ++i) m = fmaxf(m, l[i]);
+        m = warp_max(m);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            p[i] = lane * V + i < E ? expf(l[i] - m) : 0.0f;
+            s += p[i];
+        }
+        s = 1.0f / warp_sum(s);
+#pragma unroll
+        for (int i = 0; i < V; ++i) p[i] *= s;
+        *top = m;
+        *by = s;
+    }
+}
+
+// The groups that stay: bit g of the result.  A group's score is the sum of its two largest keys.
+template <int V>
+__device__ __forceinline__ uint32_t choose_groups(const uint32_t (&key)[V], const RouterArgs& a, int lane) {
+    const int size = a.E / a.groups;
+    uint32_t score = 0;  // lane g: group g's
+    for (int g = 0; g < a.groups; ++g) {
+        uint32_t hi = 0, lo = 0;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int e = lane * V + i - g * size;
+            const uint32_t k = e >= 0 && e < size ? max(key[i], kKeyNegInf) : 0;
+            lo = max(lo, min(hi, k));
+            hi = max(hi, k);
+        }
+        const uint32_t top = __reduce_max_sync(kAll, hi);
+        const bool owner = lane == __ffs(__ballot_sync(kAll, hi == top)) - 1;
+        const uint32_t next = __reduce_max_sync(kAll, owner ? lo : hi);
+        const uint32_t s = size > 1 ? ordered(unordered(top) + unordered(next)) : top;
+        if (lane == g) score = s;
+    }
+    uint32_t kept = 0;
+    for (int i = 0; i < a.topk_groups; ++i) {
+        const uint32_t top = __reduce_max_sync(kAll, score);
+        const int g = __ffs(__ballot_sync(kAll, score == top)) - 1;
+        if (lane == g) score = 0;
+        kept |= 1u << g;
+    }
+    return kept;
+}
+
+template <typename T, int V, bool kSigmoid>
+__global__ void __launch_bounds__(kRouterThreads) route_kernel(const RouterArgs a) {
+    const int lane = threadIdx.x & 31;
+    grid_wait();
+    grid_launch_next();
+    for (int64_t t = (int64_t)blockIdx.x * kRouterWarps + (threadIdx.x >> 5); t < a.tokens; t += (int64_t)gridDim.x * kRouterWarps) {
+        if (a.mask && !a.mask[t]) {
+            if (lane < a.K) {
+                a.idx[t * a.K + lane] = -1;
+                a.weights[t * a.K + lane] = 0.0f;
+            }
+            continue;
+        }
+        const T* row = static_cast<const T*>(a.logits) + t * a.stride;
+        float l[V];
+        load_logits(row, a.E, lane, a.vec, l);
+        uint32_t key[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int e = lane * V + i;
+            key[i] = e < a.E ? ordered(a.bias ? l[i] + a.bias[e] : l[i]) : 0;
+        }
+        uint32_t kept = kAll;
+        if (a.groups > 1) kept = choose_groups(key, a, lane);
+        const int size = a.E / a.groups;
+        uint32_t best = 0;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int e = lane * V + i;
+            if (key[i] <= kKeyNegInf || (a.groups > 1 && !(kept >> min(e / size, 31) & 1))) key[i] = 0;
+            best = max(best, key[i]);
+        }
+        // choice k ends in lane k: its expert and its logit
+        int expert = -1;
+        float logit = -INFINITY;
+        for (int k = 0; k < a.K; ++k) {
+            const uint32_t top = __reduce_max_sync(kAll, best);
+            if (top == 0) break;
+            const int owner = __ffs(__ballot_sync(kAll, best == top)) - 1;
+            int at = 0;
+            float mine = 0.0f;
+            if (lane == owner) {
+                bool found = false;
+                best = 0;
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    if (!found && key[i] == top) {
+                        found = true;
+                        at = i;
+                        mine = l[i];
+                        key[i] = 0;
+                    }
+                    best = max(best, key[i]);
+                }
+            }
+            at = __shfl_sync(kAll, at, owner);
+            mine = __shfl_sync(kAll, mine, owner);
+            if (lane == k) {
+                expert = owner * V + at;
+                logit = mine;
+            }
+        }
+        float w;
+        if (kSigmoid) {
+            float slope;
+            w = expert >= 0 ? sigmoid_of(logit, &slope) : 0.0f;
+            if (a.normalize) w /= warp_sum(w) + 1e-20f;
+        } else if (a.normalize) {
+            const float m = warp_max(logit);
+            w = expert >= 0 ? expf(logit - m) : 0.0f;
+            w /= warp_sum(w);
+        } else {
+            float p[V], slope[V], top, by;
+            scores<V, false>(l, a.E, lane, p, slope, &top, &by);
+            w = expf(logit - top) * by;
+        }
+        if (lane < a.K) {
+            a.idx[t * a.K + lane] = expert;
+            a.weights[t * a.K + lane] = expert >= 0 ? w * a.scale : 0.0f;
+        }
+    }
+}
+
+// ---- balance loss -------------------------------------------------------------------
+struct BalanceArgs {
+    const void* logits;
+    const int64_t* idx;
+    int64_t stride, T;  // tokens of a sequence
+    int S, E, K, blocks;  // blocks of a sequence
+    bool vec;
+    float coef;
+    // workspace: [S][blocks][E] sums of q and choices, [S][blocks] tokens, [S] losses, the counter of the last block
+    float* part;
+    int* part_counts;
+    int* part_tokens;
+    float* seq_loss;
+    uint32_t* ticket;
+    float* loss;
+    int32_t* counts;
+    float* factors;
+    uint32_t* status;
+};
+
+template <typename T, int V, bool kSigmoid>
+__global__ void __launch_bounds__(kRouterThreads) balance_kernel(const BalanceArgs a) {
+    __shared__ float sums[kRouterMaxExperts];
+    __shared__ int hist[kRouterMaxExperts];
+    __shared__ int used_tokens;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    grid_wait();
+    grid_launch_next();
+    for (int e = threadIdx.x; e < a.E; e += kRouterThreads) hist[e] = 0;
+    if (threadIdx.x == 0) used_tokens = 0;
+    if (blockIdx.x == 0 && threadIdx.x == 0) *a.ticket = 0;
+    __syncthreads();
+    const int s = blockIdx.x / a.blocks, b = blockIdx.x - s * a.blocks;
+    float acc[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) acc[i] = 0.0f;
+    int tokens = 0;
+    bool bad = false;
+    for (int64_t t = (int64_t)b * kRouterWarps + warp; t < a.T; t += (int64_t)a.blocks * kRouterWarps) {
+        const int64_t row = s * a.T + t;
+        bool chose = false;
+        if (lane < a.K) {
+            const int64_t e = a.idx[row * a.K + lane];
+            chose = e >= 0 && e < a.E;
+            bad |= e < -1 || e >= a.E;
+            if (chose) atomicAdd(&hist[(int)e], 1);
+        }
+        if (!__any_sync(kAll, chose)) continue;
+        ++tokens;
+        float l[V], p[V], slope[V], top, by;
+        load_logits(static_cast<const T*>(a.logits) + row * a.stride, a.E, lane, a.vec, l);
+        scores<V, kSigmoid>(l, a.E, lane, p, slope, &top, &by);
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[i] += kSigmoid ? p[i] * by : p[i];
+    }
+    if (lane == 0 && tokens) atomicAdd(&used_tokens, tokens);
+    for (int w = 0; w < kRouterWarps; ++w) {  // in warp order
+        if (warp == w)
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const int e = lane * V + i;
+                if (e < a.E) sums[e] = w ? sums[e] + acc[i] : acc[i];
+            }
+        __syncthreads();
+    }
+    const int64_t at = (int64_t)blockIdx.x * a.E;
+    for (int e = threadIdx.x; e < a.E; e += kRouterThreads) {
+        a.part[at + e] = sums[e];
+        a.part_counts[at + e] = hist[e];
+    }
+    if (threadIdx.x == 0) a.part_tokens[blockIdx.x] = used_tokens;
+    if (bad && a.status) flag(a.status, FLAG_INVALID_TOPK);
+}
+
+template <typename T>
+__device__ __forceinline__ T block_sum(T v, T* buf) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = v;
+    __syncthreads();
+    T s = buf[0];
+    for (int i = 1; i < kRouterWarps; ++i) s += buf[i];
+    return s;
+}
+
+// A block per sequence: its counts, factors and loss; the last block to end adds the losses in order.
+__global__ void __launch_bounds__(kRouterThreads) balance_finish_kernel(const BalanceArgs a) {
+    __shared__ long long ibuf[kRouterWarps];
+    __shared__ float fbuf[kRouterWarps];
+    __shared__ bool last;
+    grid_wait();
+    grid_launch_next();
+    constexpr int kMost = kRouterMaxExperts / kRouterThreads;
+    const int s = blockIdx.x;
+    float p[kMost];
+    int c[kMost];
+    long long pairs = 0, tokens = 0;
+#pragma unroll
+    for (int i = 0; i < kMost; ++i) {
+        const int e = threadIdx.x + i * kRouterThreads;
+        p[i] = 0.0f;
+        c[i] = 0;
+        if (e < a.E)
+            for (int b = 0; b < a.blocks; ++b) {
+                const int64_t at = ((int64_t)s * a.blocks + b) * a.E + e;
+                p[i] += a.part[at];
+                c[i] += a.part_counts[at];
+            }
+        pairs += c[i];
+    }
+    for (int b = threadIdx.x; b < a.blocks; b += kRouterThreads) tokens += a.part_tokens[s * a.blocks + b];
+    pairs = block_sum(pairs, ibuf);
+    tokens = block_sum(tokens, ibuf);
+    // coef / (S m n): the same for every expert
+    const float unit = pairs ? (float)((double)a.coef / ((double)a.S * (double)pairs * (double)tokens)) : 0.0f;
+    float loss = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kMost; ++i) {
+        const int e = threadIdx.x + i * kRouterThreads;
+        if (e < a.E) {
+            a.counts[s * a.E + e] = c[i];
+            a.factors[s * a.E + e] = unit * (float)((long long)c[i] * a.E - pairs);
+            loss += unit * (float)((long long)c[i] * a.E) * p[i];
+        }
+    }
+    loss = block_sum(loss, fbuf);
+    if (threadIdx.x == 0) {
+        a.seq_loss[s] = loss;
+        __threadfence();
+        last = atomicAdd(a.ticket, 1u) == (uint32_t)a.S - 1;
+    }
+    __syncthreads();
+    if (!last) return;
+    __threadfence();
+    float sum = 0.0f;
+    for (int i = threadIdx.x; i < a.S; i += kRouterThreads) sum += __ldcg(a.seq_loss + i);
+    sum = block_sum(sum, fbuf);
+    if (threadIdx.x == 0) *a.loss = sum;
+}
+
+// ---- gradient of the logits -----------------------------------------------------------
+struct RouterBackArgs {
+    const void* logits;
+    const int64_t* idx;
+    const float* dweights;  // null: none
+    const float* factors;   // null: no balance loss
+    const float* dloss;
+    void* dlogits;
+    int64_t stride, dstride, tokens, T;
+    int E, K;
+    bool normalize, vec, dvec;
+    float scale;
+    uint32_t* status;
+};
+
+template <typename T, int V>
+__device__ __forceinline__ void store_logits(T* row, int E, int lane, bool vec, const float (&v)[V]) {
+    constexpr int kPer = 16 / sizeof(T);
+    if constexpr (V % kPer == 0) {
+        if (vec) {
+#pragma unroll
+            for (int c = 0; c < V; c += kPer) {
+                const int e = lane * V + c;
+                if (e >= E) continue;
+                int4 r;
+                int* o = &r.x;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if constexpr (sizeof(T) == 4) {
+                        o[i] = __float_as_int(v[c + i]);
+                    } else {
+                        const __nv_bfloat162 b = __floats2bfloat162_rn(v[c + 2 * i], v[c + 2 * i + 1]);
+                        o[i] = *reinterpret_cast<const int*>(&b);
+                    }
+                }
+                st_na_v4(row + e, r);
+            }
+            return;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        if (lane * V + i < E) row[lane * V + i] = (T)v[i];
+}
+
+template <typename T, int V, bool kSigmoid>
+__global__ void __launch_bounds__(kRouterThreads) router_backward_kernel(const RouterBackArgs a) {
+    const int lane = threadIdx.x & 31;
+    grid_wait();
+    grid_launch_next();
+    const float dloss = a.factors ? *a.dloss : 0.0f;
+    bool bad = false;
+    for (int64_t t = (int64_t)blockIdx.x * kRouterWarps + (threadIdx.x >> 5); t < a.tokens; t += (int64_t)gridDim.x * kRouterWarps) {
+        const T* row = static_cast<const T*>(a.logits) + t * a.stride;
+        T* out = static_cast<T*>(a.dlogits) + t * a.dstride;
+        int e = -1;
+        if (lane < a.K) {
+            const int64_t i = a.idx[t * a.K + lane];
+            bad |= i < -1 || i >= a.E;
+            e = i >= 0 && i < a.E ? (int)i : -1;
+        }
+        float d[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) d[i] = 0.0f;
+        if (!__any_sync(kAll, e >= 0)) {  // a padded token
+            store_logits(out, a.E, lane, a.dvec, d);
+            continue;
+        }
+        const float logit = e >= 0 ? (float)row[e] : -INFINITY;
+        const float g = a.dweights && e >= 0 ? a.dweights[t * a.K + lane] * a.scale : 0.0f;
+        // the chosen experts' share of the gradient, in lane k for choice k
+        float near = 0.0f, inner = 0.0f;
+        // softmax of the whole row, or sigmoid: for the balance loss, and for weights that are not normalised
+        if (a.factors || (!kSigmoid && !a.normalize)) {
+            float l[V], p[V], slope[V], top, by;
+            load_logits(row, a.E, lane, a.vec, l);
+            scores<V, kSigmoid>(l, a.E, lane, p, slope, &top, &by);
+            if (a.factors) {
+                const float* f = a.factors + t / a.T * a.E + lane * V;
+                float fv[V], sum = 0.0f;
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    fv[i] = lane * V + i < a.E ? f[i] : 0.0f;
+                    sum = fmaf(fv[i], p[i], sum);
+                }
+                sum = warp_sum(sum) * (kSigmoid ? by : 1.0f);
+#pragma unroll
+                for (int i = 0; i < V; ++i) d[i] = dloss * (fv[i] - sum) * (kSigmoid ? slope[i] * by : p[i]);
+            }
+            if (!kSigmoid && !a.normalize && a.dweights) {
+                near = e >= 0 ? expf(logit - top) * by * g : 0.0f;
+                inner = warp_sum(near);
+#pragma unroll
+                for (int i = 0; i < V; ++i) d[i] -= p[i] * inner;
+            }
+        }
+        if (a.dweights && (kSigmoid || a.normalize)) {
+            if (kSigmoid) {
+                float slope = 0.0f;
+                float w = e >= 0 ? sigmoid_of(logit, &slope) : 0.0f;
+                if (e < 0) slope = 0.0f;
+                if (a.normalize) {
+                    const float by = 1.0f / (warp_sum(w) + 1e-20f);
+                    inner = warp_sum(g * w * by);
+                    near = slope * (g - inner) * by;
+                } else {
+                    near = slope * g;
+                }
+            } else {
+                const float m = warp_max(logit);
+                float w = e >= 0 ? expf(logit - m) : 0.0f;
+                w /= warp_sum(w);
+                inner = warp_sum(w * g);
+                near = w * (g - inner);
+            }
+            if (e < 0) near = 0.0f;
+        }
+        if (a.dweights)
+            for (int k = 0; k < a.K; ++k) {
+                const int at = __shfl_sync(kAll, e, k) - lane * V;
+                const float v = __shfl_sync(kAll, near, k);
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+                    if (at == i) d[i] += v;
+            }
+        store_logits(out, a.E, lane, a.dvec, d);
+    }
+    if (bad && a.status) flag(a.status, FLAG_INVALID_TOPK);
+}
+
+// ---- host -------------------------------------------------------------------------
+// The kernel for these experts (lanes hold 1, 2, 4, .. 32 each), type of logits and scoring.
+#define EP_BY_EXPERTS(kernel, T, sig, E)                                                     \
+    ((E) <= 32    ? kernel<T, 1, sig>                                                        \
+     : (E) <= 64  ? kernel<T, 2, sig>                                                        \
+     : (E) <= 128 ? kernel<T, 4, sig>                                                        \
+     : (E) <= 256 ? kernel<T, 8, sig>                                                        \
+     : (E) <= 512 ? kernel<T, 16, sig>                                                       \
+                  : kernel<T, 32, sig>)
+#define EP_ROUTER_KERNEL(kernel, r)                                                                                     \
+    ((r)->logits_type == EP_F32                                                                                         \
+         ? ((r)->scoring == EP_SIGMOID ? EP_BY_EXPERTS(kernel, float, true, (r)->experts)                               \
+                                       : EP_BY_EXPERTS(kernel, float, false, (r)->experts))                             \
+         : ((r)->scoring == EP_SIGMOID ? EP_BY_EXPERTS(kernel, __nv_bfloat16, true, (r)->experts)                       \
+                                       : EP_BY_EXPERTS(kernel, __nv_bfloat16, false, (r)->experts)))
+
+static ep_status check_router(const char* fn, const ep_router* r, const void* logits, int64_t stride) {
+    if (!r) return set_error(EP_ERR_INVALID_ARG, "%s: null descriptor", fn);
+    if (r->experts < 1 || r->experts > kRouterMaxExperts || r->topk < 1 || r->topk > kMaxTopk || r->topk > r->experts)
+        return set_error(EP_ERR_INVALID_ARG, "%s: %d of %d experts (at most %d of %d)", fn, r->topk, r->experts, kMaxTopk, kRouterMaxExperts);
+    if (r->tokens < 0 || r->tokens > (int64_t)INT_MAX) return set_error(EP_ERR_INVALID_ARG, "%s: %lld tokens", fn, (long long)r->tokens);
+    if (r->logits_type < 0 || r->logits_type > EP_F32 || r->scoring < 0 || r->scoring > EP_SIGMOID)
+        return set_error(EP_ERR_INVALID_ARG, "%s: type %d, scoring %d", fn, r->logits_type, r->scoring);
+    if (r->tokens > 0 && (!logits || !aligned_to(logits, r->logits_type == EP_F32 ? 4 : 2) || (r->tokens > 1 && stride < r->experts)))
+        return set_error(EP_ERR_INVALID_ARG, "%s: logits, rows %lld elements apart for %d experts", fn, (long long)stride, r->experts);
+    return EP_OK;
+}
+static bool by_vectors(const ep_router* r, const void* p, int64_t stride) {
+    const int per = r->logits_type == EP_F32 ? 4 : 8;
+    return aligned16(p) && stride % per == 0 && r->experts % per == 0;
+}
+static ep_status router_blocks(int64_t tokens, int64_t* blocks) {
+    int dev = 0, sms = 0;
+    EP_CUDA(cudaGetDevice(&dev));
+    EP_CUDA(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
+    const int64_t most = (int64_t)sms * 6, need = (tokens + kRouterWarps - 1) / kRouterWarps;
+    *blocks = need < most ? need : most;
+    return EP_OK;
+}
+
+// Blocks of one sequence: enough for the device over all of them, each with two tokens a warp or more.
+static int balance_blocks(int64_t S, int64_t T, int sms) {
+    int64_t b = ((int64_t)sms * 4 + S - 1) / S;
+    const int64_t most = (T + 2 * kRouterWarps - 1) / (2 * kRouterWarps);
+    if (b > most) b = most;
+    return b < 1 ? 1 : (int)b;
+}
+static int64_t balance_bytes(int64_t S, int blocks, int E) { return (S * blocks * (2 * (int64_t)E + 1) + S + 1) * 4; }
+
+}  // namespace ep
+
+using namespace ep;
+
+extern "C" ep_status ep_route(const ep_router* r, const void* logits, int64_t logits_stride, const float* bias, const uint8_t* mask,
+                              int64_t* topk_idx, float* topk_weights, void* stream) {
+    const char* fn = "ep_route";
+    EP_TRY(check_router(fn, r, logits, logits_stride));
+    if (r->groups < 1 || r->groups > kRouterMaxGroups || r->experts % r->groups || r->topk_groups < 1 || r->topk_groups > r->groups ||
+        r->topk > r->topk_groups * (r->experts / r->groups))
+        return set_error(EP_ERR_INVALID_ARG, "%s: %d of %d groups (at most %d) of %d experts for %d choices", fn, r->topk_groups, r->groups,
+                         kRouterMaxGroups, r->experts, r->topk);
+    if (r->tokens == 0) return EP_OK;
+    if (!topk_idx || !topk_weights || !aligned_to(topk_idx, 8) || !aligned_to(topk_weights, 4) || !aligned_to(bias, 4))
+        return set_error(EP_ERR_INVALID_ARG, "%s: topk_idx, topk_weights and bias aligned to their elements", fn);
+    int64_t blocks = 0;
+    EP_TRY(router_blocks(r->tokens, &blocks));
+    const RouterArgs a = {logits, logits_stride, r->tokens, r->experts, r->topk, r->groups, r->topk_groups, r->normalize != 0,
+                          by_vectors(r, logits, logits_stride), r->scale, bias, mask, topk_idx, topk_weights};
+    return launch_next(EP_ROUTER_KERNEL(route_kernel, r), blocks, kRouterThreads, stream, a);
+}
+
+extern "C" int64_t ep_balance_loss_workspace(const ep_router* r, int32_t sequences) {
+    int dev = 0, sms = 0;
+    if (!r || sequences < 1 || r->experts < 1 || r->experts > kRouterMaxExperts || r->tokens < 0 || r->tokens > INT_MAX ||
+        cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return 0;
+    return balance_bytes(sequences, balance_blocks(sequences, r->tokens / sequences, sms), r->experts);
+}
+
+extern "C" ep_status ep_balance_loss(const ep_router* r, const void* logits, int64_t logits_stride, const int64_t* topk_idx,
+                                     int32_t sequences, float coef, float* loss, int32_t* counts, float* factors, void* workspace,
+                                     int64_t workspace_bytes, uint32_t* status_out, void* stream) {
+    const char* fn = "ep_balance_loss";
+    EP_TRY(check_router(fn, r, logits, logits_stride));
+    if (sequences < 1 || r->tokens % sequences)
+        return set_error(EP_ERR_INVALID_ARG, "%s: %lld tokens in %d sequences", fn, (long long)r->tokens, sequences);
+    if ((r->tokens > 0 && !topk_idx) || !loss || !counts || !factors || !aligned_to(topk_idx, 8) || !aligned_to(loss, 4) ||
+        !aligned_to(counts, 4) || !aligned_to(factors, 4) || !aligned_to(status_out, 4))
+        return set_error(EP_ERR_INVALID_ARG, "%s: topk_idx, loss, counts and factors, aligned to their elements", fn);
+    int dev = 0, sms = 0;
+    EP_CUDA(cudaGetDevice(&dev));
+    EP_CUDA(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
+    const int64_t T = r->tokens / sequences;
+    const int blocks = balance_blocks(sequences, T, sms);
+    const int64_t need = balance_bytes(sequences, blocks, r->experts);
+    if (!workspace || !aligned16(workspace) || workspace_bytes < need)
+        return set_error(EP_ERR_INVALID_ARG, "%s: workspace of %lld bytes (16-byte aligned), %lld needed", fn, (long long)workspace_bytes, (long long)need);
+    if (r->tokens * r->topk > INT_MAX) return set_error(EP_ERR_INVALID_ARG, "%s: %lld tokens with %d choices", fn, (long long)r->tokens, r->topk);
+    if ((int64_t)sequences * blocks > INT_MAX) return set_error(EP_ERR_INVALID_ARG, "%s: %d sequences", fn, sequences);
+    const int64_t n = (int64_t)sequences * blocks * r->experts;
+    float* ws = static_cast<float*>(workspace);
+    const BalanceArgs a = {logits, topk_idx, logits_stride, T, sequences, r->experts, r->topk, blocks, by_vectors(r, logits, logits_stride), coef,
+                           ws, reinterpret_cast<int*>(ws + n), reinterpret_cast<int*>(ws + 2 * n),
+                           ws + 2 * n + (int64_t)sequences * blocks, reinterpret_cast<uint32_t*>(ws + 2 * n + (int64_t)sequences * blocks + sequences),
+                           loss, counts, factors, status_out};
+    EP_TRY(launch_next(EP_ROUTER_KERNEL(balance_kernel, r), (int64_t)sequences * blocks, kRouterThreads, stream, a));
+    return launch_next(balance_finish_kernel, sequences, kRouterThreads, stream, a);
+}
+
+extern "C" ep_status ep_router_backward(const ep_router* r, const void* logits, int64_t logits_stride, const int64_t* topk_idx,
+                                        const float* dweights, const float* factors, int32_t sequences, const float* dloss, void* dlogits,
+                                        int64_t dlogits_stride, uint32_t* status_out, void* stream) {
+    const char* fn = "ep_router_backward";
+    EP_TRY(check_router(fn, r, logits, logits_stride));
+    if (r->tokens == 0) return EP_OK;
+    if (!factors != !dloss) return set_error(EP_ERR_INVALID_ARG, "%s: factors come with the loss's gradient", fn);
+    if (!factors && !dweights) return set_error(EP_ERR_INVALID_ARG, "%s: no gradient comes in", fn);
+    if (factors && (sequences < 1 || r->tokens % sequences))
+        return set_error(EP_ERR_INVALID_ARG, "%s: %lld tokens in %d sequences", fn, (long long)r->tokens, sequences);
+    if (!topk_idx || !dlogits || !aligned_to(topk_idx, 8) || !aligned_to(dweights, 4) || !aligned_to(factors, 4) || !aligned_to(dloss, 4) ||
+        !aligned_to(dlogits, r->logits_type == EP_F32 ? 4 : 2) || !aligned_to(status_out, 4) || (r->tokens > 1 && dlogits_stride < r->experts))
+        return set_error(EP_ERR_INVALID_ARG, "%s: topk_idx, gradients and dlogits (rows %lld elements apart), aligned to their elements", fn,
+                         (long long)dlogits_stride);
+    int64_t blocks = 0;
+    EP_TRY(router_blocks(r->tokens, &blocks));
+    const RouterBackArgs a = {logits, topk_idx, dweights, factors, dloss, dlogits, logits_stride, dlogits_stride, r->tokens,
+                              factors ? r->tokens / sequences : 1, r->experts, r->topk, r->normalize != 0, by_vectors(r, logits, logits_stride),
+                              by_vectors(r, dlogits, dlogits_stride), r->scale, status_out};
+    return launch_next(EP_ROUTER_KERNEL(router_backward_kernel, r), blocks, kRouterThreads, stream, a);
+}

@@ -483,6 +483,103 @@ ep_status ep_moe_tokens(const void* x, int64_t x_stride, int32_t num_tokens, con
                         void* stream);
 
 /* ------------------------------------------------------------------------ */
+/* What comes before dispatch: the norm and the router.  The pages take x,     */
+/* topk_idx and topk_weights as given, so they name none of it                 */
+/* ------------------------------------------------------------------------ */
+
+typedef enum ep_type { EP_BF16 = 0, EP_F32 = 1 } ep_type;
+
+/* RMS norm of rows of `hidden` channels (a multiple of 8, at most 16384), with
+ * the residual's addition:
+ *   h = x + residual, rounded to the residual's type (without one: h = x);
+ *   n = h * (mean of h^2 over the channels + eps)^(-1/2) * weight, in fp32;
+ *   residual_out = h, y = bf16(n), fp8_rows = n as FP8 rows in the layout and by
+ *   the rule of ep_quantize_fp8, from the fp32 n (a NaN among 128 channels makes
+ *   their scale and codes NaN).
+ * x and y bf16; residual (nullable, then residual_out too) of residual_type;
+ * weight [hidden] of weight_type.  y or fp8_rows may be NULL, not both; FP8 rows
+ * take a multiple of 128 channels.  Strides in elements (fp8_stride: bytes); all
+ * arrays 16-byte aligned, rows whole 16 bytes apart.  residual_out may be the
+ * residual itself, and y may be x itself.  eps > 0.  The squares' sum has to stay
+ * below 3.4e38 (|h| up to 1e17 does).  Asynchronous, no allocation. */
+ep_status ep_rms_norm(const void* x, int64_t x_stride, const void* residual, int64_t residual_stride, int32_t residual_type,
+                      const void* weight, int32_t weight_type, float eps, int64_t rows, int32_t hidden, void* residual_out,
+                      int64_t residual_out_stride, void* y, int64_t y_stride, uint8_t* fp8_rows, int64_t fp8_stride, void* stream);
+
+/* Its backward pass.  dy bf16: the gradient of n; h (of h_type): what the forward
+ * pass took the norm of (residual_out, or x); dresidual (nullable, of h_type): the
+ * gradient that reaches h from elsewhere.  With g = dy * weight and s the row's
+ * (mean h^2 + eps)^(-1/2):
+ *   dx = dresidual + s * (g - h * s^2 * mean(g * h)), of h_type: the gradient of x
+ *        and of the residual alike (dx may be dresidual itself);
+ *   dweight [hidden] fp32 = sum over rows of dy * h * s, written, not added to.
+ * The order of the sums depends on the sizes and the device alone.  The workspace
+ * (16-byte aligned, ep_rms_norm_backward_workspace bytes on the current device)
+ * belongs to the call until it has finished. */
+int64_t ep_rms_norm_backward_workspace(int64_t rows, int32_t hidden);
+ep_status ep_rms_norm_backward(const void* dy, int64_t dy_stride, const void* h, int64_t h_stride, int32_t h_type, const void* weight,
+                               int32_t weight_type, float eps, const void* dresidual, int64_t dresidual_stride, int64_t rows,
+                               int32_t hidden, void* dx, int64_t dx_stride, float* dweight, void* workspace, int64_t workspace_bytes,
+                               void* stream);
+
+typedef enum ep_scoring { EP_SOFTMAX = 0, EP_SIGMOID = 1 } ep_scoring;
+
+/* A router over `experts` (1..1024) with topk (1..32, at most experts) choices a
+ * token.  groups and topk_groups are read by ep_route alone, normalize and scale
+ * by ep_route and ep_router_backward. */
+typedef struct ep_router {
+    int64_t tokens;
+    int32_t experts, topk;
+    int32_t logits_type;         /* ep_type of the logits and of their gradient              */
+    int32_t scoring;             /* ep_scoring                                               */
+    int32_t normalize;           /* weights over the sum of the chosen experts' scores        */
+    int32_t groups, topk_groups; /* choose among the experts of topk_groups of `groups` equal
+                                    runs of experts (1..32; nodes, say); 1, 1: among all       */
+    float scale;                 /* of the weights                                            */
+} ep_router;
+
+/* Logits [tokens][experts] (rows logits_stride elements apart) to topk_idx
+ * [tokens][topk] and topk_weights, as the layout and dispatch calls read them.
+ *   Choice: by key = fp32(logit + bias[expert]) (bias nullable, fp32), largest first,
+ *   equal keys by the lowest expert; NaN is larger than any number, as in a sort, and
+ *   -inf is never chosen: where fewer than topk experts are left, the last entries
+ *   are -1 with weight 0.  With groups, first the topk_groups runs with the largest
+ *   fp32 sum of their two largest keys (one key where a run is one expert).
+ *   Weights, from the logits alone, times scale: softmax over all experts, or with
+ *   normalize over the chosen; sigmoid, or with normalize sigmoid / (the chosen
+ *   ones' sum + 1e-20).
+ * mask (nullable, [tokens] bytes): a token with 0 is padding, all -1 with weight 0. */
+ep_status ep_route(const ep_router* router, const void* logits, int64_t logits_stride, const float* bias, const uint8_t* mask,
+                   int64_t* topk_idx, float* topk_weights, void* stream);
+
+/* The balance loss of a router, over `sequences` equal runs of tokens (sequences,
+ * microbatches or ranks), and its per-expert counts.  With c[s][e] the entries of
+ * topk_idx that name e, m[s] their number, n[s] the tokens of s with an entry, and
+ * q the softmax of a token's logits, or its sigmoids over their sum:
+ *   loss [1] = coef * mean over s of sum over e of experts * c[s][e] / m[s] * (mean of q[t][e] over the n[s] tokens)
+ *   counts [sequences][experts] = c
+ *   factors [sequences][experts] = F[s][e] less its mean over e, where loss = sum of F[s][e] * q[t][e]:
+ *   what ep_router_backward takes.
+ * -1 entries and tokens without an entry count for nothing, nor does a sequence
+ * without one; an entry outside [-1, experts) is skipped and ORs 1 into status_out
+ * (device, nullable, zeroed by the caller).  tokens * topk below 2^31.  fp32 sums in an
+ * order that depends on the sizes and the device alone.  Workspace as
+ * ep_rms_norm_backward's. */
+int64_t ep_balance_loss_workspace(const ep_router* router, int32_t sequences);
+ep_status ep_balance_loss(const ep_router* router, const void* logits, int64_t logits_stride, const int64_t* topk_idx, int32_t sequences,
+                          float coef, float* loss, int32_t* counts, float* factors, void* workspace, int64_t workspace_bytes,
+                          uint32_t* status_out, void* stream);
+
+/* The gradient of the logits (of their type, [tokens][experts], rows dlogits_stride
+ * apart; may be the logits themselves): of the weights, given dweights [tokens][topk]
+ * (nullable), and of the balance loss, given its factors and its gradient dloss [1]
+ * (fp32, on the device; both nullable).  The choice and the factors are constants.
+ * A token without an entry gets 0; entries outside [-1, experts) as above. */
+ep_status ep_router_backward(const ep_router* router, const void* logits, int64_t logits_stride, const int64_t* topk_idx,
+                             const float* dweights, const float* factors, int32_t sequences, const float* dloss, void* dlogits,
+                             int64_t dlogits_stride, uint32_t* status_out, void* stream);
+
+/* ------------------------------------------------------------------------ */
 /* Low-latency mode ([P1] 低延迟模式; [P2] low-latency ping-pong; [P3] 2.2, 4.2) */
 /* ------------------------------------------------------------------------ */
 
