@@ -35,10 +35,12 @@ from . import _lib
 from ._lib import EpConfig, EpDispatchHandle, EpError, check
 
 from .experts import check_status, expert_gemm, expert_swiglu, fp8_row_views, moe_tokens, moe_tokens_workspace, new_status
+from .fp4 import expert_gemm_fp4, expert_swiglu_fp4, fp4_row_views, quantize_fp4
 from .norm import rms_norm, rms_norm_backward, rms_norm_backward_workspace
 from .router import balance_loss, balance_loss_workspace, route, router_backward
 
 __all__ = ["Context", "LLBuffer", "EpError", "load_library", "ll_size_hint", "ll_message_bytes",
+           "quantize_fp4", "expert_gemm_fp4", "expert_swiglu_fp4", "fp4_row_views",
            "rms_norm", "rms_norm_backward", "rms_norm_backward_workspace",
            "route", "balance_loss", "balance_loss_workspace", "router_backward",
            "expert_gemm", "expert_swiglu", "fp8_row_views", "moe_tokens", "moe_tokens_workspace", "new_status", "check_status"]
@@ -387,6 +389,32 @@ class Context:
             _ptr(o["perm_src_token"]), _ptr(o.get("perm_weight")), o["permuted_xq"].shape[0], _stream(stream)))
         return o
 
+    # ---- FP4 rows ----------------------------------------------------------------
+    @property
+    def fp4_row_bytes(self) -> int:
+        return int(self.lib.ep_fp4_row_bytes(self.H))
+
+    def quantize_fp4(self, x, stream=None, out=None):
+        """Every token once into an FP4 row (H/2 bytes of e2m1 codes, H/32 E8M0 scales)."""
+        _require_cuda(x)
+        if out is None:
+            with torch.cuda.stream(stream):
+                out = torch.empty(self.R * self.T, self.fp4_row_bytes, dtype=torch.uint8, device=self.device)
+        quantize_fp4(x.view(-1, self.H), out=fp4_row_views(out, self.H), stream=stream)
+        return out
+
+    def dispatch_permuted_fp4(self, xq, topk_idx, topk_weights, handle: Handle, stream=None, out=None) -> dict:
+        _require_cuda(xq, topk_idx, topk_weights)
+        P = handle.num_perm_rows
+        o = out if out is not None else dict(
+            permuted_xq=torch.empty(P, self.fp4_row_bytes, dtype=torch.uint8, device=self.device),
+            perm_src_token=self._i32(P), perm_weight=torch.empty(P, dtype=torch.float32, device=self.device))
+        cs = handle.c_struct()
+        check("ep_dispatch_permuted_fp4", self.lib.ep_dispatch_permuted_fp4(
+            self._ctx, _ptr(xq), _ptr(topk_idx), _ptr(topk_weights), ctypes.byref(cs), _ptr(o["permuted_xq"]),
+            _ptr(o["perm_src_token"]), _ptr(o.get("perm_weight")), o["permuted_xq"].shape[0], _stream(stream)))
+        return o
+
     # ---- combine ---------------------------------------------------------------
     def combine(self, handle: Handle, expert_out, topk_idx, topk_weights, stream=None, out=None, hier=False):
         _require_cuda(expert_out, topk_idx, topk_weights)
@@ -423,6 +451,21 @@ class Context:
         with N = H what combine reads."""
         x, xs = fp8_row_views(permuted_xq, w.shape[2])
         return expert_gemm(x, xs, w, w_scales, out=out, stream=stream, **self._groups(handle))
+
+    def expert_swiglu_fp4(self, handle: Handle, permuted_xq, w13, w13_scales, stream=None, out=None):
+        """expert_swiglu of the permuted FP4 rows with MXFP4 weights [E][2I][H/2]: FP4 rows of I channels in the same layout."""
+        inter = w13.shape[1] // 2
+        if out is None:
+            with torch.cuda.stream(stream):
+                out = torch.empty(permuted_xq.shape[0], int(self.lib.ep_fp4_row_bytes(inter)), dtype=torch.uint8, device=self.device)
+        x, xs = fp4_row_views(permuted_xq, 2 * w13.shape[2])
+        expert_swiglu_fp4(x, xs, w13, w13_scales, out=fp4_row_views(out, inter), stream=stream, **self._groups(handle))
+        return out
+
+    def expert_gemm_fp4(self, handle: Handle, permuted_xq, w, w_scales, stream=None, out=None):
+        """expert_gemm of the permuted FP4 rows with MXFP4 weights [E][N][K/2]: bf16 [P][N]."""
+        x, xs = fp4_row_views(permuted_xq, 2 * w.shape[2])
+        return expert_gemm_fp4(x, xs, w, w_scales, out=out, stream=stream, **self._groups(handle))
 
     # ---- hierarchical dispatch -------------------------------------------------
     def dispatch_hier(self, x, topk_idx, topk_weights, handle: Handle, stream=None, out=None, staging=None) -> dict:

@@ -92,6 +92,11 @@ SIGNATURES = {
     "ep_expert_swiglu": (INT, [P, P, P, P, I64, P, I64, P, P]),
     "ep_moe_tokens_workspace": (I64, [I32, I32, P]),
     "ep_moe_tokens": (INT, [P, I64, I32, P, P, I32, P, P, I64, P, I64, P, P]),
+    "ep_fp4_row_bytes": (I64, [INT]),
+    "ep_quantize_fp4": (INT, [P, I64, I64, I32, P, I64, P, I64, P]),
+    "ep_dispatch_permuted_fp4": (INT, [P, P, P, P, ctypes.POINTER(EpDispatchHandle), P, P, P, I64, P]),
+    "ep_expert_gemm_fp4": (INT, [P, P, P, P, I64, P, P]),
+    "ep_expert_swiglu_fp4": (INT, [P, P, P, P, I64, P, I64, P, P]),
     "ep_rms_norm": (INT, [P, I64, P, I64, I32, P, I32, F32, I64, I32, P, I64, P, I64, P, I64, P]),
     "ep_rms_norm_backward_workspace": (I64, [I64, I32]),
     "ep_rms_norm_backward": (INT, [P, I64, P, I64, I32, P, I32, F32, P, I64, I64, I32, P, I64, P, P, I64, P]),

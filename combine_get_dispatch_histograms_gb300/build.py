@@ -18,7 +18,7 @@ INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(OUT_DIR, "libep_gb300.so")
 SOURCES = ["ep_layout_notify.cu", "ep_copy.cu", "ep_combine.cu", "ep_ll.cu", "ep_fp8.cu", "ep_gemm.cu",
-           "ep_moe_tokens.cu", "ep_norm.cu", "ep_router.cu"]
+           "ep_moe_tokens.cu", "ep_norm.cu", "ep_router.cu", "ep_fp4.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

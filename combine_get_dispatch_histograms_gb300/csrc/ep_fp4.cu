@@ -1,0 +1,583 @@
+// ep_fp4.cu -- MXFP4 rows and the experts' products on them: quantisation, y = x w^T per group of
+// rows, and the first product with its activation and requantisation fused.
+//
+// Mathematics.  Row r, output channel n, blocks b of 32 along K, codes x, w (e2m1) and E8M0 bytes:
+//   y[r][n] = sum_b 2^(sx[r][b] - 127) 2^(sw[n][b] - 127) sum_{k in b} x[r][k] w[n][k]
+// which tcgen05.mma computes whole (kind::mxf4, block scales from tensor memory, fp32 sums), so that the
+// accumulator leaves tensor memory once a tile, not once a block of K.
+//
+// Shape.  128 rows x kBN weight rows a tile.  One warp copies codes (256 of K, 128 bytes a row, a
+// stage), four stage scales: each thread loads its rows' bytes and writes them where tcgen05.cp reads them
+// (32 rows of 16 bytes: row r's four bytes at (r % 32) * 16 + r / 32 * 4), one issues copies of scales and
+// products, four write the results.  With 192 weight rows a tile tensor memory holds two accumulators and
+// the scales beside them, so that a tile is written while the next is multiplied.
+#include <atomic>
+
+#include "ep_fp4.cuh"
+#include "ep_groups.cuh"
+
+namespace ep {
+
+constexpr int k4BM = 128;         // rows of a tile
+constexpr int k4BK = 256;         // codes of K a stage: 128 bytes a row
+constexpr int k4BoxRows = 32;     // rows of one copy of x
+constexpr int k4ScaleWarps = 4, k4OutWarps = 4;
+constexpr int k4Threads = 128 + 32 * (k4ScaleWarps + k4OutWarps);
+constexpr int k4TileRing = 4;
+constexpr int64_t k4WaitNs = 2000000000ll;
+
+template <int kBN>
+struct Fp4Shape {
+    static constexpr int kChunks = (kBN + 127) / 128;               // of 128 weight rows' scales
+    static constexpr int kCodesA = k4BM * 128, kCodesB = kBN * 128;
+    static constexpr int kScalesA = 2 * 512, kScalesB = 2 * kChunks * 512;  // [128 of K][chunk][32][16]
+    static constexpr int kStage = kCodesA + kCodesB + kScalesA + kScalesB;
+    static constexpr int kStages = kBN > 128 ? 5 : 8;
+    static constexpr int kOutRow = 34 * 2;                          // bytes of a staged row of 32 bf16: rows fall into other banks
+    static constexpr int kOut = 32 * kOutRow;
+    static constexpr size_t kSmem = 1024 + kStages * kStage + k4OutWarps * kOut;
+    // columns of tensor memory: two accumulators, then two sets of scales in turn
+    static constexpr int kScaleCols = 8 + 2 * kChunks * 4, kScaleAt = 2 * kBN;
+    static constexpr int kCols = 2 * kBN + 2 * kScaleCols > 256 ? 512 : 256;
+};
+
+struct Fp4Args : TileArgs {
+    const uint8_t* x_scales;
+    int64_t x_sstride;
+    const uint8_t* w_scales;
+    int N, K, KT;       // KT: stages of K
+    void* out;          // bf16 rows, or codes
+    int64_t out_stride; // elements; codes: bytes
+    uint8_t* out_scales;
+    int64_t out_sstride;
+    bool out_vec, out_wide;   // 16- and 32-byte stores
+    bool x_vec, w_vec;        // 16-byte loads of scales
+    uint32_t* status;
+};
+
+template <int kStages>
+struct Fp4Shared {
+    uint64_t full[kStages], scales[kStages], done[kStages], acc_full[2], acc_empty[2];
+    uint64_t tile_full[k4TileRing], tile_empty[k4TileRing], drain;
+    uint32_t tmem;
+    int abort;
+    GemmTile tile[k4TileRing];
+};
+
+// A ring of kSize slots, kSize any number.
+template <int kSize>
+struct Turn {
+    int slot = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void next() {
+        if (++slot == kSize) {
+            slot = 0;
+            phase ^= 1;
+        }
+    }
+};
+
+// 16 bytes of scales from byte `at` of a row with `bytes` of them (a multiple of 4); 0 past its end.
+__device__ __forceinline__ uint4 load_scales(const uint8_t* row, int at, int bytes, bool vec) {
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (vec && at + 16 <= bytes) return *reinterpret_cast<const uint4*>(row + at);
+    if (at < bytes) v.x = *reinterpret_cast<const uint32_t*>(row + at);
+    if (at + 4 < bytes) v.y = *reinterpret_cast<const uint32_t*>(row + at + 4);
+    if (at + 8 < bytes) v.z = *reinterpret_cast<const uint32_t*>(row + at + 8);
+    if (at + 12 < bytes) v.w = *reinterpret_cast<const uint32_t*>(row + at + 12);
+    return v;
+}
+
+// kSwiglu: half of the tile's weight rows are gate rows, half the up rows of the same channels.
+template <bool kSwiglu, int kBN>
+__global__ void __launch_bounds__(k4Threads, 1)
+fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w, const Fp4Args a) {
+    using Shape = Fp4Shape<kBN>;
+    constexpr int kStages = Shape::kStages, kHalf = kBN / 2;
+    extern __shared__ __align__(1024) uint8_t dyn[];
+    __shared__ Fp4Shared<kStages> sh;
+    // codes of all stages first, each on 1024 bytes; then the scales, then the rows on their way out
+    uint8_t* codes = dyn + ((1024u - (smem_u32(dyn) & 1023u)) & 1023u);
+    constexpr int kCodes = Shape::kCodesA + Shape::kCodesB, kScales = Shape::kScalesA + Shape::kScalesB;
+    uint8_t* scales = codes + kStages * kCodes;
+    uint8_t* out_stage = scales + kStages * kScales;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    volatile int* abort = &sh.abort;
+    const uint32_t full = smem_u32(sh.full), staged = smem_u32(sh.scales), done = smem_u32(sh.done);
+    const uint32_t acc_full = smem_u32(sh.acc_full), acc_empty = smem_u32(sh.acc_empty);
+    const uint32_t tile_full = smem_u32(sh.tile_full), tile_empty = smem_u32(sh.tile_empty);
+
+    if (tid == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&sh.full[s], 1);
+            mbar_init(&sh.scales[s], k4ScaleWarps);
+            mbar_init(&sh.done[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&sh.acc_full[b], 1);
+            mbar_init(&sh.acc_empty[b], k4OutWarps);
+        }
+        for (int b = 0; b < k4TileRing; ++b) {
+            mbar_init(&sh.tile_full[b], 1);
+            mbar_init(&sh.tile_empty[b], 2 + k4ScaleWarps + k4OutWarps);
+            sh.tile[b].rows = 0;
+        }
+        mbar_init(&sh.drain, 1);
+        sh.abort = 0;
+        fence_mbar_init();
+        tma_prefetch_desc(&map_x);
+        tma_prefetch_desc(&map_w);
+    }
+    if (warp == 2) tmem_alloc<1>(&sh.tmem, Shape::kCols);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    // All above may run beside the end of the kernel before; the kernel after may do the same.
+    grid_wait();
+    grid_launch_next();
+    const uint32_t tmem = sh.tmem;
+
+    if (warp == 3) {
+        // ---- tiles
+        TileWalk<k4BM> walk;
+        RingPos<k4TileRing> tr;
+        for (int t = blockIdx.x;; t += gridDim.x) {
+            GemmTile tile = {0, 0, 0, 0};
+            const bool some = walk.find(a, min(t, a.most), lane, &tile);
+            if (t >= a.most) tile.rows = 0;  // groups that overlap may have any number of tiles
+            mbar_wait_warp<true>(tr.bar(tile_empty), tr.phase() ^ 1, k4WaitNs, abort);
+            if (__any_sync(0xffffffffu, *abort)) break;
+            if (lane == 0) {
+                sh.tile[tr.slot()] = tile;
+                mbar_arrive(tr.bar(tile_full));
+            }
+            ++tr.n;
+            if (!some || t >= a.most) {
+                walk.cut |= some;
+                break;
+            }
+        }
+        if (walk.cut && a.status && blockIdx.x == 0) flag(a.status, FLAG_CAPACITY);
+    } else if (warp == 0) {
+        if (lane == 0) {
+            // ---- copies of codes
+            RingPos<k4TileRing> tr;
+            Turn<kStages> st;
+            bool ok = true;
+            while (ok) {
+                if (!mbar_wait_or_abort<true>(tr.bar(tile_full), tr.phase(), k4WaitNs, abort)) break;
+                const GemmTile tile = sh.tile[tr.slot()];
+                mbar_arrive(tr.bar(tile_empty));
+                ++tr.n;
+                if (tile.rows == 0) break;
+                const int boxes = (tile.rows + k4BoxRows - 1) / k4BoxRows;
+                const uint32_t bytes = boxes * k4BoxRows * 128 + kBN * 128;
+                const int w0 = kSwiglu ? tile.n * kHalf : tile.n * kBN, w1 = a.N / 2 + w0;
+                for (int kt = 0; kt < a.KT; ++kt) {
+                    if (!mbar_wait_or_abort<true>(done + st.slot * 8, st.phase ^ 1, k4WaitNs, abort)) {
+                        ok = false;
+                        break;
+                    }
+                    uint8_t* sa = codes + st.slot * kCodes;
+                    const uint32_t bar = full + st.slot * 8;
+                    mbar_arrive_expect_tx(&sh.full[st.slot], bytes);
+                    tma_load_3d<1>(sa + Shape::kCodesA, &map_w, kt * 128, w0, tile.g, bar);
+                    if (kSwiglu) tma_load_3d<1>(sa + Shape::kCodesA + kHalf * 128, &map_w, kt * 128, w1, tile.g, bar);
+                    for (int b = 0; b < boxes; ++b)
+                        tma_load_2d<1>(sa + b * k4BoxRows * 128, &map_x, kt * 128, tile.row0 + b * k4BoxRows, bar);
+                    st.next();
+                }
+            }
+            // no copy may be in flight when the block ends, also after a wait that ran out: the last phase that
+            // a stage's copies complete is the one before its next
+            for (int u = 0; u < kStages; ++u) {
+                mbar_wait_bounded(&sh.full[st.slot], st.phase ^ 1, k4WaitNs);
+                st.next();
+            }
+        }
+    } else if (warp == 1) {
+        // ---- copies of scales into tensor memory, products
+        constexpr uint32_t idesc0 = idesc_mxf4(k4BM, kBN, 0), idesc2 = idesc_mxf4(k4BM, kBN, 2);
+        const uint64_t da0 = smem_desc_sw128(codes), db0 = smem_desc_sw128(codes + Shape::kCodesA), ds0 = smem_desc_rows16(scales);
+        RingPos<k4TileRing> tr;
+        Turn<kStages> st;
+        uint32_t set = 0;
+        while (true) {
+            mbar_wait_warp<true>(tr.bar(tile_full), tr.phase(), k4WaitNs, abort);
+            const int rows = sh.tile[tr.slot()].rows;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(tr.bar(tile_empty));
+            const uint32_t c = tr.n & 1, turn = tr.n >> 1 & 1;
+            ++tr.n;
+            if (rows == 0 || __any_sync(0xffffffffu, *abort)) break;
+            mbar_wait_warp<true>(acc_empty + c * 8, turn ^ 1, k4WaitNs, abort);
+#pragma unroll 1
+            for (int kt = 0; kt < a.KT; ++kt) {
+                mbar_wait_warp<true>(full + st.slot * 8, st.phase, k4WaitNs, abort);
+                mbar_wait_warp<true>(staged + st.slot * 8, st.phase, k4WaitNs, abort);
+                tc_fence_after();
+                if (elect_one()) {
+                    const uint32_t sa = tmem + Shape::kScaleAt + set * Shape::kScaleCols, sb = sa + 8;
+                    const uint64_t ds = ds0 + st.slot * (kScales >> 4);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) tmem_copy_scales<1>(sa + h * 4, ds + h * 32);
+#pragma unroll
+                    for (int h = 0; h < 2 * Shape::kChunks; ++h) tmem_copy_scales<1>(sb + h * 4, ds + (Shape::kScalesA >> 4) + h * 32);
+                    const uint32_t at = st.slot * (kCodes >> 4);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        mma_mxf4<1>(tmem + c * kBN, da0 + at + k * 2, db0 + at + k * 2, k & 1 ? idesc2 : idesc0, sa + (k >> 1) * 4,
+                                    sb + (k >> 1) * 4 * Shape::kChunks, kt > 0 || k > 0);
+                    mma_commit<1>(done + st.slot * 8);
+                    if (kt == a.KT - 1) mma_commit<1>(acc_full + c * 8);
+                }
+                __syncwarp();
+                st.next();
+                set ^= 1;
+            }
+        }
+        // every product has finished before tensor memory is freed
+        if (elect_one()) mma_commit<1>(smem_u32(&sh.drain));
+        __syncwarp();
+        mbar_wait_bounded(&sh.drain, 0, k4WaitNs);
+    } else if (warp >= 4 && warp < 4 + k4ScaleWarps) {
+        // ---- scales: thread r those of row r, and of weight rows r and 128 + r, two stages' with one load, the next
+        // two on their way meanwhile
+        const int r = tid - 128, bytes = a.K / 32;
+        RingPos<k4TileRing> tr;
+        Turn<kStages> st;
+        const uint32_t to = (uint32_t)((r & 31) * 16 + (r >> 5) * 4);
+        while (true) {
+            mbar_wait_warp<true>(tr.bar(tile_full), tr.phase(), k4WaitNs, abort);
+            const GemmTile tile = sh.tile[tr.slot()];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(tr.bar(tile_empty));
+            ++tr.n;
+            if (tile.rows == 0 || __any_sync(0xffffffffu, *abort)) break;
+            auto weight_row = [&](int i) {  // of the group, or -1
+                if (i >= kBN) return -1;
+                const int n = !kSwiglu ? tile.n * kBN + i : i < kHalf ? tile.n * kHalf + i : a.N / 2 + tile.n * kHalf + i - kHalf;
+                return n < a.N ? n : -1;
+            };
+            const int n0 = weight_row(r), n1 = weight_row(128 + r);
+            const uint8_t* px = r < tile.rows ? a.x_scales + (int64_t)(tile.row0 + r) * a.x_sstride : nullptr;
+            const uint8_t* p0 = n0 >= 0 ? a.w_scales + ((int64_t)tile.g * a.N + n0) * bytes : nullptr;
+            const uint8_t* p1 = n1 >= 0 ? a.w_scales + ((int64_t)tile.g * a.N + n1) * bytes : nullptr;
+            const uint4 zero = make_uint4(0, 0, 0, 0);
+            uint4 nx, n0v, n1v;
+            auto fetch = [&](int at) {
+                nx = px ? load_scales(px, at, bytes, a.x_vec) : zero;
+                n0v = p0 ? load_scales(p0, at, bytes, a.w_vec) : zero;
+                n1v = Shape::kChunks > 1 && p1 ? load_scales(p1, at, bytes, a.w_vec) : zero;
+            };
+            fetch(0);
+#pragma unroll 1
+            for (int kt = 0; kt < a.KT; kt += 2) {
+                const uint4 vx = nx, v0 = n0v, v1 = n1v;
+                if (kt + 2 < a.KT) fetch(kt * 8 + 16);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    if (kt + h >= a.KT) break;
+                    mbar_wait_warp<true>(done + st.slot * 8, st.phase ^ 1, k4WaitNs, abort);
+                    uint8_t* d = scales + st.slot * kScales + to;
+                    *reinterpret_cast<uint32_t*>(d) = h ? vx.z : vx.x;
+                    *reinterpret_cast<uint32_t*>(d + 512) = h ? vx.w : vx.y;
+                    uint8_t* db = d + Shape::kScalesA;
+                    *reinterpret_cast<uint32_t*>(db) = h ? v0.z : v0.x;
+                    *reinterpret_cast<uint32_t*>(db + 512 * Shape::kChunks) = h ? v0.w : v0.y;
+                    if (Shape::kChunks > 1) {
+                        *reinterpret_cast<uint32_t*>(db + 512) = h ? v1.z : v1.x;
+                        *reinterpret_cast<uint32_t*>(db + 512 * 3) = h ? v1.w : v1.y;
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(staged + st.slot * 8);
+                    st.next();
+                }
+            }
+        }
+    } else if (warp >= 4 + k4ScaleWarps) {
+        // ---- results: a lane a row, 32 columns at a time
+        const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);
+        uint8_t* stage = out_stage + (warp & 3) * Shape::kOut;
+        RingPos<k4TileRing> tr;
+        while (true) {
+            mbar_wait_warp<true>(tr.bar(tile_full), tr.phase(), k4WaitNs, abort);
+            const GemmTile tile = sh.tile[tr.slot()];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(tr.bar(tile_empty));
+            const uint32_t c = tr.n & 1, turn = tr.n >> 1 & 1;
+            ++tr.n;
+            if (tile.rows == 0 || __any_sync(0xffffffffu, *abort)) break;
+            mbar_wait_warp<true>(acc_full + c * 8, turn, k4WaitNs, abort);
+            tc_fence_after();
+            const int first = (warp & 3) * 32, rows = min(32, tile.rows - first);  // of this warp
+            if (rows > 0) {
+                const int64_t row0 = tile.row0 + first;
+                if constexpr (kSwiglu) {
+                    for (int q = 0; q < kHalf / 32; ++q) {
+                        const int ch = tile.n * kHalf + q * 32;
+                        if (ch >= a.N / 2) break;
+                        float g[32], u[32];
+                        tmem_ld(lanes + c * kBN + q * 32, g);
+                        tmem_ld(lanes + c * kBN + kHalf + q * 32, u);
+                        tmem_wait_ld(g);
+                        tmem_wait_ld(u);
+                        float m = 0.0f;
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            g[i] = silu_mul(g[i], u[i]);
+                            m = max_or_nan(m, fabsf(g[i]));
+                        }
+                        const uint32_t b = e8m0_of(m);
+                        const float by = e8m0_inverse(b);
+                        if (lane < rows) {
+                            const int4 v = make_int4((int)e2m1x8(g, by), (int)e2m1x8(g + 8, by), (int)e2m1x8(g + 16, by), (int)e2m1x8(g + 24, by));
+                            *reinterpret_cast<int4*>(static_cast<uint8_t*>(a.out) + (row0 + lane) * a.out_stride + ch / 2) = v;
+                            a.out_scales[(row0 + lane) * a.out_sstride + ch / 32] = (uint8_t)b;
+                        }
+                    }
+                } else {
+                    __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.out) + row0 * a.out_stride;
+                    for (int q = 0; q < kBN / 32; ++q) {
+                        const int n0 = tile.n * kBN + q * 32;
+                        if (n0 >= a.N) break;
+                        float v[32];
+                        tmem_ld(lanes + c * kBN + q * 32, v);
+                        tmem_wait_ld(v);
+                        uint32_t p[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+                            p[i] = *reinterpret_cast<const uint32_t*>(&b);
+                        }
+                        if (a.out_vec && n0 + 32 <= a.N) {
+                            if (lane < rows) {
+                                __nv_bfloat16* d = o + lane * a.out_stride + n0;
+                                if (a.out_wide) {
+                                    st_global_32(d, p);
+                                    st_global_32(d + 16, p + 8);
+                                } else {
+#pragma unroll
+                                    for (int i = 0; i < 4; ++i) reinterpret_cast<int4*>(d)[i] = *reinterpret_cast<const int4*>(p + 4 * i);
+                                }
+                            }
+                        } else {  // through shared memory, so that lanes store neighbours
+                            uint32_t* mine = reinterpret_cast<uint32_t*>(stage + lane * Shape::kOutRow);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) mine[i] = p[i];
+                            __syncwarp();
+                            if (n0 + lane < a.N)
+                                for (int i = 0; i < rows; ++i)
+                                    o[i * a.out_stride + n0 + lane] = *reinterpret_cast<const __nv_bfloat16*>(stage + i * Shape::kOutRow + lane * 2);
+                            __syncwarp();
+                        }
+                    }
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_hand_back(acc_empty + c * 8);
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 2) tmem_free<1>(tmem, Shape::kCols);
+    if (tid == 0 && *abort && a.status) flag(a.status, FLAG_TIMEOUT);
+}
+
+// ---- quantisation ---------------------------------------------------------------------
+// 8 channels a thread, four neighbours a block of 32: bound by memory, loads of 512 bytes a warp.
+__global__ void __launch_bounds__(256) quantize_fp4_kernel(const __nv_bfloat16* x, int64_t x_stride, int64_t rows, int K, uint8_t* codes,
+                                                           int64_t code_stride, uint8_t* scales, int64_t scale_stride) {
+    grid_wait();
+    grid_launch_next();
+    const int per_row = K / 8;
+    const int64_t total = rows * per_row;  // a multiple of 16: groups of four lanes are whole
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < (total + 31) / 32 * 32; i += (int64_t)gridDim.x * 256) {
+        const int64_t row = i / per_row;
+        const int at = (int)(i - row * per_row);
+        float v[8] = {}, m = 0.0f;
+        if (i < total) {
+            const int4 p = ld_nc_na_v4(x + row * x_stride + at * 8);
+            const uint32_t u[4] = {(uint32_t)p.x, (uint32_t)p.y, (uint32_t)p.z, (uint32_t)p.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                v[2 * j] = __uint_as_float(u[j] << 16);
+                v[2 * j + 1] = __uint_as_float(u[j] & 0xffff0000u);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) m = max_or_nan(m, fabsf(v[j]));
+        m = max_or_nan(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        m = max_or_nan(m, __shfl_xor_sync(0xffffffffu, m, 2));
+        const uint32_t b = e8m0_of(m);
+        if (i < total) {
+            *reinterpret_cast<uint32_t*>(codes + row * code_stride + at * 4) = e2m1x8(v, e8m0_inverse(b));
+            if ((at & 3) == 0) scales[row * scale_stride + at / 4] = (uint8_t)b;
+        }
+    }
+}
+
+// ---- host -------------------------------------------------------------------------
+static ep_status check_fp4(const char* fn, const ep_fp4_rows* x, const ep_row_groups* g, const ep_fp4_weight* w, const uint32_t* status_out) {
+    if (!x || !g || !w) return set_error(EP_ERR_INVALID_ARG, "%s: null descriptor", fn);
+    if (w->groups < 1 || w->groups > kMaxGroups)
+        return set_error(EP_ERR_INVALID_ARG, "%s: groups %d outside 1..%d", fn, w->groups, kMaxGroups);
+    if (w->n < 1 || w->n > 0x7fffffff - 512 || w->k < 128 || w->k % 128)
+        return set_error(EP_ERR_INVALID_ARG, "%s: weight rows %d, channels %d (a multiple of 128)", fn, w->n, w->k);
+    if (!w->codes || !w->scales || !aligned16(w->codes) || !aligned_to(w->scales, 4))
+        return set_error(EP_ERR_INVALID_ARG, "%s: weight codes (16-byte aligned) and scales (4-byte aligned) are required", fn);
+    if (x->rows < 0 || x->rows > 0x7fffffff - 2 * k4BM) return set_error(EP_ERR_INVALID_ARG, "%s: %lld rows", fn, (long long)x->rows);
+    if (x->rows > 0) {
+        if (!x->codes || !x->scales || !aligned16(x->codes) || !aligned_to(x->scales, 4))
+            return set_error(EP_ERR_INVALID_ARG, "%s: row codes (16-byte aligned) and scales (4-byte aligned) are required", fn);
+        if (x->code_stride < w->k / 2 || x->code_stride % 16 || x->scale_stride < w->k / 32 || x->scale_stride % 4)
+            return set_error(EP_ERR_INVALID_ARG, "%s: row strides %lld, %lld for %d channels", fn, (long long)x->code_stride,
+                             (long long)x->scale_stride, w->k);
+    }
+    if (!aligned_to(g->counts, 4) || !aligned_to(g->offsets, 4) || !aligned_to(g->bases, 4) || !aligned_to(status_out, 4))
+        return set_error(EP_ERR_INVALID_ARG, "%s: a pointer is not aligned to its elements", fn);
+    if (g->bases && g->per_base < 1) return set_error(EP_ERR_INVALID_ARG, "%s: groups per base %d", fn, g->per_base);
+    if (g->stride < 0 || g->expected < 0)
+        return set_error(EP_ERR_INVALID_ARG, "%s: group stride %lld, expected rows %lld", fn, (long long)g->stride, (long long)g->expected);
+    return EP_OK;
+}
+
+template <bool kSwiglu, int kBN>
+static ep_status launch_fp4_shape(const char* fn, const ep_fp4_rows* x, const ep_fp4_weight* w, Fp4Args a, int sms, int dev, void* stream) {
+    using Shape = Fp4Shape<kBN>;
+    constexpr int kTileN = kSwiglu ? kBN / 2 : kBN;
+    a.n_tiles = ((kSwiglu ? w->n / 2 : w->n) + kTileN - 1) / kTileN;
+    const int64_t most = most_tiles(a, k4BM);
+    if (most > kMaxTiles) return set_error(EP_ERR_INVALID_ARG, "%s: %lld tiles", fn, (long long)most);
+    a.most = (int)most;
+    CUtensorMap map_x, map_w;
+    {
+        const cuuint64_t dims[2] = {(cuuint64_t)w->k / 2, (cuuint64_t)x->rows};
+        const cuuint64_t strides[1] = {(cuuint64_t)x->code_stride};
+        const cuuint32_t box[2] = {128, k4BoxRows};
+        EP_TRY(encode_rows(&map_x, x->codes, 2, dims, strides, box, fn));
+    }
+    {
+        const cuuint64_t dims[3] = {(cuuint64_t)w->k / 2, (cuuint64_t)w->n, (cuuint64_t)w->groups};
+        const cuuint64_t strides[2] = {(cuuint64_t)w->k / 2, (cuuint64_t)w->k / 2 * (cuuint64_t)w->n};
+        const cuuint32_t box[3] = {128, (cuuint32_t)kTileN, 1};
+        EP_TRY(encode_rows(&map_w, w->codes, 3, dims, strides, box, fn));
+    }
+    static std::atomic<bool> known[kMaxDevicesTracked];  // devices whose launch attribute is set
+    if (dev >= kMaxDevicesTracked || !known[dev].load(std::memory_order_relaxed)) {
+        EP_CUDA(cudaFuncSetAttribute(fp4_gemm_kernel<kSwiglu, kBN>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Shape::kSmem));
+        if (dev < kMaxDevicesTracked) known[dev].store(true, std::memory_order_relaxed);
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(most < sms ? most : sms));
+    cfg.blockDim = dim3(k4Threads);
+    cfg.dynamicSmemBytes = Shape::kSmem;
+    cfg.stream = as_stream(stream);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    EP_CUDA(cudaLaunchKernelEx(&cfg, fp4_gemm_kernel<kSwiglu, kBN>, map_x, map_w, a));
+    return EP_OK;
+}
+
+template <bool kSwiglu>
+static ep_status launch_fp4(const char* fn, const ep_fp4_rows* x, const ep_row_groups* g, const ep_fp4_weight* w, Fp4Args a, void* stream) {
+    a.x_scales = x->scales;
+    a.x_sstride = x->scale_stride;
+    a.x_vec = aligned16(x->scales) && x->scale_stride % 16 == 0;
+    a.w_scales = w->scales;
+    a.w_vec = aligned16(w->scales) && w->k % 512 == 0;
+    a.G = w->groups;
+    a.N = w->n;
+    a.K = w->k;
+    a.KT = (w->k + k4BK - 1) / k4BK;
+    a.counts = g->counts;
+    a.offsets = g->offsets;
+    a.bases = g->bases;
+    a.per_base = g->per_base;
+    a.group_stride = g->stride;
+    a.rows = x->rows;
+    int dev = 0, sms = 0;
+    EP_CUDA(cudaGetDevice(&dev));
+    EP_CUDA(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
+    a.n_tiles = (w->n + 191) / 192;
+    if (most_tiles(a, k4BM) * 2 <= sms) return launch_fp4_shape<kSwiglu, 64>(fn, x, w, a, sms, dev, stream);
+    return launch_fp4_shape<kSwiglu, 192>(fn, x, w, a, sms, dev, stream);
+}
+
+}  // namespace ep
+
+using namespace ep;
+
+extern "C" int64_t ep_fp4_row_bytes(int hidden) { return hidden > 0 ? fp4_row_bytes(hidden) : 0; }
+
+extern "C" ep_status ep_quantize_fp4(const void* x, int64_t x_stride, int64_t rows, int32_t channels, uint8_t* codes, int64_t code_stride,
+                                     uint8_t* scales, int64_t scale_stride, void* stream) {
+    const char* fn = "ep_quantize_fp4";
+    if (rows < 0 || rows > 0x7fffffff || channels < 128 || channels % 128)
+        return set_error(EP_ERR_INVALID_ARG, "%s: %lld rows of %d channels (a multiple of 128)", fn, (long long)rows, channels);
+    if (rows == 0) return EP_OK;
+    if (!x || !codes || !scales || !aligned16(x) || !aligned16(codes) || !aligned_to(scales, 4))
+        return set_error(EP_ERR_INVALID_ARG, "%s: x and codes (16-byte aligned) and scales (4-byte aligned) are required", fn);
+    if (x_stride % 8 || code_stride % 16 || scale_stride % 4 ||
+        (rows > 1 && (x_stride < channels || code_stride < channels / 2 || scale_stride < channels / 32)))
+        return set_error(EP_ERR_INVALID_ARG, "%s: row strides %lld, %lld, %lld for %d channels", fn, (long long)x_stride, (long long)code_stride,
+                         (long long)scale_stride, channels);
+    int dev = 0, sms = 0;
+    EP_CUDA(cudaGetDevice(&dev));
+    EP_CUDA(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
+    const int64_t need = (rows * (channels / 8) + 255) / 256, most = (int64_t)sms * 8;
+    return launch_next(quantize_fp4_kernel, need < most ? need : most, 256, stream, static_cast<const __nv_bfloat16*>(x), x_stride, rows, channels,
+                       codes, code_stride, scales, scale_stride);
+}
+
+extern "C" ep_status ep_dispatch_permuted_fp4(ep_ctx* c, const uint8_t* xq, const int64_t* topk_idx, const float* topk_weights,
+                                              const ep_dispatch_handle* h, uint8_t* permuted_xq, int32_t* perm_src_token, float* perm_weight,
+                                              int64_t perm_capacity_rows, void* stream) {
+    if (!c) return set_error(EP_ERR_INVALID_ARG, "ctx is NULL");
+    if (c->cfg.hidden % 128) return set_error(EP_ERR_INVALID_ARG, "FP4 rows need hidden %% 128 == 0");
+    return dispatch_permuted_rows(c, xq, fp4_row_bytes(c->cfg.hidden), topk_idx, topk_weights, h, permuted_xq, perm_src_token, perm_weight,
+                                  perm_capacity_rows, stream);
+}
+
+extern "C" ep_status ep_expert_gemm_fp4(const ep_fp4_rows* x, const ep_row_groups* groups, const ep_fp4_weight* w, void* out, int64_t out_stride,
+                                        uint32_t* status_out, void* stream) {
+    const char* fn = "ep_expert_gemm_fp4";
+    EP_TRY(check_fp4(fn, x, groups, w, status_out));
+    if (x->rows == 0) return EP_OK;
+    if (!out || out_stride < w->n || !aligned_to(out, 2))
+        return set_error(EP_ERR_INVALID_ARG, "%s: output (2-byte aligned), stride %lld for %d channels", fn, (long long)out_stride, w->n);
+    Fp4Args a{};
+    a.out = out;
+    a.out_stride = out_stride;
+    a.out_vec = aligned16(out) && out_stride % 8 == 0;
+    a.out_wide = aligned_to(out, 32) && out_stride % 16 == 0;
+    a.status = status_out;
+    return launch_fp4<false>(fn, x, groups, w, a, stream);
+}
+
+extern "C" ep_status ep_expert_swiglu_fp4(const ep_fp4_rows* x, const ep_row_groups* groups, const ep_fp4_weight* w13, uint8_t* out,
+                                          int64_t out_stride, uint8_t* out_scales, int64_t out_scale_stride, uint32_t* status_out, void* stream) {
+    const char* fn = "ep_expert_swiglu_fp4";
+    EP_TRY(check_fp4(fn, x, groups, w13, status_out));
+    if (w13->n % 256) return set_error(EP_ERR_INVALID_ARG, "%s: %d weight rows (gate and up, each a multiple of 128)", fn, w13->n);
+    if (x->rows == 0) return EP_OK;
+    const int inter = w13->n / 2;
+    if (!out || !out_scales || !aligned16(out) || !aligned_to(out_scales, 4) || out_stride < inter / 2 || out_stride % 16 ||
+        out_scale_stride < inter / 32 || out_scale_stride % 4)
+        return set_error(EP_ERR_INVALID_ARG, "%s: output rows (16-byte aligned, strides %lld, %lld) for %d channels", fn, (long long)out_stride,
+                         (long long)out_scale_stride, inter);
+    Fp4Args a{};
+    a.out = out;
+    a.out_stride = out_stride;
+    a.out_scales = out_scales;
+    a.out_sstride = out_scale_stride;
+    a.status = status_out;
+    return launch_fp4<true>(fn, x, groups, w13, a, stream);
+}

@@ -36,7 +36,7 @@
 #include <initializer_list>
 
 #include "ep_fp8.cuh"
-#include "ep_tcgen05.cuh"
+#include "ep_groups.cuh"
 
 namespace ep {
 
@@ -66,22 +66,15 @@ struct GemmShape {
 constexpr int kTileRing = 4;            // tiles announced ahead
 constexpr int kScaleChunk = 8;          // blocks of K whose scales are staged together
 constexpr int kScaleRing = 2;
-constexpr int kMaxGroups = 4096;
-constexpr int kMaxTiles = 1 << 25;      // 32 groups' tiles, and a block's next tile, stay within 31 bits; no memory holds more
-constexpr int kChunkRows = 2048;       // rows that share a pass over the weight's tiles
 constexpr int kSplitStride = kBN + 4;  // floats of a row of sums: rows fall into other banks
 constexpr int64_t kGemmWaitNs = 2000000000ll;
 
-struct GemmArgs {
+struct GemmArgs : TileArgs {
     const float* x_scales;
     int64_t x_sstride;
     const float* w_scales;
     int64_t w_sgroup;   // floats of one group's scales
-    int G, N, K, KB, n_tiles;
-    int most;           // tiles of groups that share no row, at most
-    const int32_t *counts, *offsets, *bases;
-    int per_base;
-    int64_t group_stride, rows;
+    int N, K, KB;
     void* out;          // bf16 rows, or e4m3 codes
     int64_t out_stride; // elements
     float* out_scales;
@@ -91,12 +84,6 @@ struct GemmArgs {
     bool out_clip;      // rows end at a multiple of 16 bytes, so that a tiled copy that crosses their end is cut there
     bool x_vec;         // 16-byte loads of row scales
     uint32_t* status;
-};
-
-struct GemmTile {
-    int g, n;   // group, column tile
-    int row0;   // first row
-    int rows;   // 1 .. rows of a tile; 0: no tile is left
 };
 
 struct GemmShared {
@@ -111,89 +98,9 @@ struct GemmShared {
     float scale[kScaleRing][kScaleChunk][2][kBM];
 };
 
-__device__ __forceinline__ int64_t group_first(const GemmArgs& a, int g) {
-    int64_t r = a.offsets ? (int64_t)a.offsets[g] : (int64_t)g * a.group_stride;
-    if (a.bases) r += a.bases[g / a.per_base];
-    return r;
-}
-// Rows of group g inside the arrays: what lies past their end is cut off and flagged.
-__device__ __forceinline__ int group_rows(const GemmArgs& a, int g, bool* cut) {
-    int64_t n = a.counts ? (int64_t)a.counts[g] : a.group_stride;
-    const int64_t f = group_first(a, g);
-    if (n <= 0) return 0;
-    if (!a.offsets && n > a.group_stride) {  // more than its region holds
-        *cut = true;
-        n = a.group_stride;
-    }
-    if (f < 0 || f >= a.rows) {
-        *cut = true;
-        return 0;
-    }
-    if (f + n > a.rows) {
-        *cut = true;
-        n = a.rows - f;
-    }
-    return (int)n;
-}
-
-// Position in a ring of barriers, by the number of steps taken: the slot's
-// barrier and the parity of its next phase.  kSize is a power of two.
-template <int kSize>
-struct RingPos {
-    uint32_t n = 0;
-    __device__ __forceinline__ int slot() const { return n & (kSize - 1); }
-    __device__ __forceinline__ uint32_t phase() const { return n / kSize & 1; }
-    __device__ __forceinline__ uint32_t bar(uint32_t first) const { return first + slot() * 8; }
-};
 // The stages and accumulators need none: every tile starts at stage 0 and
 // accumulator 0, so that in the unrolled loops both are constants, and bit u of
 // a mask is the parity of slot u's next phase.
-
-// One warp walks the groups for tile t, t + units, ...: 32 groups at a time,
-// each lane one group's tiles.  Groups in order; inside a group, chunks of
-// kChunkRows rows, column tiles inside a chunk, row tiles innermost, so that
-// what runs at the same time shares a chunk of rows and few weight tiles.
-template <int kTileM>
-struct TileWalk {
-    static constexpr int kChunkM = kChunkRows / kTileM;
-    int g0 = -32, start = 0, sum = 0;  // batch of groups, its first tile, its tiles
-    int inc, tiles, rows, first;       // this lane's group: tiles up to and with it, tiles, rows, first row
-    bool cut = false;
-
-    // false: no tile t.  A group has at most kMaxTiles tiles, and t is no larger, so that no sum passes 31 bits.
-    __device__ __forceinline__ bool find(const GemmArgs& a, int t, int lane, GemmTile* out) {
-        while (t >= start + sum) {
-            start += sum;
-            g0 += 32;
-            if (g0 >= a.G) {
-                sum = 0;
-                g0 = a.G;
-                return false;
-            }
-            const int g = g0 + lane;
-            rows = g < a.G ? group_rows(a, g, &cut) : 0;
-            first = rows ? (int)group_first(a, g) : 0;
-            tiles = (rows + kTileM - 1) / kTileM * a.n_tiles;
-            inc = tiles;
-            for (int o = 1; o < 32; o <<= 1) {
-                const int v = __shfl_up_sync(0xffffffffu, inc, o);
-                if (lane >= o) inc += v;
-            }
-            sum = __shfl_sync(0xffffffffu, inc, 31);
-        }
-        const int src = __ffs(__ballot_sync(0xffffffffu, t < start + inc)) - 1;
-        const int n = __shfl_sync(0xffffffffu, rows, src);
-        int r = t - start - __shfl_sync(0xffffffffu, inc - tiles, src);
-        const int mt = (n + kTileM - 1) / kTileM, chunk = r / (kChunkM * a.n_tiles);
-        r -= chunk * kChunkM * a.n_tiles;
-        const int m0 = chunk * kChunkM, mc = min(kChunkM, mt - m0), m = m0 + r % mc;
-        out->g = g0 + src;
-        out->n = r / mc;
-        out->row0 = __shfl_sync(0xffffffffu, first, src) + m * kTileM;
-        out->rows = min(kTileM, n - m * kTileM);
-        return true;
-    }
-};
 
 // kSwiglu: the tile's 256 weight rows are 128 gate rows and the 128 up rows of
 // the same channels; otherwise 256 consecutive rows.
@@ -719,13 +626,6 @@ static ep_status check_products(const char* fn, const ep_fp8_rows* x, const ep_r
     if (g->stride < 0 || g->expected < 0)
         return set_error(EP_ERR_INVALID_ARG, "%s: group stride %lld, expected rows %lld", fn, (long long)g->stride, (long long)g->expected);
     return EP_OK;
-}
-
-// Tiles of a launch, at most: a group's last tile may be partial, and a group
-// with a tile has a row.
-static int64_t most_tiles(const GemmArgs& a, int tile_rows) {
-    const int64_t most = (a.rows + (int64_t)a.G * (tile_rows - 1)) / tile_rows;
-    return (most < a.rows ? most : a.rows) * a.n_tiles;
 }
 
 template <bool kSwiglu, int kCtas, bool kSplit>

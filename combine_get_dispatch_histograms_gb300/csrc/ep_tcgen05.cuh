@@ -238,6 +238,35 @@ __device__ __forceinline__ void mma_bf16_ss(uint32_t d, uint64_t a, uint64_t b, 
         "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
         : "memory");
 }
+// D[kCtas * 128 x N] (+)= A[kCtas * 128 x 64] B[N x 64]^T, two e2m1 codes a byte in shared memory, each 32 codes times
+// 2^(their E8M0 byte - 127).  sa, sb: columns of tensor memory with the scales: row r's in lane r % 32 (of every 32 lanes)
+// of column r / 32, four bytes for 128 codes; the descriptor says which two of them (idesc_mxf4).
+template <int kCtas>
+__device__ __forceinline__ void mma_mxf4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa, uint32_t sb, bool add) {
+    if constexpr (kCtas == 2)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.u32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"((uint32_t)add)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.u32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"((uint32_t)add)
+            : "memory");
+}
+// 512 bytes of shared memory, 32 rows of 16, to 4 columns of tensor memory, the same in every 32 lanes; before the
+// products that this thread issues later, after those that it issued before.
+template <int kCtas>
+__device__ __forceinline__ void tmem_copy_scales(uint32_t d, uint64_t desc) {
+    if constexpr (kCtas == 2)
+        asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(d), "l"(desc) : "memory");
+    else
+        asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(d), "l"(desc) : "memory");
+}
 // Arrives on `bar` (of both blocks) when every tcgen05.mma this thread issued has finished.
 template <int kCtas>
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
@@ -306,12 +335,22 @@ __device__ __forceinline__ void tmem_wait_ld(float (&v)[16]) {
 __device__ __forceinline__ uint64_t smem_desc_sw128(const void* p) {
     return (uint64_t)((smem_u32(p) & 0x3ffffu) >> 4) | (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
 }
+// The same of 32 rows of 16 bytes, one behind the other (8-row atoms of 128 bytes, no swizzle).
+__device__ __forceinline__ uint64_t smem_desc_rows16(const void* p) {
+    return (uint64_t)((smem_u32(p) & 0x3ffffu) >> 4) | (8ull << 32) | (1ull << 46);
+}
 // Instruction descriptor: fp32 accumulator, e4m3 x e4m3, both K-major.
 __host__ __device__ constexpr uint32_t idesc_e4m3(int m, int n) {
     return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
 // The same with bf16 x bf16.
 __host__ __device__ constexpr uint32_t idesc_bf16(int m, int n) { return idesc_e4m3(m, n) | (1u << 7) | (1u << 10); }
+
+// e2m1 x e2m1 with E8M0 scales, both K-major; scale: 0 or 2, the first of the two bytes of both scale columns.
+__host__ __device__ constexpr uint32_t idesc_mxf4(int m, int n, int scale) {
+    return ((uint32_t)scale << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | (1u << 23) | ((uint32_t)(m >> 4) << 24) |
+           ((uint32_t)scale << 29);
+}
 
 // silu(g) * u with the approximate power and reciprocal.  Off by at most 8 * 2^-23 of itself for g >= 0; for g < 0 by
 // |g| * 2^-23 more, since rounding the power's argument g * log2(e) moves the power by up to 2^-24 |g| of itself, and so

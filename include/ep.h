@@ -483,6 +483,59 @@ ep_status ep_moe_tokens(const void* x, int64_t x_stride, int32_t num_tokens, con
                         void* stream);
 
 /* ------------------------------------------------------------------------ */
+/* The same in 4 bits: MXFP4 rows and weights (OCP Microscaling Formats 1.0)    */
+/* ------------------------------------------------------------------------ */
+
+/* Two e2m1 codes a byte, the lower channel in the lower half, and per 32 channels
+ * one E8M0 byte b: their scale is 2^(b - 127), 255 a NaN. */
+
+/* Bytes of one FP4 row: H / 2 of codes, then H / 32 scales, padded to 16. */
+int64_t ep_fp4_row_bytes(int hidden);
+
+/* Rows of bf16 [rows][channels] (channels a multiple of 128) to MXFP4: per 32
+ * channels b = max(floor(log2 amax) - 2 + 127, 0), code = e2m1 of x * 2^(127 - b),
+ * nearest even, with 6 as the largest magnitude; an infinity or a NaN among the 32
+ * makes b 255.  x_stride in elements, a multiple of 8 (x 16-byte aligned);
+ * code_stride (a multiple of 16) and scale_stride (of 4) in bytes. */
+ep_status ep_quantize_fp4(const void* x, int64_t x_stride, int64_t rows, int32_t channels, uint8_t* codes, int64_t code_stride,
+                          uint8_t* scales, int64_t scale_stride, void* stream);
+
+/* ep_dispatch_permuted on FP4 rows: same metadata, same row positions. */
+ep_status ep_dispatch_permuted_fp4(ep_ctx* ctx, const uint8_t* xq, const int64_t* topk_idx, const float* topk_weights,
+                                   const ep_dispatch_handle* handle, uint8_t* permuted_xq, int32_t* perm_src_token, float* perm_weight,
+                                   int64_t perm_capacity_rows, void* stream);
+
+/* FP4 rows: row r has its codes at codes + r * code_stride (a multiple of 16) and its
+ * scales at scales + r * scale_stride (a multiple of 4; 4-byte aligned), bytes both. */
+typedef struct ep_fp4_rows {
+    const uint8_t* codes;
+    int64_t code_stride;
+    const uint8_t* scales;
+    int64_t scale_stride;
+    int64_t rows; /* rows that the arrays hold: nothing past them is read or written */
+} ep_fp4_rows;
+
+/* FP4 weights: codes [groups][n][k / 2] (contiguous, 16-byte aligned) and scales
+ * [groups][n][k / 32] (4-byte aligned).  groups 1..4096, k a multiple of 128. */
+typedef struct ep_fp4_weight {
+    const uint8_t* codes;
+    const uint8_t* scales;
+    int32_t groups, n, k;
+} ep_fp4_weight;
+
+/* ep_expert_gemm on FP4 rows and weights: y[r][c] = bf16( sum over k of x[r][k] *
+ * w[g][c][k] ), codes times scales, the sum in fp32 on the tensor cores, rounded
+ * once.  Groups, capacity and status as there. */
+ep_status ep_expert_gemm_fp4(const ep_fp4_rows* x, const ep_row_groups* groups, const ep_fp4_weight* w, void* out, int64_t out_stride,
+                             uint32_t* status_out, void* stream);
+/* ep_expert_swiglu on FP4 rows and weights; h = silu(gate) * up in fp32 leaves as FP4
+ * rows of I channels by the rule of ep_quantize_fp4 (I a multiple of 128):
+ * out codes, out_stride bytes apart (a multiple of 16), and out_scales,
+ * out_scale_stride bytes apart (a multiple of 4). */
+ep_status ep_expert_swiglu_fp4(const ep_fp4_rows* x, const ep_row_groups* groups, const ep_fp4_weight* w13, uint8_t* out, int64_t out_stride,
+                               uint8_t* out_scales, int64_t out_scale_stride, uint32_t* status_out, void* stream);
+
+/* ------------------------------------------------------------------------ */
 /* What comes before dispatch: the norm and the router.  The pages take x,     */
 /* topk_idx and topk_weights as given, so they name none of it                 */
 /* ------------------------------------------------------------------------ */
