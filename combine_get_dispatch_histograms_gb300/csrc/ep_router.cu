@@ -91,9 +91,16 @@ __device__ __forceinline__ void load_logits(const T* row, int E, int lane, bool 
     for (int i = 0; i < V; ++i) v[i] = lane * V + i < E ? (float)row[lane * V + i] : -INFINITY;
 }
 
+// e^x for x <= 0.  Rounding x * log2(e) moves the result by |x| 2^-24 of itself, log2(e)'s own rounding by less, and
+// the approximate power by 2 units of 2^-23: (|x| + 4) 2^-23 covers it.  Below 2^-126 the result is 0.
+__device__ __forceinline__ float exp_of(float x) {
+    float e;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * 1.4426950408889634f));
+    return e;
+}
 // sigmoid(l) and its slope, from e^-|l|: neither cancels.
 __device__ __forceinline__ float sigmoid_of(float l, float* slope) {
-    const float e = expf(-fabsf(l)), r = 1.0f / (1.0f + e);
+    const float e = exp_of(-fabsf(l)), r = __fdividef(1.0f, 1.0f + e);
     *slope = e * r * r;
     return l < 0.0f ? e * r : r;  // a NaN stays one: r
 }
@@ -119,7 +126,7 @@ __device__ __forceinline__ void scores(const float (&l)[V], int E, int lane, flo
         m = warp_max(m);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            p[i] = lane * V + i < E ? expf(l[i] - m) : 0.0f;
+            p[i] = lane * V + i < E ? exp_of(l[i] - m) : 0.0f;
             s += p[i];
         }
         s = 1.0f / warp_sum(s);
@@ -130,7 +137,48 @@ __device__ __forceinline__ void scores(const float (&l)[V], int E, int lane, flo
     }
 }
 
-// The groups that stay: bit g of the result.  A group's score is the sum of its two largest keys.
+// A lane's two largest keys and where they are, of those not taken yet (bit i of `taken`: key i).
+template <int V>
+struct LaneTop {
+    uint32_t k1, k2;
+    int i1, i2;
+    __device__ __forceinline__ void scan(const uint32_t (&key)[V], uint32_t taken) {
+        k1 = k2 = 0;
+        i1 = i2 = 0;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const uint32_t k = taken >> i & 1 ? 0 : key[i];
+            if (k > k1) {
+                k2 = k1, i2 = i1;
+                k1 = k, i1 = i;
+            } else if (k > k2) {
+                k2 = k, i2 = i;
+            }
+        }
+    }
+};
+
+// Whether this lane's group stays; a group's score is the sum of its two largest keys.  Lanes that hold whole groups'
+// parts (V divides the group, a power of two of lanes each): the lanes' two largest are merged, and a group's rank is the
+// number of groups before it.
+template <int V>
+__device__ __forceinline__ bool keep_group(const LaneTop<V>& top, const RouterArgs& a, int lane, int lanes) {
+    uint32_t hi = top.k1, lo = V > 1 ? top.k2 : 0;
+    for (int o = 1; o < lanes; o <<= 1) {
+        const uint32_t h = __shfl_xor_sync(kAll, hi, o), l = __shfl_xor_sync(kAll, lo, o);
+        lo = max(max(lo, l), min(hi, h));
+        hi = max(hi, h);
+    }
+    const uint32_t score = V * lanes > 1 ? ordered(unordered(hi) + unordered(lo)) : hi;
+    const int mine = lane / lanes;
+    int before = 0;
+    for (int g = 0; g < a.groups; ++g) {
+        const uint32_t other = __shfl_sync(kAll, score, g * lanes);
+        before += other > score || (other == score && g < mine);
+    }
+    return before < a.topk_groups;
+}
+// Any other groups, one after the other: bit g of the result.
 template <int V>
 __device__ __forceinline__ uint32_t choose_groups(const uint32_t (&key)[V], const RouterArgs& a, int lane) {
     const int size = a.E / a.groups;
@@ -140,7 +188,7 @@ __device__ __forceinline__ uint32_t choose_groups(const uint32_t (&key)[V], cons
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int e = lane * V + i - g * size;
-            const uint32_t k = e >= 0 && e < size ? max(key[i], kKeyNegInf) : 0;
+            const uint32_t k = e >= 0 && e < size ? key[i] : 0;
             lo = max(lo, min(hi, k));
             hi = max(hi, k);
         }
@@ -160,11 +208,13 @@ __device__ __forceinline__ uint32_t choose_groups(const uint32_t (&key)[V], cons
     return kept;
 }
 
-template <typename T, int V, bool kSigmoid>
+template <typename T, int V, bool kSigmoid, bool kGroups>
 __global__ void __launch_bounds__(kRouterThreads) route_kernel(const RouterArgs a) {
     const int lane = threadIdx.x & 31;
     grid_wait();
     grid_launch_next();
+    const int size = kGroups ? a.E / a.groups : 0;
+    const bool whole = kGroups && size % V == 0 && (size / V & (size / V - 1)) == 0;
     for (int64_t t = (int64_t)blockIdx.x * kRouterWarps + (threadIdx.x >> 5); t < a.tokens; t += (int64_t)gridDim.x * kRouterWarps) {
         if (a.mask && !a.mask[t]) {
             if (lane < a.K) {
@@ -176,52 +226,52 @@ __global__ void __launch_bounds__(kRouterThreads) route_kernel(const RouterArgs 
         const T* row = static_cast<const T*>(a.logits) + t * a.stride;
         float l[V];
         load_logits(row, a.E, lane, a.vec, l);
-        uint32_t key[V];
+        uint32_t key[V];  // 0 past the last expert, kKeyNegInf for -inf
+        if (a.bias) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int e = lane * V + i;
-            key[i] = e < a.E ? ordered(a.bias ? l[i] + a.bias[e] : l[i]) : 0;
-        }
-        uint32_t kept = kAll;
-        if (a.groups > 1) kept = choose_groups(key, a, lane);
-        const int size = a.E / a.groups;
-        uint32_t best = 0;
+            for (int i = 0; i < V; ++i) {
+                const int e = lane * V + i;
+                key[i] = e < a.E ? ordered(l[i] + a.bias[e]) : 0;
+            }
+        } else {
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int e = lane * V + i;
-            if (key[i] <= kKeyNegInf || (a.groups > 1 && !(kept >> min(e / size, 31) & 1))) key[i] = 0;
-            best = max(best, key[i]);
+            for (int i = 0; i < V; ++i) key[i] = lane * V + i < a.E ? ordered(l[i]) : 0;
         }
-        // choice k ends in lane k: its expert and its logit
+        LaneTop<V> top;
+        uint32_t taken = 0;
+        if (kGroups && !whole) {
+            const uint32_t kept = choose_groups(key, a, lane);
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (!(kept >> min((lane * V + i) / size, 31) & 1)) key[i] = 0;
+        }
+        top.scan(key, 0);
+        if (kGroups && whole && !keep_group(top, a, lane, size / V)) {
+            taken = kAll;
+            top.k1 = top.k2 = 0;
+        }
+        // choice k ends in lane k
         int expert = -1;
-        float logit = -INFINITY;
+        bool second = true;  // k2 is known
         for (int k = 0; k < a.K; ++k) {
-            const uint32_t top = __reduce_max_sync(kAll, best);
-            if (top == 0) break;
-            const int owner = __ffs(__ballot_sync(kAll, best == top)) - 1;
-            int at = 0;
-            float mine = 0.0f;
+            const uint32_t most = __reduce_max_sync(kAll, top.k1);
+            if (most <= kKeyNegInf) break;
+            const int owner = __ffs(__ballot_sync(kAll, top.k1 == most)) - 1;
+            const int at = __shfl_sync(kAll, top.i1, owner);
+            if (lane == k) expert = owner * V + at;
             if (lane == owner) {
-                bool found = false;
-                best = 0;
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    if (!found && key[i] == top) {
-                        found = true;
-                        at = i;
-                        mine = l[i];
-                        key[i] = 0;
-                    }
-                    best = max(best, key[i]);
+                taken |= 1u << top.i1;
+                if (V == 1 || second) {
+                    top.k1 = V == 1 ? 0 : top.k2;
+                    top.i1 = top.i2;
+                    second = false;
+                } else {
+                    top.scan(key, taken);
+                    second = true;
                 }
             }
-            at = __shfl_sync(kAll, at, owner);
-            mine = __shfl_sync(kAll, mine, owner);
-            if (lane == k) {
-                expert = owner * V + at;
-                logit = mine;
-            }
         }
+        const float logit = expert >= 0 ? (float)row[expert] : -INFINITY;
         float w;
         if (kSigmoid) {
             float slope;
@@ -229,12 +279,12 @@ __global__ void __launch_bounds__(kRouterThreads) route_kernel(const RouterArgs 
             if (a.normalize) w /= warp_sum(w) + 1e-20f;
         } else if (a.normalize) {
             const float m = warp_max(logit);
-            w = expert >= 0 ? expf(logit - m) : 0.0f;
+            w = expert >= 0 ? exp_of(logit - m) : 0.0f;
             w /= warp_sum(w);
         } else {
-            float p[V], slope[V], top, by;
-            scores<V, false>(l, a.E, lane, p, slope, &top, &by);
-            w = expf(logit - top) * by;
+            float p[V], slope[V], most, by;
+            scores<V, false>(l, a.E, lane, p, slope, &most, &by);
+            w = exp_of(logit - most) * by;
         }
         if (lane < a.K) {
             a.idx[t * a.K + lane] = expert;
@@ -429,9 +479,28 @@ __device__ __forceinline__ void store_logits(T* row, int E, int lane, bool vec, 
         if (lane * V + i < E) row[lane * V + i] = (T)v[i];
 }
 
+template <int V>
+__device__ __forceinline__ void add_shared(const float* p, float (&d)[V]) {
+    if constexpr (V % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < V; i += 4) {
+            const float4 v = *reinterpret_cast<const float4*>(p + i);
+            d[i] += v.x, d[i + 1] += v.y, d[i + 2] += v.z, d[i + 3] += v.w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) d[i] += p[i];
+    }
+}
+
 template <typename T, int V, bool kSigmoid>
 __global__ void __launch_bounds__(kRouterThreads) router_backward_kernel(const RouterBackArgs a) {
+    __shared__ __align__(16) float rows[kRouterWarps][32 * V];
     const int lane = threadIdx.x & 31;
+    float* mine = rows[threadIdx.x >> 5];
+#pragma unroll
+    for (int i = 0; i < V; ++i) mine[i * 32 + lane] = 0.0f;
+    __syncwarp();
     grid_wait();
     grid_launch_next();
     const float dloss = a.factors ? *a.dloss : 0.0f;
@@ -474,7 +543,7 @@ __global__ void __launch_bounds__(kRouterThreads) router_backward_kernel(const R
                 for (int i = 0; i < V; ++i) d[i] = dloss * (fv[i] - sum) * (kSigmoid ? slope[i] * by : p[i]);
             }
             if (!kSigmoid && !a.normalize && a.dweights) {
-                near = e >= 0 ? expf(logit - top) * by * g : 0.0f;
+                near = e >= 0 ? exp_of(logit - top) * by * g : 0.0f;
                 inner = warp_sum(near);
 #pragma unroll
                 for (int i = 0; i < V; ++i) d[i] -= p[i] * inner;
@@ -494,21 +563,35 @@ __global__ void __launch_bounds__(kRouterThreads) router_backward_kernel(const R
                 }
             } else {
                 const float m = warp_max(logit);
-                float w = e >= 0 ? expf(logit - m) : 0.0f;
+                float w = e >= 0 ? exp_of(logit - m) : 0.0f;
                 w /= warp_sum(w);
                 inner = warp_sum(w * g);
                 near = w * (g - inner);
             }
             if (e < 0) near = 0.0f;
         }
-        if (a.dweights)
-            for (int k = 0; k < a.K; ++k) {
-                const int at = __shfl_sync(kAll, e, k) - lane * V;
-                const float v = __shfl_sync(kAll, near, k);
-#pragma unroll
-                for (int i = 0; i < V; ++i)
-                    if (at == i) d[i] += v;
+        if (a.dweights) {
+            // choice k's share to the lane that holds its expert, by a row of shared memory that is 0 between tokens;
+            // a token that names an expert twice adds the shares in the order of the choices
+            if (e >= 0) mine[e] = __int_as_float(lane);
+            __syncwarp();
+            const bool twice = e >= 0 && __float_as_int(mine[e]) != lane;
+            __syncwarp();
+            if (!__any_sync(kAll, twice)) {
+                if (e >= 0) mine[e] = near;
+            } else {
+                if (e >= 0) mine[e] = 0.0f;
+                for (int k = 0; k < a.K; ++k) {
+                    __syncwarp();
+                    if (lane == k && e >= 0) mine[e] += near;
+                }
             }
+            __syncwarp();
+            add_shared<V>(mine + lane * V, d);
+            __syncwarp();
+            if (e >= 0) mine[e] = 0.0f;
+            __syncwarp();
+        }
         store_logits(out, a.E, lane, a.dvec, d);
     }
     if (bad && a.status) flag(a.status, FLAG_INVALID_TOPK);
@@ -529,6 +612,11 @@ __global__ void __launch_bounds__(kRouterThreads) router_backward_kernel(const R
                                        : EP_BY_EXPERTS(kernel, float, false, (r)->experts))                             \
          : ((r)->scoring == EP_SIGMOID ? EP_BY_EXPERTS(kernel, __nv_bfloat16, true, (r)->experts)                       \
                                        : EP_BY_EXPERTS(kernel, __nv_bfloat16, false, (r)->experts)))
+
+template <typename T, int V, bool kSigmoid>
+constexpr auto route_all = route_kernel<T, V, kSigmoid, false>;
+template <typename T, int V, bool kSigmoid>
+constexpr auto route_groups = route_kernel<T, V, kSigmoid, true>;
 
 static ep_status check_router(const char* fn, const ep_router* r, const void* logits, int64_t stride) {
     if (!r) return set_error(EP_ERR_INVALID_ARG, "%s: null descriptor", fn);
@@ -582,7 +670,7 @@ extern "C" ep_status ep_route(const ep_router* r, const void* logits, int64_t lo
     EP_TRY(router_blocks(r->tokens, &blocks));
     const RouterArgs a = {logits, logits_stride, r->tokens, r->experts, r->topk, r->groups, r->topk_groups, r->normalize != 0,
                           by_vectors(r, logits, logits_stride), r->scale, bias, mask, topk_idx, topk_weights};
-    return launch_next(EP_ROUTER_KERNEL(route_kernel, r), blocks, kRouterThreads, stream, a);
+    return launch_next(r->topk_groups < r->groups ? EP_ROUTER_KERNEL(route_groups, r) : EP_ROUTER_KERNEL(route_all, r), blocks, kRouterThreads, stream, a);
 }
 
 extern "C" int64_t ep_balance_loss_workspace(const ep_router* r, int32_t sequences) {
