@@ -4,9 +4,8 @@
 // A warp per token.  Lane i holds experts i V .. i V + V - 1 of the row in registers, so that the lowest
 // expert of equal ones is the first of the lowest lane.
 //
-// Choice.  key = fp32(logit + bias), compared as integers in the same order (NaN the largest, -inf and
-// closed groups 0 = never chosen); top-k by repeated maxima: a warp-wide maximum of the lanes' best, whose
-// first owner gives up its first expert of that key.  Lane k keeps choice k.
+// Choice.  key = fp32(logit + bias), compared as integers in the same order (NaN the largest, -inf and what
+// closed groups hold never chosen).  Lane k ends with choice k.
 //
 // Balance.  With c_se the choices of expert e in sequence s, m_s = sum_e c_se, n_s the tokens that chose:
 //   F_se = coef E c_se / (S m_s n_s),   loss = sum_s sum_e F_se sum_t q_ste,   q: softmax, or sigmoid / its sum
@@ -15,6 +14,7 @@
 // the load is nearly balanced.
 //   softmax:  dl_e = q_e (F_e - sum_j F_j q_j);   sigmoid (p, p' = p (1 - p)):  dl_e = p'_e (F_e - sum_j F_j q_j) / sum p
 #include <climits>
+#include <initializer_list>
 
 #include "ep_tcgen05.cuh"
 
@@ -27,9 +27,11 @@ constexpr uint32_t kAll = 0xffffffffu;
 
 struct RouterArgs {
     const void* logits;
-    int64_t stride, tokens;
+    int64_t stride;
+    uint32_t tokens;  // below 2^31, so that a step past them stays within 32 bits
     int E, K, groups, topk_groups;
-    bool normalize, vec;
+    bool normalize;
+    int vec;
     float scale;
     const float* bias;
     const uint8_t* mask;
@@ -37,10 +39,10 @@ struct RouterArgs {
     float* weights;
 };
 
-// Ordered as the floats are; both zeros alike, every NaN the largest.
+// Ordered as the floats are.  Adding +0 makes both zeros alike and every NaN the one that sums give, 0x7fffffff,
+// whose key is the largest.
 __device__ __forceinline__ uint32_t ordered(float v) {
-    if (v != v) return kAll;
-    const uint32_t u = __float_as_uint(v + 0.0f);
+    const uint32_t u = __float_as_uint(__fadd_rn(v, 0.0f));
     return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
 }
 __device__ __forceinline__ float unordered(uint32_t k) {
@@ -52,37 +54,49 @@ __device__ __forceinline__ float warp_sum(float v) {
     for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
     return v;
 }
-__device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-    for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, o));
-    return v;
+__device__ __forceinline__ float warp_max(float v) {  // a NaN counts only where all are
+    float m;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
+    return m;
 }
 
-// This lane's V logits of a row; -inf past the last expert.
+// This lane's V logits of a row; -inf past the last expert.  vec: the bytes a lane may take at once.
 template <typename T, int V>
-__device__ __forceinline__ void load_logits(const T* row, int E, int lane, bool vec, float (&v)[V]) {
-    constexpr int kPer = 16 / sizeof(T);
-    if constexpr (V % kPer == 0) {
-        if (vec) {
+__device__ __forceinline__ void load_logits(const T* row, int E, int lane, int vec, float (&v)[V]) {
+    auto unpack = [&](const uint32_t* u, int words, int at) {
 #pragma unroll
-            for (int c = 0; c < V; c += kPer) {
-                const int e = lane * V + c;
-                if (e < E) {
-                    const int4 r = ld_nc_na_v4(row + e);
-                    const uint32_t u[4] = {(uint32_t)r.x, (uint32_t)r.y, (uint32_t)r.z, (uint32_t)r.w};
+        for (int i = 0; i < words; ++i) {
+            if constexpr (sizeof(T) == 4) {
+                v[at + i] = __uint_as_float(u[i]);
+            } else {
+                v[at + 2 * i] = __uint_as_float(u[i] << 16);
+                v[at + 2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+            }
+        }
+    };
+    if constexpr (V * sizeof(T) >= 16) {
+        if (vec >= 16) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        if constexpr (sizeof(T) == 4) {
-                            v[c + i] = __uint_as_float(u[i]);
-                        } else {
-                            v[c + 2 * i] = __uint_as_float(u[i] << 16);
-                            v[c + 2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-                        }
+            for (int i = 0; i < V; ++i) v[i] = -INFINITY;
+            constexpr int kWide = V * sizeof(T) >= 32 ? 32 : 16;
+            if (kWide == 32 && vec == 32) {
+                constexpr int kPer = 32 / sizeof(T);
+#pragma unroll
+                for (int c = 0; c < V; c += kPer)
+                    if (lane * V + c < E) {
+                        uint32_t u[8];
+                        ld_nc_32(row + lane * V + c, u);
+                        unpack(u, 8, c);
                     }
-                } else {
+            } else {
+                constexpr int kPer = 16 / sizeof(T);
 #pragma unroll
-                    for (int i = 0; i < kPer; ++i) v[c + i] = -INFINITY;
-                }
+                for (int c = 0; c < V; c += kPer)
+                    if (lane * V + c < E) {
+                        const int4 r = ld_nc_na_v4(row + lane * V + c);
+                        const uint32_t u[4] = {(uint32_t)r.x, (uint32_t)r.y, (uint32_t)r.z, (uint32_t)r.w};
+                        unpack(u, 4, c);
+                    }
             }
             return;
         }
@@ -105,20 +119,19 @@ __device__ __forceinline__ float sigmoid_of(float l, float* slope) {
     return l < 0.0f ? e * r : r;  // a NaN stays one: r
 }
 
-// The scores of a row: softmax, with *top the largest logit and *by 1 / sum of e^(l - top); or sigmoid and its
+// The scores of a row (-inf past the last expert gives 0): softmax, with *top the largest logit and *by 1 / sum of e^(l - top); or sigmoid and its
 // slope, with *by 1 / its sum (0 for a sum of 0).
 template <int V, bool kSigmoid>
-__device__ __forceinline__ void scores(const float (&l)[V], int E, int lane, float (&p)[V], float (&slope)[V], float* top, float* by) {
+__device__ __forceinline__ void scores(const float (&l)[V], float (&p)[V], float (&slope)[V], float* top, float* by) {
     if constexpr (kSigmoid) {
         float s = 0.0f;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             p[i] = sigmoid_of(l[i], &slope[i]);
-            if (lane * V + i >= E) p[i] = slope[i] = 0.0f;
             s += p[i];
         }
         s = warp_sum(s);
-        *by = s != 0.0f ? 1.0f / s : 0.0f;
+        *by = s != 0.0f ? __fdividef(1.0f, s) : 0.0f;
     } else {
         float m = l[0], s = 0.0f;
 #pragma unroll
@@ -126,10 +139,10 @@ __device__ __forceinline__ void scores(const float (&l)[V], int E, int lane, flo
         m = warp_max(m);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            p[i] = lane * V + i < E ? exp_of(l[i] - m) : 0.0f;
+            p[i] = exp_of(l[i] - m);
             s += p[i];
         }
-        s = 1.0f / warp_sum(s);
+        s = __fdividef(1.0f, warp_sum(s));
 #pragma unroll
         for (int i = 0; i < V; ++i) p[i] *= s;
         *top = m;
@@ -137,33 +150,17 @@ __device__ __forceinline__ void scores(const float (&l)[V], int E, int lane, flo
     }
 }
 
-// A lane's two largest keys and where they are, of those not taken yet (bit i of `taken`: key i).
-template <int V>
-struct LaneTop {
-    uint32_t k1, k2;
-    int i1, i2;
-    __device__ __forceinline__ void scan(const uint32_t (&key)[V], uint32_t taken) {
-        k1 = k2 = 0;
-        i1 = i2 = 0;
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const uint32_t k = taken >> i & 1 ? 0 : key[i];
-            if (k > k1) {
-                k2 = k1, i2 = i1;
-                k1 = k, i1 = i;
-            } else if (k > k2) {
-                k2 = k, i2 = i;
-            }
-        }
-    }
-};
-
-// Whether this lane's group stays; a group's score is the sum of its two largest keys.  Lanes that hold whole groups'
-// parts (V divides the group, a power of two of lanes each): the lanes' two largest are merged, and a group's rank is the
+// Whether this lane's group stays; a group's score is the sum of its two largest keys.  Lanes that hold whole parts of
+// groups (V divides the group, a power of two of lanes each): the lanes' two largest are merged, and a group's rank is the
 // number of groups before it.
 template <int V>
-__device__ __forceinline__ bool keep_group(const LaneTop<V>& top, const RouterArgs& a, int lane, int lanes) {
-    uint32_t hi = top.k1, lo = V > 1 ? top.k2 : 0;
+__device__ __forceinline__ bool keep_group(const uint32_t (&key)[V], const RouterArgs& a, int lane, int lanes) {
+    uint32_t hi = key[0], lo = 0;
+#pragma unroll
+    for (int i = 1; i < V; ++i) {
+        lo = max(lo, min(hi, key[i]));
+        hi = max(hi, key[i]);
+    }
     for (int o = 1; o < lanes; o <<= 1) {
         const uint32_t h = __shfl_xor_sync(kAll, hi, o), l = __shfl_xor_sync(kAll, lo, o);
         lo = max(max(lo, l), min(hi, h));
@@ -172,6 +169,7 @@ __device__ __forceinline__ bool keep_group(const LaneTop<V>& top, const RouterAr
     const uint32_t score = V * lanes > 1 ? ordered(unordered(hi) + unordered(lo)) : hi;
     const int mine = lane / lanes;
     int before = 0;
+#pragma unroll 4
     for (int g = 0; g < a.groups; ++g) {
         const uint32_t other = __shfl_sync(kAll, score, g * lanes);
         before += other > score || (other == score && g < mine);
@@ -208,87 +206,150 @@ __device__ __forceinline__ uint32_t choose_groups(const uint32_t (&key)[V], cons
     return kept;
 }
 
+// The K largest keys by K warp-wide maxima, the first owner giving up its first: any number of candidates.
+template <int V>
+__device__ __forceinline__ int choose_one_by_one(uint32_t (&key)[V], int K, int lane) {
+    int expert = -1;
+    for (int k = 0; k < K; ++k) {
+        uint32_t best = 0;
+        int at = 0;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (key[i] > best) {
+                best = key[i];
+                at = i;
+            }
+        const uint32_t most = __reduce_max_sync(kAll, best);
+        if (most <= kKeyNegInf) break;
+        const int owner = __ffs(__ballot_sync(kAll, best == most)) - 1;
+        const int e = __shfl_sync(kAll, lane * V + at, owner);
+        if (lane == k) expert = e;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (lane * V + i == e) key[i] = 0;
+    }
+    return expert;
+}
+
+// Choice k's expert, in lane k: the K-th largest of the lanes' best keys bounds the K-th largest key from below, so that
+// the keys from there on, mostly K and a few, are all that has to be ranked: they are listed, a lane each, and a
+// candidate's rank is the number of larger ones.  Equal candidates show as two that want the same place; then the lower
+// experts among them count as larger.  Where there are more than 32, the choices are made one by one.
+struct RouteList {
+    uint32_t key[32];
+    int expert[32];
+};
+template <int V>
+__device__ __forceinline__ int choose(uint32_t (&key)[V], int K, int lane, RouteList& list) {
+    uint32_t best = key[0];
+#pragma unroll
+    for (int i = 1; i < V; ++i) best = max(best, key[i]);
+    uint32_t least = 0;
+#pragma unroll 4
+    for (int k = 0; k < K; ++k) {  // equal ones go at once, which only lowers the bound
+        least = __reduce_max_sync(kAll, best);
+        if (best == least) best = 0;
+    }
+    least = max(least, kKeyNegInf + 1);
+    int total = 0;
+    list.key[lane] = 0;
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const bool on = key[i] >= least;
+        const uint32_t all = __ballot_sync(kAll, on);
+        const int to = total + __popc(all & lanemask_lt());
+        if (on && to < 32) {
+            list.key[to] = key[i];
+            list.expert[to] = lane * V + i;
+        }
+        total += __popc(all);
+    }
+    if (total > 32) return choose_one_by_one(key, K, lane);
+    __syncwarp();
+    const uint32_t mine = list.key[lane];
+    const int expert = list.expert[lane];
+    int rank = 0;
+    for (int i = 0; i < total; i += 4) {
+        const uint4 other = *reinterpret_cast<const uint4*>(list.key + i);
+        rank += other.x > mine;
+        rank += other.y > mine;
+        rank += other.z > mine;
+        rank += other.w > mine;
+    }
+    __syncwarp();
+    if (lane < total) list.expert[rank] = expert;
+    __syncwarp();
+    const bool lost = lane < total && list.expert[rank] != expert;
+    if (__any_sync(kAll, lost)) {
+        for (int i = 0; i < total; ++i) {
+            const uint32_t other = __shfl_sync(kAll, mine, i);
+            const int e = __shfl_sync(kAll, expert, i);
+            rank += other == mine && e < expert;
+        }
+        __syncwarp();
+        if (lane < total) list.expert[rank] = expert;
+        __syncwarp();
+    }
+    return lane < total && lane < K ? list.expert[lane] : -1;
+}
+
 template <typename T, int V, bool kSigmoid, bool kGroups>
-__global__ void __launch_bounds__(kRouterThreads) route_kernel(const RouterArgs a) {
+__global__ void __launch_bounds__(kRouterThreads, V <= 8 ? 5 : 1) route_kernel(const RouterArgs a) {
+    __shared__ __align__(16) RouteList lists[kRouterWarps];
     const int lane = threadIdx.x & 31;
     grid_wait();
     grid_launch_next();
     const int size = kGroups ? a.E / a.groups : 0;
     const bool whole = kGroups && size % V == 0 && (size / V & (size / V - 1)) == 0;
-    for (int64_t t = (int64_t)blockIdx.x * kRouterWarps + (threadIdx.x >> 5); t < a.tokens; t += (int64_t)gridDim.x * kRouterWarps) {
-        if (a.mask && !a.mask[t]) {
-            if (lane < a.K) {
-                a.idx[t * a.K + lane] = -1;
-                a.weights[t * a.K + lane] = 0.0f;
-            }
-            continue;
-        }
+    float bias[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) bias[i] = a.bias && lane * V + i < a.E ? a.bias[lane * V + i] : 0.0f;
+    for (uint32_t t = blockIdx.x * kRouterWarps + (threadIdx.x >> 5); t < a.tokens; t += gridDim.x * kRouterWarps) {
         const T* row = static_cast<const T*>(a.logits) + t * a.stride;
         float l[V];
         load_logits(row, a.E, lane, a.vec, l);
-        uint32_t key[V];  // 0 past the last expert, kKeyNegInf for -inf
-        if (a.bias) {
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const int e = lane * V + i;
-                key[i] = e < a.E ? ordered(l[i] + a.bias[e]) : 0;
+        if (a.mask && !a.mask[t]) {
+            if (lane < a.K) {
+                a.idx[(int64_t)t * a.K + lane] = -1;
+                a.weights[(int64_t)t * a.K + lane] = 0.0f;
             }
-        } else {
+            continue;
+        }
+        uint32_t key[V];  // kKeyNegInf past the last expert
 #pragma unroll
-            for (int i = 0; i < V; ++i) key[i] = lane * V + i < a.E ? ordered(l[i]) : 0;
-        }
-        LaneTop<V> top;
-        uint32_t taken = 0;
-        if (kGroups && !whole) {
-            const uint32_t kept = choose_groups(key, a, lane);
+        for (int i = 0; i < V; ++i) key[i] = ordered(l[i] + bias[i]);  // -inf stays past the last expert
+        if (kGroups) {
+            if (whole) {
+                if (!keep_group(key, a, lane, size / V))
 #pragma unroll
-            for (int i = 0; i < V; ++i)
-                if (!(kept >> min((lane * V + i) / size, 31) & 1)) key[i] = 0;
-        }
-        top.scan(key, 0);
-        if (kGroups && whole && !keep_group(top, a, lane, size / V)) {
-            taken = kAll;
-            top.k1 = top.k2 = 0;
-        }
-        // choice k ends in lane k
-        int expert = -1;
-        bool second = true;  // k2 is known
-        for (int k = 0; k < a.K; ++k) {
-            const uint32_t most = __reduce_max_sync(kAll, top.k1);
-            if (most <= kKeyNegInf) break;
-            const int owner = __ffs(__ballot_sync(kAll, top.k1 == most)) - 1;
-            const int at = __shfl_sync(kAll, top.i1, owner);
-            if (lane == k) expert = owner * V + at;
-            if (lane == owner) {
-                taken |= 1u << top.i1;
-                if (V == 1 || second) {
-                    top.k1 = V == 1 ? 0 : top.k2;
-                    top.i1 = top.i2;
-                    second = false;
-                } else {
-                    top.scan(key, taken);
-                    second = true;
-                }
+                    for (int i = 0; i < V; ++i) key[i] = 0;
+            } else {
+                const uint32_t kept = choose_groups(key, a, lane);
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+                    if (!(kept >> min((lane * V + i) / size, 31) & 1)) key[i] = 0;
             }
         }
+        const int expert = choose(key, a.K, lane, lists[threadIdx.x >> 5]);
         const float logit = expert >= 0 ? (float)row[expert] : -INFINITY;
         float w;
         if (kSigmoid) {
             float slope;
             w = expert >= 0 ? sigmoid_of(logit, &slope) : 0.0f;
-            if (a.normalize) w /= warp_sum(w) + 1e-20f;
+            if (a.normalize) w = __fdividef(w, warp_sum(w) + 1e-20f);
         } else if (a.normalize) {
             const float m = warp_max(logit);
             w = expert >= 0 ? exp_of(logit - m) : 0.0f;
-            w /= warp_sum(w);
+            w = __fdividef(w, warp_sum(w));
         } else {
             float p[V], slope[V], most, by;
-            scores<V, false>(l, a.E, lane, p, slope, &most, &by);
+            scores<V, false>(l, p, slope, &most, &by);
             w = exp_of(logit - most) * by;
         }
         if (lane < a.K) {
-            a.idx[t * a.K + lane] = expert;
-            a.weights[t * a.K + lane] = expert >= 0 ? w * a.scale : 0.0f;
+            a.idx[(int64_t)t * a.K + lane] = expert;
+            a.weights[(int64_t)t * a.K + lane] = expert >= 0 ? w * a.scale : 0.0f;
         }
     }
 }
@@ -299,7 +360,7 @@ struct BalanceArgs {
     const int64_t* idx;
     int64_t stride, T;  // tokens of a sequence
     int S, E, K, blocks;  // blocks of a sequence
-    bool vec;
+    int vec;
     float coef;
     // workspace: [S][blocks][E] sums of q and choices, [S][blocks] tokens, [S] losses, the counter of the last block
     float* part;
@@ -314,7 +375,7 @@ struct BalanceArgs {
 };
 
 template <typename T, int V, bool kSigmoid>
-__global__ void __launch_bounds__(kRouterThreads) balance_kernel(const BalanceArgs a) {
+__global__ void __launch_bounds__(kRouterThreads, V <= 8 ? 6 : 1) balance_kernel(const BalanceArgs a) {
     __shared__ float sums[kRouterMaxExperts];
     __shared__ int hist[kRouterMaxExperts];
     __shared__ int used_tokens;
@@ -333,6 +394,8 @@ __global__ void __launch_bounds__(kRouterThreads) balance_kernel(const BalanceAr
     bool bad = false;
     for (int64_t t = (int64_t)b * kRouterWarps + warp; t < a.T; t += (int64_t)a.blocks * kRouterWarps) {
         const int64_t row = s * a.T + t;
+        float l[V], p[V], slope[V], top, by;
+        load_logits(static_cast<const T*>(a.logits) + row * a.stride, a.E, lane, a.vec, l);
         bool chose = false;
         if (lane < a.K) {
             const int64_t e = a.idx[row * a.K + lane];
@@ -342,9 +405,7 @@ __global__ void __launch_bounds__(kRouterThreads) balance_kernel(const BalanceAr
         }
         if (!__any_sync(kAll, chose)) continue;
         ++tokens;
-        float l[V], p[V], slope[V], top, by;
-        load_logits(static_cast<const T*>(a.logits) + row * a.stride, a.E, lane, a.vec, l);
-        scores<V, kSigmoid>(l, a.E, lane, p, slope, &top, &by);
+        scores<V, kSigmoid>(l, p, slope, &top, &by);
 #pragma unroll
         for (int i = 0; i < V; ++i) acc[i] += kSigmoid ? p[i] * by : p[i];
     }
@@ -367,6 +428,8 @@ __global__ void __launch_bounds__(kRouterThreads) balance_kernel(const BalanceAr
     if (bad && a.status) flag(a.status, FLAG_INVALID_TOPK);
 }
 
+constexpr int kFinishThreads = 1024;
+
 template <typename T>
 __device__ __forceinline__ T block_sum(T v, T* buf) {
 #pragma unroll
@@ -374,53 +437,54 @@ __device__ __forceinline__ T block_sum(T v, T* buf) {
     __syncthreads();
     if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = v;
     __syncthreads();
-    T s = buf[0];
-    for (int i = 1; i < kRouterWarps; ++i) s += buf[i];
-    return s;
+    v = buf[threadIdx.x & 31];
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
+    return v;
 }
 
-// A block per sequence: its counts, factors and loss; the last block to end adds the losses in order.
-__global__ void __launch_bounds__(kRouterThreads) balance_finish_kernel(const BalanceArgs a) {
-    __shared__ long long ibuf[kRouterWarps];
-    __shared__ float fbuf[kRouterWarps];
+// A block per sequence: its counts, factors and loss; the last block to end adds the losses in order.  A thread adds
+// every (1024 / width)-th block's part of one expert, width: the experts rounded up to a power of two.
+__global__ void __launch_bounds__(kFinishThreads) balance_finish_kernel(const BalanceArgs a, int width) {
+    __shared__ long long ibuf[32];
+    __shared__ float fbuf[32];
+    __shared__ float sums[kFinishThreads];
+    __shared__ int hist[kFinishThreads];
+    __shared__ float unit;
     __shared__ bool last;
     grid_wait();
     grid_launch_next();
-    constexpr int kMost = kRouterMaxExperts / kRouterThreads;
-    const int s = blockIdx.x;
-    float p[kMost];
-    int c[kMost];
-    long long pairs = 0, tokens = 0;
-#pragma unroll
-    for (int i = 0; i < kMost; ++i) {
-        const int e = threadIdx.x + i * kRouterThreads;
-        p[i] = 0.0f;
-        c[i] = 0;
-        if (e < a.E)
-            for (int b = 0; b < a.blocks; ++b) {
-                const int64_t at = ((int64_t)s * a.blocks + b) * a.E + e;
-                p[i] += a.part[at];
-                c[i] += a.part_counts[at];
-            }
-        pairs += c[i];
-    }
-    for (int b = threadIdx.x; b < a.blocks; b += kRouterThreads) tokens += a.part_tokens[s * a.blocks + b];
-    pairs = block_sum(pairs, ibuf);
-    tokens = block_sum(tokens, ibuf);
-    // coef / (S m n): the same for every expert
-    const float unit = pairs ? (float)((double)a.coef / ((double)a.S * (double)pairs * (double)tokens)) : 0.0f;
-    float loss = 0.0f;
-#pragma unroll
-    for (int i = 0; i < kMost; ++i) {
-        const int e = threadIdx.x + i * kRouterThreads;
-        if (e < a.E) {
-            a.counts[s * a.E + e] = c[i];
-            a.factors[s * a.E + e] = unit * (float)((long long)c[i] * a.E - pairs);
-            loss += unit * (float)((long long)c[i] * a.E) * p[i];
+    const int s = blockIdx.x, tid = threadIdx.x, e = tid & (width - 1);
+    float p = 0.0f;
+    int c = 0;
+    if (e < a.E)
+#pragma unroll 4
+        for (int b = tid / width; b < a.blocks; b += kFinishThreads / width) {
+            const int64_t at = ((int64_t)s * a.blocks + b) * a.E + e;
+            p += a.part[at];
+            c += a.part_counts[at];
         }
+    sums[tid] = p;
+    hist[tid] = c;
+    long long tokens = 0;
+    for (int b = tid; b < a.blocks; b += kFinishThreads) tokens += a.part_tokens[(int64_t)s * a.blocks + b];
+    const long long pairs = block_sum((long long)c, ibuf);
+    tokens = block_sum(tokens, ibuf);
+    // coef / (S m n), the same for every expert: in 64 bits, which one thread is enough for
+    if (tid == 0) unit = pairs ? (float)((double)a.coef / ((double)a.S * (double)pairs * (double)tokens)) : 0.0f;
+    __syncthreads();
+    float loss = 0.0f;
+    if (tid < a.E) {  // the first part's thread
+        for (int i = tid + width; i < kFinishThreads; i += width) {
+            p += sums[i];
+            c += hist[i];
+        }
+        a.counts[(int64_t)s * a.E + e] = c;
+        a.factors[(int64_t)s * a.E + e] = unit * (float)((long long)c * a.E - pairs);
+        loss = unit * (float)((long long)c * a.E) * p;
     }
     loss = block_sum(loss, fbuf);
-    if (threadIdx.x == 0) {
+    if (tid == 0) {
         a.seq_loss[s] = loss;
         __threadfence();
         last = atomicAdd(a.ticket, 1u) == (uint32_t)a.S - 1;
@@ -429,9 +493,9 @@ __global__ void __launch_bounds__(kRouterThreads) balance_finish_kernel(const Ba
     if (!last) return;
     __threadfence();
     float sum = 0.0f;
-    for (int i = threadIdx.x; i < a.S; i += kRouterThreads) sum += __ldcg(a.seq_loss + i);
+    for (int i = tid; i < a.S; i += kFinishThreads) sum += __ldcg(a.seq_loss + i);
     sum = block_sum(sum, fbuf);
-    if (threadIdx.x == 0) *a.loss = sum;
+    if (tid == 0) *a.loss = sum;
 }
 
 // ---- gradient of the logits -----------------------------------------------------------
@@ -442,34 +506,41 @@ struct RouterBackArgs {
     const float* factors;   // null: no balance loss
     const float* dloss;
     void* dlogits;
-    int64_t stride, dstride, tokens, T;
+    int64_t stride, dstride;
+    uint32_t tokens, T;
     int E, K;
-    bool normalize, vec, dvec;
+    bool normalize;
+    int vec, dvec, fvec;
     float scale;
     uint32_t* status;
 };
 
 template <typename T, int V>
-__device__ __forceinline__ void store_logits(T* row, int E, int lane, bool vec, const float (&v)[V]) {
-    constexpr int kPer = 16 / sizeof(T);
-    if constexpr (V % kPer == 0) {
-        if (vec) {
+__device__ __forceinline__ void store_logits(T* row, int E, int lane, int vec, const float (&v)[V]) {
+    constexpr int kWords = V * sizeof(T) / 4;
+    if constexpr (V * sizeof(T) >= 16) {
+        if (vec >= 16) {
+            uint32_t u[kWords];
 #pragma unroll
-            for (int c = 0; c < V; c += kPer) {
-                const int e = lane * V + c;
-                if (e >= E) continue;
-                int4 r;
-                int* o = &r.x;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if constexpr (sizeof(T) == 4) {
-                        o[i] = __float_as_int(v[c + i]);
-                    } else {
-                        const __nv_bfloat162 b = __floats2bfloat162_rn(v[c + 2 * i], v[c + 2 * i + 1]);
-                        o[i] = *reinterpret_cast<const int*>(&b);
-                    }
+            for (int i = 0; i < kWords; ++i) {
+                if constexpr (sizeof(T) == 4) {
+                    u[i] = __float_as_uint(v[i]);
+                } else {
+                    const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+                    u[i] = *reinterpret_cast<const uint32_t*>(&b);
                 }
-                st_na_v4(row + e, r);
+            }
+            if (kWords >= 8 && vec == 32) {
+                constexpr int kPer = 32 / sizeof(T);
+#pragma unroll
+                for (int c = 0; c < kWords / 8; ++c)
+                    if (lane * V + c * kPer < E) st_global_32(row + lane * V + c * kPer, u + c * 8);
+            } else {
+                constexpr int kPer = 16 / sizeof(T);
+#pragma unroll
+                for (int c = 0; c < kWords / 4; ++c)
+                    if (lane * V + c * kPer < E)
+                        st_na_v4(row + lane * V + c * kPer, make_int4((int)u[4 * c], (int)u[4 * c + 1], (int)u[4 * c + 2], (int)u[4 * c + 3]));
             }
             return;
         }
@@ -494,7 +565,7 @@ __device__ __forceinline__ void add_shared(const float* p, float (&d)[V]) {
 }
 
 template <typename T, int V, bool kSigmoid>
-__global__ void __launch_bounds__(kRouterThreads) router_backward_kernel(const RouterBackArgs a) {
+__global__ void __launch_bounds__(kRouterThreads, V <= 8 ? 5 : 1) router_backward_kernel(const RouterBackArgs a) {
     __shared__ __align__(16) float rows[kRouterWarps][32 * V];
     const int lane = threadIdx.x & 31;
     float* mine = rows[threadIdx.x >> 5];
@@ -504,16 +575,22 @@ __global__ void __launch_bounds__(kRouterThreads) router_backward_kernel(const R
     grid_wait();
     grid_launch_next();
     const float dloss = a.factors ? *a.dloss : 0.0f;
+    // softmax of the whole row, or sigmoid: for the balance loss, and for weights that are not normalised
+    const bool whole = a.factors || (!kSigmoid && !a.normalize);
     bool bad = false;
-    for (int64_t t = (int64_t)blockIdx.x * kRouterWarps + (threadIdx.x >> 5); t < a.tokens; t += (int64_t)gridDim.x * kRouterWarps) {
+    for (uint32_t t = blockIdx.x * kRouterWarps + (threadIdx.x >> 5); t < a.tokens; t += gridDim.x * kRouterWarps) {
         const T* row = static_cast<const T*>(a.logits) + t * a.stride;
-        T* out = static_cast<T*>(a.dlogits) + t * a.dstride;
+        float l[V];
+        if (whole) load_logits(row, a.E, lane, a.vec, l);
         int e = -1;
+        float g = 0.0f;
         if (lane < a.K) {
-            const int64_t i = a.idx[t * a.K + lane];
+            const int64_t i = a.idx[(int64_t)t * a.K + lane];
             bad |= i < -1 || i >= a.E;
             e = i >= 0 && i < a.E ? (int)i : -1;
+            if (a.dweights && e >= 0) g = a.dweights[(int64_t)t * a.K + lane] * a.scale;
         }
+        T* out = static_cast<T*>(a.dlogits) + t * a.dstride;
         float d[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) d[i] = 0.0f;
@@ -521,21 +598,32 @@ __global__ void __launch_bounds__(kRouterThreads) router_backward_kernel(const R
             store_logits(out, a.E, lane, a.dvec, d);
             continue;
         }
-        const float logit = e >= 0 ? (float)row[e] : -INFINITY;
-        const float g = a.dweights && e >= 0 ? a.dweights[t * a.K + lane] * a.scale : 0.0f;
+        float logit = -INFINITY;
+        if (a.dweights) {
+            if (whole) {  // by way of shared memory
+#pragma unroll
+                for (int i = 0; i < V; ++i) mine[lane * V + i] = l[i];
+                __syncwarp();
+                if (e >= 0) logit = mine[e];
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < V; ++i) mine[lane * V + i] = 0.0f;
+                __syncwarp();
+            } else if (e >= 0) {
+                logit = (float)row[e];
+            }
+        }
         // the chosen experts' share of the gradient, in lane k for choice k
         float near = 0.0f, inner = 0.0f;
-        // softmax of the whole row, or sigmoid: for the balance loss, and for weights that are not normalised
-        if (a.factors || (!kSigmoid && !a.normalize)) {
-            float l[V], p[V], slope[V], top, by;
-            load_logits(row, a.E, lane, a.vec, l);
-            scores<V, kSigmoid>(l, a.E, lane, p, slope, &top, &by);
+        if (whole) {
+            float p[V], slope[V], top, by;
+            scores<V, kSigmoid>(l, p, slope, &top, &by);
             if (a.factors) {
-                const float* f = a.factors + t / a.T * a.E + lane * V;
                 float fv[V], sum = 0.0f;
+                load_logits(a.factors + (int64_t)(t / a.T) * a.E, a.E, lane, a.fvec, fv);
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
-                    fv[i] = lane * V + i < a.E ? f[i] : 0.0f;
+                    if (lane * V + i >= a.E) fv[i] = 0.0f;
                     sum = fmaf(fv[i], p[i], sum);
                 }
                 sum = warp_sum(sum) * (kSigmoid ? by : 1.0f);
@@ -555,7 +643,7 @@ __global__ void __launch_bounds__(kRouterThreads) router_backward_kernel(const R
                 float w = e >= 0 ? sigmoid_of(logit, &slope) : 0.0f;
                 if (e < 0) slope = 0.0f;
                 if (a.normalize) {
-                    const float by = 1.0f / (warp_sum(w) + 1e-20f);
+                    const float by = __fdividef(1.0f, warp_sum(w) + 1e-20f);
                     inner = warp_sum(g * w * by);
                     near = slope * (g - inner) * by;
                 } else {
@@ -564,7 +652,7 @@ __global__ void __launch_bounds__(kRouterThreads) router_backward_kernel(const R
             } else {
                 const float m = warp_max(logit);
                 float w = e >= 0 ? exp_of(logit - m) : 0.0f;
-                w /= warp_sum(w);
+                w = __fdividef(w, warp_sum(w));
                 inner = warp_sum(w * g);
                 near = w * (g - inner);
             }
@@ -629,22 +717,25 @@ static ep_status check_router(const char* fn, const ep_router* r, const void* lo
         return set_error(EP_ERR_INVALID_ARG, "%s: logits, rows %lld elements apart for %d experts", fn, (long long)stride, r->experts);
     return EP_OK;
 }
-static bool by_vectors(const ep_router* r, const void* p, int64_t stride) {
-    const int per = r->logits_type == EP_F32 ? 4 : 8;
-    return aligned16(p) && stride % per == 0 && r->experts % per == 0;
+// Bytes that a lane may take of these rows at once: 32, 16, or one expert's.
+static int by_vectors(int experts, int type, const void* p, int64_t stride) {
+    const int size = type == EP_F32 ? 4 : 2;
+    for (const int bytes : {32, 16})
+        if (aligned_to(p, bytes) && stride * size % bytes == 0 && experts * size % bytes == 0) return bytes;
+    return size;
 }
 static ep_status router_blocks(int64_t tokens, int64_t* blocks) {
     int dev = 0, sms = 0;
     EP_CUDA(cudaGetDevice(&dev));
     EP_CUDA(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
-    const int64_t most = (int64_t)sms * 6, need = (tokens + kRouterWarps - 1) / kRouterWarps;
+    const int64_t most = (int64_t)sms * 8, need = (tokens + kRouterWarps - 1) / kRouterWarps;
     *blocks = need < most ? need : most;
     return EP_OK;
 }
 
 // Blocks of one sequence: enough for the device over all of them, each with two tokens a warp or more.
 static int balance_blocks(int64_t S, int64_t T, int sms) {
-    int64_t b = ((int64_t)sms * 4 + S - 1) / S;
+    int64_t b = ((int64_t)sms * 6 + S - 1) / S;
     const int64_t most = (T + 2 * kRouterWarps - 1) / (2 * kRouterWarps);
     if (b > most) b = most;
     return b < 1 ? 1 : (int)b;
@@ -668,8 +759,8 @@ extern "C" ep_status ep_route(const ep_router* r, const void* logits, int64_t lo
         return set_error(EP_ERR_INVALID_ARG, "%s: topk_idx, topk_weights and bias aligned to their elements", fn);
     int64_t blocks = 0;
     EP_TRY(router_blocks(r->tokens, &blocks));
-    const RouterArgs a = {logits, logits_stride, r->tokens, r->experts, r->topk, r->groups, r->topk_groups, r->normalize != 0,
-                          by_vectors(r, logits, logits_stride), r->scale, bias, mask, topk_idx, topk_weights};
+    const RouterArgs a = {logits, logits_stride, (uint32_t)r->tokens, r->experts, r->topk, r->groups, r->topk_groups, r->normalize != 0,
+                          by_vectors(r->experts, r->logits_type, logits, logits_stride), r->scale, bias, mask, topk_idx, topk_weights};
     return launch_next(r->topk_groups < r->groups ? EP_ROUTER_KERNEL(route_groups, r) : EP_ROUTER_KERNEL(route_all, r), blocks, kRouterThreads, stream, a);
 }
 
@@ -703,12 +794,14 @@ extern "C" ep_status ep_balance_loss(const ep_router* r, const void* logits, int
     if ((int64_t)sequences * blocks > INT_MAX) return set_error(EP_ERR_INVALID_ARG, "%s: %d sequences", fn, sequences);
     const int64_t n = (int64_t)sequences * blocks * r->experts;
     float* ws = static_cast<float*>(workspace);
-    const BalanceArgs a = {logits, topk_idx, logits_stride, T, sequences, r->experts, r->topk, blocks, by_vectors(r, logits, logits_stride), coef,
+    const BalanceArgs a = {logits, topk_idx, logits_stride, T, sequences, r->experts, r->topk, blocks, by_vectors(r->experts, r->logits_type, logits, logits_stride), coef,
                            ws, reinterpret_cast<int*>(ws + n), reinterpret_cast<int*>(ws + 2 * n),
                            ws + 2 * n + (int64_t)sequences * blocks, reinterpret_cast<uint32_t*>(ws + 2 * n + (int64_t)sequences * blocks + sequences),
                            loss, counts, factors, status_out};
     EP_TRY(launch_next(EP_ROUTER_KERNEL(balance_kernel, r), (int64_t)sequences * blocks, kRouterThreads, stream, a));
-    return launch_next(balance_finish_kernel, sequences, kRouterThreads, stream, a);
+    int width = 32;
+    while (width < r->experts) width *= 2;
+    return launch_next(balance_finish_kernel, sequences, kFinishThreads, stream, a, width);
 }
 
 extern "C" ep_status ep_router_backward(const ep_router* r, const void* logits, int64_t logits_stride, const int64_t* topk_idx,
@@ -727,8 +820,8 @@ extern "C" ep_status ep_router_backward(const ep_router* r, const void* logits, 
                          (long long)dlogits_stride);
     int64_t blocks = 0;
     EP_TRY(router_blocks(r->tokens, &blocks));
-    const RouterBackArgs a = {logits, topk_idx, dweights, factors, dloss, dlogits, logits_stride, dlogits_stride, r->tokens,
-                              factors ? r->tokens / sequences : 1, r->experts, r->topk, r->normalize != 0, by_vectors(r, logits, logits_stride),
-                              by_vectors(r, dlogits, dlogits_stride), r->scale, status_out};
+    const RouterBackArgs a = {logits, topk_idx, dweights, factors, dloss, dlogits, logits_stride, dlogits_stride, (uint32_t)r->tokens,
+                              (uint32_t)(factors ? r->tokens / sequences : 1), r->experts, r->topk, r->normalize != 0, by_vectors(r->experts, r->logits_type, logits, logits_stride),
+                              by_vectors(r->experts, r->logits_type, dlogits, dlogits_stride), by_vectors(r->experts, EP_F32, factors, r->experts), r->scale, status_out};
     return launch_next(EP_ROUTER_KERNEL(router_backward_kernel, r), blocks, kRouterThreads, stream, a);
 }
