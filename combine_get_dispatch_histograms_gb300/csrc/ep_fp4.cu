@@ -472,18 +472,7 @@ static ep_status launch_fp4_shape(const char* fn, const ep_fp4_rows* x, const ep
         EP_CUDA(cudaFuncSetAttribute(fp4_gemm_kernel<kSwiglu, kBN>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Shape::kSmem));
         if (dev < kMaxDevicesTracked) known[dev].store(true, std::memory_order_relaxed);
     }
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(most < sms ? most : sms));
-    cfg.blockDim = dim3(k4Threads);
-    cfg.dynamicSmemBytes = Shape::kSmem;
-    cfg.stream = as_stream(stream);
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    EP_CUDA(cudaLaunchKernelEx(&cfg, fp4_gemm_kernel<kSwiglu, kBN>, map_x, map_w, a));
-    return EP_OK;
+    return launch_next(fp4_gemm_kernel<kSwiglu, kBN>, most < sms ? most : sms, k4Threads, stream, Shared{Shape::kSmem}, map_x, map_w, a);
 }
 
 template <bool kSwiglu>

@@ -236,11 +236,15 @@ ep_status dispatch_permuted_rows(ep_ctx* c, const void* x, int64_t row_bytes, co
 inline cudaStream_t as_stream(void* s) { return reinterpret_cast<cudaStream_t>(s); }
 
 // A kernel that may start while the one before drains: it calls grid_wait before its first access to memory.
+struct Shared {
+    size_t bytes;  // dynamic shared memory
+};
 template <typename... Params, typename... Args>
-ep_status launch_next(void (*kernel)(Params...), int64_t blocks, int threads, void* stream, const Args&... args) {
+ep_status launch_next(void (*kernel)(Params...), int64_t blocks, int threads, void* stream, Shared shared, const Args&... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)blocks);
     cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = shared.bytes;
     cfg.stream = as_stream(stream);
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -249,6 +253,10 @@ ep_status launch_next(void (*kernel)(Params...), int64_t blocks, int threads, vo
     cfg.numAttrs = 1;
     EP_CUDA(cudaLaunchKernelEx(&cfg, kernel, args...));
     return EP_OK;
+}
+template <typename... Params, typename... Args>
+ep_status launch_next(void (*kernel)(Params...), int64_t blocks, int threads, void* stream, const Args&... args) {
+    return launch_next(kernel, blocks, threads, stream, Shared{0}, args...);
 }
 
 }  // namespace ep

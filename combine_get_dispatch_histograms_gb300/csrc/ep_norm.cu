@@ -10,6 +10,8 @@
 //
 // Both are bound by memory: every array is read or written once.  A row stays in the registers of
 // one block (of one warp up to 1024 channels) between its sum and its outputs.
+#include <atomic>
+
 #include "ep_fp8.cuh"
 #include "ep_tcgen05.cuh"
 
@@ -78,23 +80,30 @@ struct Raw8<__nv_bfloat16> {
 };
 template <>
 struct Raw8<float> {
-    int4 a, b;
+    uint32_t u[8];
     __device__ __forceinline__ void load(const float* p) {
-        a = ld_na_v4(p);
-        b = ld_na_v4(p + 4);
+        if ((reinterpret_cast<uintptr_t>(p) & 31) == 0) {
+            ld_global_32(p, u);
+        } else {
+            const int4 a = ld_na_v4(p), b = ld_na_v4(p + 4);
+            u[0] = a.x, u[1] = a.y, u[2] = a.z, u[3] = a.w, u[4] = b.x, u[5] = b.y, u[6] = b.z, u[7] = b.w;
+        }
     }
     __device__ __forceinline__ void get(float* v) const {
-        const int u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = __int_as_float(u[i]);
+        for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(u[i]);
     }
     __device__ __forceinline__ void round(float* v) {
-        a = make_int4(__float_as_int(v[0]), __float_as_int(v[1]), __float_as_int(v[2]), __float_as_int(v[3]));
-        b = make_int4(__float_as_int(v[4]), __float_as_int(v[5]), __float_as_int(v[6]), __float_as_int(v[7]));
+#pragma unroll
+        for (int i = 0; i < 8; ++i) u[i] = __float_as_uint(v[i]);
     }
     __device__ __forceinline__ void store(float* p) const {
-        st_na_v4(p, a);
-        st_na_v4(p + 4, b);
+        if ((reinterpret_cast<uintptr_t>(p) & 31) == 0) {
+            st_global_32(p, u);
+        } else {
+            st_na_v4(p, make_int4((int)u[0], (int)u[1], (int)u[2], (int)u[3]));
+            st_na_v4(p + 4, make_int4((int)u[4], (int)u[5], (int)u[6], (int)u[7]));
+        }
     }
 };
 
@@ -233,98 +242,220 @@ __global__ void __launch_bounds__(kMax) norm_kernel(const NormArgs a) {
     }
 }
 
-template <int kV, int kMax, bool kWarp, int kRes>
-__global__ void __launch_bounds__(kMax) norm_backward_kernel(const NormBackArgs a) {
+// The 8 channels' share of a row's sums, and then of its outputs.
+struct BackRow {
+    float s, c;  // the row's scale, and s^2 mean(g h)
+};
+__device__ __forceinline__ void back_sums(const float* h, const float* g, const float* w, float (&sum)[2]) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        sum[0] = fmaf(h[j], h[j], sum[0]);
+        sum[1] = fmaf(g[j] * w[j], h[j], sum[1]);
+    }
+}
+__device__ __forceinline__ BackRow back_row(const float (&sum)[2], const NormBackArgs& a) {
+    BackRow r;
+    r.s = rsqrtf(sum[0] / (float)a.hidden + a.eps);
+    r.c = r.s * r.s * (sum[1] / (float)a.hidden);
+    return r;
+}
+__device__ __forceinline__ void back_outputs(const BackRow& r, const float* h, const float* g, const float* w, float* d, float* dw) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        d[j] = fmaf(r.s, fmaf(-h[j], r.c, g[j] * w[j]), d[j]);
+        dw[j] = fmaf(g[j], h[j] * r.s, dw[j]);
+    }
+}
+
+// Up to 1024 channels: a warp a row, which stays in its registers.
+template <int kV, int kRes>
+__global__ void __launch_bounds__(256) norm_backward_warps(const NormBackArgs a) {
     using T = ResType<kRes>;
-    __shared__ float buf[2][2][32];
-    __shared__ float block_dw[kWarp ? kV * 256 : 1];
+    __shared__ float block_dw[kV * 256];
     grid_wait();
     grid_launch_next();
-    const int team = kWarp ? 32 : blockDim.x, me = kWarp ? threadIdx.x & 31 : threadIdx.x;
-    const int per = kWarp ? blockDim.x >> 5 : 1;
-    const int64_t step = (int64_t)gridDim.x * per;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int vecs = a.hidden >> 3;
     float dw[kV][8];
 #pragma unroll
     for (int i = 0; i < kV; ++i)
 #pragma unroll
         for (int j = 0; j < 8; ++j) dw[i][j] = 0.0f;
-    int turn = 0;
-    for (int64_t row = (int64_t)blockIdx.x * per + (kWarp ? threadIdx.x >> 5 : 0); row < a.rows; row += step, ++turn) {
+    for (int64_t row = (int64_t)blockIdx.x * 8 + warp; row < a.rows; row += (int64_t)gridDim.x * 8) {
         Raw8<__nv_bfloat16> pg[kV];
         Raw8<T> ph[kV], pd[kV];
 #pragma unroll
         for (int i = 0; i < kV; ++i) {
-            const int v = me + i * team;
+            const int v = lane + i * 32;
             if (v < vecs) {
                 pg[i].load(a.dy + row * a.dy_stride + v * 8);
                 ph[i].load(static_cast<const T*>(a.h) + row * a.h_stride + v * 8);
                 if (a.dres) pd[i].load(static_cast<const T*>(a.dres) + row * a.dres_stride + v * 8);
             }
         }
-        float sum[2] = {0.0f, 0.0f};  // h^2, g h
+        float sum[2] = {0.0f, 0.0f};
 #pragma unroll
         for (int i = 0; i < kV; ++i) {
-            const int v = me + i * team;
+            const int v = lane + i * 32;
             if (v < vecs) {
                 float h[8], g[8], w[8];
                 ph[i].get(h);
                 pg[i].get(g);
                 load_weight8(a.weight, a.weight_f32, v * 8, w);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    sum[0] = fmaf(h[j], h[j], sum[0]);
-                    sum[1] = fmaf(g[j] * w[j], h[j], sum[1]);
-                }
+                back_sums(h, g, w, sum);
             }
         }
-        row_sums<kWarp>(sum, buf, turn);
-        const float s = rsqrtf(sum[0] / (float)a.hidden + a.eps);
-        const float c = s * s * (sum[1] / (float)a.hidden);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) {
+            sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], o);
+            sum[1] += __shfl_xor_sync(0xffffffffu, sum[1], o);
+        }
+        const BackRow r = back_row(sum, a);
 #pragma unroll
         for (int i = 0; i < kV; ++i) {
-            const int v = me + i * team;
+            const int v = lane + i * 32;
             if (v < vecs) {
                 float h[8], g[8], w[8], d[8] = {};
                 ph[i].get(h);
                 pg[i].get(g);
                 load_weight8(a.weight, a.weight_f32, v * 8, w);
                 if (a.dres) pd[i].get(d);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    d[j] = fmaf(s, fmaf(-h[j], c, g[j] * w[j]), d[j]);
-                    dw[i][j] = fmaf(g[j], h[j] * s, dw[i][j]);
-                }
+                back_outputs(r, h, g, w, d, dw[i]);
                 Raw8<T> o;
                 o.round(d);
                 o.store(static_cast<T*>(a.dx) + row * a.dx_stride + v * 8);
             }
         }
     }
-    // the block's part of dw; warps that share a block add theirs in warp order
-    if constexpr (kWarp) {
-        for (int w = 0; w < per; ++w) {
-            if ((threadIdx.x >> 5) == w)
+    // the block's part of dw, its warps' in order
+    for (int w = 0; w < 8; ++w) {
+        if (warp == w)
 #pragma unroll
-                for (int i = 0; i < kV; ++i)
+            for (int i = 0; i < kV; ++i)
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        float* p = &block_dw[(me + i * 32) * 8 + j];
-                        *p = w ? *p + dw[i][j] : dw[i][j];
-                    }
-            __syncthreads();
-        }
-        for (int c = threadIdx.x; c < a.hidden; c += blockDim.x) a.part[(int64_t)blockIdx.x * a.hidden + c] = block_dw[c];
+                for (int j = 0; j < 8; ++j) {
+                    float* p = &block_dw[(lane + i * 32) * 8 + j];
+                    *p = w ? *p + dw[i][j] : dw[i][j];
+                }
+        __syncthreads();
+    }
+    for (int c = threadIdx.x; c < a.hidden; c += 256) a.part[(int64_t)blockIdx.x * a.hidden + c] = block_dw[c];
+}
+
+// More channels: a block a row.  The rows to come are on their way into shared memory by bulk copies (a stage holds dy, h
+// and d of one row, up to kBackStages of them), so that loads go on while a row is summed and written; a thread's
+// registers hold its 16 channels of dw.
+constexpr int kBackStages = 4;
+constexpr int64_t kBackWaitNs = 2000000000ll;
+
+template <typename T>
+__device__ __forceinline__ void shared8(const T* p, float* v) {
+    Raw8<T> r;
+    if constexpr (sizeof(T) == 2) {
+        r.a = *reinterpret_cast<const int4*>(p);
     } else {
+        const uint4 x = *reinterpret_cast<const uint4*>(p), y = *reinterpret_cast<const uint4*>(p + 4);
+        r.u[0] = x.x, r.u[1] = x.y, r.u[2] = x.z, r.u[3] = x.w, r.u[4] = y.x, r.u[5] = y.y, r.u[6] = y.z, r.u[7] = y.w;
+    }
+    r.get(v);
+}
+
+template <int kRes>
+__global__ void __launch_bounds__(1024) norm_backward_block(const NormBackArgs a, int stages) {
+    using T = ResType<kRes>;
+    extern __shared__ __align__(128) uint8_t ring[];
+    __shared__ uint64_t full[kBackStages];
+    __shared__ float buf[2][2][32];
+    __shared__ int abort;
+    const int tid = threadIdx.x, vecs = a.hidden >> 3;
+    const uint32_t dy_bytes = a.hidden * 2, h_bytes = a.hidden * sizeof(T);
+    const uint32_t stage = dy_bytes + (a.dres ? 2 : 1) * h_bytes;
+    if (tid == 0) {
+        for (int s = 0; s < kBackStages; ++s) mbar_init(&full[s], 1);
+        abort = 0;
+        fence_mbar_init();
+    }
+    __syncthreads();
+    grid_wait();
+    grid_launch_next();
+    auto issue = [&](int64_t row, int s) {
+        uint8_t* d = ring + s * stage;
+        mbar_arrive_expect_tx(&full[s], stage);
+        bulk_g2s(d, a.dy + row * a.dy_stride, dy_bytes, &full[s]);
+        bulk_g2s(d + dy_bytes, static_cast<const T*>(a.h) + row * a.h_stride, h_bytes, &full[s]);
+        if (a.dres) bulk_g2s(d + dy_bytes + h_bytes, static_cast<const T*>(a.dres) + row * a.dres_stride, h_bytes, &full[s]);
+    };
+    int64_t next = blockIdx.x;  // the next row to copy
+    if (tid == 0)
+        for (int s = 0; s < stages && next < a.rows; ++s, next += gridDim.x) issue(next, s);
+    float dw[2][8] = {};
+    int s = 0, turn = 0;
+    uint32_t phase = 0;
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, ++turn) {
+        // a copy that does not come ends the row loop for the whole block, and its part of dw is NaN
+        if (!mbar_wait_bounded(&full[s], phase, kBackWaitNs)) abort = 1;
+        const uint8_t* p = ring + s * stage;
+        const __nv_bfloat16* sg = reinterpret_cast<const __nv_bfloat16*>(p);
+        const T* sh = reinterpret_cast<const T*>(p + dy_bytes);
+        const T* sd = reinterpret_cast<const T*>(p + dy_bytes + h_bytes);
+        float sum[2] = {0.0f, 0.0f};
 #pragma unroll
-      for (int i = 0; i < kV; ++i) {
-        const int v = me + i * team;
+        for (int i = 0; i < 2; ++i) {
+            const int v = tid + i * blockDim.x;
+            if (v < vecs) {
+                float h[8], g[8], w[8];
+                shared8(sh + v * 8, h);
+                shared8(sg + v * 8, g);
+                load_weight8(a.weight, a.weight_f32, v * 8, w);
+                back_sums(h, g, w, sum);
+            }
+        }
+        row_sums<false>(sum, buf, turn);
+        if (*static_cast<volatile int*>(&abort)) break;
+        // every thread has left the row before: its stage takes the next copy
+        if (tid == 0 && turn > 0 && stages > 1 && next < a.rows) {
+            issue(next, s == 0 ? stages - 1 : s - 1);
+            next += gridDim.x;
+        }
+        const BackRow r = back_row(sum, a);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int v = tid + i * blockDim.x;
+            if (v < vecs) {
+                float h[8], g[8], w[8], d[8] = {};
+                shared8(sh + v * 8, h);
+                shared8(sg + v * 8, g);
+                load_weight8(a.weight, a.weight_f32, v * 8, w);
+                if (a.dres) shared8(sd + v * 8, d);
+                back_outputs(r, h, g, w, d, dw[i]);
+                Raw8<T> o;
+                o.round(d);
+                o.store(static_cast<T*>(a.dx) + row * a.dx_stride + v * 8);
+            }
+        }
+        if (stages == 1) {
+            __syncthreads();
+            if (tid == 0 && next < a.rows) {
+                issue(next, 0);
+                next += gridDim.x;
+            }
+        }
+        if (++s == stages) {
+            s = 0;
+            phase ^= 1;
+        }
+    }
+    if (abort && tid == 0)  // no copy may be in flight when the block ends
+        for (int i = 0; i < stages; ++i) mbar_wait_bounded(&full[i], i < s ? phase ^ 1 : phase, kBackWaitNs);
+    const float bad = abort ? __int_as_float(0x7fffffff) : 0.0f;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int v = tid + i * blockDim.x;
         if (v < vecs) {
             float* p = a.part + (int64_t)blockIdx.x * a.hidden + v * 8;
-            *reinterpret_cast<float4*>(p) = make_float4(dw[i][0], dw[i][1], dw[i][2], dw[i][3]);
-            *reinterpret_cast<float4*>(p + 4) = make_float4(dw[i][4], dw[i][5], dw[i][6], dw[i][7]);
+            *reinterpret_cast<float4*>(p) = make_float4(dw[i][0] + bad, dw[i][1] + bad, dw[i][2] + bad, dw[i][3] + bad);
+            *reinterpret_cast<float4*>(p + 4) = make_float4(dw[i][4] + bad, dw[i][5] + bad, dw[i][6] + bad, dw[i][7] + bad);
         }
-      }
     }
 }
 
@@ -354,31 +485,27 @@ static ep_status sm_count(int* sms) {
     return EP_OK;
 }
 
-constexpr int kNormPerSm = 6, kNormBackPerSm = 2;  // blocks of up to 256 threads
-
-// Who works on a row: `kind` 0..2: a warp with 1, 2 or 4 vectors a lane; 3: a block with one vector a thread;
-// 4: a block of up to 256 threads with 4; 5: of up to 1024 with 2.
+// Who works on a row of the forward pass: `kind` 0..2: a warp with 1, 2 or 4 vectors a lane; 3: a block with one vector a
+// thread; 4: a block of up to 256 threads with 4; 5: of up to 1024 with 2.
+constexpr int kNormPerSm = 6;  // blocks of up to 256 threads
 struct NormShape {
     int kind, threads, blocks;
 };
-static NormShape norm_shape(int64_t rows, int hidden, int sms, bool backward) {
-    int per_sm = backward ? kNormBackPerSm : kNormPerSm;
+static NormShape norm_shape(int64_t rows, int hidden, int sms) {
     const int vecs = hidden / 8;
     NormShape s;
-    int64_t units;
+    int64_t units = rows, per_sm = kNormPerSm;
     if (vecs <= 128) {
         s.kind = vecs <= 32 ? 0 : vecs <= 64 ? 1 : 2;
         s.threads = 256;
         units = (rows + 7) / 8;
     } else {
-        s.kind = vecs <= 1024 ? (rows <= sms && !backward ? 3 : 4) : 5;
+        s.kind = vecs <= 1024 ? (rows <= sms ? 3 : 4) : 5;
         const int v = s.kind == 3 ? 1 : s.kind == 4 ? 4 : 2;
         s.threads = ((vecs + v - 1) / v + 31) / 32 * 32;
-        units = rows;
         if (s.threads > 256) per_sm = s.kind == 3 ? 1 : 2;
     }
-    const int64_t most = (int64_t)sms * per_sm;
-    s.blocks = (int)(units < most ? units : most);
+    s.blocks = (int)(units < sms * per_sm ? units : sms * per_sm);
     return s;
 }
 
@@ -393,15 +520,37 @@ static ep_status launch_norm(const NormArgs& a, const NormShape& s, void* stream
         default: return launch_next(norm_kernel<2, 1024, false, kRes>, s.blocks, s.threads, stream, a);
     }
 }
+
+// Blocks of the backward pass, each with a part of dw, at most: by warps three a processor; by blocks as many as its
+// registers hold, up to 8.
+static int back_threads(int hidden) { return ((hidden / 8 + 1) / 2 + 31) / 32 * 32; }
+static int back_blocks(int64_t rows, int hidden, int sms) {
+    const int per_sm = hidden <= 1024 ? 3 : 1024 / back_threads(hidden) < 8 ? 1024 / back_threads(hidden) : 8;
+    const int64_t units = hidden <= 1024 ? (rows + 7) / 8 : rows, most = (int64_t)per_sm * sms;
+    return (int)(units < most ? units : most);
+}
+
 template <int kRes>
-static ep_status launch_norm_backward(const NormBackArgs& a, const NormShape& s, void* stream) {
-    switch (s.kind) {
-        case 0: return launch_next(norm_backward_kernel<1, 256, true, kRes>, s.blocks, s.threads, stream, a);
-        case 1: return launch_next(norm_backward_kernel<2, 256, true, kRes>, s.blocks, s.threads, stream, a);
-        case 2: return launch_next(norm_backward_kernel<4, 256, true, kRes>, s.blocks, s.threads, stream, a);
-        case 4: return launch_next(norm_backward_kernel<4, 256, false, kRes>, s.blocks, s.threads, stream, a);
-        default: return launch_next(norm_backward_kernel<2, 1024, false, kRes>, s.blocks, s.threads, stream, a);
+static ep_status launch_back(const NormBackArgs& a, int sms, int* blocks, void* stream) {
+    const int vecs = a.hidden / 8;
+    if (vecs <= 32) return launch_next(norm_backward_warps<1, kRes>, *blocks, 256, stream, a);
+    if (vecs <= 64) return launch_next(norm_backward_warps<2, kRes>, *blocks, 256, stream, a);
+    if (vecs <= 128) return launch_next(norm_backward_warps<4, kRes>, *blocks, 256, stream, a);
+    // A block's sums wait for each other, so that two blocks or more share a processor where two rows each fit.
+    const int threads = back_threads(a.hidden), stage = a.hidden * (2 + (a.dres ? 2 : 1) * (int)sizeof(ResType<kRes>));
+    constexpr int kMost = 208 * 1024;
+    int per_sm = 1024 / threads < 8 ? 1024 / threads : 8;
+    while (per_sm > 1 && per_sm * 2 * stage > kMost) --per_sm;
+    const int fit = kMost / per_sm / stage, stages = fit < kBackStages ? fit : kBackStages;
+    if (*blocks > per_sm * sms) *blocks = per_sm * sms;
+    int dev = 0;
+    EP_CUDA(cudaGetDevice(&dev));
+    static std::atomic<bool> known[kMaxDevicesTracked];  // devices whose launch attribute is set
+    if (dev >= kMaxDevicesTracked || !known[dev].load(std::memory_order_relaxed)) {
+        EP_CUDA(cudaFuncSetAttribute(norm_backward_block<kRes>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost));
+        if (dev < kMaxDevicesTracked) known[dev].store(true, std::memory_order_relaxed);
     }
+    return launch_next(norm_backward_block<kRes>, *blocks, threads, stream, Shared{(size_t)stages * stage}, a, stages);
 }
 
 static int type_bytes(int type) { return type == EP_F32 ? 4 : 2; }
@@ -450,14 +599,14 @@ extern "C" ep_status ep_rms_norm(const void* x, int64_t x_stride, const void* re
     EP_TRY(sm_count(&sms));
     const NormArgs a = {static_cast<const __nv_bfloat16*>(x), residual, weight, residual_out, static_cast<__nv_bfloat16*>(y), fp8_rows,
                         x_stride, residual_stride, residual_out_stride, y_stride, fp8_stride, rows, hidden, eps, weight_type == EP_F32};
-    const NormShape s = norm_shape(rows, hidden, sms, false);
+    const NormShape s = norm_shape(rows, hidden, sms);
     return !residual ? launch_norm<0>(a, s, stream) : residual_type == EP_BF16 ? launch_norm<1>(a, s, stream) : launch_norm<2>(a, s, stream);
 }
 
 extern "C" int64_t ep_rms_norm_backward_workspace(int64_t rows, int32_t hidden) {
     int sms = 0;
     if (rows <= 0 || rows > 0x7fffffff || hidden < 8 || hidden % 8 || hidden > kNormMaxHidden || sm_count(&sms) != EP_OK) return 0;
-    return (int64_t)norm_shape(rows, hidden, sms, true).blocks * hidden * 4;
+    return (int64_t)back_blocks(rows, hidden, sms) * hidden * 4;
 }
 
 extern "C" ep_status ep_rms_norm_backward(const void* dy, int64_t dy_stride, const void* h, int64_t h_stride, int32_t h_type,
@@ -467,7 +616,7 @@ extern "C" ep_status ep_rms_norm_backward(const void* dy, int64_t dy_stride, con
     const char* fn = "ep_rms_norm_backward";
     EP_TRY(check_norm(fn, rows, hidden, eps, h_type, weight, weight_type));
     if (!dweight || !aligned_to(dweight, 4)) return set_error(EP_ERR_INVALID_ARG, "%s: dweight is required", fn);
-    NormShape s = {0, 256, 0};
+    int blocks = 0;
     if (rows > 0) {
         EP_TRY(check_rows(fn, "dy", dy, dy_stride, rows, hidden, EP_BF16));
         EP_TRY(check_rows(fn, "h", h, h_stride, rows, hidden, h_type));
@@ -475,13 +624,13 @@ extern "C" ep_status ep_rms_norm_backward(const void* dy, int64_t dy_stride, con
         if (dresidual) EP_TRY(check_rows(fn, "dresidual", dresidual, dresidual_stride, rows, hidden, h_type));
         int sms = 0;
         EP_TRY(sm_count(&sms));
-        s = norm_shape(rows, hidden, sms, true);
-        if (!workspace || !aligned16(workspace) || workspace_bytes < (int64_t)s.blocks * hidden * 4)
+        blocks = back_blocks(rows, hidden, sms);
+        if (!workspace || !aligned16(workspace) || workspace_bytes < (int64_t)blocks * hidden * 4)
             return set_error(EP_ERR_INVALID_ARG, "%s: workspace of %lld bytes (16-byte aligned), %lld needed", fn,
-                             (long long)workspace_bytes, (long long)s.blocks * hidden * 4);
+                             (long long)workspace_bytes, (long long)blocks * hidden * 4);
         const NormBackArgs a = {static_cast<const __nv_bfloat16*>(dy), h, dresidual, weight, dx, static_cast<float*>(workspace),
                                 dy_stride, h_stride, dresidual_stride, dx_stride, rows, hidden, eps, weight_type == EP_F32};
-        EP_TRY(h_type == EP_BF16 ? launch_norm_backward<1>(a, s, stream) : launch_norm_backward<2>(a, s, stream));
+        EP_TRY(h_type == EP_BF16 ? launch_back<1>(a, sms, &blocks, stream) : launch_back<2>(a, sms, &blocks, stream));
     }
-    return launch_next(norm_weight_kernel, (hidden + 31) / 32, 256, stream, static_cast<const float*>(workspace), s.blocks, hidden, dweight);
+    return launch_next(norm_weight_kernel, (hidden + 31) / 32, 256, stream, static_cast<const float*>(workspace), blocks, hidden, dweight);
 }
