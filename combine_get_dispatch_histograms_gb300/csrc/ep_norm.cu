@@ -491,7 +491,7 @@ constexpr int kNormPerSm = 6;  // blocks of up to 256 threads
 struct NormShape {
     int kind, threads, blocks;
 };
-static NormShape norm_shape(int64_t rows, int hidden, int sms) {
+static NormShape norm_shape(int64_t rows, int hidden, int sms, bool wide) {
     const int vecs = hidden / 8;
     NormShape s;
     int64_t units = rows, per_sm = kNormPerSm;
@@ -500,10 +500,10 @@ static NormShape norm_shape(int64_t rows, int hidden, int sms) {
         s.threads = 256;
         units = (rows + 7) / 8;
     } else {
-        s.kind = vecs <= 1024 ? (rows <= sms ? 3 : 4) : 5;
+        s.kind = vecs > 1024 ? 5 : rows <= sms ? 3 : wide ? 5 : 4;
         const int v = s.kind == 3 ? 1 : s.kind == 4 ? 4 : 2;
         s.threads = ((vecs + v - 1) / v + 31) / 32 * 32;
-        if (s.threads > 256) per_sm = s.kind == 3 ? 1 : 2;
+        per_sm = s.kind == 3 ? 1 : s.kind == 5 ? 1024 / s.threads : kNormPerSm;
     }
     s.blocks = (int)(units < sms * per_sm ? units : sms * per_sm);
     return s;
@@ -599,7 +599,7 @@ extern "C" ep_status ep_rms_norm(const void* x, int64_t x_stride, const void* re
     EP_TRY(sm_count(&sms));
     const NormArgs a = {static_cast<const __nv_bfloat16*>(x), residual, weight, residual_out, static_cast<__nv_bfloat16*>(y), fp8_rows,
                         x_stride, residual_stride, residual_out_stride, y_stride, fp8_stride, rows, hidden, eps, weight_type == EP_F32};
-    const NormShape s = norm_shape(rows, hidden, sms);
+    const NormShape s = norm_shape(rows, hidden, sms, residual && residual_type == EP_F32);
     return !residual ? launch_norm<0>(a, s, stream) : residual_type == EP_BF16 ? launch_norm<1>(a, s, stream) : launch_norm<2>(a, s, stream);
 }
 

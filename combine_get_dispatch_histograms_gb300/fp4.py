@@ -32,11 +32,14 @@ def quantize_fp4(x, out=None, stream=None):
         _refuse(f"quantize_fp4: bf16 rows [rows][K] or [E][rows][K], K a multiple of 128: got {x.dtype} {tuple(shape)}")
     k = shape[-1]
     if out is None:
-        out = _empty(x, stream, (*shape[:-1], k // 2), _U8), _empty(x, stream, (*shape[:-1], k // 32), _U8)
-    codes, scales = out
-    _call("ep_quantize_fp4", index, x.data_ptr(), _step("quantize_fp4: x", x), x.numel() // k, k, codes.data_ptr(),
-          _output("quantize_fp4: out codes", codes, shape, k // 2, (_U8,), index), scales.data_ptr(),
-          _output("quantize_fp4: out scales", scales, shape, k // 32, (_U8,), index), _stream_of(stream, index))
+        cs, ss = k // 2, k // 32
+        codes, scales = _empty(x, stream, (*shape[:-1], cs), _U8), _empty(x, stream, (*shape[:-1], ss), _U8)
+    else:
+        codes, scales = out
+        cs = _output("quantize_fp4: out codes", codes, shape, k // 2, (_U8,), index)
+        ss = _output("quantize_fp4: out scales", scales, shape, k // 32, (_U8,), index)
+    _call("ep_quantize_fp4", index, x.data_ptr(), _step("quantize_fp4: x", x), x.numel() // k, k, codes.data_ptr(), cs, scales.data_ptr(), ss,
+          _stream_of(stream, index))
     return codes, scales
 
 
@@ -91,10 +94,12 @@ def _products(name, x, x_scales, w, w_scales, counts, offsets, bases, expected):
 def expert_gemm_fp4(x, x_scales, w, w_scales, counts=None, offsets=None, out=None, status=None, stream=None, *, bases=None, expected_rows=0):
     """y = x w^T per expert: bf16 [rows][N] (or [E][cap][N]).  Rows of no expert are not written.  Arguments as expert_gemm's."""
     index, shape, n, cx, cg, cw = _products("expert_gemm_fp4", x, x_scales, w, w_scales, counts, offsets, bases, expected_rows)
+    step = n
     if out is None:
         out = _empty(x, stream, (*shape[:-1], n), _BF16)
-    _call("ep_expert_gemm_fp4", index, cx, cg, cw, out.data_ptr(), _output("expert_gemm_fp4: out", out, shape, n, (_BF16,), index),
-          _status_ptr(status, index), _stream_of(stream, index))
+    else:
+        step = _output("expert_gemm_fp4: out", out, shape, n, (_BF16,), index)
+    _call("ep_expert_gemm_fp4", index, cx, cg, cw, out.data_ptr(), step, _status_ptr(status, index), _stream_of(stream, index))
     return out
 
 
@@ -107,10 +112,12 @@ def expert_swiglu_fp4(x, x_scales, w13, w13_scales, counts=None, offsets=None, o
         _refuse(f"expert_swiglu_fp4: {n} weight rows are no gate and up of a multiple of 128 each")
     inter = n // 2
     if out is None:
-        out = _empty(x, stream, (*shape[:-1], inter // 2), _U8), _empty(x, stream, (*shape[:-1], inter // 32), _U8)
-    codes, scales = out
-    _call("ep_expert_swiglu_fp4", index, cx, cg, cw, codes.data_ptr(),
-          _output("expert_swiglu_fp4: out codes", codes, shape, inter // 2, (_U8,), index), scales.data_ptr(),
-          _output("expert_swiglu_fp4: out scales", scales, shape, inter // 32, (_U8,), index), _status_ptr(status, index),
+        cs, ss = inter // 2, inter // 32
+        codes, scales = _empty(x, stream, (*shape[:-1], cs), _U8), _empty(x, stream, (*shape[:-1], ss), _U8)
+    else:
+        codes, scales = out
+        cs = _output("expert_swiglu_fp4: out codes", codes, shape, inter // 2, (_U8,), index)
+        ss = _output("expert_swiglu_fp4: out scales", scales, shape, inter // 32, (_U8,), index)
+    _call("ep_expert_swiglu_fp4", index, cx, cg, cw, codes.data_ptr(), cs, scales.data_ptr(), ss, _status_ptr(status, index),
           _stream_of(stream, index))
     return codes, scales

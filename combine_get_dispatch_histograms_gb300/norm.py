@@ -8,6 +8,8 @@ the weight.  The FP8 rows are those of Context.quantize_fp8: what dispatch_fp8 a
 """
 from __future__ import annotations
 
+import functools
+
 import torch
 
 from . import _lib
@@ -22,6 +24,13 @@ def _rows(name, t, shape, dtypes, index):
     if t.dtype not in dtypes or t.shape != shape or t.get_device() != index:
         _refuse(f"{name}: {' or '.join(str(d) for d in dtypes)} {tuple(shape)} on the same CUDA device: got {t.dtype} {tuple(t.shape)}")
     return _step(name, t) if t.dim() > 1 else shape[-1]
+
+
+def _made(name, given, like, stream, shape, dtype, index):
+    """(output, elements between its rows): the given one, checked, or a new one on `like`'s device."""
+    if given is None:
+        return _empty(like, stream, shape, dtype), shape[-1]
+    return given, _rows(name, given, shape, (dtype,), index)
 
 
 def _inputs(name, x, weight):
@@ -43,31 +52,30 @@ def rms_norm(x, weight, eps=1e-6, residual=None, y=True, fp8=False, out=None, st
     y, fp8: which outputs to make.  out: a dict with some of them to write into; "residual" may be the residual itself and
     "y" may be x, so that nothing is allocated."""
     index, shape, rows, hidden = _inputs("rms_norm", x, weight)
-    got = {} if out is None else dict(out)
+    given = {} if out is None else out
+    got = {}
     sx = _rows("rms_norm: x", x, shape, (_BF16,), index)
     rt = sr = so = sy = sq = 0
+    r_at = o_at = y_at = q_at = None  # without an output: no array
     if residual is not None:
+        kind = residual.dtype
         sr = _rows("rms_norm: residual", residual, shape, (_BF16, _F32), index)
-        rt = _TYPES[residual.dtype]
-        if got.get("residual") is None:
-            got["residual"] = _empty(x, stream, shape, residual.dtype)
-        so = _rows("rms_norm: out residual", got["residual"], shape, (residual.dtype,), index)
-    elif got.get("residual") is not None:
+        rt, r_at = _TYPES[kind], residual.data_ptr()
+        got["residual"], so = _made("rms_norm: out residual", given.get("residual"), x, stream, shape, kind, index)
+        o_at = got["residual"].data_ptr()
+    elif given.get("residual") is not None:
         _refuse("rms_norm: an output for the residual, but no residual")
-    if y or got.get("y") is not None:
-        if got.get("y") is None:
-            got["y"] = _empty(x, stream, shape, _BF16)
-        sy = _rows("rms_norm: out y", got["y"], shape, (_BF16,), index)
-    if fp8 or got.get("rows") is not None:
+    if y or given.get("y") is not None:
+        got["y"], sy = _made("rms_norm: out y", given.get("y"), x, stream, shape, _BF16, index)
+        y_at = got["y"].data_ptr()
+    if fp8 or given.get("rows") is not None:
         if hidden % 128:
             _refuse(f"rms_norm: FP8 rows of {hidden} channels (a multiple of 128)")
         size = (hidden + hidden // 32 + 15) // 16 * 16
-        if got.get("rows") is None:
-            got["rows"] = _empty(x, stream, (rows, size), _U8)
-        sq = _rows("rms_norm: out rows", got["rows"], (rows, size), (_U8,), index)
-    ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
-    _call("ep_rms_norm", index, x.data_ptr(), sx, ptr(residual), sr, rt, weight.data_ptr(), _TYPES[weight.dtype], eps, rows, hidden,
-          ptr(got.get("residual")), so, ptr(got.get("y")), sy, ptr(got.get("rows")), sq, _stream_of(stream, index))
+        got["rows"], sq = _made("rms_norm: out rows", given.get("rows"), x, stream, (rows, size), _U8, index)
+        q_at = got["rows"].data_ptr()
+    _call("ep_rms_norm", index, x.data_ptr(), sx, r_at, sr, rt, weight.data_ptr(), _TYPES[weight.dtype], eps, rows, hidden, o_at, so, y_at, sy,
+          q_at, sq, _stream_of(stream, index))
     return got
 
 
@@ -81,8 +89,8 @@ def rms_norm_backward(dy, h, weight, eps=1e-6, dresidual=None, out=None, workspa
     sh = _rows("rms_norm_backward: h", h, shape, (_BF16, _F32), index)
     sg = _rows("rms_norm_backward: dy", dy, shape, (_BF16,), index)
     sd = 0 if dresidual is None else _rows("rms_norm_backward: dresidual", dresidual, shape, (h.dtype,), index)
-    dx, dweight = (_empty(h, stream, shape, h.dtype), _empty(h, stream, (hidden,), _F32)) if out is None else out
-    so = _rows("rms_norm_backward: out dx", dx, shape, (h.dtype,), index)
+    dx, dweight = (None, _empty(h, stream, (hidden,), _F32)) if out is None else out
+    dx, so = _made("rms_norm_backward: out dx", dx, h, stream, shape, h.dtype, index)
     if dweight.dtype != _F32 or dweight.shape != (hidden,) or not dweight.is_contiguous() or dweight.get_device() != index:
         _refuse(f"rms_norm_backward: out dweight fp32 [{hidden}], contiguous, on the same device")
     if workspace is None:
@@ -100,6 +108,7 @@ def rms_norm_backward_workspace(rows: int, hidden: int) -> int:
     return int(_lib.load().ep_rms_norm_backward_workspace(rows, hidden))
 
 
+@functools.lru_cache(maxsize=1024)
 def _workspace_bytes(name: str, index: int, *args) -> int:
     with torch.cuda.device(index):
         return int(_entry(name)(*args))

@@ -60,9 +60,14 @@ def route(logits, topk: int, bias=None, mask=None, scoring="softmax", normalize=
     r = _descriptor("route", logits, shape, topk, scoring, normalize, groups, groups if topk_groups is None else topk_groups, scale)
     bias_at = None if bias is None else _plain("route: bias", bias, shape[-1:], _F32, index)
     mask_at = None if mask is None else _plain("route: mask", mask, lead, _BOOL if mask.dtype == _BOOL else _U8, index)
-    idx, weights = (_empty(logits, stream, (*lead, topk), _I64), _empty(logits, stream, (*lead, topk), _F32)) if out is None else out
-    _call("ep_route", index, r, logits.data_ptr(), step, bias_at, mask_at, _plain("route: out topk_idx", idx, (*lead, topk), _I64, index),
-          _plain("route: out topk_weights", weights, (*lead, topk), _F32, index), _stream_of(stream, index))
+    shape = (*lead, topk)
+    if out is None:
+        idx, weights = _empty(logits, stream, shape, _I64), _empty(logits, stream, shape, _F32)
+    else:
+        idx, weights = out
+        _plain("route: out topk_idx", idx, shape, _I64, index)
+        _plain("route: out topk_weights", weights, shape, _F32, index)
+    _call("ep_route", index, r, logits.data_ptr(), step, bias_at, mask_at, idx.data_ptr(), weights.data_ptr(), _stream_of(stream, index))
     return idx, weights
 
 
@@ -81,17 +86,21 @@ def balance_loss(logits, topk_idx, coef=1.0, scoring="softmax", out=None, worksp
     sequences = lead[0] if len(lead) == 2 else 1
     idx_at = _plain("balance_loss: topk_idx", topk_idx, (*lead, topk), _I64, index)
     r = _descriptor("balance_loss", logits, shape, topk, scoring)
-    got = {"loss": _empty(logits, stream, (1,), _F32), "counts": _empty(logits, stream, (sequences, experts), _I32),
-           "factors": _empty(logits, stream, (sequences, experts), _F32)} if out is None else out
-    at = [_plain(f"balance_loss: out {k}", got[k], s, d, index)
-          for k, s, d in (("loss", (1,), _F32), ("counts", (sequences, experts), _I32), ("factors", (sequences, experts), _F32))]
+    if out is None:
+        shape = (sequences, experts)
+        loss, counts, factors = _empty(logits, stream, (1,), _F32), _empty(logits, stream, shape, _I32), _empty(logits, stream, shape, _F32)
+    else:
+        loss, counts, factors = out["loss"], out["counts"], out["factors"]
+        _plain("balance_loss: out loss", loss, (1,), _F32, index)
+        _plain("balance_loss: out counts", counts, (sequences, experts), _I32, index)
+        _plain("balance_loss: out factors", factors, (sequences, experts), _F32, index)
     if workspace is None:
         workspace = _empty(logits, stream, (_workspace_bytes("ep_balance_loss_workspace", index, r, sequences),), _U8)
     elif not workspace.is_contiguous() or workspace.get_device() != index:
         _refuse("balance_loss: workspace must be contiguous, on the same device")
-    _call("ep_balance_loss", index, r, logits.data_ptr(), step, idx_at, sequences, coef, *at, workspace.data_ptr(), workspace.nbytes,
-          _status_ptr(status, index), _stream_of(stream, index))
-    return got
+    _call("ep_balance_loss", index, r, logits.data_ptr(), step, idx_at, sequences, coef, loss.data_ptr(), counts.data_ptr(),
+          factors.data_ptr(), workspace.data_ptr(), workspace.nbytes, _status_ptr(status, index), _stream_of(stream, index))
+    return {"loss": loss, "counts": counts, "factors": factors}
 
 
 def balance_loss_workspace(tokens: int, experts: int, sequences: int = 1) -> int:
@@ -115,10 +124,13 @@ def router_backward(logits, topk_idx, dweights=None, factors=None, dloss=None, s
     f_at = None if factors is None else _plain("router_backward: factors", factors, (sequences, experts), _F32, index)
     dl_at = None if dloss is None else _plain("router_backward: dloss", dloss, (1,), _F32, index)
     r = _descriptor("router_backward", logits, shape, topk, scoring, normalize, 1, 1, scale)
+    out_step = experts
     if out is None:
         out = _empty(logits, stream, shape, logits.dtype)
     elif out.dtype != logits.dtype or out.shape != shape or out.get_device() != index:
         _refuse(f"router_backward: out {logits.dtype} {tuple(shape)} on the same CUDA device: got {out.dtype} {tuple(out.shape)}")
-    _call("ep_router_backward", index, r, logits.data_ptr(), step, idx_at, dw_at, f_at, sequences, dl_at, out.data_ptr(),
-          _step("router_backward: out", out), _status_ptr(status, index), _stream_of(stream, index))
+    else:
+        out_step = _step("router_backward: out", out)
+    _call("ep_router_backward", index, r, logits.data_ptr(), step, idx_at, dw_at, f_at, sequences, dl_at, out.data_ptr(), out_step,
+          _status_ptr(status, index), _stream_of(stream, index))
     return out
