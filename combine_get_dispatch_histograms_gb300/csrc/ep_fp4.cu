@@ -12,6 +12,7 @@
 // products, four write the results.  With 192 weight rows a tile tensor memory holds two accumulators and
 // the scales beside them, so that a tile is written while the next is multiplied.
 #include <atomic>
+#include <cstdlib>
 
 #include "ep_fp4.cuh"
 #include "ep_groups.cuh"
@@ -24,18 +25,25 @@ constexpr int k4BoxRows = 32;     // rows of one copy of x
 constexpr int k4ScaleWarps = 4, k4OutWarps = 4;
 constexpr int k4Threads = 128 + 32 * (k4ScaleWarps + k4OutWarps);
 constexpr int k4TileRing = 4;
+constexpr int k4Group = 4;        // stages whose scales are staged together: 32 bytes of a row, a whole sector
+constexpr int k4Slots = 2;        // of such groups
 constexpr int64_t k4WaitNs = 2000000000ll;
 
-template <int kBN>
+// kCtas = 2: a pair of blocks makes a tile of 256 rows; each copies half of the weight's rows, so that an SM takes in 28 KB
+// of codes a stage instead of 40, and all of the weight rows' scales.
+template <int kBN, int kCtas>
 struct Fp4Shape {
+    static constexpr int kTileM = kCtas * k4BM;
     static constexpr int kChunks = (kBN + 127) / 128;               // of 128 weight rows' scales
-    static constexpr int kCodesA = k4BM * 128, kCodesB = kBN * 128;
+    static constexpr int kCodesA = k4BM * 128, kCodesB = kBN / kCtas * 128;
     static constexpr int kScalesA = 2 * 512, kScalesB = 2 * kChunks * 512;  // [128 of K][chunk][32][16]
-    static constexpr int kStage = kCodesA + kCodesB + kScalesA + kScalesB;
-    static constexpr int kStages = kBN > 128 ? 5 : 8;
+    static constexpr int kCodes = kCodesA + kCodesB, kScales = kScalesA + kScalesB;
     static constexpr int kOutRow = 34 * 2;                          // bytes of a staged row of 32 bf16: rows fall into other banks
     static constexpr int kOut = 32 * kOutRow;
-    static constexpr size_t kSmem = 1024 + kStages * kStage + k4OutWarps * kOut;
+    static constexpr int kSlot = k4Group * kScales;                 // the scales that are staged together
+    static constexpr int kRest = k4Slots * kSlot + k4OutWarps * kOut;
+    static constexpr int kStages = (225 * 1024 - kRest) / kCodes < 8 ? (225 * 1024 - kRest) / kCodes : 8;
+    static constexpr size_t kSmem = 1024 + kStages * kCodes + kRest;
     // columns of tensor memory: two accumulators, then two sets of scales in turn
     static constexpr int kScaleCols = 8 + 2 * kChunks * 4, kScaleAt = 2 * kBN;
     static constexpr int kCols = 2 * kBN + 2 * kScaleCols > 256 ? 512 : 256;
@@ -51,13 +59,13 @@ struct Fp4Args : TileArgs {
     uint8_t* out_scales;
     int64_t out_sstride;
     bool out_vec, out_wide;   // 16- and 32-byte stores
-    bool x_vec, w_vec;        // 16-byte loads of scales
+    int x_vec, w_vec;         // bytes of scales that a load may take: 32, 16 or 4
     uint32_t* status;
 };
 
 template <int kStages>
 struct Fp4Shared {
-    uint64_t full[kStages], scales[kStages], done[kStages], acc_full[2], acc_empty[2];
+    uint64_t full[kStages], done[kStages], scale_full[k4Slots], scale_empty[k4Slots], acc_full[2], acc_empty[2];
     uint64_t tile_full[k4TileRing], tile_empty[k4TileRing], drain;
     uint32_t tmem;
     int abort;
@@ -77,45 +85,63 @@ struct Turn {
     }
 };
 
-// 16 bytes of scales from byte `at` of a row with `bytes` of them (a multiple of 4); 0 past its end.
-__device__ __forceinline__ uint4 load_scales(const uint8_t* row, int at, int bytes, bool vec) {
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (vec && at + 16 <= bytes) return *reinterpret_cast<const uint4*>(row + at);
-    if (at < bytes) v.x = *reinterpret_cast<const uint32_t*>(row + at);
-    if (at + 4 < bytes) v.y = *reinterpret_cast<const uint32_t*>(row + at + 4);
-    if (at + 8 < bytes) v.z = *reinterpret_cast<const uint32_t*>(row + at + 8);
-    if (at + 12 < bytes) v.w = *reinterpret_cast<const uint32_t*>(row + at + 12);
-    return v;
+// 32 bytes of scales, four stages', from byte `at` of a row with `bytes` of them (a multiple of 4); 0 past its end.
+struct Scales32 {
+    uint32_t v[8];
+};
+__device__ __forceinline__ Scales32 load_scales(const uint8_t* row, int at, int bytes, int vec) {
+    Scales32 s;
+    if (vec == 32 && at + 32 <= bytes) {
+        asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(s.v[0]), "=r"(s.v[1]), "=r"(s.v[2]), "=r"(s.v[3]), "=r"(s.v[4]), "=r"(s.v[5]), "=r"(s.v[6]), "=r"(s.v[7])
+                     : "l"(row + at));
+        return s;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; i += 4) {
+        if (vec >= 16 && at + i * 4 + 16 <= bytes) {
+            const uint4 q = *reinterpret_cast<const uint4*>(row + at + i * 4);
+            s.v[i] = q.x, s.v[i + 1] = q.y, s.v[i + 2] = q.z, s.v[i + 3] = q.w;
+        } else {
+#pragma unroll
+            for (int j = i; j < i + 4; ++j) s.v[j] = at + j * 4 < bytes ? *reinterpret_cast<const uint32_t*>(row + at + j * 4) : 0;
+        }
+    }
+    return s;
 }
 
 // kSwiglu: half of the tile's weight rows are gate rows, half the up rows of the same channels.
-template <bool kSwiglu, int kBN>
+template <bool kSwiglu, int kBN, int kCtas>
 __global__ void __launch_bounds__(k4Threads, 1)
 fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w, const Fp4Args a) {
-    using Shape = Fp4Shape<kBN>;
-    constexpr int kStages = Shape::kStages, kHalf = kBN / 2;
+    using Shape = Fp4Shape<kBN, kCtas>;
+    constexpr int kStages = Shape::kStages, kCodes = Shape::kCodes, kScales = Shape::kScales, kHalf = kBN / 2, kTileM = Shape::kTileM;
     extern __shared__ __align__(1024) uint8_t dyn[];
     __shared__ Fp4Shared<kStages> sh;
     // codes of all stages first, each on 1024 bytes; then the scales, then the rows on their way out
     uint8_t* codes = dyn + ((1024u - (smem_u32(dyn) & 1023u)) & 1023u);
-    constexpr int kCodes = Shape::kCodesA + Shape::kCodesB, kScales = Shape::kScalesA + Shape::kScalesB;
     uint8_t* scales = codes + kStages * kCodes;
-    uint8_t* out_stage = scales + kStages * kScales;
+    uint8_t* out_stage = scales + k4Slots * Shape::kSlot;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rank = kCtas == 2 ? (int)cluster_rank() : 0, unit = blockIdx.x / kCtas, units = gridDim.x / kCtas;
     volatile int* abort = &sh.abort;
-    const uint32_t full = smem_u32(sh.full), staged = smem_u32(sh.scales), done = smem_u32(sh.done);
+    const uint32_t full = smem_u32(sh.full), done = smem_u32(sh.done);
+    const uint32_t scale_full = smem_u32(sh.scale_full), scale_empty = smem_u32(sh.scale_empty);
     const uint32_t acc_full = smem_u32(sh.acc_full), acc_empty = smem_u32(sh.acc_empty);
     const uint32_t tile_full = smem_u32(sh.tile_full), tile_empty = smem_u32(sh.tile_empty);
 
     if (tid == 0) {
         for (int s = 0; s < kStages; ++s) {
             mbar_init(&sh.full[s], 1);
-            mbar_init(&sh.scales[s], k4ScaleWarps);
             mbar_init(&sh.done[s], 1);
+        }
+        for (int b = 0; b < k4Slots; ++b) {
+            mbar_init(&sh.scale_full[b], k4ScaleWarps + (kCtas == 2 && rank == 0));
+            mbar_init(&sh.scale_empty[b], 1);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&sh.acc_full[b], 1);
-            mbar_init(&sh.acc_empty[b], k4OutWarps);
+            mbar_init(&sh.acc_empty[b], kCtas * k4OutWarps);
         }
         for (int b = 0; b < k4TileRing; ++b) {
             mbar_init(&sh.tile_full[b], 1);
@@ -128,9 +154,10 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
         tma_prefetch_desc(&map_x);
         tma_prefetch_desc(&map_w);
     }
-    if (warp == 2) tmem_alloc<1>(&sh.tmem, Shape::kCols);
+    if (warp == 2) tmem_alloc<kCtas>(&sh.tmem, Shape::kCols);
     tc_fence_before();
     __syncthreads();
+    if (kCtas == 2) cluster_sync();  // both blocks' barriers are ready
     tc_fence_after();
     // All above may run beside the end of the kernel before; the kernel after may do the same.
     grid_wait();
@@ -139,9 +166,9 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
 
     if (warp == 3) {
         // ---- tiles
-        TileWalk<k4BM> walk;
+        TileWalk<kTileM> walk;
         RingPos<k4TileRing> tr;
-        for (int t = blockIdx.x;; t += gridDim.x) {
+        for (int t = unit;; t += units) {
             GemmTile tile = {0, 0, 0, 0};
             const bool some = walk.find(a, min(t, a.most), lane, &tile);
             if (t >= a.most) tile.rows = 0;  // groups that overlap may have any number of tiles
@@ -160,7 +187,7 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
         if (walk.cut && a.status && blockIdx.x == 0) flag(a.status, FLAG_CAPACITY);
     } else if (warp == 0) {
         if (lane == 0) {
-            // ---- copies of codes
+            // ---- copies of codes: each block fills its own half of a stage; block 0's barrier counts the bytes of both
             RingPos<k4TileRing> tr;
             Turn<kStages> st;
             bool ok = true;
@@ -170,82 +197,115 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
                 mbar_arrive(tr.bar(tile_empty));
                 ++tr.n;
                 if (tile.rows == 0) break;
-                const int boxes = (tile.rows + k4BoxRows - 1) / k4BoxRows;
-                const uint32_t bytes = boxes * k4BoxRows * 128 + kBN * 128;
-                const int w0 = kSwiglu ? tile.n * kHalf : tile.n * kBN, w1 = a.N / 2 + w0;
+                const int boxes0 = (min(tile.rows, k4BM) + k4BoxRows - 1) / k4BoxRows;
+                const int boxes1 = (max(tile.rows - k4BM, 0) + k4BoxRows - 1) / k4BoxRows;
+                const uint32_t bytes = (boxes0 + boxes1) * k4BoxRows * 128 + kBN * 128;
+                const int boxes = rank ? boxes1 : boxes0, row = tile.row0 + rank * k4BM;
+                const int w0 = kSwiglu ? tile.n * kHalf : tile.n * kBN, w1 = kSwiglu ? a.N / 2 + w0 : w0 + kHalf;
+                const uint32_t full0 = kCtas == 2 ? smem_of(full, 0) : full;
                 for (int kt = 0; kt < a.KT; ++kt) {
                     if (!mbar_wait_or_abort<true>(done + st.slot * 8, st.phase ^ 1, k4WaitNs, abort)) {
                         ok = false;
                         break;
                     }
                     uint8_t* sa = codes + st.slot * kCodes;
-                    const uint32_t bar = full + st.slot * 8;
-                    mbar_arrive_expect_tx(&sh.full[st.slot], bytes);
-                    tma_load_3d<1>(sa + Shape::kCodesA, &map_w, kt * 128, w0, tile.g, bar);
-                    if (kSwiglu) tma_load_3d<1>(sa + Shape::kCodesA + kHalf * 128, &map_w, kt * 128, w1, tile.g, bar);
+                    const uint32_t bar = full0 + st.slot * 8;
+                    if (rank == 0) mbar_arrive_expect_tx(&sh.full[st.slot], bytes);
+                    tma_load_3d<kCtas>(sa + Shape::kCodesA, &map_w, kt * 128, rank ? w1 : w0, tile.g, bar);
+                    if (kCtas == 1 && kSwiglu) tma_load_3d<kCtas>(sa + Shape::kCodesA + kHalf * 128, &map_w, kt * 128, w1, tile.g, bar);
                     for (int b = 0; b < boxes; ++b)
-                        tma_load_2d<1>(sa + b * k4BoxRows * 128, &map_x, kt * 128, tile.row0 + b * k4BoxRows, bar);
+                        tma_load_2d<kCtas>(sa + b * k4BoxRows * 128, &map_x, kt * 128, row + b * k4BoxRows, bar);
                     st.next();
                 }
             }
-            // no copy may be in flight when the block ends, also after a wait that ran out: the last phase that
+            // no copy may be in flight when the blocks end, also after a wait that ran out: the last phase that
             // a stage's copies complete is the one before its next
-            for (int u = 0; u < kStages; ++u) {
-                mbar_wait_bounded(&sh.full[st.slot], st.phase ^ 1, k4WaitNs);
-                st.next();
-            }
+            if (rank == 0)
+                for (int u = 0; u < kStages; ++u) {
+                    mbar_wait_bounded(&sh.full[st.slot], st.phase ^ 1, k4WaitNs);
+                    st.next();
+                }
         }
     } else if (warp == 1) {
-        // ---- copies of scales into tensor memory, products
-        constexpr uint32_t idesc0 = idesc_mxf4(k4BM, kBN, 0), idesc2 = idesc_mxf4(k4BM, kBN, 2);
-        const uint64_t da0 = smem_desc_sw128(codes), db0 = smem_desc_sw128(codes + Shape::kCodesA), ds0 = smem_desc_rows16(scales);
-        RingPos<k4TileRing> tr;
-        Turn<kStages> st;
-        uint32_t set = 0;
-        while (true) {
-            mbar_wait_warp<true>(tr.bar(tile_full), tr.phase(), k4WaitNs, abort);
-            const int rows = sh.tile[tr.slot()].rows;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(tr.bar(tile_empty));
-            const uint32_t c = tr.n & 1, turn = tr.n >> 1 & 1;
-            ++tr.n;
-            if (rows == 0 || __any_sync(0xffffffffu, *abort)) break;
-            mbar_wait_warp<true>(acc_empty + c * 8, turn ^ 1, k4WaitNs, abort);
-#pragma unroll 1
-            for (int kt = 0; kt < a.KT; ++kt) {
-                mbar_wait_warp<true>(full + st.slot * 8, st.phase, k4WaitNs, abort);
-                mbar_wait_warp<true>(staged + st.slot * 8, st.phase, k4WaitNs, abort);
-                tc_fence_after();
-                if (elect_one()) {
-                    const uint32_t sa = tmem + Shape::kScaleAt + set * Shape::kScaleCols, sb = sa + 8;
-                    const uint64_t ds = ds0 + st.slot * (kScales >> 4);
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) tmem_copy_scales<1>(sa + h * 4, ds + h * 32);
-#pragma unroll
-                    for (int h = 0; h < 2 * Shape::kChunks; ++h) tmem_copy_scales<1>(sb + h * 4, ds + (Shape::kScalesA >> 4) + h * 32);
-                    const uint32_t at = st.slot * (kCodes >> 4);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        mma_mxf4<1>(tmem + c * kBN, da0 + at + k * 2, db0 + at + k * 2, k & 1 ? idesc2 : idesc0, sa + (k >> 1) * 4,
-                                    sb + (k >> 1) * 4 * Shape::kChunks, kt > 0 || k > 0);
-                    mma_commit<1>(done + st.slot * 8);
-                    if (kt == a.KT - 1) mma_commit<1>(acc_full + c * 8);
-                }
+        if (rank == 0) {
+            // ---- copies of scales into tensor memory, products: for both blocks of a pair by the first
+            constexpr uint32_t idesc0 = idesc_mxf4(kTileM, kBN, 0), idesc2 = idesc_mxf4(kTileM, kBN, 2);
+            const uint64_t da0 = smem_desc_sw128(codes), db0 = smem_desc_sw128(codes + Shape::kCodesA), ds0 = smem_desc_rows16(scales);
+            RingPos<k4TileRing> tr;
+            Turn<kStages> st;
+            Turn<k4Slots> sl;
+            uint32_t set = 0;
+            while (true) {
+                mbar_wait_warp<true>(tr.bar(tile_full), tr.phase(), k4WaitNs, abort);
+                const int rows = sh.tile[tr.slot()].rows;
                 __syncwarp();
-                st.next();
-                set ^= 1;
+                if (lane == 0) mbar_arrive(tr.bar(tile_empty));
+                const uint32_t c = tr.n & 1, turn = tr.n >> 1 & 1;
+                ++tr.n;
+                if (rows == 0 || __any_sync(0xffffffffu, *abort)) break;
+                mbar_wait_warp<true>(acc_empty + c * 8, turn ^ 1, k4WaitNs, abort);
+#pragma unroll 1
+                for (int kt = 0; kt < a.KT; ++kt) {
+                    const int g = kt & (k4Group - 1);
+                    if (g == 0) mbar_wait_warp<true>(scale_full + sl.slot * 8, sl.phase, k4WaitNs, abort);
+                    mbar_wait_warp<true>(full + st.slot * 8, st.phase, k4WaitNs, abort);
+                    tc_fence_after();
+                    if (elect_one()) {
+                        const uint32_t sa = tmem + Shape::kScaleAt + set * Shape::kScaleCols, sb = sa + 8;
+                        const uint64_t ds = ds0 + sl.slot * (Shape::kSlot >> 4) + g * (kScales >> 4);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) tmem_copy_scales<kCtas>(sa + h * 4, ds + h * 32);
+#pragma unroll
+                        for (int h = 0; h < 2 * Shape::kChunks; ++h)
+                            tmem_copy_scales<kCtas>(sb + h * 4, ds + (Shape::kScalesA >> 4) + h * 32);
+                        const uint32_t at = st.slot * (kCodes >> 4);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            mma_mxf4<kCtas>(tmem + c * kBN, da0 + at + k * 2, db0 + at + k * 2, k & 1 ? idesc2 : idesc0, sa + (k >> 1) * 4,
+                                            sb + (k >> 1) * 4 * Shape::kChunks, kt > 0 || k > 0);
+                        mma_commit<kCtas>(done + st.slot * 8);
+                        if (g == k4Group - 1 || kt == a.KT - 1) mma_commit<kCtas>(scale_empty + sl.slot * 8);
+                        if (kt == a.KT - 1) mma_commit<kCtas>(acc_full + c * 8);
+                    }
+                    __syncwarp();
+                    st.next();
+                    if (g == k4Group - 1 || kt == a.KT - 1) sl.next();
+                    set ^= 1;
+                }
+            }
+            // every product has finished before either block frees its tensor memory: the second block waits for this one below
+            if (elect_one()) mma_commit_here<kCtas>(smem_u32(&sh.drain));
+            __syncwarp();
+            mbar_wait_bounded(&sh.drain, 0, k4WaitNs);
+        } else {
+            // ---- the second block's scales are in place: told to the first block by a warp that has no loads under way,
+            // which a release would wait for
+            const uint32_t full0 = smem_of(scale_full, 0);
+            RingPos<k4TileRing> tr;
+            Turn<k4Slots> sl;
+            while (true) {
+                mbar_wait_warp<true>(tr.bar(tile_full), tr.phase(), k4WaitNs, abort);
+                const int rows = sh.tile[tr.slot()].rows;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(tr.bar(tile_empty));
+                ++tr.n;
+                if (rows == 0 || __any_sync(0xffffffffu, *abort)) break;
+#pragma unroll 1
+                for (int kt = 0; kt < a.KT; kt += k4Group) {
+                    mbar_wait_warp<true>(scale_full + sl.slot * 8, sl.phase, k4WaitNs, abort);
+                    if (lane == 0) mbar_arrive_cluster(full0 + sl.slot * 8);
+                    sl.next();
+                }
             }
         }
-        // every product has finished before tensor memory is freed
-        if (elect_one()) mma_commit<1>(smem_u32(&sh.drain));
-        __syncwarp();
-        mbar_wait_bounded(&sh.drain, 0, k4WaitNs);
     } else if (warp >= 4 && warp < 4 + k4ScaleWarps) {
-        // ---- scales: thread r those of row r, and of weight rows r and 128 + r, two stages' with one load, the next
-        // two on their way meanwhile
+        // ---- scales: thread r those of row r, and of weight rows r and 128 + r, of four stages at once: a load takes a whole
+        // sector, the next group's is on its way, and the fence that shows them to the tensor cores, which takes some 500
+        // cycles, comes once in four stages (one in each: a row of K 7168 11.8 us)
+        constexpr int kAhead = 2;
         const int r = tid - 128, bytes = a.K / 32;
         RingPos<k4TileRing> tr;
-        Turn<kStages> st;
+        Turn<k4Slots> sl;
         const uint32_t to = (uint32_t)((r & 31) * 16 + (r >> 5) * 4);
         while (true) {
             mbar_wait_warp<true>(tr.bar(tile_full), tr.phase(), k4WaitNs, abort);
@@ -259,46 +319,51 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
                 const int n = !kSwiglu ? tile.n * kBN + i : i < kHalf ? tile.n * kHalf + i : a.N / 2 + tile.n * kHalf + i - kHalf;
                 return n < a.N ? n : -1;
             };
-            const int n0 = weight_row(r), n1 = weight_row(128 + r);
-            const uint8_t* px = r < tile.rows ? a.x_scales + (int64_t)(tile.row0 + r) * a.x_sstride : nullptr;
+            const int n0 = weight_row(r), n1 = weight_row(128 + r), row = rank * k4BM + r;
+            const uint8_t* px = row < tile.rows ? a.x_scales + (int64_t)(tile.row0 + row) * a.x_sstride : nullptr;
             const uint8_t* p0 = n0 >= 0 ? a.w_scales + ((int64_t)tile.g * a.N + n0) * bytes : nullptr;
             const uint8_t* p1 = n1 >= 0 ? a.w_scales + ((int64_t)tile.g * a.N + n1) * bytes : nullptr;
-            const uint4 zero = make_uint4(0, 0, 0, 0);
-            uint4 nx, n0v, n1v;
-            auto fetch = [&](int at) {
-                nx = px ? load_scales(px, at, bytes, a.x_vec) : zero;
-                n0v = p0 ? load_scales(p0, at, bytes, a.w_vec) : zero;
-                n1v = Shape::kChunks > 1 && p1 ? load_scales(p1, at, bytes, a.w_vec) : zero;
-            };
-            fetch(0);
-#pragma unroll 1
-            for (int kt = 0; kt < a.KT; kt += 2) {
-                const uint4 vx = nx, v0 = n0v, v1 = n1v;
-                if (kt + 2 < a.KT) fetch(kt * 8 + 16);
+            Scales32 vx[kAhead], v0[kAhead], v1[kAhead];
+            auto fetch = [&](int i, int at) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    if (kt + h >= a.KT) break;
-                    mbar_wait_warp<true>(done + st.slot * 8, st.phase ^ 1, k4WaitNs, abort);
-                    uint8_t* d = scales + st.slot * kScales + to;
-                    *reinterpret_cast<uint32_t*>(d) = h ? vx.z : vx.x;
-                    *reinterpret_cast<uint32_t*>(d + 512) = h ? vx.w : vx.y;
-                    uint8_t* db = d + Shape::kScalesA;
-                    *reinterpret_cast<uint32_t*>(db) = h ? v0.z : v0.x;
-                    *reinterpret_cast<uint32_t*>(db + 512 * Shape::kChunks) = h ? v0.w : v0.y;
-                    if (Shape::kChunks > 1) {
-                        *reinterpret_cast<uint32_t*>(db + 512) = h ? v1.z : v1.x;
-                        *reinterpret_cast<uint32_t*>(db + 512 * 3) = h ? v1.w : v1.y;
+                for (int j = 0; j < 8; ++j) vx[i].v[j] = v0[i].v[j] = v1[i].v[j] = 0;
+                if (at >= bytes) return;
+                if (px) vx[i] = load_scales(px, at, bytes, a.x_vec);
+                if (p0) v0[i] = load_scales(p0, at, bytes, a.w_vec);
+                if (Shape::kChunks > 1 && p1) v1[i] = load_scales(p1, at, bytes, a.w_vec);
+            };
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) fetch(i, i * 32);
+#pragma unroll 1
+            for (int kt = 0; kt < a.KT; kt += k4Group * kAhead) {
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i) {
+                    if (kt + k4Group * i >= a.KT) break;
+                    mbar_wait_warp<true>(scale_empty + sl.slot * 8, sl.phase ^ 1, k4WaitNs, abort);
+                    uint8_t* d = scales + sl.slot * Shape::kSlot + to;
+#pragma unroll
+                    for (int h = 0; h < k4Group; ++h, d += kScales) {
+                        *reinterpret_cast<uint32_t*>(d) = vx[i].v[2 * h];
+                        *reinterpret_cast<uint32_t*>(d + 512) = vx[i].v[2 * h + 1];
+                        uint8_t* db = d + Shape::kScalesA;
+                        *reinterpret_cast<uint32_t*>(db) = v0[i].v[2 * h];
+                        *reinterpret_cast<uint32_t*>(db + 512 * Shape::kChunks) = v0[i].v[2 * h + 1];
+                        if (Shape::kChunks > 1) {
+                            *reinterpret_cast<uint32_t*>(db + 512) = v1[i].v[2 * h];
+                            *reinterpret_cast<uint32_t*>(db + 512 * 3) = v1[i].v[2 * h + 1];
+                        }
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(staged + st.slot * 8);
-                    st.next();
+                    if (lane == 0) mbar_arrive(scale_full + sl.slot * 8);
+                    sl.next();
+                    fetch(i, (kt / k4Group + kAhead + i) * 32);
                 }
             }
         }
     } else if (warp >= 4 + k4ScaleWarps) {
         // ---- results: a lane a row, 32 columns at a time
-        const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);
+        const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21), free_bar = kCtas == 2 ? smem_of(acc_empty, 0) : acc_empty;
         uint8_t* stage = out_stage + (warp & 3) * Shape::kOut;
         RingPos<k4TileRing> tr;
         while (true) {
@@ -311,7 +376,7 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
             if (tile.rows == 0 || __any_sync(0xffffffffu, *abort)) break;
             mbar_wait_warp<true>(acc_full + c * 8, turn, k4WaitNs, abort);
             tc_fence_after();
-            const int first = (warp & 3) * 32, rows = min(32, tile.rows - first);  // of this warp
+            const int first = rank * k4BM + (warp & 3) * 32, rows = min(32, tile.rows - first);  // of this warp
             if (rows > 0) {
                 const int64_t row0 = tile.row0 + first;
                 if constexpr (kSwiglu) {
@@ -377,15 +442,18 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_hand_back(acc_empty + c * 8);
+            if (lane == 0) mbar_hand_back(free_bar + c * 8);
         }
     }
     __syncwarp();
     tc_fence_before();
     __syncthreads();
+    if (kCtas == 2) cluster_sync();
     tc_fence_after();
-    if (warp == 2) tmem_free<1>(tmem, Shape::kCols);
+    if (warp == 2) tmem_free<kCtas>(tmem, Shape::kCols);
     if (tid == 0 && *abort && a.status) flag(a.status, FLAG_TIMEOUT);
+    __syncwarp();
+    if (kCtas == 2) cluster_sync();  // neither block ends while the other still frees
 }
 
 // ---- quantisation ---------------------------------------------------------------------
@@ -446,12 +514,12 @@ static ep_status check_fp4(const char* fn, const ep_fp4_rows* x, const ep_row_gr
     return EP_OK;
 }
 
-template <bool kSwiglu, int kBN>
+template <bool kSwiglu, int kBN, int kCtas>
 static ep_status launch_fp4_shape(const char* fn, const ep_fp4_rows* x, const ep_fp4_weight* w, Fp4Args a, int sms, int dev, void* stream) {
-    using Shape = Fp4Shape<kBN>;
+    using Shape = Fp4Shape<kBN, kCtas>;
     constexpr int kTileN = kSwiglu ? kBN / 2 : kBN;
     a.n_tiles = ((kSwiglu ? w->n / 2 : w->n) + kTileN - 1) / kTileN;
-    const int64_t most = most_tiles(a, k4BM);
+    const int64_t most = most_tiles(a, Shape::kTileM);
     if (most > kMaxTiles) return set_error(EP_ERR_INVALID_ARG, "%s: %lld tiles", fn, (long long)most);
     a.most = (int)most;
     CUtensorMap map_x, map_w;
@@ -464,24 +532,32 @@ static ep_status launch_fp4_shape(const char* fn, const ep_fp4_rows* x, const ep
     {
         const cuuint64_t dims[3] = {(cuuint64_t)w->k / 2, (cuuint64_t)w->n, (cuuint64_t)w->groups};
         const cuuint64_t strides[2] = {(cuuint64_t)w->k / 2, (cuuint64_t)w->k / 2 * (cuuint64_t)w->n};
-        const cuuint32_t box[3] = {128, (cuuint32_t)kTileN, 1};
+        const cuuint32_t box[3] = {128, kSwiglu || kCtas == 2 ? kBN / 2 : kBN, 1};
         EP_TRY(encode_rows(&map_w, w->codes, 3, dims, strides, box, fn));
     }
     static std::atomic<bool> known[kMaxDevicesTracked];  // devices whose launch attribute is set
     if (dev >= kMaxDevicesTracked || !known[dev].load(std::memory_order_relaxed)) {
-        EP_CUDA(cudaFuncSetAttribute(fp4_gemm_kernel<kSwiglu, kBN>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Shape::kSmem));
+        EP_CUDA(cudaFuncSetAttribute(fp4_gemm_kernel<kSwiglu, kBN, kCtas>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Shape::kSmem));
         if (dev < kMaxDevicesTracked) known[dev].store(true, std::memory_order_relaxed);
     }
-    return launch_next(fp4_gemm_kernel<kSwiglu, kBN>, most < sms ? most : sms, k4Threads, stream, Shared{Shape::kSmem}, map_x, map_w, a);
+    const int64_t units = most < sms / kCtas ? most : sms / kCtas;
+    return launch_next(fp4_gemm_kernel<kSwiglu, kBN, kCtas>, units * kCtas, k4Threads, stream, Shared{Shape::kSmem, kCtas}, map_x, map_w, a);
+}
+
+static bool fp4_by_pairs(int64_t rows) {
+    static const char* e = getenv("FP4_PAIRS");
+    if (e) return rows >= atoi(e);
+    return rows > k4BM;
 }
 
 template <bool kSwiglu>
 static ep_status launch_fp4(const char* fn, const ep_fp4_rows* x, const ep_row_groups* g, const ep_fp4_weight* w, Fp4Args a, void* stream) {
     a.x_scales = x->scales;
     a.x_sstride = x->scale_stride;
-    a.x_vec = aligned16(x->scales) && x->scale_stride % 16 == 0;
+    auto vec = [](const void* p, int64_t stride) { return aligned_to(p, 32) && stride % 32 == 0 ? 32 : aligned16(p) && stride % 16 == 0 ? 16 : 4; };
+    a.x_vec = vec(x->scales, x->scale_stride);
     a.w_scales = w->scales;
-    a.w_vec = aligned16(w->scales) && w->k % 512 == 0;
+    a.w_vec = vec(w->scales, w->k / 32);
     a.G = w->groups;
     a.N = w->n;
     a.K = w->k;
@@ -496,8 +572,13 @@ static ep_status launch_fp4(const char* fn, const ep_fp4_rows* x, const ep_row_g
     EP_CUDA(cudaGetDevice(&dev));
     EP_CUDA(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
     a.n_tiles = (w->n + 191) / 192;
-    if (most_tiles(a, k4BM) * 2 <= sms) return launch_fp4_shape<kSwiglu, 64>(fn, x, w, a, sms, dev, stream);
-    return launch_fp4_shape<kSwiglu, 192>(fn, x, w, a, sms, dev, stream);
+    if (most_tiles(a, k4BM) * 2 <= sms) return launch_fp4_shape<kSwiglu, 64, 1>(fn, x, w, a, sms, dev, stream);
+    // Rows of a group: as the caller expects, or what the arrays hold, shared out; regions with counts are sized for the
+    // worst case, and a low-latency step fills a few percent of them.
+    const int64_t per_group =
+        g->expected > 0 ? g->expected : x->rows / w->groups / (w->groups > 1 && !g->offsets && g->counts ? 16 : 1);
+    if (fp4_by_pairs(per_group)) return launch_fp4_shape<kSwiglu, 192, 2>(fn, x, w, a, sms, dev, stream);
+    return launch_fp4_shape<kSwiglu, 192, 1>(fn, x, w, a, sms, dev, stream);
 }
 
 }  // namespace ep

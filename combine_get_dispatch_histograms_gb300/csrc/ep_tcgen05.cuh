@@ -154,6 +154,11 @@ __device__ __forceinline__ void mbar_hand_back(uint32_t bar) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
+// The same for what the arriving threads wrote to shared memory, with a fence of the async proxy where that reads it.
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
 // ---- tiled bulk copies (the innermost coordinate is a multiple of 16 bytes) ------
 // Into this block's shared memory; `bar` (a cluster address) counts the bytes,
 // with kCtas = 2 also where it lies in the other block of the pair.

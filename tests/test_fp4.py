@@ -225,6 +225,30 @@ def test_dense(rows, K, N):
 
 
 @gpu
+@pytest.mark.parametrize("expected", [1, 1000])
+@pytest.mark.parametrize("K,N", [(128, 256), (640, 512), (1408, 768), (2048, 1280), (7168, 256)])
+def test_both_shapes_on_long_and_ragged_groups(K, N, expected):
+    """One block a tile or two, whatever the groups hold."""
+    for counts in (LONG, RAGGED):
+        cnt, off, hoff, rows = groups_of(counts, 2)
+        g = gen(K + N + expected)
+        x, xs = rows4(rows, K, g)
+        w, ws = weight4(len(counts), N, K, g)
+        out = torch.full((rows, N), 7.0, dtype=BF, device="cuda")
+        ep.expert_gemm_fp4(x, xs, w, ws, counts=cnt, offsets=off, out=out, expected_rows=expected)
+        hc, hs = (torch.full((rows, n), 7, dtype=torch.uint8, device="cuda") for n in (N // 4, N // 64))
+        ep.expert_swiglu_fp4(x, xs, w, ws, counts=cnt, offsets=off, out=(hc, hs), expected_rows=expected)
+        own = torch.zeros(rows, dtype=torch.bool, device="cuda")
+        for e, (o, c) in enumerate(zip(hoff, counts)):
+            own[o:o + c] = True
+            if c:
+                X, W = values4(x[o:o + c], xs[o:o + c]), values4(w[e], ws[e])
+                assert_bf16_close(out[o:o + c], *product64(X, W), f"group {e}")
+                assert_fp4_close(hc[o:o + c], hs[o:o + c], *swiglu64(X, W))
+        assert (out[~own] == 7.0).all() and (hc[~own] == 7).all() and (hs[~own] == 7).all()
+
+
+@gpu
 def test_regions_with_and_without_counts():
     E, cap, K, N = 5, 40, 384, 200
     g = gen(5)
