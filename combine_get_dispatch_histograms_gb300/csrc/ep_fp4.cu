@@ -12,7 +12,6 @@
 // products, four write the results.  With 192 weight rows a tile tensor memory holds two accumulators and
 // the scales beside them, so that a tile is written while the next is multiplied.
 #include <atomic>
-#include <cstdlib>
 
 #include "ep_fp4.cuh"
 #include "ep_groups.cuh"
@@ -25,23 +24,18 @@ constexpr int k4BoxRows = 32;     // rows of one copy of x
 constexpr int k4ScaleWarps = 4, k4OutWarps = 4;
 constexpr int k4Threads = 128 + 32 * (k4ScaleWarps + k4OutWarps);
 constexpr int k4TileRing = 4;
-constexpr int k4Group = 4;        // stages whose scales are staged together: 32 bytes of a row, a whole sector
-constexpr int k4Slots = 2;        // of such groups
+constexpr int k4Group = 2;        // stages whose scales are staged together
 constexpr int64_t k4WaitNs = 2000000000ll;
 
-// kCtas = 2: a pair of blocks makes a tile of 256 rows; each copies half of the weight's rows, so that an SM takes in 28 KB
-// of codes a stage instead of 40, and all of the weight rows' scales.
-template <int kBN, int kCtas>
+template <bool kSwiglu, int kBN>
 struct Fp4Shape {
-    static constexpr int kTileM = kCtas * k4BM;
     static constexpr int kChunks = (kBN + 127) / 128;               // of 128 weight rows' scales
-    static constexpr int kCodesA = k4BM * 128, kCodesB = kBN / kCtas * 128;
-    static constexpr int kScalesA = 2 * 512, kScalesB = 2 * kChunks * 512;  // [128 of K][chunk][32][16]
-    static constexpr int kCodes = kCodesA + kCodesB, kScales = kScalesA + kScalesB;
-    static constexpr int kOutRow = 34 * 2;                          // bytes of a staged row of 32 bf16: rows fall into other banks
-    static constexpr int kOut = 32 * kOutRow;
+    static constexpr int kCodesA = k4BM * 128, kCodesB = kBN * 128, kCodes = kCodesA + kCodesB;
+    static constexpr int kScalesA = 2 * 512, kScalesB = 2 * kChunks * 512, kScales = kScalesA + kScalesB;  // [128 of K][chunk][32][16]
     static constexpr int kSlot = k4Group * kScales;                 // the scales that are staged together
-    static constexpr int kRest = k4Slots * kSlot + k4OutWarps * kOut;
+    static constexpr int kSlots = kSwiglu ? 4 : 2;
+    static constexpr int kOut = kSwiglu ? 0 : 32 * 64;              // of a warp's output on its way: 32 rows of 32 columns
+    static constexpr int kRest = kSlots * kSlot + k4OutWarps * kOut;
     static constexpr int kStages = (225 * 1024 - kRest) / kCodes < 8 ? (225 * 1024 - kRest) / kCodes : 8;
     static constexpr size_t kSmem = 1024 + kStages * kCodes + kRest;
     // columns of tensor memory: two accumulators, then two sets of scales in turn
@@ -58,14 +52,15 @@ struct Fp4Args : TileArgs {
     int64_t out_stride; // elements; codes: bytes
     uint8_t* out_scales;
     int64_t out_sstride;
-    bool out_vec, out_wide;   // 16- and 32-byte stores
+    bool out_vec;             // 16-byte stores
+    bool out_clip;            // rows end at a multiple of 16 bytes, so that a copy that crosses their end is cut there
     int x_vec, w_vec;         // bytes of scales that a load may take: 32, 16 or 4
     uint32_t* status;
 };
 
-template <int kStages>
+template <int kStages, int kSlots>
 struct Fp4Shared {
-    uint64_t full[kStages], done[kStages], scale_full[k4Slots], scale_empty[k4Slots], acc_full[2], acc_empty[2];
+    uint64_t full[kStages], done[kStages], scale_full[kSlots], scale_empty[kSlots], acc_full[2], acc_empty[2];
     uint64_t tile_full[k4TileRing], tile_empty[k4TileRing], drain;
     uint32_t tmem;
     int abort;
@@ -111,19 +106,19 @@ __device__ __forceinline__ Scales32 load_scales(const uint8_t* row, int at, int 
 }
 
 // kSwiglu: half of the tile's weight rows are gate rows, half the up rows of the same channels.
-template <bool kSwiglu, int kBN, int kCtas>
+template <bool kSwiglu, int kBN>
 __global__ void __launch_bounds__(k4Threads, 1)
-fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w, const Fp4Args a) {
-    using Shape = Fp4Shape<kBN, kCtas>;
-    constexpr int kStages = Shape::kStages, kCodes = Shape::kCodes, kScales = Shape::kScales, kHalf = kBN / 2, kTileM = Shape::kTileM;
+fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_box,
+                const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_out, const Fp4Args a) {
+    using Shape = Fp4Shape<kSwiglu, kBN>;
+    constexpr int kStages = Shape::kStages, kSlots = Shape::kSlots, kCodes = Shape::kCodes, kScales = Shape::kScales, kHalf = kBN / 2;
     extern __shared__ __align__(1024) uint8_t dyn[];
-    __shared__ Fp4Shared<kStages> sh;
+    __shared__ Fp4Shared<kStages, kSlots> sh;
     // codes of all stages first, each on 1024 bytes; then the scales, then the rows on their way out
     uint8_t* codes = dyn + ((1024u - (smem_u32(dyn) & 1023u)) & 1023u);
     uint8_t* scales = codes + kStages * kCodes;
-    uint8_t* out_stage = scales + k4Slots * Shape::kSlot;
+    uint8_t* out_stage = scales + kSlots * Shape::kSlot;  // on 1024 bytes too
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int rank = kCtas == 2 ? (int)cluster_rank() : 0, unit = blockIdx.x / kCtas, units = gridDim.x / kCtas;
     volatile int* abort = &sh.abort;
     const uint32_t full = smem_u32(sh.full), done = smem_u32(sh.done);
     const uint32_t scale_full = smem_u32(sh.scale_full), scale_empty = smem_u32(sh.scale_empty);
@@ -135,13 +130,13 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
             mbar_init(&sh.full[s], 1);
             mbar_init(&sh.done[s], 1);
         }
-        for (int b = 0; b < k4Slots; ++b) {
-            mbar_init(&sh.scale_full[b], k4ScaleWarps + (kCtas == 2 && rank == 0));
+        for (int b = 0; b < kSlots; ++b) {
+            mbar_init(&sh.scale_full[b], k4ScaleWarps);
             mbar_init(&sh.scale_empty[b], 1);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&sh.acc_full[b], 1);
-            mbar_init(&sh.acc_empty[b], kCtas * k4OutWarps);
+            mbar_init(&sh.acc_empty[b], k4OutWarps);
         }
         for (int b = 0; b < k4TileRing; ++b) {
             mbar_init(&sh.tile_full[b], 1);
@@ -152,12 +147,12 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
         sh.abort = 0;
         fence_mbar_init();
         tma_prefetch_desc(&map_x);
+        tma_prefetch_desc(&map_box);
         tma_prefetch_desc(&map_w);
     }
-    if (warp == 2) tmem_alloc<kCtas>(&sh.tmem, Shape::kCols);
+    if (warp == 2) tmem_alloc<1>(&sh.tmem, Shape::kCols);
     tc_fence_before();
     __syncthreads();
-    if (kCtas == 2) cluster_sync();  // both blocks' barriers are ready
     tc_fence_after();
     // All above may run beside the end of the kernel before; the kernel after may do the same.
     grid_wait();
@@ -166,9 +161,9 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
 
     if (warp == 3) {
         // ---- tiles
-        TileWalk<kTileM> walk;
+        TileWalk<k4BM> walk;
         RingPos<k4TileRing> tr;
-        for (int t = unit;; t += units) {
+        for (int t = blockIdx.x;; t += gridDim.x) {
             GemmTile tile = {0, 0, 0, 0};
             const bool some = walk.find(a, min(t, a.most), lane, &tile);
             if (t >= a.most) tile.rows = 0;  // groups that overlap may have any number of tiles
@@ -187,7 +182,8 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
         if (walk.cut && a.status && blockIdx.x == 0) flag(a.status, FLAG_CAPACITY);
     } else if (warp == 0) {
         if (lane == 0) {
-            // ---- copies of codes: each block fills its own half of a stage; block 0's barrier counts the bytes of both
+            // ---- copies of codes; a whole tile's rows come as one copy (as four of 32: 1024 rows a group, first product 513 us
+            // for 464)
             RingPos<k4TileRing> tr;
             Turn<kStages> st;
             bool ok = true;
@@ -197,115 +193,90 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
                 mbar_arrive(tr.bar(tile_empty));
                 ++tr.n;
                 if (tile.rows == 0) break;
-                const int boxes0 = (min(tile.rows, k4BM) + k4BoxRows - 1) / k4BoxRows;
-                const int boxes1 = (max(tile.rows - k4BM, 0) + k4BoxRows - 1) / k4BoxRows;
-                const uint32_t bytes = (boxes0 + boxes1) * k4BoxRows * 128 + kBN * 128;
-                const int boxes = rank ? boxes1 : boxes0, row = tile.row0 + rank * k4BM;
-                const int w0 = kSwiglu ? tile.n * kHalf : tile.n * kBN, w1 = kSwiglu ? a.N / 2 + w0 : w0 + kHalf;
-                const uint32_t full0 = kCtas == 2 ? smem_of(full, 0) : full;
+                const int boxes = (tile.rows + k4BoxRows - 1) / k4BoxRows;
+                const uint32_t bytes = boxes * k4BoxRows * 128 + kBN * 128;
+                const int w0 = kSwiglu ? tile.n * kHalf : tile.n * kBN;
                 for (int kt = 0; kt < a.KT; ++kt) {
                     if (!mbar_wait_or_abort<true>(done + st.slot * 8, st.phase ^ 1, k4WaitNs, abort)) {
                         ok = false;
                         break;
                     }
                     uint8_t* sa = codes + st.slot * kCodes;
-                    const uint32_t bar = full0 + st.slot * 8;
-                    if (rank == 0) mbar_arrive_expect_tx(&sh.full[st.slot], bytes);
-                    tma_load_3d<kCtas>(sa + Shape::kCodesA, &map_w, kt * 128, rank ? w1 : w0, tile.g, bar);
-                    if (kCtas == 1 && kSwiglu) tma_load_3d<kCtas>(sa + Shape::kCodesA + kHalf * 128, &map_w, kt * 128, w1, tile.g, bar);
-                    for (int b = 0; b < boxes; ++b)
-                        tma_load_2d<kCtas>(sa + b * k4BoxRows * 128, &map_x, kt * 128, row + b * k4BoxRows, bar);
+                    const uint32_t bar = full + st.slot * 8;
+                    mbar_arrive_expect_tx(&sh.full[st.slot], bytes);
+                    tma_load_3d<1>(sa + Shape::kCodesA, &map_w, kt * 128, w0, tile.g, bar);
+                    if (kSwiglu) tma_load_3d<1>(sa + Shape::kCodesA + kHalf * 128, &map_w, kt * 128, a.N / 2 + w0, tile.g, bar);
+                    if (boxes == k4BM / k4BoxRows) tma_load_2d<1>(sa, &map_x, kt * 128, tile.row0, bar);
+                    else
+                        for (int b = 0; b < boxes; ++b)
+                            tma_load_2d<1>(sa + b * k4BoxRows * 128, &map_box, kt * 128, tile.row0 + b * k4BoxRows, bar);
                     st.next();
                 }
             }
             // no copy may be in flight when the blocks end, also after a wait that ran out: the last phase that
             // a stage's copies complete is the one before its next
-            if (rank == 0)
-                for (int u = 0; u < kStages; ++u) {
-                    mbar_wait_bounded(&sh.full[st.slot], st.phase ^ 1, k4WaitNs);
-                    st.next();
-                }
+            for (int u = 0; u < kStages; ++u) {
+                mbar_wait_bounded(&sh.full[st.slot], st.phase ^ 1, k4WaitNs);
+                st.next();
+            }
         }
     } else if (warp == 1) {
-        if (rank == 0) {
-            // ---- copies of scales into tensor memory, products: for both blocks of a pair by the first
-            constexpr uint32_t idesc0 = idesc_mxf4(kTileM, kBN, 0), idesc2 = idesc_mxf4(kTileM, kBN, 2);
-            const uint64_t da0 = smem_desc_sw128(codes), db0 = smem_desc_sw128(codes + Shape::kCodesA), ds0 = smem_desc_rows16(scales);
-            RingPos<k4TileRing> tr;
-            Turn<kStages> st;
-            Turn<k4Slots> sl;
-            uint32_t set = 0;
-            while (true) {
-                mbar_wait_warp<true>(tr.bar(tile_full), tr.phase(), k4WaitNs, abort);
-                const int rows = sh.tile[tr.slot()].rows;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(tr.bar(tile_empty));
-                const uint32_t c = tr.n & 1, turn = tr.n >> 1 & 1;
-                ++tr.n;
-                if (rows == 0 || __any_sync(0xffffffffu, *abort)) break;
-                mbar_wait_warp<true>(acc_empty + c * 8, turn ^ 1, k4WaitNs, abort);
-#pragma unroll 1
-                for (int kt = 0; kt < a.KT; ++kt) {
-                    const int g = kt & (k4Group - 1);
-                    if (g == 0) mbar_wait_warp<true>(scale_full + sl.slot * 8, sl.phase, k4WaitNs, abort);
-                    mbar_wait_warp<true>(full + st.slot * 8, st.phase, k4WaitNs, abort);
-                    tc_fence_after();
-                    if (elect_one()) {
-                        const uint32_t sa = tmem + Shape::kScaleAt + set * Shape::kScaleCols, sb = sa + 8;
-                        const uint64_t ds = ds0 + sl.slot * (Shape::kSlot >> 4) + g * (kScales >> 4);
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) tmem_copy_scales<kCtas>(sa + h * 4, ds + h * 32);
-#pragma unroll
-                        for (int h = 0; h < 2 * Shape::kChunks; ++h)
-                            tmem_copy_scales<kCtas>(sb + h * 4, ds + (Shape::kScalesA >> 4) + h * 32);
-                        const uint32_t at = st.slot * (kCodes >> 4);
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            mma_mxf4<kCtas>(tmem + c * kBN, da0 + at + k * 2, db0 + at + k * 2, k & 1 ? idesc2 : idesc0, sa + (k >> 1) * 4,
-                                            sb + (k >> 1) * 4 * Shape::kChunks, kt > 0 || k > 0);
-                        mma_commit<kCtas>(done + st.slot * 8);
-                        if (g == k4Group - 1 || kt == a.KT - 1) mma_commit<kCtas>(scale_empty + sl.slot * 8);
-                        if (kt == a.KT - 1) mma_commit<kCtas>(acc_full + c * 8);
-                    }
-                    __syncwarp();
-                    st.next();
-                    if (g == k4Group - 1 || kt == a.KT - 1) sl.next();
-                    set ^= 1;
-                }
-            }
-            // every product has finished before either block frees its tensor memory: the second block waits for this one below
-            if (elect_one()) mma_commit_here<kCtas>(smem_u32(&sh.drain));
+        // ---- copies of scales into tensor memory, products
+        constexpr uint32_t idesc0 = idesc_mxf4(k4BM, kBN, 0), idesc2 = idesc_mxf4(k4BM, kBN, 2);
+        const uint64_t da0 = smem_desc_sw128(codes), db0 = smem_desc_sw128(codes + Shape::kCodesA), ds0 = smem_desc_rows16(scales);
+        RingPos<k4TileRing> tr;
+        Turn<kStages> st;
+        Turn<kSlots> sl;
+        uint32_t set = 0;
+        while (true) {
+            mbar_wait_warp<true>(tr.bar(tile_full), tr.phase(), k4WaitNs, abort);
+            const int rows = sh.tile[tr.slot()].rows;
             __syncwarp();
-            mbar_wait_bounded(&sh.drain, 0, k4WaitNs);
-        } else {
-            // ---- the second block's scales are in place: told to the first block by a warp that has no loads under way,
-            // which a release would wait for
-            const uint32_t full0 = smem_of(scale_full, 0);
-            RingPos<k4TileRing> tr;
-            Turn<k4Slots> sl;
-            while (true) {
-                mbar_wait_warp<true>(tr.bar(tile_full), tr.phase(), k4WaitNs, abort);
-                const int rows = sh.tile[tr.slot()].rows;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(tr.bar(tile_empty));
-                ++tr.n;
-                if (rows == 0 || __any_sync(0xffffffffu, *abort)) break;
+            if (lane == 0) mbar_arrive(tr.bar(tile_empty));
+            const uint32_t c = tr.n & 1, turn = tr.n >> 1 & 1;
+            ++tr.n;
+            if (rows == 0 || __any_sync(0xffffffffu, *abort)) break;
+            mbar_wait_warp<true>(acc_empty + c * 8, turn ^ 1, k4WaitNs, abort);
 #pragma unroll 1
-                for (int kt = 0; kt < a.KT; kt += k4Group) {
-                    mbar_wait_warp<true>(scale_full + sl.slot * 8, sl.phase, k4WaitNs, abort);
-                    if (lane == 0) mbar_arrive_cluster(full0 + sl.slot * 8);
-                    sl.next();
+            for (int kt = 0; kt < a.KT; ++kt) {
+                const int g = kt & (k4Group - 1);
+                if (g == 0) mbar_wait_warp<true>(scale_full + sl.slot * 8, sl.phase, k4WaitNs, abort);
+                mbar_wait_warp<true>(full + st.slot * 8, st.phase, k4WaitNs, abort);
+                tc_fence_after();
+                if (elect_one()) {
+                    const uint32_t sa = tmem + Shape::kScaleAt + set * Shape::kScaleCols, sb = sa + 8;
+                    const uint64_t ds = ds0 + sl.slot * (Shape::kSlot >> 4) + g * (kScales >> 4);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) tmem_copy_scales<1>(sa + h * 4, ds + h * 32);
+#pragma unroll
+                    for (int h = 0; h < 2 * Shape::kChunks; ++h)
+                        tmem_copy_scales<1>(sb + h * 4, ds + (Shape::kScalesA >> 4) + h * 32);
+                    const uint32_t at = st.slot * (kCodes >> 4);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        mma_mxf4<1>(tmem + c * kBN, da0 + at + k * 2, db0 + at + k * 2, k & 1 ? idesc2 : idesc0, sa + (k >> 1) * 4,
+                                        sb + (k >> 1) * 4 * Shape::kChunks, kt > 0 || k > 0);
+                    mma_commit<1>(done + st.slot * 8);
+                    if (g == k4Group - 1 || kt == a.KT - 1) mma_commit<1>(scale_empty + sl.slot * 8);
+                    if (kt == a.KT - 1) mma_commit<1>(acc_full + c * 8);
                 }
+                __syncwarp();
+                st.next();
+                if (g == k4Group - 1 || kt == a.KT - 1) sl.next();
+                set ^= 1;
             }
         }
+        // every product has finished before tensor memory is freed
+        if (elect_one()) mma_commit<1>(smem_u32(&sh.drain));
+        __syncwarp();
+        mbar_wait_bounded(&sh.drain, 0, k4WaitNs);
     } else if (warp >= 4 && warp < 4 + k4ScaleWarps) {
-        // ---- scales: thread r those of row r, and of weight rows r and 128 + r, of four stages at once: a load takes a whole
-        // sector, the next group's is on its way, and the fence that shows them to the tensor cores, which takes some 500
-        // cycles, comes once in four stages (one in each: a row of K 7168 11.8 us)
+        // ---- scales: thread r those of row r, and of weight rows r and 128 + r.  A load takes four stages' (a whole sector)
+        // and the next is on its way; two stages' are shown to the tensor cores with one fence
         constexpr int kAhead = 2;
         const int r = tid - 128, bytes = a.K / 32;
         RingPos<k4TileRing> tr;
-        Turn<k4Slots> sl;
+        Turn<kSlots> sl;
         const uint32_t to = (uint32_t)((r & 31) * 16 + (r >> 5) * 4);
         while (true) {
             mbar_wait_warp<true>(tr.bar(tile_full), tr.phase(), k4WaitNs, abort);
@@ -319,8 +290,8 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
                 const int n = !kSwiglu ? tile.n * kBN + i : i < kHalf ? tile.n * kHalf + i : a.N / 2 + tile.n * kHalf + i - kHalf;
                 return n < a.N ? n : -1;
             };
-            const int n0 = weight_row(r), n1 = weight_row(128 + r), row = rank * k4BM + r;
-            const uint8_t* px = row < tile.rows ? a.x_scales + (int64_t)(tile.row0 + row) * a.x_sstride : nullptr;
+            const int n0 = weight_row(r), n1 = weight_row(128 + r);
+            const uint8_t* px = r < tile.rows ? a.x_scales + (int64_t)(tile.row0 + r) * a.x_sstride : nullptr;
             const uint8_t* p0 = n0 >= 0 ? a.w_scales + ((int64_t)tile.g * a.N + n0) * bytes : nullptr;
             const uint8_t* p1 = n1 >= 0 ? a.w_scales + ((int64_t)tile.g * a.N + n1) * bytes : nullptr;
             Scales32 vx[kAhead], v0[kAhead], v1[kAhead];
@@ -335,35 +306,38 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
 #pragma unroll
             for (int i = 0; i < kAhead; ++i) fetch(i, i * 32);
 #pragma unroll 1
-            for (int kt = 0; kt < a.KT; kt += k4Group * kAhead) {
+            for (int kt = 0; kt < a.KT; kt += 4 * kAhead) {
 #pragma unroll
                 for (int i = 0; i < kAhead; ++i) {
-                    if (kt + k4Group * i >= a.KT) break;
-                    mbar_wait_warp<true>(scale_empty + sl.slot * 8, sl.phase ^ 1, k4WaitNs, abort);
-                    uint8_t* d = scales + sl.slot * Shape::kSlot + to;
 #pragma unroll
-                    for (int h = 0; h < k4Group; ++h, d += kScales) {
-                        *reinterpret_cast<uint32_t*>(d) = vx[i].v[2 * h];
-                        *reinterpret_cast<uint32_t*>(d + 512) = vx[i].v[2 * h + 1];
-                        uint8_t* db = d + Shape::kScalesA;
-                        *reinterpret_cast<uint32_t*>(db) = v0[i].v[2 * h];
-                        *reinterpret_cast<uint32_t*>(db + 512 * Shape::kChunks) = v0[i].v[2 * h + 1];
-                        if (Shape::kChunks > 1) {
-                            *reinterpret_cast<uint32_t*>(db + 512) = v1[i].v[2 * h];
-                            *reinterpret_cast<uint32_t*>(db + 512 * 3) = v1[i].v[2 * h + 1];
+                    for (int j = 0; j < 4; j += k4Group) {
+                        if (kt + 4 * i + j >= a.KT) break;
+                        mbar_wait_warp<true>(scale_empty + sl.slot * 8, sl.phase ^ 1, k4WaitNs, abort);
+                        uint8_t* d = scales + sl.slot * Shape::kSlot + to;
+#pragma unroll
+                        for (int h = j; h < j + k4Group; ++h, d += kScales) {
+                            *reinterpret_cast<uint32_t*>(d) = vx[i].v[2 * h];
+                            *reinterpret_cast<uint32_t*>(d + 512) = vx[i].v[2 * h + 1];
+                            uint8_t* db = d + Shape::kScalesA;
+                            *reinterpret_cast<uint32_t*>(db) = v0[i].v[2 * h];
+                            *reinterpret_cast<uint32_t*>(db + 512 * Shape::kChunks) = v0[i].v[2 * h + 1];
+                            if (Shape::kChunks > 1) {
+                                *reinterpret_cast<uint32_t*>(db + 512) = v1[i].v[2 * h];
+                                *reinterpret_cast<uint32_t*>(db + 512 * 3) = v1[i].v[2 * h + 1];
+                            }
                         }
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(scale_full + sl.slot * 8);
+                        sl.next();
                     }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(scale_full + sl.slot * 8);
-                    sl.next();
-                    fetch(i, (kt / k4Group + kAhead + i) * 32);
+                    fetch(i, (kt / 4 + kAhead + i) * 32);
                 }
             }
         }
     } else if (warp >= 4 + k4ScaleWarps) {
-        // ---- results: a lane a row, 32 columns at a time
-        const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21), free_bar = kCtas == 2 ? smem_of(acc_empty, 0) : acc_empty;
+        // ---- results: a lane a row
+        const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);
         uint8_t* stage = out_stage + (warp & 3) * Shape::kOut;
         RingPos<k4TileRing> tr;
         while (true) {
@@ -376,7 +350,7 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
             if (tile.rows == 0 || __any_sync(0xffffffffu, *abort)) break;
             mbar_wait_warp<true>(acc_full + c * 8, turn, k4WaitNs, abort);
             tc_fence_after();
-            const int first = rank * k4BM + (warp & 3) * 32, rows = min(32, tile.rows - first);  // of this warp
+            const int first = (warp & 3) * 32, rows = min(32, tile.rows - first);  // of this warp
             if (rows > 0) {
                 const int64_t row0 = tile.row0 + first;
                 if constexpr (kSwiglu) {
@@ -403,57 +377,71 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
                         }
                     }
                 } else {
+                    // 32 columns at a time through shared memory in the 64-byte swizzle.  A full set of rows goes out as one
+                    // copy, which the next columns hide; the rows of a group's last tile, and unaligned rows, by the lanes,
+                    // neighbours by neighbours.  So are the last columns where N is no multiple of 8: a copy writes whole 16
+                    // bytes, also past the row's end.
                     __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.out) + row0 * a.out_stride;
                     for (int q = 0; q < kBN / 32; ++q) {
                         const int n0 = tile.n * kBN + q * 32;
                         if (n0 >= a.N) break;
                         float v[32];
                         tmem_ld(lanes + c * kBN + q * 32, v);
+                        bulk_wait_read<0>();  // lane 0's copy of the columns before has read the buffer
                         tmem_wait_ld(v);
-                        uint32_t p[16];
+                        __syncwarp();
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-                            p[i] = *reinterpret_cast<const uint32_t*>(&b);
+                        for (int i = 0; i < 4; ++i) {
+                            __nv_bfloat162 p[4];
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) p[j] = __floats2bfloat162_rn(v[i * 8 + 2 * j], v[i * 8 + 2 * j + 1]);
+                            *reinterpret_cast<int4*>(stage + lane * 64 + ((i ^ (lane >> 1 & 3)) << 4)) = *reinterpret_cast<const int4*>(p);
                         }
-                        if (a.out_vec && n0 + 32 <= a.N) {
-                            if (lane < rows) {
-                                __nv_bfloat16* d = o + lane * a.out_stride + n0;
-                                if (a.out_wide) {
-                                    st_global_32(d, p);
-                                    st_global_32(d + 16, p + 8);
+                        if (a.out_vec && rows == 32 && (a.out_clip || n0 + 32 <= a.N)) {
+                            fence_proxy_async_smem();
+                            __syncwarp();
+                            if (lane == 0) {
+                                tma_store_2d(&map_out, stage, n0 * 2, (int)row0);
+                                bulk_commit();
+                            }
+                            continue;
+                        }
+                        __syncwarp();
+                        auto at = [&](int i, int k) { return stage + i * 64 + (((k >> 3) ^ (i >> 1 & 3)) << 4) + (k & 7) * 2; };
+                        if (a.out_vec) {
+                            const int k = (lane & 3) * 8;
+                            for (int i = lane >> 2; i < rows; i += 8) {
+                                const int4 w = *reinterpret_cast<const int4*>(at(i, k));
+                                __nv_bfloat16* d = o + i * a.out_stride + n0 + k;
+                                if (n0 + k + 8 <= a.N) {
+                                    *reinterpret_cast<int4*>(d) = w;
                                 } else {
-#pragma unroll
-                                    for (int i = 0; i < 4; ++i) reinterpret_cast<int4*>(d)[i] = *reinterpret_cast<const int4*>(p + 4 * i);
+                                    const __nv_bfloat16* e = reinterpret_cast<const __nv_bfloat16*>(&w);
+                                    for (int j = 0; j < 8; ++j)
+                                        if (n0 + k + j < a.N) d[j] = e[j];
                                 }
                             }
-                        } else {  // through shared memory, so that lanes store neighbours
-                            uint32_t* mine = reinterpret_cast<uint32_t*>(stage + lane * Shape::kOutRow);
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) mine[i] = p[i];
-                            __syncwarp();
+                        } else {
                             if (n0 + lane < a.N)
                                 for (int i = 0; i < rows; ++i)
-                                    o[i * a.out_stride + n0 + lane] = *reinterpret_cast<const __nv_bfloat16*>(stage + i * Shape::kOutRow + lane * 2);
-                            __syncwarp();
+                                    o[i * a.out_stride + n0 + lane] = *reinterpret_cast<const __nv_bfloat16*>(at(i, lane));
                         }
+                        __syncwarp();
                     }
                 }
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_hand_back(free_bar + c * 8);
+            if (lane == 0) mbar_hand_back(acc_empty + c * 8);
         }
+        bulk_wait_all();
     }
     __syncwarp();
     tc_fence_before();
     __syncthreads();
-    if (kCtas == 2) cluster_sync();
     tc_fence_after();
-    if (warp == 2) tmem_free<kCtas>(tmem, Shape::kCols);
+    if (warp == 2) tmem_free<1>(tmem, Shape::kCols);
     if (tid == 0 && *abort && a.status) flag(a.status, FLAG_TIMEOUT);
-    __syncwarp();
-    if (kCtas == 2) cluster_sync();  // neither block ends while the other still frees
 }
 
 // ---- quantisation ---------------------------------------------------------------------
@@ -514,40 +502,41 @@ static ep_status check_fp4(const char* fn, const ep_fp4_rows* x, const ep_row_gr
     return EP_OK;
 }
 
-template <bool kSwiglu, int kBN, int kCtas>
+template <bool kSwiglu, int kBN>
 static ep_status launch_fp4_shape(const char* fn, const ep_fp4_rows* x, const ep_fp4_weight* w, Fp4Args a, int sms, int dev, void* stream) {
-    using Shape = Fp4Shape<kBN, kCtas>;
+    using Shape = Fp4Shape<kSwiglu, kBN>;
     constexpr int kTileN = kSwiglu ? kBN / 2 : kBN;
     a.n_tiles = ((kSwiglu ? w->n / 2 : w->n) + kTileN - 1) / kTileN;
-    const int64_t most = most_tiles(a, Shape::kTileM);
+    const int64_t most = most_tiles(a, k4BM);
     if (most > kMaxTiles) return set_error(EP_ERR_INVALID_ARG, "%s: %lld tiles", fn, (long long)most);
     a.most = (int)most;
-    CUtensorMap map_x, map_w;
+    CUtensorMap map_x, map_box, map_w, map_out;
     {
         const cuuint64_t dims[2] = {(cuuint64_t)w->k / 2, (cuuint64_t)x->rows};
         const cuuint64_t strides[1] = {(cuuint64_t)x->code_stride};
-        const cuuint32_t box[2] = {128, k4BoxRows};
+        const cuuint32_t box[2] = {128, k4BM}, part[2] = {128, k4BoxRows};
         EP_TRY(encode_rows(&map_x, x->codes, 2, dims, strides, box, fn));
+        EP_TRY(encode_rows(&map_box, x->codes, 2, dims, strides, part, fn));
     }
     {
         const cuuint64_t dims[3] = {(cuuint64_t)w->k / 2, (cuuint64_t)w->n, (cuuint64_t)w->groups};
         const cuuint64_t strides[2] = {(cuuint64_t)w->k / 2, (cuuint64_t)w->k / 2 * (cuuint64_t)w->n};
-        const cuuint32_t box[3] = {128, kSwiglu || kCtas == 2 ? kBN / 2 : kBN, 1};
+        const cuuint32_t box[3] = {128, (cuuint32_t)kTileN, 1};
         EP_TRY(encode_rows(&map_w, w->codes, 3, dims, strides, box, fn));
+    }
+    map_out = map_x;  // used for aligned bf16 rows only
+    if (!kSwiglu && a.out_vec) {
+        const cuuint64_t dims[2] = {(cuuint64_t)w->n * 2, (cuuint64_t)x->rows};
+        const cuuint64_t strides[1] = {(cuuint64_t)a.out_stride * 2};
+        const cuuint32_t box[2] = {64, 32};
+        EP_TRY(encode_rows(&map_out, a.out, 2, dims, strides, box, fn, CU_TENSOR_MAP_SWIZZLE_64B));
     }
     static std::atomic<bool> known[kMaxDevicesTracked];  // devices whose launch attribute is set
     if (dev >= kMaxDevicesTracked || !known[dev].load(std::memory_order_relaxed)) {
-        EP_CUDA(cudaFuncSetAttribute(fp4_gemm_kernel<kSwiglu, kBN, kCtas>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Shape::kSmem));
+        EP_CUDA(cudaFuncSetAttribute(fp4_gemm_kernel<kSwiglu, kBN>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Shape::kSmem));
         if (dev < kMaxDevicesTracked) known[dev].store(true, std::memory_order_relaxed);
     }
-    const int64_t units = most < sms / kCtas ? most : sms / kCtas;
-    return launch_next(fp4_gemm_kernel<kSwiglu, kBN, kCtas>, units * kCtas, k4Threads, stream, Shared{Shape::kSmem, kCtas}, map_x, map_w, a);
-}
-
-static bool fp4_by_pairs(int64_t rows) {
-    static const char* e = getenv("FP4_PAIRS");
-    if (e) return rows >= atoi(e);
-    return rows > k4BM;
+    return launch_next(fp4_gemm_kernel<kSwiglu, kBN>, most < sms ? most : sms, k4Threads, stream, Shared{Shape::kSmem}, map_x, map_box, map_w, map_out, a);
 }
 
 template <bool kSwiglu>
@@ -572,13 +561,8 @@ static ep_status launch_fp4(const char* fn, const ep_fp4_rows* x, const ep_row_g
     EP_CUDA(cudaGetDevice(&dev));
     EP_CUDA(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
     a.n_tiles = (w->n + 191) / 192;
-    if (most_tiles(a, k4BM) * 2 <= sms) return launch_fp4_shape<kSwiglu, 64, 1>(fn, x, w, a, sms, dev, stream);
-    // Rows of a group: as the caller expects, or what the arrays hold, shared out; regions with counts are sized for the
-    // worst case, and a low-latency step fills a few percent of them.
-    const int64_t per_group =
-        g->expected > 0 ? g->expected : x->rows / w->groups / (w->groups > 1 && !g->offsets && g->counts ? 16 : 1);
-    if (fp4_by_pairs(per_group)) return launch_fp4_shape<kSwiglu, 192, 2>(fn, x, w, a, sms, dev, stream);
-    return launch_fp4_shape<kSwiglu, 192, 1>(fn, x, w, a, sms, dev, stream);
+    if (most_tiles(a, k4BM) * 2 <= sms) return launch_fp4_shape<kSwiglu, 64>(fn, x, w, a, sms, dev, stream);
+    return launch_fp4_shape<kSwiglu, 192>(fn, x, w, a, sms, dev, stream);
 }
 
 }  // namespace ep
@@ -627,7 +611,7 @@ extern "C" ep_status ep_expert_gemm_fp4(const ep_fp4_rows* x, const ep_row_group
     a.out = out;
     a.out_stride = out_stride;
     a.out_vec = aligned16(out) && out_stride % 8 == 0;
-    a.out_wide = aligned_to(out, 32) && out_stride % 16 == 0;
+    a.out_clip = w->n % 8 == 0;
     a.status = status_out;
     return launch_fp4<false>(fn, x, groups, w, a, stream);
 }
