@@ -24,6 +24,11 @@ constexpr int kRouterThreads = 256, kRouterWarps = kRouterThreads / 32;
 constexpr int kRouterMaxExperts = 1024, kRouterMaxGroups = 32;
 constexpr uint32_t kKeyNegInf = 0x007fffffu;  // the ordered key of -inf
 constexpr uint32_t kAll = 0xffffffffu;
+// Blocks that a processor holds at least, which the grids are made for: one more wave costs as much as the first.
+template <int V>
+constexpr int kPerSm = V <= 8 ? 5 : V == 16 ? 3 : 2;
+constexpr int blocks_per_sm(int experts) { return experts <= 256 ? kPerSm<8> : experts <= 512 ? kPerSm<16> : kPerSm<32>; }
+constexpr int balance_per_sm(int experts) { return experts <= 256 ? 4 : blocks_per_sm(experts); }
 
 struct RouterArgs {
     const void* logits;
@@ -295,13 +300,13 @@ __device__ __forceinline__ int choose(uint32_t (&key)[V], int K, int lane, Route
 }
 
 template <typename T, int V, bool kSigmoid, bool kGroups>
-__global__ void __launch_bounds__(kRouterThreads, V <= 8 ? 5 : 1) route_kernel(const RouterArgs a) {
+__global__ void __launch_bounds__(kRouterThreads, kPerSm<V>) route_kernel(const RouterArgs a) {
     __shared__ __align__(16) RouteList lists[kRouterWarps];
     const int lane = threadIdx.x & 31;
     grid_wait();
     grid_launch_next();
     const int size = kGroups ? a.E / a.groups : 0;
-    const bool whole = kGroups && size % V == 0 && (size / V & (size / V - 1)) == 0;
+    const bool whole = size && size % V == 0 && (size / V & (size / V - 1)) == 0;
     float bias[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) bias[i] = a.bias && lane * V + i < a.E ? a.bias[lane * V + i] : 0.0f;
@@ -328,7 +333,7 @@ __global__ void __launch_bounds__(kRouterThreads, V <= 8 ? 5 : 1) route_kernel(c
                 const uint32_t kept = choose_groups(key, a, lane);
 #pragma unroll
                 for (int i = 0; i < V; ++i)
-                    if (!(kept >> min((lane * V + i) / size, 31) & 1)) key[i] = 0;
+                    if (!(kept >> min((lane * V + i) / max(size, 1), 31) & 1)) key[i] = 0;
             }
         }
         const int expert = choose(key, a.K, lane, lists[threadIdx.x >> 5]);
@@ -375,7 +380,7 @@ struct BalanceArgs {
 };
 
 template <typename T, int V, bool kSigmoid>
-__global__ void __launch_bounds__(kRouterThreads, V <= 8 ? 6 : 1) balance_kernel(const BalanceArgs a) {
+__global__ void __launch_bounds__(kRouterThreads, V <= 8 ? 4 : kPerSm<V>) balance_kernel(const BalanceArgs a) {
     __shared__ float sums[kRouterMaxExperts];
     __shared__ int hist[kRouterMaxExperts];
     __shared__ int used_tokens;
@@ -392,22 +397,32 @@ __global__ void __launch_bounds__(kRouterThreads, V <= 8 ? 6 : 1) balance_kernel
     for (int i = 0; i < V; ++i) acc[i] = 0.0f;
     int tokens = 0;
     bool bad = false;
-    for (int64_t t = (int64_t)b * kRouterWarps + warp; t < a.T; t += (int64_t)a.blocks * kRouterWarps) {
-        const int64_t row = s * a.T + t;
-        float l[V], p[V], slope[V], top, by;
-        load_logits(static_cast<const T*>(a.logits) + row * a.stride, a.E, lane, a.vec, l);
-        bool chose = false;
-        if (lane < a.K) {
-            const int64_t e = a.idx[row * a.K + lane];
-            chose = e >= 0 && e < a.E;
-            bad |= e < -1 || e >= a.E;
-            if (chose) atomicAdd(&hist[(int)e], 1);
-        }
-        if (!__any_sync(kAll, chose)) continue;
-        ++tokens;
-        scores<V, kSigmoid>(l, p, slope, &top, &by);
+    // two tokens at a time, where registers allow it: their loads and sums wait together
+    constexpr int kU = V <= 8 ? 2 : 1;
+    const int64_t step = (int64_t)a.blocks * kRouterWarps;
+    for (int64_t t0 = (int64_t)b * kRouterWarps + warp; t0 < a.T; t0 += kU * step) {
+        float l[kU][V], p[V], slope[V], top, by;
+        int64_t e[kU];
 #pragma unroll
-        for (int i = 0; i < V; ++i) acc[i] += kSigmoid ? p[i] * by : p[i];
+        for (int u = 0; u < kU; ++u) {
+            const int64_t t = t0 + u * step, row = s * a.T + t;
+            e[u] = -1;
+            if (t < a.T) {
+                load_logits(static_cast<const T*>(a.logits) + row * a.stride, a.E, lane, a.vec, l[u]);
+                if (lane < a.K) e[u] = a.idx[row * a.K + lane];
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+            const bool chose = e[u] >= 0 && e[u] < a.E;
+            bad |= e[u] < -1 || e[u] >= a.E;
+            if (chose) atomicAdd(&hist[(int)e[u]], 1);
+            if (!__any_sync(kAll, chose)) continue;
+            ++tokens;
+            scores<V, kSigmoid>(l[u], p, slope, &top, &by);
+#pragma unroll
+            for (int i = 0; i < V; ++i) acc[i] += kSigmoid ? p[i] * by : p[i];
+        }
     }
     if (lane == 0 && tokens) atomicAdd(&used_tokens, tokens);
     for (int w = 0; w < kRouterWarps; ++w) {  // in warp order
@@ -565,7 +580,7 @@ __device__ __forceinline__ void add_shared(const float* p, float (&d)[V]) {
 }
 
 template <typename T, int V, bool kSigmoid>
-__global__ void __launch_bounds__(kRouterThreads, V <= 8 ? 5 : 1) router_backward_kernel(const RouterBackArgs a) {
+__global__ void __launch_bounds__(kRouterThreads, kPerSm<V>) router_backward_kernel(const RouterBackArgs a) {
     __shared__ __align__(16) float rows[kRouterWarps][32 * V];
     const int lane = threadIdx.x & 31;
     float* mine = rows[threadIdx.x >> 5];
@@ -724,18 +739,19 @@ static int by_vectors(int experts, int type, const void* p, int64_t stride) {
         if (aligned_to(p, bytes) && stride * size % bytes == 0 && experts * size % bytes == 0) return bytes;
     return size;
 }
-static ep_status router_blocks(int64_t tokens, int64_t* blocks) {
+static ep_status router_blocks(const ep_router* r, int64_t* blocks) {
     int dev = 0, sms = 0;
     EP_CUDA(cudaGetDevice(&dev));
     EP_CUDA(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
-    const int64_t most = (int64_t)sms * 8, need = (tokens + kRouterWarps - 1) / kRouterWarps;
+    const int64_t most = (int64_t)sms * blocks_per_sm(r->experts), need = (r->tokens + kRouterWarps - 1) / kRouterWarps;
     *blocks = need < most ? need : most;
     return EP_OK;
 }
 
-// Blocks of one sequence: enough for the device over all of them, each with two tokens a warp or more.
-static int balance_blocks(int64_t S, int64_t T, int sms) {
-    int64_t b = ((int64_t)sms * 6 + S - 1) / S;
+// Blocks of one sequence: one wave over all of them (928 blocks for 912 places: 31 us for 24), each with two tokens a
+// warp or more.
+static int balance_blocks(int64_t S, int64_t T, int experts, int sms) {
+    int64_t b = (int64_t)sms * balance_per_sm(experts) / S;
     const int64_t most = (T + 2 * kRouterWarps - 1) / (2 * kRouterWarps);
     if (b > most) b = most;
     return b < 1 ? 1 : (int)b;
@@ -758,7 +774,7 @@ extern "C" ep_status ep_route(const ep_router* r, const void* logits, int64_t lo
     if (!topk_idx || !topk_weights || !aligned_to(topk_idx, 8) || !aligned_to(topk_weights, 4) || !aligned_to(bias, 4))
         return set_error(EP_ERR_INVALID_ARG, "%s: topk_idx, topk_weights and bias aligned to their elements", fn);
     int64_t blocks = 0;
-    EP_TRY(router_blocks(r->tokens, &blocks));
+    EP_TRY(router_blocks(r, &blocks));
     const RouterArgs a = {logits, logits_stride, (uint32_t)r->tokens, r->experts, r->topk, r->groups, r->topk_groups, r->normalize != 0,
                           by_vectors(r->experts, r->logits_type, logits, logits_stride), r->scale, bias, mask, topk_idx, topk_weights};
     return launch_next(r->topk_groups < r->groups ? EP_ROUTER_KERNEL(route_groups, r) : EP_ROUTER_KERNEL(route_all, r), blocks, kRouterThreads, stream, a);
@@ -769,7 +785,7 @@ extern "C" int64_t ep_balance_loss_workspace(const ep_router* r, int32_t sequenc
     if (!r || sequences < 1 || r->experts < 1 || r->experts > kRouterMaxExperts || r->tokens < 0 || r->tokens > INT_MAX ||
         cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
         return 0;
-    return balance_bytes(sequences, balance_blocks(sequences, r->tokens / sequences, sms), r->experts);
+    return balance_bytes(sequences, balance_blocks(sequences, r->tokens / sequences, r->experts, sms), r->experts);
 }
 
 extern "C" ep_status ep_balance_loss(const ep_router* r, const void* logits, int64_t logits_stride, const int64_t* topk_idx,
@@ -786,7 +802,7 @@ extern "C" ep_status ep_balance_loss(const ep_router* r, const void* logits, int
     EP_CUDA(cudaGetDevice(&dev));
     EP_CUDA(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
     const int64_t T = r->tokens / sequences;
-    const int blocks = balance_blocks(sequences, T, sms);
+    const int blocks = balance_blocks(sequences, T, r->experts, sms);
     const int64_t need = balance_bytes(sequences, blocks, r->experts);
     if (!workspace || !aligned16(workspace) || workspace_bytes < need)
         return set_error(EP_ERR_INVALID_ARG, "%s: workspace of %lld bytes (16-byte aligned), %lld needed", fn, (long long)workspace_bytes, (long long)need);
@@ -819,7 +835,7 @@ extern "C" ep_status ep_router_backward(const ep_router* r, const void* logits, 
         return set_error(EP_ERR_INVALID_ARG, "%s: topk_idx, gradients and dlogits (rows %lld elements apart), aligned to their elements", fn,
                          (long long)dlogits_stride);
     int64_t blocks = 0;
-    EP_TRY(router_blocks(r->tokens, &blocks));
+    EP_TRY(router_blocks(r, &blocks));
     const RouterBackArgs a = {logits, topk_idx, dweights, factors, dloss, dlogits, logits_stride, dlogits_stride, (uint32_t)r->tokens,
                               (uint32_t)(factors ? r->tokens / sequences : 1), r->experts, r->topk, r->normalize != 0, by_vectors(r->experts, r->logits_type, logits, logits_stride),
                               by_vectors(r->experts, r->logits_type, dlogits, dlogits_stride), by_vectors(r->experts, EP_F32, factors, r->experts), r->scale, status_out};
