@@ -580,7 +580,7 @@ __device__ __forceinline__ void add_shared(const float* p, float (&d)[V]) {
 }
 
 template <typename T, int V, bool kSigmoid>
-__global__ void __launch_bounds__(kRouterThreads, kPerSm<V>) router_backward_kernel(const RouterBackArgs a) {
+__global__ void __launch_bounds__(kRouterThreads, V <= 8 ? 4 : kPerSm<V>) router_backward_kernel(const RouterBackArgs a) {
     __shared__ __align__(16) float rows[kRouterWarps][32 * V];
     const int lane = threadIdx.x & 31;
     float* mine = rows[threadIdx.x >> 5];
@@ -593,18 +593,36 @@ __global__ void __launch_bounds__(kRouterThreads, kPerSm<V>) router_backward_ker
     // softmax of the whole row, or sigmoid: for the balance loss, and for weights that are not normalised
     const bool whole = a.factors || (!kSigmoid && !a.normalize);
     bool bad = false;
-    for (uint32_t t = blockIdx.x * kRouterWarps + (threadIdx.x >> 5); t < a.tokens; t += gridDim.x * kRouterWarps) {
-        const T* row = static_cast<const T*>(a.logits) + t * a.stride;
-        float l[V];
-        if (whole) load_logits(row, a.E, lane, a.vec, l);
-        int e = -1;
-        float g = 0.0f;
+    // two tokens at a time, where registers allow it: their loads wait together
+    constexpr int kU = V <= 8 ? 2 : 1;
+    const uint32_t step = gridDim.x * kRouterWarps;
+    for (uint32_t t0 = blockIdx.x * kRouterWarps + (threadIdx.x >> 5); t0 < a.tokens; t0 += kU * step) {
+      float rows_l[kU][V], rows_g[kU], rows_logit[kU];
+      int rows_e[kU];
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        const uint32_t t = t0 + u * step;
+        rows_e[u] = -1;
+        rows_g[u] = 0.0f;
+        if (t >= a.tokens) continue;
+        if (whole) load_logits(static_cast<const T*>(a.logits) + t * a.stride, a.E, lane, a.vec, rows_l[u]);
         if (lane < a.K) {
             const int64_t i = a.idx[(int64_t)t * a.K + lane];
             bad |= i < -1 || i >= a.E;
-            e = i >= 0 && i < a.E ? (int)i : -1;
-            if (a.dweights && e >= 0) g = a.dweights[(int64_t)t * a.K + lane] * a.scale;
+            rows_e[u] = i >= 0 && i < a.E ? (int)i : -1;
+            if (a.dweights) rows_g[u] = a.dweights[(int64_t)t * a.K + lane] * a.scale;
         }
+      }
+#pragma unroll
+      for (int u = 0; u < kU; ++u)
+        rows_logit[u] = a.dweights && rows_e[u] >= 0 ? (float)static_cast<const T*>(a.logits)[(t0 + u * step) * a.stride + rows_e[u]] : -INFINITY;
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        const uint32_t t = t0 + u * step;
+        if (t >= a.tokens) break;
+        const float(&l)[V] = rows_l[u];
+        const int e = rows_e[u];
+        const float logit = rows_logit[u], g = e >= 0 ? rows_g[u] : 0.0f;
         T* out = static_cast<T*>(a.dlogits) + t * a.dstride;
         float d[V];
 #pragma unroll
@@ -612,21 +630,6 @@ __global__ void __launch_bounds__(kRouterThreads, kPerSm<V>) router_backward_ker
         if (!__any_sync(kAll, e >= 0)) {  // a padded token
             store_logits(out, a.E, lane, a.dvec, d);
             continue;
-        }
-        float logit = -INFINITY;
-        if (a.dweights) {
-            if (whole) {  // by way of shared memory
-#pragma unroll
-                for (int i = 0; i < V; ++i) mine[lane * V + i] = l[i];
-                __syncwarp();
-                if (e >= 0) logit = mine[e];
-                __syncwarp();
-#pragma unroll
-                for (int i = 0; i < V; ++i) mine[lane * V + i] = 0.0f;
-                __syncwarp();
-            } else if (e >= 0) {
-                logit = (float)row[e];
-            }
         }
         // the chosen experts' share of the gradient, in lane k for choice k
         float near = 0.0f, inner = 0.0f;
@@ -696,6 +699,7 @@ __global__ void __launch_bounds__(kRouterThreads, kPerSm<V>) router_backward_ker
             __syncwarp();
         }
         store_logits(out, a.E, lane, a.dvec, d);
+      }
     }
     if (bad && a.status) flag(a.status, FLAG_INVALID_TOPK);
 }
@@ -739,11 +743,11 @@ static int by_vectors(int experts, int type, const void* p, int64_t stride) {
         if (aligned_to(p, bytes) && stride * size % bytes == 0 && experts * size % bytes == 0) return bytes;
     return size;
 }
-static ep_status router_blocks(const ep_router* r, int64_t* blocks) {
+static ep_status router_blocks(const ep_router* r, int per_sm, int64_t* blocks) {
     int dev = 0, sms = 0;
     EP_CUDA(cudaGetDevice(&dev));
     EP_CUDA(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
-    const int64_t most = (int64_t)sms * blocks_per_sm(r->experts), need = (r->tokens + kRouterWarps - 1) / kRouterWarps;
+    const int64_t most = (int64_t)sms * per_sm, need = (r->tokens + kRouterWarps - 1) / kRouterWarps;
     *blocks = need < most ? need : most;
     return EP_OK;
 }
@@ -774,7 +778,7 @@ extern "C" ep_status ep_route(const ep_router* r, const void* logits, int64_t lo
     if (!topk_idx || !topk_weights || !aligned_to(topk_idx, 8) || !aligned_to(topk_weights, 4) || !aligned_to(bias, 4))
         return set_error(EP_ERR_INVALID_ARG, "%s: topk_idx, topk_weights and bias aligned to their elements", fn);
     int64_t blocks = 0;
-    EP_TRY(router_blocks(r, &blocks));
+    EP_TRY(router_blocks(r, blocks_per_sm(r->experts), &blocks));
     const RouterArgs a = {logits, logits_stride, (uint32_t)r->tokens, r->experts, r->topk, r->groups, r->topk_groups, r->normalize != 0,
                           by_vectors(r->experts, r->logits_type, logits, logits_stride), r->scale, bias, mask, topk_idx, topk_weights};
     return launch_next(r->topk_groups < r->groups ? EP_ROUTER_KERNEL(route_groups, r) : EP_ROUTER_KERNEL(route_all, r), blocks, kRouterThreads, stream, a);
@@ -835,7 +839,7 @@ extern "C" ep_status ep_router_backward(const ep_router* r, const void* logits, 
         return set_error(EP_ERR_INVALID_ARG, "%s: topk_idx, gradients and dlogits (rows %lld elements apart), aligned to their elements", fn,
                          (long long)dlogits_stride);
     int64_t blocks = 0;
-    EP_TRY(router_blocks(r, &blocks));
+    EP_TRY(router_blocks(r, balance_per_sm(r->experts), &blocks));
     const RouterBackArgs a = {logits, topk_idx, dweights, factors, dloss, dlogits, logits_stride, dlogits_stride, (uint32_t)r->tokens,
                               (uint32_t)(factors ? r->tokens / sequences : 1), r->experts, r->topk, r->normalize != 0, by_vectors(r->experts, r->logits_type, logits, logits_stride),
                               by_vectors(r->experts, r->logits_type, dlogits, dlogits_stride), by_vectors(r->experts, EP_F32, factors, r->experts), r->scale, status_out};
