@@ -446,71 +446,80 @@ __global__ void __launch_bounds__(kRouterThreads, V <= 8 ? 4 : kPerSm<V>) balanc
 constexpr int kFinishThreads = 1024;
 
 template <typename T>
-__device__ __forceinline__ T block_sum(T v, T* buf) {
-#pragma unroll
-    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = buf[threadIdx.x & 31];
+__device__ __forceinline__ T warp_total(T v) {
 #pragma unroll
     for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
     return v;
 }
 
 // A block per sequence: its counts, factors and loss; the last block to end adds the losses in order.  A thread adds
-// every (1024 / width)-th block's part of one expert, width: the experts rounded up to a power of two.
+// every (threads / width)-th block's part of one expert, width: the experts rounded up to a power of two.
 __global__ void __launch_bounds__(kFinishThreads) balance_finish_kernel(const BalanceArgs a, int width) {
-    __shared__ long long ibuf[32];
-    __shared__ float fbuf[32];
+    __shared__ long long pairs_of[32], tokens_of[32];  // by warp
+    __shared__ float loss_of[32];
     __shared__ float sums[kFinishThreads];
     __shared__ int hist[kFinishThreads];
+    __shared__ long long all_pairs;
     __shared__ float unit;
-    __shared__ bool last;
     grid_wait();
     grid_launch_next();
-    const int s = blockIdx.x, tid = threadIdx.x, e = tid & (width - 1);
+    const int s = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5, e = tid & (width - 1);
+    const int parts = blockDim.x / width;
     float p = 0.0f;
     int c = 0;
     if (e < a.E)
 #pragma unroll 4
-        for (int b = tid / width; b < a.blocks; b += kFinishThreads / width) {
+        for (int b = tid / width; b < a.blocks; b += parts) {
             const int64_t at = ((int64_t)s * a.blocks + b) * a.E + e;
             p += a.part[at];
             c += a.part_counts[at];
         }
+    long long tokens = 0;
+    for (int b = tid; b < a.blocks; b += blockDim.x) tokens += a.part_tokens[(int64_t)s * a.blocks + b];
     sums[tid] = p;
     hist[tid] = c;
-    long long tokens = 0;
-    for (int b = tid; b < a.blocks; b += kFinishThreads) tokens += a.part_tokens[(int64_t)s * a.blocks + b];
-    const long long pairs = block_sum((long long)c, ibuf);
-    tokens = block_sum(tokens, ibuf);
-    // coef / (S m n), the same for every expert: in 64 bits, which one thread is enough for
-    if (tid == 0) unit = pairs ? (float)((double)a.coef / ((double)a.S * (double)pairs * (double)tokens)) : 0.0f;
+    const long long pairs = warp_total((long long)c);
+    tokens = warp_total(tokens);
+    if (lane == 0) {
+        pairs_of[warp] = pairs;
+        tokens_of[warp] = tokens;
+    }
+    __syncthreads();
+    if (warp == 0) {
+        const long long m = warp_total(lane < warps ? pairs_of[lane] : 0ll), n = warp_total(lane < warps ? tokens_of[lane] : 0ll);
+        if (lane == 0) {  // coef / (S m n), the same for every expert: in 64 bits, which one thread is enough for
+            all_pairs = m;
+            unit = m ? (float)((double)a.coef / ((double)a.S * (double)m * (double)n)) : 0.0f;
+        }
+    }
     __syncthreads();
     float loss = 0.0f;
     if (tid < a.E) {  // the first part's thread
-        for (int i = tid + width; i < kFinishThreads; i += width) {
+        for (int i = tid + width; i < (int)blockDim.x; i += width) {
             p += sums[i];
             c += hist[i];
         }
         a.counts[(int64_t)s * a.E + e] = c;
-        a.factors[(int64_t)s * a.E + e] = unit * (float)((long long)c * a.E - pairs);
+        a.factors[(int64_t)s * a.E + e] = unit * (float)((long long)c * a.E - all_pairs);
         loss = unit * (float)((long long)c * a.E) * p;
     }
-    loss = block_sum(loss, fbuf);
-    if (tid == 0) {
+    loss = warp_total(loss);
+    if (lane == 0) loss_of[warp] = loss;
+    __syncthreads();
+    if (warp != 0) return;
+    loss = warp_total(lane < warps ? loss_of[lane] : 0.0f);
+    bool last = false;
+    if (lane == 0) {
         a.seq_loss[s] = loss;
         __threadfence();
         last = atomicAdd(a.ticket, 1u) == (uint32_t)a.S - 1;
     }
-    __syncthreads();
-    if (!last) return;
+    if (!__any_sync(kAll, last)) return;
     __threadfence();
     float sum = 0.0f;
-    for (int i = tid; i < a.S; i += kFinishThreads) sum += __ldcg(a.seq_loss + i);
-    sum = block_sum(sum, fbuf);
-    if (tid == 0) *a.loss = sum;
+    for (int i = lane; i < a.S; i += 32) sum += __ldcg(a.seq_loss + i);
+    sum = warp_total(sum);
+    if (lane == 0) *a.loss = sum;
 }
 
 // ---- gradient of the logits -----------------------------------------------------------
@@ -819,9 +828,10 @@ extern "C" ep_status ep_balance_loss(const ep_router* r, const void* logits, int
                            ws + 2 * n + (int64_t)sequences * blocks, reinterpret_cast<uint32_t*>(ws + 2 * n + (int64_t)sequences * blocks + sequences),
                            loss, counts, factors, status_out};
     EP_TRY(launch_next(EP_ROUTER_KERNEL(balance_kernel, r), (int64_t)sequences * blocks, kRouterThreads, stream, a));
-    int width = 32;
+    int width = 32, parts = 1;
     while (width < r->experts) width *= 2;
-    return launch_next(balance_finish_kernel, sequences, kFinishThreads, stream, a, width);
+    while (parts < blocks && width * parts < kFinishThreads) parts *= 2;
+    return launch_next(balance_finish_kernel, sequences, width * parts, stream, a, width);
 }
 
 extern "C" ep_status ep_router_backward(const ep_router* r, const void* logits, int64_t logits_stride, const int64_t* topk_idx,
