@@ -247,15 +247,15 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
                     const uint32_t sa = tmem + Shape::kScaleAt + set * Shape::kScaleCols, sb = sa + 8;
                     const uint64_t ds = ds0 + sl.slot * (Shape::kSlot >> 4) + g * (kScales >> 4);
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) tmem_copy_scales<1>(sa + h * 4, ds + h * 32);
+                    for (int h = 0; h < 2; ++h) tmem_copy_scales(sa + h * 4, ds + h * 32);
 #pragma unroll
                     for (int h = 0; h < 2 * Shape::kChunks; ++h)
-                        tmem_copy_scales<1>(sb + h * 4, ds + (Shape::kScalesA >> 4) + h * 32);
+                        tmem_copy_scales(sb + h * 4, ds + (Shape::kScalesA >> 4) + h * 32);
                     const uint32_t at = st.slot * (kCodes >> 4);
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        mma_mxf4<1>(tmem + c * kBN, da0 + at + k * 2, db0 + at + k * 2, k & 1 ? idesc2 : idesc0, sa + (k >> 1) * 4,
-                                        sb + (k >> 1) * 4 * Shape::kChunks, kt > 0 || k > 0);
+                        mma_mxf4(tmem + c * kBN, da0 + at + k * 2, db0 + at + k * 2, k & 1 ? idesc2 : idesc0, sa + (k >> 1) * 4,
+                                 sb + (k >> 1) * 4 * Shape::kChunks, kt > 0 || k > 0);
                     mma_commit<1>(done + st.slot * 8);
                     if (g == k4Group - 1 || kt == a.KT - 1) mma_commit<1>(scale_empty + sl.slot * 8);
                     if (kt == a.KT - 1) mma_commit<1>(acc_full + c * 8);

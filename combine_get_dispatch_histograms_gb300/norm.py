@@ -23,7 +23,11 @@ def _rows(name, t, shape, dtypes, index):
     """Elements between the rows of a row array of this shape."""
     if t.dtype not in dtypes or t.shape != shape or t.get_device() != index:
         _refuse(f"{name}: {' or '.join(str(d) for d in dtypes)} {tuple(shape)} on the same CUDA device: got {t.dtype} {tuple(t.shape)}")
-    return _step(name, t) if t.dim() > 1 else shape[-1]
+    if len(shape) == 1:
+        if not t.is_contiguous():
+            _refuse(f"{name}: channels must be contiguous (strides {t.stride()})")
+        return shape[0]
+    return _step(name, t)
 
 
 def _made(name, given, like, stream, shape, dtype, index):

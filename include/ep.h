@@ -568,7 +568,8 @@ ep_status ep_rms_norm(const void* x, int64_t x_stride, const void* residual, int
  *   dweight [hidden] fp32 = sum over rows of dy * h * s, written, not added to.
  * The order of the sums depends on the sizes and the device alone.  The workspace
  * (16-byte aligned, ep_rms_norm_backward_workspace bytes on the current device)
- * belongs to the call until it has finished. */
+ * belongs to the call until it has finished.  Should a bounded wait (2 s) for its
+ * own copies run out, dweight is NaN. */
 int64_t ep_rms_norm_backward_workspace(int64_t rows, int32_t hidden);
 ep_status ep_rms_norm_backward(const void* dy, int64_t dy_stride, const void* h, int64_t h_stride, int32_t h_type, const void* weight,
                                int32_t weight_type, float eps, const void* dresidual, int64_t dresidual_stride, int64_t rows,
@@ -608,7 +609,8 @@ ep_status ep_route(const ep_router* router, const void* logits, int64_t logits_s
 /* The balance loss of a router, over `sequences` equal runs of tokens (sequences,
  * microbatches or ranks), and its per-expert counts.  With c[s][e] the entries of
  * topk_idx that name e, m[s] their number, n[s] the tokens of s with an entry, and
- * q the softmax of a token's logits, or its sigmoids over their sum:
+ * q the softmax of a token's logits, or its sigmoids over their sum (sigmoids below
+ * 2^-126 count as 0, and over a sum of 0 as 0):
  *   loss [1] = coef * mean over s of sum over e of experts * c[s][e] / m[s] * (mean of q[t][e] over the n[s] tokens)
  *   counts [sequences][experts] = c
  *   factors [sequences][experts] = F[s][e] less its mean over e, where loss = sum of F[s][e] * q[t][e]:

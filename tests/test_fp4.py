@@ -283,6 +283,23 @@ def test_rows_outside_the_arrays_are_cut_off_and_flagged():
 
 
 @gpu
+def test_rows_further_apart_than_32_bits_reach():
+    K, N, far = 256, 100, (1 << 30) + 16
+    g = gen(13)
+    x = torch.as_strided(torch.empty(3 * far, dtype=BF, device="cuda"), (3, K), (far, 1))
+    x.copy_(randn((3, K), g))
+    big = torch.empty(6 * far, dtype=torch.uint8, device="cuda")
+    codes, scales = torch.as_strided(big, (3, K // 2), (2 * far, 1)), torch.as_strided(big, (3, K // 32), (2 * far, 1), 1024)
+    ep.quantize_fp4(x, out=(codes, scales))
+    want = ep.quantize_fp4(x.contiguous())
+    assert torch.equal(codes, want[0]) and torch.equal(scales, want[1])
+    w, ws = weight4(1, N, K, g)
+    out = torch.as_strided(torch.empty(3 * far, dtype=BF, device="cuda"), (3, N), (far, 1))
+    ep.expert_gemm_fp4(codes, scales, w[0], ws[0], out=out)
+    assert torch.equal(out, ep.expert_gemm_fp4(*want, w[0], ws[0]))
+
+
+@gpu
 def test_a_nan_stays_in_its_row_and_column():
     K, N, rows = 512, 256, 130
     g = gen(7)

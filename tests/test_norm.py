@@ -130,6 +130,21 @@ def test_strides_three_dimensions_and_in_place():
 
 
 @gpu
+def test_rows_further_apart_than_32_bits_reach():
+    H, far = 1032, (1 << 30) + 8
+    big = torch.empty(3 * far, dtype=BF, device="cuda")
+    x = torch.as_strided(big, (3, H), (far, 1))
+    x.copy_(randn((3, H), gen(12)))
+    w = torch.ones(H, device="cuda")
+    c = x.clone()
+    assert torch.equal(ep.rms_norm(x, w)["y"], ep.rms_norm(c, w)["y"])
+    for a, b in zip(ep.rms_norm_backward(x, x, w, dresidual=x), ep.rms_norm_backward(c, c, w, dresidual=c)):
+        assert torch.equal(a, b)
+    ep.rms_norm(x, w, out={"y": x})
+    assert torch.equal(x, ep.rms_norm(c, w)["y"])
+
+
+@gpu
 def test_no_rows():
     w, x = torch.ones(128, device="cuda"), torch.empty(0, 128, device="cuda", dtype=BF)
     got = ep.rms_norm(x, w, residual=x, fp8=True)
@@ -211,7 +226,7 @@ def test_refusals_on_the_gpu():
                  lambda: ep.rms_norm(x, w, residual=x[:3]), lambda: ep.rms_norm(x, w, residual=x.half()),
                  lambda: ep.rms_norm(x, w.half()), lambda: ep.rms_norm(x, w, out={"residual": x}),
                  lambda: ep.rms_norm(x[:, ::2], w[:68]), lambda: ep.rms_norm_backward(x, x, w, dresidual=x.float()),
-                 lambda: ep.rms_norm(x, w, out={"y": x[:2]})):
+                 lambda: ep.rms_norm(x, w, out={"y": x[:2]}), lambda: ep.rms_norm(x.view(-1)[::4], w)):
         with pytest.raises(ValueError):
             call()
     for call in (lambda: ep.rms_norm(x[:, 1:129], w[:128]), lambda: ep.rms_norm(x, w, eps=0.0),

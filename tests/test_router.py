@@ -322,6 +322,23 @@ def test_entries_out_of_range_are_skipped_and_reported():
 
 
 @gpu
+def test_rows_further_apart_than_32_bits_reach():
+    E, far = 72, (1 << 30) + 8
+    big = torch.empty(3 * far, dtype=BF, device="cuda")
+    l = torch.as_strided(big, (3, E), (far, 1))
+    l.copy_(randn((3, E), gen(12)))
+    c = l.clone()
+    idx, w = ep.route(l, 5)
+    want = ep.route(c, 5)
+    assert torch.equal(idx, want[0]) and torch.equal(w, want[1])
+    got, ref = ep.balance_loss(l, idx), ep.balance_loss(c, idx)
+    assert all(torch.equal(got[k], ref[k]) for k in ref)
+    one = torch.ones(1, device="cuda")
+    want = ep.router_backward(c, idx, w, factors=ref["factors"], dloss=one)
+    assert torch.equal(ep.router_backward(l, idx, w, factors=ref["factors"], dloss=one, out=l), want)
+
+
+@gpu
 def test_no_tokens_and_in_place_gradient():
     l = torch.empty(0, 16, device="cuda")
     idx, w = ep.route(l, 4)
