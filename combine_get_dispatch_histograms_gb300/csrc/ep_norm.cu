@@ -459,22 +459,23 @@ __global__ void __launch_bounds__(1024) norm_backward_block(const NormBackArgs a
     }
 }
 
-// dw[c] = sum over blocks of part[block][c], in an order that depends on the number of blocks alone:
-// 8 rows of threads take every 8th block each, then their sums are added in order.
-__global__ void __launch_bounds__(256) norm_weight_kernel(const float* part, int blocks, int hidden, float* dw) {
-    __shared__ float sums[8][33];
+// dw[c] = sum over blocks of part[block][c], in an order that depends on the number of blocks alone: 32 rows of threads
+// take every 32nd block each, then their sums are added as a tree.
+__global__ void __launch_bounds__(1024) norm_weight_kernel(const float* part, int blocks, int hidden, float* dw) {
+    __shared__ float sums[32][33];
     grid_wait();
     grid_launch_next();
     const int lane = threadIdx.x & 31, r = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
     float s = 0.0f;
     if (c < hidden)
-        for (int b = r; b < blocks; b += 8) s += part[(int64_t)b * hidden + c];
+#pragma unroll 8
+        for (int b = r; b < blocks; b += 32) s += part[(int64_t)b * hidden + c];
     sums[r][lane] = s;
     __syncthreads();
-    if (r == 0 && c < hidden) {
-        for (int i = 1; i < 8; ++i) s += sums[i][lane];
-        dw[c] = s;
-    }
+    s = sums[lane][r];  // warp r: column r
+#pragma unroll
+    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (lane == 0 && blockIdx.x * 32 + r < hidden) dw[blockIdx.x * 32 + r] = s;
 }
 
 // ---- host -------------------------------------------------------------------------
@@ -632,5 +633,5 @@ extern "C" ep_status ep_rms_norm_backward(const void* dy, int64_t dy_stride, con
                                 dy_stride, h_stride, dresidual_stride, dx_stride, rows, hidden, eps, weight_type == EP_F32};
         EP_TRY(h_type == EP_BF16 ? launch_back<1>(a, sms, &blocks, stream) : launch_back<2>(a, sms, &blocks, stream));
     }
-    return launch_next(norm_weight_kernel, (hidden + 31) / 32, 256, stream, static_cast<const float*>(workspace), blocks, hidden, dweight);
+    return launch_next(norm_weight_kernel, (hidden + 31) / 32, 1024, stream, static_cast<const float*>(workspace), blocks, hidden, dweight);
 }
