@@ -27,10 +27,11 @@ constexpr int k4TileRing = 4;
 constexpr int k4Group = 2;        // stages whose scales are staged together
 constexpr int64_t k4WaitNs = 2000000000ll;
 
-template <bool kSwiglu, int kBN>
+template <bool kSwiglu, int kBN, int kCtas>
 struct Fp4Shape {
+    static constexpr int kTileM = kCtas * k4BM;
     static constexpr int kChunks = (kBN + 127) / 128;               // of 128 weight rows' scales
-    static constexpr int kCodesA = k4BM * 128, kCodesB = kBN * 128, kCodes = kCodesA + kCodesB;
+    static constexpr int kCodesA = k4BM * 128, kCodesB = kBN / kCtas * 128, kCodes = kCodesA + kCodesB;
     static constexpr int kScalesA = 2 * 512, kScalesB = 2 * kChunks * 512, kScales = kScalesA + kScalesB;  // [128 of K][chunk][32][16]
     static constexpr int kSlot = k4Group * kScales;                 // the scales that are staged together
     static constexpr int kSlots = kSwiglu ? 4 : 2;
@@ -106,12 +107,12 @@ __device__ __forceinline__ Scales32 load_scales(const uint8_t* row, int at, int 
 }
 
 // kSwiglu: half of the tile's weight rows are gate rows, half the up rows of the same channels.
-template <bool kSwiglu, int kBN>
+template <bool kSwiglu, int kBN, int kCtas>
 __global__ void __launch_bounds__(k4Threads, 1)
 fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_box,
                 const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_out, const Fp4Args a) {
-    using Shape = Fp4Shape<kSwiglu, kBN>;
-    constexpr int kStages = Shape::kStages, kSlots = Shape::kSlots, kCodes = Shape::kCodes, kScales = Shape::kScales, kHalf = kBN / 2;
+    using Shape = Fp4Shape<kSwiglu, kBN, kCtas>;
+    constexpr int kStages = Shape::kStages, kSlots = Shape::kSlots, kCodes = Shape::kCodes, kScales = Shape::kScales, kHalf = kBN / 2, kTileM = Shape::kTileM;
     extern __shared__ __align__(1024) uint8_t dyn[];
     __shared__ Fp4Shared<kStages, kSlots> sh;
     // codes of all stages first, each on 1024 bytes; then the scales, then the rows on their way out
@@ -119,6 +120,7 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
     uint8_t* scales = codes + kStages * kCodes;
     uint8_t* out_stage = scales + kSlots * Shape::kSlot;  // on 1024 bytes too
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rank = kCtas == 2 ? (int)cluster_rank() : 0, unit = blockIdx.x / kCtas, units = gridDim.x / kCtas;
     volatile int* abort = &sh.abort;
     const uint32_t full = smem_u32(sh.full), done = smem_u32(sh.done);
     const uint32_t scale_full = smem_u32(sh.scale_full), scale_empty = smem_u32(sh.scale_empty);
@@ -127,7 +129,7 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
 
     if (tid == 0) {
         for (int s = 0; s < kStages; ++s) {
-            mbar_init(&sh.full[s], 1);
+            mbar_init(&sh.full[s], kCtas == 2 && rank == 0 ? 2 : 1);  // its own copies, and what the other block says of its
             mbar_init(&sh.done[s], 1);
         }
         for (int b = 0; b < kSlots; ++b) {
@@ -136,7 +138,7 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&sh.acc_full[b], 1);
-            mbar_init(&sh.acc_empty[b], k4OutWarps);
+            mbar_init(&sh.acc_empty[b], kCtas * k4OutWarps);
         }
         for (int b = 0; b < k4TileRing; ++b) {
             mbar_init(&sh.tile_full[b], 1);
@@ -150,9 +152,10 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
         tma_prefetch_desc(&map_box);
         tma_prefetch_desc(&map_w);
     }
-    if (warp == 2) tmem_alloc<1>(&sh.tmem, Shape::kCols);
+    if (warp == 2) tmem_alloc<kCtas>(&sh.tmem, Shape::kCols);
     tc_fence_before();
     __syncthreads();
+    if (kCtas == 2) cluster_sync();  // both blocks' barriers are ready
     tc_fence_after();
     // All above may run beside the end of the kernel before; the kernel after may do the same.
     grid_wait();
@@ -161,9 +164,9 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
 
     if (warp == 3) {
         // ---- tiles
-        TileWalk<k4BM> walk;
+        TileWalk<kTileM> walk;
         RingPos<k4TileRing> tr;
-        for (int t = blockIdx.x;; t += gridDim.x) {
+        for (int t = unit;; t += units) {
             GemmTile tile = {0, 0, 0, 0};
             const bool some = walk.find(a, min(t, a.most), lane, &tile);
             if (t >= a.most) tile.rows = 0;  // groups that overlap may have any number of tiles
@@ -193,9 +196,12 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
                 mbar_arrive(tr.bar(tile_empty));
                 ++tr.n;
                 if (tile.rows == 0) break;
-                const int boxes = (tile.rows + k4BoxRows - 1) / k4BoxRows;
-                const uint32_t bytes = boxes * k4BoxRows * 128 + kBN * 128;
-                const int w0 = kSwiglu ? tile.n * kHalf : tile.n * kBN;
+                const int rows = min(tile.rows - rank * k4BM, k4BM), row = tile.row0 + rank * k4BM;
+                const int boxes = (max(rows, 0) + k4BoxRows - 1) / k4BoxRows;
+                const uint32_t bytes = boxes * k4BoxRows * 128 + Shape::kCodesB;
+                // the first block of a pair has the gate rows, or the first half, the second the others
+                const int first = kSwiglu ? tile.n * kHalf : tile.n * kBN, second = kSwiglu ? a.N / 2 + first : first + kHalf;
+                const int w0 = rank ? second : first;
                 for (int kt = 0; kt < a.KT; ++kt) {
                     if (!mbar_wait_or_abort<true>(done + st.slot * 8, st.phase ^ 1, k4WaitNs, abort)) {
                         ok = false;
@@ -205,11 +211,11 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
                     const uint32_t bar = full + st.slot * 8;
                     mbar_arrive_expect_tx(&sh.full[st.slot], bytes);
                     tma_load_3d<1>(sa + Shape::kCodesA, &map_w, kt * 128, w0, tile.g, bar);
-                    if (kSwiglu) tma_load_3d<1>(sa + Shape::kCodesA + kHalf * 128, &map_w, kt * 128, a.N / 2 + w0, tile.g, bar);
-                    if (boxes == k4BM / k4BoxRows) tma_load_2d<1>(sa, &map_x, kt * 128, tile.row0, bar);
+                    if (kSwiglu && kCtas == 1) tma_load_3d<1>(sa + Shape::kCodesA + kHalf * 128, &map_w, kt * 128, second, tile.g, bar);
+                    if (boxes == k4BM / k4BoxRows) tma_load_2d<1>(sa, &map_x, kt * 128, row, bar);
                     else
                         for (int b = 0; b < boxes; ++b)
-                            tma_load_2d<1>(sa + b * k4BoxRows * 128, &map_box, kt * 128, tile.row0 + b * k4BoxRows, bar);
+                            tma_load_2d<1>(sa + b * k4BoxRows * 128, &map_box, kt * 128, row + b * k4BoxRows, bar);
                     st.next();
                 }
             }
@@ -220,9 +226,33 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
                 st.next();
             }
         }
+    } else if (warp == 1 && rank != 0) {
+        // ---- the second block's copies and scales are in place: told to the first block, stage by stage
+        const uint32_t full0 = smem_of(full, 0);
+        RingPos<k4TileRing> tr;
+        Turn<kStages> st;
+        Turn<kSlots> sl;
+        while (true) {
+            mbar_wait_warp<true>(tr.bar(tile_full), tr.phase(), k4WaitNs, abort);
+            const int rows = sh.tile[tr.slot()].rows;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(tr.bar(tile_empty));
+            ++tr.n;
+            if (rows == 0 || __any_sync(0xffffffffu, *abort)) break;
+#pragma unroll 1
+            for (int kt = 0; kt < a.KT; ++kt) {
+                if ((kt & (k4Group - 1)) == 0) {
+                    mbar_wait_warp<true>(scale_full + sl.slot * 8, sl.phase, k4WaitNs, abort);
+                    sl.next();
+                }
+                mbar_wait_warp<true>(full + st.slot * 8, st.phase, k4WaitNs, abort);
+                if (lane == 0) mbar_arrive_filled(full0 + st.slot * 8);
+                st.next();
+            }
+        }
     } else if (warp == 1) {
-        // ---- copies of scales into tensor memory, products
-        constexpr uint32_t idesc0 = idesc_mxf4(k4BM, kBN, 0), idesc2 = idesc_mxf4(k4BM, kBN, 2);
+        // ---- copies of scales into tensor memory, products: for both blocks of a pair by the first
+        constexpr uint32_t idesc0 = idesc_mxf4(kTileM, kBN, 0), idesc2 = idesc_mxf4(kTileM, kBN, 2);
         const uint64_t da0 = smem_desc_sw128(codes), db0 = smem_desc_sw128(codes + Shape::kCodesA), ds0 = smem_desc_rows16(scales);
         RingPos<k4TileRing> tr;
         Turn<kStages> st;
@@ -247,18 +277,18 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
                     const uint32_t sa = tmem + Shape::kScaleAt + set * Shape::kScaleCols, sb = sa + 8;
                     const uint64_t ds = ds0 + sl.slot * (Shape::kSlot >> 4) + g * (kScales >> 4);
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) tmem_copy_scales(sa + h * 4, ds + h * 32);
+                    for (int h = 0; h < 2; ++h) tmem_copy_scales<kCtas>(sa + h * 4, ds + h * 32);
 #pragma unroll
                     for (int h = 0; h < 2 * Shape::kChunks; ++h)
-                        tmem_copy_scales(sb + h * 4, ds + (Shape::kScalesA >> 4) + h * 32);
+                        tmem_copy_scales<kCtas>(sb + h * 4, ds + (Shape::kScalesA >> 4) + h * 32);
                     const uint32_t at = st.slot * (kCodes >> 4);
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        mma_mxf4(tmem + c * kBN, da0 + at + k * 2, db0 + at + k * 2, k & 1 ? idesc2 : idesc0, sa + (k >> 1) * 4,
+                        mma_mxf4<kCtas>(tmem + c * kBN, da0 + at + k * 2, db0 + at + k * 2, k & 1 ? idesc2 : idesc0, sa + (k >> 1) * 4,
                                  sb + (k >> 1) * 4 * Shape::kChunks, kt > 0 || k > 0);
-                    mma_commit<1>(done + st.slot * 8);
-                    if (g == k4Group - 1 || kt == a.KT - 1) mma_commit<1>(scale_empty + sl.slot * 8);
-                    if (kt == a.KT - 1) mma_commit<1>(acc_full + c * 8);
+                    mma_commit<kCtas>(done + st.slot * 8);
+                    if (g == k4Group - 1 || kt == a.KT - 1) mma_commit<kCtas>(scale_empty + sl.slot * 8);
+                    if (kt == a.KT - 1) mma_commit<kCtas>(acc_full + c * 8);
                 }
                 __syncwarp();
                 st.next();
@@ -266,8 +296,8 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
                 set ^= 1;
             }
         }
-        // every product has finished before tensor memory is freed
-        if (elect_one()) mma_commit<1>(smem_u32(&sh.drain));
+        // every product has finished before either block frees its tensor memory: the second waits for this one below
+        if (elect_one()) mma_commit_here<kCtas>(smem_u32(&sh.drain));
         __syncwarp();
         mbar_wait_bounded(&sh.drain, 0, k4WaitNs);
     } else if (warp >= 4 && warp < 4 + k4ScaleWarps) {
@@ -291,7 +321,8 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
                 return n < a.N ? n : -1;
             };
             const int n0 = weight_row(r), n1 = weight_row(128 + r);
-            const uint8_t* px = r < tile.rows ? a.x_scales + (int64_t)(tile.row0 + r) * a.x_sstride : nullptr;
+            const int row = rank * k4BM + r;
+            const uint8_t* px = row < tile.rows ? a.x_scales + (int64_t)(tile.row0 + row) * a.x_sstride : nullptr;
             const uint8_t* p0 = n0 >= 0 ? a.w_scales + ((int64_t)tile.g * a.N + n0) * bytes : nullptr;
             const uint8_t* p1 = n1 >= 0 ? a.w_scales + ((int64_t)tile.g * a.N + n1) * bytes : nullptr;
             Scales32 vx[kAhead], v0[kAhead], v1[kAhead];
@@ -337,7 +368,7 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
         }
     } else if (warp >= 4 + k4ScaleWarps) {
         // ---- results: a lane a row
-        const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);
+        const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21), free_bar = kCtas == 2 ? smem_of(acc_empty, 0) : acc_empty;
         uint8_t* stage = out_stage + (warp & 3) * Shape::kOut;
         RingPos<k4TileRing> tr;
         while (true) {
@@ -350,7 +381,7 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
             if (tile.rows == 0 || __any_sync(0xffffffffu, *abort)) break;
             mbar_wait_warp<true>(acc_full + c * 8, turn, k4WaitNs, abort);
             tc_fence_after();
-            const int first = (warp & 3) * 32, rows = min(32, tile.rows - first);  // of this warp
+            const int first = rank * k4BM + (warp & 3) * 32, rows = min(32, tile.rows - first);  // of this warp
             if (rows > 0) {
                 const int64_t row0 = tile.row0 + first;
                 if constexpr (kSwiglu) {
@@ -432,16 +463,19 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_hand_back(acc_empty + c * 8);
+            if (lane == 0) mbar_hand_back(free_bar + c * 8);
         }
         bulk_wait_all();
     }
     __syncwarp();
     tc_fence_before();
     __syncthreads();
+    if (kCtas == 2) cluster_sync();
     tc_fence_after();
-    if (warp == 2) tmem_free<1>(tmem, Shape::kCols);
+    if (warp == 2) tmem_free<kCtas>(tmem, Shape::kCols);
     if (tid == 0 && *abort && a.status) flag(a.status, FLAG_TIMEOUT);
+    __syncwarp();
+    if (kCtas == 2) cluster_sync();  // neither block ends while the other still frees
 }
 
 // ---- quantisation ---------------------------------------------------------------------
@@ -502,12 +536,12 @@ static ep_status check_fp4(const char* fn, const ep_fp4_rows* x, const ep_row_gr
     return EP_OK;
 }
 
-template <bool kSwiglu, int kBN>
+template <bool kSwiglu, int kBN, int kCtas>
 static ep_status launch_fp4_shape(const char* fn, const ep_fp4_rows* x, const ep_fp4_weight* w, Fp4Args a, int sms, int dev, void* stream) {
-    using Shape = Fp4Shape<kSwiglu, kBN>;
+    using Shape = Fp4Shape<kSwiglu, kBN, kCtas>;
     constexpr int kTileN = kSwiglu ? kBN / 2 : kBN;
     a.n_tiles = ((kSwiglu ? w->n / 2 : w->n) + kTileN - 1) / kTileN;
-    const int64_t most = most_tiles(a, k4BM);
+    const int64_t most = most_tiles(a, Shape::kTileM);
     if (most > kMaxTiles) return set_error(EP_ERR_INVALID_ARG, "%s: %lld tiles", fn, (long long)most);
     a.most = (int)most;
     CUtensorMap map_x, map_box, map_w, map_out;
@@ -521,7 +555,7 @@ static ep_status launch_fp4_shape(const char* fn, const ep_fp4_rows* x, const ep
     {
         const cuuint64_t dims[3] = {(cuuint64_t)w->k / 2, (cuuint64_t)w->n, (cuuint64_t)w->groups};
         const cuuint64_t strides[2] = {(cuuint64_t)w->k / 2, (cuuint64_t)w->k / 2 * (cuuint64_t)w->n};
-        const cuuint32_t box[3] = {128, (cuuint32_t)kTileN, 1};
+        const cuuint32_t box[3] = {128, kSwiglu || kCtas == 2 ? kBN / 2 : kBN, 1};
         EP_TRY(encode_rows(&map_w, w->codes, 3, dims, strides, box, fn));
     }
     map_out = map_x;  // used for aligned bf16 rows only
@@ -533,11 +567,19 @@ static ep_status launch_fp4_shape(const char* fn, const ep_fp4_rows* x, const ep
     }
     static std::atomic<bool> known[kMaxDevicesTracked];  // devices whose launch attribute is set
     if (dev >= kMaxDevicesTracked || !known[dev].load(std::memory_order_relaxed)) {
-        EP_CUDA(cudaFuncSetAttribute(fp4_gemm_kernel<kSwiglu, kBN>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Shape::kSmem));
+        EP_CUDA(cudaFuncSetAttribute(fp4_gemm_kernel<kSwiglu, kBN, kCtas>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Shape::kSmem));
         if (dev < kMaxDevicesTracked) known[dev].store(true, std::memory_order_relaxed);
     }
-    return launch_next(fp4_gemm_kernel<kSwiglu, kBN>, most < sms ? most : sms, k4Threads, stream, Shared{Shape::kSmem}, map_x, map_box, map_w, map_out, a);
+    const int64_t units = most < sms / kCtas ? most : sms / kCtas;
+    return launch_next(fp4_gemm_kernel<kSwiglu, kBN, kCtas>, units * kCtas, k4Threads, stream, Shared{Shape::kSmem, kCtas}, map_x, map_box, map_w, map_out, a);
 }
+
+// Whether pairs of blocks make the first product's tiles: one of theirs costs 1.65 of one block's, and has twice the rows.
+// 40 groups, K 7168, 2I 4096, us by one block / by pairs: 256 rows a group 136 / 127, 448 242 / 206, 640 295 / 290, 768 355 /
+// 302, 1024 481 / 397, 2048 941 / 755; but 256 groups of 256 rows on average, popular and unpopular, 1020 / 1075: half a
+// tile of each group is empty on average.  (The second product, whose results are its larger part, gains 3 % at best:
+// 2048 rows 537 / 515.)
+static bool fp4_by_pairs(int64_t rows) { return rows > 3 * k4BM; }
 
 template <bool kSwiglu>
 static ep_status launch_fp4(const char* fn, const ep_fp4_rows* x, const ep_row_groups* g, const ep_fp4_weight* w, Fp4Args a, void* stream) {
@@ -561,8 +603,14 @@ static ep_status launch_fp4(const char* fn, const ep_fp4_rows* x, const ep_row_g
     EP_CUDA(cudaGetDevice(&dev));
     EP_CUDA(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
     a.n_tiles = (w->n + 191) / 192;
-    if (most_tiles(a, k4BM) * 2 <= sms) return launch_fp4_shape<kSwiglu, 64>(fn, x, w, a, sms, dev, stream);
-    return launch_fp4_shape<kSwiglu, 192>(fn, x, w, a, sms, dev, stream);
+    if (most_tiles(a, k4BM) * 2 <= sms) return launch_fp4_shape<kSwiglu, 64, 1>(fn, x, w, a, sms, dev, stream);
+    if constexpr (kSwiglu) {
+        // Rows of a group: as the caller expects, or what the arrays hold, shared out; regions with counts are sized for the
+        // worst case, and a low-latency step fills a few percent of them.
+        const int64_t rows = g->expected > 0 ? g->expected : x->rows / w->groups / (w->groups > 1 && !g->offsets && g->counts ? 16 : 1);
+        if (fp4_by_pairs(rows)) return launch_fp4_shape<kSwiglu, 192, 2>(fn, x, w, a, sms, dev, stream);
+    }
+    return launch_fp4_shape<kSwiglu, 192, 1>(fn, x, w, a, sms, dev, stream);
 }
 
 }  // namespace ep

@@ -238,6 +238,7 @@ inline cudaStream_t as_stream(void* s) { return reinterpret_cast<cudaStream_t>(s
 // A kernel that may start while the one before drains: it calls grid_wait before its first access to memory.
 struct Shared {
     size_t bytes;  // dynamic shared memory
+    int cluster = 1;
 };
 template <typename... Params, typename... Args>
 ep_status launch_next(void (*kernel)(Params...), int64_t blocks, int threads, void* stream, Shared shared, const Args&... args) {
@@ -246,11 +247,14 @@ ep_status launch_next(void (*kernel)(Params...), int64_t blocks, int threads, vo
     cfg.blockDim = dim3((unsigned)threads);
     cfg.dynamicSmemBytes = shared.bytes;
     cfg.stream = as_stream(stream);
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = shared.cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = shared.cluster > 1 ? 2 : 1;
     EP_CUDA(cudaLaunchKernelEx(&cfg, kernel, args...));
     return EP_OK;
 }

@@ -154,6 +154,13 @@ __device__ __forceinline__ void mbar_hand_back(uint32_t bar) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
+// The same for shared memory of the arriving block, which the tensor cores read: bulk copies and fenced writes that
+// the arriving thread has waited for.  A release at cluster scope costs it some 1800 cycles (measured), one at block scope
+// orders what it has waited for and is not seen in the kernel's time.
+__device__ __forceinline__ void mbar_arrive_filled(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
 // ---- tiled bulk copies (the innermost coordinate is a multiple of 16 bytes) ------
 // Into this block's shared memory; `bar` (a cluster address) counts the bytes,
 // with kCtas = 2 also where it lies in the other block of the pair.
@@ -252,21 +259,35 @@ __device__ __forceinline__ void mma_bf16_ss(uint32_t d, uint64_t a, uint64_t b, 
         "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
         : "memory");
 }
-// D[128 x N] (+)= A[128 x 64] B[N x 64]^T, by one block, two e2m1 codes a byte in shared memory, each 32 codes times
-// 2^(their E8M0 byte - 127).  sa, sb: columns of tensor memory with the scales: row r's in lane r % 32 (of every 32 lanes)
-// of column r / 32, four bytes for 128 codes; the descriptor says which two of them (idesc_mxf4).
+// D[kCtas * 128 x N] (+)= A[kCtas * 128 x 64] B[N x 64]^T, two e2m1 codes a byte in shared memory, each 32 codes times
+// 2^(their E8M0 byte - 127).  sa, sb: columns of tensor memory with the scales, of both blocks with kCtas = 2 (of each
+// block's rows of A, and of all of B's): row r's in lane r % 32 (of every 32 lanes) of column r / 32, four bytes for 128
+// codes; the descriptor says which two of them (idesc_mxf4).
+template <int kCtas>
 __device__ __forceinline__ void mma_mxf4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa, uint32_t sb, bool add) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.u32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"((uint32_t)add)
-        : "memory");
+    if constexpr (kCtas == 2)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.u32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"((uint32_t)add)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.u32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"((uint32_t)add)
+            : "memory");
 }
-// 512 bytes of shared memory, 32 rows of 16, to 4 columns of tensor memory, the same in every 32 lanes; before the
-// products that this thread issues later, after those that it issued before.
+// 512 bytes of shared memory, 32 rows of 16, to 4 columns of tensor memory, the same in every 32 lanes, with kCtas = 2 in
+// each block its own; before the products that this thread issues later, after those that it issued before.
+template <int kCtas>
 __device__ __forceinline__ void tmem_copy_scales(uint32_t d, uint64_t desc) {
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(d), "l"(desc) : "memory");
+    if constexpr (kCtas == 2)
+        asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(d), "l"(desc) : "memory");
+    else
+        asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(d), "l"(desc) : "memory");
 }
 // Arrives on `bar` (of both blocks) when every tcgen05.mma this thread issued has finished.
 template <int kCtas>
