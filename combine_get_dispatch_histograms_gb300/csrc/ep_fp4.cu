@@ -6,11 +6,17 @@
 // which tcgen05.mma computes whole (kind::mxf4, block scales from tensor memory, fp32 sums), so that the
 // accumulator leaves tensor memory once a tile, not once a block of K.
 //
-// Shape.  128 rows x kBN weight rows a tile.  One warp copies codes (256 of K, 128 bytes a row, a
-// stage), four stage scales: each thread loads its rows' bytes and writes them where tcgen05.cp reads them
-// (32 rows of 16 bytes: row r's four bytes at (r % 32) * 16 + r / 32 * 4), one issues copies of scales and
-// products, four write the results.  With 192 weight rows a tile tensor memory holds two accumulators and
-// the scales beside them, so that a tile is written while the next is multiplied.
+// Shape.  128 rows x 192 weight rows a tile (64 where the tiles are few): tensor memory then holds two
+// accumulators and the scales beside them, so that a tile is written while the next is multiplied.  One warp
+// copies codes (a stage is 256 of K, 128 bytes a row), four stage scales: each thread loads its rows' bytes and
+// writes them where tcgen05.cp reads them (32 rows of 16 bytes: row r's four bytes at (r % 32) * 16 + r / 32 * 4),
+// one issues copies of scales and products, four write the results.
+//
+// Bound.  Up to 128 rows a group the weights' bytes: 256 groups of about 64 rows, K 7168, 2I 4096 594 us, K 2048, N 7168
+// 325 us, 6.7 TB/s.  With long groups shared memory: a stage's codes are written to it and read from it once, 82 KB at
+// 128 bytes a cycle = 640 cycles, and a stage takes 650 (the products some 370).  Pairs of blocks share the weight's
+// rows, 56 KB a stage and SM: first product, 40 groups of 2048 rows, 941 us by one block, 755 by pairs (6.4 PFLOP/s).
+// A fifth stage, or weights fetched ahead into the second-level cache, change nothing.
 #include <atomic>
 
 #include "ep_fp4.cuh"
@@ -27,6 +33,8 @@ constexpr int k4TileRing = 4;
 constexpr int k4Group = 2;        // stages whose scales are staged together
 constexpr int64_t k4WaitNs = 2000000000ll;
 
+// kCtas = 2: a pair of blocks makes a tile of 256 rows, each with its own rows and half of the weight's, and with the
+// scales of all of the weight's.
 template <bool kSwiglu, int kBN, int kCtas>
 struct Fp4Shape {
     static constexpr int kTileM = kCtas * k4BM;

@@ -8,8 +8,14 @@
 // and backward, with g = dy w and d the gradient that reaches h from elsewhere:
 //   dh_c = d_c + s (g_c - h_c s^2 (sum_j g_j h_j) / H),   dw_c = sum over rows of dy_c h_c s
 //
-// Both are bound by memory: every array is read or written once.  A row stays in the registers of
-// one block (of one warp up to 1024 channels) between its sum and its outputs.
+// Both are bound by memory: every array is read or written once.  Forward, a row stays in the registers
+// of one block (of one warp up to 1024 channels) between its sum and its outputs, with the next row's loads
+// on their way: 32768 rows of 7168 with a bf16 residual, bf16 and FP8 out, 335 us (6.3 TB/s of 6.8 measured for
+// a copy); with an fp32 residual two vectors a thread and more blocks, since four take 108 registers (4099
+// rows of 4104: 42 -> 33.5 us, 6.0 TB/s).  A single row of 7168 takes 2.9 us.  Backward, rows come by bulk
+// copies into shared memory, up to four ahead, and two blocks or more share a processor, since a block's
+// two sums a row wait for each other (16384 rows of 7168: by registers alone 187 us, one block a processor
+// 184, two 161: 5.8 TB/s).
 #include <atomic>
 
 #include "ep_fp8.cuh"
