@@ -53,11 +53,6 @@ struct NormBackArgs {
 };
 
 // 8 channels at a time.  Plain loads: an output may be the input's own memory.
-__device__ __forceinline__ int4 ld_na_v4(const void* p) {
-    int4 v;
-    asm volatile("ld.global.L1::no_allocate.v4.s32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
-    return v;
-}
 template <typename T>
 struct Raw8;  // 8 channels as they lie in memory
 template <>

@@ -73,7 +73,8 @@ __device__ __forceinline__ float warp_max(float v) {  // a NaN counts only where
     return m;
 }
 
-// This lane's V logits of a row; -inf past the last expert.  vec: the bytes a lane may take at once.
+// This lane's V logits of a row; -inf past the last expert.  vec: the bytes a lane may take at once.  Plain loads: the
+// gradient may overwrite the logits.
 template <typename T, int V>
 __device__ __forceinline__ void load_logits(const T* row, int E, int lane, int vec, float (&v)[V]) {
     auto unpack = [&](const uint32_t* u, int words, int at) {
@@ -98,7 +99,7 @@ __device__ __forceinline__ void load_logits(const T* row, int E, int lane, int v
                 for (int c = 0; c < V; c += kPer)
                     if (lane * V + c < E) {
                         uint32_t u[8];
-                        ld_nc_32(row + lane * V + c, u);
+                        ld_global_32(row + lane * V + c, u);
                         unpack(u, 8, c);
                     }
             } else {
@@ -106,7 +107,7 @@ __device__ __forceinline__ void load_logits(const T* row, int E, int lane, int v
 #pragma unroll
                 for (int c = 0; c < V; c += kPer)
                     if (lane * V + c < E) {
-                        const int4 r = ld_nc_na_v4(row + lane * V + c);
+                        const int4 r = ld_na_v4(row + lane * V + c);
                         const uint32_t u[4] = {(uint32_t)r.x, (uint32_t)r.y, (uint32_t)r.z, (uint32_t)r.w};
                         unpack(u, 4, c);
                     }

@@ -81,17 +81,17 @@ __device__ __forceinline__ void st_global_32(void* p, const uint32_t* v) {
 }
 
 // 32 bytes from a 32-byte aligned address: a whole sector a lane, where lanes' 16 bytes would each take half of one
-// and every sector twice.  Not for memory that the kernel writes (nc), or for that too.
-__device__ __forceinline__ void ld_nc_32(const void* p, uint32_t* v) {
-    asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
-                 : "l"(p));
-}
+// and every sector twice.  Also for memory that the kernel writes later.
 __device__ __forceinline__ void ld_global_32(const void* p, uint32_t* v) {
     asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                  : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
                  : "l"(p)
                  : "memory");
+}
+__device__ __forceinline__ int4 ld_na_v4(const void* p) {
+    int4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.s32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
+    return v;
 }
 
 // Programmatic launches.  grid_wait: until the kernel before has ended and its writes are visible.  It ends

@@ -339,6 +339,41 @@ def test_rows_further_apart_than_32_bits_reach():
 
 
 @gpu
+@pytest.mark.parametrize("S,T,E,K", [(1, 20011, 256, 8), (3, 9001, 33, 4), (2, 7001, 160, 6), (5, 3333, 512, 10), (1, 9999, 1000, 3)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_more_tokens_than_one_wave(S, T, E, K, dtype):
+    """Every warp has several tokens, some of them padded; the choice against a stable sort, all else as above."""
+    g = gen(S * T)
+    logits = (randn((S, T, E), g) + randn((E,), g)).to(dtype)
+    mask = torch.rand((S, T), generator=g, device="cuda") < 0.9
+    idx, w = ep.route(logits, K, mask=mask)
+    want = torch.sort(logits.float(), dim=-1, descending=True, stable=True).indices[..., :K]
+    assert torch.equal(idx, torch.where(mask[..., None], want, -1))
+    span = span_of(scores64(logits, "softmax")[2])
+    ref = weights64(logits, idx, "softmax", True)[0]
+    assert_within(w, ref, (span + 48) * 2.0 ** -23 * ref)
+    got = ep.balance_loss(logits, idx)
+    loss, counts, F, q, used, _ = balance64(logits, idx, 1.0, "softmax")
+    assert torch.equal(got["counts"].long(), counts)
+    # a warp adds at most T / 600 tokens of a sequence (or 2 * 8 a block), then 8 warps, at most 608 blocks
+    assert_within(got["loss"][0], loss, (span.max() + T / 600 + 700) * 2.0 ** -23 * loss, "loss")
+    dw = randn((S, T, K), g)
+    one = torch.ones(1, device="cuda")
+    dl = ep.router_backward(logits, idx, dw, factors=got["factors"], dloss=one)
+    f = (F - F.mean(-1, keepdim=True))[:, None]
+    inner, mag_inner = (f * q).sum(-1, keepdim=True), (f.abs() * q).sum(-1, keepdim=True)
+    d = torch.where(idx >= 0, dw.double(), 0.0)
+    near = ref * (d - (d * ref).sum(-1, keepdim=True))
+    near_mag = ref * (d.abs() + (d.abs() * ref).sum(-1, keepdim=True))
+    at = idx.clamp(min=0)
+    want = (q * (f - inner) * used[..., None]).scatter_add(-1, at, near)
+    mag = (q * (f.abs() + mag_inner)).scatter_add(-1, at, near_mag)
+    assert_within(dl, want, HALF[dtype] * want.abs() + 4 * (span + 96) * 2.0 ** -23 * mag, "dlogits")
+    same = ep.router_backward(logits, idx, dw, factors=got["factors"], dloss=one, out=logits)
+    assert same is logits and torch.equal(same, dl)
+
+
+@gpu
 def test_no_tokens_and_in_place_gradient():
     l = torch.empty(0, 16, device="cuda")
     idx, w = ep.route(l, 4)
