@@ -265,7 +265,6 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
         RingPos<k4TileRing> tr;
         Turn<kStages> st;
         Turn<kSlots> sl;
-        uint32_t set = 0;
         while (true) {
             mbar_wait_warp<true>(tr.bar(tile_full), tr.phase(), k4WaitNs, abort);
             const int rows = sh.tile[tr.slot()].rows;
@@ -275,33 +274,44 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
             ++tr.n;
             if (rows == 0 || __any_sync(0xffffffffu, *abort)) break;
             mbar_wait_warp<true>(acc_empty + c * 8, turn ^ 1, k4WaitNs, abort);
+            // two stages, one group of scales, at a time: the waits, the choice of a lane and the commits take a stage
+            // alone 335 cycles of its 540
 #pragma unroll 1
-            for (int kt = 0; kt < a.KT; ++kt) {
-                const int g = kt & (k4Group - 1);
-                if (g == 0) mbar_wait_warp<true>(scale_full + sl.slot * 8, sl.phase, k4WaitNs, abort);
-                mbar_wait_warp<true>(full + st.slot * 8, st.phase, k4WaitNs, abort);
+            for (int kt = 0; kt < a.KT; kt += k4Group) {
+                const bool two = kt + 1 < a.KT;
+                const Turn<kStages> st0 = st;
+                st.next();
+                mbar_wait_warp<true>(scale_full + sl.slot * 8, sl.phase, k4WaitNs, abort);
+                mbar_wait_warp<true>(full + st0.slot * 8, st0.phase, k4WaitNs, abort);
+                if (two) mbar_wait_warp<true>(full + st.slot * 8, st.phase, k4WaitNs, abort);
                 tc_fence_after();
                 if (elect_one()) {
-                    const uint32_t sa = tmem + Shape::kScaleAt + set * Shape::kScaleCols, sb = sa + 8;
-                    const uint64_t ds = ds0 + sl.slot * (Shape::kSlot >> 4) + g * (kScales >> 4);
+                    const uint64_t ds = ds0 + sl.slot * (Shape::kSlot >> 4);
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) tmem_copy_scales<kCtas>(sa + h * 4, ds + h * 32);
+                    for (int g = 0; g < k4Group; ++g) {
+                        const uint32_t sa = tmem + Shape::kScaleAt + g * Shape::kScaleCols;
 #pragma unroll
-                    for (int h = 0; h < 2 * Shape::kChunks; ++h)
-                        tmem_copy_scales<kCtas>(sb + h * 4, ds + (Shape::kScalesA >> 4) + h * 32);
-                    const uint32_t at = st.slot * (kCodes >> 4);
+                        for (int h = 0; h < 2 + 2 * Shape::kChunks; ++h)  // the rows' two, then the weights', as they lie
+                            tmem_copy_scales<kCtas>(sa + h * 4, ds + g * (kScales >> 4) + h * 32);
+                    }
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        mma_mxf4<kCtas>(tmem + c * kBN, da0 + at + k * 2, db0 + at + k * 2, k & 1 ? idesc2 : idesc0, sa + (k >> 1) * 4,
-                                 sb + (k >> 1) * 4 * Shape::kChunks, kt > 0 || k > 0);
-                    mma_commit<kCtas>(done + st.slot * 8);
-                    if (g == k4Group - 1 || kt == a.KT - 1) mma_commit<kCtas>(scale_empty + sl.slot * 8);
-                    if (kt == a.KT - 1) mma_commit<kCtas>(acc_full + c * 8);
+                    for (int g = 0; g < k4Group; ++g) {
+                        if (g == 1 && !two) break;
+                        const uint32_t sa = tmem + Shape::kScaleAt + g * Shape::kScaleCols, sb = sa + 8;
+                        const int slot = g ? st.slot : st0.slot;
+                        const uint32_t at = slot * (kCodes >> 4);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            mma_mxf4<kCtas>(tmem + c * kBN, da0 + at + k * 2, db0 + at + k * 2, k & 1 ? idesc2 : idesc0, sa + (k >> 1) * 4,
+                                            sb + (k >> 1) * 4 * Shape::kChunks, kt > 0 || g > 0 || k > 0);
+                        mma_commit<kCtas>(done + slot * 8);
+                    }
+                    mma_commit<kCtas>(scale_empty + sl.slot * 8);
+                    if (kt + k4Group >= a.KT) mma_commit<kCtas>(acc_full + c * 8);
                 }
                 __syncwarp();
-                st.next();
-                if (g == k4Group - 1 || kt == a.KT - 1) sl.next();
-                set ^= 1;
+                if (two) st.next();
+                sl.next();
             }
         }
         // every product has finished before either block frees its tensor memory: the second waits for this one below
