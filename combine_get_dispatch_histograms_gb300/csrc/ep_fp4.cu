@@ -18,6 +18,7 @@
 // rows, 56 KB a stage and SM: first product, 40 groups of 2048 rows, 941 us by one block, 755 by pairs (6.4 PFLOP/s).
 // A fifth stage, or weights fetched ahead into the second-level cache, change nothing.
 #include <atomic>
+#include <initializer_list>
 
 #include "ep_fp4.cuh"
 #include "ep_groups.cuh"
@@ -29,6 +30,7 @@ constexpr int k4BK = 256;         // codes of K a stage: 128 bytes a row
 constexpr int k4BoxRows = 32;     // rows of one copy of x
 constexpr int k4ScaleWarps = 4, k4OutWarps = 4;
 constexpr int k4Threads = 128 + 32 * (k4ScaleWarps + k4OutWarps);
+constexpr int kSplitRow = 64 + 4;  // floats of a row of sums: rows fall into other banks
 constexpr int k4TileRing = 4;
 constexpr int k4Group = 2;        // stages whose scales are staged together
 constexpr int64_t k4WaitNs = 2000000000ll;
@@ -95,7 +97,7 @@ struct Scales32 {
 };
 __device__ __forceinline__ Scales32 load_scales(const uint8_t* row, int at, int bytes, int vec) {
     Scales32 s;
-    if (vec == 32 && at + 32 <= bytes) {
+    if (vec == 32 && at % 32 == 0 && at + 32 <= bytes) {
         asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                      : "=r"(s.v[0]), "=r"(s.v[1]), "=r"(s.v[2]), "=r"(s.v[3]), "=r"(s.v[4]), "=r"(s.v[5]), "=r"(s.v[6]), "=r"(s.v[7])
                      : "l"(row + at));
@@ -115,7 +117,10 @@ __device__ __forceinline__ Scales32 load_scales(const uint8_t* row, int at, int 
 }
 
 // kSwiglu: half of the tile's weight rows are gate rows, half the up rows of the same channels.
-template <bool kSwiglu, int kBN, int kCtas>
+// kSplit (kBN = 64, one block): the blocks of a cluster make one tile, each from its share of the stages, two by two.  For
+// launches with fewer tiles than SMs: a block alone brings in some 45 GB/s from memory, whatever it has under way.  Every
+// cluster has at most one tile.
+template <bool kSwiglu, int kBN, int kCtas, bool kSplit>
 __global__ void __launch_bounds__(k4Threads, 1)
 fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_box,
                 const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_out, const Fp4Args a) {
@@ -128,7 +133,11 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
     uint8_t* scales = codes + kStages * kCodes;
     uint8_t* out_stage = scales + kSlots * Shape::kSlot;  // on 1024 bytes too
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int rank = kCtas == 2 ? (int)cluster_rank() : 0, unit = blockIdx.x / kCtas, units = gridDim.x / kCtas;
+    const int rank = kCtas == 2 ? (int)cluster_rank() : 0;
+    const int part = kSplit ? (int)cluster_rank() : 0, parts = kSplit ? cluster_size() : 1;
+    const int unit = blockIdx.x / (kCtas * parts), units = gridDim.x / (kCtas * parts);
+    const int pairs = (a.KT + k4Group - 1) / k4Group;
+    const int kt0 = kSplit ? part * pairs / parts * k4Group : 0, kt1 = kSplit ? min((part + 1) * pairs / parts * k4Group, a.KT) : a.KT;
     volatile int* abort = &sh.abort;
     const uint32_t full = smem_u32(sh.full), done = smem_u32(sh.done);
     const uint32_t scale_full = smem_u32(sh.scale_full), scale_empty = smem_u32(sh.scale_empty);
@@ -210,7 +219,7 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
                 // the first block of a pair has the gate rows, or the first half, the second the others
                 const int first = kSwiglu ? tile.n * kHalf : tile.n * kBN, second = kSwiglu ? a.N / 2 + first : first + kHalf;
                 const int w0 = rank ? second : first;
-                for (int kt = 0; kt < a.KT; ++kt) {
+                for (int kt = kt0; kt < kt1; ++kt) {
                     if (!mbar_wait_or_abort<true>(done + st.slot * 8, st.phase ^ 1, k4WaitNs, abort)) {
                         ok = false;
                         break;
@@ -277,8 +286,8 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
             // two stages, one group of scales, at a time: the waits, the choice of a lane and the commits take a stage
             // alone 335 cycles of its 540
 #pragma unroll 1
-            for (int kt = 0; kt < a.KT; kt += k4Group) {
-                const bool two = kt + 1 < a.KT;
+            for (int kt = kt0; kt < kt1; kt += k4Group) {
+                const bool two = kt + 1 < kt1;
                 const Turn<kStages> st0 = st;
                 st.next();
                 mbar_wait_warp<true>(scale_full + sl.slot * 8, sl.phase, k4WaitNs, abort);
@@ -303,11 +312,11 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
                             mma_mxf4<kCtas>(tmem + c * kBN, da0 + at + k * 2, db0 + at + k * 2, k & 1 ? idesc2 : idesc0, sa + (k >> 1) * 4,
-                                            sb + (k >> 1) * 4 * Shape::kChunks, kt > 0 || g > 0 || k > 0);
+                                            sb + (k >> 1) * 4 * Shape::kChunks, kt > kt0 || g > 0 || k > 0);
                         mma_commit<kCtas>(done + slot * 8);
                     }
                     mma_commit<kCtas>(scale_empty + sl.slot * 8);
-                    if (kt + k4Group >= a.KT) mma_commit<kCtas>(acc_full + c * 8);
+                    if (kt + k4Group >= kt1) mma_commit<kCtas>(acc_full + c * 8);
                 }
                 __syncwarp();
                 if (two) st.next();
@@ -353,14 +362,14 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
                 if (Shape::kChunks > 1 && p1) v1[i] = load_scales(p1, at, bytes, a.w_vec);
             };
 #pragma unroll
-            for (int i = 0; i < kAhead; ++i) fetch(i, i * 32);
+            for (int i = 0; i < kAhead; ++i) fetch(i, kt0 * 8 + i * 32);
 #pragma unroll 1
-            for (int kt = 0; kt < a.KT; kt += 4 * kAhead) {
+            for (int kt = kt0; kt < kt1; kt += 4 * kAhead) {
 #pragma unroll
                 for (int i = 0; i < kAhead; ++i) {
 #pragma unroll
                     for (int j = 0; j < 4; j += k4Group) {
-                        if (kt + 4 * i + j >= a.KT) break;
+                        if (kt + 4 * i + j >= kt1) break;
                         mbar_wait_warp<true>(scale_empty + sl.slot * 8, sl.phase ^ 1, k4WaitNs, abort);
                         uint8_t* d = scales + sl.slot * Shape::kSlot + to;
 #pragma unroll
@@ -380,7 +389,7 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
                         if (lane == 0) mbar_arrive(scale_full + sl.slot * 8);
                         sl.next();
                     }
-                    fetch(i, (kt / 4 + kAhead + i) * 32);
+                    fetch(i, kt * 8 + (kAhead + i) * 32);
                 }
             }
         }
@@ -402,7 +411,18 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
             const int first = rank * k4BM + (warp & 3) * 32, rows = min(32, tile.rows - first);  // of this warp
             if (rows > 0) {
                 const int64_t row0 = tile.row0 + first;
-                if constexpr (kSwiglu) {
+                if constexpr (kSplit) {
+                    // the ring is idle now: the block's sums wait there for the cluster's
+                    float* d = reinterpret_cast<float*>(codes) + (first + lane) * kSplitRow;
+#pragma unroll
+                    for (int q = 0; q < kBN / 32; ++q) {
+                        float v[32];
+                        tmem_ld(lanes + c * kBN + q * 32, v);
+                        tmem_wait_ld(v);
+#pragma unroll
+                        for (int i = 0; i < 32; i += 4) *reinterpret_cast<float4*>(d + q * 32 + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+                    }
+                } else if constexpr (kSwiglu) {
                     for (int q = 0; q < kHalf / 32; ++q) {
                         const int ch = tile.n * kHalf + q * 32;
                         if (ch >= a.N / 2) break;
@@ -484,6 +504,53 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
             if (lane == 0) mbar_hand_back(free_bar + c * 8);
         }
         bulk_wait_all();
+        if constexpr (kSplit) {
+            // rows part, part + parts, ..., a warp each: the blocks' sums in block order
+            __syncwarp();
+            cluster_sync();
+            const GemmTile tile = sh.tile[0];
+            const bool some = tr.n > 0 && tile.rows > 0 && !*abort;
+            for (int r = part + parts * (warp & 3); some && r < tile.rows; r += parts * k4OutWarps) {
+                const uint32_t at = smem_u32(codes) + r * kSplitRow * 4;
+                const int64_t row = tile.row0 + r;
+                float2 v = make_float2(0.0f, 0.0f);
+                if constexpr (kSwiglu) {  // gate and up of one channel a lane: a block of 32 a row
+                    for (int b = 0; b < parts; ++b) {
+                        v.x += ld_cluster_f32(smem_of(at + lane * 4, b));
+                        v.y += ld_cluster_f32(smem_of(at + (kHalf + lane) * 4, b));
+                    }
+                    const float h = silu_mul(v.x, v.y);
+                    float m = fabsf(h);
+#pragma unroll
+                    for (int o = 16; o; o >>= 1) m = max_or_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+                    const uint32_t b = e8m0_of(m);
+                    const float mate = __shfl_down_sync(0xffffffffu, h, 1), by = e8m0_inverse(b);
+                    if (lane % 2 == 0)
+                        static_cast<uint8_t*>(a.out)[row * a.out_stride + tile.n * (kHalf / 2) + lane / 2] =
+                            (uint8_t)__nv_cvt_float2_to_fp4x2(make_float2(h * by, mate * by), __NV_E2M1, cudaRoundNearest);
+                    if (lane == 0) a.out_scales[row * a.out_sstride + tile.n] = (uint8_t)b;
+                } else {
+                    for (int b = 0; b < parts; ++b) {
+                        const float2 w = ld_cluster_f32x2(smem_of(at + lane * 8, b));
+                        v.x += w.x;
+                        v.y += w.y;
+                    }
+                    const int n = tile.n * kBN + lane * 2;
+                    __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.out) + row * a.out_stride + n;
+                    if (a.out_vec && n + 2 <= a.N) {
+                        *reinterpret_cast<__nv_bfloat162*>(o) = __floats2bfloat162_rn(v.x, v.y);
+                    } else {
+                        if (n < a.N) o[0] = __float2bfloat16_rn(v.x);
+                        if (n + 1 < a.N) o[1] = __float2bfloat16_rn(v.y);
+                    }
+                }
+            }
+        }
+    }
+    if constexpr (kSplit) {
+        __syncwarp();
+        if (warp < 4 + k4ScaleWarps) cluster_sync();
+        cluster_sync();  // no block ends while another reads its sums
     }
     __syncwarp();
     tc_fence_before();
@@ -554,8 +621,8 @@ static ep_status check_fp4(const char* fn, const ep_fp4_rows* x, const ep_row_gr
     return EP_OK;
 }
 
-template <bool kSwiglu, int kBN, int kCtas>
-static ep_status launch_fp4_shape(const char* fn, const ep_fp4_rows* x, const ep_fp4_weight* w, Fp4Args a, int sms, int dev, void* stream) {
+template <bool kSwiglu, int kBN, int kCtas, bool kSplit>
+static ep_status launch_fp4_shape(const char* fn, const ep_fp4_rows* x, const ep_fp4_weight* w, Fp4Args a, int sms, int cluster, int dev, void* stream) {
     using Shape = Fp4Shape<kSwiglu, kBN, kCtas>;
     constexpr int kTileN = kSwiglu ? kBN / 2 : kBN;
     a.n_tiles = ((kSwiglu ? w->n / 2 : w->n) + kTileN - 1) / kTileN;
@@ -585,11 +652,20 @@ static ep_status launch_fp4_shape(const char* fn, const ep_fp4_rows* x, const ep
     }
     static std::atomic<bool> known[kMaxDevicesTracked];  // devices whose launch attribute is set
     if (dev >= kMaxDevicesTracked || !known[dev].load(std::memory_order_relaxed)) {
-        EP_CUDA(cudaFuncSetAttribute(fp4_gemm_kernel<kSwiglu, kBN, kCtas>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Shape::kSmem));
+        EP_CUDA(cudaFuncSetAttribute(fp4_gemm_kernel<kSwiglu, kBN, kCtas, kSplit>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Shape::kSmem));
         if (dev < kMaxDevicesTracked) known[dev].store(true, std::memory_order_relaxed);
     }
-    const int64_t units = most < sms / kCtas ? most : sms / kCtas;
-    return launch_next(fp4_gemm_kernel<kSwiglu, kBN, kCtas>, units * kCtas, k4Threads, stream, Shared{Shape::kSmem, kCtas}, map_x, map_box, map_w, map_out, a);
+    const int64_t units = most < sms / cluster ? most : sms / cluster;
+    return launch_next(fp4_gemm_kernel<kSwiglu, kBN, kCtas, kSplit>, units * cluster, k4Threads, stream, Shared{Shape::kSmem, cluster}, map_x, map_box, map_w, map_out, a);
+}
+
+// Blocks that share a tile's K where the tiles are few: each four stages or more, and no more blocks than SMs (clusters of
+// 8 leave some SMs of a group of SMs without one).
+static int fp4_split(int64_t tiles, int stages, int sms) {
+    struct Rule { int split, percent; };  // share of the SMs
+    for (const Rule r : {Rule{8, 66}, {4, 100}, {2, 100}})
+        if (stages >= r.split * 2 * k4Group && tiles * r.split * 100 <= (int64_t)sms * r.percent) return r.split;
+    return 1;
 }
 
 // Whether pairs of blocks make the first product's tiles: one of theirs costs 1.65 of one block's, and has twice the rows.
@@ -621,14 +697,19 @@ static ep_status launch_fp4(const char* fn, const ep_fp4_rows* x, const ep_row_g
     EP_CUDA(cudaGetDevice(&dev));
     EP_CUDA(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
     a.n_tiles = (w->n + 191) / 192;
-    if (most_tiles(a, k4BM) * 2 <= sms) return launch_fp4_shape<kSwiglu, 64, 1>(fn, x, w, a, sms, dev, stream);
+    if (most_tiles(a, k4BM) * 2 <= sms) {
+        a.n_tiles = (w->n + 63) / 64;
+        const int split = fp4_split(most_tiles(a, k4BM), a.KT, sms);
+        if (split > 1) return launch_fp4_shape<kSwiglu, 64, 1, true>(fn, x, w, a, sms, split, dev, stream);
+        return launch_fp4_shape<kSwiglu, 64, 1, false>(fn, x, w, a, sms, 1, dev, stream);
+    }
     if constexpr (kSwiglu) {
         // Rows of a group: as the caller expects, or what the arrays hold, shared out; regions with counts are sized for the
         // worst case, and a low-latency step fills a few percent of them.
         const int64_t rows = g->expected > 0 ? g->expected : x->rows / w->groups / (w->groups > 1 && !g->offsets && g->counts ? 16 : 1);
-        if (fp4_by_pairs(rows)) return launch_fp4_shape<kSwiglu, 192, 2>(fn, x, w, a, sms, dev, stream);
+        if (fp4_by_pairs(rows)) return launch_fp4_shape<kSwiglu, 192, 2, false>(fn, x, w, a, sms, 2, dev, stream);
     }
-    return launch_fp4_shape<kSwiglu, 192, 1>(fn, x, w, a, sms, dev, stream);
+    return launch_fp4_shape<kSwiglu, 192, 1, false>(fn, x, w, a, sms, 1, dev, stream);
 }
 
 }  // namespace ep
