@@ -43,6 +43,7 @@ struct RouterArgs {
     int64_t stride;
     uint32_t tokens;  // below 2^31, so that a step past them stays within 32 bits
     int E, K, groups, topk_groups;
+    int group_size, lanes_log;  // lanes_log: a group is 1 << lanes_log whole lanes; -1: it is not
     bool normalize;
     int vec;
     float scale;
@@ -165,35 +166,38 @@ __device__ __forceinline__ void scores(const float (&l)[V], float (&p)[V], float
 }
 
 // Whether this lane's group stays; a group's score is the sum of its two largest keys.  Lanes that hold whole parts of
-// groups (V divides the group, a power of two of lanes each): the lanes' two largest are merged, and a group's rank is the
-// number of groups before it.
+// groups (V divides the group, a power of two of lanes each): the lanes' two largest are merged.
 template <int V>
-__device__ __forceinline__ bool keep_group(const uint32_t (&key)[V], const RouterArgs& a, int lane, int lanes) {
+__device__ __forceinline__ bool keep_group(const uint32_t (&key)[V], const RouterArgs& a, int lane) {
     uint32_t hi = key[0], lo = 0;
 #pragma unroll
     for (int i = 1; i < V; ++i) {
         lo = max(lo, min(hi, key[i]));
         hi = max(hi, key[i]);
     }
-    for (int o = 1; o < lanes; o <<= 1) {
+    for (int o = 1; o < 1 << a.lanes_log; o <<= 1) {
         const uint32_t h = __shfl_xor_sync(kAll, hi, o), l = __shfl_xor_sync(kAll, lo, o);
         lo = max(max(lo, l), min(hi, h));
         hi = max(hi, h);
     }
-    const uint32_t score = V * lanes > 1 ? ordered(unordered(hi) + unordered(lo)) : hi;
-    const int mine = lane / lanes;
-    int before = 0;
-#pragma unroll 4
-    for (int g = 0; g < a.groups; ++g) {
-        const uint32_t other = __shfl_sync(kAll, score, g * lanes);
-        before += other > score || (other == score && g < mine);
+    const uint32_t score = a.group_size > 1 ? ordered(unordered(hi) + unordered(lo)) : hi;
+    // lane g: group g's score, taken out as it is chosen
+    uint32_t left = __shfl_sync(kAll, score, lane << a.lanes_log & 31);
+    if (lane >= a.groups) left = 0;
+    bool taken = false;
+    for (int i = 0; i < a.topk_groups; ++i) {
+        const uint32_t most = __reduce_max_sync(kAll, left);
+        if (lane == __ffs(__ballot_sync(kAll, left == most)) - 1) {
+            left = 0;
+            taken = true;
+        }
     }
-    return before < a.topk_groups;
+    return __ballot_sync(kAll, taken) >> (lane >> a.lanes_log) & 1;
 }
 // Any other groups, one after the other: bit g of the result.
 template <int V>
 __device__ __forceinline__ uint32_t choose_groups(const uint32_t (&key)[V], const RouterArgs& a, int lane) {
-    const int size = a.E / a.groups;
+    const int size = a.group_size;
     uint32_t score = 0;  // lane g: group g's
     for (int g = 0; g < a.groups; ++g) {
         uint32_t hi = 0, lo = 0;
@@ -247,7 +251,8 @@ __device__ __forceinline__ int choose_one_by_one(uint32_t (&key)[V], int K, int 
 
 // Choice k's expert, in lane k: the K-th largest of the lanes' best keys bounds the K-th largest key from below, so that
 // the keys from there on, mostly K and a few, are all that has to be ranked: they are listed, a lane each, and a
-// candidate's rank is the number of larger ones.  Equal candidates show as two that want the same place; then the lower
+// candidate's rank is the number of larger ones (a looser bound in fewer steps, the least of the best of 8 runs of lanes,
+// leaves 17 of them and takes 31 us for 29).  Equal candidates show as two that want the same place; then the lower
 // experts among them count as larger.  Where there are more than 32, the choices are made one by one.
 struct RouteList {
     uint32_t key[32];
@@ -314,8 +319,6 @@ __global__ void __launch_bounds__(kRouterThreads, kPerSm<V>) route_kernel(const 
     const int lane = threadIdx.x & 31;
     grid_wait();
     grid_launch_next();
-    const int size = kGroups ? a.E / a.groups : 0;
-    const bool whole = size && size % V == 0 && (size / V & (size / V - 1)) == 0;
     float bias[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) bias[i] = a.bias && lane * V + i < a.E ? a.bias[lane * V + i] : 0.0f;
@@ -334,15 +337,15 @@ __global__ void __launch_bounds__(kRouterThreads, kPerSm<V>) route_kernel(const 
 #pragma unroll
         for (int i = 0; i < V; ++i) key[i] = ordered(l[i] + bias[i]);  // -inf stays past the last expert
         if (kGroups) {
-            if (whole) {
-                if (!keep_group(key, a, lane, size / V))
+            if (a.lanes_log >= 0) {
+                if (!keep_group(key, a, lane))
 #pragma unroll
                     for (int i = 0; i < V; ++i) key[i] = 0;
             } else {
                 const uint32_t kept = choose_groups(key, a, lane);
 #pragma unroll
                 for (int i = 0; i < V; ++i)
-                    if (!(kept >> min((lane * V + i) / max(size, 1), 31) & 1)) key[i] = 0;
+                    if (!(kept >> min((lane * V + i) / a.group_size, 31) & 1)) key[i] = 0;
             }
         }
         const int expert = choose(key, a.K, lane, lists[threadIdx.x >> 5]);
@@ -797,7 +800,12 @@ extern "C" ep_status ep_route(const ep_router* r, const void* logits, int64_t lo
         return set_error(EP_ERR_INVALID_ARG, "%s: topk_idx, topk_weights and bias aligned to their elements", fn);
     int64_t blocks = 0;
     EP_TRY(router_blocks(r, blocks_per_sm(r->experts), &blocks));
-    const RouterArgs a = {logits, logits_stride, (uint32_t)r->tokens, r->experts, r->topk, r->groups, r->topk_groups, r->normalize != 0,
+    int held = 1, lanes_log = -1;  // experts a lane holds, as EP_BY_WARPS
+    while (32 * held < r->experts) held *= 2;
+    const int size = r->experts / r->groups;
+    if (size % held == 0 && (size / held & (size / held - 1)) == 0)
+        for (lanes_log = 0; held << lanes_log < size;) ++lanes_log;
+    const RouterArgs a = {logits, logits_stride, (uint32_t)r->tokens, r->experts, r->topk, r->groups, r->topk_groups, size, lanes_log, r->normalize != 0,
                           by_vectors(r->experts, r->logits_type, logits, logits_stride), r->scale, bias, mask, topk_idx, topk_weights};
     return launch_next(r->topk_groups < r->groups ? EP_ROUTER_KERNEL(route_groups, r) : EP_ROUTER_KERNEL(route_all, r), blocks, kRouterThreads, stream, a);
 }
