@@ -600,6 +600,24 @@ __device__ __forceinline__ void add_shared(const float* p, float (&d)[V]) {
     }
 }
 
+// This lane's V factors; 0 past the last expert.  Cached: a sequence's tokens share them.
+template <int V>
+__device__ __forceinline__ void load_factors(const float* row, int E, int lane, int vec, float (&f)[V]) {
+    if constexpr (V % 4 == 0) {
+        if (vec >= 16) {
+#pragma unroll
+            for (int i = 0; i < V; i += 4) {
+                const int e = lane * V + i;
+                const float4 v = e < E ? __ldg(reinterpret_cast<const float4*>(row + e)) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                f[i] = v.x, f[i + 1] = v.y, f[i + 2] = v.z, f[i + 3] = v.w;
+            }
+            return;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) f[i] = lane * V + i < E ? __ldg(row + lane * V + i) : 0.0f;
+}
+
 template <typename T, int V, bool kSigmoid>
 __global__ void __launch_bounds__(kRouterThreads, V <= 8 ? 4 : kPerSm<V>) router_backward_kernel(const RouterBackArgs a) {
     __shared__ __align__(16) float rows[kRouterWarps][32 * V];
@@ -659,12 +677,9 @@ __global__ void __launch_bounds__(kRouterThreads, V <= 8 ? 4 : kPerSm<V>) router
             scores<V, kSigmoid>(l, p, slope, &top, &by);
             if (a.factors) {
                 float fv[V], sum = 0.0f;
-                load_logits(a.factors + (int64_t)(t / a.T) * a.E, a.E, lane, a.fvec, fv);
+                load_factors(a.factors + (int64_t)(t / a.T) * a.E, a.E, lane, a.fvec, fv);
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    if (lane * V + i >= a.E) fv[i] = 0.0f;
-                    sum = fmaf(fv[i], p[i], sum);
-                }
+                for (int i = 0; i < V; ++i) sum = fmaf(fv[i], p[i], sum);
                 sum = warp_sum(sum) * (kSigmoid ? by : 1.0f);
 #pragma unroll
                 for (int i = 0; i < V; ++i) d[i] = dloss * (fv[i] - sum) * (kSigmoid ? slope[i] * by : p[i]);
