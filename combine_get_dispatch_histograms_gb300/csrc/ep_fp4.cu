@@ -15,8 +15,9 @@
 // Bound.  Up to 128 rows a group the weights' bytes: 256 groups of about 64 rows, K 7168, 2I 4096 594 us, K 2048, N 7168
 // 325 us, 6.7 TB/s.  With long groups shared memory: a stage's codes are written to it and read from it once, 82 KB at
 // 128 bytes a cycle = 640 cycles, and a stage takes 650 (the products some 370).  Pairs of blocks share the weight's
-// rows, 56 KB a stage and SM: first product, 40 groups of 2048 rows, 941 us by one block, 755 by pairs (6.4 PFLOP/s).
-// A fifth stage, or weights fetched ahead into the second-level cache, change nothing.
+// rows, 56 KB a stage and SM: first product, 40 groups of 2048 rows, 914 us by one block, 737 by pairs (6.5 PFLOP/s).
+// A fifth stage changes nothing, weights fetched ahead into the second-level cache cost time.  With few tiles, what one
+// SM brings in from memory: one row, K 7168, N 4096 11.2 us by 64 blocks, 8.3 by 128 in clusters of two.
 #include <atomic>
 #include <initializer_list>
 
@@ -283,8 +284,7 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
             ++tr.n;
             if (rows == 0 || __any_sync(0xffffffffu, *abort)) break;
             mbar_wait_warp<true>(acc_empty + c * 8, turn ^ 1, k4WaitNs, abort);
-            // two stages, one group of scales, at a time: the waits, the choice of a lane and the commits take a stage
-            // alone 335 cycles of its 540
+            // two stages, one group of scales, at a time (one: pairs, 2048 rows a group 755 us for 737)
 #pragma unroll 1
             for (int kt = kt0; kt < kt1; kt += k4Group) {
                 const bool two = kt + 1 < kt1;
@@ -669,8 +669,8 @@ static int fp4_split(int64_t tiles, int stages, int sms) {
 }
 
 // Whether pairs of blocks make the first product's tiles: one of theirs costs 1.65 of one block's, and has twice the rows.
-// 40 groups, K 7168, 2I 4096, us by one block / by pairs: 256 rows a group 136 / 127, 448 242 / 206, 640 295 / 290, 768 355 /
-// 302, 1024 481 / 397, 2048 941 / 755; but 256 groups of 256 rows on average, popular and unpopular, 1020 / 1075: half a
+// 40 groups, K 7168, 2I 4096, us by one block / by pairs: 256 rows a group 135 / 128, 448 238 / 204, 640 297 / 285, 768 371 /
+// 296, 1024 460 / 386, 2048 914 / 737; but 256 groups of 256 rows on average, popular and unpopular, 1020 / 1075: half a
 // tile of each group is empty on average.  (The second product, whose results are its larger part, gains 3 % at best:
 // 2048 rows 537 / 515.)
 static bool fp4_by_pairs(int64_t rows) { return rows > 3 * k4BM; }
