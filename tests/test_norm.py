@@ -154,6 +154,22 @@ def test_no_rows():
 
 
 @gpu
+@pytest.mark.parametrize("rows,H", [(300, 256), (500, 2048), (3, 16384)])
+def test_given_workspaces(rows, H):
+    x, _, w, g = make(rows, H, None, BF, 14)
+    dy = randn((rows, H), g).to(BF)
+    want = ep.rms_norm_backward(dy, x, w)
+    ws = torch.full((ep.rms_norm_backward_workspace(rows, H),), 255, dtype=torch.uint8, device="cuda")   # NaN, if it were read
+    for _ in range(2):
+        got = ep.rms_norm_backward(dy, x, w, workspace=ws)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    with pytest.raises(ep.EpError):
+        ep.rms_norm_backward(dy, x, w, workspace=ws[:-16])
+    with pytest.raises(ValueError):
+        ep.rms_norm_backward(dy, x, w, workspace=ws[::2])
+
+
+@gpu
 def test_zeros_nan_and_infinity_stay_in_their_rows():
     rows, H = 5, 384
     x, _, w, _ = make(rows, H, None, F32, 8)

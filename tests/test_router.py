@@ -300,6 +300,49 @@ def test_same_expert_twice_padding_and_empty_sequences():
 
 
 @gpu
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+def test_padding_may_hold_anything_and_closed_experts_get_nothing(scoring):
+    S, T, E, K = 3, 50, 40, 4
+    logits = randn((S, T, E), gen(21))
+    logits[..., [3, 17, 39]] = -INF                             # closed
+    logits[..., 5] = torch.finfo(F32).min
+    mask = torch.rand((S, T), generator=gen(22), device="cuda") < 0.7
+    clean = ep.route(logits, K, mask=mask, scoring=scoring)
+    dw = randn((S, T, K), gen(23))
+    one = torch.ones(1, device="cuda")
+
+    def step(l, d):
+        idx, w = ep.route(l, K, mask=mask, scoring=scoring)
+        bal = ep.balance_loss(l, idx, scoring=scoring)
+        return idx, w, bal["loss"], bal["counts"], ep.router_backward(l, idx, d, factors=bal["factors"], dloss=one, scoring=scoring)
+    want = step(logits, dw)
+    assert torch.equal(want[0], clean[0]) and not torch.isin(want[0], torch.tensor([3, 17, 39], device="cuda")).any()
+    assert torch.isfinite(want[2]).all() and torch.isfinite(want[4]).all()
+    assert (want[4][..., [3, 17, 39]] == 0).all() and (want[4][~mask] == 0).all() and (want[3][:, [3, 17, 39]] == 0).all()
+    dirty, d = logits.clone(), dw.clone()
+    dirty[~mask] = float("nan")
+    dirty[0, ~mask[0]] = INF
+    d[~mask] = float("nan")
+    assert all(torch.equal(a, b) for a, b in zip(step(dirty, d), want))
+
+
+@gpu
+def test_given_outputs_and_workspaces():
+    l = randn((3, 40, 24), gen(24))
+    idx, _ = ep.route(l, 2)
+    want = ep.balance_loss(l, idx, 0.3)
+    out = {k: torch.full_like(v, 9) for k, v in want.items()}
+    ws = torch.full((ep.balance_loss_workspace(120, 24, 3),), 255, dtype=torch.uint8, device="cuda")
+    for _ in range(2):
+        got = ep.balance_loss(l, idx, 0.3, out=out, workspace=ws)
+        assert all(got[k] is out[k] and torch.equal(got[k], want[k]) for k in want)
+    with pytest.raises(ep.EpError):
+        ep.balance_loss(l, idx, workspace=ws[:-16])
+    with pytest.raises(ValueError):
+        ep.balance_loss(l, idx, out=out | {"counts": out["loss"]})
+
+
+@gpu
 def test_entries_out_of_range_are_skipped_and_reported():
     logits = randn((6, 8), gen(7))
     idx = torch.zeros(6, 2, device="cuda", dtype=torch.int64)
