@@ -92,14 +92,16 @@ struct Turn {
     }
 };
 
-// 32 bytes of scales, four stages', from byte `at` of a row with `bytes` of them (a multiple of 4); 0 past its end.
+// 32 bytes of scales, four stages', from byte `at` of a row with `bytes` of them (a multiple of 4); 0 past its end.  Plain
+// loads, since the kernel before may still write them when this one is launched; by the first-level cache (past it: 256
+// groups of about 64 rows, first product 603 us for 599).
 struct Scales32 {
     uint32_t v[8];
 };
 __device__ __forceinline__ Scales32 load_scales(const uint8_t* row, int at, int bytes, int vec) {
     Scales32 s;
     if (vec == 32 && at % 32 == 0 && at + 32 <= bytes) {
-        asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+        asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                      : "=r"(s.v[0]), "=r"(s.v[1]), "=r"(s.v[2]), "=r"(s.v[3]), "=r"(s.v[4]), "=r"(s.v[5]), "=r"(s.v[6]), "=r"(s.v[7])
                      : "l"(row + at));
         return s;
@@ -576,7 +578,7 @@ __global__ void __launch_bounds__(256) quantize_fp4_kernel(const __nv_bfloat16* 
         const int at = (int)(i - row * per_row);
         float v[8] = {}, m = 0.0f;
         if (i < total) {
-            const int4 p = ld_nc_na_v4(x + row * x_stride + at * 8);
+            const int4 p = ld_na_v4(x + row * x_stride + at * 8);
             const uint32_t u[4] = {(uint32_t)p.x, (uint32_t)p.y, (uint32_t)p.z, (uint32_t)p.w};
 #pragma unroll
             for (int j = 0; j < 4; ++j) {

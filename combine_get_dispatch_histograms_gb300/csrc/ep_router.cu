@@ -134,8 +134,8 @@ __device__ __forceinline__ float sigmoid_of(float l, float* slope) {
     return l < 0.0f ? e * r : r;  // a NaN stays one: r
 }
 
-// The scores of a row (-inf past the last expert gives 0): softmax, with *top the largest logit and *by 1 / sum of e^(l - top); or sigmoid and its
-// slope, with *by 1 / its sum (0 for a sum of 0).
+// The scores of a row (-inf past the last expert gives 0): softmax, with *top the largest logit and *by 1 / sum of
+// e^(l - top); or sigmoid and its slope, with *by 1 / its sum (0 for a sum of 0).
 template <int V, bool kSigmoid>
 __device__ __forceinline__ void scores(const float (&l)[V], float (&p)[V], float (&slope)[V], float* top, float* by) {
     if constexpr (kSigmoid) {
@@ -600,7 +600,8 @@ __device__ __forceinline__ void add_shared(const float* p, float (&d)[V]) {
     }
 }
 
-// This lane's V factors; 0 past the last expert.  Cached: a sequence's tokens share them.
+// This lane's V factors; 0 past the last expert.  Cached: a sequence's tokens share them.  Plain loads: the kernel before
+// may still write them when this one is launched.
 template <int V>
 __device__ __forceinline__ void load_factors(const float* row, int E, int lane, int vec, float (&f)[V]) {
     if constexpr (V % 4 == 0) {
@@ -608,14 +609,14 @@ __device__ __forceinline__ void load_factors(const float* row, int E, int lane, 
 #pragma unroll
             for (int i = 0; i < V; i += 4) {
                 const int e = lane * V + i;
-                const float4 v = e < E ? __ldg(reinterpret_cast<const float4*>(row + e)) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                const float4 v = e < E ? *reinterpret_cast<const float4*>(row + e) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                 f[i] = v.x, f[i + 1] = v.y, f[i + 2] = v.z, f[i + 3] = v.w;
             }
             return;
         }
     }
 #pragma unroll
-    for (int i = 0; i < V; ++i) f[i] = lane * V + i < E ? __ldg(row + lane * V + i) : 0.0f;
+    for (int i = 0; i < V; ++i) f[i] = lane * V + i < E ? row[lane * V + i] : 0.0f;
 }
 
 template <typename T, int V, bool kSigmoid>
@@ -815,7 +816,7 @@ extern "C" ep_status ep_route(const ep_router* r, const void* logits, int64_t lo
         return set_error(EP_ERR_INVALID_ARG, "%s: topk_idx, topk_weights and bias aligned to their elements", fn);
     int64_t blocks = 0;
     EP_TRY(router_blocks(r, blocks_per_sm(r->experts), &blocks));
-    int held = 1, lanes_log = -1;  // experts a lane holds, as EP_BY_WARPS
+    int held = 1, lanes_log = -1;  // experts a lane holds, as EP_BY_EXPERTS
     while (32 * held < r->experts) held *= 2;
     const int size = r->experts / r->groups;
     if (size % held == 0 && (size / held & (size / held - 1)) == 0)

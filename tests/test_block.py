@@ -106,6 +106,59 @@ def test_a_training_steps_gradients(scoring, normalize):
         assert float((a.double() - b).norm() / b.norm()) < 2.0 ** -5
 
 
+@gpu
+def test_steps_that_share_buffers_without_waits():
+    """Launches overlap: a step rewrites what the step before has just read, and reads what its own last kernel wrote."""
+    S, T, E, K, H, I = 2, 200, 64, 4, 512, 256
+    g = gen(31)
+    steps = range(9)
+    xs = [randn((S * T, H), g).to(BF) * 2.0 ** (i - 4) for i in steps]  # scales differ from step to step
+    wn, wr = 1 + 0.1 * randn((H,), g), randn((E, H), g) * H ** -0.5
+    logits = [(x.float() @ wr.t()).view(S, T, E) for x in xs]
+    (w13, s13), (w2, s2) = weight4(1, 2 * I, H, g), weight4(1, H, I, g)
+    dw, one = randn((S, T, K), g), torch.ones(1, device="cuda")
+    empty = lambda *s, t=torch.uint8: torch.empty(s, dtype=t, device="cuda")  # noqa: E731
+    F32 = torch.float32
+
+    def buffers():
+        return dict(norm=dict(y=empty(S * T, H, t=BF)), route=(empty(S, T, K, t=torch.int64), empty(S, T, K, t=F32)),
+                    balance=dict(loss=empty(1, t=F32), counts=empty(S, E, t=torch.int32), factors=empty(S, E, t=F32)),
+                    workspace=empty(ep.balance_loss_workspace(S * T, E, S)), q=(empty(S * T, H // 2), empty(S * T, H // 32)),
+                    h=(empty(S * T, I // 2), empty(S * T, I // 32)))
+
+    def step(i, b, out):
+        idx, _ = ep.route(logits[i], K, out=b["route"])
+        factors = ep.balance_loss(logits[i], idx, out=b["balance"], workspace=b["workspace"])["factors"]
+        ep.router_backward(logits[i], idx, dw, factors=factors, dloss=one, out=out[0])
+        y = ep.rms_norm(xs[i], wn, out=b["norm"])["y"]
+        ep.quantize_fp4(xs[i] if i % 2 else y, out=b["q"])
+        ep.expert_swiglu_fp4(*b["q"], w13, s13, out=b["h"])
+        ep.expert_gemm_fp4(*b["h"], w2, s2, out=out[1])
+    outs = lambda: [(empty(S, T, E, t=F32), empty(S * T, H, t=BF)) for _ in steps]  # noqa: E731
+    alone, got, shared = outs(), outs(), buffers()
+    for i in steps:
+        step(i, buffers(), alone[i])
+        torch.cuda.synchronize()
+    assert len({float(y.float().norm()) for _, y in alone}) == len(steps)
+
+    def run():
+        for i in steps:
+            step(i, shared, got[i])
+    run()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    for _ in range(20):
+        graph.replay()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for o in got:
+            for t in o:
+                t.zero_()
+        graph.replay()
+        assert all(torch.equal(a, b) for x, y in zip(alone, got) for a, b in zip(x, y))
+
+
 def test_layer_refuses_mixed_weights():
     u8, f32 = torch.zeros(1, dtype=torch.uint8), torch.zeros(1)
     with pytest.raises(ValueError):
