@@ -6,18 +6,21 @@
 // which tcgen05.mma computes whole (kind::mxf4, block scales from tensor memory, fp32 sums), so that the
 // accumulator leaves tensor memory once a tile, not once a block of K.
 //
-// Shape.  128 rows x 192 weight rows a tile (64 where the tiles are few): tensor memory then holds two
-// accumulators and the scales beside them, so that a tile is written while the next is multiplied.  One warp
+// Shape.  128 rows x 192 or 224 weight rows a tile (64 or 128 where that fills the SMs better: fp4_choice): tensor memory
+// then holds two accumulators and the scales beside them, so that a tile is written while the next is multiplied.  One warp
 // copies codes (a stage is 256 of K, 128 bytes a row), four stage scales: each thread loads its rows' bytes and
 // writes them where tcgen05.cp reads them (32 rows of 16 bytes: row r's four bytes at (r % 32) * 16 + r / 32 * 4),
 // one issues copies of scales and products, four write the results.
 //
 // Bound.  Up to 128 rows a group the weights' bytes: 256 groups of about 64 rows, K 7168, 2I 4096 594 us, K 2048, N 7168
-// 325 us, 6.7 TB/s.  With long groups shared memory: a stage's codes are written to it and read from it once, 82 KB at
-// 128 bytes a cycle = 640 cycles, and a stage takes 650 (the products some 370).  Pairs of blocks share the weight's
-// rows, 56 KB a stage and SM: first product, 40 groups of 2048 rows, 914 us by one block, 737 by pairs (6.5 PFLOP/s).
+// 324 us, 6.7 TB/s.  With long groups shared memory: a stage's codes are written to it and read from it once, 82 KB at
+// 128 bytes a cycle = 640 cycles for 192 weight rows, and a stage takes 650 (the products some 370).  Pairs of blocks share
+// the weight's rows, 56 KB a stage and SM: first product, 40 groups of 2048 rows, 914 us by one block, 737 by pairs (6.5
+// PFLOP/s); tiles of 224 rows make the same of the second product's 541 us 496 (4.8 PFLOP/s, results included).  A long run
+// of such products meets the board's power limit (65536 rows to 256 groups, first product: 976 us at first, 1060 to 1100 later).
 // A fifth stage changes nothing, weights fetched ahead into the second-level cache cost time.  With few tiles, what one
 // SM brings in from memory: one row, K 7168, N 4096 11.2 us by 64 blocks, 8.3 by 128 in clusters of two.
+#include <algorithm>
 #include <atomic>
 #include <initializer_list>
 
@@ -670,12 +673,38 @@ static int fp4_split(int64_t tiles, int stages, int sms) {
     return 1;
 }
 
-// Whether pairs of blocks make the first product's tiles: one of theirs costs 1.65 of one block's, and has twice the rows.
-// 40 groups, K 7168, 2I 4096, us by one block / by pairs: 256 rows a group 135 / 128, 448 238 / 204, 640 297 / 285, 768 371 /
-// 296, 1024 460 / 386, 2048 914 / 737; but 256 groups of 256 rows on average, popular and unpopular, 1020 / 1075: half a
-// tile of each group is empty on average.  (The second product, whose results are its larger part, gains 3 % at best:
-// 2048 rows 537 / 515.)
-static bool fp4_by_pairs(int64_t rows) { return rows > 3 * k4BM; }
+// The shape of a launch's tiles: the one with the least rounds over the SMs * cost of a round, the widest of equal ones.  A
+// round's cost is what bounds it, the rows of codes that a stage brings into an SM, 128 + columns.  us by 192 columns / by what
+// is chosen: second product, K 2048, N 7168, 40 groups of 2048 rows 541 / 496 (224: 6 % fewer bytes a column, and N is 32 of
+// them); one group, K 7168, 1000 rows: N 4096 26.4 / 18.0 (224), N 7168 27.8 / 27.8 (by 224 30.0), N 2048 15.5 / 13.6 (128);
+// K 4096, N 4096, 777 rows 16.4 / 12.6 (128); first product, 300 rows, 2I 4096, by 64 20.7, by 128 13.8.
+// Pairs of blocks (first product) have twice the rows at 0.825 of a round of 192's cost.  40 groups, K 7168, 2I 4096, us by
+// one block / by pairs: 256 rows a group 135 / 128, 448 238 / 204, 640 297 / 285, 768 371 / 296, 1024 460 / 386, 2048 914 / 737;
+// but 256 groups of 256 rows on average, popular and unpopular, 1020 / 1075: half a tile of each group is empty on average,
+// so that they need more than 384 rows.  (The second product, whose results are its larger part, gains 3 % at best.)
+struct Fp4Choice {
+    int columns, ctas;
+};
+static Fp4Choice fp4_choice(bool swiglu, int64_t rows, int groups, int64_t n, int sms) {
+    auto rounds = [&](int columns, int ctas) {
+        const int64_t tiles = std::max<int64_t>((rows + ctas * k4BM - 1) / (ctas * k4BM), 1) * groups * ((n + columns - 1) / columns), units = sms / ctas;
+        return (tiles + units - 1) / units;
+    };
+    Fp4Choice best = {64, 1};
+    int64_t least = rounds(64, 1) * (k4BM + 64);
+    auto consider = [&](int columns, int ctas, int cost) {
+        const int64_t c = rounds(columns, ctas) * cost;
+        if (c <= least) {
+            least = c;
+            best = {columns, ctas};
+        }
+    };
+    consider(128, 1, k4BM + 128);
+    consider(192, 1, k4BM + 192);
+    if (!swiglu) consider(224, 1, k4BM + 224);
+    if (swiglu && rows > 3 * k4BM) consider(192, 2, 264);
+    return best;
+}
 
 template <bool kSwiglu>
 static ep_status launch_fp4(const char* fn, const ep_fp4_rows* x, const ep_row_groups* g, const ep_fp4_weight* w, Fp4Args a, void* stream) {
@@ -698,18 +727,19 @@ static ep_status launch_fp4(const char* fn, const ep_fp4_rows* x, const ep_row_g
     int dev = 0, sms = 0;
     EP_CUDA(cudaGetDevice(&dev));
     EP_CUDA(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
-    a.n_tiles = (w->n + 191) / 192;
-    if (most_tiles(a, k4BM) * 2 <= sms) {
-        a.n_tiles = (w->n + 63) / 64;
-        const int split = fp4_split(most_tiles(a, k4BM), a.KT, sms);
-        if (split > 1) return launch_fp4_shape<kSwiglu, 64, 1, true>(fn, x, w, a, sms, split, dev, stream);
-        return launch_fp4_shape<kSwiglu, 64, 1, false>(fn, x, w, a, sms, 1, dev, stream);
-    }
+    a.n_tiles = (w->n + 63) / 64;
+    const int split = fp4_split(most_tiles(a, k4BM), a.KT, sms);
+    if (split > 1) return launch_fp4_shape<kSwiglu, 64, 1, true>(fn, x, w, a, sms, split, dev, stream);
+    // Rows of a group: as the caller expects, or what the arrays hold, shared out; regions with counts are sized for the
+    // worst case, and a low-latency step fills a few percent of them.
+    const int64_t rows = g->expected > 0 ? std::min<int64_t>(g->expected, 0x7fffffff) : x->rows / w->groups / (w->groups > 1 && !g->offsets && g->counts ? 16 : 1);
+    const Fp4Choice c = fp4_choice(kSwiglu, rows, w->groups, w->n, sms);
+    if (c.columns == 64) return launch_fp4_shape<kSwiglu, 64, 1, false>(fn, x, w, a, sms, 1, dev, stream);
+    if (c.columns == 128) return launch_fp4_shape<kSwiglu, 128, 1, false>(fn, x, w, a, sms, 1, dev, stream);
     if constexpr (kSwiglu) {
-        // Rows of a group: as the caller expects, or what the arrays hold, shared out; regions with counts are sized for the
-        // worst case, and a low-latency step fills a few percent of them.
-        const int64_t rows = g->expected > 0 ? g->expected : x->rows / w->groups / (w->groups > 1 && !g->offsets && g->counts ? 16 : 1);
-        if (fp4_by_pairs(rows)) return launch_fp4_shape<kSwiglu, 192, 2, false>(fn, x, w, a, sms, 2, dev, stream);
+        if (c.ctas == 2) return launch_fp4_shape<kSwiglu, 192, 2, false>(fn, x, w, a, sms, 2, dev, stream);
+    } else {
+        if (c.columns == 224) return launch_fp4_shape<kSwiglu, 224, 1, false>(fn, x, w, a, sms, 1, dev, stream);
     }
     return launch_fp4_shape<kSwiglu, 192, 1, false>(fn, x, w, a, sms, 1, dev, stream);
 }

@@ -249,6 +249,41 @@ def test_both_shapes_on_long_and_ragged_groups(K, N, expected):
 
 
 @gpu
+@pytest.mark.parametrize("K,N", [(640, 224), (1408, 512), (640, 896), (384, 1099), (1152, 1280), (640, 2304), (256, 4099), (2304, 2048)])
+def test_every_tile_width_gives_the_same(K, N):
+    """The rows that a caller expects choose the tiles' width, not what comes out: K is summed in the same order by each."""
+    for counts in (RAGGED, LONG, [0, 700, 1, 130, 2]):
+        cnt, off, hoff, rows = groups_of(counts, 2)
+        g = gen(K + N)
+        x, xs = rows4(rows, K, g)
+        w, ws = weight4(len(counts), N, K, g)
+        st = ep.new_status()
+        first = None
+        for expected in (1, 200, 300, 600, 1000, 4000, 2 ** 40):
+            out = torch.full((rows, N + 5), 7.0, dtype=BF, device="cuda")[:, :N]  # rows not on 16 bytes
+            wide = torch.full((rows, (N + 7) // 8 * 8), 7.0, dtype=BF, device="cuda")[:, :N]
+            got = [ep.expert_gemm_fp4(x, xs, w, ws, counts=cnt, offsets=off, out=o, status=st, expected_rows=expected) for o in (out, wide)]
+            if N % 256 == 0:
+                h = tuple(torch.full((rows, n), 7, dtype=torch.uint8, device="cuda") for n in (N // 4, N // 64))
+                got += ep.expert_swiglu_fp4(x, xs, w, ws, counts=cnt, offsets=off, out=h, status=st, expected_rows=expected)
+            first = first or got
+            assert all(torch.equal(a, b) for a, b in zip(first, got)) and torch.equal(out, wide)
+            for o in (out, wide):
+                base = torch.as_strided(o, (rows, o.stride(0)), (o.stride(0), 1))
+                assert (base[:, N:] == 7).all(), "written past the rows' ends"
+        ep.check_status(st)
+        own = torch.zeros(rows, dtype=torch.bool, device="cuda")
+        for e, (o, c) in enumerate(zip(hoff, counts)):
+            own[o:o + c] = True
+            if c:
+                X, W = values4(x[o:o + c], xs[o:o + c]), values4(w[e], ws[e])
+                assert_bf16_close(first[0][o:o + c], *product64(X, W), f"group {e}")
+                if N % 256 == 0:
+                    assert_fp4_close(first[2][o:o + c], first[3][o:o + c], *swiglu64(X, W))
+        assert all((t[~own] == 7).all() for t in first), "rows of no group were written"
+
+
+@gpu
 def test_regions_with_and_without_counts():
     E, cap, K, N = 5, 40, 384, 200
     g = gen(5)
