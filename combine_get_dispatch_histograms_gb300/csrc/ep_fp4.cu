@@ -16,7 +16,7 @@
 // 324 us, 6.7 TB/s.  With long groups shared memory: a stage's codes are written to it and read from it once, 82 KB at
 // 128 bytes a cycle = 640 cycles for 192 weight rows, and a stage takes 650 (the products some 370).  Pairs of blocks share
 // the weight's rows, 56 KB a stage and SM: first product, 40 groups of 2048 rows, 914 us by one block, 737 by pairs (6.5
-// PFLOP/s); tiles of 224 rows make the same of the second product's 541 us 496 (4.8 PFLOP/s, results included).  A long run
+// PFLOP/s); the second 541 us by 192 weight rows a tile, 496 by 224, 466 by pairs (5.2 PFLOP/s, results included).  A long run
 // of such products meets the board's power limit (65536 rows to 256 groups, first product: 976 us at first, 1060 to 1100 later).
 // A fifth stage changes nothing, weights fetched ahead into the second-level cache cost time.  With few tiles, what one
 // SM brings in from memory: one row, K 7168, N 4096 11.2 us by 64 blocks, 8.3 by 128 in clusters of two.
@@ -678,10 +678,12 @@ static int fp4_split(int64_t tiles, int stages, int sms) {
 // is chosen: second product, K 2048, N 7168, 40 groups of 2048 rows 541 / 496 (224: 6 % fewer bytes a column, and N is 32 of
 // them); one group, K 7168, 1000 rows: N 4096 26.4 / 18.0 (224), N 7168 27.8 / 27.8 (by 224 30.0), N 2048 15.5 / 13.6 (128);
 // K 4096, N 4096, 777 rows 16.4 / 12.6 (128); first product, 300 rows, 2I 4096, by 64 20.7, by 128 13.8.
-// Pairs of blocks (first product) have twice the rows at 0.825 of a round of 192's cost.  40 groups, K 7168, 2I 4096, us by
-// one block / by pairs: 256 rows a group 135 / 128, 448 238 / 204, 640 297 / 285, 768 371 / 296, 1024 460 / 386, 2048 914 / 737;
-// but 256 groups of 256 rows on average, popular and unpopular, 1020 / 1075: half a tile of each group is empty on average,
-// so that they need more than 384 rows.  (The second product, whose results are its larger part, gains 3 % at best.)
+// Pairs of blocks have twice the rows, at 0.825 of a round of 192's cost for the first product, 0.935 of one of 224's for the
+// second, whose results are a larger part.  40 groups, us by one block / by pairs: K 7168, 2I 4096, 256 rows a group 135 / 128,
+// 448 238 / 204, 640 297 / 285, 768 371 / 296, 1024 460 / 386, 2048 914 / 737; K 2048, N 7168, 448 133 / 129, 640 164 / 164,
+// 1024 257 / 243, 2048 498 / 466.  But 256 groups of 256 rows on average, popular and unpopular, 1020 / 1075: half a tile of
+// each group is empty on average, so that they need more than 384 rows.  And a launch of one round gains nothing: 777 rows,
+// 4096 -> 4096 12.6 / 13.3.
 struct Fp4Choice {
     int columns, ctas;
 };
@@ -702,7 +704,7 @@ static Fp4Choice fp4_choice(bool swiglu, int64_t rows, int groups, int64_t n, in
     consider(128, 1, k4BM + 128);
     consider(192, 1, k4BM + 192);
     if (!swiglu) consider(224, 1, k4BM + 224);
-    if (swiglu && rows > 3 * k4BM) consider(192, 2, 264);
+    if (rows > 3 * k4BM && least > k4BM + 224) consider(swiglu ? 192 : 224, 2, swiglu ? 264 : 330);
     return best;
 }
 
@@ -739,6 +741,7 @@ static ep_status launch_fp4(const char* fn, const ep_fp4_rows* x, const ep_row_g
     if constexpr (kSwiglu) {
         if (c.ctas == 2) return launch_fp4_shape<kSwiglu, 192, 2, false>(fn, x, w, a, sms, 2, dev, stream);
     } else {
+        if (c.ctas == 2) return launch_fp4_shape<kSwiglu, 224, 2, false>(fn, x, w, a, sms, 2, dev, stream);
         if (c.columns == 224) return launch_fp4_shape<kSwiglu, 224, 1, false>(fn, x, w, a, sms, 1, dev, stream);
     }
     return launch_fp4_shape<kSwiglu, 192, 1, false>(fn, x, w, a, sms, 1, dev, stream);
