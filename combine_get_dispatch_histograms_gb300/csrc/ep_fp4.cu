@@ -681,9 +681,10 @@ static int fp4_split(int64_t tiles, int stages, int sms) {
 // Pairs of blocks have twice the rows, at 0.825 of a round of 192's cost for the first product, 0.935 of one of 224's for the
 // second, whose results are a larger part.  40 groups, us by one block / by pairs: K 7168, 2I 4096, 256 rows a group 135 / 128,
 // 448 238 / 204, 640 297 / 285, 768 371 / 296, 1024 460 / 386, 2048 914 / 737; K 2048, N 7168, 448 133 / 129, 640 164 / 164,
-// 1024 257 / 243, 2048 498 / 466.  But 256 groups of 256 rows on average, popular and unpopular, 1020 / 1075: half a tile of
-// each group is empty on average, so that they need more than 384 rows.  And a launch of one round gains nothing: 777 rows,
-// 4096 -> 4096 12.6 / 13.3.
+// 1024 257 / 243, 2048 498 / 466.  But half a tile of each group is empty on average where their lengths vary: first product,
+// 256 groups of 256 rows on average 1020 / 1075, 64 of 512 423 / 390; second, 64 of 512 237 / 244, of 1024 425 / 426, of 1536
+// 624 / 616; so that they need more than 384 rows, and several groups of the second product more than 1024.  And a launch of
+// one round gains nothing: 777 rows, 4096 -> 4096 12.6 / 13.3.
 struct Fp4Choice {
     int columns, ctas;
 };
@@ -704,7 +705,7 @@ static Fp4Choice fp4_choice(bool swiglu, int64_t rows, int groups, int64_t n, in
     consider(128, 1, k4BM + 128);
     consider(192, 1, k4BM + 192);
     if (!swiglu) consider(224, 1, k4BM + 224);
-    if (rows > 3 * k4BM && least > k4BM + 224) consider(swiglu ? 192 : 224, 2, swiglu ? 264 : 330);
+    if (rows > (swiglu || groups == 1 ? 3 : 8) * k4BM && least > k4BM + 224) consider(swiglu ? 192 : 224, 2, swiglu ? 264 : 330);
     return best;
 }
 
