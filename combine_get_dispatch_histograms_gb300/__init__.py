@@ -167,8 +167,9 @@ class Context:
 
     # ---- routing ---------------------------------------------------------------
     def route(self, logits: torch.Tensor, stream=None, out=None, topk_nodes: Optional[int] = None, **how):
-        """(topk_idx, topk_weights) [R][T][K] of router logits [R][T][E], as router.route.  topk_nodes: each token's experts on
-        that many of the N nodes at most, so that the node-wise dispatch sends so many copies."""
+        """(topk_idx, topk_weights) [R][T][K] of router logits [R][T][E], as router.route (keys="scores" for a router whose bias
+        balances the load).  topk_nodes: each token's experts on that many of the N nodes at most, so that the node-wise
+        dispatch sends so many copies."""
         if logits.shape != (self.R, self.T, self.E):
             raise ValueError(f"Context.route: logits {(self.R, self.T, self.E)}: got {tuple(logits.shape)}")
         if topk_nodes is not None:

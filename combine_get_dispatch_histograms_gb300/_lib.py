@@ -54,7 +54,7 @@ class EpMoeWeights(ctypes.Structure):
 
 class EpRouter(ctypes.Structure):
     _fields_ = [("tokens", I64), ("experts", I32), ("topk", I32), ("logits_type", I32), ("scoring", I32), ("normalize", I32),
-                ("groups", I32), ("topk_groups", I32), ("scale", F32)]
+                ("groups", I32), ("topk_groups", I32), ("scale", F32), ("keys", I32), ("group_keys", I32)]
 
 
 # name -> (restype, argtypes); every name here is declared in include/ep.h

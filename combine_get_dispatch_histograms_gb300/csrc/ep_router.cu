@@ -4,8 +4,9 @@
 // A warp per token.  Lane i holds experts i V .. i V + V - 1 of the row in registers, so that the lowest
 // expert of equal ones is the first of the lowest lane.
 //
-// Choice.  key = fp32(logit + bias), compared as integers in the same order (NaN the largest, -inf and what
-// closed groups hold never chosen).  Lane k ends with choice k.
+// Choice.  key = fp32(logit + bias) or fp32(score + bias), compared as integers in the same order (NaN the largest,
+// -inf and what closed groups hold never chosen).  Lane k ends with choice k.  Without a bias and without sums
+// over a group both keys choose alike, since the scores grow with the logits; with either they do not.
 //
 // Balance.  With c_se the choices of expert e in sequence s, m_s = sum_e c_se, n_s the tokens that chose:
 //   F_se = coef E c_se / (S m_s n_s),   loss = sum_s sum_e F_se sum_t q_ste,   q: softmax, or sigmoid / its sum
@@ -44,6 +45,7 @@ struct RouterArgs {
     uint32_t tokens;  // below 2^31, so that a step past them stays within 32 bits
     int E, K, groups, topk_groups;
     int group_size, lanes_log;  // lanes_log: a group is 1 << lanes_log whole lanes; -1: it is not
+    bool group_sums;            // a group counts its two largest keys, not the largest alone
     bool normalize;
     int vec;
     float scale;
@@ -165,7 +167,7 @@ __device__ __forceinline__ void scores(const float (&l)[V], float (&p)[V], float
     }
 }
 
-// Whether this lane's group stays; a group's score is the sum of its two largest keys.  Lanes that hold whole parts of
+// Whether this lane's group stays; a group counts the sum of its two largest keys, or the largest.  Lanes that hold whole parts of
 // groups (V divides the group, a power of two of lanes each): the lanes' two largest are merged.
 template <int V>
 __device__ __forceinline__ bool keep_group(const uint32_t (&key)[V], const RouterArgs& a, int lane) {
@@ -180,7 +182,7 @@ __device__ __forceinline__ bool keep_group(const uint32_t (&key)[V], const Route
         lo = max(max(lo, l), min(hi, h));
         hi = max(hi, h);
     }
-    const uint32_t score = a.group_size > 1 ? ordered(unordered(hi) + unordered(lo)) : hi;
+    const uint32_t score = a.group_sums ? ordered(unordered(hi) + unordered(lo)) : hi;
     // lane g: group g's score, taken out as it is chosen
     uint32_t left = __shfl_sync(kAll, score, lane << a.lanes_log & 31);
     if (lane >= a.groups) left = 0;
@@ -211,7 +213,7 @@ __device__ __forceinline__ uint32_t choose_groups(const uint32_t (&key)[V], cons
         const uint32_t top = __reduce_max_sync(kAll, hi);
         const bool owner = lane == __ffs(__ballot_sync(kAll, hi == top)) - 1;
         const uint32_t next = __reduce_max_sync(kAll, owner ? lo : hi);
-        const uint32_t s = size > 1 ? ordered(unordered(top) + unordered(next)) : top;
+        const uint32_t s = a.group_sums ? ordered(unordered(top) + unordered(next)) : top;
         if (lane == g) score = s;
     }
     uint32_t kept = 0;
@@ -313,7 +315,10 @@ __device__ __forceinline__ int choose(uint32_t (&key)[V], int K, int lane, Route
     return lane < total && lane < K ? list.expert[lane] : -1;
 }
 
-template <typename T, int V, bool kSigmoid, bool kGroups>
+// What the keys are made of.  By scores, groups are chosen first where topk_groups says so.
+enum KeyKind { kByLogits, kByLogitsOfGroups, kByScores };
+
+template <typename T, int V, bool kSigmoid, int kKind>
 __global__ void __launch_bounds__(kRouterThreads, kPerSm<V>) route_kernel(const RouterArgs a) {
     __shared__ __align__(16) RouteList lists[kRouterWarps];
     const int lane = threadIdx.x & 31;
@@ -334,9 +339,17 @@ __global__ void __launch_bounds__(kRouterThreads, kPerSm<V>) route_kernel(const 
             continue;
         }
         uint32_t key[V];  // kKeyNegInf past the last expert
+        float most, by;   // of a softmax
+        if constexpr (kKind == kByScores) {
+            float p[V], slope[V];
+            scores<V, kSigmoid>(l, p, slope, &most, &by);
 #pragma unroll
-        for (int i = 0; i < V; ++i) key[i] = ordered(l[i] + bias[i]);  // -inf stays past the last expert
-        if (kGroups) {
+            for (int i = 0; i < V; ++i) key[i] = l[i] == -INFINITY ? kKeyNegInf : ordered(p[i] + bias[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i) key[i] = ordered(l[i] + bias[i]);  // -inf stays past the last expert
+        }
+        if (kKind == kByLogitsOfGroups || (kKind == kByScores && a.topk_groups < a.groups)) {
             if (a.lanes_log >= 0) {
                 if (!keep_group(key, a, lane))
 #pragma unroll
@@ -360,8 +373,10 @@ __global__ void __launch_bounds__(kRouterThreads, kPerSm<V>) route_kernel(const 
             w = expert >= 0 ? exp_of(logit - m) : 0.0f;
             w = __fdividef(w, warp_sum(w));
         } else {
-            float p[V], slope[V], most, by;
-            scores<V, false>(l, p, slope, &most, &by);
+            if constexpr (kKind != kByScores) {
+                float p[V], slope[V];
+                scores<V, false>(l, p, slope, &most, &by);
+            }
             w = exp_of(logit - most) * by;
         }
         if (lane < a.K) {
@@ -758,9 +773,11 @@ __global__ void __launch_bounds__(kRouterThreads, V <= 8 ? 4 : kPerSm<V>) router
                                        : EP_BY_EXPERTS(kernel, __nv_bfloat16, false, (r)->experts)))
 
 template <typename T, int V, bool kSigmoid>
-constexpr auto route_all = route_kernel<T, V, kSigmoid, false>;
+constexpr auto route_all = route_kernel<T, V, kSigmoid, kByLogits>;
 template <typename T, int V, bool kSigmoid>
-constexpr auto route_groups = route_kernel<T, V, kSigmoid, true>;
+constexpr auto route_groups = route_kernel<T, V, kSigmoid, kByLogitsOfGroups>;
+template <typename T, int V, bool kSigmoid>
+constexpr auto route_scores = route_kernel<T, V, kSigmoid, kByScores>;
 
 static ep_status check_router(const char* fn, const ep_router* r, const void* logits, int64_t stride) {
     if (!r) return set_error(EP_ERR_INVALID_ARG, "%s: null descriptor", fn);
@@ -811,6 +828,8 @@ extern "C" ep_status ep_route(const ep_router* r, const void* logits, int64_t lo
         r->topk > r->topk_groups * (r->experts / r->groups))
         return set_error(EP_ERR_INVALID_ARG, "%s: %d of %d groups (at most %d) of %d experts for %d choices", fn, r->topk_groups, r->groups,
                          kRouterMaxGroups, r->experts, r->topk);
+    if (r->keys < 0 || r->keys > EP_KEYS_SCORES || r->group_keys < 0 || r->group_keys > 2)
+        return set_error(EP_ERR_INVALID_ARG, "%s: keys %d, %d keys of a group", fn, r->keys, r->group_keys);
     if (r->tokens == 0) return EP_OK;
     if (!topk_idx || !topk_weights || !aligned_to(topk_idx, 8) || !aligned_to(topk_weights, 4) || !aligned_to(bias, 4))
         return set_error(EP_ERR_INVALID_ARG, "%s: topk_idx, topk_weights and bias aligned to their elements", fn);
@@ -821,9 +840,13 @@ extern "C" ep_status ep_route(const ep_router* r, const void* logits, int64_t lo
     const int size = r->experts / r->groups;
     if (size % held == 0 && (size / held & (size / held - 1)) == 0)
         for (lanes_log = 0; held << lanes_log < size;) ++lanes_log;
-    const RouterArgs a = {logits, logits_stride, (uint32_t)r->tokens, r->experts, r->topk, r->groups, r->topk_groups, size, lanes_log, r->normalize != 0,
+    const RouterArgs a = {logits, logits_stride, (uint32_t)r->tokens, r->experts, r->topk, r->groups, r->topk_groups, size, lanes_log,
+                          size > 1 && r->group_keys != 1, r->normalize != 0,
                           by_vectors(r->experts, r->logits_type, logits, logits_stride), r->scale, bias, mask, topk_idx, topk_weights};
-    return launch_next(r->topk_groups < r->groups ? EP_ROUTER_KERNEL(route_groups, r) : EP_ROUTER_KERNEL(route_all, r), blocks, kRouterThreads, stream, a);
+    return launch_next(r->keys == EP_KEYS_SCORES    ? EP_ROUTER_KERNEL(route_scores, r)
+                       : r->topk_groups < r->groups ? EP_ROUTER_KERNEL(route_groups, r)
+                                                    : EP_ROUTER_KERNEL(route_all, r),
+                       blocks, kRouterThreads, stream, a);
 }
 
 extern "C" int64_t ep_balance_loss_workspace(const ep_router* r, int32_t sequences) {

@@ -20,7 +20,12 @@ from .norm import _workspace_bytes
 _I64, _I32, _F32, _U8, _BOOL = torch.int64, torch.int32, torch.float32, torch.uint8, torch.bool
 _TYPES = {torch.bfloat16: 0, _F32: 1}
 _SCORING = {"softmax": 0, "sigmoid": 1}
-_ROUTER = struct.Struct("@qiiiiiiif0P").pack   # ep_router as the C side lays it out
+_KEYS = {"logits": 0, "scores": 1}
+_PACK = struct.Struct("@qiiiiiiifii0P").pack   # ep_router as the C side lays it out
+
+
+def _ROUTER(tokens, experts, topk, logits_type, scoring, normalize, groups, topk_groups, scale, keys=0, group_keys=2):
+    return _PACK(tokens, experts, topk, logits_type, scoring, normalize, groups, topk_groups, scale, keys, group_keys)
 
 
 def _logits(name, t):
@@ -39,25 +44,34 @@ def _plain(name, t, shape, dtype, index):
     return t.data_ptr()
 
 
-def _descriptor(name, logits, shape, topk, scoring, normalize=True, groups=1, topk_groups=1, scale=1.0):
+def _descriptor(name, logits, shape, topk, scoring, normalize=True, groups=1, topk_groups=1, scale=1.0, keys="logits",
+                group_keys=2):
     if scoring not in _SCORING:
         _refuse(f"{name}: scoring {scoring!r}: 'softmax' or 'sigmoid'")
+    if keys not in _KEYS or group_keys not in (1, 2):
+        _refuse(f"{name}: keys {keys!r}: 'logits' or 'scores'; group_keys {group_keys!r}: 1 or 2")
     tokens = shape[0] * (shape[1] if len(shape) == 3 else 1)
-    return _ROUTER(tokens, shape[-1], topk, _TYPES[logits.dtype], _SCORING[scoring], bool(normalize), groups, topk_groups, scale)
+    return _ROUTER(tokens, shape[-1], topk, _TYPES[logits.dtype], _SCORING[scoring], bool(normalize), groups, topk_groups, scale, _KEYS[keys],
+                   group_keys)
 
 
 def route(logits, topk: int, bias=None, mask=None, scoring="softmax", normalize=True, scale=1.0, groups=1, topk_groups=None, out=None,
-          stream=None):
-    """(topk_idx int64, topk_weights fp32) [..][topk]: the experts with the largest logit + bias, the lowest of equal ones
-    first, and their weights from the logits alone.
+          stream=None, *, keys="logits", group_keys=2):
+    """(topk_idx int64, topk_weights fp32) [..][topk]: the experts with the largest key, the lowest of equal ones first, and
+    their weights from the logits alone.
 
     scoring "softmax": over all experts, or with normalize over the chosen; "sigmoid": with normalize over the chosen
     ones' sum + 1e-20; all times scale.  -inf is never chosen: entries without an expert are -1 with weight 0.
-    bias fp32 [E]; mask [..] (bool or uint8), 0 for padding.  groups, topk_groups: choose among the experts of the
-    topk_groups of `groups` equal runs of experts (the experts of a node, say) with the largest sum of two keys."""
+    bias fp32 [E]; mask [..] (bool or uint8), 0 for padding.
+    keys "logits": key = logit + bias; "scores": key = score + bias, the score by `scoring` (the softmax over all experts),
+    as a router is trained whose bias balances the load.  The two choose differently where there is a bias or where groups
+    are ranked by sums.
+    groups, topk_groups: choose among the experts of the topk_groups of `groups` equal runs of experts (the experts of a
+    node, say) with the largest sum of their two largest keys, or with group_keys=1 the largest key."""
     index, shape, step = _logits("route: logits", logits)
     lead = shape[:-1]
-    r = _descriptor("route", logits, shape, topk, scoring, normalize, groups, groups if topk_groups is None else topk_groups, scale)
+    r = _descriptor("route", logits, shape, topk, scoring, normalize, groups, groups if topk_groups is None else topk_groups, scale, keys,
+                    group_keys)
     bias_at = None if bias is None else _plain("route: bias", bias, shape[-1:], _F32, index)
     mask_at = None if mask is None else _plain("route: mask", mask, lead, _BOOL if mask.dtype == _BOOL else _U8, index)
     shape = (*lead, topk)

@@ -577,10 +577,11 @@ ep_status ep_rms_norm_backward(const void* dy, int64_t dy_stride, const void* h,
                                void* stream);
 
 typedef enum ep_scoring { EP_SOFTMAX = 0, EP_SIGMOID = 1 } ep_scoring;
+typedef enum ep_keys { EP_KEYS_LOGITS = 0, EP_KEYS_SCORES = 1 } ep_keys;
 
 /* A router over `experts` (1..1024) with topk (1..32, at most experts) choices a
- * token.  groups and topk_groups are read by ep_route alone, normalize and scale
- * by ep_route and ep_router_backward. */
+ * token.  groups, topk_groups, keys and group_keys are read by ep_route alone,
+ * normalize and scale by ep_route and ep_router_backward. */
 typedef struct ep_router {
     int64_t tokens;
     int32_t experts, topk;
@@ -590,15 +591,25 @@ typedef struct ep_router {
     int32_t groups, topk_groups; /* choose among the experts of topk_groups of `groups` equal
                                     runs of experts (1..32; nodes, say); 1, 1: among all       */
     float scale;                 /* of the weights                                            */
+    int32_t keys;                /* ep_keys: what the bias is added to                         */
+    int32_t group_keys;          /* keys that a group counts: 2 or 0 its two largest, 1 its
+                                    largest                                                    */
 } ep_router;
 
 /* Logits [tokens][experts] (rows logits_stride elements apart) to topk_idx
  * [tokens][topk] and topk_weights, as the layout and dispatch calls read them.
- *   Choice: by key = fp32(logit + bias[expert]) (bias nullable, fp32), largest first,
- *   equal keys by the lowest expert; NaN is larger than any number, as in a sort, and
- *   -inf is never chosen: where fewer than topk experts are left, the last entries
- *   are -1 with weight 0.  With groups, first the topk_groups runs with the largest
- *   fp32 sum of their two largest keys (one key where a run is one expert).
+ *   Choice: by key, largest first, equal keys by the lowest expert; NaN is larger than
+ *   any number, as in a sort, and -inf is never chosen: where fewer than topk experts
+ *   are left, the last entries are -1 with weight 0.  With groups, first the
+ *   topk_groups runs with the largest fp32 sum of their two largest keys (one key where
+ *   a run is one expert), or with group_keys 1 the largest key.
+ *     EP_KEYS_LOGITS: key = fp32(logit + bias[expert]) (bias nullable, fp32);
+ *     EP_KEYS_SCORES: key = fp32(score + bias[expert]), score the fp32 softmax over all
+ *     experts or sigmoid, off by at most (|x| + 48) 2^-23 of itself, x the exponent's
+ *     argument; a logit of -inf is never chosen.
+ *   The two differ where there is a bias, and where a group counts two keys.  A router
+ *   whose bias balances the load is trained with the bias on the scores, and ranks its
+ *   groups by them: it takes EP_KEYS_SCORES.
  *   Weights, from the logits alone, times scale: softmax over all experts, or with
  *   normalize over the chosen; sigmoid, or with normalize sigmoid / (the chosen
  *   ones' sum + 1e-20).
