@@ -367,13 +367,13 @@ __global__ void __launch_bounds__(1024) norm_backward_block(const NormBackArgs a
     extern __shared__ __align__(128) uint8_t ring[];
     __shared__ uint64_t full[kBackStages];
     __shared__ float buf[2][2][32];
-    __shared__ int abort;
+    __shared__ int abort[2];  // of the rows in turn: all threads of the block leave the loop at the same row
     const int tid = threadIdx.x, vecs = a.hidden >> 3;
     const uint32_t dy_bytes = a.hidden * 2, h_bytes = a.hidden * sizeof(T);
     const uint32_t stage = dy_bytes + (a.dres ? 2 : 1) * h_bytes;
     if (tid == 0) {
         for (int s = 0; s < kBackStages; ++s) mbar_init(&full[s], 1);
-        abort = 0;
+        abort[0] = abort[1] = 0;
         fence_mbar_init();
     }
     __syncthreads();
@@ -392,9 +392,11 @@ __global__ void __launch_bounds__(1024) norm_backward_block(const NormBackArgs a
     float dw[2][8] = {};
     int s = 0, turn = 0;
     uint32_t phase = 0;
-    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, ++turn) {
-        // a copy that does not come ends the row loop for the whole block, and its part of dw is NaN
-        if (!mbar_wait_bounded(&full[s], phase, kBackWaitNs)) abort = 1;
+    bool gave_up = false;
+    int64_t row = blockIdx.x;
+    for (; row < a.rows; row += gridDim.x, ++turn) {
+        // a copy that does not come ends the row loop for the whole block
+        if (!mbar_wait_bounded(&full[s], phase, kBackWaitNs)) abort[turn & 1] = 1;
         const uint8_t* p = ring + s * stage;
         const __nv_bfloat16* sg = reinterpret_cast<const __nv_bfloat16*>(p);
         const T* sh = reinterpret_cast<const T*>(p + dy_bytes);
@@ -412,7 +414,8 @@ __global__ void __launch_bounds__(1024) norm_backward_block(const NormBackArgs a
             }
         }
         row_sums<false>(sum, buf, turn);
-        if (*static_cast<volatile int*>(&abort)) break;
+        gave_up = *static_cast<volatile int*>(&abort[turn & 1]);
+        if (gave_up) break;
         // every thread has left the row before: its stage takes the next copy
         if (tid == 0 && turn > 0 && stages > 1 && next < a.rows) {
             issue(next, s == 0 ? stages - 1 : s - 1);
@@ -446,9 +449,19 @@ __global__ void __launch_bounds__(1024) norm_backward_block(const NormBackArgs a
             phase ^= 1;
         }
     }
-    if (abort && tid == 0)  // no copy may be in flight when the block ends
-        for (int i = 0; i < stages; ++i) mbar_wait_bounded(&full[i], i < s ? phase ^ 1 : phase, kBackWaitNs);
-    const float bad = abort ? __int_as_float(0x7fffffff) : 0.0f;
+    // Then its part of dw is NaN, and so is dx from that row on: whoever reads either sees it.
+    const float bad = gave_up ? __int_as_float(0x7fffffff) : 0.0f;
+    if (gave_up) {
+        if (tid == 0)  // no copy may be in flight when the block ends
+            for (int i = 0; i < stages; ++i) mbar_wait_bounded(&full[i], i < s ? phase ^ 1 : phase, kBackWaitNs);
+        for (; row < a.rows; row += gridDim.x)
+            for (int v = tid; v < vecs; v += blockDim.x) {
+                float d[8] = {bad, bad, bad, bad, bad, bad, bad, bad};
+                Raw8<T> o;
+                o.round(d);
+                o.store(static_cast<T*>(a.dx) + row * a.dx_stride + v * 8);
+            }
+    }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int v = tid + i * blockDim.x;

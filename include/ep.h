@@ -569,7 +569,7 @@ ep_status ep_rms_norm(const void* x, int64_t x_stride, const void* residual, int
  * The order of the sums depends on the sizes and the device alone.  The workspace
  * (16-byte aligned, ep_rms_norm_backward_workspace bytes on the current device)
  * belongs to the call until it has finished.  Should a bounded wait (2 s) for its
- * own copies run out, dweight is NaN. */
+ * own copies run out, dweight is NaN, and so are the rows of dx that were not made. */
 int64_t ep_rms_norm_backward_workspace(int64_t rows, int32_t hidden);
 ep_status ep_rms_norm_backward(const void* dy, int64_t dy_stride, const void* h, int64_t h_stride, int32_t h_type, const void* weight,
                                int32_t weight_type, float eps, const void* dresidual, int64_t dresidual_stride, int64_t rows,
