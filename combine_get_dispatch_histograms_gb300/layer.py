@@ -23,12 +23,14 @@ FEW_TOKENS = 64
 
 class MoELayer:
     """w13 = [gate; up] [E][2I][H] and w2 [E][H][I]: e4m3 codes with fp32 scales per 128 x 128 block, or MXFP4 codes
-    [..][H/2], [..][I/2] with uint8 scales [..][H/32], [..][I/32]."""
+    [..][H/2], [..][I/2] with uint8 scales [..][H/32], [..][I/32].  bf16 weights, without scales (None), run up to FEW_TOKENS
+    tokens."""
 
     def __init__(self, w13: torch.Tensor, w13_scales: torch.Tensor, w2: torch.Tensor, w2_scales: torch.Tensor):
         self.w13, self.w13_scales, self.w2, self.w2_scales = w13, w13_scales, w2, w2_scales
-        self.fp4 = w13_scales.dtype == torch.uint8
-        if (w2_scales.dtype == torch.uint8) != self.fp4:
+        four = [s is not None and s.dtype == torch.uint8 for s in (w13_scales, w2_scales)]
+        self.fp4 = four[0]
+        if four[0] != four[1]:
             raise ValueError("MoELayer: both weights e4m3 with fp32 scales, or both MXFP4 with uint8 scales")
 
     def forward(self, ctx: Context, x: torch.Tensor, topk_idx: torch.Tensor, topk_weights: torch.Tensor) -> torch.Tensor:
@@ -41,6 +43,7 @@ class MoELayer:
         if ctx.R * ctx.T <= FEW_TOKENS:
             return moe_tokens(x.view(-1, ctx.H), topk_idx.view(-1, ctx.K), topk_weights.view(-1, ctx.K), self.w13, self.w2,
                               self.w13_scales, self.w2_scales, status=ctx.lib.ep_ctx_status_word(ctx._ctx)).view(x.shape)
+        self._need_scales("forward")
         _, h = ctx.layout_notify(topk_idx, wait=False)
         rows = ctx.dispatch_permuted_quant(x, topk_idx, topk_weights, h)["permuted_xq"]
         hidden = ctx.expert_swiglu(h, rows, self.w13, self.w13_scales)
@@ -51,6 +54,11 @@ class MoELayer:
         errors: buf.check()."""
         if self.fp4:
             raise ValueError("MoELayer.forward_ll: the low-latency buffer carries FP8 rows, for e4m3 weights")
+        self._need_scales("forward_ll")
         packed = buf.dispatch(x, topk_idx)
         hidden = buf.expert_swiglu(packed, self.w13, self.w13_scales)
         return buf.combine(buf.expert_gemm(hidden, packed, self.w2, self.w2_scales), topk_idx, topk_weights, packed)
+
+    def _need_scales(self, name: str):
+        if self.w13_scales is None or self.w2_scales is None:
+            raise ValueError(f"MoELayer.{name}: weights without scales run up to {FEW_TOKENS} tokens, by forward")
