@@ -16,7 +16,7 @@
 // 324 us, 6.7 TB/s.  With long groups shared memory: a stage's codes are written to it and read from it once, 82 KB at
 // 128 bytes a cycle = 640 cycles for 192 weight rows, and a stage takes 650 (the products some 370).  Pairs of blocks share
 // the weight's rows, 56 KB a stage and SM: first product, 40 groups of 2048 rows, 914 us by one block, 737 by pairs (6.5
-// PFLOP/s); the second 541 us by 192 weight rows a tile, 496 by 224, 466 by pairs (5.2 PFLOP/s, results included).  A long run
+// PFLOP/s); the second 541 us by 192 weight rows a tile, 500 by 224, 411 by pairs (5.9 PFLOP/s, results included).  A long run
 // of such products meets the board's power limit (65536 rows to 256 groups, first product: 976 us at first, 1060 to 1100 later).
 // A fifth stage changes nothing, weights fetched ahead into the second-level cache cost time.  With few tiles, what one
 // SM brings in from memory: one row, K 7168, N 4096 11.2 us by 64 blocks, 8.3 by 128 in clusters of two.
@@ -40,7 +40,11 @@ constexpr int k4Group = 2;        // stages whose scales are staged together
 constexpr int64_t k4WaitNs = 2000000000ll;
 
 // kCtas = 2: a pair of blocks makes a tile of 256 rows, each with its own rows and half of the weight's, and with the
-// scales of all of the weight's.
+// scales of all of the weight's.  The first issues the products of both, which read both blocks' memory: the second's
+// copies count on the first's barriers, and one of its warps tells the first of scales in place, by a release at cluster
+// scope that covers shared memory (us, 40 groups of 2048 rows, first / second product: 739 / 406; by the scales' warps
+// themselves 758 / 408; by two warps with a release of all memory 910 / 447; stage by stage for codes and scales, with
+// a release at block scope, which does not reach the other block, 736 / 461).
 template <bool kSwiglu, int kBN, int kCtas>
 struct Fp4Shape {
     static constexpr int kTileM = kCtas * k4BM;
@@ -48,7 +52,7 @@ struct Fp4Shape {
     static constexpr int kCodesA = k4BM * 128, kCodesB = kBN / kCtas * 128, kCodes = kCodesA + kCodesB;
     static constexpr int kScalesA = 2 * 512, kScalesB = 2 * kChunks * 512, kScales = kScalesA + kScalesB;  // [128 of K][chunk][32][16]
     static constexpr int kSlot = k4Group * kScales;                 // the scales that are staged together
-    static constexpr int kSlots = kSwiglu ? 4 : 2;
+    static constexpr int kSlots = kSwiglu || kCtas == 2 ? 4 : 2;    // no stage less for the four of a pair
     static constexpr int kOut = kSwiglu ? 0 : 32 * 64;              // of a warp's output on its way: 32 rows of 32 columns
     static constexpr int kRest = kSlots * kSlot + k4OutWarps * kOut;
     static constexpr int kStages = (225 * 1024 - kRest) / kCodes < 8 ? (225 * 1024 - kRest) / kCodes : 8;
@@ -152,11 +156,11 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
 
     if (tid == 0) {
         for (int s = 0; s < kStages; ++s) {
-            mbar_init(&sh.full[s], kCtas == 2 && rank == 0 ? 2 : 1);  // its own copies, and what the other block says of its
+            mbar_init(&sh.full[s], 1);
             mbar_init(&sh.done[s], 1);
         }
         for (int b = 0; b < kSlots; ++b) {
-            mbar_init(&sh.scale_full[b], k4ScaleWarps);
+            mbar_init(&sh.scale_full[b], k4ScaleWarps + (kCtas == 2 && rank == 0 ? 1 : 0));  // its own, and what the other block of a pair tells
             mbar_init(&sh.scale_empty[b], 1);
         }
         for (int b = 0; b < 2; ++b) {
@@ -219,9 +223,11 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
                 mbar_arrive(tr.bar(tile_empty));
                 ++tr.n;
                 if (tile.rows == 0) break;
-                const int rows = min(tile.rows - rank * k4BM, k4BM), row = tile.row0 + rank * k4BM;
-                const int boxes = (max(rows, 0) + k4BoxRows - 1) / k4BoxRows;
-                const uint32_t bytes = boxes * k4BoxRows * 128 + Shape::kCodesB;
+                // a pair's bytes all count on the first block's barriers
+                const int boxes0 = (min(tile.rows, k4BM) + k4BoxRows - 1) / k4BoxRows, boxes1 = (max(tile.rows - k4BM, 0) + k4BoxRows - 1) / k4BoxRows;
+                const int boxes = rank ? boxes1 : boxes0, row = tile.row0 + rank * k4BM;
+                const uint32_t bytes = (kCtas == 2 ? boxes0 + boxes1 : boxes0) * k4BoxRows * 128 + kCtas * Shape::kCodesB;
+                const uint32_t full0 = kCtas == 2 ? smem_of(full, 0) : full;
                 // the first block of a pair has the gate rows, or the first half, the second the others
                 const int first = kSwiglu ? tile.n * kHalf : tile.n * kBN, second = kSwiglu ? a.N / 2 + first : first + kHalf;
                 const int w0 = rank ? second : first;
@@ -231,29 +237,32 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
                         break;
                     }
                     uint8_t* sa = codes + st.slot * kCodes;
-                    const uint32_t bar = full + st.slot * 8;
-                    mbar_arrive_expect_tx(&sh.full[st.slot], bytes);
-                    tma_load_3d<1>(sa + Shape::kCodesA, &map_w, kt * 128, w0, tile.g, bar);
+                    const uint32_t bar = full0 + st.slot * 8;
+                    if (rank == 0) mbar_arrive_expect_tx(&sh.full[st.slot], bytes);
+                    tma_load_3d<kCtas>(sa + Shape::kCodesA, &map_w, kt * 128, w0, tile.g, bar);
                     if (kSwiglu && kCtas == 1) tma_load_3d<1>(sa + Shape::kCodesA + kHalf * 128, &map_w, kt * 128, second, tile.g, bar);
-                    if (boxes == k4BM / k4BoxRows) tma_load_2d<1>(sa, &map_x, kt * 128, row, bar);
+                    if (boxes == k4BM / k4BoxRows) tma_load_2d<kCtas>(sa, &map_x, kt * 128, row, bar);
                     else
                         for (int b = 0; b < boxes; ++b)
-                            tma_load_2d<1>(sa + b * k4BoxRows * 128, &map_box, kt * 128, row + b * k4BoxRows, bar);
+                            tma_load_2d<kCtas>(sa + b * k4BoxRows * 128, &map_box, kt * 128, row + b * k4BoxRows, bar);
                     st.next();
                 }
             }
             // no copy may be in flight when the blocks end, also after a wait that ran out: the last phase that
             // a stage's copies complete is the one before its next
-            for (int u = 0; u < kStages; ++u) {
+            for (int u = 0; u < kStages && rank == 0; ++u) {
                 mbar_wait_bounded(&sh.full[st.slot], st.phase ^ 1, k4WaitNs);
                 st.next();
             }
+            // The first block may have given up before it counted the second's last ones, which land in microseconds.
+            if (rank != 0 && *abort)
+                for (const uint64_t t0 = globaltimer_ns(); globaltimer_ns() - t0 < 1000000;) {
+                }
         }
     } else if (warp == 1 && rank != 0) {
-        // ---- the second block's copies and scales are in place: told to the first block, stage by stage
-        const uint32_t full0 = smem_of(full, 0);
+        // ---- the second block's scales are in place: told to the first block
+        const uint32_t told = smem_of(scale_full, 0);
         RingPos<k4TileRing> tr;
-        Turn<kStages> st;
         Turn<kSlots> sl;
         while (true) {
             mbar_wait_warp<true>(tr.bar(tile_full), tr.phase(), k4WaitNs, abort);
@@ -263,14 +272,10 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
             ++tr.n;
             if (rows == 0 || __any_sync(0xffffffffu, *abort)) break;
 #pragma unroll 1
-            for (int kt = 0; kt < a.KT; ++kt) {
-                if ((kt & (k4Group - 1)) == 0) {
-                    mbar_wait_warp<true>(scale_full + sl.slot * 8, sl.phase, k4WaitNs, abort);
-                    sl.next();
-                }
-                mbar_wait_warp<true>(full + st.slot * 8, st.phase, k4WaitNs, abort);
-                if (lane == 0) mbar_arrive_filled(full0 + st.slot * 8);
-                st.next();
+            for (int kt = 0; kt < a.KT; kt += k4Group) {
+                mbar_wait_warp<true>(scale_full + sl.slot * 8, sl.phase, k4WaitNs, abort);
+                if (lane == 0) mbar_arrive_mate(told + sl.slot * 8);
+                sl.next();
             }
         }
     } else if (warp == 1) {
@@ -295,9 +300,10 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
                 const bool two = kt + 1 < kt1;
                 const Turn<kStages> st0 = st;
                 st.next();
-                mbar_wait_warp<true>(scale_full + sl.slot * 8, sl.phase, k4WaitNs, abort);
-                mbar_wait_warp<true>(full + st0.slot * 8, st0.phase, k4WaitNs, abort);
-                if (two) mbar_wait_warp<true>(full + st.slot * 8, st.phase, k4WaitNs, abort);
+                mbar_wait_warp<true, kCtas == 2>(scale_full + sl.slot * 8, sl.phase, k4WaitNs, abort);
+                mbar_wait_warp<true, kCtas == 2>(full + st0.slot * 8, st0.phase, k4WaitNs, abort);
+                if (two) mbar_wait_warp<true, kCtas == 2>(full + st.slot * 8, st.phase, k4WaitNs, abort);
+                if (kCtas == 2) fence_acquire_mate();
                 tc_fence_after();
                 if (elect_one()) {
                     const uint64_t ds = ds0 + sl.slot * (Shape::kSlot >> 4);

@@ -10,11 +10,20 @@ namespace ep {
 // ---- bounded mbarrier waits, on shared addresses -----------------------------------
 // kLong: a thread that has to wait is suspended for up to 20 us instead of the
 // system's own limit, so that waiting warps do not take issue slots from those
-// that share their scheduler.
-template <bool kLong>
+// that share their scheduler.  kCluster: for what another block of the cluster
+// tells, ordered by fence_acquire_mate after the wait.
+template <bool kLong, bool kCluster = false>
 __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
     uint32_t ok;
-    if constexpr (kLong)
+    if constexpr (kLong && kCluster)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity), "r"(20000u)
+            : "memory");
+    else if constexpr (kLong)
         asm volatile(
             "{\n\t.reg .pred p;\n\t"
             "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
@@ -57,12 +66,12 @@ __device__ __forceinline__ bool mbar_wait_or_abort(uint32_t bar, uint32_t parity
 }
 // The same for a whole warp, which stays together; after a give-up it returns
 // as after success, and the caller looks at *abort where it can leave.
-template <bool kLong = false>
+template <bool kLong = false, bool kCluster = false>
 __device__ __forceinline__ void mbar_wait_warp(uint32_t bar, uint32_t parity, int64_t limit_ns, volatile int* abort) {
-    if (__all_sync(0xffffffffu, mbar_try<kLong>(bar, parity))) return;
+    if (__all_sync(0xffffffffu, mbar_try<kLong, kCluster>(bar, parity))) return;
     uint64_t t0 = 0;
     for (uint32_t i = 1;; ++i) {
-        if (__all_sync(0xffffffffu, mbar_try<kLong>(bar, parity))) return;
+        if (__all_sync(0xffffffffu, mbar_try<kLong, kCluster>(bar, parity))) return;
         if ((i & 255u) == 0) {
             const uint64_t t = globaltimer_ns();
             if (t0 == 0) t0 = t;
@@ -159,12 +168,14 @@ __device__ __forceinline__ void mbar_hand_back(uint32_t bar) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-// The same for shared memory of the arriving block, which the tensor cores read: bulk copies and fenced writes that
-// the arriving thread has waited for.  A release at cluster scope costs it some 1800 cycles (measured), one at block scope
-// orders what it has waited for and is not seen in the kernel's time.
-__device__ __forceinline__ void mbar_arrive_filled(uint32_t bar) {
-    asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+// The same after writes to the arriving block's shared memory, fenced for the tensor cores, which the other block's are
+// to read: a release at cluster scope, of shared memory alone.  With fence_acquire_mate after the wait the two
+// blocks synchronise.
+__device__ __forceinline__ void mbar_arrive_mate(uint32_t bar) {
+    asm volatile("fence.release.sync_restrict::shared::cta.cluster;" ::: "memory");
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+__device__ __forceinline__ void fence_acquire_mate() { asm volatile("fence.acquire.sync_restrict::shared::cluster.cluster;" ::: "memory"); }
 
 // ---- tiled bulk copies (the innermost coordinate is a multiple of 16 bytes) ------
 // Into this block's shared memory; `bar` (a cluster address) counts the bytes,
