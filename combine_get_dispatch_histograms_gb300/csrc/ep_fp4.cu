@@ -681,16 +681,15 @@ static int fp4_split(int64_t tiles, int stages, int sms) {
 
 // The shape of a launch's tiles: the one with the least rounds over the SMs * cost of a round, the widest of equal ones.  A
 // round's cost is what bounds it, the rows of codes that a stage brings into an SM, 128 + columns.  us by 192 columns / by what
-// is chosen: second product, K 2048, N 7168, 40 groups of 2048 rows 541 / 496 (224: 6 % fewer bytes a column, and N is 32 of
-// them); one group, K 7168, 1000 rows: N 4096 26.4 / 18.0 (224), N 7168 27.8 / 27.8 (by 224 30.0), N 2048 15.5 / 13.6 (128);
+// is chosen: second product, K 2048, N 7168, 40 groups of 2048 rows 541 / 500 (224: 6 % fewer bytes a column, and N is 32 of
+// them); one group, K 7168, 1000 rows: N 4096 26.4 / 18.0 (224), N 7168 27.8 / 23.2 (by 224 30.0; pairs), N 2048 15.5 / 13.6 (128);
 // K 4096, N 4096, 777 rows 16.4 / 12.6 (128); first product, 300 rows, 2I 4096, by 64 20.7, by 128 13.8.
-// Pairs of blocks have twice the rows, at 0.825 of a round of 192's cost for the first product, 0.935 of one of 224's for the
-// second, whose results are a larger part.  40 groups, us by one block / by pairs: K 7168, 2I 4096, 256 rows a group 135 / 128,
-// 448 238 / 204, 640 297 / 285, 768 371 / 296, 1024 460 / 386, 2048 914 / 737; K 2048, N 7168, 448 133 / 129, 640 164 / 164,
-// 1024 257 / 243, 2048 498 / 466.  But half a tile of each group is empty on average where their lengths vary: first product,
-// 256 groups of 256 rows on average 1020 / 1075, 64 of 512 423 / 390; second, 64 of 512 237 / 244, of 1024 425 / 426, of 1536
-// 624 / 616; so that they need more than 384 rows, and several groups of the second product more than 1024.  And a launch of
-// one round gains nothing: 777 rows, 4096 -> 4096 12.6 / 13.3.
+// Pairs of blocks have twice the rows, at 0.825 of a round's cost by one block.  40 groups, us by one block / by pairs: K 7168,
+// 2I 4096, 256 rows a group 137 / 129, 448 242 / 206, 640 297 / 284, 768 371 / 296, 1024 460 / 390, 2048 900 / 739; K 2048, N
+// 7168, 448 134 / 116, 640 165 / 160, 1024 258 / 214, 2048 500 / 411.  Half a tile of each group is empty on average where their
+// lengths vary: second product, 64 groups of 512 rows on average 236 / 214, of 1024 423 / 375, of 1536 615 / 532 (K 512, N
+// 4096, 512 rows 85 / 87); first product, 64 of 512 423 / 380, but 256 of 256 1020 / 1075, so that they need more than 384.
+// And a launch of one round gains nothing: 777 rows, 4096 -> 4096 12.6 / 13.3.
 struct Fp4Choice {
     int columns, ctas;
 };
@@ -711,7 +710,7 @@ static Fp4Choice fp4_choice(bool swiglu, int64_t rows, int groups, int64_t n, in
     consider(128, 1, k4BM + 128);
     consider(192, 1, k4BM + 192);
     if (!swiglu) consider(224, 1, k4BM + 224);
-    if (rows > (swiglu || groups == 1 ? 3 : 8) * k4BM && least > k4BM + 224) consider(swiglu ? 192 : 224, 2, swiglu ? 264 : 330);
+    if (rows > 3 * k4BM && least > k4BM + 224) consider(swiglu ? 192 : 224, 2, swiglu ? 264 : 290);
     return best;
 }
 
