@@ -223,10 +223,11 @@ fp4_gemm_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant
                 mbar_arrive(tr.bar(tile_empty));
                 ++tr.n;
                 if (tile.rows == 0) break;
-                // a pair's bytes all count on the first block's barriers
-                const int boxes0 = (min(tile.rows, k4BM) + k4BoxRows - 1) / k4BoxRows, boxes1 = (max(tile.rows - k4BM, 0) + k4BoxRows - 1) / k4BoxRows;
-                const int boxes = rank ? boxes1 : boxes0, row = tile.row0 + rank * k4BM;
-                const uint32_t bytes = (kCtas == 2 ? boxes0 + boxes1 : boxes0) * k4BoxRows * 128 + kCtas * Shape::kCodesB;
+                const int rows = min(tile.rows - rank * k4BM, k4BM), row = tile.row0 + rank * k4BM;
+                const int boxes = (max(rows, 0) + k4BoxRows - 1) / k4BoxRows;
+                uint32_t bytes = boxes * k4BoxRows * 128 + Shape::kCodesB;
+                if (kCtas == 2)  // a pair's bytes all count on the first block's barriers
+                    bytes += (max(tile.rows - k4BM, 0) + k4BoxRows - 1) / k4BoxRows * k4BoxRows * 128 + Shape::kCodesB;
                 const uint32_t full0 = kCtas == 2 ? smem_of(full, 0) : full;
                 // the first block of a pair has the gate rows, or the first half, the second the others
                 const int first = kSwiglu ? tile.n * kHalf : tile.n * kBN, second = kSwiglu ? a.N / 2 + first : first + kHalf;
