@@ -16,7 +16,7 @@
 // 324 us, 6.7 TB/s.  With long groups shared memory: a stage's codes are written to it and read from it once, 82 KB at
 // 128 bytes a cycle = 640 cycles for 192 weight rows, and a stage takes 650 (the products some 370).  Pairs of blocks share
 // the weight's rows, 56 KB a stage and SM: first product, 40 groups of 2048 rows, 914 us by one block, 737 by pairs (6.5
-// PFLOP/s); the second 541 us by 192 weight rows a tile, 500 by 224, 411 by pairs (5.9 PFLOP/s, results included).  A long run
+// PFLOP/s); the second 541 us by 192 weight rows a tile, 500 by 224, 406 by pairs (5.9 PFLOP/s, results included).  A long run
 // of such products meets the board's power limit (65536 rows to 256 groups, first product: 976 us at first, 1060 to 1100 later).
 // A fifth stage changes nothing, weights fetched ahead into the second-level cache cost time.  With few tiles, what one
 // SM brings in from memory: one row, K 7168, N 4096 11.2 us by 64 blocks, 8.3 by 128 in clusters of two.

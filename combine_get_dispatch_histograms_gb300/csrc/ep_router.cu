@@ -17,7 +17,8 @@
 //
 // Bound.  Not memory yet (256 experts, fp32: 1 KB a token), but the instructions of a token, some 365 for a choice
 // of 8, 570 by groups with a bias, 400 for the gradient, and with that the warps that wait for loads meanwhile:
-// route 32768 tokens, 4 of 8 groups, 21 us (79 by maxima over the warp, one choice at a time; issue slots 72 % full);
+// route 32768 tokens, 4 of 8 groups, 21 us (79 by maxima over the warp, one choice at a time; issue slots 72 % full),
+// by scores 24 (some 610 instructions); without groups 14.5, by scores 18;
 // 65536 tokens of 32 sequences: route 29 us, loss 24, gradient 35.  What brought it there: whole sectors a lane (two
 // halves of each twice: gradient 49 -> 44), grids of one wave (loss 31 -> 24), two tokens' loads together.  Teams of
 // 8 or 16 lanes a token share a row's sums among tokens, but hold 32 or 16 experts a lane, and the registers of that
